@@ -10,6 +10,11 @@ Operations (the passages that define them are cited in include/hs.h):
   gather_rows    single-stride gather of resolved pool rows
   offload_pages  post-forward proactive copy of completed pages, all layers in one launch
   hot_reset      empty the hot buffers
+and on the rows themselves (include/hs_latent.h, latent.py):
+  append_rows    rotate, quantise and store the rows of new tokens
+  attend_rows    absorbed latent attention over row ids
+  attend_pages   absorbed latent attention over whole contexts through a block table
+  attend_expanded  attention over keys and values expanded to every head (prompts)
 """
 from __future__ import annotations
 
@@ -518,3 +523,7 @@ class PreparedStep:
             _check(self.L.hs_offload_pages(self.pool.handle, _dev_i32(gpu_blocks, "gpu_blocks"),
                                            _dev_i32(host_blocks, "host_blocks"), int(n), None, self.stream),
                    "hs_offload_pages")
+
+
+from .latent import (append_rows, attend_expanded, attend_pages, attend_rows, attend_workspace_bytes,  # noqa: E402
+                     alloc_attend_workspace)

@@ -6,6 +6,7 @@
 #include <new>
 
 #include "hs_internal.cuh"
+#include "latent.cuh"
 
 struct hs_pool {
   hs::PoolGeom g;
@@ -76,6 +77,16 @@ MissOrder call_miss_order(const hs_pool* pool, int32_t nl, int64_t ng, int32_t R
 void count_launch(int k) { g_launches.fetch_add(k, std::memory_order_relaxed); }
 
 int pool_device(const hs_pool* pool) { return pool ? pool->device : -1; }
+
+int device_sms(int dev) { return sm_count(dev); }
+
+bool pool_layer(const hs_pool* pool, int32_t layer, LayerView* v) {
+  if (!pool || layer < 0 || layer >= pool->g.num_layers) return false;
+  const PoolGeom& g = pool->g;
+  *v = LayerView{pool->ptrs.gpu[layer], g.row_bytes, g.page_size, g.num_gpu_blocks,
+                 (int64_t)g.num_gpu_blocks * g.page_size, pool->device, sm_count(pool->device)};
+  return true;
+}
 
 }  // namespace hs
 

@@ -1,0 +1,221 @@
+"""Operators on the latent rows of the paged KV pool (include/hs_latent.h).
+
+  append_rows      write the rows of new tokens (rotation + quantisation + store, one launch)
+  attend_rows      absorbed latent attention over row ids (resolve_topk's out_rows)
+  attend_pages     absorbed latent attention over whole contexts through a block table
+  attend_expanded  attention over keys and values expanded to every head (prompts)
+
+Thin marshalling like the rest of the binding: no CPU fallback, every refusal of the library raises."""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import torch
+
+from . import Pool, _check, _dev_i32, _opt, _stream, lib
+
+LATENT_DIM, ROPE_DIM, NOPE_DIM, VALUE_DIM = 512, 64, 128, 128
+ROW_BYTES_FP8, ROW_BYTES_BF16 = 656, 1152
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+_i32, _i64, _p, _f = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float
+
+
+class AppendC(ctypes.Structure):
+    _fields_ = [("n", _i64), ("rows", _p), ("positions", _p), ("rotation", _p), ("num_positions", _i32),
+                ("interleaved", _i32), ("dtype", _i32), ("heads", _i32), ("latent", _p), ("latent_stride", _i64),
+                ("rope", _p), ("rope_stride", _i64), ("q_rope", _p), ("q_token_stride", _i64), ("q_head_stride", _i64),
+                ("q_out", _p), ("q_out_token_stride", _i64), ("q_out_head_stride", _i64), ("status", _p)]
+
+
+class AttendC(ctypes.Structure):
+    _fields_ = [("heads", _i32), ("scale", _f), ("q_latent", _p), ("ql_token_stride", _i64), ("ql_head_stride", _i64),
+                ("q_rope", _p), ("qr_token_stride", _i64), ("qr_head_stride", _i64), ("out", _p),
+                ("out_token_stride", _i64), ("out_head_stride", _i64), ("lse", _p), ("status", _p)]
+
+
+class ExpandedC(ctypes.Structure):
+    _fields_ = [("seqs", _i32), ("heads", _i32), ("causal", _i32), ("scale", _f), ("q_tokens", _i64),
+                ("k_tokens", _i64), ("cu_q", _p), ("cu_k", _p), ("q_nope", _p), ("qn_token_stride", _i64),
+                ("qn_head_stride", _i64), ("q_rope", _p), ("qr_token_stride", _i64), ("qr_head_stride", _i64),
+                ("k_nope", _p), ("kn_token_stride", _i64), ("kn_head_stride", _i64), ("k_rope", _p),
+                ("kr_token_stride", _i64), ("v", _p), ("v_token_stride", _i64), ("v_head_stride", _i64), ("out", _p),
+                ("out_token_stride", _i64), ("out_head_stride", _i64), ("lse", _p), ("status", _p)]
+
+
+_bound = None
+
+
+def _lib():
+    global _bound
+    if _bound is None:
+        L = lib()
+        L.hs_append_rows.restype = _i32
+        L.hs_append_rows.argtypes = [_p, _i32, ctypes.POINTER(AppendC), _p]
+        L.hs_attend_workspace_bytes.restype = ctypes.c_size_t
+        L.hs_attend_workspace_bytes.argtypes = []
+        L.hs_attend_rows.restype = _i32
+        L.hs_attend_rows.argtypes = [_p, _i32, _p, _i64, _i32, ctypes.POINTER(AttendC), _p, ctypes.c_size_t, _p]
+        L.hs_attend_pages.restype = _i32
+        L.hs_attend_pages.argtypes = [_p, _i32, _p, _p, _i32, _i32, _i32, ctypes.POINTER(AttendC), _p, ctypes.c_size_t, _p]
+        L.hs_attend_expanded.restype = _i32
+        L.hs_attend_expanded.argtypes = [ctypes.POINTER(ExpandedC), _p]
+        _bound = L
+    return _bound
+
+
+def _tensor(t: torch.Tensor, name: str, shape: tuple, dtype=torch.bfloat16) -> None:
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda:
+        raise TypeError(f"{name} must be a {dtype} CUDA tensor")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+    if t.numel() and t.stride(-1) != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+
+
+def _f32(t: Optional[torch.Tensor], name: str, shape: tuple):
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or not t.is_cuda or not t.is_contiguous() or tuple(t.shape) != shape:
+        raise TypeError(f"{name} must be a contiguous float32 CUDA tensor of shape {shape}")
+    return t.data_ptr()
+
+
+def append_rows(pool: Pool, rows: torch.Tensor, latent: torch.Tensor, rope: torch.Tensor, positions: torch.Tensor,
+                rotation: torch.Tensor, *, layer: int = 0, q_rope: Optional[torch.Tensor] = None,
+                q_out: Optional[torch.Tensor] = None, interleaved: bool = False,
+                status: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+    """Writes the pool rows of n new tokens of one layer: rows int32 [n] (-1: none), latent [n][512], rope
+    [n][64] (not yet rotated), positions int32 [n], rotation fp32 [num_positions][64] (32 cosines, 32 sines).
+    q_rope [n][heads][64], of the same type, is rotated into q_out (a new tensor, or q_rope itself) in the
+    same launch; returns q_out.  latent, rope and q_rope share a type: bf16, fp16 or fp32."""
+    n = int(rows.numel())
+    dt = _DTYPES.get(latent.dtype)
+    if dt is None:
+        raise TypeError("latent must be bf16, fp16 or fp32")
+    _tensor(latent, "latent", (n, LATENT_DIM), latent.dtype)
+    _tensor(rope, "rope", (n, ROPE_DIM), latent.dtype)
+    if positions.numel() != n:
+        raise ValueError("positions must have one entry per row")
+    if rotation.dim() != 2 or rotation.shape[1] != ROPE_DIM:
+        raise ValueError("rotation must be [num_positions][64]")
+    heads, q, qo = 0, (None, 0, 0), (None, 0, 0)
+    if q_rope is not None:
+        heads = int(q_rope.shape[1]) if q_rope.dim() == 3 else -1
+        _tensor(q_rope, "q_rope", (n, heads, ROPE_DIM), latent.dtype)
+        if q_out is None:
+            q_out = torch.empty((n, heads, ROPE_DIM), dtype=latent.dtype, device=q_rope.device)
+        _tensor(q_out, "q_out", (n, heads, ROPE_DIM), latent.dtype)
+        q = (q_rope.data_ptr(), q_rope.stride(0), q_rope.stride(1))
+        qo = (q_out.data_ptr(), q_out.stride(0), q_out.stride(1))
+    elif q_out is not None:
+        raise ValueError("q_out without q_rope")
+    a = AppendC(n, _dev_i32(rows, "rows"), _dev_i32(positions, "positions"),
+                _f32(rotation, "rotation", tuple(rotation.shape)), int(rotation.shape[0]), int(bool(interleaved)), dt,
+                heads, latent.data_ptr(), latent.stride(0), rope.data_ptr(), rope.stride(0), *q, *qo,
+                _opt(status, "status"))
+    _check(_lib().hs_append_rows(pool.handle, int(layer), ctypes.byref(a), _stream(stream)), "hs_append_rows")
+    return q_out
+
+
+def attend_workspace_bytes() -> int:
+    return int(_lib().hs_attend_workspace_bytes())
+
+
+def alloc_attend_workspace(device="cuda") -> torch.Tensor:
+    """Workspace of attend_rows and attend_pages, for any shape; calls that share one must be ordered on one
+    stream."""
+    with torch.cuda.device(device):
+        return torch.empty(max(16, attend_workspace_bytes()), dtype=torch.uint8, device=device)
+
+
+def _attend(lead: tuple, q_latent, q_rope, scale, out, lse, status, workspace):
+    """Marshals an absorbed call whose query tensors have the leading dimensions `lead` (tokens) and heads."""
+    heads = int(q_latent.shape[len(lead)]) if q_latent.dim() == len(lead) + 2 else -1
+    _tensor(q_latent, "q_latent", (*lead, heads, LATENT_DIM))
+    _tensor(q_rope, "q_rope", (*lead, heads, ROPE_DIM))
+    if out is None:
+        out = torch.empty((*lead, heads, LATENT_DIM), dtype=torch.bfloat16, device=q_latent.device)
+    _tensor(out, "out", (*lead, heads, LATENT_DIM))
+    if lse is None:
+        lse = torch.empty((*lead, heads), dtype=torch.float32, device=q_latent.device)
+    lse_p = _f32(lse, "lse", (*lead, heads))
+    if workspace is None:
+        workspace = alloc_attend_workspace(q_latent.device)
+    if workspace.dtype != torch.uint8 or not workspace.is_cuda or not workspace.is_contiguous():
+        raise TypeError("workspace must be a contiguous uint8 CUDA tensor")
+
+    def strides(t, name):
+        if len(lead) == 2 and lead[0] > 1 and lead[1] > 1 and t.stride(0) != lead[1] * t.stride(1):
+            raise ValueError(f"{name}'s two leading dimensions must merge into one")
+        return (t.stride(len(lead) - 1) if len(lead) == 1 or lead[1] > 1 else t.stride(0)), t.stride(len(lead))
+
+    a = AttendC(heads, float(scale), q_latent.data_ptr(), *strides(q_latent, "q_latent"), q_rope.data_ptr(),
+                *strides(q_rope, "q_rope"), out.data_ptr(), *strides(out, "out"), lse_p, _opt(status, "status"))
+    return a, out, lse, workspace
+
+
+def attend_rows(pool: Pool, rows: torch.Tensor, q_latent: torch.Tensor, q_rope: torch.Tensor, scale: float, *,
+                layer: int = 0, out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                status: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Absorbed attention of n query tokens over their own rows: rows int32 [n][K] (-1: skipped), q_latent bf16
+    [n][heads][512], q_rope bf16 [n][heads][64] (rotated) -> (out bf16 [n][heads][512], lse fp32 [n][heads])."""
+    if rows.dim() != 2:
+        raise ValueError("rows must be [tokens][K]")
+    n, K = int(rows.shape[0]), int(rows.shape[1])
+    a, out, lse, ws = _attend((n,), q_latent, q_rope, scale, out, lse, status, workspace)
+    _check(_lib().hs_attend_rows(pool.handle, int(layer), _dev_i32(rows, "rows"), n, K, ctypes.byref(a),
+                                 ws.data_ptr(), ws.numel(), _stream(stream)), "hs_attend_rows")
+    return out, lse
+
+
+def attend_pages(pool: Pool, block_table: torch.Tensor, ctx_len: torch.Tensor, q_latent: torch.Tensor,
+                 q_rope: torch.Tensor, scale: float, *, layer: int = 0, out: Optional[torch.Tensor] = None,
+                 lse: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None, stream=None):
+    """Absorbed attention over whole contexts: block_table int32 [R][max_pages], ctx_len int32 [R], q_latent bf16
+    [R][P][heads][512], q_rope bf16 [R][P][heads][64]; position p of request r sees its first
+    ctx_len[r] - P + 1 + p tokens -> (out bf16 [R][P][heads][512], lse fp32 [R][P][heads])."""
+    if q_latent.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("q_latent must be [R][P][heads][512] and block_table [R][max_pages]")
+    R, P = int(q_latent.shape[0]), int(q_latent.shape[1])
+    if block_table.shape[0] != R or ctx_len.numel() != R:
+        raise ValueError("block_table and ctx_len must have one entry per request")
+    a, out, lse, ws = _attend((R, P), q_latent, q_rope, scale, out, lse, status, workspace)
+    _check(_lib().hs_attend_pages(pool.handle, int(layer), _dev_i32(block_table, "block_table"),
+                                  _dev_i32(ctx_len, "ctx_len"), R, P, int(block_table.shape[1]), ctypes.byref(a),
+                                  ws.data_ptr(), ws.numel(), _stream(stream)), "hs_attend_pages")
+    return out, lse
+
+
+def attend_expanded(q_nope: torch.Tensor, q_rope: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tensor,
+                    v: torch.Tensor, cu_q: torch.Tensor, cu_k: torch.Tensor, scale: float, *, causal: bool = True,
+                    out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                    status: Optional[torch.Tensor] = None, stream=None):
+    """Attention of ragged sequences over expanded keys and values: q_nope bf16 [Tq][heads][128], q_rope bf16
+    [Tq][heads][64] and k_rope bf16 [Tk][64] (rotated; the key part is shared by the heads), k_nope and v bf16
+    [Tk][heads][128], cu_q and cu_k int32 [seqs + 1] -> (out bf16 [Tq][heads][128], lse fp32 [Tq][heads]).
+    causal: the queries are the last tokens of their sequence."""
+    if q_nope.dim() != 3 or k_rope.dim() != 2:
+        raise ValueError("q_nope must be [Tq][heads][128] and k_rope [Tk][64]")
+    Tq, H, Tk = int(q_nope.shape[0]), int(q_nope.shape[1]), int(k_rope.shape[0])
+    _tensor(q_nope, "q_nope", (Tq, H, NOPE_DIM))
+    _tensor(q_rope, "q_rope", (Tq, H, ROPE_DIM))
+    _tensor(k_nope, "k_nope", (Tk, H, NOPE_DIM))
+    _tensor(k_rope, "k_rope", (Tk, ROPE_DIM))
+    _tensor(v, "v", (Tk, H, VALUE_DIM))
+    if cu_q.numel() < 1 or cu_q.numel() != cu_k.numel():
+        raise ValueError("cu_q and cu_k must both have one entry more than there are sequences")
+    if out is None:
+        out = torch.empty((Tq, H, VALUE_DIM), dtype=torch.bfloat16, device=q_nope.device)
+    _tensor(out, "out", (Tq, H, VALUE_DIM))
+    if lse is None:
+        lse = torch.empty((Tq, H), dtype=torch.float32, device=q_nope.device)
+    a = ExpandedC(int(cu_q.numel()) - 1, H, int(bool(causal)), float(scale), Tq, Tk, _dev_i32(cu_q, "cu_q"),
+                  _dev_i32(cu_k, "cu_k"), q_nope.data_ptr(), q_nope.stride(0), q_nope.stride(1), q_rope.data_ptr(),
+                  q_rope.stride(0), q_rope.stride(1), k_nope.data_ptr(), k_nope.stride(0), k_nope.stride(1),
+                  k_rope.data_ptr(), k_rope.stride(0), v.data_ptr(), v.stride(0), v.stride(1), out.data_ptr(),
+                  out.stride(0), out.stride(1), _f32(lse, "lse", (Tq, H)), _opt(status, "status"))
+    _check(_lib().hs_attend_expanded(ctypes.byref(a), _stream(stream)), "hs_attend_expanded")
+    return out, lse
