@@ -103,7 +103,7 @@ size_t hs_attend_workspace_bytes(void) {
 hs_status hs_attend_rows(const hs_pool* pool, int32_t layer, const int32_t* rows, int64_t tokens, int32_t K,
                          const hs_attend* a, void* workspace, size_t workspace_bytes, hs_stream_t stream) {
   HS_RANGE("hs_attend_rows");
-  if (tokens < 0 || tokens > INT32_MAX || K < 0) return HS_ERR_INVALID_ARG;
+  if (tokens < 0 || tokens > INT32_MAX || K < 0 || K > (1 << 30)) return HS_ERR_INVALID_ARG;
   hs::AttendParams p;
   hs::LayerView v;
   const hs_status st = prepare_attend(pool, layer, a, tokens, workspace, workspace_bytes, p, v);
@@ -128,7 +128,7 @@ hs_status hs_attend_pages(const hs_pool* pool, int32_t layer, const int32_t* blo
   if (tokens > INT32_MAX) return HS_ERR_INVALID_ARG;
   const hs_status st = prepare_attend(pool, layer, a, tokens, workspace, workspace_bytes, p, v);
   if (st != HS_OK || tokens == 0) return st;
-  if (!ctx_len || (max_pages > 0 && !block_table) || (int64_t)max_pages * v.page_size > INT32_MAX)
+  if (!ctx_len || (max_pages > 0 && !block_table) || (int64_t)max_pages * v.page_size > (1 << 30))
     return HS_ERR_INVALID_ARG;
   p.paged = 1;
   p.table = block_table;
