@@ -6,21 +6,35 @@
 //   S^T[128 keys][N]  = K[128][576] * Q^T[576][N]          (36 steps of 16)
 //   O^T[512][N]      += V^T[512][128] * P^T[128][N]         (4 row blocks x 8 steps)
 // V is the latent part of K: the same bytes, once read as a K-major and once as an M-major operand.  The softmax
-// is online with a lazy reference: weights are exp2(s - m) with any m that keeps them in range, since fp32 sums
-// and bf16 weights have the same relative precision at every magnitude.  m starts as the first tile's maximum and
-// moves (with O and the sums rescaled) only when a score exceeds it by kLazy, so the maximum over 128 lanes is
-// rarely needed.  Sums are kept per key lane and joined once per unit.
+// is online with a lazy reference: weights are exp2(t), t = s - m, with any m that keeps them in range, since fp32 sums
+// have the same relative precision at every magnitude.  m starts kTop below the first tile's maximum and moves (with O
+// and the sums rescaled) only when a score exceeds it by kLazy, so the maximum over 128 lanes is rarely needed.  Sums
+// are kept per key lane and joined once per unit.
+//
+// Types.  bf16 rows: both products in bf16.  fp8 rows: both in fp16, because an e4m3 code becomes fp16 in one
+// instruction for two and fp16's 11 bits hold it exactly, while its range is narrow; so every factor is brought into
+// range by a power of two, which costs no precision: a key's row by skey (its values are code * scale / skey, its rotated
+// part divided by it too), a query column by qs, and the weights by skey / skey0 on their way to the second product,
+// where skey0 is the largest skey of the unit so far.  Then S = S' skey qs, and O = O' skey0.
 //
 // Layout.  A unit is (item, group of N columns); units are cut into tiles, numbered in order, and every CTA takes
 // an equal run of tiles; a unit that several CTAs share leaves partial results in the workspace, which
-// combine_kernel joins in a fixed order.  One CTA per SM, 16 warps:
-//   warps 0-7   producers: load the next tile's rows into registers while the current one is in use, and store
-//               them (fp8 dequantised to bf16) into the 128-byte-swizzled tile as its parts become free;
-//   warps 8-11  softmax and results (lane = key, later lane = latent dimension);
-//   warp 12     issues the products.
-// The warpgroups trade registers (kRegs*): the launch gives every thread 128.
-// The tile (128 x 576 bf16, 144 KB) has one buffer, released in five parts (four 128-dimension blocks after their
-// product with P, the key part after S, or after P when P takes its place).
+// combine_kernel joins in a fixed order.  One CTA per SM, 32 warps (the warpgroups trade registers, kRegs*):
+//   warp 29      resolves the keys of up to kAhead tiles to row ids;
+//   warps 24-27  copy the latent parts of the rows into the places that the current tile's parts leave;
+//   warps 0-15   bring the tile into operand form: fp8 codes land in half of their part's place and are widened to fp16
+//                there (a warp owns 8 keys); the rotated parts and scales come through registers, a tile ahead;
+//   warp 28      issues the products;
+//   warps 16-23  softmax and results: lane = key, later lane = latent dimension; each of the two groups of four
+//                warps has half of the columns.
+// The tile (128 x 576, 144 KB) has one buffer, released in five parts (four 128-dimension blocks after their product
+// with P, the rotated part after S, or after P when P takes its place).  Other ways to load were slower: to registers,
+// ahead of time, because what is in flight towards registers needs L1, of which this much shared memory leaves 28 KB
+// (a tile is 84 KB; the loads then wait for one another and hold up every other access to shared memory); by the copy
+// engine, which takes 73 cycles a row and 77 for four gathered pieces of 128 B (16-byte asynchronous copies: 16 KB in
+// 410 cycles from L2, 800 from HBM with every SM loading); prefetching rows into L2 gained nothing.
+#include <type_traits>
+
 #include "latent.cuh"
 #include "tc.cuh"
 
@@ -28,18 +42,26 @@ namespace hs {
 namespace {
 
 constexpr int kTile = 128;
-constexpr int kProducerWarps = 8;
-constexpr int kThreads = 512;  // four warpgroups; warps 13-15 only take part in the set-up
-constexpr int kMmaWarp = kProducerWarps + 4;
+constexpr int kProducerWarps = 16, kSoftmaxWarps = 8;
+constexpr int kMmaWarp = kProducerWarps + kSoftmaxWarps, kIdWarp = kMmaWarp + 1;
+constexpr int kThreads = (kMmaWarp + 4) * 32;
+constexpr int kAhead = 4;
 constexpr int kMaxCols = 64;
-constexpr int kRegsLaunch = 128, kRegsProducer = 144, kRegsSoftmax = 168, kRegsMma = 56;
-static_assert(2 * kRegsProducer + kRegsSoftmax + kRegsMma <= 4 * kRegsLaunch, "more registers than the launch has");
+constexpr int kRegsLaunch = 72, kRegsProducer = 64, kRegsSoftmax = 96, kRegsMma = 56;
+static_assert(kProducerWarps * kRegsProducer + kSoftmaxWarps * kRegsSoftmax + 4 * kRegsMma <=
+                  kThreads / 32 * kRegsLaunch,
+              "more registers than the launch has");
 template <int kRegs>
 __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs)); }
 template <int kRegs>
 __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs)); }
 constexpr int kSub = kTile * 128;  // bytes of a sub-tile: 128 keys x 64 bf16
-constexpr float kLazy = 64.f;      // log2 units by which a score may exceed the reference
+// In log2 units: where a new reference puts the largest score, and the most that a score may reach before it moves.
+// fp16 weights are normal from 2^-14 to 2^16; bf16 weights have fp32's range.
+template <bool kF16>
+struct Range {
+  static constexpr float kTop = kF16 ? 7.f : 0.f, kLazy = kF16 ? 15.f : 64.f;
+};
 
 // Workspace: partial results [2 per CTA][kMaxCols][512], their log2 sums [2 per CTA][kMaxCols], run starts [CTA].
 struct RunStart {
@@ -59,9 +81,8 @@ __device__ __forceinline__ int tiles_of(int keys) { return max(1, (keys + kTile 
 
 // Where a role is in the CTA's run of tiles.
 struct Cursor {
-  int item, group, tile, tiles, keys;
-  int64_t left;
-  __device__ __forceinline__ void start(const AttendParams& p, const RunStart& r, int64_t run) {
+  int item, group, tile, tiles, keys, left;
+  __device__ __forceinline__ void start(const AttendParams& p, const RunStart& r, int run) {
     item = r.item;
     group = r.off / r.tiles;
     tile = r.off - group * r.tiles;
@@ -110,21 +131,27 @@ struct Smem {
   static constexpr bool kAlias = N == 64;  // no room for P of 64 columns: it takes the key part's place
   static constexpr int kP = kAlias ? 8 * kSub : kQ + kQBytes;
   static constexpr int kMisc = kQ + kQBytes + (kAlias ? 0 : kTile * N * 2);
-  // misc: barriers, references, joined sums, column limits
-  static constexpr int kBytes = kMisc + 1024 + 16 * N * 4 + 1024;  // + alignment of the base
+  // misc: barriers (256 B), row ids [kAhead][128], results' offsets [N] (64 bits), then floats: references, factors,
+  // limits, scalars [N] each, joined values [4][N], query scales [2][N], key scales [128]
+  static constexpr int kIds = kMisc + 256;
+  static constexpr int kOffsets = kIds + kAhead * kTile * 4;
+  static constexpr int kRef = kOffsets + N * 8;
+  static constexpr int kQScale = 8 * N, kKeyScale = 10 * N;
+  static constexpr int kBytes = kRef + (10 * N + kTile) * 4 + 1024;  // + alignment of the base
 };
-enum Bar { kFull = 0, kEmpty = 5, kQFull = 10, kQEmpty, kSFull, kPReady, kOFull, kDrain, kBars };
+enum Bar { kFull = 0, kEmpty = 5, kQFull = 10, kQEmpty, kSFull, kPReady, kOFull, kDrain, kIdFull, kIdEmpty = kIdFull + kAhead,
+           kBars = kIdEmpty + kAhead };
+static_assert(kBars * 8 <= 256, "barriers");
 
 template <int N>
 constexpr int tmem_cols() { return N == 64 ? 512 : N == 32 ? 256 : 128; }
 
-// Reduction of N values over the warp's 32 lanes by halving: lane l ends with the results of columns
-// l * N / 32 .. (N = 16: column l / 2).
-template <int N, typename F>
+// Reduction of n values over the warp's 32 lanes by halving: lane l ends with the result of column l * n / 32.
+template <int n, typename F>
 __device__ __forceinline__ void halve(float* v, int lane, F f) {
 #pragma unroll
-  for (int half = N / 2, d = 16; d; half >>= 1, d >>= 1) {
-    if (half == 0) {  // N = 16: the two lanes of a column
+  for (int half = n / 2, d = 16; d; half >>= 1, d >>= 1) {
+    if (half == 0) {  // the lanes of a column
       v[0] = f(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], d));
     } else {
 #pragma unroll
@@ -137,32 +164,73 @@ __device__ __forceinline__ void halve(float* v, int lane, F f) {
   }
 }
 
-__device__ __forceinline__ uint4 ldg_row(const uint8_t* p) {
+// Loads from a row, or zeros: predicated, so that nothing waits for them before their use.
+template <int kOff>
+__device__ __forceinline__ uint4 ldg16(const uint8_t* p, bool there) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+      "mov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
+      "@p ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4 + %5];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(p), "n"(kOff), "r"((uint32_t)there));
   return v;
+}
+__device__ __forceinline__ float ldg_scale(const uint8_t* p, bool there) {
+  float v;
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.f32 %0, 0f00000000;\n\t@p ld.global.nc.f32 %0, [%1];\n\t}"
+               : "=&f"(v)
+               : "l"(p), "r"((uint32_t)there));
+  return v;
+}
+// 16 bytes to shared memory, asynchronously; zeros when there is nothing to copy.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void sts(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
-// 4 e4m3 codes times scale -> 4 bf16
-__device__ __forceinline__ uint2 dequant4(uint32_t w, float scale) {
-  uint32_t a, b;
+__device__ __forceinline__ void sts8(uint32_t a, uint32_t x, uint32_t y) {
+  asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(a), "r"(x), "r"(y) : "memory");
+}
+// 4 e4m3 codes -> 4 fp16
+__device__ __forceinline__ uint2 codes4(uint32_t w) {
+  uint2 r;
   asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-      : "=r"(a), "=r"(b)
+      : "=r"(r.x), "=r"(r.y)
       : "r"(w));
-  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a));
-  const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&b));
-  return make_uint2(tc::pack_bf16(x.x * scale, x.y * scale), tc::pack_bf16(y.x * scale, y.y * scale));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// 2 bf16 times a power of two -> 2 fp16
+__device__ __forceinline__ uint32_t bf16_to_half(uint32_t w, float f) {
+  return pack_half(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xFFFF0000u) * f);
+}
+// 2 codes (as fp16) times a scale, rounded to bf16, times a power of two -> 2 fp16
+__device__ __forceinline__ uint32_t scaled_half(uint32_t codes, float scale, float f) {
+  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&codes));
+  return bf16_to_half(tc::pack_bf16(x.x * scale, x.y * scale), f);
+}
+// Largest magnitude of 8 bf16 (NaN is passed over).
+__device__ __forceinline__ float max_bf16x8(uint4 v) {
+  uint32_t a = v.x & 0x7FFF7FFFu, b = v.y & 0x7FFF7FFFu, c = v.z & 0x7FFF7FFFu, d = v.w & 0x7FFF7FFFu;
+  asm("{\n\tmax.bf16x2 %0, %0, %1;\n\tmax.bf16x2 %2, %2, %3;\n\tmax.bf16x2 %0, %0, %2;\n\t}" : "+r"(a), "+r"(b), "+r"(c) : "r"(d));
+  return fmaxf(__uint_as_float(a << 16), __uint_as_float(a & 0xFFFF0000u));
 }
 
-__device__ __forceinline__ void bar_softmax() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void bar_softmax() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 __device__ __forceinline__ bool any_softmax(bool x) {
   uint32_t r;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
       : "r"((uint32_t)x)
       : "memory");
@@ -172,381 +240,502 @@ __device__ __forceinline__ bool any_softmax(bool x) {
 // ---------------------------------------------------------------------------------------------------------
 // Producers
 
-// Query tile of a unit: N columns x 576, zero for columns past the item's.
+// Query tile of a unit: N columns x 576, zero for columns past the item's; asynchronous copies (one group), which the
+// caller waits for.
 template <int N>
-__device__ __forceinline__ void load_queries(const AttendParams& p, uint32_t q, int item, int group, int tid) {
-  constexpr int kChunks = N * 72;  // 16-byte chunks: column-major over (column, chunk of the 576)
+__device__ __forceinline__ void copy_queries(const AttendParams& p, uint32_t q, int item, int group) {
+  constexpr int kPer = kProducerWarps * 32 / N;  // threads of a column
+  const int col = threadIdx.x / kPer, j0 = threadIdx.x % kPer;
+  const int c = group * N + col;
+  const int pos = p.P > 1 ? c / p.heads : 0, head = c - pos * p.heads;
+  const int64_t tok = (int64_t)item * p.P + pos;
+  const bool there = c < p.cols;
+  const __nv_bfloat16* lat = there ? p.q_latent + tok * p.ql_tok + head * p.ql_head : p.q_latent;
+  const __nv_bfloat16* rope = there ? p.q_rope + tok * p.qr_tok + head * p.qr_head : p.q_rope;
 #pragma unroll 3
-  for (int i = tid; i < kChunks; i += kProducerWarps * 32) {
-    const int col = i / 72, j = i - col * 72;
-    const int c = group * N + col;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (c < p.cols) {
-      const int pos = c / p.heads, head = c - pos * p.heads;
-      const int64_t tok = (int64_t)item * p.P + pos;
-      const __nv_bfloat16* src = j < 64 ? p.q_latent + tok * p.ql_tok + head * p.ql_head + 8 * j
-                                        : p.q_rope + tok * p.qr_tok + head * p.qr_head + 8 * (j - 64);
-      v = __ldg(reinterpret_cast<const uint4*>(src));
-    }
-    sts(q + (j >> 3) * (N * 128) + col * 128 + (((j & 7) ^ (col & 7)) << 4), v.x, v.y, v.z, v.w);
+  for (int j = j0; j < 72; j += kPer)
+    copy16(q + (j >> 3) * (N * 128) + col * 128 + (((j & 7) ^ (col & 7)) << 4), j < 64 ? lat + 8 * j : rope + 8 * (j - 64),
+           there);
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+// The same in fp16 by plain loads: a column is divided by qs, a power of two (mostly 1) that brings it into
+// fp16's range.  Two passes over the queries, so that few registers are needed beside the rows in flight.
+template <int N>
+__device__ __forceinline__ void convert_queries(const AttendParams& p, uint32_t q, float* qs, int item, int group) {
+  constexpr int kPer = kProducerWarps * 32 / N;  // threads of a column: neighbouring lanes
+  const int col = threadIdx.x / kPer, j0 = threadIdx.x % kPer;
+  const int c = group * N + col;
+  const int pos = p.P > 1 ? c / p.heads : 0, head = c - pos * p.heads;
+  const int64_t tok = (int64_t)item * p.P + pos;
+  const bool there = c < p.cols;
+  const __nv_bfloat16* lat = there ? p.q_latent + tok * p.ql_tok + head * p.ql_head : p.q_latent;
+  const __nv_bfloat16* rope = there ? p.q_rope + tok * p.qr_tok + head * p.qr_head : p.q_rope;
+  auto chunk = [&](int j) { return __ldg(reinterpret_cast<const uint4*>(j < 64 ? lat + 8 * j : rope + 8 * (j - 64))); };
+  float top = 0.f;
+#pragma unroll 3
+  for (int j = j0; j < 72; j += kPer) top = fmaxf(top, max_bf16x8(chunk(j)));
+#pragma unroll
+  for (int d = 1; d < kPer; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+  // left as they are when their largest magnitude is in 2^-2 .. 2^15: fp16 then keeps all but what is 2^-23 of it
+  const int b = (int)(__float_as_uint(top) >> 23);
+  const int e = top == 0.f || (b >= 125 && b < 142) ? 127 : min(max(b - 14, 1), 240);
+  const float f = there ? __uint_as_float((uint32_t)(254 - e) << 23) : 0.f;
+  if (j0 == 0) qs[col] = __uint_as_float((uint32_t)e << 23);
+#pragma unroll 3
+  for (int j = j0; j < 72; j += kPer) {
+    uint4 v = there ? chunk(j) : make_uint4(0, 0, 0, 0);
+    sts(q + (j >> 3) * (N * 128) + col * 128 + (((j & 7) ^ (col & 7)) << 4), bf16_to_half(v.x, f), bf16_to_half(v.y, f),
+        bf16_to_half(v.z, f), bf16_to_half(v.w, f));
   }
 }
 
-template <int N>
-__device__ __forceinline__ void produce_fp8(const AttendParams& p, uint32_t tile, uint32_t q, uint32_t bars, Cursor cur,
-                                            int groups, tc::Waiter& w) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int key0 = warp * 16 + (lane >> 3), j = lane & 7;  // this lane's keys key0 + 4 i, its 16-byte piece j
-  uint4 lat[4][4], rope[4];
-  float4 sc[4];
-  const uint8_t* row[4];
-  int ids[4];
-  bool bad = false;  // reported by the softmax warps
-
-  Cursor ahead = cur;  // the tile whose rows are fetched next
+// Part kPart of two rows.
+template <int kPart, int kPieces>
+__device__ __forceinline__ void load_part(const uint8_t* const (&row)[2], uint4 (&v)[kPieces][2]) {
+  constexpr int kAt = kPart * kPieces * 128;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int id = key_row(p, ahead.item, ahead.tile * kTile + key0 + 4 * i, ahead.keys, bad);
-    row[i] = id < 0 ? nullptr : p.base + (int64_t)id * HS_ROW_BYTES_FP8;
+  for (int i = 0; i < 2; ++i) {
+    v[0][i] = ldg16<kAt>(row[i], true);
+    if (kPieces == 2) v[kPieces - 1][i] = ldg16<kAt + 128>(row[i], true);
   }
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  auto fetch = [&](int c, int i) { lat[c][i] = row[i] ? ldg_row(row[i] + 128 * c + 16 * j) : zero; };
-  auto fetch_rope = [&](int i) { rope[i] = row[i] ? ldg_row(row[i] + 528 + 16 * j) : zero; };
-  auto fetch_scales = [&](int i) {
-    const uint4 s = row[i] ? ldg_row(row[i] + 512) : zero;
-    sc[i] = make_float4(__uint_as_float(s.x), __uint_as_float(s.y), __uint_as_float(s.z), __uint_as_float(s.w));
-  };
-#pragma unroll
-  for (int i = 0; i < 4; ++i) fetch_scales(i);
-#pragma unroll
-  for (int c = 0; c < 4; ++c)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) fetch(c, i);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) fetch_rope(i);
-  ahead.next(p, groups);
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    ids[i] = ahead.left > 0 ? key_row(p, ahead.item, ahead.tile * kTile + key0 + 4 * i, ahead.keys, bad) : -1;
+}
 
-  bool fresh = true;
-  uint32_t it = 0, seg = 0;
-  while (cur.left > 0) {
-    if (fresh) {
-      if (seg > 0) w.wait(bars + 8 * kQEmpty, (seg - 1) & 1);
-      load_queries<N>(p, q, cur.item, cur.group, threadIdx.x);
-      tc::fence_async_smem();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(bars + 8 * kQFull);
-      ++seg;
+template <int N, bool kF16>
+__device__ __forceinline__ void produce_tiles(const AttendParams& p, uint32_t tile, uint32_t q, const int* ids, float* qs,
+                                              float* skey, uint32_t bars, Cursor cur, int groups, tc::Waiter& w) {
+  constexpr int kRowBytes = kF16 ? HS_ROW_BYTES_FP8 : HS_ROW_BYTES_BF16;
+  constexpr int kPieces = kF16 ? 1 : 2;  // 128-byte pieces of a row in a part
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int sub = lane >> 3, j = lane & 7;
+  const int key0 = warp * 8 + sub;  // this lane's keys key0 and key0 + 4, its 16-byte piece j
+  uint4 even[kPieces][2], odd[kPieces][2];  // parts 0, 2 and 1, 3 on their way
+  uint4 rope[2];
+  float sc[2];  // lanes j and j + 4 of a key hold its scale of group j
+  const uint8_t* row[2];
+  uint32_t missing = 0, missing_next = 0;  // bit i: key key0 + 4 i has no row (row 0 is read and replaced by zeros)
+  auto take_ids = [&](uint32_t t) {
+    const int slot = t % kAhead;
+    w.wait(bars + 8 * (kIdFull + slot), (t / kAhead) & 1);
+    const int a = ids[slot * kTile + key0], b = ids[slot * kTile + key0 + 4];
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(bars + 8 * (kIdEmpty + slot));
+    missing_next = (a < 0 ? 1u : 0u) | (b < 0 ? 2u : 0u);
+    row[0] = p.base + (int64_t)max(a, 0) * kRowBytes + 16 * j;
+    row[1] = p.base + (int64_t)max(b, 0) * kRowBytes + 16 * j;
+  };
+  auto load_rest = [&]() {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (kF16) sc[i] = ldg_scale(row[i] + kLatent + 4 * (j & 3) - 16 * j, true);
+      rope[i] = ldg16<kRowBytes - 128>(row[i], true);
     }
-    // rows of the tile ahead; their ids arrived during the last tile
+  };
+  // where this lane stores: lanes of the upper sub-tile store the halves of their 16 values in the other order, so that
+  // no two lanes of a store share a bank
+  const bool flip = kF16 && (j >> 2);
+  uint32_t at[2][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) row[i] = ids[i] < 0 ? nullptr : p.base + (int64_t)ids[i] * HS_ROW_BYTES_FP8;
-    const bool more = ahead.left > 0;
-    if (more) ahead.next(p, groups);
+  for (int i = 0; i < 2; ++i) {
+    const int swz = sub + 4 * i;  // key % 8
+    const uint32_t to = tile + (key0 + 4 * i) * 128;
+    if (kF16) {
+      at[i][0] = to + (j >> 2) * kSub + ((((j & 3) * 2 + flip) ^ swz) << 4);
+      at[i][1] = to + (j >> 2) * kSub + ((((j & 3) * 2 + !flip) ^ swz) << 4);
+    } else {
+      at[i][0] = to + ((j ^ swz) << 4);
+      at[i][1] = at[i][0] + kSub;
+    }
+  }
+  float inv[2];
+  uint32_t ratio[2];
+  bool exact = true;  // every scale is a power of two
+  auto store = [&](int c, uint4 (&v)[kPieces][2]) {
+    const uint32_t off = 2 * c * kSub;
+    if (missing) {  // (never the whole warp's business: a lane's own rows)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      ids[i] = ahead.left > 0 ? key_row(p, ahead.item, ahead.tile * kTile + key0 + 4 * i, ahead.keys, bad) : -1;
+      for (int i = 0; i < 2; ++i)
+        if (missing >> i & 1)
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      if (it > 0) w.wait(bars + 8 * (kEmpty + c), (it - 1) & 1);
-      const uint32_t sub = tile + (2 * c + (j >> 2)) * kSub;
+          for (int x = 0; x < kPieces; ++x) v[x][i] = make_uint4(0, 0, 0, 0);
+    }
+    __syncwarp();
+    if constexpr (kF16) {
+      const int from = (lane & 24) | c;
+      if (exact) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int key = key0 + 4 * i;
-        const float s = c == 0 ? sc[i].x : c == 1 ? sc[i].y : c == 2 ? sc[i].z : sc[i].w;
-        const uint2 a = dequant4(lat[c][i].x, s), b = dequant4(lat[c][i].y, s);
-        const uint2 d = dequant4(lat[c][i].z, s), e = dequant4(lat[c][i].w, s);
-        const uint32_t at = sub + key * 128;
-        const int ch = (j & 3) * 2;
-        // lanes of the upper sub-tile write their halves in the other order: no two lanes of a store share a bank
-        const bool flip = j >> 2;
-        sts(at + (((ch + flip) ^ (key & 7)) << 4), flip ? d.x : a.x, flip ? d.y : a.y, flip ? e.x : b.x, flip ? e.y : b.y);
-        sts(at + (((ch + !flip) ^ (key & 7)) << 4), flip ? a.x : d.x, flip ? a.y : d.y, flip ? b.x : e.x, flip ? b.y : e.y);
-        if (more) {
-          fetch(c, i);
-          if (c == 3) fetch_scales(i);
+        for (int i = 0; i < 2; ++i) {
+          const uint4 u = v[0][i];
+          const uint32_t r = __shfl_sync(0xFFFFFFFFu, ratio[i], from);
+          const uint2 a = codes4(flip ? u.z : u.x), b = codes4(flip ? u.w : u.y);
+          const uint2 d = codes4(flip ? u.x : u.z), e = codes4(flip ? u.y : u.w);
+          sts(at[i][0] + off, mul_half2(a.x, r), mul_half2(a.y, r), mul_half2(b.x, r), mul_half2(b.y, r));
+          sts(at[i][1] + off, mul_half2(d.x, r), mul_half2(d.y, r), mul_half2(e.x, r), mul_half2(e.y, r));
+        }
+      } else {
+#pragma unroll 1
+        for (int n = 0; n < 8; ++n) {  // a word of four codes at a time
+          const int i = n >> 2, word = n & 3;
+          const uint4 u = i ? v[0][1] : v[0][0];
+          const float z = __shfl_sync(0xFFFFFFFFu, i ? sc[1] : sc[0], from), f = i ? inv[1] : inv[0];
+          const uint2 a = codes4(word == 0 ? u.x : word == 1 ? u.y : word == 2 ? u.z : u.w);
+          const bool second = (word >> 1) != (int)flip;
+          const uint32_t to = i ? (second ? at[1][1] : at[1][0]) : (second ? at[0][1] : at[0][0]);
+          sts8(to + off + (word & 1) * 8, scaled_half(a.x, z, f), scaled_half(a.y, z, f));
         }
       }
-      tc::fence_async_smem();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(bars + 8 * (kFull + c));
-    }
-    if (it > 0) w.wait(bars + 8 * (kEmpty + 4), (it - 1) & 1);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int key = key0 + 4 * i;
-      sts(tile + 8 * kSub + key * 128 + ((j ^ (key & 7)) << 4), rope[i].x, rope[i].y, rope[i].z, rope[i].w);
-      if (more) fetch_rope(i);
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int x = 0; x < kPieces; ++x) sts(at[i][x] + off, v[x][i].x, v[x][i].y, v[x][i].z, v[x][i].w);
     }
+  };
+  auto signal = [&](int bar) {
     tc::fence_async_smem();
     __syncwarp();
-    if (lane == 0) tc::mbar_arrive(bars + 8 * (kFull + 4));
-    fresh = cur.next(p, groups);
+    if (lane == 0) tc::mbar_arrive(bars + 8 * bar);
+  };
+  take_ids(0);
+  load_rest();
+  load_part<0, kPieces>(row, even);
+  load_part<1, kPieces>(row, odd);
+  bool fresh = true;
+  uint32_t it = 0, seg = 0;
+#pragma unroll 1
+  while (cur.left > 0) {
+    if (fresh) {
+      if (seg > 0) w.wait(bars + 8 * kQEmpty, (seg - 1) & 1);
+      if (kF16) {
+        convert_queries<N>(p, q, qs + (seg & 1) * N, cur.item, cur.group);
+      } else {
+        copy_queries<N>(p, q, cur.item, cur.group);
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+      }
+      signal(kQFull);
+      ++seg;
+    }
+    missing = missing_next;
+    if (kF16) {
+      // skey: 2^7 below the power of two that covers the largest scale (codes reach 448 * 2^7 < 65504), and so that the
+      // rotated part stays below 2^15
+      exact = true;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (missing >> i & 1) sc[i] = 0.f, rope[i] = make_uint4(0, 0, 0, 0);
+        const uint32_t sb = __float_as_uint(sc[i]) & 0x7FFFFFFFu;
+        exact &= (sb & 0x7FFFFFu) == 0;
+        int e = (int)(sb >> 23) + ((sb & 0x7FFFFFu) ? 1 : 0) - 7;
+        e = max(e, (int)(__float_as_uint(max_bf16x8(rope[i])) >> 23) + 1 - 15);
+#pragma unroll
+        for (int d = 1; d < 8; d <<= 1) e = max(e, __shfl_xor_sync(0xFFFFFFFFu, e, d));
+        e = min(max(e, 1), 240);
+        inv[i] = __uint_as_float((uint32_t)(254 - e) << 23);
+        const float r = sc[i] * inv[i];
+        ratio[i] = pack_half(r, r);
+      }
+      exact = __all_sync(0xFFFFFFFFu, exact);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (missing >> i & 1) rope[i] = make_uint4(0, 0, 0, 0);
+    }
+    auto free_part = [&](int c) {
+      if (it > 0) w.wait(bars + 8 * (kEmpty + c), (it - 1) & 1);
+    };
+    free_part(0);
+    if (kF16 && j == 0) {  // the softmax of the tile before has read its own
+      skey[key0] = 1.f / inv[0];
+      skey[key0 + 4] = 1.f / inv[1];
+    }
+    store(0, even);
+    signal(kFull + 0);
+    load_part<2, kPieces>(row, even);
+    free_part(1);
+    store(1, odd);
+    signal(kFull + 1);
+    load_part<3, kPieces>(row, odd);
+    const bool next_fresh = cur.next(p, groups);
+    const bool more = cur.left > 0;
+    if (more) take_ids(it + 1);
+    free_part(2);
+    store(2, even);
+    signal(kFull + 2);
+    if (more) load_part<0, kPieces>(row, even);
+    free_part(3);
+    store(3, odd);
+    signal(kFull + 3);
+    if (more) load_part<1, kPieces>(row, odd);
+    free_part(4);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t to = tile + 8 * kSub + (key0 + 4 * i) * 128 + ((j ^ (sub + 4 * i)) << 4);
+      if (kF16)
+        sts(to, bf16_to_half(rope[i].x, inv[i]), bf16_to_half(rope[i].y, inv[i]), bf16_to_half(rope[i].z, inv[i]),
+            bf16_to_half(rope[i].w, inv[i]));
+      else
+        sts(to, rope[i].x, rope[i].y, rope[i].z, rope[i].w);
+    }
+    signal(kFull + 4);
+    if (more) load_rest();
+    fresh = next_fresh;
     ++it;
   }
 }
 
-// bf16 rows need no conversion: 16-byte asynchronous copies straight into the swizzled tile, the next tile's rows
-// prefetched into L2 meanwhile.
-template <int N>
-__device__ __forceinline__ void produce_bf16(const AttendParams& p, uint32_t tile, uint32_t q, uint32_t bars, Cursor cur,
-                                             int groups, tc::Waiter& w) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int key0 = warp * 16 + (lane >> 3), j = lane & 7;
-  bool bad = false;
-  bool fresh = true;
-  uint32_t it = 0, seg = 0;
-  int ids[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) ids[i] = key_row(p, cur.item, cur.tile * kTile + key0 + 4 * i, cur.keys, bad);
+// Row ids of the tiles to come (one warp).
+__device__ __forceinline__ void resolve_rows(const AttendParams& p, int* ids, uint32_t bars, Cursor cur, int groups,
+                                              tc::Waiter& w) {
+  const int lane = threadIdx.x & 31;
+  uint32_t it = 0;
+  bool any_bad = false;
+#pragma unroll 1
   while (cur.left > 0) {
-    if (fresh) {
-      if (seg > 0) w.wait(bars + 8 * kQEmpty, (seg - 1) & 1);
-      load_queries<N>(p, q, cur.item, cur.group, threadIdx.x);
-      tc::fence_async_smem();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(bars + 8 * kQFull);
-      ++seg;
-    }
-    const uint8_t* row[4];
+    const int slot = it % kAhead;
+    int id[4];
+    bool bad = false;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) row[i] = ids[i] < 0 ? nullptr : p.base + (int64_t)ids[i] * HS_ROW_BYTES_BF16;
-    Cursor ahead = cur;
-    fresh = ahead.next(p, groups);
+    for (int i = 0; i < 4; ++i) id[i] = key_row(p, cur.item, cur.tile * kTile + lane + 32 * i, cur.keys, bad);
+    any_bad |= bad && cur.group == 0;
+    if (it >= kAhead) w.wait(bars + 8 * (kIdEmpty + slot), (it / kAhead - 1) & 1);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      ids[i] = ahead.left > 0 ? key_row(p, ahead.item, ahead.tile * kTile + key0 + 4 * i, ahead.keys, bad) : -1;
-    auto copy = [&](int sub, int i) {
-      const int key = key0 + 4 * i;
-      const uint32_t dst = tile + sub * kSub + key * 128 + ((j ^ (key & 7)) << 4);
-      const uint8_t* src = row[i] ? row[i] + 128 * sub + 16 * j : p.base;
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(row[i] ? 16 : 0) : "memory");
-    };
-    // part c is signalled once the copies of part c + 1 have been issued
-#pragma unroll
-    for (int c = 0; c < 6; ++c) {
-      if (c < 5) {
-        if (it > 0) w.wait(bars + 8 * (kEmpty + c), (it - 1) & 1);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (c < 4) {
-            copy(2 * c, i);
-            copy(2 * c + 1, i);
-          } else {
-            copy(8, i);
-          }
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        if (c == 1) {  // the ids of the next tile have arrived by now
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (ids[i] >= 0) {
-              const uint8_t* r = p.base + (int64_t)ids[i] * HS_ROW_BYTES_BF16;
-              asm volatile("prefetch.global.L2 [%0];" ::"l"(r + 128 * j));
-              if (j == 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(r + 1024));
-            }
-        }
-      }
-      if (c > 0) {
-        if (c < 5)
-          asm volatile("cp.async.wait_group 1;" ::: "memory");
-        else
-          asm volatile("cp.async.wait_group 0;" ::: "memory");
-        tc::fence_async_smem();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(bars + 8 * (kFull + c - 1));
-      }
-    }
-    cur = ahead;
+    for (int i = 0; i < 4; ++i) ids[slot * kTile + lane + 32 * i] = id[i];
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(bars + 8 * (kIdFull + slot));
+    cur.next(p, groups);
     ++it;
   }
+  if (any_bad) report(p.status, p.paged ? HS_ERR_TABLE_RANGE : HS_ERR_ID_RANGE);
 }
 
 // ---------------------------------------------------------------------------------------------------------
-// Products (one thread)
+// Products (one warp)
 
-template <int N>
+template <int N, bool kF16>
 __device__ __forceinline__ void issue_products(const AttendParams& p, uint32_t tile, uint32_t q, uint32_t pt, uint32_t bars,
                                                uint32_t tmem, Cursor cur, int groups, tc::Waiter& w) {
   using L = Smem<N>;
-  constexpr uint32_t kIdS = tc::idesc_bf16(128, N, false, false);
-  constexpr uint32_t kIdO = tc::idesc_bf16(128, N, true, true);
+  constexpr uint32_t kIdS = tc::idesc(kF16, 128, N, false, false);
+  constexpr uint32_t kIdO = tc::idesc(kF16, 128, N, true, true);
   constexpr uint64_t kPSwizzle = N == 64 ? tc::kSwizzle128 : N == 32 ? tc::kSwizzle64 : tc::kSwizzle32;
+  const uint64_t dk = tc::desc(tile, 16, 1024, tc::kSwizzle128);    // tile as keys (K-major)
+  const uint64_t dv = tc::desc(tile, kSub, 1024, tc::kSwizzle128);  // tile as values (M-major)
+  const uint64_t dq = tc::desc(q, 16, 1024, tc::kSwizzle128);
+  const uint64_t dp = tc::desc(pt, 16, 8 * N * 2, kPSwizzle);
+  const bool leader = tc::elect();
+  auto await = [&](int bar, uint32_t parity) {
+    w.wait(bars + 8 * bar, parity);
+    __syncwarp();
+    tc::fence_after();
+  };
   bool fresh = true;
   uint32_t it = 0, seg = 0;
+#pragma unroll 1
   while (cur.left > 0) {
-    if (fresh) w.wait(bars + 8 * kQFull, seg & 1);
+    if (fresh) await(kQFull, seg & 1);
     const bool first = fresh;
-#pragma unroll
+#pragma unroll 1
     for (int c = 0; c < 5; ++c) {
-      w.wait(bars + 8 * (kFull + c), it & 1);
-      tc::fence_after();
-#pragma unroll
-      for (int k = 0; k < (c < 4 ? 8 : 4); ++k) {
-        const int sub = 2 * c + (k >> 2), in = (k & 3) * 32;
-        tc::mma_ss(tmem, tc::desc(tile + sub * kSub + in, 16, 1024, tc::kSwizzle128),
-                   tc::desc(q + sub * (N * 128) + in, 16, 1024, tc::kSwizzle128), kIdS, c > 0 || k > 0);
-      }
-    }
-    tc::commit(bars + 8 * kSFull);
-    if (!L::kAlias) tc::commit(bars + 8 * (kEmpty + 4));
-    fresh = cur.next(p, groups);
-    const bool last = fresh || cur.left == 0;
-    if (last) tc::commit(bars + 8 * kQEmpty);
-    w.wait(bars + 8 * kPReady, it & 1);
-    tc::fence_after();
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
+      await(kFull + c, it & 1);
+      const uint64_t a = dk + (uint32_t)(2 * c * kSub >> 4), b = dq + (uint32_t)(2 * c * (N * 128) >> 4);
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        tc::mma_ss(tmem + N + g * N, tc::desc(tile + 2 * g * kSub + k * 2048, kSub, 1024, tc::kSwizzle128),
-                   tc::desc(pt + k * 16 * N * 2, 16, 8 * N * 2, kPSwizzle), kIdO, !first || k > 0);
-      tc::commit(bars + 8 * (kEmpty + g));
+        if (k < 4 || c < 4)
+          tc::mma_ss(tmem, a + (((k >> 2) * kSub + (k & 3) * 32) >> 4), b + (((k >> 2) * (N * 128) + (k & 3) * 32) >> 4), kIdS,
+                     c > 0 || k > 0, leader);
     }
-    if (L::kAlias) tc::commit(bars + 8 * (kEmpty + 4));
+    tc::commit(bars + 8 * kSFull, leader);
+    if (!L::kAlias) tc::commit(bars + 8 * (kEmpty + 4), leader);
+    fresh = cur.next(p, groups);
+    const bool last = fresh || cur.left == 0;
+    if (last) tc::commit(bars + 8 * kQEmpty, leader);
+    await(kPReady, it & 1);
+#pragma unroll 1
+    for (int g = 0; g < 4; ++g) {
+      const uint64_t a = dv + (uint32_t)(2 * g * kSub >> 4);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        tc::mma_ss(tmem + N + g * N, a + (k * 2048 >> 4), dp + ((k * 16 * N * 2) >> 4), kIdO, !first || k > 0, leader);
+      tc::commit(bars + 8 * (kEmpty + g), leader);
+    }
+    if (L::kAlias) tc::commit(bars + 8 * (kEmpty + 4), leader);
     if (last) {
-      tc::commit(bars + 8 * kOFull);
+      tc::commit(bars + 8 * kOFull, leader);
       ++seg;
     }
     ++it;
   }
   // nothing of this CTA's products is in flight when the others leave
-  tc::commit(bars + 8 * kDrain);
+  tc::commit(bars + 8 * kDrain, leader);
   tc::Waiter drain;
   drain.wait(bars + 8 * kDrain, 0);
+  __syncwarp();
 }
 
 // ---------------------------------------------------------------------------------------------------------
-// Softmax and results (128 threads)
+// Softmax and results
 
-template <int N>
-__device__ __forceinline__ void softmax(const AttendParams& p, uint32_t pt, uint32_t bars, uint32_t tmem, float* ref,
-                                        float* red, Cursor cur, int groups, int sms, tc::Waiter& w) {
+template <int N, bool kF16>
+__device__ __forceinline__ void softmax(const AttendParams& p, uint32_t pt, uint32_t bars, uint32_t tmem, float* nref,
+                                        int64_t* offsets, const int* ids, Cursor cur, int groups, int sms, tc::Waiter& w) {
+  constexpr float kTop = Range<kF16>::kTop, kLazy = Range<kF16>::kLazy;
+  constexpr int kW = N / 2;  // columns of this thread
   const int tid = threadIdx.x - kProducerWarps * 32;
-  const int lane = tid & 31, warp = tid >> 5;
-  const uint32_t tm = tmem + ((uint32_t)(32 * warp) << 16);  // this warp's lanes
-  float* alpha = ref + N;                                    // [N] rescale factors, then 1 / sum
-  int* limit = reinterpret_cast<int*>(ref + 2 * N);          // [N] keys that a column sees
+  const int lane = tid & 31, warp = (tid >> 5) & 3;
+  const int c0 = (tid >> 7) * kW;                                 // its first column
+  const int key = tid & 127;                                      // its key in the tile
+  const uint32_t tm = tmem + ((uint32_t)(32 * warp) << 16) + c0;  // its warp's lanes, its columns
+  // nref: [N] the references, negated (+infinity: none yet)
+  float* alpha = nref + N;                             // [N] rescale factors, then result factors
+  int* limit = reinterpret_cast<int*>(nref + 2 * N);   // [N] keys that a column sees
+  float* scalars = nref + 3 * N;                       // skey0, its change, the warps' largest skey [4]
+  float* red = nref + 4 * N;                           // [4][N] the warps' maxima or sums
+  const float* skey = nref + Smem<N>::kKeyScale;
+  const int col = c0 + lane * kW / 32;                 // where halve() leaves this lane's result
   bool fresh = true, at_start = false;
   bool first_run = true;  // this CTA's first segment
+  bool scaled = false;    // some column of the unit has a qs other than 1
   uint32_t it = 0, seg = 0;
-  float l[N];
+  float2 l[kW / 2];
+#pragma unroll 1
   while (cur.left > 0) {
     const int item = cur.item, group = cur.group;
-    const int ncols = min(N, p.cols - group * N);
+    const float* qs = nref + Smem<N>::kQScale + (seg & 1) * N + c0;
     if (fresh) {
       at_start = cur.tile == 0;
       if (tid < N) {
-        ref[tid] = -INFINITY;
+        nref[tid] = INFINITY;
         const int c = min(group * N + tid, p.cols - 1);
-        limit[tid] = p.paged ? __ldg(p.ctx_len + item) - p.P + 1 + c / p.heads : p.K;
+        const int pos = p.P > 1 ? c / p.heads : 0;
+        limit[tid] = p.paged ? __ldg(p.ctx_len + item) - p.P + 1 + pos : p.K;
+        offsets[tid] = ((int64_t)item * p.P + pos) * p.out_tok + (c - pos * p.heads) * p.out_head;
       }
+      if (tid == 0) scalars[0] = 0.f;
 #pragma unroll
-      for (int c = 0; c < N; ++c) l[c] = 0.f;
+      for (int c = 0; c < kW / 2; ++c) l[c] = make_float2(0.f, 0.f);
       bar_softmax();
     }
-    const int k = cur.tile * kTile + tid;
-    bool bad = false;
-    const bool there = key_row(p, item, k, cur.keys, bad) >= 0;
-    if (bad && group == 0) report(p.status, p.paged ? HS_ERR_TABLE_RANGE : HS_ERR_ID_RANGE);
+    const int k = cur.tile * kTile + key;
+    const int slot = it % kAhead;
+    w.wait(bars + 8 * (kIdFull + slot), (it / kAhead) & 1);
+    const bool there = ids[slot * kTile + key] >= 0;
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(bars + 8 * (kIdEmpty + slot));
     // columns differ in what they see only in the last P - 1 keys
     const bool ragged = p.paged && p.P > 1 && (cur.tile + 1) * kTile > limit[0];
+    const bool masks = !__all_sync(0xFFFFFFFFu, there) || ragged;
     const bool first = fresh;
+    float sk = 1.f, mult = p.scale_log2;
+    if (kF16) {
+      w.wait(bars + 8 * kFull, it & 1);  // makes skey and qs visible
+      sk = skey[key];
+      mult *= sk;
+      if (fresh) scaled = __any_sync(0xFFFFFFFFu, qs[lane % kW] != 1.f);
+    }
     w.wait(bars + 8 * kSFull, it & 1);
     __syncwarp();
     tc::fence_after();
-    float s[N];
-    auto scores = [&]() {
-#pragma unroll
-      for (int c = 0; c < N; c += 16) tc::tmem_ld16(tm + c, s + c);
+    // this thread's scores in log2 units, less the references or not; -infinity where the key is hidden
+    float s[kW];
+    auto scores = [&](bool relative) {
+      tc::tmem_ld<kW>(tm, s);
       tc::tmem_wait_ld();
-      tc::touch<N>(s);
+      tc::touch<kW>(s);
+      if (kF16 && scaled) {
 #pragma unroll
-      for (int c = 0; c < N; ++c) {
-        s[c] *= p.scale_log2;
-        if (!there) s[c] = -INFINITY;
+        for (int c = 0; c < kW; ++c) s[c] *= qs[c];
       }
-      if (ragged) {
+      const float2 m2 = make_float2(mult, mult);
 #pragma unroll
-        for (int c = 0; c < N; ++c)
-          if (k >= limit[c]) s[c] = -INFINITY;
+      for (int c = 0; c < kW; c += 4) {
+        const float4 m = *reinterpret_cast<const float4*>(nref + c0 + c);
+        const float2 x = tc::fma2(make_float2(s[c], s[c + 1]), m2, relative ? make_float2(m.x, m.y) : make_float2(0.f, 0.f));
+        const float2 y = tc::fma2(make_float2(s[c + 2], s[c + 3]), m2, relative ? make_float2(m.z, m.w) : make_float2(0.f, 0.f));
+        s[c] = x.x, s[c + 1] = x.y, s[c + 2] = y.x, s[c + 3] = y.y;
+      }
+      if (masks) {
+#pragma unroll
+        for (int c = 0; c < kW; ++c)
+          if (!there || (ragged && k >= limit[c0 + c])) s[c] = -INFINITY;
       }
     };
-    scores();
-    bool over = false;
+    // twice at most: with the references as they are, and again if one had to move
+    bool moved = false;
+#pragma unroll 1
+    while (true) {
+      scores(true);
+      float top = s[0];
 #pragma unroll
-    for (int c = 0; c < N; c += 4) {
-      const float4 m = *reinterpret_cast<const float4*>(ref + c);
-      const float mm[4] = {m.x, m.y, m.z, m.w};
+      for (int c = 1; c < kW; ++c) top = fmaxf(top, s[c]);
+      if (moved || !any_softmax(top > kLazy || (kF16 && there && sk > scalars[0]))) break;
+      moved = true;
+      // a new reference for every column, kTop below the maximum of the old one's and this tile's scores
+      scores(false);
+      halve<kW>(s, lane, [](float a, float b) { return fmaxf(a, b); });
+      red[warp * N + col] = s[0];
+      if (kF16) {
+        float z = there ? sk : 0.f;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) over |= s[c + x] > mm[x] + kLazy;
-    }
-    if (any_softmax(over)) {
-      // a new reference for every column: the maximum of the old one and this tile's scores
-      halve<N>(s, lane, [](float a, float b) { return fmaxf(a, b); });
-      if (N == 64) {
-        red[warp * N + 2 * lane] = s[0];
-        red[warp * N + 2 * lane + 1] = s[1];
-      } else if (N == 32) {
-        red[warp * N + lane] = s[0];
-      } else {
-        red[warp * N + (lane >> 1)] = s[0];
+        for (int d = 1; d < 32; d <<= 1) z = fmaxf(z, __shfl_xor_sync(0xFFFFFFFFu, z, d));
+        if (lane == 0) scalars[2 + warp] = z;
       }
       bar_softmax();
       if (tid < N) {
-        const float old = ref[tid];
-        const float top = fmaxf(fmaxf(fmaxf(red[tid], red[N + tid]), fmaxf(red[2 * N + tid], red[3 * N + tid])), old);
-        ref[tid] = top;
-        alpha[tid] = old == -INFINITY ? 0.f : exp2f(old - top);
+        const float old = -nref[tid];
+        const float now = fmaxf(fmaxf(fmaxf(red[tid], red[N + tid]), fmaxf(red[2 * N + tid], red[3 * N + tid])) - kTop, old);
+        nref[tid] = -now;
+        alpha[tid] = old == -INFINITY ? 0.f : exp2f(old - now);
+      }
+      if (kF16 && tid == N) {
+        const float old = scalars[0];
+        const float now = fmaxf(fmaxf(fmaxf(scalars[2], scalars[3]), fmaxf(scalars[4], scalars[5])), old);
+        scalars[0] = now;
+        scalars[1] = now > 0.f ? old / now : 1.f;
       }
       bar_softmax();
 #pragma unroll
-      for (int c = 0; c < N; ++c) l[c] *= alpha[c];
+      for (int c = 0; c < kW / 2; ++c) l[c].x *= alpha[c0 + 2 * c], l[c].y *= alpha[c0 + 2 * c + 1];
       if (!first) {
         // the products of the tiles before have finished: they were committed before these scores
+        const float change = kF16 ? scalars[1] : 1.f;
 #pragma unroll 1
-        for (int g = 0; g < 4; ++g) {
+        for (int c = 0; c < 4 * kW; c += 8) {
+          const int g = c / kW, x0 = c % kW;
+          float o[8];
+          tc::tmem_ld<8>(tm + N + g * N + x0, o);
+          tc::tmem_wait_ld();
+          tc::touch<8>(o);
 #pragma unroll
-          for (int c = 0; c < N; c += 16) {
-            float o[16];
-            tc::tmem_ld16(tm + N + g * N + c, o);
-            tc::tmem_wait_ld();
-            tc::touch<16>(o);
-#pragma unroll
-            for (int x = 0; x < 16; ++x) o[x] *= alpha[c + x];
-            tc::tmem_st16(tm + N + g * N + c, o);
-          }
+          for (int x = 0; x < 8; ++x) o[x] *= alpha[c0 + x0 + x] * change;
+          tc::tmem_st8(tm + N + g * N + x0, o);
         }
         tc::tmem_wait_st();
       }
-      scores();
     }
     // weights, their sums per lane, and P^T: [key][column], 2 N bytes a key, swizzled like the descriptor says
+    const float share = kF16 ? (there ? sk / scalars[0] : 0.f) : 1.f;
+    const float2 share2 = make_float2(share, share);
 #pragma unroll
-    for (int c = 0; c < N; c += 8) {
+    for (int c = 0; c < kW; c += 8) {
       uint32_t out[4];
 #pragma unroll
-      for (int x = 0; x < 8; x += 4) {
-        const float4 m = *reinterpret_cast<const float4*>(ref + c + x);
-        const float mm[4] = {m.x, m.y, m.z, m.w};
-        float e[4];
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const float v = s[c + x + y];
-          e[y] = v == -INFINITY ? 0.f : tc::exp2_fast(v - mm[y]);
-          l[c + x + y] += e[y];
+      for (int x = 0; x < 4; ++x) {
+        float2 e = make_float2(tc::exp2_fast(s[c + 2 * x]), tc::exp2_fast(s[c + 2 * x + 1]));
+        l[c / 2 + x] = tc::add2(l[c / 2 + x], e);
+        if (kF16) {
+          e = tc::mul2(e, share2);
+          out[x] = pack_half(e.x, e.y);
+        } else {
+          out[x] = tc::pack_bf16(e.x, e.y);
         }
-        out[x / 2] = tc::pack_bf16(e[0], e[1]);
-        out[x / 2 + 1] = tc::pack_bf16(e[2], e[3]);
       }
-      const int sw = N == 64 ? (tid & 7) : N == 32 ? ((tid >> 1) & 3) : ((tid >> 2) & 1);
-      sts(pt + tid * (2 * N) + (((c / 8) ^ sw) << 4), out[0], out[1], out[2], out[3]);
+      const int sw = N == 64 ? (key & 7) : N == 32 ? ((key >> 1) & 3) : ((key >> 2) & 1);
+      sts(pt + key * (2 * N) + ((((c0 + c) / 8) ^ sw) << 4), out[0], out[1], out[2], out[3]);
     }
     tc::fence_async_smem();
     tc::fence_before();
-    tc::mbar_arrive(bars + 8 * kPReady);
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(bars + 8 * kPReady);
 
     const int unit_tiles = cur.tiles, tile = cur.tile;
     fresh = cur.next(p, groups);
@@ -555,28 +744,22 @@ __device__ __forceinline__ void softmax(const AttendParams& p, uint32_t pt, uint
 
     // the segment ends: join the sums, then the results
     const bool whole = at_start && tile + 1 == unit_tiles;
-    halve<N>(l, lane, [](float a, float b) { return a + b; });
-    if (N == 64) {
-      red[warp * N + 2 * lane] = l[0];
-      red[warp * N + 2 * lane + 1] = l[1];
-    } else if (N == 32) {
-      red[warp * N + lane] = l[0];
-    } else {
-      red[warp * N + (lane >> 1)] = l[0];
-    }
+    const int ncols = min(N, p.cols - group * N);
+    float* sums = reinterpret_cast<float*>(l);
+    halve<kW>(sums, lane, [](float a, float b) { return a + b; });
+    red[warp * N + col] = sums[0];
     bar_softmax();
-    const int slot = 2 * blockIdx.x + (first_run && !at_start ? 0 : 1);
+    const int part = 2 * blockIdx.x + (first_run && !at_start ? 0 : 1);
     first_run = false;
     if (tid < N) {
       const float sum = (red[tid] + red[N + tid]) + (red[2 * N + tid] + red[3 * N + tid]);
-      const float lse2 = sum == 0.f ? -INFINITY : ref[tid] + log2f(sum);
+      const float lse2 = sum == 0.f ? -INFINITY : log2f(sum) - nref[tid];
       alpha[tid] = sum == 0.f ? 0.f : 1.f / sum;
       if (!whole) {
         float* z = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(p.workspace) + ws_lse_offset(sms));
-        z[slot * kMaxCols + tid] = lse2;
+        z[part * kMaxCols + tid] = lse2;
       } else if (p.lse && tid < ncols) {
-        const int c = group * N + tid;
-        p.lse[(int64_t)item * p.cols + c] = lse2 * kLn2;
+        p.lse[(int64_t)item * p.cols + group * N + tid] = lse2 * kLn2;
       }
     }
     bar_softmax();
@@ -584,33 +767,33 @@ __device__ __forceinline__ void softmax(const AttendParams& p, uint32_t pt, uint
     __syncwarp();
     ++seg;
     tc::fence_after();
+    const float unscale = kF16 ? scalars[0] : 1.f;
+    const bool odd = lane & 1;
 #pragma unroll 1
     for (int g = 0; g < 4; ++g) {
-      float o[N];
-#pragma unroll
-      for (int c = 0; c < N; c += 16) tc::tmem_ld16(tm + N + g * N + c, o + c);
+      float o[kW];
+      tc::tmem_ld<kW>(tm + N + g * N, o);
       tc::tmem_wait_ld();
-      tc::touch<N>(o);
-      const int dim = 128 * g + tid;
-      if (!whole) {
-        float* z = p.workspace + ((int64_t)slot * kMaxCols) * kLatent + dim;
+      tc::touch<kW>(o);
+      // O' / sum * skey0, in an order that cannot overflow early
 #pragma unroll
-        for (int c = 0; c < N; ++c)
-          if (c < ncols) z[(int64_t)c * kLatent] = o[c] * alpha[c];
+      for (int c = 0; c < kW; c += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(alpha + c0 + c);
+        o[c] = o[c] * f.x * unscale, o[c + 1] = o[c + 1] * f.y * unscale;
+        o[c + 2] = o[c + 2] * f.z * unscale, o[c + 3] = o[c + 3] * f.w * unscale;
+      }
+      if (!whole) {
+        float* z = p.workspace + ((int64_t)part * kMaxCols + c0) * kLatent + 128 * g + key;
+#pragma unroll
+        for (int c = 0; c < kW; ++c) z[c * kLatent] = o[c];
       } else {
         // pairs of lanes exchange so that each writes two neighbouring dimensions of one column
+        __nv_bfloat16* dst = p.out + 128 * g + (key - odd);
 #pragma unroll
-        for (int c = 0; c < N; c += 2) {
-          const float a = o[c] * alpha[c], b = o[c + 1] * alpha[c + 1];
-          const bool odd = lane & 1;
-          const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? a : b, 1);
-          const int mine = c + odd;
-          if (mine < ncols) {
-            const int gc = group * N + mine;
-            const int pos = gc / p.heads, head = gc - pos * p.heads;
-            __nv_bfloat16* dst = p.out + ((int64_t)item * p.P + pos) * p.out_tok + head * p.out_head + (dim - odd);
-            *reinterpret_cast<uint32_t*>(dst) = odd ? tc::pack_bf16(got, b) : tc::pack_bf16(a, got);
-          }
+        for (int c = 0; c < kW; c += 2) {
+          const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? o[c] : o[c + 1], 1);
+          const uint32_t two = odd ? tc::pack_bf16(got, o[c + 1]) : tc::pack_bf16(o[c], got);
+          if (c0 + c + odd < ncols) *reinterpret_cast<uint32_t*>(dst + offsets[c0 + c + odd]) = two;
         }
       }
     }
@@ -644,6 +827,7 @@ __host__ __device__ __forceinline__ int64_t run_begin(int64_t total, int ctas, i
 template <int N, int kRowBytes>
 __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const AttendParams p, int groups, int sms) {
   using L = Smem<N>;
+  constexpr bool kF16 = kRowBytes == HS_ROW_BYTES_FP8;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~uintptr_t(1023));
   __shared__ RunStart start;
@@ -652,8 +836,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const AttendParams 
   const int warp = threadIdx.x >> 5;
   const uint32_t base = tc::smem_u32(smem);
   const uint32_t bars = base + L::kMisc;
-  float* ref = reinterpret_cast<float*>(smem + L::kMisc + 256);  // references, factors, limits: 3 N; joins: 4 N
-  float* red = ref + 4 * N;
+  float* nref = reinterpret_cast<float*>(smem + L::kRef);
+  int64_t* offsets = reinterpret_cast<int64_t*>(smem + L::kOffsets);
+  int* ids = reinterpret_cast<int*>(smem + L::kIds);
 
   // The run of tiles of this CTA.
   int64_t total, begin, run = 0;
@@ -705,9 +890,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const AttendParams 
     tc::mbar_init(bars + 8 * kQFull, kProducerWarps);
     tc::mbar_init(bars + 8 * kQEmpty, 1);
     tc::mbar_init(bars + 8 * kSFull, 1);
-    tc::mbar_init(bars + 8 * kPReady, 128);
+    tc::mbar_init(bars + 8 * kPReady, kSoftmaxWarps);
     tc::mbar_init(bars + 8 * kOFull, 1);
     tc::mbar_init(bars + 8 * kDrain, 1);
+    for (int i = 0; i < kAhead; ++i) {
+      tc::mbar_init(bars + 8 * (kIdFull + i), 1);
+      tc::mbar_init(bars + 8 * (kIdEmpty + i), kProducerWarps + kSoftmaxWarps);
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kMmaWarp) tc::tmem_alloc(tc::smem_u32(&tmem_slot), tmem_cols<N>());
@@ -718,21 +907,20 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const AttendParams 
   if (threadIdx.x == 0)
     reinterpret_cast<RunStart*>(reinterpret_cast<uint8_t*>(p.workspace) + ws_run_offset(sms))[blockIdx.x] = start;
   Cursor cur;
-  cur.start(p, start, run);
+  cur.start(p, start, (int)run);
   tc::Waiter w;
   if (warp < kProducerWarps) {
-    more_registers<kRegsProducer>();
-    if (kRowBytes == HS_ROW_BYTES_FP8)
-      produce_fp8<N>(p, base, base + L::kQ, bars, cur, groups, w);
-    else
-      produce_bf16<N>(p, base, base + L::kQ, bars, cur, groups, w);
+    fewer_registers<kRegsProducer>();
+    produce_tiles<N, kF16>(p, base, base + L::kQ, ids, nref + L::kQScale, nref + L::kKeyScale, bars, cur, groups, w);
   } else if (warp < kMmaWarp) {
     more_registers<kRegsSoftmax>();
-    softmax<N>(p, base + L::kP, bars, tmem, ref, red, cur, groups, sms, w);
+    softmax<N, kF16>(p, base + L::kP, bars, tmem, nref, offsets, ids, cur, groups, sms, w);
   } else {
     fewer_registers<kRegsMma>();
-    if (threadIdx.x == kMmaWarp * 32)
-      issue_products<N>(p, base, base + L::kQ, base + L::kP, bars, tmem, cur, groups, w);
+    if (warp == kIdWarp)
+      resolve_rows(p, ids, bars, cur, groups, w);
+    else if (warp == kMmaWarp)
+      issue_products<N, kF16>(p, base, base + L::kQ, base + L::kP, bars, tmem, cur, groups, w);
   }
   if (w.dead) report(p.status, HS_ERR_TIMEOUT);
   __syncwarp();
