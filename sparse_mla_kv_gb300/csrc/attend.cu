@@ -1,10 +1,10 @@
 // Absorbed latent attention over the rows of the paged pool, on the tensor cores.
 //
 // Mathematics.  One latent row serves all columns of an item (the heads of a token, or positions x heads of a
-// request) as key and as value.  A tile is 128 keys; both products are computed transposed, so that the tile is
-// the 128-row operand and a call with few columns wastes nothing:
-//   S^T[128 keys][N]  = K[128][576] * Q^T[576][N]          (36 steps of 16)
-//   O^T[512][N]      += V^T[512][128] * P^T[128][N]         (4 row blocks x 8 steps)
+// request) as key and as value.  A tile is 64 keys; both products are computed transposed, so that the tile is
+// the operand with 64 or 128 rows and a call with few columns wastes nothing:
+//   S^T[64 keys][N]  = K[64][576] * Q^T[576][N]           (36 steps of 16)
+//   O^T[512][N]     += V^T[512][64] * P^T[64][N]           (4 row blocks x 4 steps)
 // V is the latent part of K: the same bytes, once read as a K-major and once as an M-major operand.  The softmax
 // is online with a lazy reference: weights are exp2(t), t = s - m, with any m that keeps them in range, since fp32 sums
 // have the same relative precision at every magnitude.  m starts kTop below the first tile's maximum and moves (with O
@@ -19,20 +19,18 @@
 //
 // Layout.  A unit is (item, group of N columns); units are cut into tiles, numbered in order, and every CTA takes
 // an equal run of tiles; a unit that several CTAs share leaves partial results in the workspace, which
-// combine_kernel joins in a fixed order.  One CTA per SM, 32 warps (the warpgroups trade registers, kRegs*):
-//   warp 29      resolves the keys of up to kAhead tiles to row ids;
-//   warps 24-27  copy the latent parts of the rows into the places that the current tile's parts leave;
-//   warps 0-15   bring the tile into operand form: fp8 codes land in half of their part's place and are widened to fp16
-//                there (a warp owns 8 keys); the rotated parts and scales come through registers, a tile ahead;
-//   warp 28      issues the products;
-//   warps 16-23  softmax and results: lane = key, later lane = latent dimension; each of the two groups of four
-//                warps has half of the columns.
-// The tile (128 x 576, 144 KB) has one buffer, released in five parts (four 128-dimension blocks after their product
-// with P, the rotated part after S, or after P when P takes its place).  Other ways to load were slower: to registers,
-// ahead of time, because what is in flight towards registers needs L1, of which this much shared memory leaves 28 KB
-// (a tile is 84 KB; the loads then wait for one another and hold up every other access to shared memory); by the copy
-// engine, which takes 73 cycles a row and 77 for four gathered pieces of 128 B (16-byte asynchronous copies: 16 KB in
-// 410 cycles from L2, 800 from HBM with every SM loading); prefetching rows into L2 gained nothing.
+// combine_kernel joins in a fixed order.  One CTA per SM, 28 warps (the warpgroups trade registers, kRegs*):
+//   warp 25      resolves keys to row ids and gathers whole rows with the copy engine, four an instruction, into a ring of
+//                slots of 16 rows (80 cycles an instruction whatever the width: pieces of rows, or single rows by
+//                one-dimensional copies at 73 cycles each, were four times slower; 16-byte asynchronous copies and loads
+//                cost the load pipe 13 cycles for 512 B, which the stores below need);
+//   warps 0-15   take four rows each from the ring, widen fp8 codes to fp16, and store them as operands once their
+//                places in the tile are free;
+//   warp 24      issues the products;
+//   warps 16-23  softmax and results: lane = key (16 of a warp's lanes have one, as products of 64 rows lie in tensor
+//                memory), later lane = latent dimension; each of the two groups of four warps has half of the columns.
+// The tile (64 x 576, 72 KB) has one buffer, released in five parts: the rotated part after S, and four 128-dimension
+// blocks, each after its product with P.
 #include <type_traits>
 
 #include "latent.cuh"
@@ -41,9 +39,9 @@
 namespace hs {
 namespace {
 
-constexpr int kTile = 128;
+constexpr int kTile = 64;
 constexpr int kProducerWarps = 16, kSoftmaxWarps = 8;
-constexpr int kMmaWarp = kProducerWarps + kSoftmaxWarps, kIdWarp = kMmaWarp + 1;
+constexpr int kMmaWarp = kProducerWarps + kSoftmaxWarps, kGatherWarp = kMmaWarp + 1;
 constexpr int kThreads = (kMmaWarp + 4) * 32;
 constexpr int kAhead = 4;
 constexpr int kMaxCols = 64;
@@ -55,7 +53,7 @@ template <int kRegs>
 __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs)); }
 template <int kRegs>
 __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs)); }
-constexpr int kSub = kTile * 128;  // bytes of a sub-tile: 128 keys x 64 bf16
+constexpr int kSub = kTile * 128;  // bytes of a sub-tile: 64 keys x 64 values
 // In log2 units: where a new reference puts the largest score, and the most that a score may reach before it moves.
 // fp16 weights are normal from 2^-14 to 2^16; bf16 weights have fp32's range.
 template <bool kF16>
@@ -123,25 +121,41 @@ __device__ __forceinline__ int key_row(const AttendParams& p, int item, int k, i
   return -1;
 }
 
-template <int N>
+// Raw rows: a gather of four fp8 rows takes 4 x 656 B, padded to the copy engine's 128-byte boundaries; four bf16
+// rows come in two halves of 4 x 576 B (a box is at most 256 elements wide).
+template <bool kF16>
+struct Raw {
+  static constexpr int kRow = kF16 ? HS_ROW_BYTES_FP8 : HS_ROW_BYTES_BF16;
+  static constexpr int kBox = kF16 ? kRow : kRow / 2;  // bytes of a row that one gather brings
+  static constexpr int kFour = kF16 ? 2688 : 4 * kRow;
+  static constexpr int kSlot = 4 * kFour;              // 16 rows
+  static constexpr int kTx = 16 * kRow;
+};
+
+template <int N, bool kF16>
 struct Smem {
-  static constexpr int kTileBytes = 9 * kSub;
-  static constexpr int kQ = kTileBytes;
-  static constexpr int kQBytes = 9 * N * 128;
-  static constexpr bool kAlias = N == 64;  // no room for P of 64 columns: it takes the key part's place
-  static constexpr int kP = kAlias ? 8 * kSub : kQ + kQBytes;
-  static constexpr int kMisc = kQ + kQBytes + (kAlias ? 0 : kTile * N * 2);
-  // misc: barriers (256 B), row ids [kAhead][128], results' offsets [N] (64 bits), then floats: references, factors,
-  // limits, scalars [N] each, joined values [4][N], query scales [2][N], key scales [128]
-  static constexpr int kIds = kMisc + 256;
+  static constexpr int kQ = 9 * kSub;
+  static constexpr bool kAlias = !kF16 && N == 64;  // no room for P: it takes the rotated part's place
+  static constexpr int kP = kAlias ? 8 * kSub : kQ + 9 * N * 128;
+  static constexpr int kRaw = kQ + 9 * N * 128 + (kAlias ? 0 : kTile * N * 2);
+  // after the ring: barriers (384 B), row ids [kAhead][64], results' offsets [N] (64 bits), then floats: references,
+  // factors, limits, scalars [N] each, joined values [4][N], query scales [2][N], key scales [64]
+  static constexpr int kMiscBytes = 384 + kAhead * kTile * 4 + N * 8 + (10 * N + kTile) * 4;
+  static constexpr int kFit = (232448 - 1024 - kMiscBytes - kRaw) / Raw<kF16>::kSlot;
+  static constexpr int kSlots = kFit < 8 ? kFit : 8;
+  static constexpr int kMisc = kRaw + kSlots * Raw<kF16>::kSlot;
+  static constexpr int kIds = kMisc + 384;
   static constexpr int kOffsets = kIds + kAhead * kTile * 4;
   static constexpr int kRef = kOffsets + N * 8;
   static constexpr int kQScale = 8 * N, kKeyScale = 10 * N;
-  static constexpr int kBytes = kRef + (10 * N + kTile) * 4 + 1024;  // + alignment of the base
+  static constexpr int kBytes = kMisc + kMiscBytes + 1024;  // + alignment of the base
+  // a tile's four slots fit: so they can all be on their way before its row ids are published, and who has seen the
+  // ids knows that the slots' earlier uses are over, which the parity of a barrier alone cannot tell
+  static_assert(kSlots >= 4, "ring");
 };
-enum Bar { kFull = 0, kEmpty = 5, kQFull = 10, kQEmpty, kSFull, kPReady, kOFull, kDrain, kIdFull, kIdEmpty = kIdFull + kAhead,
-           kBars = kIdEmpty + kAhead };
-static_assert(kBars * 8 <= 256, "barriers");
+enum Bar { kFull = 0, kEmpty = 5, kQFull = 10, kQEmpty, kSFull, kPReady, kOFull, kDrain, kRawFull = 16, kRawEmpty = 24,
+           kIdFull = 32, kIdEmpty = kIdFull + kAhead, kBars = kIdEmpty + kAhead };
+static_assert(kBars * 8 <= 384, "barriers");
 
 template <int N>
 constexpr int tmem_cols() { return N == 64 ? 512 : N == 32 ? 256 : 128; }
@@ -164,23 +178,14 @@ __device__ __forceinline__ void halve(float* v, int lane, F f) {
   }
 }
 
-// Loads from a row, or zeros: predicated, so that nothing waits for them before their use.
-template <int kOff>
-__device__ __forceinline__ uint4 ldg16(const uint8_t* p, bool there) {
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
   uint4 v;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
-      "mov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
-      "@p ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4 + %5];\n\t}"
-      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
-      : "l"(p), "n"(kOff), "r"((uint32_t)there));
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
   return v;
 }
-__device__ __forceinline__ float ldg_scale(const uint8_t* p, bool there) {
+__device__ __forceinline__ float lds_f(uint32_t a) {
   float v;
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.f32 %0, 0f00000000;\n\t@p ld.global.nc.f32 %0, [%1];\n\t}"
-               : "=&f"(v)
-               : "l"(p), "r"((uint32_t)there));
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
   return v;
 }
 // 16 bytes to shared memory, asynchronously; zeros when there is nothing to copy.
@@ -189,9 +194,6 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there
 }
 __device__ __forceinline__ void sts(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
-}
-__device__ __forceinline__ void sts8(uint32_t a, uint32_t x, uint32_t y) {
-  asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(a), "r"(x), "r"(y) : "memory");
 }
 // 4 e4m3 codes -> 4 fp16
 __device__ __forceinline__ uint2 codes4(uint32_t w) {
@@ -290,221 +292,197 @@ __device__ __forceinline__ void convert_queries(const AttendParams& p, uint32_t 
   }
 }
 
-// Part kPart of two rows.
-template <int kPart, int kPieces>
-__device__ __forceinline__ void load_part(const uint8_t* const (&row)[2], uint4 (&v)[kPieces][2]) {
-  constexpr int kAt = kPart * kPieces * 128;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    v[0][i] = ldg16<kAt>(row[i], true);
-    if (kPieces == 2) v[kPieces - 1][i] = ldg16<kAt + 128>(row[i], true);
-  }
-}
-
 template <int N, bool kF16>
-__device__ __forceinline__ void produce_tiles(const AttendParams& p, uint32_t tile, uint32_t q, const int* ids, float* qs,
-                                              float* skey, uint32_t bars, Cursor cur, int groups, tc::Waiter& w) {
-  constexpr int kRowBytes = kF16 ? HS_ROW_BYTES_FP8 : HS_ROW_BYTES_BF16;
-  constexpr int kPieces = kF16 ? 1 : 2;  // 128-byte pieces of a row in a part
+__device__ __forceinline__ void produce_tiles(const AttendParams& p, uint32_t base, const int* ids, float* qs, float* skey,
+                                              uint32_t bars, Cursor cur, int groups, tc::Waiter& w) {
+  using L = Smem<N, kF16>;
+  using R = Raw<kF16>;
+  constexpr int kPieces = kF16 ? 1 : 2;  // 16-byte pieces of a part that a lane handles
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane >> 3, j = lane & 7;
-  const int key0 = warp * 8 + sub;  // this lane's keys key0 and key0 + 4, its 16-byte piece j
-  uint4 even[kPieces][2], odd[kPieces][2];  // parts 0, 2 and 1, 3 on their way
-  uint4 rope[2];
-  float sc[2];  // lanes j and j + 4 of a key hold its scale of group j
-  const uint8_t* row[2];
-  uint32_t missing = 0, missing_next = 0;  // bit i: key key0 + 4 i has no row (row 0 is read and replaced by zeros)
-  auto take_ids = [&](uint32_t t) {
-    const int slot = t % kAhead;
-    w.wait(bars + 8 * (kIdFull + slot), (t / kAhead) & 1);
-    const int a = ids[slot * kTile + key0], b = ids[slot * kTile + key0 + 4];
-    __syncwarp();
-    if (lane == 0) tc::mbar_arrive(bars + 8 * (kIdEmpty + slot));
-    missing_next = (a < 0 ? 1u : 0u) | (b < 0 ? 2u : 0u);
-    row[0] = p.base + (int64_t)max(a, 0) * kRowBytes + 16 * j;
-    row[1] = p.base + (int64_t)max(b, 0) * kRowBytes + 16 * j;
-  };
-  auto load_rest = [&]() {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (kF16) sc[i] = ldg_scale(row[i] + kLatent + 4 * (j & 3) - 16 * j, true);
-      rope[i] = ldg16<kRowBytes - 128>(row[i], true);
-    }
-  };
-  // where this lane stores: lanes of the upper sub-tile store the halves of their 16 values in the other order, so that
-  // no two lanes of a store share a bank
+  const int key = warp * 4 + sub;  // this lane's key; of each 128 bytes of its row, the 16-byte piece j
+  const int swz = key & 7;
+  // lanes of the upper sub-tile store the halves of their 16 values in the other order, so that no two lanes of a store
+  // share a bank
   const bool flip = kF16 && (j >> 2);
-  uint32_t at[2][2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int swz = sub + 4 * i;  // key % 8
-    const uint32_t to = tile + (key0 + 4 * i) * 128;
-    if (kF16) {
-      at[i][0] = to + (j >> 2) * kSub + ((((j & 3) * 2 + flip) ^ swz) << 4);
-      at[i][1] = to + (j >> 2) * kSub + ((((j & 3) * 2 + !flip) ^ swz) << 4);
-    } else {
-      at[i][0] = to + ((j ^ swz) << 4);
-      at[i][1] = at[i][0] + kSub;
-    }
+  uint32_t at[2];
+  if (kF16) {
+    at[0] = base + (j >> 2) * kSub + key * 128 + ((((j & 3) * 2 + flip) ^ swz) << 4);
+    at[1] = base + (j >> 2) * kSub + key * 128 + ((((j & 3) * 2 + !flip) ^ swz) << 4);
+  } else {
+    at[0] = base + key * 128 + ((j ^ swz) << 4);
+    at[1] = at[0] + kSub;
   }
-  float inv[2];
-  uint32_t ratio[2];
-  bool exact = true;  // every scale is a power of two
-  auto store = [&](int c, uint4 (&v)[kPieces][2]) {
-    const uint32_t off = 2 * c * kSub;
-    if (missing) {  // (never the whole warp's business: a lane's own rows)
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (missing >> i & 1)
-#pragma unroll
-          for (int x = 0; x < kPieces; ++x) v[x][i] = make_uint4(0, 0, 0, 0);
-    }
-    __syncwarp();
-    if constexpr (kF16) {
-      const int from = (lane & 24) | c;
-      if (exact) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint4 u = v[0][i];
-          const uint32_t r = __shfl_sync(0xFFFFFFFFu, ratio[i], from);
-          const uint2 a = codes4(flip ? u.z : u.x), b = codes4(flip ? u.w : u.y);
-          const uint2 d = codes4(flip ? u.x : u.z), e = codes4(flip ? u.y : u.w);
-          sts(at[i][0] + off, mul_half2(a.x, r), mul_half2(a.y, r), mul_half2(b.x, r), mul_half2(b.y, r));
-          sts(at[i][1] + off, mul_half2(d.x, r), mul_half2(d.y, r), mul_half2(e.x, r), mul_half2(e.y, r));
-        }
-      } else {
-#pragma unroll 1
-        for (int n = 0; n < 8; ++n) {  // a word of four codes at a time
-          const int i = n >> 2, word = n & 3;
-          const uint4 u = i ? v[0][1] : v[0][0];
-          const float z = __shfl_sync(0xFFFFFFFFu, i ? sc[1] : sc[0], from), f = i ? inv[1] : inv[0];
-          const uint2 a = codes4(word == 0 ? u.x : word == 1 ? u.y : word == 2 ? u.z : u.w);
-          const bool second = (word >> 1) != (int)flip;
-          const uint32_t to = i ? (second ? at[1][1] : at[1][0]) : (second ? at[0][1] : at[0][0]);
-          sts8(to + off + (word & 1) * 8, scaled_half(a.x, z, f), scaled_half(a.y, z, f));
-        }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int x = 0; x < kPieces; ++x) sts(at[i][x] + off, v[x][i].x, v[x][i].y, v[x][i].z, v[x][i].w);
-    }
-  };
   auto signal = [&](int bar) {
     tc::fence_async_smem();
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(bars + 8 * bar);
   };
-  take_ids(0);
-  load_rest();
-  load_part<0, kPieces>(row, even);
-  load_part<1, kPieces>(row, odd);
   bool fresh = true;
   uint32_t it = 0, seg = 0;
+  uint32_t ring = warp >> 2;  // this warp's rows: slot ring % kSlots, its use number ring / kSlots
 #pragma unroll 1
   while (cur.left > 0) {
     if (fresh) {
       if (seg > 0) w.wait(bars + 8 * kQEmpty, (seg - 1) & 1);
       if (kF16) {
-        convert_queries<N>(p, q, qs + (seg & 1) * N, cur.item, cur.group);
+        convert_queries<N>(p, base + L::kQ, qs + (seg & 1) * N, cur.item, cur.group);
       } else {
-        copy_queries<N>(p, q, cur.item, cur.group);
+        copy_queries<N>(p, base + L::kQ, cur.item, cur.group);
         asm volatile("cp.async.wait_group 0;" ::: "memory");
       }
       signal(kQFull);
       ++seg;
     }
-    missing = missing_next;
-    if (kF16) {
+    // the rows, from the ring
+    const int slot = it % kAhead;
+    w.wait(bars + 8 * (kIdFull + slot), (it / kAhead) & 1);
+    const bool there = ids[slot * kTile + key] >= 0;
+    const uint32_t from = ring % L::kSlots;
+    w.wait(bars + 8 * (kRawFull + from), (ring / L::kSlots) & 1);
+    __syncwarp();
+    uint4 v[4][2], rope;
+    float sc = 0.f;
+    {
+      const uint32_t raw = base + L::kRaw + from * R::kSlot + (warp & 3) * R::kFour;
+      auto piece = [&](int off) {  // 16 bytes of the lane's row from byte `off`
+        if (kF16) return lds16(raw + sub * R::kRow + off);
+        return lds16(raw + sub * R::kBox + off + (off >= R::kBox ? 3 * R::kBox : 0));
+      };
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        v[c][0] = piece(128 * kPieces * c + 16 * j);
+        if (kPieces == 2) v[c][1] = piece(256 * c + 128 + 16 * j);
+      }
+      rope = piece(R::kRow - 128 + 16 * j);
+      if (kF16) sc = lds_f(raw + sub * R::kRow + kLatent + 4 * (j & 3));
+    }
+    tc::fence_async_smem();  // the copy engine's next write to the slot comes after these reads
+    __syncwarp();
+    if (lane == 0) {
+      tc::mbar_arrive(bars + 8 * (kRawEmpty + from));
+      tc::mbar_arrive(bars + 8 * (kIdEmpty + slot));
+    }
+    ring += 4;
+    if (!there) {  // (row 0 was read in its place)
+      sc = 0.f;
+      rope = make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[c][0] = v[c][1] = make_uint4(0, 0, 0, 0);
+    }
+    __syncwarp();
+    float inv = 1.f;
+    if constexpr (kF16) {
       // skey: 2^7 below the power of two that covers the largest scale (codes reach 448 * 2^7 < 65504), and so that the
       // rotated part stays below 2^15
-      exact = true;
+      const uint32_t sb = __float_as_uint(sc) & 0x7FFFFFFFu;
+      const bool exact = __all_sync(0xFFFFFFFFu, (sb & 0x7FFFFFu) == 0);  // every scale is a power of two
+      int e = (int)(sb >> 23) + ((sb & 0x7FFFFFu) ? 1 : 0) - 7;
+      e = max(e, (int)(__float_as_uint(max_bf16x8(rope)) >> 23) + 1 - 15);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (missing >> i & 1) sc[i] = 0.f, rope[i] = make_uint4(0, 0, 0, 0);
-        const uint32_t sb = __float_as_uint(sc[i]) & 0x7FFFFFFFu;
-        exact &= (sb & 0x7FFFFFu) == 0;
-        int e = (int)(sb >> 23) + ((sb & 0x7FFFFFu) ? 1 : 0) - 7;
-        e = max(e, (int)(__float_as_uint(max_bf16x8(rope[i])) >> 23) + 1 - 15);
+      for (int d = 1; d < 8; d <<= 1) e = max(e, __shfl_xor_sync(0xFFFFFFFFu, e, d));
+      e = min(max(e, 1), 240);
+      inv = __uint_as_float((uint32_t)(254 - e) << 23);
+      const uint32_t ratio = pack_half(sc * inv, sc * inv);
 #pragma unroll
-        for (int d = 1; d < 8; d <<= 1) e = max(e, __shfl_xor_sync(0xFFFFFFFFu, e, d));
-        e = min(max(e, 1), 240);
-        inv[i] = __uint_as_float((uint32_t)(254 - e) << 23);
-        const float r = sc[i] * inv[i];
-        ratio[i] = pack_half(r, r);
+      for (int c = 0; c < 4; ++c) {
+        const uint4 u = v[c][0];
+        const int src = (lane & 24) | c;  // lanes c and c + 4 of a key have its scale of group c
+        uint2 a = codes4(flip ? u.z : u.x), b = codes4(flip ? u.w : u.y);
+        uint2 d = codes4(flip ? u.x : u.z), f = codes4(flip ? u.y : u.w);
+        if (exact) {
+          const uint32_t r = __shfl_sync(0xFFFFFFFFu, ratio, src);
+          a.x = mul_half2(a.x, r), a.y = mul_half2(a.y, r), b.x = mul_half2(b.x, r), b.y = mul_half2(b.y, r);
+          d.x = mul_half2(d.x, r), d.y = mul_half2(d.y, r), f.x = mul_half2(f.x, r), f.y = mul_half2(f.y, r);
+        } else {
+          const float z = __shfl_sync(0xFFFFFFFFu, sc, src);
+          a.x = scaled_half(a.x, z, inv), a.y = scaled_half(a.y, z, inv);
+          b.x = scaled_half(b.x, z, inv), b.y = scaled_half(b.y, z, inv);
+          d.x = scaled_half(d.x, z, inv), d.y = scaled_half(d.y, z, inv);
+          f.x = scaled_half(f.x, z, inv), f.y = scaled_half(f.y, z, inv);
+        }
+        v[c][0] = make_uint4(a.x, a.y, b.x, b.y);
+        v[c][1] = make_uint4(d.x, d.y, f.x, f.y);
       }
-      exact = __all_sync(0xFFFFFFFFu, exact);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (missing >> i & 1) rope[i] = make_uint4(0, 0, 0, 0);
+      rope = make_uint4(bf16_to_half(rope.x, inv), bf16_to_half(rope.y, inv), bf16_to_half(rope.z, inv), bf16_to_half(rope.w, inv));
     }
+    // the operands, part by part as their places become free
     auto free_part = [&](int c) {
       if (it > 0) w.wait(bars + 8 * (kEmpty + c), (it - 1) & 1);
     };
-    free_part(0);
-    if (kF16 && j == 0) {  // the softmax of the tile before has read its own
-      skey[key0] = 1.f / inv[0];
-      skey[key0 + 4] = 1.f / inv[1];
-    }
-    store(0, even);
-    signal(kFull + 0);
-    load_part<2, kPieces>(row, even);
-    free_part(1);
-    store(1, odd);
-    signal(kFull + 1);
-    load_part<3, kPieces>(row, odd);
-    const bool next_fresh = cur.next(p, groups);
-    const bool more = cur.left > 0;
-    if (more) take_ids(it + 1);
-    free_part(2);
-    store(2, even);
-    signal(kFull + 2);
-    if (more) load_part<0, kPieces>(row, even);
-    free_part(3);
-    store(3, odd);
-    signal(kFull + 3);
-    if (more) load_part<1, kPieces>(row, odd);
-    free_part(4);
+    auto put_rope = [&]() {
+      free_part(4);
+      sts(base + 8 * kSub + key * 128 + ((j ^ swz) << 4), rope.x, rope.y, rope.z, rope.w);
+      signal(kFull + 4);
+    };
+    if (!L::kAlias) put_rope();
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t to = tile + 8 * kSub + (key0 + 4 * i) * 128 + ((j ^ (sub + 4 * i)) << 4);
-      if (kF16)
-        sts(to, bf16_to_half(rope[i].x, inv[i]), bf16_to_half(rope[i].y, inv[i]), bf16_to_half(rope[i].z, inv[i]),
-            bf16_to_half(rope[i].w, inv[i]));
-      else
-        sts(to, rope[i].x, rope[i].y, rope[i].z, rope[i].w);
+    for (int c = 0; c < 4; ++c) {
+      free_part(c);
+      if (kF16 && c == 0 && j == 0) skey[key] = 1.f / inv;  // (the softmax of the tile before has read its own)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) sts(at[x] + 2 * c * kSub, v[c][x].x, v[c][x].y, v[c][x].z, v[c][x].w);
+      signal(kFull + c);
     }
-    signal(kFull + 4);
-    if (more) load_rest();
-    fresh = next_fresh;
+    if (L::kAlias) put_rope();
+    fresh = cur.next(p, groups);
     ++it;
   }
 }
 
-// Row ids of the tiles to come (one warp).
-__device__ __forceinline__ void resolve_rows(const AttendParams& p, int* ids, uint32_t bars, Cursor cur, int groups,
-                                              tc::Waiter& w) {
+// Row ids of the tiles to come, and their rows on the way to the ring (one warp; lane l < 16: keys 4 l .. 4 l + 3).  Keys
+// without a row read row 0, which the producers replace by zeros.
+template <int N, bool kF16>
+__device__ __forceinline__ void gather_rows(const AttendParams& p, const CUtensorMap* map, uint32_t base, int* ids,
+                                            uint32_t bars, Cursor cur, int groups, tc::Waiter& w) {
+  using L = Smem<N, kF16>;
+  using R = Raw<kF16>;
   const int lane = threadIdx.x & 31;
-  uint32_t it = 0;
-  bool any_bad = false;
+  uint32_t it = 0, ring = 0;
+  bool any_bad = false, bad = false;
+  int4 id, next;
+  auto resolve = [&]() {
+    int r[4] = {-1, -1, -1, -1};
+    bad = false;
+    if (lane < 16 && cur.left > 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r[i] = key_row(p, cur.item, cur.tile * kTile + 4 * lane + i, cur.keys, bad);
+    }
+    any_bad |= bad && cur.group == 0;
+    next = make_int4(r[0], r[1], r[2], r[3]);
+  };
+  resolve();
 #pragma unroll 1
   while (cur.left > 0) {
+    id = next;
     const int slot = it % kAhead;
-    int id[4];
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) id[i] = key_row(p, cur.item, cur.tile * kTile + lane + 32 * i, cur.keys, bad);
-    any_bad |= bad && cur.group == 0;
     if (it >= kAhead) w.wait(bars + 8 * (kIdEmpty + slot), (it / kAhead - 1) & 1);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) ids[slot * kTile + lane + 32 * i] = id[i];
     __syncwarp();
-    if (lane == 0) tc::mbar_arrive(bars + 8 * (kIdFull + slot));
+    if (lane < 16) *reinterpret_cast<int4*>(ids + slot * kTile + 4 * lane) = id;
     cur.next(p, groups);
     ++it;
+    resolve();  // the next tile's ids are on their way while this one's rows are gathered
+    id.x = max(id.x, 0), id.y = max(id.y, 0), id.z = max(id.z, 0), id.w = max(id.w, 0);
+#pragma unroll 1
+    for (int s = 0; s < 4; ++s, ++ring) {
+      const uint32_t to = ring % L::kSlots;
+      if (ring >= L::kSlots) w.wait(bars + 8 * (kRawEmpty + to), (ring / L::kSlots - 1) & 1);
+      const uint32_t full = bars + 8 * (kRawFull + to);
+      if (lane == 0) tc::mbar_expect(full, R::kTx);
+      __syncwarp();
+      if (lane >> 2 == s) {
+        const uint32_t dst = base + L::kRaw + to * R::kSlot + (lane & 3) * R::kFour;
+        tc::gather4(dst, map, 0, id, full);
+        if (!kF16) tc::gather4(dst + 4 * R::kBox, map, R::kBox / 4, id, full);
+      }
+      __syncwarp();
+    }
+    if (lane == 0) tc::mbar_arrive(bars + 8 * (kIdFull + slot));
   }
+  // no copy is in flight when the CTA ends
+  tc::Waiter drain;
+  for (uint32_t r = ring > L::kSlots ? ring - L::kSlots : 0; r < ring; ++r)
+    drain.wait(bars + 8 * (kRawFull + r % L::kSlots), (r / L::kSlots) & 1);
   if (any_bad) report(p.status, p.paged ? HS_ERR_TABLE_RANGE : HS_ERR_ID_RANGE);
 }
 
@@ -514,8 +492,8 @@ __device__ __forceinline__ void resolve_rows(const AttendParams& p, int* ids, ui
 template <int N, bool kF16>
 __device__ __forceinline__ void issue_products(const AttendParams& p, uint32_t tile, uint32_t q, uint32_t pt, uint32_t bars,
                                                uint32_t tmem, Cursor cur, int groups, tc::Waiter& w) {
-  using L = Smem<N>;
-  constexpr uint32_t kIdS = tc::idesc(kF16, 128, N, false, false);
+  using L = Smem<N, kF16>;
+  constexpr uint32_t kIdS = tc::idesc(kF16, kTile, N, false, false);
   constexpr uint32_t kIdO = tc::idesc(kF16, 128, N, true, true);
   constexpr uint64_t kPSwizzle = N == 64 ? tc::kSwizzle128 : N == 32 ? tc::kSwizzle64 : tc::kSwizzle32;
   const uint64_t dk = tc::desc(tile, 16, 1024, tc::kSwizzle128);    // tile as keys (K-major)
@@ -535,14 +513,15 @@ __device__ __forceinline__ void issue_products(const AttendParams& p, uint32_t t
     if (fresh) await(kQFull, seg & 1);
     const bool first = fresh;
 #pragma unroll 1
-    for (int c = 0; c < 5; ++c) {
+    for (int n = 0; n < 5; ++n) {
+      const int c = L::kAlias ? n : n == 0 ? 4 : n - 1;  // the rotated part as its place becomes free: first, or last
       await(kFull + c, it & 1);
       const uint64_t a = dk + (uint32_t)(2 * c * kSub >> 4), b = dq + (uint32_t)(2 * c * (N * 128) >> 4);
 #pragma unroll
       for (int k = 0; k < 8; ++k)
         if (k < 4 || c < 4)
           tc::mma_ss(tmem, a + (((k >> 2) * kSub + (k & 3) * 32) >> 4), b + (((k >> 2) * (N * 128) + (k & 3) * 32) >> 4), kIdS,
-                     c > 0 || k > 0, leader);
+                     n > 0 || k > 0, leader);
     }
     tc::commit(bars + 8 * kSFull, leader);
     if (!L::kAlias) tc::commit(bars + 8 * (kEmpty + 4), leader);
@@ -554,7 +533,7 @@ __device__ __forceinline__ void issue_products(const AttendParams& p, uint32_t t
     for (int g = 0; g < 4; ++g) {
       const uint64_t a = dv + (uint32_t)(2 * g * kSub >> 4);
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
+      for (int k = 0; k < kTile / 16; ++k)
         tc::mma_ss(tmem + N + g * N, a + (k * 2048 >> 4), dp + ((k * 16 * N * 2) >> 4), kIdO, !first || k > 0, leader);
       tc::commit(bars + 8 * (kEmpty + g), leader);
     }
@@ -583,14 +562,16 @@ __device__ __forceinline__ void softmax(const AttendParams& p, uint32_t pt, uint
   const int tid = threadIdx.x - kProducerWarps * 32;
   const int lane = tid & 31, warp = (tid >> 5) & 3;
   const int c0 = (tid >> 7) * kW;                                 // its first column
-  const int key = tid & 127;                                      // its key in the tile
+  const int dim = tid & 127;                                      // later, its dimension of a block of 128
+  const bool has_key = lane < 16;  // products of 64 rows: row i lies in lane i % 16 of a warp's 32
+  const int key = 16 * warp + (lane & 15);                        // its key in the tile
   const uint32_t tm = tmem + ((uint32_t)(32 * warp) << 16) + c0;  // its warp's lanes, its columns
   // nref: [N] the references, negated (+infinity: none yet)
   float* alpha = nref + N;                             // [N] rescale factors, then result factors
   int* limit = reinterpret_cast<int*>(nref + 2 * N);   // [N] keys that a column sees
   float* scalars = nref + 3 * N;                       // skey0, its change, the warps' largest skey [4]
   float* red = nref + 4 * N;                           // [4][N] the warps' maxima or sums
-  const float* skey = nref + Smem<N>::kKeyScale;
+  const float* skey = nref + Smem<N, kF16>::kKeyScale;
   const int col = c0 + lane * kW / 32;                 // where halve() leaves this lane's result
   bool fresh = true, at_start = false;
   bool first_run = true;  // this CTA's first segment
@@ -600,8 +581,9 @@ __device__ __forceinline__ void softmax(const AttendParams& p, uint32_t pt, uint
 #pragma unroll 1
   while (cur.left > 0) {
     const int item = cur.item, group = cur.group;
-    const float* qs = nref + Smem<N>::kQScale + (seg & 1) * N + c0;
+    const float* qs = nref + Smem<N, kF16>::kQScale + (seg & 1) * N + c0;
     if (fresh) {
+      bar_softmax();  // every thread is done with the unit before
       at_start = cur.tile == 0;
       if (tid < N) {
         nref[tid] = INFINITY;
@@ -618,12 +600,12 @@ __device__ __forceinline__ void softmax(const AttendParams& p, uint32_t pt, uint
     const int k = cur.tile * kTile + key;
     const int slot = it % kAhead;
     w.wait(bars + 8 * (kIdFull + slot), (it / kAhead) & 1);
-    const bool there = ids[slot * kTile + key] >= 0;
+    const bool there = has_key && ids[slot * kTile + key] >= 0;
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(bars + 8 * (kIdEmpty + slot));
     // columns differ in what they see only in the last P - 1 keys
     const bool ragged = p.paged && p.P > 1 && (cur.tile + 1) * kTile > limit[0];
-    const bool masks = !__all_sync(0xFFFFFFFFu, there) || ragged;
+    const bool masks = !__all_sync(0xFFFFFFFFu, there || !has_key) || ragged;
     const bool first = fresh;
     float sk = 1.f, mult = p.scale_log2;
     if (kF16) {
@@ -667,10 +649,15 @@ __device__ __forceinline__ void softmax(const AttendParams& p, uint32_t pt, uint
       float top = s[0];
 #pragma unroll
       for (int c = 1; c < kW; ++c) top = fmaxf(top, s[c]);
-      if (moved || !any_softmax(top > kLazy || (kF16 && there && sk > scalars[0]))) break;
+      if (moved || !any_softmax(has_key && (top > kLazy || (kF16 && there && sk > scalars[0])))) break;
       moved = true;
       // a new reference for every column, kTop below the maximum of the old one's and this tile's scores
       scores(false);
+      if (!has_key) {
+#pragma unroll
+        for (int c = 0; c < kW; ++c) s[c] = -INFINITY;
+      }
+      __syncwarp();
       halve<kW>(s, lane, [](float a, float b) { return fmaxf(a, b); });
       red[warp * N + col] = s[0];
       if (kF16) {
@@ -730,7 +717,7 @@ __device__ __forceinline__ void softmax(const AttendParams& p, uint32_t pt, uint
         }
       }
       const int sw = N == 64 ? (key & 7) : N == 32 ? ((key >> 1) & 3) : ((key >> 2) & 1);
-      sts(pt + key * (2 * N) + ((((c0 + c) / 8) ^ sw) << 4), out[0], out[1], out[2], out[3]);
+      if (has_key) sts(pt + key * (2 * N) + ((((c0 + c) / 8) ^ sw) << 4), out[0], out[1], out[2], out[3]);
     }
     tc::fence_async_smem();
     tc::fence_before();
@@ -746,6 +733,11 @@ __device__ __forceinline__ void softmax(const AttendParams& p, uint32_t pt, uint
     const bool whole = at_start && tile + 1 == unit_tiles;
     const int ncols = min(N, p.cols - group * N);
     float* sums = reinterpret_cast<float*>(l);
+    if (!has_key) {
+#pragma unroll
+      for (int c = 0; c < kW; ++c) sums[c] = 0.f;
+    }
+    __syncwarp();
     halve<kW>(sums, lane, [](float a, float b) { return a + b; });
     red[warp * N + col] = sums[0];
     bar_softmax();
@@ -783,12 +775,12 @@ __device__ __forceinline__ void softmax(const AttendParams& p, uint32_t pt, uint
         o[c + 2] = o[c + 2] * f.z * unscale, o[c + 3] = o[c + 3] * f.w * unscale;
       }
       if (!whole) {
-        float* z = p.workspace + ((int64_t)part * kMaxCols + c0) * kLatent + 128 * g + key;
+        float* z = p.workspace + ((int64_t)part * kMaxCols + c0) * kLatent + 128 * g + dim;
 #pragma unroll
         for (int c = 0; c < kW; ++c) z[c * kLatent] = o[c];
       } else {
         // pairs of lanes exchange so that each writes two neighbouring dimensions of one column
-        __nv_bfloat16* dst = p.out + 128 * g + (key - odd);
+        __nv_bfloat16* dst = p.out + 128 * g + (dim - odd);
 #pragma unroll
         for (int c = 0; c < kW; c += 2) {
           const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? o[c] : o[c + 1], 1);
@@ -825,9 +817,10 @@ __device__ int64_t block_scan(int64_t v, int64_t* total, int64_t* scratch) {
 __host__ __device__ __forceinline__ int64_t run_begin(int64_t total, int ctas, int b) { return total * b / ctas; }
 
 template <int N, int kRowBytes>
-__global__ void __launch_bounds__(kThreads, 1) attend_kernel(const AttendParams p, int groups, int sms) {
-  using L = Smem<N>;
+__global__ void __launch_bounds__(kThreads, 1) attend_kernel(const AttendParams p, const __grid_constant__ CUtensorMap map,
+                                                             int groups, int sms) {
   constexpr bool kF16 = kRowBytes == HS_ROW_BYTES_FP8;
+  using L = Smem<N, kF16>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~uintptr_t(1023));
   __shared__ RunStart start;
@@ -893,6 +886,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const AttendParams 
     tc::mbar_init(bars + 8 * kPReady, kSoftmaxWarps);
     tc::mbar_init(bars + 8 * kOFull, 1);
     tc::mbar_init(bars + 8 * kDrain, 1);
+    for (int i = 0; i < L::kSlots; ++i) {
+      tc::mbar_init(bars + 8 * (kRawFull + i), 1);
+      tc::mbar_init(bars + 8 * (kRawEmpty + i), 4);
+    }
     for (int i = 0; i < kAhead; ++i) {
       tc::mbar_init(bars + 8 * (kIdFull + i), 1);
       tc::mbar_init(bars + 8 * (kIdEmpty + i), kProducerWarps + kSoftmaxWarps);
@@ -911,14 +908,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const AttendParams 
   tc::Waiter w;
   if (warp < kProducerWarps) {
     fewer_registers<kRegsProducer>();
-    produce_tiles<N, kF16>(p, base, base + L::kQ, ids, nref + L::kQScale, nref + L::kKeyScale, bars, cur, groups, w);
+    produce_tiles<N, kF16>(p, base, ids, nref + L::kQScale, nref + L::kKeyScale, bars, cur, groups, w);
   } else if (warp < kMmaWarp) {
     more_registers<kRegsSoftmax>();
     softmax<N, kF16>(p, base + L::kP, bars, tmem, nref, offsets, ids, cur, groups, sms, w);
   } else {
     fewer_registers<kRegsMma>();
-    if (warp == kIdWarp)
-      resolve_rows(p, ids, bars, cur, groups, w);
+    if (warp == kGatherWarp)
+      gather_rows<N, kF16>(p, &map, base, ids, bars, cur, groups, w);
     else if (warp == kMmaWarp)
       issue_products<N, kF16>(p, base, base + L::kQ, base + L::kP, bars, tmem, cur, groups, w);
   }
@@ -985,7 +982,7 @@ cudaError_t launch(const AttendParams& p, int sms, cudaStream_t s) {
     // the register trade waits for ever if the launch has fewer than it hands out
     if (e == cudaSuccess && a.numRegs != kRegsLaunch) e = cudaErrorInvalidKernelImage;
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(attend_kernel<N, kRowBytes>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<N>::kBytes);
+      e = cudaFuncSetAttribute(attend_kernel<N, kRowBytes>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<N, kRowBytes == HS_ROW_BYTES_FP8>::kBytes);
     return e;
   }();
   if (ready != cudaSuccess) return ready;
@@ -999,7 +996,9 @@ cudaError_t launch(const AttendParams& p, int sms, cudaStream_t s) {
     if (units * tiles < grid) grid = (int)(units * tiles);
     cut = tiles > 1 && units % grid != 0;
   }
-  attend_kernel<N, kRowBytes><<<grid, kThreads, Smem<N>::kBytes, s>>>(p, groups, sms);
+  CUtensorMap map;
+  if (!tc::gather_map(&map, p.base, p.row_bytes, p.num_rows, Raw<kRowBytes == HS_ROW_BYTES_FP8>::kBox)) return cudaErrorUnknown;
+  attend_kernel<N, kRowBytes><<<grid, kThreads, Smem<N, kRowBytes == HS_ROW_BYTES_FP8>::kBytes, s>>>(p, map, groups, sms);
   count_launch();
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !cut || grid < 2) return e;

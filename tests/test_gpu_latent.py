@@ -642,3 +642,24 @@ def test_refusals():
     refused(1, hs.attend_expanded, q, qr8, q, k, q, cum([8]), cum([8]), SCALE,
             out=torch.empty((8, 1, 128), dtype=torch.bfloat16, device="cuda").expand(8, 2, 128))
     assert hs.launch_count() == before
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "bf16"])
+@pytest.mark.parametrize("H", [16, 20, 32, 64])
+def test_rows_same_bits_with_cold_caches(fmt, H):
+    """Runs that follow a flush of the caches, with units cut between CTAs: slots and tiles are reused while loads are
+    late, and every run gives the same bits."""
+    g = gen(71)
+    pool, tensors = make_pool(g, 100, fmt)
+    rows = torch.randint(0, 6400, (40, 2048), generator=g, device="cuda").int()
+    ql, qr = normal(g, 40, H, D), normal(g, 40, H, RD)
+    ws = hs.alloc_attend_workspace()
+    flush = torch.empty(1 << 29, dtype=torch.uint8, device="cuda")
+    first = None
+    for i in range(25):
+        flush.fill_(i)
+        out, lse = hs.attend_rows(pool, rows, ql, qr, SCALE, workspace=ws)
+        if first is None:
+            first = (out.clone(), lse.clone())
+            check_rows(tensors, fmt, rows, ql, qr, SCALE, out, lse)
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
