@@ -29,8 +29,8 @@
 //   warp 24      issues the products;
 //   warps 16-23  softmax and results: lane = key (16 of a warp's lanes have one, as products of 64 rows lie in tensor
 //                memory), later lane = latent dimension; each of the two groups of four warps has half of the columns.
-// The tile (64 x 576, 72 KB) has one buffer, released in five parts: the rotated part after S, and four 128-dimension
-// blocks, each after its product with P.
+// The tile (64 x 576, 72 KB) has one buffer, which is filled and released in two halves of 256 latent dimensions (the
+// rotated part goes with the first): a hand-over costs some hundred cycles, so that more and smaller parts were slower.
 #include <type_traits>
 
 #include "latent.cuh"
@@ -136,6 +136,7 @@ template <int N, bool kF16>
 struct Smem {
   static constexpr int kQ = 9 * kSub;
   static constexpr bool kAlias = !kF16 && N == 64;  // no room for P: it takes the rotated part's place
+  static constexpr int kRopeHalf = kAlias ? 1 : 0;
   static constexpr int kP = kAlias ? 8 * kSub : kQ + 9 * N * 128;
   static constexpr int kRaw = kQ + 9 * N * 128 + (kAlias ? 0 : kTile * N * 2);
   // after the ring: barriers (384 B), row ids [kAhead][64], results' offsets [N] (64 bits), then floats: references,
@@ -153,7 +154,7 @@ struct Smem {
   // ids knows that the slots' earlier uses are over, which the parity of a barrier alone cannot tell
   static_assert(kSlots >= 4, "ring");
 };
-enum Bar { kFull = 0, kEmpty = 5, kQFull = 10, kQEmpty, kSFull, kPReady, kOFull, kDrain, kRawFull = 16, kRawEmpty = 24,
+enum Bar { kFull = 0, kEmpty = 2, kQFull = 4, kQEmpty, kSFull, kPReady, kOFull, kDrain, kRawFull = 16, kRawEmpty = 24,
            kIdFull = 32, kIdEmpty = kIdFull + kAhead, kBars = kIdEmpty + kAhead };
 static_assert(kBars * 8 <= 384, "barriers");
 
@@ -406,25 +407,18 @@ __device__ __forceinline__ void produce_tiles(const AttendParams& p, uint32_t ba
       }
       rope = make_uint4(bf16_to_half(rope.x, inv), bf16_to_half(rope.y, inv), bf16_to_half(rope.z, inv), bf16_to_half(rope.w, inv));
     }
-    // the operands, part by part as their places become free
-    auto free_part = [&](int c) {
-      if (it > 0) w.wait(bars + 8 * (kEmpty + c), (it - 1) & 1);
-    };
-    auto put_rope = [&]() {
-      free_part(4);
-      sts(base + 8 * kSub + key * 128 + ((j ^ swz) << 4), rope.x, rope.y, rope.z, rope.w);
-      signal(kFull + 4);
-    };
-    if (!L::kAlias) put_rope();
+    // the operands, half by half as their places become free
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      free_part(c);
-      if (kF16 && c == 0 && j == 0) skey[key] = 1.f / inv;  // (the softmax of the tile before has read its own)
+    for (int h = 0; h < 2; ++h) {
+      if (it > 0) w.wait(bars + 8 * (kEmpty + h), (it - 1) & 1);
+      if (kF16 && h == 0 && j == 0) skey[key] = 1.f / inv;  // (the softmax of the tile before has read its own)
+      if (h == L::kRopeHalf) sts(base + 8 * kSub + key * 128 + ((j ^ swz) << 4), rope.x, rope.y, rope.z, rope.w);
 #pragma unroll
-      for (int x = 0; x < 2; ++x) sts(at[x] + 2 * c * kSub, v[c][x].x, v[c][x].y, v[c][x].z, v[c][x].w);
-      signal(kFull + c);
+      for (int c = 2 * h; c < 2 * h + 2; ++c)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) sts(at[x] + 2 * c * kSub, v[c][x].x, v[c][x].y, v[c][x].z, v[c][x].w);
+      signal(kFull + h);
     }
-    if (L::kAlias) put_rope();
     fresh = cur.next(p, groups);
     ++it;
   }
@@ -512,19 +506,27 @@ __device__ __forceinline__ void issue_products(const AttendParams& p, uint32_t t
   while (cur.left > 0) {
     if (fresh) await(kQFull, seg & 1);
     const bool first = fresh;
-#pragma unroll 1
-    for (int n = 0; n < 5; ++n) {
-      const int c = L::kAlias ? n : n == 0 ? 4 : n - 1;  // the rotated part as its place becomes free: first, or last
-      await(kFull + c, it & 1);
-      const uint64_t a = dk + (uint32_t)(2 * c * kSub >> 4), b = dq + (uint32_t)(2 * c * (N * 128) >> 4);
+    bool accumulate = false;
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (k < 4 || c < 4)
+    for (int h = 0; h < 2; ++h) {
+      await(kFull + h, it & 1);
+      if (h == L::kRopeHalf) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          tc::mma_ss(tmem, dk + ((8 * kSub + k * 32) >> 4), dq + ((8 * N * 128 + k * 32) >> 4), kIdS, accumulate || k > 0, leader);
+        accumulate = true;
+      }
+#pragma unroll 1
+      for (int c = 2 * h; c < 2 * h + 2; ++c) {
+        const uint64_t a = dk + (uint32_t)(2 * c * kSub >> 4), b = dq + (uint32_t)(2 * c * (N * 128) >> 4);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
           tc::mma_ss(tmem, a + (((k >> 2) * kSub + (k & 3) * 32) >> 4), b + (((k >> 2) * (N * 128) + (k & 3) * 32) >> 4), kIdS,
-                     n > 0 || k > 0, leader);
+                     accumulate || k > 0, leader);
+        accumulate = true;
+      }
     }
     tc::commit(bars + 8 * kSFull, leader);
-    if (!L::kAlias) tc::commit(bars + 8 * (kEmpty + 4), leader);
     fresh = cur.next(p, groups);
     const bool last = fresh || cur.left == 0;
     if (last) tc::commit(bars + 8 * kQEmpty, leader);
@@ -535,9 +537,8 @@ __device__ __forceinline__ void issue_products(const AttendParams& p, uint32_t t
 #pragma unroll
       for (int k = 0; k < kTile / 16; ++k)
         tc::mma_ss(tmem + N + g * N, a + (k * 2048 >> 4), dp + ((k * 16 * N * 2) >> 4), kIdO, !first || k > 0, leader);
-      tc::commit(bars + 8 * (kEmpty + g), leader);
+      if (g & 1) tc::commit(bars + 8 * (kEmpty + g / 2), leader);
     }
-    if (L::kAlias) tc::commit(bars + 8 * (kEmpty + 4), leader);
     if (last) {
       tc::commit(bars + 8 * kOFull, leader);
       ++seg;
@@ -876,7 +877,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const AttendParams 
   if ((int)blockIdx.x >= ctas) return;
 
   if (threadIdx.x == 0) {
-    for (int c = 0; c < 5; ++c) {
+    for (int c = 0; c < 2; ++c) {
       tc::mbar_init(bars + 8 * (kFull + c), kProducerWarps);
       tc::mbar_init(bars + 8 * (kEmpty + c), 1);
     }
