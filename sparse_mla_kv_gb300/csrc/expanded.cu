@@ -1,68 +1,460 @@
-// Attention over keys and values expanded to every head: prompts and prompt chunks.
+// Attention over keys and values expanded to every head, on the tensor cores: prompts and prompt chunks.
 //
-// First form: one warp per (query, head), running maximum and sum.
+// Mathematics.  A query row keeps a reference m, a sum l and an accumulator O over the key tiles:
+//   S = Q K^T (192 = 128 of the head + 64 of the shared rotated part), P = exp2(S scale - m), l += sum P, O += P V.
+// The reference is lazy: it starts as the first tile's maximum and moves (with l and O rescaled) only when a score exceeds
+// it by kLazy; bf16 weights have fp32's range, so nothing is lost by it.  The rotated part of the keys is read where it is,
+// once for each head, and never copied to every head.
+//
+// Layout.  A work item is (sequence, head, 256 queries): two tiles of 128 queries over the same key tiles of 128, so that
+// a key or value loaded serves 256 queries (81 KB a key tile; one query tile alone would need 64 B a cycle from L2).
+// 12 warps, one CTA per SM, items taken in a fixed stride:
+//   warps 0-3, 4-7   softmax and results of query tile 0 and 1, a row a thread;
+//   warp 8           issues the products, and zeroes value rows past a sequence's end before their product (a weight of
+//                    zero does not cancel a NaN there);
+//   warp 9           loads by the copy engine.
+// Shared memory: 96 KB of queries and a ring of eight 16 KB units (128 keys x 64 dimensions); a key tile is three units
+// of keys, then two of values.  Tensor memory: S and O of both tiles, 4 x 128 columns; P, in bf16, takes S's place and is
+// the left operand of the second product from there.
+// Bound: the tensor pipe, 12 x 64 + 8 x 64 cycles for 128 queries x 128 keys.
 #include "latent.cuh"
+#include "tc.cuh"
 
 namespace hs {
 namespace {
 
-__global__ void __launch_bounds__(128) expanded_kernel(const hs_expanded a, float scale_log2) {
+constexpr int kQRows = 128, kKeys = 128, kBlock = 2 * kQRows;
+constexpr int kUnit = kKeys * 128;  // bytes of a unit
+constexpr int kRing = 8, kUnitsK = 3, kUnitsV = 2, kUnits = kUnitsK + kUnitsV;
+constexpr int kThreads = 12 * 32, kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kSmemBytes = 6 * kUnit + kRing * kUnit + 512 + 1024;
+constexpr float kLazy = 64.f;
+enum Bar { kFull = 0, kEmpty = kRing, kQFull = 2 * kRing, kQEmpty, kSFull, kPReady = kSFull + 2, kODone = kPReady + 2,
+           kDrain = kODone + 2, kBars };
+static_assert(kBars * 8 <= 512, "barriers");
+
+struct Maps {
+  CUtensorMap q_nope, q_rope, k_nope, k_rope, v;
+  int32_t head_step[4];  // of q_nope, q_rope, k_nope, v: 0 where all heads read one
+};
+
+// One work item: rows [q0, q0 + rows) of the query tensors, keys [k0, k0 + keys).
+struct Item {
+  int head, q0, rows, k0, keys;
+  int shift;  // query row r (counted from q0) sees the keys below r + shift (keys, where not causal)
+  int tiles[2];  // key tiles of each query tile; -1: no such query tile
+  __device__ __forceinline__ int query_tiles() const { return rows > kQRows ? 2 : 1; }
+  __device__ __forceinline__ int most() const { return max(tiles[0], tiles[1]); }
+};
+
+// Sequence s: its rows, or nothing where its offsets are not ascending within the tensors.
+__device__ __forceinline__ bool sequence(const hs_expanded& a, int s, int* q0, int* q1, int* k0, int* k1) {
+  *q0 = __ldg(a.cu_q + s), *q1 = __ldg(a.cu_q + s + 1), *k0 = __ldg(a.cu_k + s), *k1 = __ldg(a.cu_k + s + 1);
+  return *q0 >= 0 && *q1 >= *q0 && *q1 <= a.q_tokens && *k0 >= 0 && *k1 >= *k0 && *k1 <= a.k_tokens;
+}
+
+// Work item number n (a warp's lanes together); false when there are no more.  Items are numbered by sequence, then by
+// block of queries from the last (the longest) to the first, then by head.
+__device__ __forceinline__ bool find_item(const hs_expanded& a, int64_t n, Item* it) {
   const int lane = threadIdx.x & 31;
-  const int64_t u = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (u >= a.q_tokens * a.heads) return;
-  if (u == 0 && lane == 0)
-    for (int s = 0; s < a.seqs; ++s) {
-      const int x0 = __ldg(a.cu_q + s), x1 = __ldg(a.cu_q + s + 1), y0 = __ldg(a.cu_k + s), y1 = __ldg(a.cu_k + s + 1);
-      if (x0 < 0 || x1 < x0 || x1 > a.q_tokens || y0 < 0 || y1 < y0 || y1 > a.k_tokens) report(a.status, HS_ERR_ID_RANGE);
+  const int64_t block = n / a.heads;
+  int64_t before = 0;
+  for (int s0 = 0; s0 < a.seqs; s0 += 32) {
+    const int s = s0 + lane;
+    int q0 = 0, q1 = 0, k0 = 0, k1 = 0;
+    const bool ok = s < a.seqs && sequence(a, s, &q0, &q1, &k0, &k1);
+    const int blocks = ok ? (q1 - q0 + kBlock - 1) / kBlock : 0;
+    int64_t upto = blocks;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t y = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+      if (lane >= d) upto += y;
     }
-  const int64_t i = u / a.heads;
-  const int h = (int)(u - i * a.heads);
-  int b = -1, q0 = 0, q1 = 0;
-  for (int s = 0; s < a.seqs; ++s) {
-    q0 = __ldg(a.cu_q + s), q1 = __ldg(a.cu_q + s + 1);
-    if (i >= q0 && i < q1) {
-      b = s;
-      break;
+    const unsigned has = __ballot_sync(0xFFFFFFFFu, block < before + upto);
+    if (has) {
+      const int who = __ffs(has) - 1;
+      const int from_end = (int)(before + __shfl_sync(0xFFFFFFFFu, upto, who) - 1 - block);
+      q0 = __shfl_sync(0xFFFFFFFFu, q0, who), q1 = __shfl_sync(0xFFFFFFFFu, q1, who);
+      k0 = __shfl_sync(0xFFFFFFFFu, k0, who), k1 = __shfl_sync(0xFFFFFFFFu, k1, who);
+      const int first = from_end * kBlock;
+      it->head = (int)(n - block * a.heads);
+      it->q0 = q0 + first;
+      it->rows = min(kBlock, q1 - q0 - first);
+      it->k0 = k0;
+      it->keys = k1 - k0;
+      it->shift = a.causal ? first + 1 + (k1 - k0) - (q1 - q0) : 0;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int last = min(it->rows, (t + 1) * kQRows) - 1;  // the tile's last row sees most
+        const int sees = a.causal ? min(it->keys, last + it->shift) : it->keys;
+        it->tiles[t] = last < t * kQRows ? -1 : max(0, (sees + kKeys - 1) / kKeys);
+      }
+      return true;
+    }
+    before += __shfl_sync(0xFFFFFFFFu, upto, 31);
+  }
+  return false;
+}
+
+__device__ __forceinline__ void load3(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+// ---- loads (one lane) ----
+__device__ __forceinline__ void load_items(const hs_expanded& a, const Maps& m, uint32_t q, uint32_t ring, uint32_t bars) {
+  tc::Waiter w;
+  const bool leader = tc::elect();
+  uint32_t u = 0, count = 0;
+  Item it;
+  for (int64_t n = blockIdx.x; find_item(a, n, &it); n += gridDim.x) {
+    if (it.most() <= 0) continue;
+    if (count > 0) w.wait(bars + 8 * kQEmpty, (count - 1) & 1);
+    ++count;
+    __syncwarp();
+    const int hq = it.head * m.head_step[0], hr = it.head * m.head_step[1], hk = it.head * m.head_step[2],
+              hv = it.head * m.head_step[3];
+    if (leader) {
+      tc::mbar_expect(bars + 8 * kQFull, it.query_tiles() * 3 * kUnit);
+      for (int t = 0; t < it.query_tiles(); ++t) {
+        const uint32_t to = q + t * 3 * kUnit;
+        const int row = it.q0 + t * kQRows;
+        load3(to, &m.q_nope, 0, hq, row, bars + 8 * kQFull);
+        load3(to + kUnit, &m.q_nope, 64, hq, row, bars + 8 * kQFull);
+        load3(to + 2 * kUnit, &m.q_rope, 0, hr, row, bars + 8 * kQFull);
+      }
+    }
+    const int tiles = it.most();
+#pragma unroll 1
+    for (int j = 0; j < tiles; ++j) {
+      const int row = it.k0 + j * kKeys;
+#pragma unroll 1
+      for (int i = 0; i < kUnits; ++i, ++u) {
+        const uint32_t slot = u % kRing;
+        if (u >= kRing) w.wait(bars + 8 * (kEmpty + slot), (u / kRing - 1) & 1);
+        __syncwarp();
+        if (leader) {
+          const uint32_t bar = bars + 8 * (kFull + slot), to = ring + slot * kUnit;
+          tc::mbar_expect(bar, kUnit);
+          if (i < 2)
+            load3(to, &m.k_nope, 64 * i, hk, row, bar);
+          else if (i == 2)
+            load3(to, &m.k_rope, 0, 0, row, bar);
+          else
+            load3(to, &m.v, 64 * (i - 3), hv, row, bar);
+        }
+      }
     }
   }
-  if (b < 0) return;
-  const int k0 = __ldg(a.cu_k + b), k1 = __ldg(a.cu_k + b + 1);
-  if (q0 < 0 || q1 > a.q_tokens || k0 < 0 || k1 < k0 || k1 > a.k_tokens) return;
-  int64_t keys = k1 - k0;
-  if (a.causal) keys = min(keys, (i - q0) + 1 + keys - (q1 - q0));
-  const __nv_bfloat16* qn = static_cast<const __nv_bfloat16*>(a.q_nope) + i * a.qn_token_stride + h * a.qn_head_stride;
-  const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(a.q_rope) + i * a.qr_token_stride + h * a.qr_head_stride;
-  float q[6], acc[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
-  for (int x = 0; x < 4; ++x) q[x] = __bfloat162float(qn[4 * lane + x]);
-  for (int x = 0; x < 2; ++x) q[4 + x] = __bfloat162float(qr[2 * lane + x]);
-  for (int64_t j = k0; j < k0 + keys; ++j) {
-    const __nv_bfloat16* kn = static_cast<const __nv_bfloat16*>(a.k_nope) + j * a.kn_token_stride + h * a.kn_head_stride;
-    const __nv_bfloat16* kr = static_cast<const __nv_bfloat16*>(a.k_rope) + j * a.kr_token_stride;
-    const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v) + j * a.v_token_stride + h * a.v_head_stride;
-    float s = 0.f;
-    for (int x = 0; x < 4; ++x) s += q[x] * __bfloat162float(kn[4 * lane + x]);
-    for (int x = 0; x < 2; ++x) s += q[4 + x] * __bfloat162float(kr[2 * lane + x]);
-    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-    s *= scale_log2;
-    const float top = fmaxf(m, s);
-    const float keep = m == -INFINITY ? 0.f : exp2f(m - top), w = exp2f(s - top);
-    l = l * keep + w;
-    for (int x = 0; x < 4; ++x) acc[x] = acc[x] * keep + w * __bfloat162float(v[4 * lane + x]);
-    m = top;
+  // no copy is in flight when the CTA ends
+  tc::Waiter drain;
+  for (uint32_t r = u > kRing ? u - kRing : 0; r < u; ++r) drain.wait(bars + 8 * (kFull + r % kRing), (r / kRing) & 1);
+  if (count > 0) drain.wait(bars + 8 * kQFull, (count - 1) & 1);
+  if (w.dead) report(a.status, HS_ERR_TIMEOUT);
+}
+
+// ---- products (one warp) ----
+__device__ __forceinline__ void issue_items(const hs_expanded& a, uint32_t q, uint32_t ring, uint32_t bars, uint32_t tmem) {
+  constexpr uint32_t kIdS = tc::idesc(false, 128, kKeys, false, false);
+  constexpr uint32_t kIdO = tc::idesc(false, 128, 64, false, true);
+  tc::Waiter w;
+  const bool leader = tc::elect();
+  const uint64_t dq = tc::desc(q, 16, 1024, tc::kSwizzle128);
+  const uint64_t dk = tc::desc(ring, 16, 1024, tc::kSwizzle128);
+  const uint64_t dv = tc::desc(ring, 16, 1024, tc::kSwizzle128);  // dimensions contiguous, 64 of them: one atom wide
+  auto await = [&](int bar, uint32_t parity) {
+    w.wait(bars + 8 * bar, parity);
+    __syncwarp();
+    tc::fence_after();
+  };
+  uint32_t base = 0, count = 0;
+  uint32_t phase[2] = {0, 0};  // key tiles done by each query tile
+  Item it;
+  for (int64_t n = blockIdx.x; find_item(a, n, &it); n += gridDim.x) {
+    const int tiles = it.most();
+    if (tiles <= 0) continue;
+    const bool partial = it.keys - (tiles - 1) * kKeys < kKeys;
+    auto scores = [&](int t, int j) {  // S of query tile t and key tile j
+#pragma unroll 1
+      for (int i = 0; i < kUnitsK; ++i) {
+        const uint32_t x = base + j * kUnits + i;
+        await(kFull + x % kRing, (x / kRing) & 1);
+        const uint64_t da = dq + (uint32_t)((t * 3 + i) * kUnit >> 4), db = dk + (uint32_t)((x % kRing) * kUnit >> 4);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tc::mma_ss(tmem + t * 128, da + (k * 32 >> 4), db + (k * 32 >> 4), kIdS, i > 0 || k > 0, leader);
+      }
+      tc::commit(bars + 8 * (kSFull + t), leader);
+    };
+    auto release = [&](int j, int from, int to) {  // units of key tile j, when all products so far have read them
+      for (int i = from; i < to; ++i) tc::commit(bars + 8 * (kEmpty + (base + j * kUnits + i) % kRing), leader);
+    };
+    await(kQFull, count & 1);
+    ++count;
+#pragma unroll 1
+    for (int t = 0; t < 2; ++t)
+      if (it.tiles[t] > 0) {
+        if (phase[t] > 0) await(kODone + t, (phase[t] - 1) & 1);  // the item before: its last P has been read
+        scores(t, 0);
+      }
+    release(0, 0, kUnitsK);
+    if (tiles == 1) tc::commit(bars + 8 * kQEmpty, leader);
+#pragma unroll 1
+    for (int j = 0; j < tiles; ++j) {
+      const int last_of_values = it.tiles[1] > j ? 1 : 0;
+#pragma unroll 1
+      for (int t = 0; t < 2; ++t) {
+        if (j >= it.tiles[t]) continue;
+        await(kPReady + t, phase[t] & 1);
+        const bool fix = partial && j == tiles - 1 && (t == 0 || it.tiles[0] <= j);  // by the first that reads them
+#pragma unroll 1
+        for (int i = 0; i < kUnitsV; ++i) {
+          const uint32_t x = base + j * kUnits + kUnitsK + i;
+          await(kFull + x % kRing, (x / kRing) & 1);
+          if (fix) {
+            const int valid = it.keys - j * kKeys;
+            for (int k = threadIdx.x & 31; k < (kKeys - valid) * 8; k += 32) {
+              const uint32_t at = ring + (x % kRing) * kUnit + (valid + (k >> 3)) * 128 + (k & 7) * 16;
+              asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0u) : "memory");
+            }
+            tc::fence_async_smem();
+            __syncwarp();
+          }
+          const uint64_t db = dv + (uint32_t)((x % kRing) * kUnit >> 4);
+          // P: 16 keys are 8 columns
+#pragma unroll
+          for (int k = 0; k < kKeys / 16; ++k)
+            tc::mma_ts(tmem + 256 + t * 128 + i * 64, tmem + t * 128 + k * 8, db + (k * 2048 >> 4), kIdO, j > 0 || k > 0, leader);
+        }
+        tc::commit(bars + 8 * (kODone + t), leader);
+        if (t == last_of_values) release(j, kUnitsK, kUnits);
+        if (j + 1 < it.tiles[t]) {
+          await(kODone + t, phase[t] & 1);  // P, in S's place, has been read
+          scores(t, j + 1);
+        }
+        ++phase[t];
+      }
+      if (j + 1 < tiles) release(j + 1, 0, kUnitsK);
+      if (j + 2 == tiles) tc::commit(bars + 8 * kQEmpty, leader);
+    }
+    base += tiles * kUnits;
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + i * a.out_token_stride + h * a.out_head_stride;
-  for (int x = 0; x < 4; ++x) o[4 * lane + x] = __float2bfloat16_rn(acc[x] * inv);
-  if (lane == 0 && a.lse) a.lse[i * a.heads + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  tc::commit(bars + 8 * kDrain, leader);
+  tc::Waiter drain;
+  drain.wait(bars + 8 * kDrain, 0);
+  __syncwarp();
+  if (w.dead) report(a.status, HS_ERR_TIMEOUT);
+}
+
+// ---- softmax and results (128 threads a query tile) ----
+__device__ __forceinline__ void softmax_items(const hs_expanded& a, float scale_log2, uint32_t bars, uint32_t tmem) {
+  tc::Waiter w;
+  const int t = threadIdx.x >> 7, lane = threadIdx.x & 31;
+  const int row_in_tile = threadIdx.x & 127;
+  const uint32_t lanes = (uint32_t)(32 * ((threadIdx.x >> 5) & 3)) << 16;
+  const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * 128;
+  uint32_t phase = 0;
+  Item it;
+  for (int64_t n = blockIdx.x; find_item(a, n, &it); n += gridDim.x) {
+    const int tiles = it.tiles[t];
+    if (tiles < 0) continue;
+    const int row = t * kQRows + row_in_tile;
+    const int sees = a.causal ? min(it.keys, row + it.shift) : it.keys;  // keys below this one are seen
+    const int all_see = a.causal ? min(it.keys, t * kQRows + it.shift) : it.keys;  // by every row of the tile
+    float m = -INFINITY;
+    float2 l2 = make_float2(0.f, 0.f);
+#pragma unroll 1
+    for (int j = 0; j < tiles; ++j, ++phase) {
+      w.wait(bars + 8 * (kSFull + t), phase & 1);
+      __syncwarp();
+      tc::fence_after();
+      float s[128];
+      tc::tmem_ld<128>(ts, s);
+      tc::tmem_wait_ld();
+      tc::touch<128>(s);
+      if ((j + 1) * kKeys > all_see) {
+        const int left = sees - j * kKeys;
+#pragma unroll
+        for (int c = 0; c < 128; ++c)
+          if (c >= left) s[c] = -INFINITY;
+      }
+      // largest and smallest: a negative scale turns them round
+      float top = s[0], low = INFINITY;
+#pragma unroll
+      for (int c = 1; c < 128; ++c) top = fmaxf(top, s[c]);
+      if (scale_log2 < 0.f) {
+#pragma unroll
+        for (int c = 0; c < 128; ++c) low = s[c] == -INFINITY ? low : fminf(low, s[c]);
+        top = top == -INFINITY ? top : low;
+      }
+      top = top == -INFINITY ? top : top * scale_log2;
+      const bool over = top > m + kLazy;  // (m = -infinity: on the first key seen)
+      if (__any_sync(0xFFFFFFFFu, over)) {
+        const float now = over ? top : m;
+        const float alpha = over ? (m == -INFINITY ? 0.f : exp2f(m - now)) : 1.f;
+        m = now;
+        l2.x *= alpha, l2.y *= alpha;
+        if (j > 0) {  // the products so far have finished: this tile's scores were issued after them
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 16) {
+            float o[16];
+            tc::tmem_ld16(to + c, o);
+            tc::tmem_wait_ld();
+            tc::touch<16>(o);
+#pragma unroll
+            for (int x = 0; x < 16; ++x) o[x] *= alpha;
+            tc::tmem_st16(to + c, o);
+          }
+          tc::tmem_wait_st();
+        }
+      }
+      // P = exp2(s scale - m): a hidden key's -infinity stays one under any finite scale times 1, zero for rows without keys
+      const float sc = scale_log2, base = m == -INFINITY ? 0.f : -m;
+      const bool hidden = (j + 1) * kKeys > all_see;
+      const float2 sc2 = make_float2(sc, sc), base2 = make_float2(base, base);
+#pragma unroll
+      for (int c = 0; c < 128; c += 32) {
+        uint32_t p[16];
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+          const float2 y = tc::fma2(make_float2(s[c + 2 * x], s[c + 2 * x + 1]), sc2, base2);
+          float2 e = make_float2(tc::exp2_fast(y.x), tc::exp2_fast(y.y));
+          if (hidden) {
+            e.x = s[c + 2 * x] == -INFINITY ? 0.f : e.x;
+            e.y = s[c + 2 * x + 1] == -INFINITY ? 0.f : e.y;
+          }
+          l2 = tc::add2(l2, e);
+          p[x] = tc::pack_bf16(e.x, e.y);
+        }
+        tc::tmem_st16(ts + c / 2, reinterpret_cast<const float*>(p));
+      }
+      tc::tmem_wait_st();
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bars + 8 * (kPReady + t));
+    }
+    // results
+    const float l = l2.x + l2.y;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (tiles > 0) {
+      w.wait(bars + 8 * (kODone + t), (phase - 1) & 1);
+      __syncwarp();
+      tc::fence_after();
+    }
+    const bool there = row < it.rows;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (int64_t)(it.q0 + (there ? row : 0)) * a.out_token_stride +
+                         it.head * a.out_head_stride;
+#pragma unroll 1
+    for (int c = 0; c < 128; c += 32) {
+      float o[32];
+      if (tiles > 0) {
+        tc::tmem_ld<32>(to + c, o);
+        tc::tmem_wait_ld();
+        tc::touch<32>(o);
+      }
+#pragma unroll
+      for (int x = 0; x < 32; ++x) o[x] = l == 0.f ? 0.f : o[x] * inv;
+      if (there) {
+#pragma unroll
+        for (int x = 0; x < 32; x += 8)
+          *reinterpret_cast<uint4*>(out + c + x) =
+              make_uint4(tc::pack_bf16(o[x], o[x + 1]), tc::pack_bf16(o[x + 2], o[x + 3]), tc::pack_bf16(o[x + 4], o[x + 5]),
+                         tc::pack_bf16(o[x + 6], o[x + 7]));
+      }
+    }
+    if (there && a.lse)
+      a.lse[(int64_t)(it.q0 + row) * a.heads + it.head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    tc::fence_before();
+  }
+  if (w.dead) report(a.status, HS_ERR_TIMEOUT);
+}
+
+__global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const hs_expanded a, const __grid_constant__ Maps maps,
+                                                               float scale_log2) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint32_t tmem_slot;
+  const uint32_t q = (tc::smem_u32(smem_raw) + 1023) & ~1023u;
+  const uint32_t ring = q + 6 * kUnit, bars = ring + kRing * kUnit;
+  const int warp = threadIdx.x >> 5;
+  if (blockIdx.x == 0)
+    for (int s = threadIdx.x; s < a.seqs; s += kThreads) {
+      int q0, q1, k0, k1;
+      if (!sequence(a, s, &q0, &q1, &k0, &k1)) report(a.status, HS_ERR_ID_RANGE);
+    }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kRing; ++i) {
+      tc::mbar_init(bars + 8 * (kFull + i), 1);
+      tc::mbar_init(bars + 8 * (kEmpty + i), 1);
+    }
+    tc::mbar_init(bars + 8 * kQFull, 1);
+    tc::mbar_init(bars + 8 * kQEmpty, 1);
+    for (int t = 0; t < 2; ++t) {
+      tc::mbar_init(bars + 8 * (kSFull + t), 1);
+      tc::mbar_init(bars + 8 * (kPReady + t), 4);
+      tc::mbar_init(bars + 8 * (kODone + t), 1);
+    }
+    tc::mbar_init(bars + 8 * kDrain, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kMmaWarp) tc::tmem_alloc(tc::smem_u32(&tmem_slot), 512);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = tmem_slot;
+  if (warp < 8)
+    softmax_items(a, scale_log2, bars, tmem);
+  else if (warp == kMmaWarp)
+    issue_items(a, q, ring, bars, tmem);
+  else if (warp == kLoadWarp)
+    load_items(a, maps, q, ring, bars);
+  __syncwarp();
+  tc::fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc::fence_after();
+    tc::tmem_free(tmem, 512);
+  }
+}
+
+// Tensor map of [tokens][heads][dims] in bf16 for boxes of 128 tokens x 64 dimensions of a head.
+bool make_map(CUtensorMap* map, const void* base, int64_t dims, int64_t heads, int64_t tokens, int64_t head_stride,
+              int64_t token_stride) {
+  if (!tc::encode_tiled()) return false;
+  const cuuint64_t size[3] = {(cuuint64_t)dims, (cuuint64_t)heads, (cuuint64_t)tokens};
+  const cuuint64_t strides[2] = {(cuuint64_t)(heads > 1 ? head_stride * 2 : 256), (cuuint64_t)(tokens > 1 ? token_stride * 2 : 256)};
+  const cuuint32_t box[3] = {64, 1, 128}, steps[3] = {1, 1, 1};
+  return tc::encode_tiled()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), size, strides, box, steps,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
 
 cudaError_t launch_expanded(const hs_expanded& a, int sms, cudaStream_t s) {
-  (void)sms;
-  const int64_t blocks = (a.q_tokens * a.heads + 3) / 4;
-  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-  expanded_kernel<<<(unsigned)blocks, 128, 0, s>>>(a, a.scale * kLog2e);
+  static const cudaError_t ready =
+      cudaFuncSetAttribute(expanded_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (ready != cudaSuccess) return ready;
+  Maps m;
+  // a head stride of zero broadcasts one head: a map of one head, read at head 0
+  const int64_t strides[4] = {a.qn_head_stride, a.qr_head_stride, a.kn_head_stride, a.v_head_stride};
+  int64_t heads[4];
+  for (int i = 0; i < 4; ++i) {
+    m.head_step[i] = strides[i] > 0 ? 1 : 0;
+    heads[i] = strides[i] > 0 ? a.heads : 1;
+  }
+  // no keys at all: the maps describe the queries, and nothing is read through them
+  const bool keys = a.k_tokens > 0;
+  if (!make_map(&m.q_nope, a.q_nope, kNope, heads[0], a.q_tokens, strides[0], a.qn_token_stride) ||
+      !make_map(&m.q_rope, a.q_rope, kRope, heads[1], a.q_tokens, strides[1], a.qr_token_stride) ||
+      (keys && (!make_map(&m.k_nope, a.k_nope, kNope, heads[2], a.k_tokens, strides[2], a.kn_token_stride) ||
+                !make_map(&m.k_rope, a.k_rope, kRope, 1, a.k_tokens, 0, a.kr_token_stride) ||
+                !make_map(&m.v, a.v, kValue, heads[3], a.k_tokens, strides[3], a.v_token_stride))))
+    return cudaErrorInvalidValue;
+  // at most this many items: every sequence may end in a block of its own
+  const int64_t most = (a.q_tokens / kBlock + a.seqs) * a.heads;
+  const int grid = (int)(most < sms ? most : sms);
+  expanded_kernel<<<grid, kThreads, kSmemBytes, s>>>(a, m, a.scale * kLog2e);
   count_launch();
   return cudaGetLastError();
 }

@@ -156,6 +156,9 @@ hs_status hs_attend_expanded(const hs_expanded* a, hs_stream_t stream) {
       !stride_ok(a->v_head_stride, 2, h) || !out_stride_ok(a->out_token_stride, 2, q, hs::kValue) ||
       !out_stride_ok(a->out_head_stride, 2, h, hs::kValue))
     return HS_ERR_INVALID_ARG;
+  if ((q > 1 && (a->qn_token_stride == 0 || a->qr_token_stride == 0)) ||
+      (k > 1 && (a->kn_token_stride == 0 || a->kr_token_stride == 0 || a->v_token_stride == 0)))
+    return HS_ERR_INVALID_ARG;
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) {
     cudaGetLastError();
