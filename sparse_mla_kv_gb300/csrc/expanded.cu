@@ -28,6 +28,9 @@ constexpr int kUnit = kKeys * 128;  // bytes of a unit
 constexpr int kRing = 8, kUnitsK = 3, kUnitsV = 2, kUnits = kUnitsK + kUnitsV;
 constexpr int kThreads = 12 * 32, kMmaWarp = 8, kLoadWarp = 9;
 constexpr int kSmemBytes = 6 * kUnit + kRing * kUnit + 512 + 1024;
+// the warpgroups trade registers
+constexpr int kRegsLaunch = 168, kRegsSoftmax = 208, kRegsOther = 88;
+static_assert(2 * kRegsSoftmax + kRegsOther <= 3 * kRegsLaunch, "more registers than the launch has");
 constexpr float kLazy = 64.f;
 enum Bar { kFull = 0, kEmpty = kRing, kQFull = 2 * kRing, kQEmpty, kSFull, kPReady = kSFull + 2, kODone = kPReady + 2,
            kDrain = kODone + 2, kBars };
@@ -254,6 +257,10 @@ __device__ __forceinline__ void softmax_items(const hs_expanded& a, float scale_
   const int row_in_tile = threadIdx.x & 127;
   const uint32_t lanes = (uint32_t)(32 * ((threadIdx.x >> 5) & 3)) << 16;
   const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * 128;
+  // a negative scale turns the scores round; a scale of zero becomes the smallest normal number, so that a hidden key's
+  // -infinity stays one
+  const bool negative = scale_log2 < 0.f;
+  const float scale = fmaxf(fabsf(scale_log2), 1.17549435e-38f);
   uint32_t phase = 0;
   Item it;
   for (int64_t n = blockIdx.x; find_item(a, n, &it); n += gridDim.x) {
@@ -273,22 +280,21 @@ __device__ __forceinline__ void softmax_items(const hs_expanded& a, float scale_
       tc::tmem_ld<128>(ts, s);
       tc::tmem_wait_ld();
       tc::touch<128>(s);
-      if ((j + 1) * kKeys > all_see) {
+      if (negative) {
+#pragma unroll
+        for (int c = 0; c < 128; ++c) s[c] = -s[c];
+      }
+      const bool hidden = (j + 1) * kKeys > all_see;
+      if (hidden) {
         const int left = sees - j * kKeys;
 #pragma unroll
         for (int c = 0; c < 128; ++c)
           if (c >= left) s[c] = -INFINITY;
       }
-      // largest and smallest: a negative scale turns them round
-      float top = s[0], low = INFINITY;
+      float top = s[0];
 #pragma unroll
       for (int c = 1; c < 128; ++c) top = fmaxf(top, s[c]);
-      if (scale_log2 < 0.f) {
-#pragma unroll
-        for (int c = 0; c < 128; ++c) low = s[c] == -INFINITY ? low : fminf(low, s[c]);
-        top = top == -INFINITY ? top : low;
-      }
-      top = top == -INFINITY ? top : top * scale_log2;
+      top *= scale;
       const bool over = top > m + kLazy;  // (m = -infinity: on the first key seen)
       if (__any_sync(0xFFFFFFFFu, over)) {
         const float now = over ? top : m;
@@ -309,10 +315,7 @@ __device__ __forceinline__ void softmax_items(const hs_expanded& a, float scale_
           tc::tmem_wait_st();
         }
       }
-      // P = exp2(s scale - m): a hidden key's -infinity stays one under any finite scale times 1, zero for rows without keys
-      const float sc = scale_log2, base = m == -INFINITY ? 0.f : -m;
-      const bool hidden = (j + 1) * kKeys > all_see;
-      const float2 sc2 = make_float2(sc, sc), base2 = make_float2(base, base);
+      const float2 sc2 = make_float2(scale, scale), base2 = make_float2(m == -INFINITY ? 0.f : -m, m == -INFINITY ? 0.f : -m);
 #pragma unroll
       for (int c = 0; c < 128; c += 32) {
         uint32_t p[16];
@@ -320,10 +323,6 @@ __device__ __forceinline__ void softmax_items(const hs_expanded& a, float scale_
         for (int x = 0; x < 16; ++x) {
           const float2 y = tc::fma2(make_float2(s[c + 2 * x], s[c + 2 * x + 1]), sc2, base2);
           float2 e = make_float2(tc::exp2_fast(y.x), tc::exp2_fast(y.y));
-          if (hidden) {
-            e.x = s[c + 2 * x] == -INFINITY ? 0.f : e.x;
-            e.y = s[c + 2 * x + 1] == -INFINITY ? 0.f : e.y;
-          }
           l2 = tc::add2(l2, e);
           p[x] = tc::pack_bf16(e.x, e.y);
         }
@@ -402,12 +401,16 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const hs_expanded
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = tmem_slot;
-  if (warp < 8)
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     softmax_items(a, scale_log2, bars, tmem);
-  else if (warp == kMmaWarp)
-    issue_items(a, q, ring, bars, tmem);
-  else if (warp == kLoadWarp)
-    load_items(a, maps, q, ring, bars);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    if (warp == kMmaWarp)
+      issue_items(a, q, ring, bars, tmem);
+    else if (warp == kLoadWarp)
+      load_items(a, maps, q, ring, bars);
+  }
   __syncwarp();
   tc::fence_before();
   __syncthreads();
@@ -432,8 +435,14 @@ bool make_map(CUtensorMap* map, const void* base, int64_t dims, int64_t heads, i
 }  // namespace
 
 cudaError_t launch_expanded(const hs_expanded& a, int sms, cudaStream_t s) {
-  static const cudaError_t ready =
-      cudaFuncSetAttribute(expanded_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  static const cudaError_t ready = [] {
+    cudaFuncAttributes f{};
+    cudaError_t e = cudaFuncGetAttributes(&f, expanded_kernel);
+    // the register trade waits for ever if the launch has fewer than it hands out
+    if (e == cudaSuccess && f.numRegs != kRegsLaunch) e = cudaErrorInvalidKernelImage;
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(expanded_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    return e;
+  }();
   if (ready != cudaSuccess) return ready;
   Maps m;
   // a head stride of zero broadcasts one head: a map of one head, read at head 0
