@@ -647,9 +647,7 @@ __device__ __forceinline__ void softmax(const AttendParams& p, uint32_t pt, uint
 #pragma unroll 1
     while (true) {
       scores(true);
-      float top = s[0];
-#pragma unroll
-      for (int c = 1; c < kW; ++c) top = fmaxf(top, s[c]);
+      const float top = tc::max_of<kW>(s);
       if (moved || !any_softmax(has_key && (top > kLazy || (kF16 && there && sk > scalars[0])))) break;
       moved = true;
       // a new reference for every column, kTop below the maximum of the old one's and this tile's scores

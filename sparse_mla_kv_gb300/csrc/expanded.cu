@@ -99,6 +99,12 @@ __device__ __forceinline__ bool find_item(const hs_expanded& a, int64_t n, Item*
   return false;
 }
 
+// This CTA's k-th item: passes over the grid in alternating directions, so that who had a long block first has a short one
+// of the next pass.
+__device__ __forceinline__ int64_t item_number(int k) {
+  return (int64_t)k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+}
+
 __device__ __forceinline__ void load3(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
@@ -112,7 +118,7 @@ __device__ __forceinline__ void load_items(const hs_expanded& a, const Maps& m, 
   const bool leader = tc::elect();
   uint32_t u = 0, count = 0;
   Item it;
-  for (int64_t n = blockIdx.x; find_item(a, n, &it); n += gridDim.x) {
+  for (int k = 0; find_item(a, item_number(k), &it); ++k) {
     if (it.most() <= 0) continue;
     if (count > 0) w.wait(bars + 8 * kQEmpty, (count - 1) & 1);
     ++count;
@@ -175,7 +181,7 @@ __device__ __forceinline__ void issue_items(const hs_expanded& a, uint32_t q, ui
   uint32_t base = 0, count = 0;
   uint32_t phase[2] = {0, 0};  // key tiles done by each query tile
   Item it;
-  for (int64_t n = blockIdx.x; find_item(a, n, &it); n += gridDim.x) {
+  for (int k = 0; find_item(a, item_number(k), &it); ++k) {
     const int tiles = it.most();
     if (tiles <= 0) continue;
     const bool partial = it.keys - (tiles - 1) * kKeys < kKeys;
@@ -263,14 +269,14 @@ __device__ __forceinline__ void softmax_items(const hs_expanded& a, float scale_
   const float scale = fmaxf(fabsf(scale_log2), 1.17549435e-38f);
   uint32_t phase = 0;
   Item it;
-  for (int64_t n = blockIdx.x; find_item(a, n, &it); n += gridDim.x) {
+  for (int k = 0; find_item(a, item_number(k), &it); ++k) {
     const int tiles = it.tiles[t];
     if (tiles < 0) continue;
     const int row = t * kQRows + row_in_tile;
     const int sees = a.causal ? min(it.keys, row + it.shift) : it.keys;  // keys below this one are seen
     const int all_see = a.causal ? min(it.keys, t * kQRows + it.shift) : it.keys;  // by every row of the tile
     float m = -INFINITY;
-    float2 l2 = make_float2(0.f, 0.f);
+    float2 la = make_float2(0.f, 0.f), lb = la;  // the sum, in four chains
 #pragma unroll 1
     for (int j = 0; j < tiles; ++j, ++phase) {
       w.wait(bars + 8 * (kSFull + t), phase & 1);
@@ -291,16 +297,13 @@ __device__ __forceinline__ void softmax_items(const hs_expanded& a, float scale_
         for (int c = 0; c < 128; ++c)
           if (c >= left) s[c] = -INFINITY;
       }
-      float top = s[0];
-#pragma unroll
-      for (int c = 1; c < 128; ++c) top = fmaxf(top, s[c]);
-      top *= scale;
+      const float top = tc::max_of<128>(s) * scale;
       const bool over = top > m + kLazy;  // (m = -infinity: on the first key seen)
       if (__any_sync(0xFFFFFFFFu, over)) {
         const float now = over ? top : m;
         const float alpha = over ? (m == -INFINITY ? 0.f : exp2f(m - now)) : 1.f;
         m = now;
-        l2.x *= alpha, l2.y *= alpha;
+        la.x *= alpha, la.y *= alpha, lb.x *= alpha, lb.y *= alpha;
         if (j > 0) {  // the products so far have finished: this tile's scores were issued after them
 #pragma unroll 1
           for (int c = 0; c < 128; c += 16) {
@@ -323,7 +326,10 @@ __device__ __forceinline__ void softmax_items(const hs_expanded& a, float scale_
         for (int x = 0; x < 16; ++x) {
           const float2 y = tc::fma2(make_float2(s[c + 2 * x], s[c + 2 * x + 1]), sc2, base2);
           float2 e = make_float2(tc::exp2_fast(y.x), tc::exp2_fast(y.y));
-          l2 = tc::add2(l2, e);
+          if (x & 1)
+            lb = tc::add2(lb, e);
+          else
+            la = tc::add2(la, e);
           p[x] = tc::pack_bf16(e.x, e.y);
         }
         tc::tmem_st16(ts + c / 2, reinterpret_cast<const float*>(p));
@@ -334,7 +340,7 @@ __device__ __forceinline__ void softmax_items(const hs_expanded& a, float scale_
       if (lane == 0) tc::mbar_arrive(bars + 8 * (kPReady + t));
     }
     // results
-    const float l = l2.x + l2.y;
+    const float l = (la.x + la.y) + (lb.x + lb.y);
     const float inv = l == 0.f ? 0.f : 1.f / l;
     if (tiles > 0) {
       w.wait(bars + 8 * (kODone + t), (phase - 1) & 1);

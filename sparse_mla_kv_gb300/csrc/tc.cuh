@@ -195,6 +195,17 @@ __device__ __forceinline__ void commit(uint32_t bar, bool leader) {
       : "memory");
 }
 
+// Largest of n values, in four chains (NaN is passed over).
+template <int n>
+__device__ __forceinline__ float max_of(const float* v) {
+  float m[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+  for (int i = 4; i < n; i += 4) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m[k] = fmaxf(m[k], v[i + k]);
+  }
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
