@@ -32,7 +32,10 @@ constexpr int kSmemBytes = 6 * kUnit + kRing * kUnit + 512 + 1024;
 constexpr int kRegsLaunch = 168, kRegsSoftmax = 208, kRegsOther = 88;
 static_assert(2 * kRegsSoftmax + kRegsOther <= 3 * kRegsLaunch, "more registers than the launch has");
 constexpr float kLazy = 64.f;
-enum Bar { kFull = 0, kEmpty = kRing, kQFull = 2 * kRing, kQEmpty, kSFull, kPReady = kSFull + 2, kODone = kPReady + 2,
+// The units of a key tile's keys arrive on one barrier, those of its values on another; a ring of eight units holds parts
+// of at most four such groups.  Units are released one by one.
+constexpr int kGroups = 4;
+enum Bar { kFull = 0, kEmpty = kGroups, kQFull = kEmpty + kRing, kQEmpty, kSFull, kPReady = kSFull + 2, kODone = kPReady + 2,
            kDrain = kODone + 2, kBars };
 static_assert(kBars * 8 <= 512, "barriers");
 
@@ -116,7 +119,7 @@ __device__ __forceinline__ void load3(uint32_t dst, const CUtensorMap* map, int 
 __device__ __forceinline__ void load_items(const hs_expanded& a, const Maps& m, uint32_t q, uint32_t ring, uint32_t bars) {
   tc::Waiter w;
   const bool leader = tc::elect();
-  uint32_t u = 0, count = 0;
+  uint32_t u = 0, count = 0, group = 0;  // units, items, key tiles so far
   Item it;
   for (int k = 0; find_item(a, item_number(k), &it); ++k) {
     if (it.most() <= 0) continue;
@@ -137,7 +140,7 @@ __device__ __forceinline__ void load_items(const hs_expanded& a, const Maps& m, 
     }
     const int tiles = it.most();
 #pragma unroll 1
-    for (int j = 0; j < tiles; ++j) {
+    for (int j = 0; j < tiles; ++j, ++group) {
       const int row = it.k0 + j * kKeys;
 #pragma unroll 1
       for (int i = 0; i < kUnits; ++i, ++u) {
@@ -145,8 +148,9 @@ __device__ __forceinline__ void load_items(const hs_expanded& a, const Maps& m, 
         if (u >= kRing) w.wait(bars + 8 * (kEmpty + slot), (u / kRing - 1) & 1);
         __syncwarp();
         if (leader) {
-          const uint32_t bar = bars + 8 * (kFull + slot), to = ring + slot * kUnit;
-          tc::mbar_expect(bar, kUnit);
+          // (a group's barrier is free: its last use was four groups ago, and their units have been released since)
+          const uint32_t bar = bars + 8 * (kFull + (2 * group + (i >= kUnitsK)) % kGroups), to = ring + slot * kUnit;
+          if (i == 0 || i == kUnitsK) tc::mbar_expect(bar, (i == 0 ? kUnitsK : kUnitsV) * kUnit);
           if (i < 2)
             load3(to, &m.k_nope, 64 * i, hk, row, bar);
           else if (i == 2)
@@ -159,7 +163,8 @@ __device__ __forceinline__ void load_items(const hs_expanded& a, const Maps& m, 
   }
   // no copy is in flight when the CTA ends
   tc::Waiter drain;
-  for (uint32_t r = u > kRing ? u - kRing : 0; r < u; ++r) drain.wait(bars + 8 * (kFull + r % kRing), (r / kRing) & 1);
+  for (uint32_t r = 2 * group > kGroups ? 2 * group - kGroups : 0; r < 2 * group; ++r)
+    drain.wait(bars + 8 * (kFull + r % kGroups), (r / kGroups) & 1);
   if (count > 0) drain.wait(bars + 8 * kQFull, (count - 1) & 1);
   if (w.dead) report(a.status, HS_ERR_TIMEOUT);
 }
@@ -178,18 +183,24 @@ __device__ __forceinline__ void issue_items(const hs_expanded& a, uint32_t q, ui
     __syncwarp();
     tc::fence_after();
   };
-  uint32_t base = 0, count = 0;
+  uint32_t base = 0, count = 0, seen = 0;  // units, items and groups so far
   uint32_t phase[2] = {0, 0};  // key tiles done by each query tile
   Item it;
   for (int k = 0; find_item(a, item_number(k), &it); ++k) {
     const int tiles = it.most();
     if (tiles <= 0) continue;
     const bool partial = it.keys - (tiles - 1) * kKeys < kKeys;
+    auto group = [&](uint32_t g) {  // waits for group g (counted over all items), once
+      if (g < seen) return;
+      await(kFull + g % kGroups, (g / kGroups) & 1);
+      seen = g + 1;
+    };
+    const uint32_t first_group = base / kUnits * 2;
     auto scores = [&](int t, int j) {  // S of query tile t and key tile j
+      group(first_group + 2 * j);
 #pragma unroll 1
       for (int i = 0; i < kUnitsK; ++i) {
         const uint32_t x = base + j * kUnits + i;
-        await(kFull + x % kRing, (x / kRing) & 1);
         const uint64_t da = dq + (uint32_t)((t * 3 + i) * kUnit >> 4), db = dk + (uint32_t)((x % kRing) * kUnit >> 4);
 #pragma unroll
         for (int k = 0; k < 4; ++k) tc::mma_ss(tmem + t * 128, da + (k * 32 >> 4), db + (k * 32 >> 4), kIdS, i > 0 || k > 0, leader);
@@ -216,11 +227,11 @@ __device__ __forceinline__ void issue_items(const hs_expanded& a, uint32_t q, ui
       for (int t = 0; t < 2; ++t) {
         if (j >= it.tiles[t]) continue;
         await(kPReady + t, phase[t] & 1);
+        group(first_group + 2 * j + 1);
         const bool fix = partial && j == tiles - 1 && (t == 0 || it.tiles[0] <= j);  // by the first that reads them
 #pragma unroll 1
         for (int i = 0; i < kUnitsV; ++i) {
           const uint32_t x = base + j * kUnits + kUnitsK + i;
-          await(kFull + x % kRing, (x / kRing) & 1);
           if (fix) {
             const int valid = it.keys - j * kKeys;
             for (int k = threadIdx.x & 31; k < (kKeys - valid) * 8; k += 32) {
@@ -388,10 +399,8 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const hs_expanded
       if (!sequence(a, s, &q0, &q1, &k0, &k1)) report(a.status, HS_ERR_ID_RANGE);
     }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kRing; ++i) {
-      tc::mbar_init(bars + 8 * (kFull + i), 1);
-      tc::mbar_init(bars + 8 * (kEmpty + i), 1);
-    }
+    for (int i = 0; i < kGroups; ++i) tc::mbar_init(bars + 8 * (kFull + i), 1);
+    for (int i = 0; i < kRing; ++i) tc::mbar_init(bars + 8 * (kEmpty + i), 1);
     tc::mbar_init(bars + 8 * kQFull, 1);
     tc::mbar_init(bars + 8 * kQEmpty, 1);
     for (int t = 0; t < 2; ++t) {
