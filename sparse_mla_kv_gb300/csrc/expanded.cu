@@ -59,48 +59,64 @@ __device__ __forceinline__ bool sequence(const hs_expanded& a, int s, int* q0, i
   return *q0 >= 0 && *q1 >= *q0 && *q1 <= a.q_tokens && *k0 >= 0 && *k1 >= *k0 && *k1 <= a.k_tokens;
 }
 
-// Work item number n (a warp's lanes together); false when there are no more.  Items are numbered by sequence, then by
-// block of queries from the last (the longest) to the first, then by head.
-__device__ __forceinline__ bool find_item(const hs_expanded& a, int64_t n, Item* it) {
-  const int lane = threadIdx.x & 31;
-  const int64_t block = n / a.heads;
-  int64_t before = 0;
-  for (int s0 = 0; s0 < a.seqs; s0 += 32) {
-    const int s = s0 + lane;
+// Hands a warp the work items by number, in ascending order.  Items are numbered by level, from the highest: a sequence of
+// b blocks has one block (of each head) on each of the levels b - 1 .. 0, and with causal masks the block of a level is
+// the longer the higher the level, so that long items come first whatever the mix of sequences.
+struct Finder {
+  int level, on_level;  // the current level and the sequences on it
+  int64_t before;       // blocks on higher levels
+
+  static __device__ __forceinline__ int blocks_of(const hs_expanded& a, int s, int* q0, int* q1, int* k0, int* k1) {
+    return s < a.seqs && sequence(a, s, q0, q1, k0, k1) ? (*q1 - *q0 + kBlock - 1) / kBlock : 0;
+  }
+  __device__ __forceinline__ void start(const hs_expanded& a) {
+    int most = 0, q0, q1, k0, k1;
+    for (int s = threadIdx.x & 31; s < a.seqs; s += 32) most = max(most, blocks_of(a, s, &q0, &q1, &k0, &k1));
+    level = __reduce_max_sync(0xFFFFFFFFu, most);
+    on_level = 0;
+    before = 0;
+  }
+  // Item number n, not below the last one asked for; false when there is none.
+  __device__ __forceinline__ bool find(const hs_expanded& a, int64_t n, Item* it) {
+    const int lane = threadIdx.x & 31;
+    const int64_t block = n / a.heads;
     int q0 = 0, q1 = 0, k0 = 0, k1 = 0;
-    const bool ok = s < a.seqs && sequence(a, s, &q0, &q1, &k0, &k1);
-    const int blocks = ok ? (q1 - q0 + kBlock - 1) / kBlock : 0;
-    int64_t upto = blocks;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int64_t y = __shfl_up_sync(0xFFFFFFFFu, upto, d);
-      if (lane >= d) upto += y;
+    while (block >= before + on_level) {
+      before += on_level;
+      if (--level < 0) return false;
+      int c = 0;
+      for (int s = lane; s < a.seqs; s += 32) c += blocks_of(a, s, &q0, &q1, &k0, &k1) > level;
+      on_level = __reduce_add_sync(0xFFFFFFFFu, c);
     }
-    const unsigned has = __ballot_sync(0xFFFFFFFFu, block < before + upto);
-    if (has) {
-      const int who = __ffs(has) - 1;
-      const int from_end = (int)(before + __shfl_sync(0xFFFFFFFFu, upto, who) - 1 - block);
+    int skip = (int)(block - before);  // the sequence wanted: this many on the level come before it
+    for (int s0 = 0;; s0 += 32) {
+      const bool here = blocks_of(a, s0 + lane, &q0, &q1, &k0, &k1) > level;
+      const unsigned has = __ballot_sync(0xFFFFFFFFu, here);
+      if (skip >= __popc(has)) {
+        skip -= __popc(has);
+        continue;
+      }
+      const int who = __fns(has, 0, skip + 1);
       q0 = __shfl_sync(0xFFFFFFFFu, q0, who), q1 = __shfl_sync(0xFFFFFFFFu, q1, who);
       k0 = __shfl_sync(0xFFFFFFFFu, k0, who), k1 = __shfl_sync(0xFFFFFFFFu, k1, who);
-      const int first = from_end * kBlock;
-      it->head = (int)(n - block * a.heads);
-      it->q0 = q0 + first;
-      it->rows = min(kBlock, q1 - q0 - first);
-      it->k0 = k0;
-      it->keys = k1 - k0;
-      it->shift = a.causal ? first + 1 + (k1 - k0) - (q1 - q0) : 0;
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const int last = min(it->rows, (t + 1) * kQRows) - 1;  // the tile's last row sees most
-        const int sees = a.causal ? min(it->keys, last + it->shift) : it->keys;
-        it->tiles[t] = last < t * kQRows ? -1 : max(0, (sees + kKeys - 1) / kKeys);
-      }
-      return true;
+      break;
     }
-    before += __shfl_sync(0xFFFFFFFFu, upto, 31);
+    const int first = level * kBlock;
+    it->head = (int)(n - block * a.heads);
+    it->q0 = q0 + first;
+    it->rows = min(kBlock, q1 - q0 - first);
+    it->k0 = k0;
+    it->keys = k1 - k0;
+    it->shift = a.causal ? first + 1 + (k1 - k0) - (q1 - q0) : 0;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int last = min(it->rows, (t + 1) * kQRows) - 1;  // the tile's last row sees most
+      const int sees = a.causal ? min(it->keys, last + it->shift) : it->keys;
+      it->tiles[t] = last < t * kQRows ? -1 : max(0, (sees + kKeys - 1) / kKeys);
+    }
+    return true;
   }
-  return false;
-}
+};
 
 // This CTA's k-th item: passes over the grid in alternating directions, so that who had a long block first has a short one
 // of the next pass.
@@ -121,7 +137,9 @@ __device__ __forceinline__ void load_items(const hs_expanded& a, const Maps& m, 
   const bool leader = tc::elect();
   uint32_t u = 0, count = 0, group = 0;  // units, items, key tiles so far
   Item it;
-  for (int k = 0; find_item(a, item_number(k), &it); ++k) {
+  Finder f;
+  f.start(a);
+  for (int k = 0; f.find(a, item_number(k), &it); ++k) {
     if (it.most() <= 0) continue;
     if (count > 0) w.wait(bars + 8 * kQEmpty, (count - 1) & 1);
     ++count;
@@ -186,7 +204,9 @@ __device__ __forceinline__ void issue_items(const hs_expanded& a, uint32_t q, ui
   uint32_t base = 0, count = 0, seen = 0;  // units, items and groups so far
   uint32_t phase[2] = {0, 0};  // key tiles done by each query tile
   Item it;
-  for (int k = 0; find_item(a, item_number(k), &it); ++k) {
+  Finder f;
+  f.start(a);
+  for (int k = 0; f.find(a, item_number(k), &it); ++k) {
     const int tiles = it.most();
     if (tiles <= 0) continue;
     const bool partial = it.keys - (tiles - 1) * kKeys < kKeys;
@@ -280,7 +300,9 @@ __device__ __forceinline__ void softmax_items(const hs_expanded& a, float scale_
   const float scale = fmaxf(fabsf(scale_log2), 1.17549435e-38f);
   uint32_t phase = 0;
   Item it;
-  for (int k = 0; find_item(a, item_number(k), &it); ++k) {
+  Finder f;
+  f.start(a);
+  for (int k = 0; f.find(a, item_number(k), &it); ++k) {
     const int tiles = it.tiles[t];
     if (tiles < 0) continue;
     const int row = t * kQRows + row_in_tile;
