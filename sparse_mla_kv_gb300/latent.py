@@ -13,7 +13,7 @@ from typing import Optional
 
 import torch
 
-from . import Pool, _check, _dev_i32, _opt, _stream, lib
+from . import Pool, _check, _dev_i32, _opt, lib
 
 LATENT_DIM, ROPE_DIM, NOPE_DIM, VALUE_DIM = 512, 64, 128, 128
 ROW_BYTES_FP8, ROW_BYTES_BF16 = 656, 1152
@@ -65,21 +65,27 @@ def _lib():
     return _bound
 
 
-def _tensor(t: torch.Tensor, name: str, shape: tuple, dtype=torch.bfloat16) -> None:
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda:
-        raise TypeError(f"{name} must be a {dtype} CUDA tensor")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
-    if t.numel() and t.stride(-1) != 1:
+def _tensor(t: torch.Tensor, name: str, shape: tuple, dtype=torch.bfloat16) -> tuple:
+    """The strides of a CUDA tensor of this shape and type whose last dimension is contiguous."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda:
+        if not isinstance(t, torch.Tensor) or t.dtype is not dtype or not t.is_cuda:
+            raise TypeError(f"{name} must be a {dtype} CUDA tensor")
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    strides = t.stride()
+    if strides[-1] != 1 and t.numel():
         raise ValueError(f"{name}'s last dimension must be contiguous")
+    return strides
 
 
 def _f32(t: Optional[torch.Tensor], name: str, shape: tuple):
-    if t is None:
-        return None
-    if t.dtype != torch.float32 or not t.is_cuda or not t.is_contiguous() or tuple(t.shape) != shape:
-        raise TypeError(f"{name} must be a contiguous float32 CUDA tensor of shape {shape}")
+    if t.dtype is not torch.float32 or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous float32 CUDA tensor of shape {tuple(shape)}")
     return t.data_ptr()
+
+
+def _on(stream, t: torch.Tensor):
+    """The raw stream to launch on: the given one, or the current one of the tensor's device."""
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def append_rows(pool: Pool, rows: torch.Tensor, latent: torch.Tensor, rope: torch.Tensor, positions: torch.Tensor,
@@ -94,8 +100,9 @@ def append_rows(pool: Pool, rows: torch.Tensor, latent: torch.Tensor, rope: torc
     dt = _DTYPES.get(latent.dtype)
     if dt is None:
         raise TypeError("latent must be bf16, fp16 or fp32")
-    _tensor(latent, "latent", (n, LATENT_DIM), latent.dtype)
-    _tensor(rope, "rope", (n, ROPE_DIM), latent.dtype)
+    dtype = latent.dtype
+    latent_stride = _tensor(latent, "latent", (n, LATENT_DIM), dtype)[0]
+    rope_stride = _tensor(rope, "rope", (n, ROPE_DIM), dtype)[0]
     if positions.numel() != n:
         raise ValueError("positions must have one entry per row")
     if rotation.dim() != 2 or rotation.shape[1] != ROPE_DIM:
@@ -103,19 +110,18 @@ def append_rows(pool: Pool, rows: torch.Tensor, latent: torch.Tensor, rope: torc
     heads, q, qo = 0, (None, 0, 0), (None, 0, 0)
     if q_rope is not None:
         heads = int(q_rope.shape[1]) if q_rope.dim() == 3 else -1
-        _tensor(q_rope, "q_rope", (n, heads, ROPE_DIM), latent.dtype)
+        st = _tensor(q_rope, "q_rope", (n, heads, ROPE_DIM), dtype)
+        q = (q_rope.data_ptr(), st[0], st[1])
         if q_out is None:
-            q_out = torch.empty((n, heads, ROPE_DIM), dtype=latent.dtype, device=q_rope.device)
-        _tensor(q_out, "q_out", (n, heads, ROPE_DIM), latent.dtype)
-        q = (q_rope.data_ptr(), q_rope.stride(0), q_rope.stride(1))
-        qo = (q_out.data_ptr(), q_out.stride(0), q_out.stride(1))
+            q_out = torch.empty((n, heads, ROPE_DIM), dtype=dtype, device=q_rope.device)
+        st = _tensor(q_out, "q_out", (n, heads, ROPE_DIM), dtype)
+        qo = (q_out.data_ptr(), st[0], st[1])
     elif q_out is not None:
         raise ValueError("q_out without q_rope")
     a = AppendC(n, _dev_i32(rows, "rows"), _dev_i32(positions, "positions"),
-                _f32(rotation, "rotation", tuple(rotation.shape)), int(rotation.shape[0]), int(bool(interleaved)), dt,
-                heads, latent.data_ptr(), latent.stride(0), rope.data_ptr(), rope.stride(0), *q, *qo,
-                _opt(status, "status"))
-    _check(_lib().hs_append_rows(pool.handle, int(layer), ctypes.byref(a), _stream(stream)), "hs_append_rows")
+                _f32(rotation, "rotation", rotation.shape), rotation.shape[0], bool(interleaved), dt, heads,
+                latent.data_ptr(), latent_stride, rope.data_ptr(), rope_stride, *q, *qo, _opt(status, "status"))
+    _check(_lib().hs_append_rows(pool.handle, int(layer), ctypes.byref(a), _on(stream, latent)), "hs_append_rows")
     return q_out
 
 
@@ -132,27 +138,27 @@ def alloc_attend_workspace(device="cuda") -> torch.Tensor:
 
 def _attend(lead: tuple, q_latent, q_rope, scale, out, lse, status, workspace):
     """Marshals an absorbed call whose query tensors have the leading dimensions `lead` (tokens) and heads."""
-    heads = int(q_latent.shape[len(lead)]) if q_latent.dim() == len(lead) + 2 else -1
-    _tensor(q_latent, "q_latent", (*lead, heads, LATENT_DIM))
-    _tensor(q_rope, "q_rope", (*lead, heads, ROPE_DIM))
+    k = len(lead)
+    heads = q_latent.shape[k] if q_latent.dim() == k + 2 else -1
+    shape, device = (*lead, heads, LATENT_DIM), q_latent.device
+    sl = _tensor(q_latent, "q_latent", shape)
+    sr = _tensor(q_rope, "q_rope", (*lead, heads, ROPE_DIM))
     if out is None:
-        out = torch.empty((*lead, heads, LATENT_DIM), dtype=torch.bfloat16, device=q_latent.device)
-    _tensor(out, "out", (*lead, heads, LATENT_DIM))
+        out = torch.empty(shape, dtype=torch.bfloat16, device=device)
+    so = _tensor(out, "out", shape)
     if lse is None:
-        lse = torch.empty((*lead, heads), dtype=torch.float32, device=q_latent.device)
-    lse_p = _f32(lse, "lse", (*lead, heads))
+        lse = torch.empty((*lead, heads), dtype=torch.float32, device=device)
     if workspace is None:
-        workspace = alloc_attend_workspace(q_latent.device)
-    if workspace.dtype != torch.uint8 or not workspace.is_cuda or not workspace.is_contiguous():
+        workspace = alloc_attend_workspace(device)
+    if workspace.dtype is not torch.uint8 or not workspace.is_cuda or not workspace.is_contiguous():
         raise TypeError("workspace must be a contiguous uint8 CUDA tensor")
-
-    def strides(t, name):
-        if len(lead) == 2 and lead[0] > 1 and lead[1] > 1 and t.stride(0) != lead[1] * t.stride(1):
-            raise ValueError(f"{name}'s two leading dimensions must merge into one")
-        return (t.stride(len(lead) - 1) if len(lead) == 1 or lead[1] > 1 else t.stride(0)), t.stride(len(lead))
-
-    a = AttendC(heads, float(scale), q_latent.data_ptr(), *strides(q_latent, "q_latent"), q_rope.data_ptr(),
-                *strides(q_rope, "q_rope"), out.data_ptr(), *strides(out, "out"), lse_p, _opt(status, "status"))
+    token = (sl[0], sr[0], so[0])
+    if k == 2 and lead[1] > 1:  # [requests][positions]: the two must merge into one dimension of tokens
+        if lead[0] > 1 and (sl[0] != lead[1] * sl[1] or sr[0] != lead[1] * sr[1] or so[0] != lead[1] * so[1]):
+            raise ValueError("the two leading dimensions of q_latent, q_rope and out must merge into one")
+        token = (sl[1], sr[1], so[1])
+    a = AttendC(heads, scale, q_latent.data_ptr(), token[0], sl[k], q_rope.data_ptr(), token[1], sr[k], out.data_ptr(),
+                token[2], so[k], _f32(lse, "lse", (*lead, heads)), _opt(status, "status"))
     return a, out, lse, workspace
 
 
@@ -163,10 +169,10 @@ def attend_rows(pool: Pool, rows: torch.Tensor, q_latent: torch.Tensor, q_rope: 
     [n][heads][512], q_rope bf16 [n][heads][64] (rotated) -> (out bf16 [n][heads][512], lse fp32 [n][heads])."""
     if rows.dim() != 2:
         raise ValueError("rows must be [tokens][K]")
-    n, K = int(rows.shape[0]), int(rows.shape[1])
+    n, K = rows.shape
     a, out, lse, ws = _attend((n,), q_latent, q_rope, scale, out, lse, status, workspace)
     _check(_lib().hs_attend_rows(pool.handle, int(layer), _dev_i32(rows, "rows"), n, K, ctypes.byref(a),
-                                 ws.data_ptr(), ws.numel(), _stream(stream)), "hs_attend_rows")
+                                 ws.data_ptr(), ws.numel(), _on(stream, q_latent)), "hs_attend_rows")
     return out, lse
 
 
@@ -185,7 +191,7 @@ def attend_pages(pool: Pool, block_table: torch.Tensor, ctx_len: torch.Tensor, q
     a, out, lse, ws = _attend((R, P), q_latent, q_rope, scale, out, lse, status, workspace)
     _check(_lib().hs_attend_pages(pool.handle, int(layer), _dev_i32(block_table, "block_table"),
                                   _dev_i32(ctx_len, "ctx_len"), R, P, int(block_table.shape[1]), ctypes.byref(a),
-                                  ws.data_ptr(), ws.numel(), _stream(stream)), "hs_attend_pages")
+                                  ws.data_ptr(), ws.numel(), _on(stream, q_latent)), "hs_attend_pages")
     return out, lse
 
 
@@ -200,22 +206,21 @@ def attend_expanded(q_nope: torch.Tensor, q_rope: torch.Tensor, k_nope: torch.Te
     if q_nope.dim() != 3 or k_rope.dim() != 2:
         raise ValueError("q_nope must be [Tq][heads][128] and k_rope [Tk][64]")
     Tq, H, Tk = int(q_nope.shape[0]), int(q_nope.shape[1]), int(k_rope.shape[0])
-    _tensor(q_nope, "q_nope", (Tq, H, NOPE_DIM))
-    _tensor(q_rope, "q_rope", (Tq, H, ROPE_DIM))
-    _tensor(k_nope, "k_nope", (Tk, H, NOPE_DIM))
-    _tensor(k_rope, "k_rope", (Tk, ROPE_DIM))
-    _tensor(v, "v", (Tk, H, VALUE_DIM))
+    sqn = _tensor(q_nope, "q_nope", (Tq, H, NOPE_DIM))
+    sqr = _tensor(q_rope, "q_rope", (Tq, H, ROPE_DIM))
+    skn = _tensor(k_nope, "k_nope", (Tk, H, NOPE_DIM))
+    skr = _tensor(k_rope, "k_rope", (Tk, ROPE_DIM))
+    sv = _tensor(v, "v", (Tk, H, VALUE_DIM))
     if cu_q.numel() < 1 or cu_q.numel() != cu_k.numel():
         raise ValueError("cu_q and cu_k must both have one entry more than there are sequences")
     if out is None:
         out = torch.empty((Tq, H, VALUE_DIM), dtype=torch.bfloat16, device=q_nope.device)
-    _tensor(out, "out", (Tq, H, VALUE_DIM))
+    so = _tensor(out, "out", (Tq, H, VALUE_DIM))
     if lse is None:
         lse = torch.empty((Tq, H), dtype=torch.float32, device=q_nope.device)
-    a = ExpandedC(int(cu_q.numel()) - 1, H, int(bool(causal)), float(scale), Tq, Tk, _dev_i32(cu_q, "cu_q"),
-                  _dev_i32(cu_k, "cu_k"), q_nope.data_ptr(), q_nope.stride(0), q_nope.stride(1), q_rope.data_ptr(),
-                  q_rope.stride(0), q_rope.stride(1), k_nope.data_ptr(), k_nope.stride(0), k_nope.stride(1),
-                  k_rope.data_ptr(), k_rope.stride(0), v.data_ptr(), v.stride(0), v.stride(1), out.data_ptr(),
-                  out.stride(0), out.stride(1), _f32(lse, "lse", (Tq, H)), _opt(status, "status"))
-    _check(_lib().hs_attend_expanded(ctypes.byref(a), _stream(stream)), "hs_attend_expanded")
+    a = ExpandedC(cu_q.numel() - 1, H, bool(causal), scale, Tq, Tk, _dev_i32(cu_q, "cu_q"), _dev_i32(cu_k, "cu_k"),
+                  q_nope.data_ptr(), sqn[0], sqn[1], q_rope.data_ptr(), sqr[0], sqr[1], k_nope.data_ptr(), skn[0], skn[1],
+                  k_rope.data_ptr(), skr[0], v.data_ptr(), sv[0], sv[1], out.data_ptr(), so[0], so[1],
+                  _f32(lse, "lse", (Tq, H)), _opt(status, "status"))
+    _check(_lib().hs_attend_expanded(ctypes.byref(a), _on(stream, q_nope)), "hs_attend_expanded")
     return out, lse
