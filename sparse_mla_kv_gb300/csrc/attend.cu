@@ -41,9 +41,9 @@ namespace {
 
 constexpr int kTile = 64;
 constexpr int kProducerWarps = 16, kSoftmaxWarps = 8;
-constexpr int kMmaWarp = kProducerWarps + kSoftmaxWarps, kGatherWarp = kMmaWarp + 1;
+constexpr int kBufs = 2;  // tiles in shared memory
+constexpr int kMmaWarp = kProducerWarps + kSoftmaxWarps;
 constexpr int kThreads = (kMmaWarp + 4) * 32;
-constexpr int kAhead = 4;
 constexpr int kMaxCols = 64;
 constexpr int kRegsLaunch = 72, kRegsProducer = 64, kRegsSoftmax = 96, kRegsMma = 56;
 static_assert(kProducerWarps * kRegsProducer + kSoftmaxWarps * kRegsSoftmax + 4 * kRegsMma <=
@@ -53,7 +53,8 @@ template <int kRegs>
 __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs)); }
 template <int kRegs>
 __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs)); }
-constexpr int kSub = kTile * 128;  // bytes of a sub-tile: 64 keys x 64 values
+constexpr int kSub = kTile * 128;    // bytes of a sub-tile: 64 keys x 64 values
+constexpr int kTileBytes = 9 * kSub;  // of which the ninth holds the rotated parts, and later the weights
 // In log2 units: where a new reference puts the largest score, and the most that a score may reach before it moves.
 // fp16 weights are normal from 2^-14 to 2^16; bf16 weights have fp32's range.
 template <bool kF16>
@@ -105,80 +106,60 @@ struct Cursor {
   }
 };
 
-// Row of key `k` of an item, or -1; bad (a data error) is set when the entry is not a valid one.
-__device__ __forceinline__ int key_row(const AttendParams& p, int item, int k, int keys, bool& bad) {
-  if (k >= keys) return -1;
-  if (!p.paged) {
-    const int r = __ldg(p.rows + (int64_t)item * p.K + k);
-    if (r >= 0 && r < p.num_rows) return r;
-    bad |= r != -1;
-    return -1;
+// What a list or a page table says of a key: loaded ahead of its use, so nothing here looks at the loaded value.
+struct Entry {
+  int value, in_page;
+  bool there, counts;
+  __device__ __forceinline__ void load(const AttendParams& p, const Cursor& cur, int key) {
+    const int k = cur.tile * kTile + key;
+    there = cur.left > 0 && k < cur.keys;
+    counts = cur.group == 0;
+    value = -1;
+    in_page = 0;
+    if (!there) return;
+    if (p.paged) {
+      const int page = k / p.page_size;
+      in_page = k - page * p.page_size;
+      value = __ldg(p.table + (int64_t)cur.item * p.max_pages + page);
+    } else {
+      value = __ldg(p.rows + (int64_t)cur.item * p.K + k);
+    }
   }
-  const int page = k / p.page_size;
-  const int b = __ldg(p.table + (int64_t)item * p.max_pages + page);
-  if (b >= 0 && b < p.num_blocks) return b * p.page_size + (k - page * p.page_size);
-  bad = true;
-  return -1;
-}
-
-// Raw rows: a gather of four fp8 rows takes 4 x 656 B, padded to the copy engine's 128-byte boundaries; four bf16
-// rows come in two halves of 4 x 576 B (a box is at most 256 elements wide).
-template <bool kF16>
-struct Raw {
-  static constexpr int kRow = kF16 ? HS_ROW_BYTES_FP8 : HS_ROW_BYTES_BF16;
-  static constexpr int kBox = kF16 ? kRow : kRow / 2;  // bytes of a row that one gather brings
-  static constexpr int kFour = kF16 ? 2688 : 4 * kRow;
-  static constexpr int kSlot = 4 * kFour;              // 16 rows
-  static constexpr int kTx = 16 * kRow;
+  // The key's row, or -1; bad (a data error) is set when the entry is not a valid one.
+  __device__ __forceinline__ int row(const AttendParams& p, bool& bad) const {
+    const bool in = value >= 0 && value < (p.paged ? (int64_t)p.num_blocks : p.num_rows);
+    bad |= there && counts && !in && (p.paged || value != -1);
+    return !in ? -1 : p.paged ? value * p.page_size + in_page : value;
+  }
 };
 
-template <int N, bool kF16>
+template <int N>
 struct Smem {
-  static constexpr int kQ = 9 * kSub;
-  static constexpr bool kAlias = !kF16 && N == 64;  // no room for P: it takes the rotated part's place
-  static constexpr int kRopeHalf = kAlias ? 1 : 0;
-  static constexpr int kP = kAlias ? 8 * kSub : kQ + 9 * N * 128;
-  static constexpr int kRaw = kQ + 9 * N * 128 + (kAlias ? 0 : kTile * N * 2);
-  // after the ring: barriers (384 B), row ids [kAhead][64], results' offsets [N] (64 bits), then floats: references,
-  // factors, limits, scalars [N] each, joined values [4][N], query scales [2][N], key scales [64]
-  static constexpr int kMiscBytes = 384 + kAhead * kTile * 4 + N * 8 + (10 * N + kTile) * 4;
-  static constexpr int kFit = (232448 - 1024 - kMiscBytes - kRaw) / Raw<kF16>::kSlot;
-  static constexpr int kSlots = kFit < 8 ? kFit : 8;
-  static constexpr int kMisc = kRaw + kSlots * Raw<kF16>::kSlot;
-  static constexpr int kIds = kMisc + 384;
-  static constexpr int kOffsets = kIds + kAhead * kTile * 4;
+  static constexpr int kQ = kBufs * kTileBytes;
+  static constexpr int kMisc = kQ + 9 * N * 128;
+  // after the queries: barriers (128 B), scales of fp8 rows [tile][key][4], results' offsets [N] (64 bits), then floats:
+  // references, factors, limits, scalars [N] each, joined values [4][N], query scales [3][N], key scales [tile][64]
+  static constexpr int kScales = kMisc + 128;
+  static constexpr int kOffsets = kScales + kBufs * kTile * 16;
   static constexpr int kRef = kOffsets + N * 8;
-  static constexpr int kQScale = 8 * N, kKeyScale = 10 * N;
-  static constexpr int kBytes = kMisc + kMiscBytes + 1024;  // + alignment of the base
-  // a tile's four slots fit: so they can all be on their way before its row ids are published, and who has seen the
-  // ids knows that the slots' earlier uses are over, which the parity of a barrier alone cannot tell
-  static_assert(kSlots >= 4, "ring");
+  static constexpr int kQScale = 8 * N, kKeyScale = 11 * N;
+  static constexpr int kBytes = kRef + (11 * N + kBufs * kTile) * 4 + 1024;  // + alignment of the base
+  static_assert(kBytes <= 232448, "shared memory");
 };
-enum Bar { kFull = 0, kEmpty = 2, kQFull = 4, kQEmpty, kSFull, kPReady, kOFull, kDrain, kRawFull = 16, kRawEmpty = 24,
-           kIdFull = 32, kIdEmpty = kIdFull + kAhead, kBars = kIdEmpty + kAhead };
-static_assert(kBars * 8 <= 384, "barriers");
+enum Bar { kFull = 0, kEmpty = 2, kQFull = 4, kQEmpty = 5, kSFull = 6, kPReady = 8, kOFull = 10, kDrain, kBars };
+static_assert(kBars * 8 <= 128, "barriers");
 
 template <int N>
 constexpr int tmem_cols() { return N == 64 ? 512 : N == 32 ? 256 : 128; }
 
-// Reduction of n values over the warp's 32 lanes by halving: lane l ends with the result of column l * n / 32.
-template <int n, typename F>
-__device__ __forceinline__ void halve(float* v, int lane, F f) {
-#pragma unroll
-  for (int half = n / 2, d = 16; d; half >>= 1, d >>= 1) {
-    if (half == 0) {  // the lanes of a column
-      v[0] = f(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], d));
-    } else {
-#pragma unroll
-      for (int i = 0; i < half; ++i) {
-        const bool up = lane & d;
-        const float send = up ? v[i] : v[i + half], keep = up ? v[i + half] : v[i];
-        v[i] = f(keep, __shfl_xor_sync(0xFFFFFFFFu, send, d));
-      }
-    }
-  }
+__device__ __forceinline__ uint2 lds8(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
 }
-
+__device__ __forceinline__ void sts4(uint32_t a, uint32_t x) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(x) : "memory");
+}
 __device__ __forceinline__ uint4 lds16(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
@@ -243,8 +224,7 @@ __device__ __forceinline__ bool any_softmax(bool x) {
 // ---------------------------------------------------------------------------------------------------------
 // Producers
 
-// Query tile of a unit: N columns x 576, zero for columns past the item's; asynchronous copies (one group), which the
-// caller waits for.
+// Query tile of a unit: N columns x 576, zero for columns past the item's; asynchronous copies, which the caller waits for.
 template <int N>
 __device__ __forceinline__ void copy_queries(const AttendParams& p, uint32_t q, int item, int group) {
   constexpr int kPer = kProducerWarps * 32 / N;  // threads of a column
@@ -259,7 +239,6 @@ __device__ __forceinline__ void copy_queries(const AttendParams& p, uint32_t q, 
   for (int j = j0; j < 72; j += kPer)
     copy16(q + (j >> 3) * (N * 128) + col * 128 + (((j & 7) ^ (col & 7)) << 4), j < 64 ? lat + 8 * j : rope + 8 * (j - 64),
            there);
-  asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
 // The same in fp16 by plain loads: a column is divided by qs, a power of two (mostly 1) that brings it into
@@ -293,87 +272,77 @@ __device__ __forceinline__ void convert_queries(const AttendParams& p, uint32_t 
   }
 }
 
+// A warp owns four keys of every tile: it copies their rows, and widens fp8 codes in place (a part's codes land in the
+// upper half of its place), with no other warp to wait for.
 template <int N, bool kF16>
-__device__ __forceinline__ void produce_tiles(const AttendParams& p, uint32_t base, const int* ids, float* qs, float* skey,
-                                              uint32_t bars, Cursor cur, int groups, tc::Waiter& w) {
-  using L = Smem<N, kF16>;
-  using R = Raw<kF16>;
-  constexpr int kPieces = kF16 ? 1 : 2;  // 16-byte pieces of a part that a lane handles
+__device__ __forceinline__ void produce_tiles(const AttendParams& p, uint32_t base, float* qs, float* skey, uint32_t bars,
+                                              Cursor cur, int groups, tc::Waiter& w) {
+  using L = Smem<N>;
+  constexpr int kRow = kF16 ? HS_ROW_BYTES_FP8 : HS_ROW_BYTES_BF16;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int sub = lane >> 3, j = lane & 7;
-  const int key = warp * 4 + sub;  // this lane's key; of each 128 bytes of its row, the 16-byte piece j
-  const int swz = key & 7;
-  // lanes of the upper sub-tile store the halves of their 16 values in the other order, so that no two lanes of a store
-  // share a bank
-  const bool flip = kF16 && (j >> 2);
-  uint32_t at[2];
-  if (kF16) {
-    at[0] = base + (j >> 2) * kSub + key * 128 + ((((j & 3) * 2 + flip) ^ swz) << 4);
-    at[1] = base + (j >> 2) * kSub + key * 128 + ((((j & 3) * 2 + !flip) ^ swz) << 4);
-  } else {
-    at[0] = base + key * 128 + ((j ^ swz) << 4);
-    at[1] = at[0] + kSub;
+  const int sub = lane >> 3, j = lane & 7;  // copies: key 4 warp + sub, of each 128 bytes of its row the 16-byte piece j
+  const int key = 4 * warp + sub, swz = key & 7;
+  const int half = lane >> 4, q = lane & 15;  // widening: keys 4 warp + half and + 2, of each 128 codes the 8 at 8 q
+  uint32_t to[2];  // where their 8 values go
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int k = 4 * warp + 2 * i + half;
+    to[i] = (q >> 3) * kSub + k * 128 + (((q & 7) ^ (k & 7)) << 4);
   }
   auto signal = [&](int bar) {
     tc::fence_async_smem();
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(bars + 8 * bar);
   };
-  bool fresh = true;
-  uint32_t it = 0, seg = 0;
-  uint32_t ring = warp >> 2;  // this warp's rows: slot ring % kSlots, its use number ring / kSlots
+  bool fresh = true, bad = false;
+  uint32_t seg = 0, it = 0;
+  Entry entry;  // of key 4 warp + lane % 4
+  entry.load(p, cur, 4 * warp + (lane & 3));
 #pragma unroll 1
   while (cur.left > 0) {
+    const uint32_t buf = it % kBufs, tile = base + buf * kTileBytes;
+    const uint32_t scales = base + L::kScales + (buf * kTile + key) * 16;
+    const int row = __shfl_sync(0xFFFFFFFFu, entry.row(p, bad), sub);
+    const bool there = row >= 0;
+    const uint8_t* src = p.base + (int64_t)max(row, 0) * kRow + 16 * j;
+    if (it >= kBufs) w.wait(bars + 8 * (kEmpty + buf), (it / kBufs - 1) & 1);
+    __syncwarp();
+    // the rows, on their way into the tile: zeros for keys that have none
+    if (kF16) {
+      if (j == 0) copy16(scales, src + kLatent, there);
+      copy16(tile + 8 * kSub + key * 128 + 16 * j, src + kRow - 128, there);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) copy16(tile + (2 * c + 1) * kSub + key * 128 + 16 * j, src + 128 * c, there);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 9; ++c) copy16(tile + c * kSub + key * 128 + ((j ^ swz) << 4), src + 128 * c, there);
+      if (j == 0) skey[buf * kTile + key] = there ? 1.f : 0.f;
+    }
     if (fresh) {
       if (seg > 0) w.wait(bars + 8 * kQEmpty, (seg - 1) & 1);
+      __syncwarp();
       if (kF16) {
-        convert_queries<N>(p, base + L::kQ, qs + (seg & 1) * N, cur.item, cur.group);
+        convert_queries<N>(p, base + L::kQ, qs + (seg % 3) * N, cur.item, cur.group);
       } else {
         copy_queries<N>(p, base + L::kQ, cur.item, cur.group);
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        asm volatile("cp.async.wait_all;" ::: "memory");
       }
       signal(kQFull);
       ++seg;
     }
-    // the rows, from the ring
-    const int slot = it % kAhead;
-    w.wait(bars + 8 * (kIdFull + slot), (it / kAhead) & 1);
-    const bool there = ids[slot * kTile + key] >= 0;
-    const uint32_t from = ring % L::kSlots;
-    w.wait(bars + 8 * (kRawFull + from), (ring / L::kSlots) & 1);
+    fresh = cur.next(p, groups);
+    ++it;
+    entry.load(p, cur, 4 * warp + (lane & 3));
+    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();
-    uint4 v[4][2], rope;
-    float sc = 0.f;
-    {
-      const uint32_t raw = base + L::kRaw + from * R::kSlot + (warp & 3) * R::kFour;
-      auto piece = [&](int off) {  // 16 bytes of the lane's row from byte `off`
-        if (kF16) return lds16(raw + sub * R::kRow + off);
-        return lds16(raw + sub * R::kBox + off + (off >= R::kBox ? 3 * R::kBox : 0));
-      };
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        v[c][0] = piece(128 * kPieces * c + 16 * j);
-        if (kPieces == 2) v[c][1] = piece(256 * c + 128 + 16 * j);
-      }
-      rope = piece(R::kRow - 128 + 16 * j);
-      if (kF16) sc = lds_f(raw + sub * R::kRow + kLatent + 4 * (j & 3));
-    }
-    tc::fence_async_smem();  // the copy engine's next write to the slot comes after these reads
-    __syncwarp();
-    if (lane == 0) {
-      tc::mbar_arrive(bars + 8 * (kRawEmpty + from));
-      tc::mbar_arrive(bars + 8 * (kIdEmpty + slot));
-    }
-    ring += 4;
-    if (!there) {  // (row 0 was read in its place)
-      sc = 0.f;
-      rope = make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) v[c][0] = v[c][1] = make_uint4(0, 0, 0, 0);
-    }
-    __syncwarp();
-    float inv = 1.f;
     if constexpr (kF16) {
+      const uint4 rope = lds16(tile + 8 * kSub + key * 128 + 16 * j);
+      const float sc = lds_f(scales + 4 * (j & 3));  // lanes j and j + 4 of a key have its scale of group j
+      uint2 v[4][2];
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) v[c][i] = lds8(tile + (2 * c + 1) * kSub + (4 * warp + 2 * i + half) * 128 + 8 * q);
       // skey: 2^7 below the power of two that covers the largest scale (codes reach 448 * 2^7 < 65504), and so that the
       // rotated part stays below 2^15
       const uint32_t sb = __float_as_uint(sc) & 0x7FFFFFFFu;
@@ -383,167 +352,131 @@ __device__ __forceinline__ void produce_tiles(const AttendParams& p, uint32_t ba
 #pragma unroll
       for (int d = 1; d < 8; d <<= 1) e = max(e, __shfl_xor_sync(0xFFFFFFFFu, e, d));
       e = min(max(e, 1), 240);
-      inv = __uint_as_float((uint32_t)(254 - e) << 23);
+      const float inv = __uint_as_float((uint32_t)(254 - e) << 23);
       const uint32_t ratio = pack_half(sc * inv, sc * inv);
+      if (j == 0) skey[buf * kTile + key] = there ? __uint_as_float((uint32_t)e << 23) : 0.f;
+      __syncwarp();  // the codes and the rotated parts are read before their places are written
+      sts(tile + 8 * kSub + key * 128 + ((j ^ swz) << 4), bf16_to_half(rope.x, inv), bf16_to_half(rope.y, inv),
+          bf16_to_half(rope.z, inv), bf16_to_half(rope.w, inv));
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const uint4 u = v[c][0];
-        const int src = (lane & 24) | c;  // lanes c and c + 4 of a key have its scale of group c
-        uint2 a = codes4(flip ? u.z : u.x), b = codes4(flip ? u.w : u.y);
-        uint2 d = codes4(flip ? u.x : u.z), f = codes4(flip ? u.y : u.w);
-        if (exact) {
-          const uint32_t r = __shfl_sync(0xFFFFFFFFu, ratio, src);
-          a.x = mul_half2(a.x, r), a.y = mul_half2(a.y, r), b.x = mul_half2(b.x, r), b.y = mul_half2(b.y, r);
-          d.x = mul_half2(d.x, r), d.y = mul_half2(d.y, r), f.x = mul_half2(f.x, r), f.y = mul_half2(f.y, r);
-        } else {
-          const float z = __shfl_sync(0xFFFFFFFFu, sc, src);
-          a.x = scaled_half(a.x, z, inv), a.y = scaled_half(a.y, z, inv);
-          b.x = scaled_half(b.x, z, inv), b.y = scaled_half(b.y, z, inv);
-          d.x = scaled_half(d.x, z, inv), d.y = scaled_half(d.y, z, inv);
-          f.x = scaled_half(f.x, z, inv), f.y = scaled_half(f.y, z, inv);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int from = (2 * i + half) * 8 + c;
+          uint2 a = codes4(v[c][i].x), b = codes4(v[c][i].y);
+          if (exact) {
+            const uint32_t r = __shfl_sync(0xFFFFFFFFu, ratio, from);
+            a.x = mul_half2(a.x, r), a.y = mul_half2(a.y, r), b.x = mul_half2(b.x, r), b.y = mul_half2(b.y, r);
+          } else {
+            const float z = __shfl_sync(0xFFFFFFFFu, sc, from), f = __shfl_sync(0xFFFFFFFFu, inv, from);
+            a.x = scaled_half(a.x, z, f), a.y = scaled_half(a.y, z, f);
+            b.x = scaled_half(b.x, z, f), b.y = scaled_half(b.y, z, f);
+          }
+          sts(tile + 2 * c * kSub + to[i], a.x, a.y, b.x, b.y);
         }
-        v[c][0] = make_uint4(a.x, a.y, b.x, b.y);
-        v[c][1] = make_uint4(d.x, d.y, f.x, f.y);
       }
-      rope = make_uint4(bf16_to_half(rope.x, inv), bf16_to_half(rope.y, inv), bf16_to_half(rope.z, inv), bf16_to_half(rope.w, inv));
     }
-    // the operands, half by half as their places become free
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (it > 0) w.wait(bars + 8 * (kEmpty + h), (it - 1) & 1);
-      if (kF16 && h == 0 && j == 0) skey[key] = 1.f / inv;  // (the softmax of the tile before has read its own)
-      if (h == L::kRopeHalf) sts(base + 8 * kSub + key * 128 + ((j ^ swz) << 4), rope.x, rope.y, rope.z, rope.w);
-#pragma unroll
-      for (int c = 2 * h; c < 2 * h + 2; ++c)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) sts(at[x] + 2 * c * kSub, v[c][x].x, v[c][x].y, v[c][x].z, v[c][x].w);
-      signal(kFull + h);
-    }
-    fresh = cur.next(p, groups);
-    ++it;
+    signal(kFull + buf);
   }
-}
-
-// Row ids of the tiles to come, and their rows on the way to the ring (one warp; lane l < 16: keys 4 l .. 4 l + 3).  Keys
-// without a row read row 0, which the producers replace by zeros.
-template <int N, bool kF16>
-__device__ __forceinline__ void gather_rows(const AttendParams& p, const CUtensorMap* map, uint32_t base, int* ids,
-                                            uint32_t bars, Cursor cur, int groups, tc::Waiter& w) {
-  using L = Smem<N, kF16>;
-  using R = Raw<kF16>;
-  const int lane = threadIdx.x & 31;
-  uint32_t it = 0, ring = 0;
-  bool any_bad = false, bad = false;
-  int4 id, next;
-  auto resolve = [&]() {
-    int r[4] = {-1, -1, -1, -1};
-    bad = false;
-    if (lane < 16 && cur.left > 0) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) r[i] = key_row(p, cur.item, cur.tile * kTile + 4 * lane + i, cur.keys, bad);
-    }
-    any_bad |= bad && cur.group == 0;
-    next = make_int4(r[0], r[1], r[2], r[3]);
-  };
-  resolve();
-#pragma unroll 1
-  while (cur.left > 0) {
-    id = next;
-    const int slot = it % kAhead;
-    if (it >= kAhead) w.wait(bars + 8 * (kIdEmpty + slot), (it / kAhead - 1) & 1);
-    __syncwarp();
-    if (lane < 16) *reinterpret_cast<int4*>(ids + slot * kTile + 4 * lane) = id;
-    cur.next(p, groups);
-    ++it;
-    resolve();  // the next tile's ids are on their way while this one's rows are gathered
-    id.x = max(id.x, 0), id.y = max(id.y, 0), id.z = max(id.z, 0), id.w = max(id.w, 0);
-#pragma unroll 1
-    for (int s = 0; s < 4; ++s, ++ring) {
-      const uint32_t to = ring % L::kSlots;
-      if (ring >= L::kSlots) w.wait(bars + 8 * (kRawEmpty + to), (ring / L::kSlots - 1) & 1);
-      const uint32_t full = bars + 8 * (kRawFull + to);
-      if (lane == 0) tc::mbar_expect(full, R::kTx);
-      __syncwarp();
-      if (lane >> 2 == s) {
-        const uint32_t dst = base + L::kRaw + to * R::kSlot + (lane & 3) * R::kFour;
-        tc::gather4(dst, map, 0, id, full);
-        if (!kF16) tc::gather4(dst + 4 * R::kBox, map, R::kBox / 4, id, full);
-      }
-      __syncwarp();
-    }
-    if (lane == 0) tc::mbar_arrive(bars + 8 * (kIdFull + slot));
-  }
-  // no copy is in flight when the CTA ends
-  tc::Waiter drain;
-  for (uint32_t r = ring > L::kSlots ? ring - L::kSlots : 0; r < ring; ++r)
-    drain.wait(bars + 8 * (kRawFull + r % L::kSlots), (r / L::kSlots) & 1);
-  if (any_bad) report(p.status, p.paged ? HS_ERR_TABLE_RANGE : HS_ERR_ID_RANGE);
+  if (bad) report(p.status, p.paged ? HS_ERR_TABLE_RANGE : HS_ERR_ID_RANGE);
 }
 
 // ---------------------------------------------------------------------------------------------------------
 // Products (one warp)
 
+// Scores of a tile as soon as it is there, results as soon as the weights are: a tile's scores are made while the
+// softmax works on the tile before.
 template <int N, bool kF16>
-__device__ __forceinline__ void issue_products(const AttendParams& p, uint32_t tile, uint32_t q, uint32_t pt, uint32_t bars,
-                                               uint32_t tmem, Cursor cur, int groups, tc::Waiter& w) {
-  using L = Smem<N, kF16>;
+__device__ __forceinline__ void issue_products(const AttendParams& p, uint32_t base, uint32_t bars, uint32_t tmem, Cursor cur,
+                                               int groups, tc::Waiter& w) {
   constexpr uint32_t kIdS = tc::idesc(kF16, kTile, N, false, false);
   constexpr uint32_t kIdO = tc::idesc(kF16, 128, N, true, true);
   constexpr uint64_t kPSwizzle = N == 64 ? tc::kSwizzle128 : N == 32 ? tc::kSwizzle64 : tc::kSwizzle32;
-  const uint64_t dk = tc::desc(tile, 16, 1024, tc::kSwizzle128);    // tile as keys (K-major)
-  const uint64_t dv = tc::desc(tile, kSub, 1024, tc::kSwizzle128);  // tile as values (M-major)
-  const uint64_t dq = tc::desc(q, 16, 1024, tc::kSwizzle128);
-  const uint64_t dp = tc::desc(pt, 16, 8 * N * 2, kPSwizzle);
+  const uint64_t dk = tc::desc(base, 16, 1024, tc::kSwizzle128);    // tile as keys (K-major)
+  const uint64_t dv = tc::desc(base, kSub, 1024, tc::kSwizzle128);  // tile as values (M-major)
+  const uint64_t dq = tc::desc(base + Smem<N>::kQ, 16, 1024, tc::kSwizzle128);
+  const uint64_t dp = tc::desc(base + 8 * kSub, 16, 8 * N * 2, kPSwizzle);
   const bool leader = tc::elect();
-  auto await = [&](int bar, uint32_t parity) {
-    w.wait(bars + 8 * bar, parity);
-    __syncwarp();
-    tc::fence_after();
-  };
+  const uint32_t total = cur.left;
+  uint32_t issued = 0, done = 0, seg = 0;  // tiles whose scores / results have been issued, units
+  uint32_t firsts = 0, lasts = 0;          // bit b: whether the tile in buffer b begins or ends a unit
   bool fresh = true;
-  uint32_t it = 0, seg = 0;
 #pragma unroll 1
-  while (cur.left > 0) {
-    if (fresh) await(kQFull, seg & 1);
-    const bool first = fresh;
-    bool accumulate = false;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      await(kFull + h, it & 1);
-      if (h == L::kRopeHalf) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          tc::mma_ss(tmem, dk + ((8 * kSub + k * 32) >> 4), dq + ((8 * N * 128 + k * 32) >> 4), kIdS, accumulate || k > 0, leader);
-        accumulate = true;
+  while (done < total && !w.dead) {
+    const bool more = issued < total && issued < done + kBufs;  // scores could be issued
+    const uint32_t sb = issued % kBufs, ob = done % kBufs;
+    const uint32_t full = bars + 8 * (kFull + sb), full_phase = issued / kBufs & 1;
+    const uint32_t ready = bars + 8 * (kPReady + ob), ready_phase = done / kBufs & 1;
+    bool results;
+    if (!more) {
+      w.wait(ready, ready_phase);
+      results = true;
+    } else if (done == issued) {
+      w.wait(full, full_phase);
+      results = false;
+    } else {
+      const long long t0 = clock64();
+      while (true) {
+        if (__all_sync(0xFFFFFFFFu, tc::mbar_test(ready, ready_phase))) {
+          results = true;
+          break;
+        }
+        if (__all_sync(0xFFFFFFFFu, tc::mbar_test(full, full_phase))) {
+          results = false;
+          break;
+        }
+        if (__any_sync(0xFFFFFFFFu, clock64() - t0 > tc::kWaitCycles)) {
+          w.dead = true;
+          break;
+        }
       }
+    }
+    __syncwarp();
+    if (__any_sync(0xFFFFFFFFu, w.dead)) {
+      w.dead = true;
+      break;
+    }
+    tc::fence_after();
+    if (results) {
+      const bool first = firsts >> ob & 1, last = lasts >> ob & 1;
+      const uint64_t a0 = dv + (uint32_t)(ob * kTileBytes >> 4), b = dp + (uint32_t)(ob * kTileBytes >> 4);
 #pragma unroll 1
-      for (int c = 2 * h; c < 2 * h + 2; ++c) {
-        const uint64_t a = dk + (uint32_t)(2 * c * kSub >> 4), b = dq + (uint32_t)(2 * c * (N * 128) >> 4);
+      for (int g = 0; g < 4; ++g) {
+        const uint64_t a = a0 + (uint32_t)(2 * g * kSub >> 4);
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)
+          tc::mma_ss(tmem + (2 + g) * N, a + (k * 2048 >> 4), b + ((k * 16 * N * 2) >> 4), kIdO, !first || k > 0, leader);
+      }
+      tc::commit(bars + 8 * (kEmpty + ob), leader);
+      if (last) tc::commit(bars + 8 * kOFull, leader);
+      ++done;
+    } else {
+      if (fresh) {
+        w.wait(bars + 8 * kQFull, seg++ & 1);
+        __syncwarp();
+        tc::fence_after();
+      }
+      const uint64_t a0 = dk + (uint32_t)(sb * kTileBytes >> 4);
+      const uint32_t d = tmem + sb * N;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        tc::mma_ss(d, a0 + ((8 * kSub + k * 32) >> 4), dq + ((8 * N * 128 + k * 32) >> 4), kIdS, k > 0, leader);
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        const uint64_t a = a0 + (uint32_t)(2 * c * kSub >> 4), b = dq + (uint32_t)(2 * c * (N * 128) >> 4);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          tc::mma_ss(tmem, a + (((k >> 2) * kSub + (k & 3) * 32) >> 4), b + (((k >> 2) * (N * 128) + (k & 3) * 32) >> 4), kIdS,
-                     accumulate || k > 0, leader);
-        accumulate = true;
+          tc::mma_ss(d, a + (((k >> 2) * kSub + (k & 3) * 32) >> 4), b + (((k >> 2) * (N * 128) + (k & 3) * 32) >> 4), kIdS, true,
+                     leader);
       }
+      tc::commit(bars + 8 * (kSFull + sb), leader);
+      firsts = (firsts & ~(1u << sb)) | (uint32_t)fresh << sb;
+      fresh = cur.next(p, groups);
+      ++issued;
+      const bool last = fresh || cur.left == 0;
+      lasts = (lasts & ~(1u << sb)) | (uint32_t)last << sb;
+      if (last) tc::commit(bars + 8 * kQEmpty, leader);
     }
-    tc::commit(bars + 8 * kSFull, leader);
-    fresh = cur.next(p, groups);
-    const bool last = fresh || cur.left == 0;
-    if (last) tc::commit(bars + 8 * kQEmpty, leader);
-    await(kPReady, it & 1);
-#pragma unroll 1
-    for (int g = 0; g < 4; ++g) {
-      const uint64_t a = dv + (uint32_t)(2 * g * kSub >> 4);
-#pragma unroll
-      for (int k = 0; k < kTile / 16; ++k)
-        tc::mma_ss(tmem + N + g * N, a + (k * 2048 >> 4), dp + ((k * 16 * N * 2) >> 4), kIdO, !first || k > 0, leader);
-      if (g & 1) tc::commit(bars + 8 * (kEmpty + g / 2), leader);
-    }
-    if (last) {
-      tc::commit(bars + 8 * kOFull, leader);
-      ++seg;
-    }
-    ++it;
   }
   // nothing of this CTA's products is in flight when the others leave
   tc::commit(bars + 8 * kDrain, leader);
@@ -555,34 +488,51 @@ __device__ __forceinline__ void issue_products(const AttendParams& p, uint32_t t
 // ---------------------------------------------------------------------------------------------------------
 // Softmax and results
 
+// Reduction over the eight lanes that have the same columns (lane % 4), of n values each.
+template <int n, typename F>
+__device__ __forceinline__ void over_keys(float* v, F f) {
+#pragma unroll
+  for (int d = 4; d < 32; d <<= 1)
+#pragma unroll
+    for (int i = 0; i < n; ++i) v[i] = f(v[i], __shfl_xor_sync(0xFFFFFFFFu, v[i], d));
+}
+
 template <int N, bool kF16>
-__device__ __forceinline__ void softmax(const AttendParams& p, uint32_t pt, uint32_t bars, uint32_t tmem, float* nref,
-                                        int64_t* offsets, const int* ids, Cursor cur, int groups, int sms, tc::Waiter& w) {
+__device__ __forceinline__ void softmax(const AttendParams& p, uint32_t base, uint32_t bars, uint32_t tmem, float* nref,
+                                        int64_t* offsets, Cursor cur, int groups, int sms, tc::Waiter& w) {
   constexpr float kTop = Range<kF16>::kTop, kLazy = Range<kF16>::kLazy;
-  constexpr int kW = N / 2;  // columns of this thread
+  constexpr int kW = N / 2, kBlocks = kW / 8;  // columns of this warp, in blocks of 8
   const int tid = threadIdx.x - kProducerWarps * 32;
   const int lane = tid & 31, warp = (tid >> 5) & 3;
   const int c0 = (tid >> 7) * kW;                                 // its first column
-  const int dim = tid & 127;                                      // later, its dimension of a block of 128
-  const bool has_key = lane < 16;  // products of 64 rows: row i lies in lane i % 16 of a warp's 32
-  const int key = 16 * warp + (lane & 15);                        // its key in the tile
+  // scores: keys key0 and key0 + 8, of each block the columns 2 (lane % 4) and the next
+  const int key0 = 16 * warp + (lane >> 2);
+  const int my = c0 + 2 * (lane & 3);
+  const int dim = tid & 127;                                      // results: dimension of a block of 128
   const uint32_t tm = tmem + ((uint32_t)(32 * warp) << 16) + c0;  // its warp's lanes, its columns
   // nref: [N] the references, negated (+infinity: none yet)
   float* alpha = nref + N;                             // [N] rescale factors, then result factors
   int* limit = reinterpret_cast<int*>(nref + 2 * N);   // [N] keys that a column sees
   float* scalars = nref + 3 * N;                       // skey0, its change, the warps' largest skey [4]
   float* red = nref + 4 * N;                           // [4][N] the warps' maxima or sums
-  const float* skey = nref + Smem<N, kF16>::kKeyScale;
-  const int col = c0 + lane * kW / 32;                 // where halve() leaves this lane's result
+  const float* skey = nref + Smem<N>::kKeyScale;
+  auto pair = [](const float* v) { return *reinterpret_cast<const float2*>(v); };
+  auto leave = [&](const float2* v) {  // joined values of this warp's columns
+    if (lane < 4) {
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b) *reinterpret_cast<float2*>(red + warp * N + my + 8 * b) = v[b];
+    }
+  };
   bool fresh = true, at_start = false;
   bool first_run = true;  // this CTA's first segment
   bool scaled = false;    // some column of the unit has a qs other than 1
   uint32_t it = 0, seg = 0;
-  float2 l[kW / 2];
+  float2 l[kBlocks];
 #pragma unroll 1
   while (cur.left > 0) {
     const int item = cur.item, group = cur.group;
-    const float* qs = nref + Smem<N, kF16>::kQScale + (seg & 1) * N + c0;
+    const float* qs = nref + Smem<N>::kQScale + (seg % 3) * N;
+    const uint32_t buf = it % kBufs, phase = it / kBufs & 1;
     if (fresh) {
       bar_softmax();  // every thread is done with the unit before
       at_start = cur.tile == 0;
@@ -595,51 +545,53 @@ __device__ __forceinline__ void softmax(const AttendParams& p, uint32_t pt, uint
       }
       if (tid == 0) scalars[0] = 0.f;
 #pragma unroll
-      for (int c = 0; c < kW / 2; ++c) l[c] = make_float2(0.f, 0.f);
+      for (int b = 0; b < kBlocks; ++b) l[b] = make_float2(0.f, 0.f);
       bar_softmax();
     }
-    const int k = cur.tile * kTile + key;
-    const int slot = it % kAhead;
-    w.wait(bars + 8 * (kIdFull + slot), (it / kAhead) & 1);
-    const bool there = has_key && ids[slot * kTile + key] >= 0;
-    __syncwarp();
-    if (lane == 0) tc::mbar_arrive(bars + 8 * (kIdEmpty + slot));
+    const int k = cur.tile * kTile + key0;
+    w.wait(bars + 8 * (kFull + buf), phase);  // makes skey and qs visible
+    const float sk[2] = {skey[buf * kTile + key0], skey[buf * kTile + key0 + 8]};
+    const bool there[2] = {sk[0] > 0.f, sk[1] > 0.f};
     // columns differ in what they see only in the last P - 1 keys
     const bool ragged = p.paged && p.P > 1 && (cur.tile + 1) * kTile > limit[0];
-    const bool masks = !__all_sync(0xFFFFFFFFu, there || !has_key) || ragged;
+    const bool masks = !__all_sync(0xFFFFFFFFu, there[0] && there[1]) || ragged;
     const bool first = fresh;
-    float sk = 1.f, mult = p.scale_log2;
-    if (kF16) {
-      w.wait(bars + 8 * kFull, it & 1);  // makes skey and qs visible
-      sk = skey[key];
-      mult *= sk;
-      if (fresh) scaled = __any_sync(0xFFFFFFFFu, qs[lane % kW] != 1.f);
+    float2 mult[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float m = kF16 ? p.scale_log2 * sk[i] : p.scale_log2;
+      mult[i] = make_float2(m, m);
     }
-    w.wait(bars + 8 * kSFull, it & 1);
+    if (kF16 && fresh) scaled = __any_sync(0xFFFFFFFFu, qs[c0 + lane % kW] != 1.f);
+    w.wait(bars + 8 * (kSFull + buf), phase);
     __syncwarp();
     tc::fence_after();
     // this thread's scores in log2 units, less the references or not; -infinity where the key is hidden
-    float s[kW];
+    float2 s[kBlocks][2];
     auto scores = [&](bool relative) {
-      tc::tmem_ld<kW>(tm, s);
+      float raw[4 * kBlocks];
+      tc::tmem_ld_rows16<kBlocks>(tm + buf * N, raw);
       tc::tmem_wait_ld();
-      tc::touch<kW>(s);
-      if (kF16 && scaled) {
+      tc::touch<4 * kBlocks>(raw);
 #pragma unroll
-        for (int c = 0; c < kW; ++c) s[c] *= qs[c];
-      }
-      const float2 m2 = make_float2(mult, mult);
+      for (int b = 0; b < kBlocks; ++b) {
+        const float2 m = relative ? pair(nref + my + 8 * b) : make_float2(0.f, 0.f);
+        const float2 z = kF16 && scaled ? pair(qs + my + 8 * b) : make_float2(1.f, 1.f);
 #pragma unroll
-      for (int c = 0; c < kW; c += 4) {
-        const float4 m = *reinterpret_cast<const float4*>(nref + c0 + c);
-        const float2 x = tc::fma2(make_float2(s[c], s[c + 1]), m2, relative ? make_float2(m.x, m.y) : make_float2(0.f, 0.f));
-        const float2 y = tc::fma2(make_float2(s[c + 2], s[c + 3]), m2, relative ? make_float2(m.z, m.w) : make_float2(0.f, 0.f));
-        s[c] = x.x, s[c + 1] = x.y, s[c + 2] = y.x, s[c + 3] = y.y;
+        for (int i = 0; i < 2; ++i) {
+          float2 x = make_float2(raw[4 * b + 2 * i], raw[4 * b + 2 * i + 1]);
+          if (kF16 && scaled) x = tc::mul2(x, z);
+          s[b][i] = tc::fma2(x, mult[i], m);
+        }
       }
       if (masks) {
 #pragma unroll
-        for (int c = 0; c < kW; ++c)
-          if (!there || (ragged && k >= limit[c0 + c])) s[c] = -INFINITY;
+        for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (!there[i] || (ragged && k + 8 * i >= limit[my + 8 * b])) s[b][i].x = -INFINITY;
+            if (!there[i] || (ragged && k + 8 * i >= limit[my + 8 * b + 1])) s[b][i].y = -INFINITY;
+          }
       }
     };
     // twice at most: with the references as they are, and again if one had to move
@@ -647,20 +599,19 @@ __device__ __forceinline__ void softmax(const AttendParams& p, uint32_t pt, uint
 #pragma unroll 1
     while (true) {
       scores(true);
-      const float top = tc::max_of<kW>(s);
-      if (moved || !any_softmax(has_key && (top > kLazy || (kF16 && there && sk > scalars[0])))) break;
+      const float top = tc::max_of<4 * kBlocks>(&s[0][0].x);
+      const float z0 = kF16 ? scalars[0] : 0.f;
+      if (moved || !any_softmax(top > kLazy || (kF16 && (sk[0] > z0 || sk[1] > z0)))) break;
       moved = true;
       // a new reference for every column, kTop below the maximum of the old one's and this tile's scores
       scores(false);
-      if (!has_key) {
+      float2 m[kBlocks];
 #pragma unroll
-        for (int c = 0; c < kW; ++c) s[c] = -INFINITY;
-      }
-      __syncwarp();
-      halve<kW>(s, lane, [](float a, float b) { return fmaxf(a, b); });
-      red[warp * N + col] = s[0];
+      for (int b = 0; b < kBlocks; ++b) m[b] = make_float2(fmaxf(s[b][0].x, s[b][1].x), fmaxf(s[b][0].y, s[b][1].y));
+      over_keys<2 * kBlocks>(&m[0].x, [](float a, float b) { return fmaxf(a, b); });
+      leave(m);
       if (kF16) {
-        float z = there ? sk : 0.f;
+        float z = fmaxf(sk[0], sk[1]);
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) z = fmaxf(z, __shfl_xor_sync(0xFFFFFFFFu, z, d));
         if (lane == 0) scalars[2 + warp] = z;
@@ -680,48 +631,52 @@ __device__ __forceinline__ void softmax(const AttendParams& p, uint32_t pt, uint
       }
       bar_softmax();
 #pragma unroll
-      for (int c = 0; c < kW / 2; ++c) l[c].x *= alpha[c0 + 2 * c], l[c].y *= alpha[c0 + 2 * c + 1];
+      for (int b = 0; b < kBlocks; ++b) l[b] = tc::mul2(l[b], pair(alpha + my + 8 * b));
       if (!first) {
-        // the products of the tiles before have finished: they were committed before these scores
+        // once the products of the tiles before have finished
+        w.wait(bars + 8 * (kEmpty + (it - 1) % kBufs), (it - 1) / kBufs & 1);
+        __syncwarp();
+        tc::fence_after();
         const float change = kF16 ? scalars[1] : 1.f;
 #pragma unroll 1
         for (int c = 0; c < 4 * kW; c += 8) {
           const int g = c / kW, x0 = c % kW;
           float o[8];
-          tc::tmem_ld<8>(tm + N + g * N + x0, o);
+          tc::tmem_ld<8>(tm + (2 + g) * N + x0, o);
           tc::tmem_wait_ld();
           tc::touch<8>(o);
 #pragma unroll
           for (int x = 0; x < 8; ++x) o[x] *= alpha[c0 + x0 + x] * change;
-          tc::tmem_st8(tm + N + g * N + x0, o);
+          tc::tmem_st8(tm + (2 + g) * N + x0, o);
         }
         tc::tmem_wait_st();
       }
     }
-    // weights, their sums per lane, and P^T: [key][column], 2 N bytes a key, swizzled like the descriptor says
-    const float share = kF16 ? (there ? sk / scalars[0] : 0.f) : 1.f;
-    const float2 share2 = make_float2(share, share);
+    // weights, their sums per thread, and P^T: [key][column], 2 N bytes a key, swizzled like the descriptor says
 #pragma unroll
-    for (int c = 0; c < kW; c += 8) {
-      uint32_t out[4];
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        float2 e = make_float2(tc::exp2_fast(s[c + 2 * x]), tc::exp2_fast(s[c + 2 * x + 1]));
-        l[c / 2 + x] = tc::add2(l[c / 2 + x], e);
-        if (kF16) {
-          e = tc::mul2(e, share2);
-          out[x] = pack_half(e.x, e.y);
-        } else {
-          out[x] = tc::pack_bf16(e.x, e.y);
-        }
-      }
+    for (int i = 0; i < 2; ++i) {
+      const int key = key0 + 8 * i;
+      const float share = kF16 && there[i] ? sk[i] / scalars[0] : 0.f;
+      const uint32_t to = base + buf * kTileBytes + 8 * kSub + key * (2 * N) + 4 * (lane & 3);
       const int sw = N == 64 ? (key & 7) : N == 32 ? ((key >> 1) & 3) : ((key >> 2) & 1);
-      if (has_key) sts(pt + key * (2 * N) + ((((c0 + c) / 8) ^ sw) << 4), out[0], out[1], out[2], out[3]);
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b) {
+        float2 e = make_float2(tc::exp2_fast(s[b][i].x), tc::exp2_fast(s[b][i].y));
+        l[b] = tc::add2(l[b], e);
+        uint32_t two;
+        if (kF16) {
+          e = tc::mul2(e, make_float2(share, share));
+          two = pack_half(e.x, e.y);
+        } else {
+          two = tc::pack_bf16(e.x, e.y);
+        }
+        sts4(to + (((c0 / 8 + b) ^ sw) << 4), two);
+      }
     }
     tc::fence_async_smem();
     tc::fence_before();
     __syncwarp();
-    if (lane == 0) tc::mbar_arrive(bars + 8 * kPReady);
+    if (lane == 0) tc::mbar_arrive(bars + 8 * (kPReady + buf));
 
     const int unit_tiles = cur.tiles, tile = cur.tile;
     fresh = cur.next(p, groups);
@@ -731,14 +686,8 @@ __device__ __forceinline__ void softmax(const AttendParams& p, uint32_t pt, uint
     // the segment ends: join the sums, then the results
     const bool whole = at_start && tile + 1 == unit_tiles;
     const int ncols = min(N, p.cols - group * N);
-    float* sums = reinterpret_cast<float*>(l);
-    if (!has_key) {
-#pragma unroll
-      for (int c = 0; c < kW; ++c) sums[c] = 0.f;
-    }
-    __syncwarp();
-    halve<kW>(sums, lane, [](float a, float b) { return a + b; });
-    red[warp * N + col] = sums[0];
+    over_keys<2 * kBlocks>(&l[0].x, [](float a, float b) { return a + b; });
+    leave(l);
     bar_softmax();
     const int part = 2 * blockIdx.x + (first_run && !at_start ? 0 : 1);
     first_run = false;
@@ -763,7 +712,7 @@ __device__ __forceinline__ void softmax(const AttendParams& p, uint32_t pt, uint
 #pragma unroll 1
     for (int g = 0; g < 4; ++g) {
       float o[kW];
-      tc::tmem_ld<kW>(tm + N + g * N, o);
+      tc::tmem_ld<kW>(tm + (2 + g) * N, o);
       tc::tmem_wait_ld();
       tc::touch<kW>(o);
       // O' / sum * skey0, in an order that cannot overflow early
@@ -816,10 +765,9 @@ __device__ int64_t block_scan(int64_t v, int64_t* total, int64_t* scratch) {
 __host__ __device__ __forceinline__ int64_t run_begin(int64_t total, int ctas, int b) { return total * b / ctas; }
 
 template <int N, int kRowBytes>
-__global__ void __launch_bounds__(kThreads, 1) attend_kernel(const AttendParams p, const __grid_constant__ CUtensorMap map,
-                                                             int groups, int sms) {
+__global__ void __launch_bounds__(kThreads, 1) attend_kernel(const AttendParams p, int groups, int sms) {
   constexpr bool kF16 = kRowBytes == HS_ROW_BYTES_FP8;
-  using L = Smem<N, kF16>;
+  using L = Smem<N>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~uintptr_t(1023));
   __shared__ RunStart start;
@@ -830,7 +778,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const AttendParams 
   const uint32_t bars = base + L::kMisc;
   float* nref = reinterpret_cast<float*>(smem + L::kRef);
   int64_t* offsets = reinterpret_cast<int64_t*>(smem + L::kOffsets);
-  int* ids = reinterpret_cast<int*>(smem + L::kIds);
 
   // The run of tiles of this CTA.
   int64_t total, begin, run = 0;
@@ -875,24 +822,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const AttendParams 
   if ((int)blockIdx.x >= ctas) return;
 
   if (threadIdx.x == 0) {
-    for (int c = 0; c < 2; ++c) {
+    for (int c = 0; c < kBufs; ++c) {
       tc::mbar_init(bars + 8 * (kFull + c), kProducerWarps);
       tc::mbar_init(bars + 8 * (kEmpty + c), 1);
+      tc::mbar_init(bars + 8 * (kSFull + c), 1);
+      tc::mbar_init(bars + 8 * (kPReady + c), kSoftmaxWarps);
     }
     tc::mbar_init(bars + 8 * kQFull, kProducerWarps);
     tc::mbar_init(bars + 8 * kQEmpty, 1);
-    tc::mbar_init(bars + 8 * kSFull, 1);
-    tc::mbar_init(bars + 8 * kPReady, kSoftmaxWarps);
     tc::mbar_init(bars + 8 * kOFull, 1);
     tc::mbar_init(bars + 8 * kDrain, 1);
-    for (int i = 0; i < L::kSlots; ++i) {
-      tc::mbar_init(bars + 8 * (kRawFull + i), 1);
-      tc::mbar_init(bars + 8 * (kRawEmpty + i), 4);
-    }
-    for (int i = 0; i < kAhead; ++i) {
-      tc::mbar_init(bars + 8 * (kIdFull + i), 1);
-      tc::mbar_init(bars + 8 * (kIdEmpty + i), kProducerWarps + kSoftmaxWarps);
-    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kMmaWarp) tc::tmem_alloc(tc::smem_u32(&tmem_slot), tmem_cols<N>());
@@ -907,16 +846,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const AttendParams 
   tc::Waiter w;
   if (warp < kProducerWarps) {
     fewer_registers<kRegsProducer>();
-    produce_tiles<N, kF16>(p, base, ids, nref + L::kQScale, nref + L::kKeyScale, bars, cur, groups, w);
+    produce_tiles<N, kF16>(p, base, nref + L::kQScale, nref + L::kKeyScale, bars, cur, groups, w);
   } else if (warp < kMmaWarp) {
     more_registers<kRegsSoftmax>();
-    softmax<N, kF16>(p, base + L::kP, bars, tmem, nref, offsets, ids, cur, groups, sms, w);
+    softmax<N, kF16>(p, base, bars, tmem, nref, offsets, cur, groups, sms, w);
   } else {
     fewer_registers<kRegsMma>();
-    if (warp == kGatherWarp)
-      gather_rows<N, kF16>(p, &map, base, ids, bars, cur, groups, w);
-    else if (warp == kMmaWarp)
-      issue_products<N, kF16>(p, base, base + L::kQ, base + L::kP, bars, tmem, cur, groups, w);
+    if (warp == kMmaWarp) issue_products<N, kF16>(p, base, bars, tmem, cur, groups, w);
   }
   if (w.dead) report(p.status, HS_ERR_TIMEOUT);
   __syncwarp();
@@ -981,7 +917,7 @@ cudaError_t launch(const AttendParams& p, int sms, cudaStream_t s) {
     // the register trade waits for ever if the launch has fewer than it hands out
     if (e == cudaSuccess && a.numRegs != kRegsLaunch) e = cudaErrorInvalidKernelImage;
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(attend_kernel<N, kRowBytes>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<N, kRowBytes == HS_ROW_BYTES_FP8>::kBytes);
+      e = cudaFuncSetAttribute(attend_kernel<N, kRowBytes>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<N>::kBytes);
     return e;
   }();
   if (ready != cudaSuccess) return ready;
@@ -995,9 +931,7 @@ cudaError_t launch(const AttendParams& p, int sms, cudaStream_t s) {
     if (units * tiles < grid) grid = (int)(units * tiles);
     cut = tiles > 1 && units % grid != 0;
   }
-  CUtensorMap map;
-  if (!tc::gather_map(&map, p.base, p.row_bytes, p.num_rows, Raw<kRowBytes == HS_ROW_BYTES_FP8>::kBox)) return cudaErrorUnknown;
-  attend_kernel<N, kRowBytes><<<grid, kThreads, Smem<N, kRowBytes == HS_ROW_BYTES_FP8>::kBytes, s>>>(p, map, groups, sms);
+  attend_kernel<N, kRowBytes><<<grid, kThreads, Smem<N>::kBytes, s>>>(p, groups, sms);
   count_launch();
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !cut || grid < 2) return e;

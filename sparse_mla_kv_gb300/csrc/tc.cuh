@@ -34,6 +34,19 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+// The same without suspending the thread when the phase is not complete.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Waits are bounded: one that has not ended after kWaitCycles SM cycles (seconds) gives up, and from then on
 // every wait of that thread returns at once, so that the kernel runs to its end; `dead` says so and the caller
 // reports HS_ERR_TIMEOUT.  Everything a kernel accesses stays in bounds whatever the waits return.
@@ -124,6 +137,26 @@ __device__ __forceinline__ void tmem_ld(uint32_t a, float* v) {
   } else {
 #pragma unroll
     for (int c = 0; c < n; c += 16) tmem_ld16(a + c, v + c);
+  }
+}
+// 16 lanes (the first of this warp's 32) x 8 n columns, spread over the warp: of each 8 columns, a thread has columns
+// 2 (lane % 4) and the next of row lane / 4, then those of row lane / 4 + 8.
+template <int n>
+__device__ __forceinline__ void tmem_ld_rows16(uint32_t a, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  if constexpr (n == 1) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
+  } else if constexpr (n == 2) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(a));
+  } else {
+    static_assert(n == 4, "blocks of 8 columns");
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(a));
   }
 }
 __device__ __forceinline__ void tmem_st16(uint32_t a, const float* v) {
