@@ -242,7 +242,7 @@ __device__ __forceinline__ void copy_queries(const AttendParams& p, uint32_t q, 
 }
 
 // The same in fp16 by plain loads: a column is divided by qs, a power of two (mostly 1) that brings it into
-// fp16's range.  Two passes over the queries, so that few registers are needed beside the rows in flight.
+// fp16's range.
 template <int N>
 __device__ __forceinline__ void convert_queries(const AttendParams& p, uint32_t q, float* qs, int item, int group) {
   constexpr int kPer = kProducerWarps * 32 / N;  // threads of a column: neighbouring lanes
@@ -253,22 +253,30 @@ __device__ __forceinline__ void convert_queries(const AttendParams& p, uint32_t 
   const bool there = c < p.cols;
   const __nv_bfloat16* lat = there ? p.q_latent + tok * p.ql_tok + head * p.ql_head : p.q_latent;
   const __nv_bfloat16* rope = there ? p.q_rope + tok * p.qr_tok + head * p.qr_head : p.q_rope;
-  auto chunk = [&](int j) { return __ldg(reinterpret_cast<const uint4*>(j < 64 ? lat + 8 * j : rope + 8 * (j - 64))); };
+  constexpr int kChunks = (72 + kPer - 1) / kPer;
+  uint4 v[kChunks];
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i) {
+    const int j = j0 + i * kPer;
+    v[i] = make_uint4(0, 0, 0, 0);
+    if (there && j < 72) v[i] = __ldg(reinterpret_cast<const uint4*>(j < 64 ? lat + 8 * j : rope + 8 * (j - 64)));
+  }
   float top = 0.f;
-#pragma unroll 3
-  for (int j = j0; j < 72; j += kPer) top = fmaxf(top, max_bf16x8(chunk(j)));
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i) top = fmaxf(top, max_bf16x8(v[i]));
 #pragma unroll
   for (int d = 1; d < kPer; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
   // left as they are when their largest magnitude is in 2^-2 .. 2^15: fp16 then keeps all but what is 2^-23 of it
   const int b = (int)(__float_as_uint(top) >> 23);
   const int e = top == 0.f || (b >= 125 && b < 142) ? 127 : min(max(b - 14, 1), 240);
-  const float f = there ? __uint_as_float((uint32_t)(254 - e) << 23) : 0.f;
+  const float f = __uint_as_float((uint32_t)(254 - e) << 23);
   if (j0 == 0) qs[col] = __uint_as_float((uint32_t)e << 23);
-#pragma unroll 3
-  for (int j = j0; j < 72; j += kPer) {
-    uint4 v = there ? chunk(j) : make_uint4(0, 0, 0, 0);
-    sts(q + (j >> 3) * (N * 128) + col * 128 + (((j & 7) ^ (col & 7)) << 4), bf16_to_half(v.x, f), bf16_to_half(v.y, f),
-        bf16_to_half(v.z, f), bf16_to_half(v.w, f));
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i) {
+    const int j = j0 + i * kPer;
+    if (j < 72)
+      sts(q + (j >> 3) * (N * 128) + col * 128 + (((j & 7) ^ (col & 7)) << 4), bf16_to_half(v[i].x, f),
+          bf16_to_half(v[i].y, f), bf16_to_half(v[i].z, f), bf16_to_half(v[i].w, f));
   }
 }
 
@@ -404,7 +412,8 @@ __device__ __forceinline__ void issue_products(const AttendParams& p, uint32_t b
 #pragma unroll 1
   while (done < total && !w.dead) {
     const bool more = issued < total && issued < done + kBufs;  // scores could be issued
-    const uint32_t sb = issued % kBufs, ob = done % kBufs;
+    // (through a reduction, so that the operands' addresses stay in uniform registers)
+    const uint32_t sb = __reduce_max_sync(0xFFFFFFFFu, issued % kBufs), ob = __reduce_max_sync(0xFFFFFFFFu, done % kBufs);
     const uint32_t full = bars + 8 * (kFull + sb), full_phase = issued / kBufs & 1;
     const uint32_t ready = bars + 8 * (kPReady + ob), ready_phase = done / kBufs & 1;
     bool results;
@@ -819,6 +828,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const AttendParams 
       }
     }
   }
+  asm volatile("griddepcontrol.launch_dependents;");  // combine_kernel waits for this kernel's results by itself
   if ((int)blockIdx.x >= ctas) return;
 
   if (threadIdx.x == 0) {
@@ -865,48 +875,59 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const AttendParams 
 }
 
 // Joins the partial results of the units that run boundary b = blockIdx.x + 1 is the first to cut: the results are
-// weighted by exp2 of their log2 sums, in the order of the runs.  128 threads: 4 dimensions each, kJoinCols columns.
+// weighted by exp2 of their log2 sums, in the order of the runs.  128 threads a column, with 4 dimensions each.
 constexpr int kJoinCols = 4;
-__global__ void __launch_bounds__(128) combine_kernel(const AttendParams p, int groups, int n, int sms, int grid) {
+__global__ void __launch_bounds__(128 * kJoinCols) combine_kernel(const AttendParams p, int groups, int n, int sms, int grid) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // for attend_kernel's results
   const uint8_t* ws = reinterpret_cast<const uint8_t*>(p.workspace);
   const RunStart* runs = reinterpret_cast<const RunStart*>(ws + ws_run_offset(sms));
   const float* lse = reinterpret_cast<const float*>(ws + ws_lse_offset(sms));
   const int b = blockIdx.x + 1;
   const int64_t total = runs[0].total;
+  const RunStart r = runs[min(b, grid - 1)];  // (there may be fewer runs than CTAs: what is read past them is not used)
   const int ctas = (int)min((int64_t)grid, total);
   if (b >= ctas) return;
-  const RunStart r = runs[b];
   const int group = r.off / r.tiles, tile = r.off - group * r.tiles;
   if (tile == 0) return;
   const int64_t unit0 = run_begin(total, ctas, b) - tile, unit1 = unit0 + r.tiles;
   if (run_begin(total, ctas, b - 1) > unit0) return;  // an earlier boundary cuts this unit
+  const int c = blockIdx.y * kJoinCols + threadIdx.x / 128, d = threadIdx.x % 128;
+  if (c >= min(n, p.cols - group * n)) return;
   int last = b;  // runs b - 1 .. last hold parts of it
   while (last + 1 < ctas && run_begin(total, ctas, last + 1) < unit1) ++last;
-  const int ncols = min(n, p.cols - group * n);
-  const int c1 = min(ncols, (int)(blockIdx.y + 1) * kJoinCols);
-  for (int c = blockIdx.y * kJoinCols; c < c1; ++c) {
-    float top = -INFINITY;
-    for (int i = b - 1; i <= last; ++i) top = fmaxf(top, lse[(2 * i + (i < b)) * kMaxCols + c]);
-    float sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = b - 1; i <= last; ++i) {
-      const int slot = 2 * i + (i < b);
-      const float z = lse[slot * kMaxCols + c];
-      const float f = z == -INFINITY ? 0.f : exp2f(z - top);
-      const float4 v = reinterpret_cast<const float4*>(p.workspace + ((int64_t)slot * kMaxCols + c) * kLatent)[threadIdx.x];
-      sum += f;
-      acc.x += f * v.x, acc.y += f * v.y, acc.z += f * v.z, acc.w += f * v.w;
+  float top = -INFINITY, sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = b - 1; i0 <= last; i0 += 4) {  // four parts at a time
+    float z[4];
+    float4 v[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int i = i0 + x, slot = 2 * i + (i < b);
+      z[x] = -INFINITY;
+      v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i <= last) {
+        z[x] = lse[slot * kMaxCols + c];
+        v[x] = reinterpret_cast<const float4*>(p.workspace + ((int64_t)slot * kMaxCols + c) * kLatent)[d];
+      }
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const int gc = group * n + c;
-    const int pos = gc / p.heads, head = gc - pos * p.heads;
-    __nv_bfloat16* dst = p.out + ((int64_t)r.item * p.P + pos) * p.out_tok + head * p.out_head + 4 * threadIdx.x;
-    *reinterpret_cast<uint2*>(dst) =
-        make_uint2(tc::pack_bf16(acc.x * inv, acc.y * inv), tc::pack_bf16(acc.z * inv, acc.w * inv));
-    if (threadIdx.x == 0 && p.lse)
-      p.lse[(int64_t)r.item * p.cols + gc] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    const float now = fmaxf(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])), top);
+    const float old = top == -INFINITY ? 0.f : exp2f(top - now);
+    sum *= old, acc.x *= old, acc.y *= old, acc.z *= old, acc.w *= old;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const float f = z[x] == -INFINITY ? 0.f : exp2f(z[x] - now);
+      sum += f;
+      acc.x += f * v[x].x, acc.y += f * v[x].y, acc.z += f * v[x].z, acc.w += f * v[x].w;
+    }
+    top = now;
   }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int gc = group * n + c;
+  const int pos = gc / p.heads, head = gc - pos * p.heads;
+  __nv_bfloat16* dst = p.out + ((int64_t)r.item * p.P + pos) * p.out_tok + head * p.out_head + 4 * d;
+  *reinterpret_cast<uint2*>(dst) =
+      make_uint2(tc::pack_bf16(acc.x * inv, acc.y * inv), tc::pack_bf16(acc.z * inv, acc.w * inv));
+  if (d == 0 && p.lse) p.lse[(int64_t)r.item * p.cols + gc] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
 template <int N, int kRowBytes>
@@ -935,9 +956,19 @@ cudaError_t launch(const AttendParams& p, int sms, cudaStream_t s) {
   count_launch();
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !cut || grid < 2) return e;
-  combine_kernel<<<dim3(grid - 1, N / kJoinCols), 128, 0, s>>>(p, groups, N, sms, grid);
+  // its launch overlaps the end of the kernel before
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(grid - 1, N / kJoinCols);
+  c.blockDim = dim3(128 * kJoinCols);
+  c.stream = s;
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &early;
+  c.numAttrs = 1;
+  e = cudaLaunchKernelEx(&c, combine_kernel, p, groups, N, sms, grid);
   count_launch();
-  return cudaGetLastError();
+  return e;
 }
 
 template <int kRowBytes>
