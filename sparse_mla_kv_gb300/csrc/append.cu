@@ -21,11 +21,12 @@ namespace {
 constexpr int kThreads = 128;
 
 template <typename T>
-struct Vec8;  // 8 values of T <-> 8 floats
+struct Vec8;  // 8 values of T as they lie in memory <-> 8 floats
 template <>
 struct Vec8<__nv_bfloat16> {
-  static __device__ __forceinline__ void load(const __nv_bfloat16* p, float* x) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
+  uint4 v;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void values(float* x) const {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -45,8 +46,9 @@ struct Vec8<__nv_bfloat16> {
 };
 template <>
 struct Vec8<__half> {
-  static __device__ __forceinline__ void load(const __half* p, float* x) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
+  uint4 v;
+  __device__ __forceinline__ void load(const __half* p) { v = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void values(float* x) const {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -67,12 +69,14 @@ struct Vec8<__half> {
 };
 template <>
 struct Vec8<float> {
-  static __device__ __forceinline__ void load(const float* p, float* x) {
+  float4 v[2];
+  __device__ __forceinline__ void load(const float* p) {
+    v[0] = reinterpret_cast<const float4*>(p)[0];
+    v[1] = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void values(float* x) const {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float4 v = reinterpret_cast<const float4*>(p)[i];
-      x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
-    }
+    for (int i = 0; i < 2; ++i) x[4 * i] = v[i].x, x[4 * i + 1] = v[i].y, x[4 * i + 2] = v[i].z, x[4 * i + 3] = v[i].w;
   }
   static __device__ __forceinline__ void store(float* p, const float* x) {
 #pragma unroll
@@ -120,58 +124,81 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo_value, float hi_value) {
   return r;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p, int units_per_token,
-                                                          int heads_per_unit, int64_t units) {
+// kHeads: heads of a query unit.  blockIdx.y is the unit of a token: 0 its row, then its queries.  Everything that does not
+// depend on another load is loaded first.
+template <typename T, int kHeads>
+__global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) {
   const hs_append& a = p.a;
   const int lane = threadIdx.x & 31;
-  const int64_t u = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  if (u >= units) return;
-  const int64_t t = u / units_per_token;
-  const int part = (int)(u - t * units_per_token);
+  const int64_t t = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  if (t >= a.n) return;
   const bool inter = a.interleaved != 0;
   const int pos = __ldg(a.positions + t);
-  const bool pos_ok = pos >= 0 && pos < a.num_positions;
-  const float* cs = a.rotation + (int64_t)(pos_ok ? pos : 0) * kRope;
   const int j = lane & 3;
+  bool pos_ok;
   float c[8], s[8];
-  if (part > 0 || lane < 4) {
-    Vec8<float>::load(cs + 8 * j, c);
-    Vec8<float>::load(cs + 32 + 8 * j, s);
-  }
-  if (part > 0) {
+  auto table = [&]() {
+    pos_ok = pos >= 0 && pos < a.num_positions;
+    const float* cs = a.rotation + (int64_t)(pos_ok ? pos : 0) * kRope;
+    Vec8<float> x, y;
+    x.load(cs + 8 * j);
+    y.load(cs + 32 + 8 * j);
+    x.values(c);
+    y.values(s);
+  };
+  if (blockIdx.y > 0) {
     const T* q = static_cast<const T*>(a.q_rope) + t * a.q_token_stride;
     T* o = static_cast<T*>(a.q_out) + t * a.q_out_token_stride;
-    const int h0 = (part - 1) * heads_per_unit;
-    const int h1 = min(a.heads, h0 + heads_per_unit);
-    for (int h = h0 + (lane >> 2); h < h1; h += 8) {
+    const int h0 = (blockIdx.y - 1) * kHeads + (lane >> 2);
+    Vec8<T> in[kHeads / 8][2];
+#pragma unroll
+    for (int i = 0; i < kHeads / 8; ++i) {
+      const int h = min(h0 + 8 * i, a.heads - 1);
+      in[i][0].load(q + h * a.q_head_stride + lo(j, inter));
+      in[i][1].load(q + h * a.q_head_stride + hi(j, inter));
+    }
+    table();
+#pragma unroll
+    for (int i = 0; i < kHeads / 8; ++i) {
+      const int h = h0 + 8 * i;
       float x[16];
-      Vec8<T>::load(q + h * a.q_head_stride + lo(j, inter), x);
-      Vec8<T>::load(q + h * a.q_head_stride + hi(j, inter), x + 8);
+      in[i][0].values(x);
+      in[i][1].values(x + 8);
       rotate(x, c, s, inter);
       if (!pos_ok)
-        for (int i = 0; i < 16; ++i) x[i] = 0.f;
-      Vec8<T>::store(o + h * a.q_out_head_stride + lo(j, inter), x);
-      Vec8<T>::store(o + h * a.q_out_head_stride + hi(j, inter), x + 8);
+        for (int e = 0; e < 16; ++e) x[e] = 0.f;
+      if (h < a.heads) {
+        Vec8<T>::store(o + h * a.q_out_head_stride + lo(j, inter), x);
+        Vec8<T>::store(o + h * a.q_out_head_stride + hi(j, inter), x + 8);
+      }
     }
     return;
   }
   const int row = __ldg(a.rows + t);
+  const T* src = static_cast<const T*>(a.latent) + t * a.latent_stride + 16 * lane;
+  Vec8<T> in[2], key[2];
+  in[0].load(src);
+  in[1].load(src + 8);
+  if (lane < 4) {
+    const T* k = static_cast<const T*>(a.rope) + t * a.rope_stride;
+    key[0].load(k + lo(j, inter));
+    key[1].load(k + hi(j, inter));
+  }
+  float r[16];
+  pos_ok = pos >= 0 && pos < a.num_positions;
+  if (lane < 4) {
+    table();
+    key[0].values(r);
+    key[1].values(r + 8);
+    rotate(r, c, s, inter);
+  }
   const bool row_ok = row >= 0 && row < p.num_rows;
   if (lane == 0 && ((row != -1 && !row_ok) || !pos_ok)) report(a.status, HS_ERR_ID_RANGE);
   if (!row_ok || !pos_ok) return;
   uint8_t* dst = p.base + (int64_t)row * p.row_bytes;
-  const T* src = static_cast<const T*>(a.latent) + t * a.latent_stride + 16 * lane;
   float x[16];
-  Vec8<T>::load(src, x);
-  Vec8<T>::load(src + 8, x + 8);
-  float r[16];
-  if (lane < 4) {
-    const T* k = static_cast<const T*>(a.rope) + t * a.rope_stride;
-    Vec8<T>::load(k + lo(j, inter), r);
-    Vec8<T>::load(k + hi(j, inter), r + 8);
-    rotate(r, c, s, inter);
-  }
+  in[0].values(x);
+  in[1].values(x + 8);
   int rope_at;
   if (p.row_bytes == HS_ROW_BYTES_FP8) {
     float amax = 0.f;
@@ -204,21 +231,25 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p, 
   }
 }
 
+template <int kHeads>
+void launch_heads(const AppendParams& p, cudaStream_t s) {
+  const dim3 grid((unsigned)((p.a.n + kThreads / 32 - 1) / (kThreads / 32)), 1 + (p.a.heads + kHeads - 1) / kHeads);
+  if (p.a.dtype == HS_BF16)
+    append_kernel<__nv_bfloat16, kHeads><<<grid, kThreads, 0, s>>>(p);
+  else if (p.a.dtype == HS_FP16)
+    append_kernel<__half, kHeads><<<grid, kThreads, 0, s>>>(p);
+  else
+    append_kernel<float, kHeads><<<grid, kThreads, 0, s>>>(p);
+}
+
 }  // namespace
 
 cudaError_t launch_append(const AppendParams& p, int sms, cudaStream_t s) {
-  const int heads_per_unit = 8;
-  const int upt = 1 + (p.a.heads + heads_per_unit - 1) / heads_per_unit;
-  const int64_t units = p.a.n * upt;
-  const int64_t blocks = (units + kThreads / 32 - 1) / (kThreads / 32);
-  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-  (void)sms;
-  if (p.a.dtype == HS_BF16)
-    append_kernel<__nv_bfloat16><<<(unsigned)blocks, kThreads, 0, s>>>(p, upt, heads_per_unit, units);
-  else if (p.a.dtype == HS_FP16)
-    append_kernel<__half><<<(unsigned)blocks, kThreads, 0, s>>>(p, upt, heads_per_unit, units);
+  // few tokens are spread further; many take fewer reads of the table
+  if (p.a.n * (1 + p.a.heads / 16) < 64 * (int64_t)sms)
+    launch_heads<8>(p, s);
   else
-    append_kernel<float><<<(unsigned)blocks, kThreads, 0, s>>>(p, upt, heads_per_unit, units);
+    launch_heads<16>(p, s);
   count_launch();
   return cudaGetLastError();
 }

@@ -56,10 +56,11 @@ __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec
 constexpr int kSub = kTile * 128;    // bytes of a sub-tile: 64 keys x 64 values
 constexpr int kTileBytes = 9 * kSub;  // of which the ninth holds the rotated parts, and later the weights
 // In log2 units: where a new reference puts the largest score, and the most that a score may reach before it moves.
-// fp16 weights are normal from 2^-14 to 2^16; bf16 weights have fp32's range.
+// fp16 weights are normal from 2^-14 to 2^16, and a key's skey may be kGrow times skey0 before that moves; bf16 weights
+// have fp32's range.
 template <bool kF16>
 struct Range {
-  static constexpr float kTop = kF16 ? 7.f : 0.f, kLazy = kF16 ? 15.f : 64.f;
+  static constexpr float kTop = kF16 ? 4.f : 0.f, kLazy = kF16 ? 12.f : 64.f, kGrow = 8.f;
 };
 
 // Workspace: partial results [2 per CTA][kMaxCols][512], their log2 sums [2 per CTA][kMaxCols], run starts [CTA].
@@ -609,7 +610,7 @@ __device__ __forceinline__ void softmax(const AttendParams& p, uint32_t base, ui
     while (true) {
       scores(true);
       const float top = tc::max_of<4 * kBlocks>(&s[0][0].x);
-      const float z0 = kF16 ? scalars[0] : 0.f;
+      const float z0 = kF16 ? scalars[0] * Range<kF16>::kGrow : 0.f;
       if (moved || !any_softmax(top > kLazy || (kF16 && (sk[0] > z0 || sk[1] > z0)))) break;
       moved = true;
       // a new reference for every column, kTop below the maximum of the old one's and this tile's scores
