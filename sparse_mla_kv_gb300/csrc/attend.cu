@@ -147,7 +147,7 @@ struct Smem {
   static constexpr int kBytes = kRef + (11 * N + kBufs * kTile) * 4 + 1024;  // + alignment of the base
   static_assert(kBytes <= 232448, "shared memory");
 };
-enum Bar { kFull = 0, kEmpty = 2, kQFull = 4, kQEmpty = 5, kSFull = 6, kPReady = 8, kOFull = 10, kDrain, kBars };
+enum Bar { kFull = 0, kEmpty = 2, kQFull = 4, kQEmpty = 5, kSFull = 6, kPReady = 8, kOFull = 10, kDrain, kBars = kDrain + 2 };
 static_assert(kBars * 8 <= 128, "barriers");
 
 template <int N>
@@ -391,107 +391,81 @@ __device__ __forceinline__ void produce_tiles(const AttendParams& p, uint32_t ba
 }
 
 // ---------------------------------------------------------------------------------------------------------
-// Products (one warp)
+// Products
 
-// Scores of a tile as soon as it is there, results as soon as the weights are: a tile's scores are made while the
-// softmax works on the tile before.
+// One warp issues the scores of every tile, another the results: each waits for one thing only, and a tile's scores are
+// made while the softmax works on the tile before.  (A tile's place in tensor memory is free when its place in shared memory
+// is: that is refilled after the results of the tile that had both.)
 template <int N, bool kF16>
-__device__ __forceinline__ void issue_products(const AttendParams& p, uint32_t base, uint32_t bars, uint32_t tmem, Cursor cur,
-                                               int groups, tc::Waiter& w) {
+__device__ __forceinline__ void issue_scores(const AttendParams& p, uint32_t base, uint32_t bars, uint32_t tmem, Cursor cur,
+                                             int groups, tc::Waiter& w) {
   constexpr uint32_t kIdS = tc::idesc(kF16, kTile, N, false, false);
-  constexpr uint32_t kIdO = tc::idesc(kF16, 128, N, true, true);
-  constexpr uint64_t kPSwizzle = N == 64 ? tc::kSwizzle128 : N == 32 ? tc::kSwizzle64 : tc::kSwizzle32;
-  const uint64_t dk = tc::desc(base, 16, 1024, tc::kSwizzle128);    // tile as keys (K-major)
-  const uint64_t dv = tc::desc(base, kSub, 1024, tc::kSwizzle128);  // tile as values (M-major)
+  const uint64_t dk = tc::desc(base, 16, 1024, tc::kSwizzle128);  // tile as keys (K-major)
   const uint64_t dq = tc::desc(base + Smem<N>::kQ, 16, 1024, tc::kSwizzle128);
-  const uint64_t dp = tc::desc(base + 8 * kSub, 16, 8 * N * 2, kPSwizzle);
   const bool leader = tc::elect();
-  const uint32_t total = cur.left;
-  uint32_t issued = 0, done = 0, seg = 0;  // tiles whose scores / results have been issued, units
-  uint32_t firsts = 0, lasts = 0;          // bit b: whether the tile in buffer b begins or ends a unit
   bool fresh = true;
+  uint32_t seg = 0;
 #pragma unroll 1
-  while (done < total && !w.dead) {
-    const bool more = issued < total && issued < done + kBufs;  // scores could be issued
-    // (through a reduction, so that the operands' addresses stay in uniform registers)
-    const uint32_t sb = __reduce_max_sync(0xFFFFFFFFu, issued % kBufs), ob = __reduce_max_sync(0xFFFFFFFFu, done % kBufs);
-    const uint32_t full = bars + 8 * (kFull + sb), full_phase = issued / kBufs & 1;
-    const uint32_t ready = bars + 8 * (kPReady + ob), ready_phase = done / kBufs & 1;
-    bool results;
-    if (!more) {
-      w.wait(ready, ready_phase);
-      results = true;
-    } else if (done == issued) {
-      w.wait(full, full_phase);
-      results = false;
-    } else {
-      const long long t0 = clock64();
-      while (true) {
-        if (__all_sync(0xFFFFFFFFu, tc::mbar_test(ready, ready_phase))) {
-          results = true;
-          break;
-        }
-        if (__all_sync(0xFFFFFFFFu, tc::mbar_test(full, full_phase))) {
-          results = false;
-          break;
-        }
-        if (__any_sync(0xFFFFFFFFu, clock64() - t0 > tc::kWaitCycles)) {
-          w.dead = true;
-          break;
-        }
-      }
-    }
+  for (uint32_t it = 0; cur.left > 0; ++it) {
+    const uint32_t buf = it % kBufs;
+    if (fresh) w.wait(bars + 8 * kQFull, seg++ & 1);
+    w.wait(bars + 8 * (kFull + buf), it / kBufs & 1);
     __syncwarp();
-    if (__any_sync(0xFFFFFFFFu, w.dead)) {
-      w.dead = true;
-      break;
-    }
     tc::fence_after();
-    if (results) {
-      const bool first = firsts >> ob & 1, last = lasts >> ob & 1;
-      const uint64_t a0 = dv + (uint32_t)(ob * kTileBytes >> 4), b = dp + (uint32_t)(ob * kTileBytes >> 4);
+    const uint64_t a0 = dk + (uint32_t)(buf * kTileBytes >> 4);
+    const uint32_t d = tmem + buf * N;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      tc::mma_ss(d, a0 + ((8 * kSub + k * 32) >> 4), dq + ((8 * N * 128 + k * 32) >> 4), kIdS, k > 0, leader);
 #pragma unroll 1
-      for (int g = 0; g < 4; ++g) {
-        const uint64_t a = a0 + (uint32_t)(2 * g * kSub >> 4);
+    for (int c = 0; c < 4; ++c) {
+      const uint64_t a = a0 + (uint32_t)(2 * c * kSub >> 4), b = dq + (uint32_t)(2 * c * (N * 128) >> 4);
 #pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
-          tc::mma_ss(tmem + (2 + g) * N, a + (k * 2048 >> 4), b + ((k * 16 * N * 2) >> 4), kIdO, !first || k > 0, leader);
-      }
-      tc::commit(bars + 8 * (kEmpty + ob), leader);
-      if (last) tc::commit(bars + 8 * kOFull, leader);
-      ++done;
-    } else {
-      if (fresh) {
-        w.wait(bars + 8 * kQFull, seg++ & 1);
-        __syncwarp();
-        tc::fence_after();
-      }
-      const uint64_t a0 = dk + (uint32_t)(sb * kTileBytes >> 4);
-      const uint32_t d = tmem + sb * N;
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        tc::mma_ss(d, a0 + ((8 * kSub + k * 32) >> 4), dq + ((8 * N * 128 + k * 32) >> 4), kIdS, k > 0, leader);
-#pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        const uint64_t a = a0 + (uint32_t)(2 * c * kSub >> 4), b = dq + (uint32_t)(2 * c * (N * 128) >> 4);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          tc::mma_ss(d, a + (((k >> 2) * kSub + (k & 3) * 32) >> 4), b + (((k >> 2) * (N * 128) + (k & 3) * 32) >> 4), kIdS, true,
-                     leader);
-      }
-      tc::commit(bars + 8 * (kSFull + sb), leader);
-      firsts = (firsts & ~(1u << sb)) | (uint32_t)fresh << sb;
-      fresh = cur.next(p, groups);
-      ++issued;
-      const bool last = fresh || cur.left == 0;
-      lasts = (lasts & ~(1u << sb)) | (uint32_t)last << sb;
-      if (last) tc::commit(bars + 8 * kQEmpty, leader);
+      for (int k = 0; k < 8; ++k)
+        tc::mma_ss(d, a + (((k >> 2) * kSub + (k & 3) * 32) >> 4), b + (((k >> 2) * (N * 128) + (k & 3) * 32) >> 4), kIdS, true,
+                   leader);
     }
+    tc::commit(bars + 8 * (kSFull + buf), leader);
+    fresh = cur.next(p, groups);
+    if (fresh || cur.left == 0) tc::commit(bars + 8 * kQEmpty, leader);
   }
   // nothing of this CTA's products is in flight when the others leave
   tc::commit(bars + 8 * kDrain, leader);
   tc::Waiter drain;
   drain.wait(bars + 8 * kDrain, 0);
+  __syncwarp();
+}
+
+template <int N, bool kF16>
+__device__ __forceinline__ void issue_results(const AttendParams& p, uint32_t base, uint32_t bars, uint32_t tmem, Cursor cur,
+                                              int groups, tc::Waiter& w) {
+  constexpr uint32_t kIdO = tc::idesc(kF16, 128, N, true, true);
+  constexpr uint64_t kPSwizzle = N == 64 ? tc::kSwizzle128 : N == 32 ? tc::kSwizzle64 : tc::kSwizzle32;
+  const uint64_t dv = tc::desc(base, kSub, 1024, tc::kSwizzle128);  // tile as values (M-major)
+  const uint64_t dp = tc::desc(base + 8 * kSub, 16, 8 * N * 2, kPSwizzle);
+  const bool leader = tc::elect();
+  bool first = true;
+#pragma unroll 1
+  for (uint32_t it = 0; cur.left > 0; ++it) {
+    const uint32_t buf = it % kBufs;
+    w.wait(bars + 8 * (kPReady + buf), it / kBufs & 1);
+    __syncwarp();
+    tc::fence_after();
+    const uint64_t a0 = dv + (uint32_t)(buf * kTileBytes >> 4), b = dp + (uint32_t)(buf * kTileBytes >> 4);
+#pragma unroll 1
+    for (int g = 0; g < 4; ++g) {
+      const uint64_t a = a0 + (uint32_t)(2 * g * kSub >> 4);
+#pragma unroll
+      for (int k = 0; k < kTile / 16; ++k)
+        tc::mma_ss(tmem + (2 + g) * N, a + (k * 2048 >> 4), b + ((k * 16 * N * 2) >> 4), kIdO, !first || k > 0, leader);
+    }
+    tc::commit(bars + 8 * (kEmpty + buf), leader);
+    first = cur.next(p, groups);
+    if (first || cur.left == 0) tc::commit(bars + 8 * kOFull, leader);
+  }
+  tc::commit(bars + 8 * (kDrain + 1), leader);
+  tc::Waiter drain;
+  drain.wait(bars + 8 * (kDrain + 1), 0);
   __syncwarp();
 }
 
@@ -843,6 +817,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const AttendParams 
     tc::mbar_init(bars + 8 * kQEmpty, 1);
     tc::mbar_init(bars + 8 * kOFull, 1);
     tc::mbar_init(bars + 8 * kDrain, 1);
+    tc::mbar_init(bars + 8 * (kDrain + 1), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kMmaWarp) tc::tmem_alloc(tc::smem_u32(&tmem_slot), tmem_cols<N>());
@@ -863,7 +838,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const AttendParams 
     softmax<N, kF16>(p, base, bars, tmem, nref, offsets, cur, groups, sms, w);
   } else {
     fewer_registers<kRegsMma>();
-    if (warp == kMmaWarp) issue_products<N, kF16>(p, base, bars, tmem, cur, groups, w);
+    if (warp == kMmaWarp)
+      issue_scores<N, kF16>(p, base, bars, tmem, cur, groups, w);
+    else if (warp == kMmaWarp + 1)
+      issue_results<N, kF16>(p, base, bars, tmem, cur, groups, w);
   }
   if (w.dead) report(p.status, HS_ERR_TIMEOUT);
   __syncwarp();
