@@ -26,9 +26,10 @@
  * Conventions: those of hs.h.  The caller owns all memory and streams; calls validate what the host can
  * see, launch on the given stream and return; data errors go to an optional device status word, which is
  * written only when there is one.  Strides are in elements; the innermost dimension is contiguous; tensor
- * pointers and strides are multiples of 16 bytes.  The current device must be the pool's (for
- * hs_attend_expanded: the one that holds the tensors).  Calls that share a workspace must be ordered on
- * one stream.
+ * pointers and strides are multiples of 16 bytes; the rows of a tensor that is written must not overlap, while
+ * one that is read may repeat them (stride 0; hs_attend_expanded takes a stride of 0 between heads, not between
+ * tokens).  The current device must be the pool's (for hs_attend_expanded: the one that holds the tensors).
+ * Calls that share a workspace must be ordered on one stream.
  */
 #ifndef HS_LATENT_H_
 #define HS_LATENT_H_
@@ -88,8 +89,8 @@ hs_status hs_append_rows(const hs_pool* pool, int32_t layer, const hs_append* a,
  * with latent c[k] (fp32 of the stored value, rounded to bf16) and rotated key r[k]:
  *   s[k] = scale * (q_latent[t][h] . c[k] + q_rope[t][h] . r[k])
  *   out[t][h] = sum_k softmax(s)[k] c[k]        lse[t][h] = log sum_k exp(s[k])
- * Sums and softmax statistics are fp32; softmax weights are rounded to bf16 before their product with
- * the latents; out is rounded once.  A token that sees no row gets zeros and lse = -infinity. */
+ * Sums and softmax statistics are fp32; softmax weights are rounded to bf16 (fp8 rows: to fp16) before their
+ * product with the latents; out is rounded once.  A token that sees no row gets zeros and lse = -infinity. */
 typedef struct {
   int32_t heads;            /* 1..HS_MAX_HEADS                                                        */
   float scale;
@@ -111,8 +112,8 @@ size_t hs_attend_workspace_bytes(void);
 
 /* tokens queries, query t over the rows rows[t][0..K): device int32 [tokens][K], the layout of
  * hs_resolve_topk's out_rows for one layer (tokens = R * P).  -1 entries are skipped; an id that occurs
- * twice counts twice.  status: HS_ERR_ID_RANGE for an id outside [-1, num_gpu_blocks * page_size), which
- * is skipped. */
+ * twice counts twice.  K is at most 2^30.  status: HS_ERR_ID_RANGE for an id outside
+ * [-1, num_gpu_blocks * page_size), which is skipped. */
 hs_status hs_attend_rows(const hs_pool* pool, int32_t layer, const int32_t* rows, int64_t tokens, int32_t K,
                          const hs_attend* a, void* workspace, size_t workspace_bytes, hs_stream_t stream);
 
@@ -122,6 +123,7 @@ hs_status hs_attend_rows(const hs_pool* pool, int32_t layer, const int32_t* rows
  * j % page_size.
  *   block_table  device int32 [R][max_pages]
  *   ctx_len      device int32 [R]
+ * max_pages * page_size is at most 2^30, and (max_pages * page_size / 64 + 1) * (P * heads / 64 + 1) below 2^31.
  * status: HS_ERR_TABLE_RANGE for a needed entry outside [0, num_gpu_blocks) or a context longer than
  * max_pages pages; the tokens concerned are skipped. */
 hs_status hs_attend_pages(const hs_pool* pool, int32_t layer, const int32_t* block_table, const int32_t* ctx_len,
@@ -132,7 +134,7 @@ hs_status hs_attend_pages(const hs_pool* pool, int32_t layer, const int32_t* blo
  *   s[i][j] = scale * (q_nope[i][h] . k_nope[j][h] + q_rope[i][h] . k_rope[j])
  *   out[i][h] = sum_j softmax(s)[i][j] v[j][h]      lse[i][h] = log sum_j exp(s[i][j])
  * With causal != 0 the queries are the last tokens of the sequence: query i (counted within it) sees the
- * keys j <= i + keys - queries.  Rounding and empty rows as in hs_attend. */
+ * keys j <= i + keys - queries.  Rounding (bf16 weights) and empty rows as in hs_attend. */
 typedef struct {
   int32_t seqs, heads;
   int32_t causal;

@@ -130,6 +130,8 @@ hs_status hs_attend_pages(const hs_pool* pool, int32_t layer, const int32_t* blo
   if (st != HS_OK || tokens == 0) return st;
   if (!ctx_len || (max_pages > 0 && !block_table) || (int64_t)max_pages * v.page_size > (1 << 30))
     return HS_ERR_INVALID_ARG;
+  // the kernel counts a request's tiles (64 keys x 64 columns) in 32 bits
+  if (((int64_t)max_pages * v.page_size / 64 + 1) * ((int64_t)P * a->heads / 64 + 1) > INT32_MAX) return HS_ERR_INVALID_ARG;
   p.paged = 1;
   p.table = block_table;
   p.ctx_len = ctx_len;
