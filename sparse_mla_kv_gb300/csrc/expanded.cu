@@ -10,9 +10,9 @@
 // a key or value loaded serves 256 queries (81 KB a key tile; one query tile alone would need 64 B a cycle from L2).
 // 12 warps, one CTA per SM, items taken in a fixed stride:
 //   warps 0-3, 4-7   softmax and results of query tile 0 and 1, a row a thread;
-//   warp 8           issues the products, and zeroes value rows past a sequence's end before their product (a weight of
-//                    zero does not cancel a NaN there);
-//   warp 9           loads by the copy engine.
+//   warps 8, 9       issue the products of query tile 0 and 1, so that neither waits for the other's softmax, and zero
+//                    value rows past a sequence's end before their product (a weight of zero does not cancel a NaN there);
+//   warp 10          loads by the copy engine.
 // Shared memory: 96 KB of queries and a ring of eight 16 KB units (128 keys x 64 dimensions); a key tile is three units
 // of keys, then two of values.  Tensor memory: S and O of both tiles, 4 x 128 columns; P, in bf16, takes S's place and is
 // the left operand of the second product from there.
@@ -26,7 +26,7 @@ namespace {
 constexpr int kQRows = 128, kKeys = 128, kBlock = 2 * kQRows;
 constexpr int kUnit = kKeys * 128;  // bytes of a unit
 constexpr int kRing = 8, kUnitsK = 3, kUnitsV = 2, kUnits = kUnitsK + kUnitsV;
-constexpr int kThreads = 12 * 32, kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kThreads = 12 * 32, kMmaWarp = 8, kLoadWarp = kMmaWarp + 2;
 constexpr int kSmemBytes = 6 * kUnit + kRing * kUnit + 512 + 1024;
 // the warpgroups trade registers
 constexpr int kRegsLaunch = 168, kRegsSoftmax = 208, kRegsOther = 88;
@@ -36,7 +36,7 @@ constexpr float kLazy = 64.f;
 // of at most four such groups.  Units are released one by one.
 constexpr int kGroups = 4;
 enum Bar { kFull = 0, kEmpty = kGroups, kQFull = kEmpty + kRing, kQEmpty, kSFull, kPReady = kSFull + 2, kODone = kPReady + 2,
-           kDrain = kODone + 2, kBars };
+           kDrain = kODone + 2, kBars = kDrain + 2 };
 static_assert(kBars * 8 <= 512, "barriers");
 
 struct Maps {
@@ -187,13 +187,15 @@ __device__ __forceinline__ void load_items(const hs_expanded& a, const Maps& m, 
   if (w.dead) report(a.status, HS_ERR_TIMEOUT);
 }
 
-// ---- products (one warp) ----
-__device__ __forceinline__ void issue_items(const hs_expanded& a, uint32_t q, uint32_t ring, uint32_t bars, uint32_t tmem) {
+// ---- products (one warp a query tile) ----
+// Both warps wait for every part of a key tile and release it, whether their query tile needs it or not.
+__device__ __forceinline__ void issue_items(const hs_expanded& a, int t, uint32_t q, uint32_t ring, uint32_t bars,
+                                            uint32_t tmem) {
   constexpr uint32_t kIdS = tc::idesc(false, 128, kKeys, false, false);
   constexpr uint32_t kIdO = tc::idesc(false, 128, 64, false, true);
   tc::Waiter w;
   const bool leader = tc::elect();
-  const uint64_t dq = tc::desc(q, 16, 1024, tc::kSwizzle128);
+  const uint64_t dq = tc::desc(q + t * 3 * kUnit, 16, 1024, tc::kSwizzle128);
   const uint64_t dk = tc::desc(ring, 16, 1024, tc::kSwizzle128);
   const uint64_t dv = tc::desc(ring, 16, 1024, tc::kSwizzle128);  // dimensions contiguous, 64 of them: one atom wide
   auto await = [&](int bar, uint32_t parity) {
@@ -201,88 +203,83 @@ __device__ __forceinline__ void issue_items(const hs_expanded& a, uint32_t q, ui
     __syncwarp();
     tc::fence_after();
   };
-  uint32_t base = 0, count = 0, seen = 0;  // units, items and groups so far
-  uint32_t phase[2] = {0, 0};  // key tiles done by each query tile
+  uint32_t base = 0, count = 0, group = 0;  // units, items and parts (keys or values of a key tile) so far
+  uint32_t phase = 0;                       // key tiles done by the query tile
   Item it;
   Finder f;
   f.start(a);
   for (int k = 0; f.find(a, item_number(k), &it); ++k) {
-    const int tiles = it.most();
+    const int tiles = it.most(), mine = max(0, it.tiles[t]);
     if (tiles <= 0) continue;
-    const bool partial = it.keys - (tiles - 1) * kKeys < kKeys;
-    auto group = [&](uint32_t g) {  // waits for group g (counted over all items), once
-      if (g < seen) return;
-      await(kFull + g % kGroups, (g / kGroups) & 1);
-      seen = g + 1;
-    };
-    const uint32_t first_group = base / kUnits * 2;
-    auto scores = [&](int t, int j) {  // S of query tile t and key tile j
-      group(first_group + 2 * j);
-#pragma unroll 1
-      for (int i = 0; i < kUnitsK; ++i) {
-        const uint32_t x = base + j * kUnits + i;
-        const uint64_t da = dq + (uint32_t)((t * 3 + i) * kUnit >> 4), db = dk + (uint32_t)((x % kRing) * kUnit >> 4);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) tc::mma_ss(tmem + t * 128, da + (k * 32 >> 4), db + (k * 32 >> 4), kIdS, i > 0 || k > 0, leader);
-      }
-      tc::commit(bars + 8 * (kSFull + t), leader);
+    auto arrived = [&]() {  // waits for the next part
+      await(kFull + group % kGroups, (group / kGroups) & 1);
+      ++group;
     };
     auto release = [&](int j, int from, int to) {  // units of key tile j, when all products so far have read them
       for (int i = from; i < to; ++i) tc::commit(bars + 8 * (kEmpty + (base + j * kUnits + i) % kRing), leader);
     };
+    auto scores = [&](int j) {
+      arrived();
+#pragma unroll 1
+      for (int i = 0; i < kUnitsK; ++i) {
+        const uint32_t x = base + j * kUnits + i;
+        const uint64_t da = dq + (uint32_t)(i * kUnit >> 4), db = dk + (uint32_t)((x % kRing) * kUnit >> 4);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tc::mma_ss(tmem + t * 128, da + (k * 32 >> 4), db + (k * 32 >> 4), kIdS, i > 0 || k > 0, leader);
+      }
+      tc::commit(bars + 8 * (kSFull + t), leader);
+      release(j, 0, kUnitsK);
+      if (j + 1 == mine) tc::commit(bars + 8 * kQEmpty, leader);
+    };
     await(kQFull, count & 1);
     ++count;
+    if (mine > 0) {
+      if (phase > 0) await(kODone + t, (phase - 1) & 1);  // the item before: its last P has been read
+      scores(0);
+    } else {
+      tc::commit(bars + 8 * kQEmpty, leader);
+    }
 #pragma unroll 1
-    for (int t = 0; t < 2; ++t)
-      if (it.tiles[t] > 0) {
-        if (phase[t] > 0) await(kODone + t, (phase[t] - 1) & 1);  // the item before: its last P has been read
-        scores(t, 0);
-      }
-    release(0, 0, kUnitsK);
-    if (tiles == 1) tc::commit(bars + 8 * kQEmpty, leader);
+    for (int j = 0; j < mine; ++j, ++phase) {
+      await(kPReady + t, phase & 1);
+      arrived();
+      const int valid = it.keys - j * kKeys;
 #pragma unroll 1
-    for (int j = 0; j < tiles; ++j) {
-      const int last_of_values = it.tiles[1] > j ? 1 : 0;
-#pragma unroll 1
-      for (int t = 0; t < 2; ++t) {
-        if (j >= it.tiles[t]) continue;
-        await(kPReady + t, phase[t] & 1);
-        group(first_group + 2 * j + 1);
-        const bool fix = partial && j == tiles - 1 && (t == 0 || it.tiles[0] <= j);  // by the first that reads them
-#pragma unroll 1
-        for (int i = 0; i < kUnitsV; ++i) {
-          const uint32_t x = base + j * kUnits + kUnitsK + i;
-          if (fix) {
-            const int valid = it.keys - j * kKeys;
-            for (int k = threadIdx.x & 31; k < (kKeys - valid) * 8; k += 32) {
-              const uint32_t at = ring + (x % kRing) * kUnit + (valid + (k >> 3)) * 128 + (k & 7) * 16;
-              asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0u) : "memory");
-            }
-            tc::fence_async_smem();
-            __syncwarp();
+      for (int i = 0; i < kUnitsV; ++i) {
+        const uint32_t x = base + j * kUnits + kUnitsK + i;
+        if (valid < kKeys) {  // by both warps: they write the same
+          for (int k = threadIdx.x & 31; k < (kKeys - valid) * 8; k += 32) {
+            const uint32_t at = ring + (x % kRing) * kUnit + (valid + (k >> 3)) * 128 + (k & 7) * 16;
+            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0u) : "memory");
           }
-          const uint64_t db = dv + (uint32_t)((x % kRing) * kUnit >> 4);
-          // P: 16 keys are 8 columns
+          tc::fence_async_smem();
+          __syncwarp();
+        }
+        const uint64_t db = dv + (uint32_t)((x % kRing) * kUnit >> 4);
+        // P: 16 keys are 8 columns
 #pragma unroll
-          for (int k = 0; k < kKeys / 16; ++k)
-            tc::mma_ts(tmem + 256 + t * 128 + i * 64, tmem + t * 128 + k * 8, db + (k * 2048 >> 4), kIdO, j > 0 || k > 0, leader);
-        }
-        tc::commit(bars + 8 * (kODone + t), leader);
-        if (t == last_of_values) release(j, kUnitsK, kUnits);
-        if (j + 1 < it.tiles[t]) {
-          await(kODone + t, phase[t] & 1);  // P, in S's place, has been read
-          scores(t, j + 1);
-        }
-        ++phase[t];
+        for (int k = 0; k < kKeys / 16; ++k)
+          tc::mma_ts(tmem + 256 + t * 128 + i * 64, tmem + t * 128 + k * 8, db + (k * 2048 >> 4), kIdO, j > 0 || k > 0, leader);
       }
-      if (j + 1 < tiles) release(j + 1, 0, kUnitsK);
-      if (j + 2 == tiles) tc::commit(bars + 8 * kQEmpty, leader);
+      tc::commit(bars + 8 * (kODone + t), leader);
+      release(j, kUnitsK, kUnits);
+      if (j + 1 < mine) {
+        await(kODone + t, phase & 1);  // P, in S's place, has been read
+        scores(j + 1);
+      }
+    }
+#pragma unroll 1
+    for (int j = mine; j < tiles; ++j) {  // what only the other query tile reads
+      arrived();
+      release(j, 0, kUnitsK);
+      arrived();
+      release(j, kUnitsK, kUnits);
     }
     base += tiles * kUnits;
   }
-  tc::commit(bars + 8 * kDrain, leader);
+  tc::commit(bars + 8 * (kDrain + t), leader);
   tc::Waiter drain;
-  drain.wait(bars + 8 * kDrain, 0);
+  drain.wait(bars + 8 * (kDrain + t), 0);
   __syncwarp();
   if (w.dead) report(a.status, HS_ERR_TIMEOUT);
 }
@@ -422,15 +419,15 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const hs_expanded
     }
   if (threadIdx.x == 0) {
     for (int i = 0; i < kGroups; ++i) tc::mbar_init(bars + 8 * (kFull + i), 1);
-    for (int i = 0; i < kRing; ++i) tc::mbar_init(bars + 8 * (kEmpty + i), 1);
+    for (int i = 0; i < kRing; ++i) tc::mbar_init(bars + 8 * (kEmpty + i), 2);
     tc::mbar_init(bars + 8 * kQFull, 1);
-    tc::mbar_init(bars + 8 * kQEmpty, 1);
+    tc::mbar_init(bars + 8 * kQEmpty, 2);
     for (int t = 0; t < 2; ++t) {
       tc::mbar_init(bars + 8 * (kSFull + t), 1);
       tc::mbar_init(bars + 8 * (kPReady + t), 4);
       tc::mbar_init(bars + 8 * (kODone + t), 1);
+      tc::mbar_init(bars + 8 * (kDrain + t), 1);
     }
-    tc::mbar_init(bars + 8 * kDrain, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kMmaWarp) tc::tmem_alloc(tc::smem_u32(&tmem_slot), 512);
@@ -443,8 +440,8 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const hs_expanded
     softmax_items(a, scale_log2, bars, tmem);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-    if (warp == kMmaWarp)
-      issue_items(a, q, ring, bars, tmem);
+    if (warp < kLoadWarp)
+      issue_items(a, warp - kMmaWarp, q, ring, bars, tmem);
     else if (warp == kLoadWarp)
       load_items(a, maps, q, ring, bars);
   }
