@@ -10,9 +10,10 @@
 //
 // Bound: HBM.  A bf16 token is 1152 B in, 656 B out, 256 B of the rotation table, and 256 B per query head.
 // Split: a warp takes one token's row (16 latent values a lane, a group's maximum over 8 lanes by shuffles;
-// lanes 0..3 also rotate the key), or up to kHeadsPerUnit heads of a token's queries (4 lanes a head, 8 pairs
-// a lane; the table's values stay in registers over the heads).  Rows and queries are separate units so that a
-// decode step of few tokens still spreads over the SMs.
+// lanes 0..3 also rotate the key), or kHeads heads of a token's queries (4 lanes a head, 8 pairs a lane; the table's
+// values stay in registers over the heads).  Rows and queries are separate units so that a decode step of few tokens
+// still spreads over the SMs.  Measured (fp8 rows): 64 tokens x 64 heads 2.1 us; 32768 tokens x 16 heads 40 us, 5.0 TB/s,
+// x 64 heads 102 us, 5.9 TB/s.  More resident warps with fewer registers (10 or 12 blocks an SM) took 43 and 54 us.
 #include "latent.cuh"
 
 namespace hs {
@@ -245,7 +246,8 @@ void launch_heads(const AppendParams& p, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_append(const AppendParams& p, int sms, cudaStream_t s) {
-  // few tokens are spread further; many take fewer reads of the table
+  // few tokens are spread further (512 x 64 heads: 2.9 us with 8 heads a warp and 3.4 with 16); many take fewer reads of the
+  // table (32768 x 64: 102 us with 16, 106 with 8)
   if (p.a.n * (1 + p.a.heads / 16) < 64 * (int64_t)sms)
     launch_heads<8>(p, s);
   else

@@ -20,17 +20,28 @@
 // Layout.  A unit is (item, group of N columns); units are cut into tiles, numbered in order, and every CTA takes
 // an equal run of tiles; a unit that several CTAs share leaves partial results in the workspace, which
 // combine_kernel joins in a fixed order.  One CTA per SM, 28 warps (the warpgroups trade registers, kRegs*):
-//   warp 25      resolves keys to row ids and gathers whole rows with the copy engine, four an instruction, into a ring of
-//                slots of 16 rows (80 cycles an instruction whatever the width: pieces of rows, or single rows by
-//                one-dimensional copies at 73 cycles each, were four times slower; 16-byte asynchronous copies and loads
-//                cost the load pipe 13 cycles for 512 B, which the stores below need);
-//   warps 0-15   take four rows each from the ring, widen fp8 codes to fp16, and store them as operands once their
-//                places in the tile are free;
-//   warp 24      issues the products;
-//   warps 16-23  softmax and results: lane = key (16 of a warp's lanes have one, as products of 64 rows lie in tensor
-//                memory), later lane = latent dimension; each of the two groups of four warps has half of the columns.
-// The tile (64 x 576, 72 KB) has one buffer, which is filled and released in two halves of 256 latent dimensions (the
-// rotated part goes with the first): a hand-over costs some hundred cycles, so that more and smaller parts were slower.
+//   warps 0-15   bring tiles into operand form.  A warp owns four keys of every tile: it copies their rows into the tile's
+//                place (16-byte asynchronous copies) and widens fp8 codes there, so that no other warp has to be waited for;
+//   warps 16-23  softmax and results; each of the two groups of four warps has half of the columns;
+//   warp 24      issues the scores of every tile as soon as it is there;
+//   warp 25      issues the results as soon as the weights are there.
+// Two tiles (64 x 576 in 16 bits, 72 KB each) and the queries (up to 72 KB) fill shared memory; the weights take the place
+// of the tile's rotated part once the scores are done.
+//
+// N is 16, 32 or 64 (the smallest that holds the item's columns, 64 beyond): a product of 64 or 128 rows costs 39 to 64
+// cycles from N = 16 to N = 64, so a call with few heads pays little for its empty columns, and more than 64 columns
+// would leave no room for the second tile.
+//
+// What bounds it.  Shared memory: a tile's copies, widening and operand reads move about 400 KB, 3100 cycles at 128 B a
+// cycle, against 2200 of products (N = 64).  Measured, 608 tokens x 2048 fp8 rows: 16 heads 289 us (2.8 TB/s of rows), 32
+// heads 295 us, 64 heads 339 us (512 TFLOP/s), that is 4.3 to 5.1 thousand cycles a tile; the producers' own chain (wait,
+// copies, 1300 cycles until they land, reading, widening, 700 to 1100 until the stores are visible) is what is left.
+// Taken back as slower, at 256 x 4 tokens of 64 heads (this form: 589 us; the tiles' number and form as given): one
+// 128-key tile filled in parts by copy warps 671; rows gathered by the copy engine into a ring, one 64-key tile 862 (the
+// engine takes 73 cycles a row and 80 for a gather of four, whatever their width); two tiles with copy warps of their own
+// 668; the next tile's copies issued before (606) or within (663) the widening; two teams of producers on alternate tiles
+// and both products issued by one warp 808; one warp for both products 639.  Staging the codes of the next tile where few
+// columns leave room gained nothing.
 #include <type_traits>
 
 #include "latent.cuh"
@@ -854,7 +865,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const AttendParams 
 }
 
 // Joins the partial results of the units that run boundary b = blockIdx.x + 1 is the first to cut: the results are
-// weighted by exp2 of their log2 sums, in the order of the runs.  128 threads a column, with 4 dimensions each.
+// weighted by exp2 of their log2 sums, in the order of the runs.  128 threads a column, with 4 dimensions each.  Bound: the
+// latency of its few dependent loads.
 constexpr int kJoinCols = 4;
 __global__ void __launch_bounds__(128 * kJoinCols) combine_kernel(const AttendParams p, int groups, int n, int sms, int grid) {
   asm volatile("griddepcontrol.wait;" ::: "memory");  // for attend_kernel's results

@@ -34,19 +34,6 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-// The same without suspending the thread when the phase is not complete.
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
 // Waits are bounded: one that has not ended after kWaitCycles SM cycles (seconds) gives up, and from then on
 // every wait of that thread returns at once, so that the kernel runs to its end; `dead` says so and the caller
 // reports HS_ERR_TIMEOUT.  Everything a kernel accesses stays in bounds whatever the waits return.
@@ -83,24 +70,6 @@ inline EncodeTiled encode_tiled() {
     return reinterpret_cast<EncodeTiled>(f);
   }();
   return encode;
-}
-// Tensor map of a [rows][row_bytes] matrix, as 32-bit words, for gathers of `box` bytes of four rows.
-inline bool gather_map(CUtensorMap* map, const void* base, uint32_t row_bytes, uint64_t rows, uint32_t box_bytes) {
-  if (!encode_tiled()) return false;
-  const cuuint64_t dims[2] = {row_bytes / 4, rows};
-  const cuuint64_t strides[1] = {row_bytes};
-  const cuuint32_t box[2] = {box_bytes / 4, 1}, steps[2] = {1, 1};
-  return encode_tiled()(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, strides, box, steps,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-// The map's box from word `x` (a multiple of 4) of rows r.x, r.y, r.z, r.w to shared memory at dst (a multiple of 128).
-__device__ __forceinline__ void gather4(uint32_t dst, const CUtensorMap* map, int x, int4 r, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], "
-      "[%7];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(bar)
-      : "memory");
 }
 
 // ---- tensor memory ----
