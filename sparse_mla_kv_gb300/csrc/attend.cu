@@ -40,8 +40,9 @@
 // 128-key tile filled in parts by copy warps 671; rows gathered by the copy engine into a ring, one 64-key tile 862 (the
 // engine takes 73 cycles a row and 80 for a gather of four, whatever their width); two tiles with copy warps of their own
 // 668; the next tile's copies issued before (606) or within (663) the widening; two teams of producers on alternate tiles
-// and both products issued by one warp 808; one warp for both products 639.  Staging the codes of the next tile where few
-// columns leave room gained nothing.
+// and both products issued by one warp 808; one warp for both products 639.  Where few columns leave room, staging the codes
+// of the next tile gained nothing, and loading them to registers a tile ahead took 291 us at 16 heads, 377 at 32 and 624 at
+// 64 (608 tokens, as above): what is in flight towards registers needs L1, which the tiles leave little of.
 #include <type_traits>
 
 #include "latent.cuh"
