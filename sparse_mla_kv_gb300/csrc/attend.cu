@@ -78,6 +78,7 @@ struct Range {
 // Workspace: partial results [2 per CTA][kMaxCols][512], their log2 sums [2 per CTA][kMaxCols], run starts [CTA].
 struct RunStart {
   int64_t total;        // tiles of the call
+  int64_t begin;        // number of the run's first tile
   int32_t item, off;    // first tile: item and tile number within it
   int32_t tiles, pad;   // tiles of one unit of the item
 };
@@ -758,7 +759,11 @@ __device__ int64_t block_scan(int64_t v, int64_t* total, int64_t* scratch) {
   return before + x - v;
 }
 
-__host__ __device__ __forceinline__ int64_t run_begin(int64_t total, int ctas, int b) { return total * b / ctas; }
+// total * b / ctas (ctas is a few hundred, and a 64-bit division some hundred instructions)
+__device__ __forceinline__ int64_t run_begin(int64_t total, int ctas, int b) {
+  const int64_t q = total >> 32 ? total / ctas : (int64_t)((uint32_t)total / (uint32_t)ctas);
+  return q * b + (int)(total - q * ctas) * b / ctas;
+}
 
 template <int N, int kRowBytes>
 __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const AttendParams p, int groups, int sms) {
@@ -787,7 +792,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const AttendParams 
       run = run_begin(total, ctas, blockIdx.x + 1) - begin;
       if (threadIdx.x == 0) {
         const int per_item = groups * tiles;
-        start = RunStart{total, (int)(begin / per_item), (int)(begin % per_item), tiles, 0};
+        const int item = begin >> 32 ? (int)(begin / per_item) : (int)((uint32_t)begin / (uint32_t)per_item);
+        start = RunStart{total, begin, item, (int)(begin - (int64_t)item * per_item), tiles, 0};
       }
     }
   } else {
@@ -809,7 +815,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const AttendParams 
         const int tiles = i < p.items ? tiles_of(item_keys(p, i)) : 0;
         int64_t all;
         const int64_t at = passed + block_scan((int64_t)tiles * groups, &all, scratch);
-        if (begin >= at && begin < at + (int64_t)tiles * groups) start = RunStart{total, i, (int)(begin - at), tiles, 0};
+        if (begin >= at && begin < at + (int64_t)tiles * groups) start = RunStart{total, begin, i, (int)(begin - at), tiles, 0};
         passed += all;
         if (begin < passed) break;
       }
@@ -876,17 +882,19 @@ __global__ void __launch_bounds__(128 * kJoinCols) combine_kernel(const AttendPa
   const float* lse = reinterpret_cast<const float*>(ws + ws_lse_offset(sms));
   const int b = blockIdx.x + 1;
   const int64_t total = runs[0].total;
-  const RunStart r = runs[min(b, grid - 1)];  // (there may be fewer runs than CTAs: what is read past them is not used)
   const int ctas = (int)min((int64_t)grid, total);
   if (b >= ctas) return;
+  const RunStart r = runs[b];
+  const int64_t before = runs[b - 1].begin;
   const int group = r.off / r.tiles, tile = r.off - group * r.tiles;
   if (tile == 0) return;
-  const int64_t unit0 = run_begin(total, ctas, b) - tile, unit1 = unit0 + r.tiles;
-  if (run_begin(total, ctas, b - 1) > unit0) return;  // an earlier boundary cuts this unit
+  const int64_t unit0 = r.begin - tile, unit1 = unit0 + r.tiles;
+  if (before > unit0) return;  // an earlier boundary cuts this unit
+  // runs b - 1 .. last hold parts of it
+  const int next = b + 1 + threadIdx.x;
+  const int last = b + __syncthreads_count(next < ctas && runs[next].begin < unit1);
   const int c = blockIdx.y * kJoinCols + threadIdx.x / 128, d = threadIdx.x % 128;
   if (c >= min(n, p.cols - group * n)) return;
-  int last = b;  // runs b - 1 .. last hold parts of it
-  while (last + 1 < ctas && run_begin(total, ctas, last + 1) < unit1) ++last;
   float top = -INFINITY, sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int i0 = b - 1; i0 <= last; i0 += 4) {  // four parts at a time
@@ -936,7 +944,7 @@ cudaError_t launch(const AttendParams& p, int sms, cudaStream_t s) {
   if (ready != cudaSuccess) return ready;
   const int groups = (p.cols + N - 1) / N;
   // a rows call knows its tiles; a pages call learns them on the device
-  int grid = sms;
+  int grid = min(sms, 128 * kJoinCols);  // (a thread of combine_kernel for each)
   bool cut = true;  // whether a unit may be shared by CTAs
   if (!p.paged) {
     const int64_t tiles = p.K > 0 ? (p.K + kTile - 1) / kTile : 1;
