@@ -8,14 +8,14 @@
 // V is the latent part of K: the same bytes, once read as a K-major and once as an M-major operand.  The softmax
 // is online with a lazy reference: weights are exp2(t), t = s - m, with any m that keeps them in range, since fp32 sums
 // have the same relative precision at every magnitude.  m starts kTop below the first tile's maximum and moves (with O
-// and the sums rescaled) only when a score exceeds it by kLazy, so the maximum over 128 lanes is rarely needed.  Sums
-// are kept per key lane and joined once per unit.
+// and the sums rescaled) only when a score exceeds it by kLazy, so the maximum over a tile's keys is rarely needed.  Sums
+// are kept per thread and joined once per unit.
 //
 // Types.  bf16 rows: both products in bf16.  fp8 rows: both in fp16, because an e4m3 code becomes fp16 in one
 // instruction for two and fp16's 11 bits hold it exactly, while its range is narrow; so every factor is brought into
 // range by a power of two, which costs no precision: a key's row by skey (its values are code * scale / skey, its rotated
 // part divided by it too), a query column by qs, and the weights by skey / skey0 on their way to the second product,
-// where skey0 is the largest skey of the unit so far.  Then S = S' skey qs, and O = O' skey0.
+// where skey0 is the unit's largest skey when it was last set.  Then S = S' skey qs, and O = O' skey0.
 //
 // Layout.  A unit is (item, group of N columns); units are cut into tiles, numbered in order, and every CTA takes
 // an equal run of tiles; a unit that several CTAs share leaves partial results in the workspace, which
@@ -36,15 +36,13 @@
 // cycle, against 2200 of products (N = 64).  Measured, 608 tokens x 2048 fp8 rows: 16 heads 289 us (2.8 TB/s of rows), 32
 // heads 295 us, 64 heads 339 us (512 TFLOP/s), that is 4.3 to 5.1 thousand cycles a tile; the producers' own chain (wait,
 // copies, 1300 cycles until they land, reading, widening, 700 to 1100 until the stores are visible) is what is left.
-// Taken back as slower, at 256 x 4 tokens of 64 heads (this form: 589 us; the tiles' number and form as given): one
+// Taken back as slower, at 256 x 4 tokens of 64 heads (this form: 590 us; the tiles' number and form as given): one
 // 128-key tile filled in parts by copy warps 671; rows gathered by the copy engine into a ring, one 64-key tile 862 (the
 // engine takes 73 cycles a row and 80 for a gather of four, whatever their width); two tiles with copy warps of their own
 // 668; the next tile's copies issued before (606) or within (663) the widening; two teams of producers on alternate tiles
 // and both products issued by one warp 808; one warp for both products 639.  Where few columns leave room, staging the codes
 // of the next tile gained nothing, and loading them to registers a tile ahead took 291 us at 16 heads, 377 at 32 and 624 at
 // 64 (608 tokens, as above): what is in flight towards registers needs L1, which the tiles leave little of.
-#include <type_traits>
-
 #include "latent.cuh"
 #include "tc.cuh"
 

@@ -17,7 +17,7 @@
 // of keys, then two of values.  Tensor memory: S and O of both tiles, 4 x 128 columns; P, in bf16, takes S's place and is
 // the left operand of the second product from there.
 // Bound: the tensor pipe, 12 x 64 + 8 x 64 cycles for 128 queries x 128 keys.  Measured: 16384 causal tokens x 8 heads
-// 493 us, 1.39 PFLOP/s (0.72 of measured), about 4.3 thousand cycles for a pair of such tiles, the items' ends included,
+// 490 us, 1.40 PFLOP/s (0.73 of a measured library product), about 4.3 thousand cycles for a pair of such tiles, the items' ends included,
 // against 2.6 of products.  What is left is each query tile's own chain (scores, their weights, results, scores of the
 // next key tile into the same place): tensor memory holds no second S.  Results begun when half of the weights are there
 // took 511 us (the two tiles' products then interleave in smaller pieces), and one warp issuing for both query tiles 522 us.

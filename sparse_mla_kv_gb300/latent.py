@@ -88,6 +88,15 @@ def _on(stream, t: torch.Tensor):
     return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
+def _empty(shape: tuple, dtype, device, stream) -> torch.Tensor:
+    """An output or workspace made here belongs to the stream that the call launches on: memory of another stream could
+    still be in use there, or be handed out again before this call's kernels are done with it."""
+    if isinstance(stream, torch.cuda.Stream):
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=device)
+    return torch.empty(shape, dtype=dtype, device=device)
+
+
 def append_rows(pool: Pool, rows: torch.Tensor, latent: torch.Tensor, rope: torch.Tensor, positions: torch.Tensor,
                 rotation: torch.Tensor, *, layer: int = 0, q_rope: Optional[torch.Tensor] = None,
                 q_out: Optional[torch.Tensor] = None, interleaved: bool = False,
@@ -113,7 +122,7 @@ def append_rows(pool: Pool, rows: torch.Tensor, latent: torch.Tensor, rope: torc
         st = _tensor(q_rope, "q_rope", (n, heads, ROPE_DIM), dtype)
         q = (q_rope.data_ptr(), st[0], st[1])
         if q_out is None:
-            q_out = torch.empty((n, heads, ROPE_DIM), dtype=dtype, device=q_rope.device)
+            q_out = _empty((n, heads, ROPE_DIM), dtype, q_rope.device, stream)
         st = _tensor(q_out, "q_out", (n, heads, ROPE_DIM), dtype)
         qo = (q_out.data_ptr(), st[0], st[1])
     elif q_out is not None:
@@ -136,7 +145,7 @@ def alloc_attend_workspace(device="cuda") -> torch.Tensor:
         return torch.empty(max(16, attend_workspace_bytes()), dtype=torch.uint8, device=device)
 
 
-def _attend(lead: tuple, q_latent, q_rope, scale, out, lse, status, workspace):
+def _attend(lead: tuple, q_latent, q_rope, scale, out, lse, status, workspace, stream):
     """Marshals an absorbed call whose query tensors have the leading dimensions `lead` (tokens) and heads."""
     k = len(lead)
     heads = q_latent.shape[k] if q_latent.dim() == k + 2 else -1
@@ -144,12 +153,12 @@ def _attend(lead: tuple, q_latent, q_rope, scale, out, lse, status, workspace):
     sl = _tensor(q_latent, "q_latent", shape)
     sr = _tensor(q_rope, "q_rope", (*lead, heads, ROPE_DIM))
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=device)
+        out = _empty(shape, torch.bfloat16, device, stream)
     so = _tensor(out, "out", shape)
     if lse is None:
-        lse = torch.empty((*lead, heads), dtype=torch.float32, device=device)
+        lse = _empty((*lead, heads), torch.float32, device, stream)
     if workspace is None:
-        workspace = alloc_attend_workspace(device)
+        workspace = _empty((max(16, attend_workspace_bytes()),), torch.uint8, device, stream)
     if workspace.dtype is not torch.uint8 or not workspace.is_cuda or not workspace.is_contiguous():
         raise TypeError("workspace must be a contiguous uint8 CUDA tensor")
     token = (sl[0], sr[0], so[0])
@@ -170,7 +179,7 @@ def attend_rows(pool: Pool, rows: torch.Tensor, q_latent: torch.Tensor, q_rope: 
     if rows.dim() != 2:
         raise ValueError("rows must be [tokens][K]")
     n, K = rows.shape
-    a, out, lse, ws = _attend((n,), q_latent, q_rope, scale, out, lse, status, workspace)
+    a, out, lse, ws = _attend((n,), q_latent, q_rope, scale, out, lse, status, workspace, stream)
     _check(_lib().hs_attend_rows(pool.handle, int(layer), _dev_i32(rows, "rows"), n, K, ctypes.byref(a),
                                  ws.data_ptr(), ws.numel(), _on(stream, q_latent)), "hs_attend_rows")
     return out, lse
@@ -188,7 +197,7 @@ def attend_pages(pool: Pool, block_table: torch.Tensor, ctx_len: torch.Tensor, q
     R, P = int(q_latent.shape[0]), int(q_latent.shape[1])
     if block_table.shape[0] != R or ctx_len.numel() != R:
         raise ValueError("block_table and ctx_len must have one entry per request")
-    a, out, lse, ws = _attend((R, P), q_latent, q_rope, scale, out, lse, status, workspace)
+    a, out, lse, ws = _attend((R, P), q_latent, q_rope, scale, out, lse, status, workspace, stream)
     _check(_lib().hs_attend_pages(pool.handle, int(layer), _dev_i32(block_table, "block_table"),
                                   _dev_i32(ctx_len, "ctx_len"), R, P, int(block_table.shape[1]), ctypes.byref(a),
                                   ws.data_ptr(), ws.numel(), _on(stream, q_latent)), "hs_attend_pages")
@@ -214,10 +223,10 @@ def attend_expanded(q_nope: torch.Tensor, q_rope: torch.Tensor, k_nope: torch.Te
     if cu_q.numel() < 1 or cu_q.numel() != cu_k.numel():
         raise ValueError("cu_q and cu_k must both have one entry more than there are sequences")
     if out is None:
-        out = torch.empty((Tq, H, VALUE_DIM), dtype=torch.bfloat16, device=q_nope.device)
+        out = _empty((Tq, H, VALUE_DIM), torch.bfloat16, q_nope.device, stream)
     so = _tensor(out, "out", (Tq, H, VALUE_DIM))
     if lse is None:
-        lse = torch.empty((Tq, H), dtype=torch.float32, device=q_nope.device)
+        lse = _empty((Tq, H), torch.float32, q_nope.device, stream)
     a = ExpandedC(cu_q.numel() - 1, H, bool(causal), scale, Tq, Tk, _dev_i32(cu_q, "cu_q"), _dev_i32(cu_k, "cu_k"),
                   q_nope.data_ptr(), sqn[0], sqn[1], q_rope.data_ptr(), sqr[0], sqr[1], k_nope.data_ptr(), skn[0], skn[1],
                   k_rope.data_ptr(), skr[0], v.data_ptr(), sv[0], sv[1], out.data_ptr(), so[0], so[1],

@@ -140,3 +140,26 @@ def test_more_refusals():
     out = torch.empty((1, 513, 1024, D), dtype=torch.bfloat16, device="cuda")
     refused(hs.attend_pages, pool, one.reshape(1, 1).expand(1, 2 ** 18).contiguous(), one, q9, r9, SCALE, out=out)
     assert hs.launch_count() == before
+
+
+def test_own_buffers_on_another_stream():
+    """Outputs and workspaces made by calls on a side stream: many in flight, while the current stream keeps allocating,
+    writing and freeing memory of the same sizes."""
+    g = gen(21)
+    pool, tensors = base.make_pool(g, 16, "fp8")
+    n, K, H = 32, 500, 16
+    rows = torch.randint(0, 1024, (n, K), generator=g, device="cuda").int()
+    ql, qr = normal(g, n, H, D), normal(g, n, H, RD)
+    want = hs.attend_rows(pool, rows, ql, qr, SCALE)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got, held = [], []
+    for _ in range(20):
+        got.append(hs.attend_rows(pool, rows, ql, qr, SCALE, stream=side))
+        churn = [torch.full_like(want[0], 7.0), torch.full_like(want[1], 7.0),
+                 torch.full((hs.alloc_attend_workspace().numel(),), 255, dtype=torch.uint8, device="cuda")]
+        held.append(churn[0].clone())
+        del churn
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[0]) and torch.equal(x, want[1]) for o, x in got)
+    assert all(bool((x == 7).all()) for x in held)
