@@ -20,7 +20,8 @@
 // 490 us, 1.40 PFLOP/s (0.73 of a measured library product), about 4.3 thousand cycles for a pair of such tiles, the items' ends included,
 // against 2.6 of products.  What is left is each query tile's own chain (scores, their weights, results, scores of the
 // next key tile into the same place): tensor memory holds no second S.  Results begun when half of the weights are there
-// took 511 us (the two tiles' products then interleave in smaller pieces), and one warp issuing for both query tiles 522 us.
+// took 511 us (the two tiles' products then interleave in smaller pieces), one warp issuing for both query tiles 522 us, and
+// two threads a row 897 us (16 softmax warps leave each thread too few registers for its half of a row).
 #include "latent.cuh"
 #include "tc.cuh"
 
