@@ -36,7 +36,7 @@
 // cycle, against 2200 of products (N = 64).  Measured, 608 tokens x 2048 fp8 rows: 16 heads 289 us (2.8 TB/s of rows), 32
 // heads 295 us, 64 heads 339 us (512 TFLOP/s), that is 4.3 to 5.1 thousand cycles a tile; the producers' own chain (wait,
 // copies, 1300 cycles until they land, reading, widening, 700 to 1100 until the stores are visible) is what is left.
-// Taken back as slower, at 256 x 4 tokens of 64 heads (this form: 590 us; the tiles' number and form as given): one
+// Taken back as slower, at 256 x 4 tokens of 64 heads (this form: 580 to 594 us; the tiles' number and form as given): one
 // 128-key tile filled in parts by copy warps 671; rows gathered by the copy engine into a ring, one 64-key tile 862 (the
 // engine takes 73 cycles a row and 80 for a gather of four, whatever their width); two tiles with copy warps of their own
 // 668; the next tile's copies issued before (606) or within (663) the widening; two teams of producers on alternate tiles
