@@ -11,11 +11,18 @@
 // and the sums rescaled) only when a score exceeds it by kLazy, so the maximum over a tile's keys is rarely needed.  Sums
 // are kept per thread and joined once per unit.
 //
-// Types.  bf16 rows: both products in bf16.  fp8 rows: both in fp16, because an e4m3 code becomes fp16 in one
-// instruction for two and fp16's 11 bits hold it exactly, while its range is narrow; so every factor is brought into
-// range by a power of two, which costs no precision: a key's row by skey (its values are code * scale / skey, its rotated
-// part divided by it too), a query column by qs, and the weights by skey / skey0 on their way to the second product,
-// where skey0 is the unit's largest skey when it was last set.  Then S = S' skey qs, and O = O' skey0.
+// Types.  bf16 rows: both products in bf16 (the two operands of one product have the same type, and bf16 values have
+// fp32's range), so the weights are rounded to 8 bits: 2e-3 of the largest result instead of 1.7e-3 in 32 bits.  fp8 rows:
+// both in fp16, because an e4m3 code becomes fp16 in one instruction for two and fp16's 11 bits hold it exactly, while its
+// range is narrow: 2^-24 (with full precision 2^-14) to 2^16.  So every factor is brought into range by a power of two: a
+// row by skey (its values are code * scale / skey, its rotated part divided by it too), a query column by qs; S = S' skey
+// qs.  A key's row enters the result as its weight times skey, so what is rounded to fp16 is that product: t below is the
+// score in log2 units plus log2 skey, and the reference m follows the largest t.  A large row then counts by its share of
+// the result, and not at all where it has no weight.  The sum of the weights takes exp2(t - m) / skey in fp32; its common
+// factor 2^m cancels in the result, and the log of the sum adds m again.
+// What fp16's range costs: within a row, bits of what is below 2^-14 skey, that is 2^-29 of the largest value that skey
+// covers (a code of 448, or the rotated part where that is larger), and all of what is below 2^-25 skey; between rows, bits of
+// a weight times skey below 2^-21 of the largest.
 //
 // Layout.  A unit is (item, group of N columns); units are cut into tiles, numbered in order, and every CTA takes
 // an equal run of tiles; a unit that several CTAs share leaves partial results in the workspace, which
@@ -66,12 +73,19 @@ __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec
 constexpr int kSub = kTile * 128;    // bytes of a sub-tile: 64 keys x 64 values
 constexpr int kTileBytes = 9 * kSub;  // of which the ninth holds the rotated parts, and later the weights
 // In log2 units: where a new reference puts the largest score, and the most that a score may reach before it moves.
-// fp16 weights are normal from 2^-14 to 2^16, and a key's skey may be kGrow times skey0 before that moves; bf16 weights
-// have fp32's range.
+// fp16 weights are normal from 2^-14 to 2^16; bf16 weights have fp32's range.
 template <bool kF16>
 struct Range {
-  static constexpr float kTop = kF16 ? 4.f : 0.f, kLazy = kF16 ? 12.f : 64.f, kGrow = 8.f;
+  static constexpr float kTop = kF16 ? 7.f : 0.f, kLazy = kF16 ? 15.f : 64.f;
 };
+// skey of an fp8 row: 2^-112 .. 2^112, as the field of a float's exponent; at the ends, fp16 still holds all e4m3 codes of the
+// smallest normal scale and all values below 2^128.  A row whose latents are all zero has no size: it gets at least 2^-60,
+// small against the rows that have one, so that it does not draw the reference up, and large enough that its weight over
+// skey stays in fp32's range beside rows of up to 2^40.
+constexpr int kMinKey = 127 - 112, kMaxKey = 127 + 112, kZeroKey = 127 - 60;
+// The sums of fp8 rows' weights are 2^-kSumShift of what they stand for: with skey over its whole range, they stay within fp32's.
+constexpr int kSumShift = 14;
+static_assert(254 - kSumShift - kMaxKey >= 1, "2^-kSumShift / skey is a normal number");
 
 // Workspace: partial results [2 per CTA][kMaxCols][512], their log2 sums [2 per CTA][kMaxCols], run starts [CTA].
 struct RunStart {
@@ -150,12 +164,12 @@ struct Smem {
   static constexpr int kQ = kBufs * kTileBytes;
   static constexpr int kMisc = kQ + 9 * N * 128;
   // after the queries: barriers (128 B), scales of fp8 rows [tile][key][4], results' offsets [N] (64 bits), then floats:
-  // references, factors, limits, scalars [N] each, joined values [4][N], query scales [3][N], key scales [tile][64]
+  // references, factors, limits [N] each, joined values [4][N], query scales [3][N], key scales [tile][64]
   static constexpr int kScales = kMisc + 128;
   static constexpr int kOffsets = kScales + kBufs * kTile * 16;
   static constexpr int kRef = kOffsets + N * 8;
-  static constexpr int kQScale = 8 * N, kKeyScale = 11 * N;
-  static constexpr int kBytes = kRef + (11 * N + kBufs * kTile) * 4 + 1024;  // + alignment of the base
+  static constexpr int kQScale = 7 * N, kKeyScale = 10 * N;
+  static constexpr int kBytes = kRef + (10 * N + kBufs * kTile) * 4 + 1024;  // + alignment of the base
   static_assert(kBytes <= 232448, "shared memory");
 };
 enum Bar { kFull = 0, kEmpty = 2, kQFull = 4, kQEmpty = 5, kSFull = 6, kPReady = 8, kOFull = 10, kDrain, kBars = kDrain + 2 };
@@ -356,22 +370,46 @@ __device__ __forceinline__ void produce_tiles(const AttendParams& p, uint32_t ba
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();
     if constexpr (kF16) {
+      const uint32_t codes = tile + kSub + (4 * warp + half) * 128 + 8 * q;
       const uint4 rope = lds16(tile + 8 * kSub + key * 128 + 16 * j);
-      const float sc = lds_f(scales + 4 * (j & 3));  // lanes j and j + 4 of a key have its scale of group j
-      uint2 v[4][2];
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) v[c][i] = lds8(tile + (2 * c + 1) * kSub + (4 * warp + 2 * i + half) * 128 + 8 * q);
+      float sc = lds_f(scales + 4 * (j & 3));  // lanes j and j + 4 of a key have its scale of group j
       // skey: 2^7 below the power of two that covers the largest scale (codes reach 448 * 2^7 < 65504), and so that the
       // rotated part stays below 2^15
       const uint32_t sb = __float_as_uint(sc) & 0x7FFFFFFFu;
       const bool exact = __all_sync(0xFFFFFFFFu, (sb & 0x7FFFFFu) == 0);  // every scale is a power of two
-      int e = (int)(sb >> 23) + ((sb & 0x7FFFFFu) ? 1 : 0) - 7;
-      e = max(e, (int)(__float_as_uint(max_bf16x8(rope)) >> 23) + 1 - 15);
+      const int from_scale = (int)(sb >> 23) + ((sb & 0x7FFFFFu) ? 1 : 0) - 7;
+      const int from_rope = (int)(__float_as_uint(max_bf16x8(rope)) >> 23) + 1 - 15;
+      uint32_t both = (uint32_t)from_scale << 16 | ((uint32_t)from_rope & 0xFFFFu);  // two maxima at once
 #pragma unroll
-      for (int d = 1; d < 8; d <<= 1) e = max(e, __shfl_xor_sync(0xFFFFFFFFu, e, d));
-      e = min(max(e, 1), 240);
+      for (int d = 1; d < 8; d <<= 1) both = __vmaxs2(both, __shfl_xor_sync(0xFFFFFFFFu, both, d));
+      const int top_rope = (int16_t)both;
+      int e = max((int)both >> 16, top_rope), least = kMinKey;
+      // A group of zeros may have any scale, and has no size.  That is looked at only where a scale is far above the rotated
+      // part, or the row is very small: elsewhere it costs the row's other values or the other rows 8 bits of the range.
+      if (__any_sync(0xFFFFFFFFu, (int)both >> 16 > top_rope + 8 || e < kZeroKey)) {
+        uint32_t set = 0;  // groups of the warp's keys that have values other than zero: bit 4 (key - 4 warp) + group
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint2 x = lds8(codes + 2 * c * kSub + 256 * i);
+            if ((x.x | x.y) & 0x7F7F7F7Fu) set |= 1u << (8 * i + c);
+          }
+        set = __reduce_or_sync(0xFFFFFFFFu, set << (4 * half)) >> (4 * sub);
+        const bool empty = !(set >> (j & 3) & 1);
+        if (empty) sc = 0.f;
+        e = empty ? 0 : from_scale;
+#pragma unroll
+        for (int d = 1; d < 4; d <<= 1) e = max(e, __shfl_xor_sync(0xFFFFFFFFu, e, d));
+        e = max(e, top_rope);
+        if (!(set & 15)) least = kZeroKey;
+      }
+      e = min(max(e, least), kMaxKey);
+      uint2 v[4][2];  // (read here and not before: the registers are needed above)
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) v[c][i] = lds8(codes + 2 * c * kSub + 256 * i);
       const float inv = __uint_as_float((uint32_t)(254 - e) << 23);
       const uint32_t ratio = pack_half(sc * inv, sc * inv);
       if (j == 0) skey[buf * kTile + key] = there ? __uint_as_float((uint32_t)e << 23) : 0.f;
@@ -508,8 +546,7 @@ __device__ __forceinline__ void softmax(const AttendParams& p, uint32_t base, ui
   // nref: [N] the references, negated (+infinity: none yet)
   float* alpha = nref + N;                             // [N] rescale factors, then result factors
   int* limit = reinterpret_cast<int*>(nref + 2 * N);   // [N] keys that a column sees
-  float* scalars = nref + 3 * N;                       // skey0, its change, the warps' largest skey [4]
-  float* red = nref + 4 * N;                           // [4][N] the warps' maxima or sums
+  float* red = nref + 3 * N;                           // [4][N] the warps' maxima or sums
   const float* skey = nref + Smem<N>::kKeyScale;
   auto pair = [](const float* v) { return *reinterpret_cast<const float2*>(v); };
   auto leave = [&](const float2* v) {  // joined values of this warp's columns
@@ -538,7 +575,6 @@ __device__ __forceinline__ void softmax(const AttendParams& p, uint32_t base, ui
         limit[tid] = p.paged ? __ldg(p.ctx_len + item) - p.P + 1 + pos : p.K;
         offsets[tid] = ((int64_t)item * p.P + pos) * p.out_tok + (c - pos * p.heads) * p.out_head;
       }
-      if (tid == 0) scalars[0] = 0.f;
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b) l[b] = make_float2(0.f, 0.f);
       bar_softmax();
@@ -551,17 +587,17 @@ __device__ __forceinline__ void softmax(const AttendParams& p, uint32_t base, ui
     const bool ragged = p.paged && p.P > 1 && (cur.tile + 1) * kTile > limit[0];
     const bool masks = !__all_sync(0xFFFFFFFFu, there[0] && there[1]) || ragged;
     const bool first = fresh;
-    float2 mult[2];
+    float mult[2], size[2];  // of a key: factor of its scores, log2 skey
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float m = kF16 ? p.scale_log2 * sk[i] : p.scale_log2;
-      mult[i] = make_float2(m, m);
+      mult[i] = kF16 ? p.scale_log2 * sk[i] : p.scale_log2;
+      size[i] = kF16 ? (float)((int)(__float_as_uint(sk[i]) >> 23) - 127) : 0.f;
     }
     if (kF16 && fresh) scaled = __any_sync(0xFFFFFFFFu, qs[c0 + lane % kW] != 1.f);
     w.wait(bars + 8 * (kSFull + buf), phase);
     __syncwarp();
     tc::fence_after();
-    // this thread's scores in log2 units, less the references or not; -infinity where the key is hidden
+    // this thread's scores in log2 units (plus log2 skey), less the references or not; -infinity where the key is hidden
     float2 s[kBlocks][2];
     auto scores = [&](bool relative) {
       float raw[4 * kBlocks];
@@ -574,9 +610,10 @@ __device__ __forceinline__ void softmax(const AttendParams& p, uint32_t base, ui
         const float2 z = kF16 && scaled ? pair(qs + my + 8 * b) : make_float2(1.f, 1.f);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          float2 x = make_float2(raw[4 * b + 2 * i], raw[4 * b + 2 * i + 1]);
-          if (kF16 && scaled) x = tc::mul2(x, z);
-          s[b][i] = tc::fma2(x, mult[i], m);
+          const float2 x = make_float2(raw[4 * b + 2 * i], raw[4 * b + 2 * i + 1]);
+          float2 f = make_float2(mult[i], mult[i]);
+          if (kF16 && scaled) f = tc::mul2(f, z);
+          s[b][i] = tc::fma2(x, f, kF16 ? tc::add2(m, make_float2(size[i], size[i])) : m);
         }
       }
       if (masks) {
@@ -595,8 +632,7 @@ __device__ __forceinline__ void softmax(const AttendParams& p, uint32_t base, ui
     while (true) {
       scores(true);
       const float top = tc::max_of<4 * kBlocks>(&s[0][0].x);
-      const float z0 = kF16 ? scalars[0] * Range<kF16>::kGrow : 0.f;
-      if (moved || !any_softmax(top > kLazy || (kF16 && (sk[0] > z0 || sk[1] > z0)))) break;
+      if (moved || !any_softmax(top > kLazy)) break;
       moved = true;
       // a new reference for every column, kTop below the maximum of the old one's and this tile's scores
       scores(false);
@@ -605,24 +641,12 @@ __device__ __forceinline__ void softmax(const AttendParams& p, uint32_t base, ui
       for (int b = 0; b < kBlocks; ++b) m[b] = make_float2(fmaxf(s[b][0].x, s[b][1].x), fmaxf(s[b][0].y, s[b][1].y));
       over_keys<2 * kBlocks>(&m[0].x, [](float a, float b) { return fmaxf(a, b); });
       leave(m);
-      if (kF16) {
-        float z = fmaxf(sk[0], sk[1]);
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) z = fmaxf(z, __shfl_xor_sync(0xFFFFFFFFu, z, d));
-        if (lane == 0) scalars[2 + warp] = z;
-      }
       bar_softmax();
       if (tid < N) {
         const float old = -nref[tid];
         const float now = fmaxf(fmaxf(fmaxf(red[tid], red[N + tid]), fmaxf(red[2 * N + tid], red[3 * N + tid])) - kTop, old);
         nref[tid] = -now;
         alpha[tid] = old == -INFINITY ? 0.f : exp2f(old - now);
-      }
-      if (kF16 && tid == N) {
-        const float old = scalars[0];
-        const float now = fmaxf(fmaxf(fmaxf(scalars[2], scalars[3]), fmaxf(scalars[4], scalars[5])), old);
-        scalars[0] = now;
-        scalars[1] = now > 0.f ? old / now : 1.f;
       }
       bar_softmax();
 #pragma unroll
@@ -632,7 +656,6 @@ __device__ __forceinline__ void softmax(const AttendParams& p, uint32_t base, ui
         w.wait(bars + 8 * (kEmpty + (it - 1) % kBufs), (it - 1) / kBufs & 1);
         __syncwarp();
         tc::fence_after();
-        const float change = kF16 ? scalars[1] : 1.f;
 #pragma unroll 1
         for (int c = 0; c < 4 * kW; c += 8) {
           const int g = c / kW, x0 = c % kW;
@@ -641,7 +664,7 @@ __device__ __forceinline__ void softmax(const AttendParams& p, uint32_t base, ui
           tc::tmem_wait_ld();
           tc::touch<8>(o);
 #pragma unroll
-          for (int x = 0; x < 8; ++x) o[x] *= alpha[c0 + x0 + x] * change;
+          for (int x = 0; x < 8; ++x) o[x] *= alpha[c0 + x0 + x];
           tc::tmem_st8(tm + (2 + g) * N + x0, o);
         }
         tc::tmem_wait_st();
@@ -651,20 +674,15 @@ __device__ __forceinline__ void softmax(const AttendParams& p, uint32_t base, ui
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int key = key0 + 8 * i;
-      const float share = kF16 && there[i] ? sk[i] / scalars[0] : 0.f;
+      // 2^-kSumShift / skey (a key that is not there has no weight)
+      const float inv = __uint_as_float((uint32_t)(254 - kSumShift - (int)(__float_as_uint(sk[i]) >> 23)) << 23);
       const uint32_t to = base + buf * kTileBytes + 8 * kSub + key * (2 * N) + 4 * (lane & 3);
       const int sw = N == 64 ? (key & 7) : N == 32 ? ((key >> 1) & 3) : ((key >> 2) & 1);
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b) {
-        float2 e = make_float2(tc::exp2_fast(s[b][i].x), tc::exp2_fast(s[b][i].y));
-        l[b] = tc::add2(l[b], e);
-        uint32_t two;
-        if (kF16) {
-          e = tc::mul2(e, make_float2(share, share));
-          two = pack_half(e.x, e.y);
-        } else {
-          two = tc::pack_bf16(e.x, e.y);
-        }
+        const float2 e = make_float2(tc::exp2_fast(s[b][i].x), tc::exp2_fast(s[b][i].y));
+        l[b] = kF16 ? tc::fma2(e, make_float2(inv, inv), l[b]) : tc::add2(l[b], e);
+        const uint32_t two = kF16 ? pack_half(e.x, e.y) : tc::pack_bf16(e.x, e.y);
         sts4(to + (((c0 / 8 + b) ^ sw) << 4), two);
       }
     }
@@ -688,8 +706,8 @@ __device__ __forceinline__ void softmax(const AttendParams& p, uint32_t base, ui
     first_run = false;
     if (tid < N) {
       const float sum = (red[tid] + red[N + tid]) + (red[2 * N + tid] + red[3 * N + tid]);
-      const float lse2 = sum == 0.f ? -INFINITY : log2f(sum) - nref[tid];
-      alpha[tid] = sum == 0.f ? 0.f : 1.f / sum;
+      const float lse2 = sum == 0.f ? -INFINITY : log2f(sum) - nref[tid] + (kF16 ? kSumShift : 0);
+      alpha[tid] = sum == 0.f ? 0.f : (kF16 ? 1.f / (1 << kSumShift) : 1.f) / sum;
       if (!whole) {
         float* z = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(p.workspace) + ws_lse_offset(sms));
         z[part * kMaxCols + tid] = lse2;
@@ -702,7 +720,6 @@ __device__ __forceinline__ void softmax(const AttendParams& p, uint32_t base, ui
     __syncwarp();
     ++seg;
     tc::fence_after();
-    const float unscale = kF16 ? scalars[0] : 1.f;
     const bool odd = lane & 1;
 #pragma unroll 1
     for (int g = 0; g < 4; ++g) {
@@ -710,12 +727,10 @@ __device__ __forceinline__ void softmax(const AttendParams& p, uint32_t base, ui
       tc::tmem_ld<kW>(tm + (2 + g) * N, o);
       tc::tmem_wait_ld();
       tc::touch<kW>(o);
-      // O' / sum * skey0, in an order that cannot overflow early
 #pragma unroll
       for (int c = 0; c < kW; c += 4) {
         const float4 f = *reinterpret_cast<const float4*>(alpha + c0 + c);
-        o[c] = o[c] * f.x * unscale, o[c + 1] = o[c + 1] * f.y * unscale;
-        o[c + 2] = o[c + 2] * f.z * unscale, o[c + 3] = o[c + 3] * f.w * unscale;
+        o[c] *= f.x, o[c + 1] *= f.y, o[c + 2] *= f.z, o[c + 3] *= f.w;
       }
       if (!whole) {
         float* z = p.workspace + ((int64_t)part * kMaxCols + c0) * kLatent + 128 * g + dim;

@@ -1,0 +1,148 @@
+"""The latent-row operators at the edges of their inputs: rows of very different sizes, rows and groups of zeros, values that
+are not finite where a token does not see them, query tokens of no sequence, values near the end of fp32's range.
+
+Tolerances, set before any run, as in tests/test_gpu_latent.py.  A key of no weight needs more than that: its score may be so
+large that the bound on a score's error, taken over all keys, says nothing.  Its own score is off by at most es_k = 52 * 2^-23
+of its sum of magnitudes; where it lies below the log of the sum by more than es_k + 60, its weight is below e^-60 in the
+kernel as in the formula, and es is the largest over the other keys."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+import sparse_mla_kv_gb300 as hs  # noqa: E402
+import test_gpu_latent as base  # noqa: E402
+from test_gpu_latent import D, RD, SCALE, gen, normal  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+def expect(q, k, v, mask, scale):
+    """base.expect with the score errors of the keys that have weight."""
+    n = k.shape[0]
+    s = ((q @ k.T) * scale).masked_fill(~mask, -math.inf)
+    lse = torch.logsumexp(s, 1)
+    low = torch.where(lse == -math.inf, 0, lse)[:, None]
+    w = torch.exp(s - low)
+    es_k = 52 * 2.0 ** -23 * abs(scale) * (q.abs() @ k.abs().T)
+    none = (s + es_k < low - 60) | ~mask
+    es = es_k.masked_fill(none, 0).amax(1)
+    a = w @ v.abs()
+    tol_o = (2.0 ** -7 + 2 * es + 2.0 ** -18 + n * 2.0 ** -27)[:, None] * a
+    return w @ v, lse, tol_o, es + 2.0 ** -18 + n * 2.0 ** -27 + 2.0 ** -22 * low[:, 0].abs()
+
+
+def check(flat, fmt, at, ql, qr, scale, out, lse, seen=None):
+    """One token's heads over the rows `at` of a pool's bytes."""
+    c, k = base.row_values(flat[at.long()], fmt)
+    q = torch.cat([ql, qr], -1).double()
+    seen = torch.ones((q.shape[0], len(at)), dtype=torch.bool, device="cuda") if seen is None else seen
+    base.close(out, lse, expect(q, k, c, seen, scale))
+
+
+# --------------------------------------------------------------------------------------------------------------------
+# rows of different sizes
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "bf16"])
+@pytest.mark.parametrize("H", [16, 32, 64])
+@pytest.mark.parametrize("power", [20, 24, 30, 40])
+@pytest.mark.parametrize("where", [0, 350, 699])
+def test_a_large_row_without_weight(fmt, H, power, where):
+    """One row 2^power times the size of the others, with a score far below theirs: first, in the middle and last."""
+    g = gen(power + where)
+    K = 700
+    lat, rope = normal(g, 704, D, dtype=torch.float32), normal(g, 704, RD)
+    lat[where] *= 2.0 ** power
+    lat[where, 3] = -6 * 2.0 ** power
+    t = base.rows_bytes(lat, rope, fmt).reshape(11, 64, -1)
+    pool = hs.Pool([t])
+    rows = torch.arange(K, device="cuda").int()[None].repeat(2, 1).contiguous()
+    ql, qr = normal(g, 2, H, D, scale=0.1), normal(g, 2, H, RD)
+    ql[:, :, 3] = 8
+    out, lse = hs.attend_rows(pool, rows, ql, qr, SCALE)
+    flat = t.reshape(704, -1)
+    for i in range(2):
+        check(flat, fmt, rows[i], ql[i], qr[i], SCALE, out[i], lse[i])
+    table, ctx = torch.arange(11, device="cuda").int()[None], torch.tensor([K], device="cuda").int()
+    out, lse = hs.attend_pages(pool, table, ctx, ql[:1, None], qr[:1, None], SCALE)
+    check(flat, fmt, rows[0], ql[0], qr[0], SCALE, out[0, 0], lse[0, 0])
+
+
+@pytest.mark.parametrize("H", [8, 40])
+@pytest.mark.parametrize("order", ["mixed", "growing", "falling"])
+def test_weights_against_sizes(H, order):
+    """Row sizes of 2^-16 .. 2^24 with weights that fall with the size, as its 0th to 1.5th power: large rows of small
+    weight, small rows that have nearly all of it, and both with equal shares of the result."""
+    g = gen(H)
+    n = 640
+    a = torch.randint(-16, 25, (n,), generator=g, device="cuda").double()
+    if order != "mixed":
+        a = torch.sort(a, descending=order == "falling").values
+    lat = normal(g, n, D).double() * torch.exp2(a)[:, None]
+    rope = normal(g, n, RD).double()
+    rope[:, 0] = -a * math.log(2)
+    t = base.rows_bytes(lat, rope, "fp8").reshape(10, 64, 656)
+    pool = hs.Pool([t])
+    rows = torch.arange(n, device="cuda").int()[None].repeat(3, 1).contiguous()
+    ql, qr = torch.zeros((3, H, D), dtype=torch.bfloat16, device="cuda"), torch.zeros((3, H, RD), dtype=torch.bfloat16, device="cuda")
+    qr[:, :, 0] = torch.linspace(0, 1.5, H, device="cuda").bfloat16()
+    out, lse = hs.attend_rows(pool, rows, ql, qr, 1.0)
+    for i in range(3):
+        check(t.reshape(n, 656), "fp8", rows[i], ql[i], qr[i], 1.0, out[i], lse[i])
+
+
+@pytest.mark.parametrize("H", [8, 64])
+@pytest.mark.parametrize("power", [-24, -40])
+def test_rows_and_groups_of_zeros(H, power):
+    """Appended rows of small values, some of them zero altogether or in one group, whose scale is 1 by definition: what is
+    zero has no size.  (A row of zeros takes part in the softmax like any other.)"""
+    g = gen(H - power)
+    n = 300
+    lat, rope = normal(g, n, D, dtype=torch.float32, scale=2.0 ** power), normal(g, n, RD, dtype=torch.float32, scale=2.0 ** power)
+    for r in (0, 70, 299):
+        lat[r], rope[r] = 0, 0
+    lat[5:60:2, 128:256] = 0
+    lat[200:230, :384] = 0
+    lat[100], rope[101] = 0, 0
+    t = torch.zeros((5, 64, 656), dtype=torch.uint8, device="cuda")
+    pool = hs.Pool([t])
+    turn = torch.cat([torch.ones(1, 32), torch.zeros(1, 32)], 1).cuda()
+    at = torch.arange(n, device="cuda").int()
+    hs.append_rows(pool, at, lat, rope, torch.zeros(n, dtype=torch.int32, device="cuda"), turn)
+    flat = t.reshape(-1, 656)
+    assert bool((flat[0, 512:528].view(torch.float32) == 1).all())
+    ql, qr = normal(g, 2, H, D, scale=2.0 ** -power), normal(g, 2, H, RD, scale=2.0 ** -power)
+    rows = at[None].repeat(2, 1).contiguous()
+    out, lse = hs.attend_rows(pool, rows, ql, qr, SCALE)
+    for i in range(2):
+        check(flat, "fp8", rows[i], ql[i], qr[i], SCALE, out[i], lse[i])
+    ctx = torch.tensor([n], device="cuda").int()
+    out, lse = hs.attend_pages(pool, torch.arange(5, device="cuda").int()[None], ctx, ql[:1, None], qr[:1, None], SCALE)
+    check(flat, "fp8", at, ql[0], qr[0], SCALE, out[0, 0], lse[0, 0])
+
+
+@pytest.mark.parametrize("K", [1, 5, 70])
+def test_fp8_rows_weights_keep_eleven_bits(K):
+    """Weights are rounded to fp16 there, 2^-11 of each, so that |out - ref| <= 2^-8 |ref| (its rounding to bf16)
+    + (1 + 2^-8) (2^-11 + 2 es + 2^-18 + n 2^-27) A.  The bound that bf16 weights need, 2^-7 A, is up to 14 times as wide
+    where terms cancel."""
+    g = gen(K)
+    pool, tensors = base.make_pool(g, 8, "fp8")
+    rows = torch.randint(0, 512, (40, K), generator=g, device="cuda").int()
+    ql, qr = normal(g, 40, 64, D), normal(g, 40, 64, RD)
+    out, lse = hs.attend_rows(pool, rows, ql, qr, SCALE)
+    flat = tensors[0].reshape(-1, 656)
+    caught = False
+    for i in range(40):
+        c, k = base.row_values(flat[rows[i].long()], "fp8")
+        q = torch.cat([ql[i], qr[i]], -1).double()
+        seen = torch.ones((64, K), dtype=torch.bool, device="cuda")
+        ref, _, wide, _ = base.expect(q, k, c, seen, SCALE)
+        s = q @ k.T * SCALE
+        w = torch.softmax(s, 1)
+        a = w @ c.abs()
+        tol = 2.0 ** -8 * ref.abs() + (1 + 2.0 ** -8) * (wide - (2.0 ** -7 - 2.0 ** -11) * a)
+        assert bool(((out[i].double() - ref).abs() <= tol).all())
+        caught |= bool(((w.bfloat16().double() @ c - ref).abs() > tol).any())
+    assert caught == (K > 1)   # the check would see weights of 8 bits
