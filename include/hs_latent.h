@@ -94,7 +94,9 @@ hs_status hs_append_rows(const hs_pool* pool, int32_t layer, const hs_append* a,
  *   s[k] = scale * (q_latent[t][h] . c[k] + q_rope[t][h] . r[k])
  *   out[t][h] = sum_k softmax(s)[k] c[k]        lse[t][h] = log sum_k exp(s[k])
  * Sums and softmax statistics are fp32; softmax weights are rounded to bf16 (fp8 rows: to fp16) before their
- * product with the latents; out is rounded once.  A token that sees no row gets zeros and lse = -infinity. */
+ * product with the latents; out is rounded once.  A token that sees no row gets zeros and lse = -infinity.
+ * A row that a token does not see has no part in its result, whatever the row holds; a NaN in one that it sees makes
+ * its result NaN, and an infinity there makes it NaN or leaves out the infinite value where the row's weight is zero. */
 typedef struct {
   int32_t heads;            /* 1..HS_MAX_HEADS                                                        */
   float scale;

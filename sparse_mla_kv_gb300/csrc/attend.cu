@@ -485,6 +485,29 @@ __device__ __forceinline__ void issue_scores(const AttendParams& p, uint32_t bas
   __syncwarp();
 }
 
+// Infinite and NaN values of the tile's keys from .. to - 1 become zeros (one warp): some columns do not see these keys, and
+// a weight of zero would not cancel such a value.  Columns that see a NaN have it in their sums already, by its score.
+template <bool kF16>
+__device__ __forceinline__ void finite_values(uint32_t tile, int from, int to) {
+  constexpr uint32_t kExponent = kF16 ? 0x7C00u : 0x7F80u;
+#pragma unroll 1
+  for (int i = from * 64 + (threadIdx.x & 31); i < to * 64; i += 32) {
+    const uint32_t at = tile + (i & 7) * kSub + (i >> 6) * 128 + (i >> 3 & 7) * 16;  // 16 bytes of key i / 64
+    const uint4 x = lds16(at);
+    uint32_t w[4] = {x.x, x.y, x.z, x.w}, kept = ~0u;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t keep = ((w[k] & kExponent) == kExponent ? 0u : 0xFFFFu) |
+                            ((w[k] >> 16 & kExponent) == kExponent ? 0u : 0xFFFF0000u);
+      w[k] &= keep;
+      kept &= keep;
+    }
+    if (~kept) sts(at, w[0], w[1], w[2], w[3]);
+  }
+  tc::fence_async_smem();
+  __syncwarp();
+}
+
 template <int N, bool kF16>
 __device__ __forceinline__ void issue_results(const AttendParams& p, uint32_t base, uint32_t bars, uint32_t tmem, Cursor cur,
                                               int groups, tc::Waiter& w) {
@@ -494,11 +517,17 @@ __device__ __forceinline__ void issue_results(const AttendParams& p, uint32_t ba
   const uint64_t dp = tc::desc(base + 8 * kSub, 16, 8 * N * 2, kPSwizzle);
   const bool leader = tc::elect();
   bool first = true;
+  int seen = INT32_MAX;  // keys that all of the group's columns see: what its first column does
 #pragma unroll 1
   for (uint32_t it = 0; cur.left > 0; ++it) {
     const uint32_t buf = it % kBufs;
+    if (first && p.paged && p.P > 1) seen = __ldg(p.ctx_len + cur.item) - p.P + 1 + cur.group * N / p.heads;
     w.wait(bars + 8 * (kPReady + buf), it / kBufs & 1);
     __syncwarp();
+    if (cur.keys > seen) {
+      const int from = max(0, seen - cur.tile * kTile), to = min(kTile, cur.keys - cur.tile * kTile);
+      if (from < to) finite_values<kF16>(base + buf * kTileBytes, from, to);
+    }
     tc::fence_after();
     const uint64_t a0 = dv + (uint32_t)(buf * kTileBytes >> 4), b = dp + (uint32_t)(buf * kTileBytes >> 4);
 #pragma unroll 1

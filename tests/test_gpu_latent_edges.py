@@ -146,3 +146,68 @@ def test_fp8_rows_weights_keep_eleven_bits(K):
         assert bool(((out[i].double() - ref).abs() <= tol).all())
         caught |= bool(((w.bfloat16().double() @ c - ref).abs() > tol).any())
     assert caught == (K > 1)   # the check would see weights of 8 bits
+
+
+# --------------------------------------------------------------------------------------------------------------------
+# values that are not finite
+
+
+@pytest.mark.parametrize("fmt,bad", [("fp8", math.nan), ("bf16", math.nan), ("bf16", math.inf)])
+@pytest.mark.parametrize("ctx,P,H", [([130, 65, 64, 5], 4, 16), ([67], 3, 64), ([5000, 700], 4, 20), ([70], 70, 2)])
+def test_pages_rows_that_a_position_does_not_see(fmt, bad, ctx, P, H):
+    """Values that are not finite in one of the last rows: only the positions that see the row may notice."""
+    g = gen(sum(ctx) + P)
+    pages = -(-max(ctx) // 64)
+    pool, tensors = base.make_pool(g, pages * len(ctx), fmt)
+    flat = tensors[0].reshape(-1, base.FMT[fmt])
+    first = []   # the first position of each request that sees the bad row
+    for r, n in enumerate(ctx):
+        p = 1 + r % (P - 1)
+        first.append(p)
+        lat = normal(g, 1, D, dtype=torch.float32)
+        lat[0, 7 + 128 * (r % 4)] = bad
+        row = base.rows_bytes(lat, normal(g, 1, RD), fmt, scales=torch.full((1, 4), 1 / 64, device="cuda") if fmt == "fp8" else None)
+        flat[r * pages * 64 + n - P + p] = row[0]
+    table = torch.arange(pages * len(ctx), device="cuda").int().reshape(len(ctx), pages)
+    cl = torch.tensor(ctx, device="cuda").int()
+    ql, qr = normal(g, len(ctx), P, H, D), normal(g, len(ctx), P, H, RD)
+    out, lse = hs.attend_pages(pool, table, cl, ql, qr, SCALE)
+    for r, n in enumerate(ctx):
+        for p in range(P):
+            if p < first[r]:
+                at = r * pages * 64 + torch.arange(n - P + 1 + p, device="cuda")
+                check(flat, fmt, at, ql[r, p], qr[r, p], SCALE, out[r, p], lse[r, p])
+            elif math.isnan(bad):
+                assert bool(torch.isnan(out[r, p]).all()) and bool(torch.isnan(lse[r, p]).all())
+
+
+
+def test_expanded_keys_under_the_causal_mask():
+    """Keys that are NaN: queries before them do not notice."""
+    g = gen(77)
+    n, H = 300, 2
+    q, kv, kr = normal(g, n, H, 192), normal(g, n, H, 256), normal(g, n, RD)
+    kv[200, 0, 5], kr[290, 3] = math.nan, math.nan
+    a = [q[..., :128], q[..., 128:], kv[..., :128], kr, kv[..., 128:]]
+    out, lse = hs.attend_expanded(*a, base.cum([n]), base.cum([n]), SCALE)
+    for h, first in ((0, 200), (1, 290)):
+        assert bool(torch.isnan(out[first:, h]).all()) and bool(torch.isnan(lse[first:, h]).all())
+        part = [x[:first, h:h + 1] for x in a[:3]] + [kr[:first], a[4][:first, h:h + 1]]
+        base.check_expanded(*part, [0, first], [0, first], SCALE, True, out[:first, h:h + 1], lse[:first, h:h + 1])
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "bf16"])
+def test_infinite_queries_stay_in_their_head(fmt):
+    """An infinite query element makes every score infinite (or NaN), some of them +infinity: NaN by the formula."""
+    g = gen(30)
+    pool, tensors = base.make_pool(g, 4, fmt)
+    rows = torch.randint(0, 256, (2, 200), generator=g, device="cuda").int()
+    ql, qr = normal(g, 2, 20, D), normal(g, 2, 20, RD)
+    clean = ql.clone()
+    ql[0, 3, 100], ql[1, 7, 0], qr[1, 19, 5] = math.inf, -math.inf, math.inf
+    out, lse = hs.attend_rows(pool, rows, ql, qr, SCALE)
+    bad = torch.zeros((2, 20), dtype=torch.bool, device="cuda")
+    bad[0, 3] = bad[1, 7] = bad[1, 19] = True
+    assert bool(torch.isnan(out[bad]).all())
+    ref, ref_l = hs.attend_rows(pool, rows, clean, qr.where(torch.isfinite(qr), torch.zeros_like(qr)), SCALE)
+    assert torch.equal(out[~bad], ref[~bad]) and torch.equal(lse[~bad], ref_l[~bad])
