@@ -140,7 +140,8 @@ hs_status hs_attend_pages(const hs_pool* pool, int32_t layer, const int32_t* blo
  *   s[i][j] = scale * (q_nope[i][h] . k_nope[j][h] + q_rope[i][h] . k_rope[j])
  *   out[i][h] = sum_j softmax(s)[i][j] v[j][h]      lse[i][h] = log sum_j exp(s[i][j])
  * With causal != 0 the queries are the last tokens of the sequence: query i (counted within it) sees the
- * keys j <= i + keys - queries.  Rounding (bf16 weights) and empty rows as in hs_attend. */
+ * keys j <= i + keys - queries.  Rounding (bf16 weights) and empty rows as in hs_attend.  Keys that a query does not
+ * see have no part in its result, whatever they and their values hold. */
 typedef struct {
   int32_t seqs, heads;
   int32_t causal;

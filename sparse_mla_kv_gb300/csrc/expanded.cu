@@ -54,6 +54,9 @@ struct Item {
   int head, q0, rows, k0, keys;
   int shift;  // query row r (counted from q0) sees the keys below r + shift (keys, where not causal)
   int tiles[2];  // key tiles of each query tile; -1: no such query tile
+  bool causal;
+  // keys that every row of query tile t sees: those below this one
+  __device__ __forceinline__ int all_see(int t) const { return causal ? min(keys, t * kQRows + shift) : keys; }
   __device__ __forceinline__ int query_tiles() const { return rows > kQRows ? 2 : 1; }
   __device__ __forceinline__ int most() const { return max(tiles[0], tiles[1]); }
 };
@@ -112,6 +115,7 @@ struct Finder {
     it->rows = min(kBlock, q1 - q0 - first);
     it->k0 = k0;
     it->keys = k1 - k0;
+    it->causal = a.causal != 0;
     it->shift = a.causal ? first + 1 + (k1 - k0) - (q1 - q0) : 0;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -195,7 +199,7 @@ __device__ __forceinline__ void load_items(const hs_expanded& a, const Maps& m, 
 // ---- products (one warp a query tile) ----
 // Both warps wait for every part of a key tile and release it, whether their query tile needs it or not.
 __device__ __forceinline__ void issue_items(const hs_expanded& a, int t, uint32_t q, uint32_t ring, uint32_t bars,
-                                            uint32_t tmem) {
+                                            uint32_t tmem, volatile int* done) {
   constexpr uint32_t kIdS = tc::idesc(false, 128, kKeys, false, false);
   constexpr uint32_t kIdO = tc::idesc(false, 128, 64, false, true);
   tc::Waiter w;
@@ -214,7 +218,7 @@ __device__ __forceinline__ void issue_items(const hs_expanded& a, int t, uint32_
   Finder f;
   f.start(a);
   for (int k = 0; f.find(a, item_number(k), &it); ++k) {
-    const int tiles = it.most(), mine = max(0, it.tiles[t]);
+    const int tiles = it.most(), mine = max(0, it.tiles[t]), whole = it.all_see(t);
     if (tiles <= 0) continue;
     auto arrived = [&]() {  // waits for the next part
       await(kFull + group % kGroups, (group / kGroups) & 1);
@@ -249,8 +253,15 @@ __device__ __forceinline__ void issue_items(const hs_expanded& a, int t, uint32_
       await(kPReady + t, phase & 1);
       arrived();
       const int valid = it.keys - j * kKeys;
+      bool skip = false;  // this tile's results are in O already
+      if ((j + 1) * kKeys > whole && done[t]) {
+        skip = true;
+        __syncwarp();
+        done[t] = 0;
+        __syncwarp();
+      }
 #pragma unroll 1
-      for (int i = 0; i < kUnitsV; ++i) {
+      for (int i = 0; i < kUnitsV && !skip; ++i) {
         const uint32_t x = base + j * kUnits + kUnitsK + i;
         if (valid < kKeys) {  // by both warps: they write the same
           for (int k = threadIdx.x & 31; k < (kKeys - valid) * 8; k += 32) {
@@ -290,7 +301,86 @@ __device__ __forceinline__ void issue_items(const hs_expanded& a, int t, uint32_
 }
 
 // ---- softmax and results (128 threads a query tile) ----
-__device__ __forceinline__ void softmax_items(const hs_expanded& a, float scale_log2, uint32_t bars, uint32_t tmem) {
+
+// A value that is infinite or NaN must not reach the queries that the causal mask hides it from, and a weight of zero does
+// not keep it from them.  So the values of a key tile that some rows do not see whole are looked through (by the softmax's
+// threads, 256 bytes each, while they wait for the scores: 6 prompts of up to 2500 tokens x 16 heads 122 -> 124 us), and where
+// one is not finite, these threads add that tile's results themselves, key by key.
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+// Whether the values of keys from .. to - 1 in a unit are all finite, in this thread's part.
+__device__ __forceinline__ bool finite_part(uint32_t unit, int from, int to) {
+  uint32_t sum = 0;  // of the values times zero: NaN once one was not finite
+#pragma unroll
+  for (int n = 0; n < kKeys; n += 16) {  // 16 keys at a time
+    const int i = n * 8 + (threadIdx.x & 127);
+    if (i < from * 8 || i >= to * 8) continue;
+    const uint4 x = lds16(unit + i * 16);
+    asm("{\n\tfma.rn.bf16x2 %0, %1, %5, %0;\n\tfma.rn.bf16x2 %0, %2, %5, %0;\n\tfma.rn.bf16x2 %0, %3, %5, %0;\n\t"
+        "fma.rn.bf16x2 %0, %4, %5, %0;\n\t}"
+        : "+r"(sum)
+        : "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w), "r"(0u));
+  }
+  return (sum & 0x7F80u) != 0x7F80u && (sum & 0x7F800000u) != 0x7F800000u;
+}
+// True when x is true for any of a query tile's threads.
+__device__ __forceinline__ bool any_of_tile(int t, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)x), "r"(1 + t)
+      : "memory");
+  return r != 0;
+}
+// O (+)= P V over the first `sees` keys of the tile, by a row's thread; P as it was left for the product.
+__device__ __forceinline__ void add_results(uint32_t ts, uint32_t to, uint32_t unit0, uint32_t unit1, int sees, bool first) {
+#pragma unroll 1
+  for (int c = 0; c < 128; c += 16) {
+    float o[16];
+#pragma unroll
+    for (int x = 0; x < 16; ++x) o[x] = 0.f;
+    if (!first) {
+      tc::tmem_ld16(to + c, o);
+      tc::tmem_wait_ld();
+      tc::touch<16>(o);
+    }
+    const uint32_t v = c < 64 ? unit0 : unit1;
+    const int piece = (c & 63) >> 3;  // 8 dimensions of a key's 64
+#pragma unroll 1
+    for (int k0 = 0; k0 < kKeys; k0 += 16) {
+      float p[8];  // 2 weights each
+      tc::tmem_ld<8>(ts + k0 / 2, p);
+      tc::tmem_wait_ld();
+      tc::touch<8>(p);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        if (k0 + k >= sees) continue;
+        const uint32_t two = __float_as_uint(p[k / 2]);
+        const float w = __uint_as_float(k & 1 ? two & 0xFFFF0000u : two << 16);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint4 x = lds16(v + (k0 + k) * 128 + (((piece + h) ^ (k & 7)) << 4));
+          const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            o[8 * h + 2 * d] += w * __uint_as_float(y[d] << 16);
+            o[8 * h + 2 * d + 1] += w * __uint_as_float(y[d] & 0xFFFF0000u);
+          }
+        }
+      }
+    }
+    __syncwarp();
+    tc::tmem_st16(to + c, o);
+  }
+  tc::tmem_wait_st();
+}
+
+__device__ __forceinline__ void softmax_items(const hs_expanded& a, float scale_log2, uint32_t ring, uint32_t bars, uint32_t tmem,
+                                              volatile int* done) {
   tc::Waiter w;
   const int t = threadIdx.x >> 7, lane = threadIdx.x & 31;
   const int row_in_tile = threadIdx.x & 127;
@@ -300,20 +390,34 @@ __device__ __forceinline__ void softmax_items(const hs_expanded& a, float scale_
   // -infinity stays one
   const bool negative = scale_log2 < 0.f;
   const float scale = fmaxf(fabsf(scale_log2), 1.17549435e-38f);
-  uint32_t phase = 0;
+  uint32_t phase = 0, passed = 0;  // key tiles of this query tile; of the CTA, in the items before
   Item it;
   Finder f;
   f.start(a);
   for (int k = 0; f.find(a, item_number(k), &it); ++k) {
     const int tiles = it.tiles[t];
+    const uint32_t before = passed;
+    passed += max(0, it.most());
     if (tiles < 0) continue;
     const int row = t * kQRows + row_in_tile;
     const int sees = a.causal ? min(it.keys, row + it.shift) : it.keys;  // keys below this one are seen
-    const int all_see = a.causal ? min(it.keys, t * kQRows + it.shift) : it.keys;  // by every row of the tile
+    const int all_see = it.all_see(t);
     float m = -INFINITY;
     float2 la = make_float2(0.f, 0.f), lb = la;  // the sum, in four chains
 #pragma unroll 1
     for (int j = 0; j < tiles; ++j, ++phase) {
+      // (the values are looked through while the scores are on their way)
+      const uint32_t u = (before + j) * kUnits + kUnitsK;
+      const uint32_t unit0 = ring + u % kRing * kUnit, unit1 = ring + (u + 1) % kRing * kUnit;
+      const int from = max(0, all_see - j * kKeys), end = min(kKeys, it.keys - j * kKeys);  // keys hidden from some rows
+      bool finite = true;
+      if (from < end) {
+        const uint32_t part = 2 * (before + j) + 1;
+        w.wait(bars + 8 * (kFull + part % kGroups), part / kGroups & 1);
+        finite = finite_part(unit0, from, end) & finite_part(unit1, from, end);
+        __syncwarp();
+        finite = !any_of_tile(t, !finite);
+      }
       w.wait(bars + 8 * (kSFull + t), phase & 1);
       __syncwarp();
       tc::fence_after();
@@ -370,6 +474,10 @@ __device__ __forceinline__ void softmax_items(const hs_expanded& a, float scale_
         tc::tmem_st16(ts + c / 2, reinterpret_cast<const float*>(p));
       }
       tc::tmem_wait_st();
+      if (!finite) {
+        add_results(ts, to, unit0, unit1, sees - j * kKeys, j == 0);
+        done[t] = 1;
+      }
       tc::fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(bars + 8 * (kPReady + t));
@@ -414,6 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const hs_expanded
                                                                float scale_log2) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t tmem_slot;
+  __shared__ int done[2];  // by query tile: the softmax has added a key tile's results itself
   const uint32_t q = (tc::smem_u32(smem_raw) + 1023) & ~1023u;
   const uint32_t ring = q + 6 * kUnit, bars = ring + kRing * kUnit;
   const int warp = threadIdx.x >> 5;
@@ -423,6 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const hs_expanded
       if (!sequence(a, s, &q0, &q1, &k0, &k1)) report(a.status, HS_ERR_ID_RANGE);
     }
   if (threadIdx.x == 0) {
+    done[0] = done[1] = 0;
     for (int i = 0; i < kGroups; ++i) tc::mbar_init(bars + 8 * (kFull + i), 1);
     for (int i = 0; i < kRing; ++i) tc::mbar_init(bars + 8 * (kEmpty + i), 2);
     tc::mbar_init(bars + 8 * kQFull, 1);
@@ -442,11 +552,11 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const hs_expanded
   const uint32_t tmem = tmem_slot;
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    softmax_items(a, scale_log2, bars, tmem);
+    softmax_items(a, scale_log2, ring, bars, tmem, done);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (warp < kLoadWarp)
-      issue_items(a, warp - kMmaWarp, q, ring, bars, tmem);
+      issue_items(a, warp - kMmaWarp, q, ring, bars, tmem, done);
     else if (warp == kLoadWarp)
       load_items(a, maps, q, ring, bars);
   }

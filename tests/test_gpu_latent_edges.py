@@ -181,6 +181,41 @@ def test_pages_rows_that_a_position_does_not_see(fmt, bad, ctx, P, H):
                 assert bool(torch.isnan(out[r, p]).all()) and bool(torch.isnan(lse[r, p]).all())
 
 
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("qn,kn", [([300], [300]), ([40, 200], [170, 456]), ([1, 130, 5], [64, 130, 300]), ([700], [700])])
+def test_expanded_values_under_the_causal_mask(qn, kn, bad):
+    """Values that are not finite in single dimensions of a few keys: queries before those keys do not notice, and the
+    others only in that dimension."""
+    H = 2
+    g = gen(sum(qn) + sum(kn))
+    q, kv, kr = normal(g, sum(qn), H, 192), normal(g, sum(kn), H, 256), normal(g, sum(kn), RD)
+    cq, ck = base.cum(qn).tolist(), base.cum(kn).tolist()
+    v = kv[..., 128:]
+    clean = v.clone()
+    marks = []
+    for b in range(len(qn)):
+        for i, back in enumerate((0, qn[b] // 3, qn[b] // 2, qn[b] - 1)):
+            key = max(kn[b] - 1 - back, 0)
+            d = (31 * i + 5) % 128
+            v[ck[b] + key, i % H, d] = bad
+            clean[ck[b] + key, i % H, d] = 0
+            marks.append((b, key, i % H, d))
+    a = (q[..., :128], q[..., 128:], kv[..., :128], kr)
+    out, lse = hs.attend_expanded(*a, v, base.cum(qn), base.cum(kn), SCALE)
+    repaired = out.clone()
+    for b, key, h, d in marks:
+        sees = torch.arange(qn[b], device="cuda") + kn[b] - qn[b] >= key
+        at = out[cq[b]:cq[b + 1], h, d]
+        assert not bool(torch.isfinite(at[sees]).any())
+        if math.isinf(bad):
+            assert bool((at[sees] == bad).all())
+    want, _ = hs.attend_expanded(*a, clean, base.cum(qn), base.cum(kn), SCALE)
+    for b, key, h, d in marks:   # what sees a mark is checked above; the rest against the formula
+        sees = torch.arange(qn[b], device="cuda") + kn[b] - qn[b] >= key
+        part = repaired[cq[b]:cq[b + 1], h, d]
+        part[sees] = want[cq[b]:cq[b + 1], h, d][sees]
+    base.check_expanded(*a, clean, cq, ck, SCALE, True, repaired, lse)
+
 
 def test_expanded_keys_under_the_causal_mask():
     """Keys that are NaN: queries before them do not notice."""
