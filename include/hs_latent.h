@@ -141,7 +141,8 @@ hs_status hs_attend_pages(const hs_pool* pool, int32_t layer, const int32_t* blo
  *   out[i][h] = sum_j softmax(s)[i][j] v[j][h]      lse[i][h] = log sum_j exp(s[i][j])
  * With causal != 0 the queries are the last tokens of the sequence: query i (counted within it) sees the
  * keys j <= i + keys - queries.  Rounding (bf16 weights) and empty rows as in hs_attend.  Keys that a query does not
- * see have no part in its result, whatever they and their values hold. */
+ * see have no part in its result, whatever they and their values hold.  Query tokens that no sequence has (cu_q leaves
+ * them out, or the sequence's offsets are bad) get zeros and -infinity. */
 typedef struct {
   int32_t seqs, heads;
   int32_t causal;

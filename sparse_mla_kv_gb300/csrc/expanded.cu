@@ -12,7 +12,8 @@
 //   warps 0-3, 4-7   softmax and results of query tile 0 and 1, a row a thread;
 //   warps 8, 9       issue the products of query tile 0 and 1, so that neither waits for the other's softmax, and zero
 //                    value rows past a sequence's end before their product (a weight of zero does not cancel a NaN there);
-//   warp 10          loads by the copy engine.
+//   warp 10          loads by the copy engine;
+//   warp 11          clears the results of query tokens that no sequence has.
 // Shared memory: 96 KB of queries and a ring of eight 16 KB units (128 keys x 64 dimensions); a key tile is three units
 // of keys, then two of values.  Tensor memory: S and O of both tiles, 4 x 128 columns; P, in bf16, takes S's place and is
 // the left operand of the second product from there.
@@ -518,6 +519,29 @@ __device__ __forceinline__ void softmax_items(const hs_expanded& a, float scale_
   if (w.dead) report(a.status, HS_ERR_TIMEOUT);
 }
 
+// ---- query tokens of no sequence (one warp) ----
+// Zeros and -infinity for the tokens that no sequence has (cu_q leaves some out, or a sequence's offsets are bad).  Offsets that
+// are all right and span the tensor leave none; else every CTA looks at its share of the tokens.
+__device__ __forceinline__ void clear_rest(const hs_expanded& a) {
+  const int lane = threadIdx.x & 31;
+  int q0, q1, k0, k1;
+  bool spans = a.seqs > 0 && __ldg(a.cu_q) == 0 && __ldg(a.cu_q + a.seqs) == a.q_tokens;
+  for (int s = lane; s < a.seqs; s += 32) spans &= sequence(a, s, &q0, &q1, &k0, &k1);
+  if (__all_sync(0xFFFFFFFFu, spans)) return;
+  for (int64_t t0 = 32 * (int64_t)blockIdx.x; t0 < a.q_tokens; t0 += 32 * (int64_t)gridDim.x) {
+    bool rest = t0 + lane < a.q_tokens;
+    for (int s = 0; s < a.seqs; ++s) rest &= !(sequence(a, s, &q0, &q1, &k0, &k1) && t0 + lane >= q0 && t0 + lane < q1);
+    for (unsigned who = __ballot_sync(0xFFFFFFFFu, rest); who; who &= who - 1) {
+      const int64_t t = t0 + __ffs(who) - 1;
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + t * a.out_token_stride;
+      for (int i = lane; i < a.heads * 16; i += 32)
+        *reinterpret_cast<uint4*>(out + (i >> 4) * a.out_head_stride + (i & 15) * 8) = make_uint4(0, 0, 0, 0);
+      if (a.lse)
+        for (int h = lane; h < a.heads; h += 32) a.lse[t * a.heads + h] = -INFINITY;
+    }
+  }
+}
+
 __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const hs_expanded a, const __grid_constant__ Maps maps,
                                                                float scale_log2) {
   extern __shared__ uint8_t smem_raw[];
@@ -559,6 +583,8 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const hs_expanded
       issue_items(a, warp - kMmaWarp, q, ring, bars, tmem, done);
     else if (warp == kLoadWarp)
       load_items(a, maps, q, ring, bars);
+    else
+      clear_rest(a);
   }
   __syncwarp();
   tc::fence_before();
@@ -611,7 +637,7 @@ cudaError_t launch_expanded(const hs_expanded& a, int sms, cudaStream_t s) {
     return cudaErrorInvalidValue;
   // at most this many items: every sequence may end in a block of its own
   const int64_t most = (a.q_tokens / kBlock + a.seqs) * a.heads;
-  const int grid = (int)(most < sms ? most : sms);
+  const int grid = (int)(most < 1 ? 1 : most < sms ? most : sms);
   expanded_kernel<<<grid, kThreads, kSmemBytes, s>>>(a, m, a.scale * kLog2e);
   count_launch();
   return cudaGetLastError();

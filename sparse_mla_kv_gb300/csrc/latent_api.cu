@@ -147,7 +147,7 @@ hs_status hs_attend_expanded(const hs_expanded* a, hs_stream_t stream) {
   if (!a || a->seqs < 0 || a->heads < 1 || a->heads > HS_MAX_HEADS || a->q_tokens < 0 || a->k_tokens < 0 ||
       a->q_tokens > INT32_MAX || a->k_tokens > INT32_MAX || !(a->scale == a->scale))
     return HS_ERR_INVALID_ARG;
-  if (a->seqs == 0 || a->q_tokens == 0) return HS_OK;
+  if (a->q_tokens == 0) return HS_OK;
   if (!a->cu_q || !a->cu_k || !aligned(a->q_nope) || !aligned(a->q_rope) || !aligned(a->out)) return HS_ERR_INVALID_ARG;
   if (a->k_tokens > 0 && (!aligned(a->k_nope) || !aligned(a->k_rope) || !aligned(a->v))) return HS_ERR_INVALID_ARG;
   const int64_t q = a->q_tokens, k = a->k_tokens, h = a->heads;

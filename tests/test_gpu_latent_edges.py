@@ -246,3 +246,51 @@ def test_infinite_queries_stay_in_their_head(fmt):
     assert bool(torch.isnan(out[bad]).all())
     ref, ref_l = hs.attend_rows(pool, rows, clean, qr.where(torch.isfinite(qr), torch.zeros_like(qr)), SCALE)
     assert torch.equal(out[~bad], ref[~bad]) and torch.equal(lse[~bad], ref_l[~bad])
+
+
+# --------------------------------------------------------------------------------------------------------------------
+# query tokens of no sequence
+
+
+@pytest.mark.parametrize("cq,ck,covered", [
+    ([0, 30, 50], [0, 30, 64], [(0, 50)]),                 # tokens after the last sequence
+    ([3, 30, 64], [0, 30, 64], [(3, 64)]),                 # and before the first
+    ([0, 32, 64], [0, 40, 65], [(0, 32)]),                 # a sequence whose keys are out of range
+    ([0, 40, 30], [0, 40, 64], [(0, 40)]),                 # or whose queries are
+    ([0, 20, 20, 64], [0, -3, 20, 64], [(20, 64)]),
+    ([70, 80], [0, 64], []),
+    ([0], [0], []),                                        # no sequence at all
+    ([0, 0, 0], [0, 10, 64], []),                          # only empty ones
+])
+@pytest.mark.parametrize("H", [1, 3])
+def test_expanded_tokens_of_no_sequence(cq, ck, covered, H):
+    """They get zeros and -infinity, like a token that sees nothing."""
+    g = gen(53)
+    n = 64
+    q, kv = normal(g, n, H, 192), normal(g, n, H, 256)
+    a = (q[..., :128], q[..., 128:], kv[..., :128], normal(g, n, RD), kv[..., 128:])
+    out = torch.full((H, n, 136), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((n, H), 7.0, device="cuda")
+    o, _ = hs.attend_expanded(*a, torch.tensor(cq, device="cuda").int(), torch.tensor(ck, device="cuda").int(), SCALE,
+                              out=out.transpose(0, 1)[..., :128], lse=lse)
+    there = torch.zeros(n, dtype=torch.bool, device="cuda")
+    for x, y in covered:
+        there[x:y] = True
+    assert bool((o[~there] == 0).all()) and bool((lse[~there] == -math.inf).all())
+    assert bool(torch.isfinite(o[there]).all()) and bool(torch.isfinite(lse[there]).all())
+    assert bool((out[..., 128:] == 7).all())
+
+
+def test_expanded_many_tokens_of_no_sequence():
+    g = gen(54)
+    n, H = 5000, 5
+    q, kv = normal(g, n, H, 192), normal(g, 100, H, 256)
+    a = (q[..., :128], q[..., 128:], kv[..., :128], normal(g, 100, RD), kv[..., 128:])
+    cq = [0] + [1000 + 3 * i for i in range(40)]
+    cq[1] = 0
+    ck = [min(i, 100) for i in range(41)]
+    out = torch.full((n, H, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    c = torch.tensor(cq, device="cuda").int()
+    out, lse = hs.attend_expanded(*a, c, torch.tensor(ck, device="cuda").int(), SCALE, out=out, causal=False)
+    assert bool((out[cq[-1]:] == 0).all()) and bool((lse[cq[-1]:] == -math.inf).all())
+    base.check_expanded(*a, cq, ck, SCALE, False, out, lse)
