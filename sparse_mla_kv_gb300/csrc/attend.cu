@@ -12,8 +12,8 @@
 // are kept per thread and joined once per unit.
 //
 // Types.  bf16 rows: both products in bf16 (the two operands of one product have the same type, and bf16 values have
-// fp32's range), so the weights are rounded to 8 bits: 2e-3 of the largest result instead of 1.7e-3 in 32 bits.  fp8 rows:
-// both in fp16, because an e4m3 code becomes fp16 in one instruction for two and fp16's 11 bits hold it exactly, while its
+// fp32's range), so the weights are rounded to 8 bits: root mean square error 2.0e-3 of the results' against 1.7e-3 with 32
+// bits and one rounding.  fp8 rows (1.67e-3 against 1.66e-3): both in fp16, because an e4m3 code becomes fp16 in one instruction for two and fp16's 11 bits hold it exactly, while its
 // range is narrow: 2^-24 (with full precision 2^-14) to 2^16.  So every factor is brought into range by a power of two: a
 // row by skey (its values are code * scale / skey, its rotated part divided by it too), a query column by qs; S = S' skey
 // qs.  A key's row enters the result as its weight times skey, so what is rounded to fp16 is that product: t below is the
@@ -73,10 +73,11 @@ __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec
 constexpr int kSub = kTile * 128;    // bytes of a sub-tile: 64 keys x 64 values
 constexpr int kTileBytes = 9 * kSub;  // of which the ninth holds the rotated parts, and later the weights
 // In log2 units: where a new reference puts the largest score, and the most that a score may reach before it moves.
-// fp16 weights are normal from 2^-14 to 2^16; bf16 weights have fp32's range.
+// fp16 weights are normal from 2^-14 to 2^16; bf16 weights have fp32's range, but so do the values that they multiply, and
+// the sums of both are fp32 too: weights of up to 2^16 leave values of 2^90 room.
 template <bool kF16>
 struct Range {
-  static constexpr float kTop = kF16 ? 7.f : 0.f, kLazy = kF16 ? 15.f : 64.f;
+  static constexpr float kTop = kF16 ? 7.f : 0.f, kLazy = kF16 ? 15.f : 16.f;
 };
 // skey of an fp8 row: 2^-112 .. 2^112, as the field of a float's exponent; at the ends, fp16 still holds all e4m3 codes of the
 // smallest normal scale and all values below 2^128.  A row whose latents are all zero has no size: it gets at least 2^-60,

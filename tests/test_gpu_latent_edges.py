@@ -249,6 +249,47 @@ def test_infinite_queries_stay_in_their_head(fmt):
 
 
 # --------------------------------------------------------------------------------------------------------------------
+# values near the end of the range
+
+
+@pytest.mark.parametrize("order", ["rising", "falling"])
+def test_expanded_large_values_and_rising_scores(order):
+    """Values of 2^90 and scores that rise by 40 over the keys: no weight may carry a sum past fp32's range."""
+    g = gen(91)
+    n, H = 500, 2
+    ramp = torch.linspace(0, 40, n, device="cuda") if order == "rising" else torch.linspace(40, 0, n, device="cuda")
+    qn, qr, kn = normal(g, n, H, 128), normal(g, n, H, RD, scale=0.1), normal(g, n, H, 128, scale=0.05)
+    qr[..., 0] = 1
+    kr = normal(g, n, RD, scale=0.1)
+    kr[:, 0] = ramp.bfloat16()
+    v = (normal(g, n, H, 128).double() * 2.0 ** 90).bfloat16()
+    for causal in (True, False):
+        out, lse = hs.attend_expanded(qn, qr, kn, kr, v, base.cum([n]), base.cum([n]), 1.0, causal=causal)
+        base.check_expanded(qn, qr, kn, kr, v, [0, n], [0, n], 1.0, causal, out, lse)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "bf16"])
+@pytest.mark.parametrize("order", ["rising", "falling"])
+def test_rows_large_values_and_rising_scores(fmt, order):
+    g = gen(92)
+    n, H = 700, 20
+    ramp = torch.linspace(0, 40, n, device="cuda") if order == "rising" else torch.linspace(40, 0, n, device="cuda")
+    rope = normal(g, n, RD)
+    rope[:, 0] = ramp.bfloat16()
+    lat = normal(g, n, D).double() * 2.0 ** 90
+    t = torch.zeros((11, 64, base.FMT[fmt]), dtype=torch.uint8, device="cuda")
+    t.reshape(704, -1)[:n] = base.rows_bytes(lat, rope, "bf16") if fmt == "bf16" else base.rows_bytes(lat, rope * 2.0 ** 80, "fp8")
+    pool = hs.Pool([t])
+    T = 160   # tokens enough that a CTA has a unit's tiles one after the other
+    rows = torch.arange(n, device="cuda").int()[None].repeat(T, 1).contiguous()
+    ql, qr = torch.zeros((T, H, D), dtype=torch.bfloat16, device="cuda"), torch.zeros((T, H, RD), dtype=torch.bfloat16, device="cuda")
+    qr[:, :, 0] = 1.0 if fmt == "bf16" else 2.0 ** -80
+    out, lse = hs.attend_rows(pool, rows, ql, qr, 1.0)
+    for i in range(0, T, 13):
+        check(t.reshape(704, -1), fmt, rows[i], ql[i], qr[i], 1.0, out[i], lse[i])
+
+
+# --------------------------------------------------------------------------------------------------------------------
 # query tokens of no sequence
 
 
