@@ -978,8 +978,9 @@ __global__ void __launch_bounds__(128 * kJoinCols) combine_kernel(const AttendPa
 }
 
 template <int N, int kRowBytes>
-cudaError_t launch(const AttendParams& p, int sms, cudaStream_t s) {
-  static const cudaError_t ready = [] {
+cudaError_t launch(const AttendParams& p, int dev, int sms, cudaStream_t s) {
+  static DeviceOnce once;
+  const cudaError_t ready = once.ready(dev, [] {
     cudaFuncAttributes a{};
     cudaError_t e = cudaFuncGetAttributes(&a, attend_kernel<N, kRowBytes>);
     // the register trade waits for ever if the launch has fewer than it hands out
@@ -987,7 +988,7 @@ cudaError_t launch(const AttendParams& p, int sms, cudaStream_t s) {
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(attend_kernel<N, kRowBytes>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<N>::kBytes);
     return e;
-  }();
+  });
   if (ready != cudaSuccess) return ready;
   const int groups = (p.cols + N - 1) / N;
   // a rows call knows its tiles; a pages call learns them on the device
@@ -1019,19 +1020,19 @@ cudaError_t launch(const AttendParams& p, int sms, cudaStream_t s) {
 }
 
 template <int kRowBytes>
-cudaError_t launch_cols(const AttendParams& p, int sms, cudaStream_t s) {
-  if (p.cols <= 16) return launch<16, kRowBytes>(p, sms, s);
-  if (p.cols <= 32) return launch<32, kRowBytes>(p, sms, s);
-  return launch<64, kRowBytes>(p, sms, s);
+cudaError_t launch_cols(const AttendParams& p, int dev, int sms, cudaStream_t s) {
+  if (p.cols <= 16) return launch<16, kRowBytes>(p, dev, sms, s);
+  if (p.cols <= 32) return launch<32, kRowBytes>(p, dev, sms, s);
+  return launch<64, kRowBytes>(p, dev, sms, s);
 }
 
 }  // namespace
 
 size_t attend_workspace_bytes(int sms) { return ws_run_offset(sms) + (size_t)sms * sizeof(RunStart); }
 
-cudaError_t launch_attend(const AttendParams& p, int sms, cudaStream_t s) {
-  return p.row_bytes == HS_ROW_BYTES_FP8 ? launch_cols<HS_ROW_BYTES_FP8>(p, sms, s)
-                                         : launch_cols<HS_ROW_BYTES_BF16>(p, sms, s);
+cudaError_t launch_attend(const AttendParams& p, int dev, int sms, cudaStream_t s) {
+  return p.row_bytes == HS_ROW_BYTES_FP8 ? launch_cols<HS_ROW_BYTES_FP8>(p, dev, sms, s)
+                                         : launch_cols<HS_ROW_BYTES_BF16>(p, dev, sms, s);
 }
 
 }  // namespace hs

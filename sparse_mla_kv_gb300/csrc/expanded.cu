@@ -611,15 +611,16 @@ bool make_map(CUtensorMap* map, const void* base, int64_t dims, int64_t heads, i
 
 }  // namespace
 
-cudaError_t launch_expanded(const hs_expanded& a, int sms, cudaStream_t s) {
-  static const cudaError_t ready = [] {
+cudaError_t launch_expanded(const hs_expanded& a, int dev, int sms, cudaStream_t s) {
+  static DeviceOnce once;
+  const cudaError_t ready = once.ready(dev, [] {
     cudaFuncAttributes f{};
     cudaError_t e = cudaFuncGetAttributes(&f, expanded_kernel);
     // the register trade waits for ever if the launch has fewer than it hands out
     if (e == cudaSuccess && f.numRegs != kRegsLaunch) e = cudaErrorInvalidKernelImage;
     if (e == cudaSuccess) e = cudaFuncSetAttribute(expanded_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     return e;
-  }();
+  });
   if (ready != cudaSuccess) return ready;
   Maps m;
   // a head stride of zero broadcasts one head: a map of one head, read at head 0

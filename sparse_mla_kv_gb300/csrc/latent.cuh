@@ -4,6 +4,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "device_once.cuh"
 #include "hs_internal.cuh"
 #include "hs_latent.h"
 
@@ -59,10 +60,11 @@ struct AttendParams {
   int32_t* status;
   float* workspace;
 };
-cudaError_t launch_attend(const AttendParams& p, int sms, cudaStream_t s);
+// dev: the current device, sms its number of SMs.
+cudaError_t launch_attend(const AttendParams& p, int dev, int sms, cudaStream_t s);
 size_t attend_workspace_bytes(int sms);
 
-cudaError_t launch_expanded(const hs_expanded& a, int sms, cudaStream_t s);
+cudaError_t launch_expanded(const hs_expanded& a, int dev, int sms, cudaStream_t s);
 
 // Records a data error: the status word keeps the largest code seen.
 __device__ __forceinline__ void report(int32_t* status, int32_t code) {

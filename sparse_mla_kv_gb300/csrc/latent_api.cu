@@ -114,7 +114,7 @@ hs_status hs_attend_rows(const hs_pool* pool, int32_t layer, const int32_t* rows
   p.items = (int32_t)tokens;
   p.P = 1;
   p.cols = a->heads;
-  return status_of(hs::launch_attend(p, v.sms, stream));
+  return status_of(hs::launch_attend(p, v.device, v.sms, stream));
 }
 
 hs_status hs_attend_pages(const hs_pool* pool, int32_t layer, const int32_t* block_table, const int32_t* ctx_len,
@@ -139,7 +139,7 @@ hs_status hs_attend_pages(const hs_pool* pool, int32_t layer, const int32_t* blo
   p.items = R;
   p.P = P;
   p.cols = P * a->heads;
-  return status_of(hs::launch_attend(p, v.sms, stream));
+  return status_of(hs::launch_attend(p, v.device, v.sms, stream));
 }
 
 hs_status hs_attend_expanded(const hs_expanded* a, hs_stream_t stream) {
@@ -168,7 +168,7 @@ hs_status hs_attend_expanded(const hs_expanded* a, hs_stream_t stream) {
   }
   const int sms = hs::device_sms(dev);
   if (sms <= 0) return HS_ERR_CUDA;
-  return status_of(hs::launch_expanded(*a, sms, stream));
+  return status_of(hs::launch_expanded(*a, dev, sms, stream));
 }
 
 }  // extern "C"

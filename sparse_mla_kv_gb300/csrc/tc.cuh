@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace hs {
 namespace tc {
 
@@ -59,17 +61,18 @@ __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.a
 typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-// The driver's encoder of tensor maps, or nullptr.
+// The driver's encoder of tensor maps, or nullptr (not kept: the next call asks again).
 inline EncodeTiled encode_tiled() {
-  static const EncodeTiled encode = [] {
-    void* f = nullptr;
+  static std::atomic<void*> encode{nullptr};
+  void* f = encode.load();
+  if (!f) {
     cudaDriverEntryPointQueryResult found;
     if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
         found != cudaDriverEntryPointSuccess)
-      f = nullptr;
-    return reinterpret_cast<EncodeTiled>(f);
-  }();
-  return encode;
+      return nullptr;
+    encode.store(f);
+  }
+  return reinterpret_cast<EncodeTiled>(f);
 }
 
 // ---- tensor memory ----
