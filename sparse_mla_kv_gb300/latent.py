@@ -5,7 +5,8 @@
   attend_pages     absorbed latent attention over whole contexts through a block table
   attend_expanded  attention over keys and values expanded to every head (prompts)
 
-Thin marshalling like the rest of the binding: no CPU fallback, every refusal of the library raises."""
+Thin marshalling like the rest of the binding: no CPU fallback, every refusal of the library raises.  All tensors of a call
+must be on the current device."""
 from __future__ import annotations
 
 import ctypes
@@ -13,10 +14,11 @@ from typing import Optional
 
 import torch
 
-from . import Pool, _check, _dev_i32, _opt, lib
+from . import Pool, _check, lib
 
 LATENT_DIM, ROPE_DIM, NOPE_DIM, VALUE_DIM = 512, 64, 128, 128
 ROW_BYTES_FP8, ROW_BYTES_BF16 = 656, 1152
+_I32 = torch.int32
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 _i32, _i64, _p, _f = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float
@@ -65,11 +67,32 @@ def _lib():
     return _bound
 
 
-def _tensor(t: torch.Tensor, name: str, shape: tuple, dtype=torch.bfloat16) -> tuple:
-    """The strides of a CUDA tensor of this shape and type whose last dimension is contiguous."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_cuda:
-        if not isinstance(t, torch.Tensor) or t.dtype is not dtype or not t.is_cuda:
-            raise TypeError(f"{name} must be a {dtype} CUDA tensor")
+_current_device = torch._C._cuda_getDevice
+
+
+def _here(t: torch.Tensor, name: str) -> int:
+    """The device that all of a call's tensors must be on: that of its first one, which must be the current device (the
+    kernels are launched there)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    dev = t.get_device()
+    if dev != _current_device():
+        raise ValueError(f"{name} is on device {dev}, but device {_current_device()} is current")
+    return dev
+
+
+def _refuse(t, name: str, dev: int, dtype):
+    """Raises what is wrong with the type or the device of a tensor, if it is one of these."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or not t.is_cuda:
+        raise TypeError(f"{name} must be a {dtype} CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on device {t.get_device()}, not on device {dev} with the other tensors")
+
+
+def _tensor(t: torch.Tensor, name: str, shape: tuple, dev: int, dtype=torch.bfloat16) -> tuple:
+    """The strides of a tensor of this shape, type and device whose last dimension is contiguous."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _refuse(t, name, dev, dtype)
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     strides = t.stride()
     if strides[-1] != 1 and t.numel():
@@ -77,9 +100,11 @@ def _tensor(t: torch.Tensor, name: str, shape: tuple, dtype=torch.bfloat16) -> t
     return strides
 
 
-def _f32(t: Optional[torch.Tensor], name: str, shape: tuple):
-    if t.dtype is not torch.float32 or t.shape != shape or not t.is_cuda or not t.is_contiguous():
-        raise TypeError(f"{name} must be a contiguous float32 CUDA tensor of shape {tuple(shape)}")
+def _whole(t: torch.Tensor, name: str, dtype, dev: int, shape=None) -> int:
+    """The address of a contiguous tensor of this type and device (and shape)."""
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous() or (shape is not None and t.shape != shape):
+        _refuse(t, name, dev, dtype)
+        raise TypeError(f"{name} must be contiguous" + (f" and have shape {tuple(shape)}" if shape is not None else ""))
     return t.data_ptr()
 
 
@@ -110,8 +135,9 @@ def append_rows(pool: Pool, rows: torch.Tensor, latent: torch.Tensor, rope: torc
     if dt is None:
         raise TypeError("latent must be bf16, fp16 or fp32")
     dtype = latent.dtype
-    latent_stride = _tensor(latent, "latent", (n, LATENT_DIM), dtype)[0]
-    rope_stride = _tensor(rope, "rope", (n, ROPE_DIM), dtype)[0]
+    dev = _here(latent, "latent")
+    latent_stride = _tensor(latent, "latent", (n, LATENT_DIM), dev, dtype)[0]
+    rope_stride = _tensor(rope, "rope", (n, ROPE_DIM), dev, dtype)[0]
     if positions.numel() != n:
         raise ValueError("positions must have one entry per row")
     if rotation.dim() != 2 or rotation.shape[1] != ROPE_DIM:
@@ -119,17 +145,18 @@ def append_rows(pool: Pool, rows: torch.Tensor, latent: torch.Tensor, rope: torc
     heads, q, qo = 0, (None, 0, 0), (None, 0, 0)
     if q_rope is not None:
         heads = int(q_rope.shape[1]) if q_rope.dim() == 3 else -1
-        st = _tensor(q_rope, "q_rope", (n, heads, ROPE_DIM), dtype)
+        st = _tensor(q_rope, "q_rope", (n, heads, ROPE_DIM), dev, dtype)
         q = (q_rope.data_ptr(), st[0], st[1])
         if q_out is None:
             q_out = _empty((n, heads, ROPE_DIM), dtype, q_rope.device, stream)
-        st = _tensor(q_out, "q_out", (n, heads, ROPE_DIM), dtype)
+        st = _tensor(q_out, "q_out", (n, heads, ROPE_DIM), dev, dtype)
         qo = (q_out.data_ptr(), st[0], st[1])
     elif q_out is not None:
         raise ValueError("q_out without q_rope")
-    a = AppendC(n, _dev_i32(rows, "rows"), _dev_i32(positions, "positions"),
-                _f32(rotation, "rotation", rotation.shape), rotation.shape[0], bool(interleaved), dt, heads,
-                latent.data_ptr(), latent_stride, rope.data_ptr(), rope_stride, *q, *qo, _opt(status, "status"))
+    a = AppendC(n, _whole(rows, "rows", _I32, dev), _whole(positions, "positions", _I32, dev),
+                _whole(rotation, "rotation", torch.float32, dev), rotation.shape[0], bool(interleaved), dt, heads,
+                latent.data_ptr(), latent_stride, rope.data_ptr(), rope_stride, *q, *qo,
+                status if status is None else _whole(status, "status", _I32, dev))
     _check(_lib().hs_append_rows(pool.handle, int(layer), ctypes.byref(a), _on(stream, latent)), "hs_append_rows")
     return q_out
 
@@ -149,26 +176,27 @@ def _attend(lead: tuple, q_latent, q_rope, scale, out, lse, status, workspace, s
     """Marshals an absorbed call whose query tensors have the leading dimensions `lead` (tokens) and heads."""
     k = len(lead)
     heads = q_latent.shape[k] if q_latent.dim() == k + 2 else -1
+    dev = _here(q_latent, "q_latent")
     shape, device = (*lead, heads, LATENT_DIM), q_latent.device
-    sl = _tensor(q_latent, "q_latent", shape)
-    sr = _tensor(q_rope, "q_rope", (*lead, heads, ROPE_DIM))
+    sl = _tensor(q_latent, "q_latent", shape, dev)
+    sr = _tensor(q_rope, "q_rope", (*lead, heads, ROPE_DIM), dev)
     if out is None:
         out = _empty(shape, torch.bfloat16, device, stream)
-    so = _tensor(out, "out", shape)
+    so = _tensor(out, "out", shape, dev)
     if lse is None:
         lse = _empty((*lead, heads), torch.float32, device, stream)
     if workspace is None:
         workspace = _empty((max(16, attend_workspace_bytes()),), torch.uint8, device, stream)
-    if workspace.dtype is not torch.uint8 or not workspace.is_cuda or not workspace.is_contiguous():
-        raise TypeError("workspace must be a contiguous uint8 CUDA tensor")
+    ws = (_whole(workspace, "workspace", torch.uint8, dev), workspace.numel())
     token = (sl[0], sr[0], so[0])
     if k == 2 and lead[1] > 1:  # [requests][positions]: the two must merge into one dimension of tokens
         if lead[0] > 1 and (sl[0] != lead[1] * sl[1] or sr[0] != lead[1] * sr[1] or so[0] != lead[1] * so[1]):
             raise ValueError("the two leading dimensions of q_latent, q_rope and out must merge into one")
         token = (sl[1], sr[1], so[1])
     a = AttendC(heads, scale, q_latent.data_ptr(), token[0], sl[k], q_rope.data_ptr(), token[1], sr[k], out.data_ptr(),
-                token[2], so[k], _f32(lse, "lse", (*lead, heads)), _opt(status, "status"))
-    return a, out, lse, workspace
+                token[2], so[k], _whole(lse, "lse", torch.float32, dev, (*lead, heads)),
+                status if status is None else _whole(status, "status", _I32, dev))
+    return a, out, lse, ws, dev
 
 
 def attend_rows(pool: Pool, rows: torch.Tensor, q_latent: torch.Tensor, q_rope: torch.Tensor, scale: float, *,
@@ -179,9 +207,9 @@ def attend_rows(pool: Pool, rows: torch.Tensor, q_latent: torch.Tensor, q_rope: 
     if rows.dim() != 2:
         raise ValueError("rows must be [tokens][K]")
     n, K = rows.shape
-    a, out, lse, ws = _attend((n,), q_latent, q_rope, scale, out, lse, status, workspace, stream)
-    _check(_lib().hs_attend_rows(pool.handle, int(layer), _dev_i32(rows, "rows"), n, K, ctypes.byref(a),
-                                 ws.data_ptr(), ws.numel(), _on(stream, q_latent)), "hs_attend_rows")
+    a, out, lse, ws, dev = _attend((n,), q_latent, q_rope, scale, out, lse, status, workspace, stream)
+    _check(_lib().hs_attend_rows(pool.handle, int(layer), _whole(rows, "rows", _I32, dev), n, K, ctypes.byref(a),
+                                 *ws, _on(stream, q_latent)), "hs_attend_rows")
     return out, lse
 
 
@@ -197,10 +225,10 @@ def attend_pages(pool: Pool, block_table: torch.Tensor, ctx_len: torch.Tensor, q
     R, P = int(q_latent.shape[0]), int(q_latent.shape[1])
     if block_table.shape[0] != R or ctx_len.numel() != R:
         raise ValueError("block_table and ctx_len must have one entry per request")
-    a, out, lse, ws = _attend((R, P), q_latent, q_rope, scale, out, lse, status, workspace, stream)
-    _check(_lib().hs_attend_pages(pool.handle, int(layer), _dev_i32(block_table, "block_table"),
-                                  _dev_i32(ctx_len, "ctx_len"), R, P, int(block_table.shape[1]), ctypes.byref(a),
-                                  ws.data_ptr(), ws.numel(), _on(stream, q_latent)), "hs_attend_pages")
+    a, out, lse, ws, dev = _attend((R, P), q_latent, q_rope, scale, out, lse, status, workspace, stream)
+    _check(_lib().hs_attend_pages(pool.handle, int(layer), _whole(block_table, "block_table", _I32, dev),
+                                  _whole(ctx_len, "ctx_len", _I32, dev), R, P, int(block_table.shape[1]), ctypes.byref(a),
+                                  *ws, _on(stream, q_latent)), "hs_attend_pages")
     return out, lse
 
 
@@ -215,21 +243,24 @@ def attend_expanded(q_nope: torch.Tensor, q_rope: torch.Tensor, k_nope: torch.Te
     if q_nope.dim() != 3 or k_rope.dim() != 2:
         raise ValueError("q_nope must be [Tq][heads][128] and k_rope [Tk][64]")
     Tq, H, Tk = int(q_nope.shape[0]), int(q_nope.shape[1]), int(k_rope.shape[0])
-    sqn = _tensor(q_nope, "q_nope", (Tq, H, NOPE_DIM))
-    sqr = _tensor(q_rope, "q_rope", (Tq, H, ROPE_DIM))
-    skn = _tensor(k_nope, "k_nope", (Tk, H, NOPE_DIM))
-    skr = _tensor(k_rope, "k_rope", (Tk, ROPE_DIM))
-    sv = _tensor(v, "v", (Tk, H, VALUE_DIM))
+    dev = _here(q_nope, "q_nope")
+    sqn = _tensor(q_nope, "q_nope", (Tq, H, NOPE_DIM), dev)
+    sqr = _tensor(q_rope, "q_rope", (Tq, H, ROPE_DIM), dev)
+    skn = _tensor(k_nope, "k_nope", (Tk, H, NOPE_DIM), dev)
+    skr = _tensor(k_rope, "k_rope", (Tk, ROPE_DIM), dev)
+    sv = _tensor(v, "v", (Tk, H, VALUE_DIM), dev)
     if cu_q.numel() < 1 or cu_q.numel() != cu_k.numel():
         raise ValueError("cu_q and cu_k must both have one entry more than there are sequences")
     if out is None:
         out = _empty((Tq, H, VALUE_DIM), torch.bfloat16, q_nope.device, stream)
-    so = _tensor(out, "out", (Tq, H, VALUE_DIM))
+    so = _tensor(out, "out", (Tq, H, VALUE_DIM), dev)
     if lse is None:
         lse = _empty((Tq, H), torch.float32, q_nope.device, stream)
-    a = ExpandedC(cu_q.numel() - 1, H, bool(causal), scale, Tq, Tk, _dev_i32(cu_q, "cu_q"), _dev_i32(cu_k, "cu_k"),
+    a = ExpandedC(cu_q.numel() - 1, H, bool(causal), scale, Tq, Tk, _whole(cu_q, "cu_q", _I32, dev),
+                  _whole(cu_k, "cu_k", _I32, dev),
                   q_nope.data_ptr(), sqn[0], sqn[1], q_rope.data_ptr(), sqr[0], sqr[1], k_nope.data_ptr(), skn[0], skn[1],
                   k_rope.data_ptr(), skr[0], v.data_ptr(), sv[0], sv[1], out.data_ptr(), so[0], so[1],
-                  _f32(lse, "lse", (Tq, H)), _opt(status, "status"))
+                  _whole(lse, "lse", torch.float32, dev, (Tq, H)),
+                  status if status is None else _whole(status, "status", _I32, dev))
     _check(_lib().hs_attend_expanded(ctypes.byref(a), _on(stream, q_nope)), "hs_attend_expanded")
     return out, lse
