@@ -1,7 +1,7 @@
 """Build libhs.so in-tree with nvcc for sm_103a (no cmake; translation units compiled in parallel).
 
 build(variant="checked") builds the bounds-checked library, libhs_checked.so (HS_CHECKED=1), into its
-own object folder."""
+own object folder; build(variant="timeout") one whose bounded waits run out at once, for their test."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -27,7 +27,7 @@ def _stale(out: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-VARIANTS = {"": (), "checked": ("-DHS_CHECKED=1",)}
+VARIANTS = {"": (), "checked": ("-DHS_CHECKED=1",), "timeout": ("-DHS_WAIT_CYCLES=0",)}
 
 
 def lib_path(variant: str = "") -> str:

@@ -481,7 +481,7 @@ __device__ __forceinline__ void issue_scores(const AttendParams& p, uint32_t bas
   }
   // nothing of this CTA's products is in flight when the others leave
   tc::commit(bars + 8 * kDrain, leader);
-  tc::Waiter drain;
+  tc::Drain drain;
   drain.wait(bars + 8 * kDrain, 0);
   __syncwarp();
 }
@@ -543,7 +543,7 @@ __device__ __forceinline__ void issue_results(const AttendParams& p, uint32_t ba
     if (first || cur.left == 0) tc::commit(bars + 8 * kOFull, leader);
   }
   tc::commit(bars + 8 * (kDrain + 1), leader);
-  tc::Waiter drain;
+  tc::Drain drain;
   drain.wait(bars + 8 * (kDrain + 1), 0);
   __syncwarp();
 }

@@ -144,18 +144,21 @@ __device__ __forceinline__ void load3(uint32_t dst, const CUtensorMap* map, int 
 }
 
 // ---- loads (one lane) ----
-__device__ __forceinline__ void load_items(const hs_expanded& a, const Maps& m, uint32_t q, uint32_t ring, uint32_t bars) {
+// Bytes are announced only on a barrier whose phase before is complete.  In order that is so already (a part's barrier had its
+// last use four parts ago, and units of later parts have been released since); the waits for it matter when another warp's
+// wait gave up, which releases units early.  After a wait that gave up nothing more is announced.
+struct Loader {
   tc::Waiter w;
-  const bool leader = tc::elect();
-  uint32_t u = 0, count = 0, group = 0;  // units, items, key tiles so far
-  Item it;
-  Finder f;
-  f.start(a);
-  for (int k = 0; f.find(a, item_number(k), &it); ++k) {
-    if (it.most() <= 0) continue;
-    if (count > 0) w.wait(bars + 8 * kQEmpty, (count - 1) & 1);
-    ++count;
-    __syncwarp();
+  uint32_t u = 0, items = 0, parts = 0;  // units, items, parts (keys or values of a key tile) so far
+
+  // One item's queries, keys and values; false after a wait that gave up.
+  __device__ __forceinline__ bool load(const Maps& m, const Item& it, uint32_t q, uint32_t ring, uint32_t bars, bool leader) {
+    if (items > 0) {
+      w.wait(bars + 8 * kQEmpty, (items - 1) & 1);
+      w.wait(bars + 8 * kQFull, (items - 1) & 1);
+    }
+    if (__any_sync(0xFFFFFFFFu, w.dead)) return false;
+    ++items;
     const int hq = it.head * m.head_step[0], hr = it.head * m.head_step[1], hk = it.head * m.head_step[2],
               hv = it.head * m.head_step[3];
     if (leader) {
@@ -170,17 +173,22 @@ __device__ __forceinline__ void load_items(const hs_expanded& a, const Maps& m, 
     }
     const int tiles = it.most();
 #pragma unroll 1
-    for (int j = 0; j < tiles; ++j, ++group) {
+    for (int j = 0; j < tiles; ++j) {
       const int row = it.k0 + j * kKeys;
 #pragma unroll 1
       for (int i = 0; i < kUnits; ++i, ++u) {
         const uint32_t slot = u % kRing;
         if (u >= kRing) w.wait(bars + 8 * (kEmpty + slot), (u / kRing - 1) & 1);
+        const bool begins = i == 0 || i == kUnitsK;
+        if (begins) {
+          if (parts >= kGroups) w.wait(bars + 8 * (kFull + parts % kGroups), (parts / kGroups - 1) & 1);
+          if (__any_sync(0xFFFFFFFFu, w.dead)) return false;
+          ++parts;
+        }
         __syncwarp();
         if (leader) {
-          // (a group's barrier is free: its last use was four groups ago, and their units have been released since)
-          const uint32_t bar = bars + 8 * (kFull + (2 * group + (i >= kUnitsK)) % kGroups), to = ring + slot * kUnit;
-          if (i == 0 || i == kUnitsK) tc::mbar_expect(bar, (i == 0 ? kUnitsK : kUnitsV) * kUnit);
+          const uint32_t bar = bars + 8 * (kFull + (parts - 1) % kGroups), to = ring + slot * kUnit;
+          if (begins) tc::mbar_expect(bar, (i == 0 ? kUnitsK : kUnitsV) * kUnit);
           if (i < 2)
             load3(to, &m.k_nope, 64 * i, hk, row, bar);
           else if (i == 2)
@@ -190,13 +198,24 @@ __device__ __forceinline__ void load_items(const hs_expanded& a, const Maps& m, 
         }
       }
     }
+    return true;
   }
+};
+
+__device__ __forceinline__ void load_items(const hs_expanded& a, const Maps& m, uint32_t q, uint32_t ring, uint32_t bars) {
+  const bool leader = tc::elect();
+  Loader l;
+  Item it;
+  Finder f;
+  f.start(a);
+  for (int k = 0; f.find(a, item_number(k), &it); ++k)
+    if (it.most() > 0 && !l.load(m, it, q, ring, bars, leader)) break;
   // no copy is in flight when the CTA ends
-  tc::Waiter drain;
-  for (uint32_t r = 2 * group > kGroups ? 2 * group - kGroups : 0; r < 2 * group; ++r)
+  tc::Drain drain;
+  for (uint32_t r = l.parts > kGroups ? l.parts - kGroups : 0; r < l.parts; ++r)
     drain.wait(bars + 8 * (kFull + r % kGroups), (r / kGroups) & 1);
-  if (count > 0) drain.wait(bars + 8 * kQFull, (count - 1) & 1);
-  if (w.dead) report(a.status, HS_ERR_TIMEOUT);
+  if (l.items > 0) drain.wait(bars + 8 * kQFull, (l.items - 1) & 1);
+  if (l.w.dead) report(a.status, HS_ERR_TIMEOUT);
 }
 
 // ---- products (one warp a query tile) ----
@@ -297,7 +316,7 @@ __device__ __forceinline__ void issue_items(const hs_expanded& a, int t, uint32_
     base += tiles * kUnits;
   }
   tc::commit(bars + 8 * (kDrain + t), leader);
-  tc::Waiter drain;
+  tc::Drain drain;
   drain.wait(bars + 8 * (kDrain + t), 0);
   __syncwarp();
   if (w.dead) report(a.status, HS_ERR_TIMEOUT);

@@ -36,23 +36,45 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-// Waits are bounded: one that has not ended after kWaitCycles SM cycles (seconds) gives up, and from then on
+// The same without suspending the thread.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// Waits are bounded: one that has not ended after kLimit SM cycles (seconds) gives up, and from then on
 // every wait of that thread returns at once, so that the kernel runs to its end; `dead` says so and the caller
-// reports HS_ERR_TIMEOUT.  Everything a kernel accesses stays in bounds whatever the waits return.
-constexpr long long kWaitCycles = 4000000000LL;
-struct Waiter {
+// reports HS_ERR_TIMEOUT.  Everything a kernel accesses stays in bounds whatever the waits return.  Who starts copies on a
+// barrier must stop when a wait has given up: a phase must not be announced before the one before it is complete.
+// HS_WAIT_CYCLES sets the limit for a build in which waits run out; the drains at a kernel's end, which wait for its own copies
+// and products in flight, keep theirs.
+#ifndef HS_WAIT_CYCLES
+#define HS_WAIT_CYCLES 4000000000LL
+#endif
+template <long long kLimit>
+struct BoundedWait {
   bool dead = false;
   __device__ __forceinline__ void wait(uint32_t bar, uint32_t parity) {
-    if (dead || mbar_try(bar, parity)) return;
+    // (a try suspends the thread for a while, which may be longer than a short limit)
+    if (dead || (kLimit < 1000 ? mbar_test(bar, parity) : mbar_try(bar, parity))) return;
     const long long t0 = clock64();
-    while (!mbar_try(bar, parity)) {
-      if (clock64() - t0 > kWaitCycles) {
+    while (!(kLimit < 1000 ? mbar_test(bar, parity) : mbar_try(bar, parity))) {
+      if (clock64() - t0 > kLimit) {
         dead = true;
         return;
       }
     }
   }
 };
+using Waiter = BoundedWait<HS_WAIT_CYCLES>;
+using Drain = BoundedWait<4000000000LL>;
 
 // Makes this thread's generic stores to shared memory visible to the tensor core and the copy engine.
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
