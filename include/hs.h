@@ -390,7 +390,7 @@ int64_t hs_launch_count(void);
  * output position) is checked against the extent of its buffer before the access, and a violation
  * skips the access and is recorded.  Synchronises the current device, then returns the site of the
  * first violation recorded since the previous call and clears it:
- *   0 none; 1 table page; 2 hot-state slot; 3 miss-list index; 4 GPU pool row; 5 host pool row;
+ *   0 none; 1 table page or list position; 2 hot-state slot; 3 miss-list index; 4 GPU pool row; 5 host pool row;
  *   6 output position; 7 repeat-chain link; -2 the device or the record could not be read.
  * Returns -1 in the normal build, which compiles these checks away (its data errors are reported
  * through the status words described above). */

@@ -16,6 +16,8 @@
 // x 64 heads 102 us, 5.9 TB/s.  More resident warps with fewer registers (10 or 12 blocks an SM) took 43 and 54 us.
 #include "latent.cuh"
 
+HS_CHECK_WORD
+
 namespace hs {
 namespace {
 
@@ -195,7 +197,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
   }
   const bool row_ok = row >= 0 && row < p.num_rows;
   if (lane == 0 && ((row != -1 && !row_ok) || !pos_ok)) report(a.status, HS_ERR_ID_RANGE);
-  if (!row_ok || !pos_ok) return;
+  if (!row_ok || !pos_ok || !HS_CHECK((int64_t)row * p.row_bytes + p.row_bytes <= p.num_rows * p.row_bytes, kChkPoolRow)) return;
   uint8_t* dst = p.base + (int64_t)row * p.row_bytes;
   float x[16];
   in[0].values(x);
@@ -244,6 +246,20 @@ void launch_heads(const AppendParams& p, cudaStream_t s) {
 }
 
 }  // namespace
+
+uint32_t check_take_append() {
+#if HS_CHECKED
+  unsigned v = 0u, z = 0u;
+  if (cudaMemcpyFromSymbol(&v, hs_check_word_, sizeof(v)) != cudaSuccess ||
+      cudaMemcpyToSymbol(hs_check_word_, &z, sizeof(z)) != cudaSuccess) {
+    cudaGetLastError();
+    return 0xFFFFFFFFu;
+  }
+  return v;
+#else
+  return 0u;
+#endif
+}
 
 cudaError_t launch_append(const AppendParams& p, int sms, cudaStream_t s) {
   // few tokens are spread further (512 x 64 heads: 2.9 us with 8 heads a warp and 3.4 with 16); many take fewer reads of the

@@ -53,6 +53,8 @@
 #include "latent.cuh"
 #include "tc.cuh"
 
+HS_CHECK_WORD
+
 namespace hs {
 namespace {
 
@@ -147,16 +149,18 @@ struct Entry {
     if (p.paged) {
       const int page = k / p.page_size;
       in_page = k - page * p.page_size;
-      value = __ldg(p.table + (int64_t)cur.item * p.max_pages + page);
+      if (HS_CHECK(cur.item < p.items && page < p.max_pages, kChkTablePage))
+        value = __ldg(p.table + (int64_t)cur.item * p.max_pages + page);
     } else {
-      value = __ldg(p.rows + (int64_t)cur.item * p.K + k);
+      if (HS_CHECK(cur.item < p.items && k < p.K, kChkTablePage)) value = __ldg(p.rows + (int64_t)cur.item * p.K + k);
     }
   }
   // The key's row, or -1; bad (a data error) is set when the entry is not a valid one.
   __device__ __forceinline__ int row(const AttendParams& p, bool& bad) const {
     const bool in = value >= 0 && value < (p.paged ? (int64_t)p.num_blocks : p.num_rows);
     bad |= there && counts && !in && (p.paged || value != -1);
-    return !in ? -1 : p.paged ? value * p.page_size + in_page : value;
+    const int r = !in ? -1 : p.paged ? value * p.page_size + in_page : value;
+    return HS_CHECK(r >= -1 && r < p.num_rows, kChkPoolRow) ? r : -1;
   }
 };
 
@@ -734,14 +738,15 @@ __device__ __forceinline__ void softmax(const AttendParams& p, uint32_t base, ui
     bar_softmax();
     const int part = 2 * blockIdx.x + (first_run && !at_start ? 0 : 1);
     first_run = false;
+    const bool in_place = HS_CHECK(item < p.items && group * N < p.cols && part < 2 * sms, kChkOutPos);
     if (tid < N) {
       const float sum = (red[tid] + red[N + tid]) + (red[2 * N + tid] + red[3 * N + tid]);
       const float lse2 = sum == 0.f ? -INFINITY : log2f(sum) - nref[tid] + (kF16 ? kSumShift : 0);
       alpha[tid] = sum == 0.f ? 0.f : (kF16 ? 1.f / (1 << kSumShift) : 1.f) / sum;
       if (!whole) {
         float* z = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(p.workspace) + ws_lse_offset(sms));
-        z[part * kMaxCols + tid] = lse2;
-      } else if (p.lse && tid < ncols) {
+        if (in_place) z[part * kMaxCols + tid] = lse2;
+      } else if (p.lse && tid < ncols && in_place) {
         p.lse[(int64_t)item * p.cols + group * N + tid] = lse2 * kLn2;
       }
     }
@@ -765,7 +770,8 @@ __device__ __forceinline__ void softmax(const AttendParams& p, uint32_t base, ui
       if (!whole) {
         float* z = p.workspace + ((int64_t)part * kMaxCols + c0) * kLatent + 128 * g + dim;
 #pragma unroll
-        for (int c = 0; c < kW; ++c) z[c * kLatent] = o[c];
+        for (int c = 0; c < kW; ++c)
+          if (in_place) z[c * kLatent] = o[c];
       } else {
         // pairs of lanes exchange so that each writes two neighbouring dimensions of one column
         __nv_bfloat16* dst = p.out + 128 * g + (dim - odd);
@@ -773,7 +779,7 @@ __device__ __forceinline__ void softmax(const AttendParams& p, uint32_t base, ui
         for (int c = 0; c < kW; c += 2) {
           const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? o[c] : o[c + 1], 1);
           const uint32_t two = odd ? tc::pack_bf16(got, o[c + 1]) : tc::pack_bf16(o[c], got);
-          if (c0 + c + odd < ncols) *reinterpret_cast<uint32_t*>(dst + offsets[c0 + c + odd]) = two;
+          if (c0 + c + odd < ncols && in_place) *reinterpret_cast<uint32_t*>(dst + offsets[c0 + c + odd]) = two;
         }
       }
     }
@@ -942,6 +948,7 @@ __global__ void __launch_bounds__(128 * kJoinCols) combine_kernel(const AttendPa
   const int last = b + __syncthreads_count(next < ctas && runs[next].begin < unit1);
   const int c = blockIdx.y * kJoinCols + threadIdx.x / 128, d = threadIdx.x % 128;
   if (c >= min(n, p.cols - group * n)) return;
+  if (!HS_CHECK(r.item >= 0 && r.item < p.items && 2 * last < 2 * sms, kChkOutPos)) return;
   float top = -INFINITY, sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int i0 = b - 1; i0 <= last; i0 += 4) {  // four parts at a time
@@ -1027,6 +1034,20 @@ cudaError_t launch_cols(const AttendParams& p, int dev, int sms, cudaStream_t s)
 }
 
 }  // namespace
+
+uint32_t check_take_attend() {
+#if HS_CHECKED
+  unsigned v = 0u, z = 0u;
+  if (cudaMemcpyFromSymbol(&v, hs_check_word_, sizeof(v)) != cudaSuccess ||
+      cudaMemcpyToSymbol(hs_check_word_, &z, sizeof(z)) != cudaSuccess) {
+    cudaGetLastError();
+    return 0xFFFFFFFFu;
+  }
+  return v;
+#else
+  return 0u;
+#endif
+}
 
 size_t attend_workspace_bytes(int sms) { return ws_run_offset(sms) + (size_t)sms * sizeof(RunStart); }
 

@@ -28,6 +28,8 @@
 #include "latent.cuh"
 #include "tc.cuh"
 
+HS_CHECK_WORD
+
 namespace hs {
 namespace {
 
@@ -512,7 +514,7 @@ __device__ __forceinline__ void softmax_items(const hs_expanded& a, float scale_
       __syncwarp();
       tc::fence_after();
     }
-    const bool there = row < it.rows;
+    const bool there = row < it.rows && HS_CHECK(it.q0 >= 0 && it.q0 + row < a.q_tokens && it.head < a.heads, kChkOutPos);
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (int64_t)(it.q0 + (there ? row : 0)) * a.out_token_stride +
                          it.head * a.out_head_stride;
 #pragma unroll 1
@@ -629,6 +631,20 @@ bool make_map(CUtensorMap* map, const void* base, int64_t dims, int64_t heads, i
 }
 
 }  // namespace
+
+uint32_t check_take_expanded() {
+#if HS_CHECKED
+  unsigned v = 0u, z = 0u;
+  if (cudaMemcpyFromSymbol(&v, hs_check_word_, sizeof(v)) != cudaSuccess ||
+      cudaMemcpyToSymbol(hs_check_word_, &z, sizeof(z)) != cudaSuccess) {
+    cudaGetLastError();
+    return 0xFFFFFFFFu;
+  }
+  return v;
+#else
+  return 0u;
+#endif
+}
 
 cudaError_t launch_expanded(const hs_expanded& a, int dev, int sms, cudaStream_t s) {
   static DeviceOnce once;

@@ -115,10 +115,13 @@ int32_t hs_check_status(void) {
     cudaGetLastError();
     return -2;
   }
-  const uint32_t a = hs::check_take_resolve();
-  const uint32_t b = hs::check_take_gather();
-  if (a == 0xFFFFFFFFu || b == 0xFFFFFFFFu) return -2;
-  return (int32_t)(a ? a : b);
+  uint32_t first = 0u;
+  for (const uint32_t site : {hs::check_take_resolve(), hs::check_take_gather(), hs::check_take_append(),
+                              hs::check_take_attend(), hs::check_take_expanded()}) {
+    if (site == 0xFFFFFFFFu) return -2;
+    if (!first) first = site;
+  }
+  return (int32_t)first;
 #else
   return -1;
 #endif

@@ -62,7 +62,7 @@ namespace hs {
 
 // Sites of the bounds-checked build's checks (the value hs_check_status returns).
 enum CheckSite : uint32_t {
-  kChkTablePage = 1,  // resolver: a page index outside the request's table row
+  kChkTablePage = 1,  // a page index outside the request's table row; attention: a position outside its list
   kChkStateSlot = 2,  // resolver: a slot index outside the unit's hot state
   kChkMissList = 3,   // resolver: a miss-list index outside the unit's list
   kChkPoolRow = 4,    // a GPU pool row outside the pool (miss destination)
@@ -73,6 +73,9 @@ enum CheckSite : uint32_t {
 // Reads and clears the check word of each kernel file (0 in the normal build).
 uint32_t check_take_resolve();
 uint32_t check_take_gather();
+uint32_t check_take_append();
+uint32_t check_take_attend();
+uint32_t check_take_expanded();
 
 // Per-layer base pointers, passed to kernels by value (kernel parameter space, no device
 // allocation).  host[] holds device-usable addresses of the pinned host pool.
