@@ -21,11 +21,13 @@
  *   HS_ROW_BYTES_BF16 (1152)  512 latent values in bf16 | 64 rotated key values in bf16.
  * Pools of other row sizes are refused (HS_ERR_INVALID_ARG).  hs_append_rows writes scales that are
  * powers of two, so that code * scale is exact in bf16; the attention calls read any finite scale and
- * round code * scale to bf16.  They multiply fp8 rows in fp16, each row divided by a power of two of its own:
- * within a row, values (rotated ones included) keep their bits down to 2^-29 of the largest that the row's
- * scales and rotated part cover and are zero below 2^-40 of it; between rows, what a row adds to a result keeps its
- * bits down to 2^-21 of the largest share and is nothing below 2^-31 of it.  The rows that one token sees may
- * differ in size by up to 2^100.  A group of zeros has no size, whatever its scale.
+ * round code * scale to bf16.  They multiply fp8 rows in fp16, rows and query columns divided by powers of two:
+ *   within a row, values (rotated ones included) keep their bits down to 2^-29 of the largest that the row's
+ *   scales and rotated part cover, and are zero below 2^-40 of it;
+ *   within a query (of one head), values keep their bits down to 2^-15 of its largest;
+ *   between rows, a weight times the row's size keeps its bits down to 2^-21 of the largest such product, and is
+ *   zero below 2^-32 of it.  The rows that one token sees may differ in size by up to 2^100.
+ * A group of zeros has no size, whatever its scale.
  *
  * Conventions: those of hs.h.  The caller owns all memory and streams; calls validate what the host can
  * see, launch on the given stream and return; data errors go to an optional device status word, which is

@@ -6,23 +6,24 @@
 //   S^T[64 keys][N]  = K[64][576] * Q^T[576][N]           (36 steps of 16)
 //   O^T[512][N]     += V^T[512][64] * P^T[64][N]           (4 row blocks x 4 steps)
 // V is the latent part of K: the same bytes, once read as a K-major and once as an M-major operand.  The softmax
-// is online with a lazy reference: weights are exp2(t), t = s - m, with any m that keeps them in range, since fp32 sums
-// have the same relative precision at every magnitude.  m starts kTop below the first tile's maximum and moves (with O
-// and the sums rescaled) only when a score exceeds it by kLazy, so the maximum over a tile's keys is rarely needed.  Sums
-// are kept per thread and joined once per unit.
+// is online with a lazy reference: weights are exp2(t - m), t the scores in log2 units, with any m that keeps them in
+// range, since fp32 sums have the same relative precision at every magnitude.  m starts kTop below the first tile's maximum
+// and moves (with O and the sums rescaled) only when a score exceeds it by kLazy, so the maximum over a tile's keys is rarely
+// needed.  Sums are kept per thread and joined once per unit.
 //
-// Types.  bf16 rows: both products in bf16 (the two operands of one product have the same type, and bf16 values have
-// fp32's range), so the weights are rounded to 8 bits: root mean square error 2.0e-3 of the results' against 1.7e-3 with 32
-// bits and one rounding.  fp8 rows (1.67e-3 against 1.66e-3): both in fp16, because an e4m3 code becomes fp16 in one instruction for two and fp16's 11 bits hold it exactly, while its
-// range is narrow: 2^-24 (with full precision 2^-14) to 2^16.  So every factor is brought into range by a power of two: a
-// row by skey (its values are code * scale / skey, its rotated part divided by it too), a query column by qs; S = S' skey
-// qs.  A key's row enters the result as its weight times skey, so what is rounded to fp16 is that product: t below is the
-// score in log2 units plus log2 skey, and the reference m follows the largest t.  A large row then counts by its share of
-// the result, and not at all where it has no weight.  The sum of the weights takes exp2(t - m) / skey in fp32; its common
-// factor 2^m cancels in the result, and the log of the sum adds m again.
+// Types.  bf16 rows: both products in bf16.  The two operands of a product have one type, and bf16 values have fp32's
+// range, so the weights are rounded to 8 bits: root mean square error 2.0e-3 of the results', against 1.7e-3 with 32 bits and
+// one rounding.  fp8 rows: both in fp16 (1.67e-3 against 1.66e-3), because an e4m3 code becomes fp16 in one instruction for
+// two and fp16's 11 bits hold it exactly, while its range is narrow: 2^-24 (with full precision 2^-14) to 2^16.  So every
+// factor is brought into range by a power of two: a row by skey (its values are code * scale / skey, its rotated part divided
+// by it too), a query column by qs; S = S' skey qs.  A row enters the result as its weight times skey, so what is rounded to
+// fp16 is that product: t above is then the score in log2 units plus log2 skey, and the reference m follows the largest t.  A
+// large row thus counts by its share of the result, and not at all where it has no weight.  The sum of the weights takes
+// exp2(t - m) / skey in fp32; its common factor 2^m cancels in the result, and the log of the sum adds m again.
 // What fp16's range costs: within a row, bits of what is below 2^-14 skey, that is 2^-29 of the largest value that skey
 // covers (a code of 448, or the rotated part where that is larger), and all of what is below 2^-25 skey; between rows, bits of
-// a weight times skey below 2^-21 of the largest.
+// a weight times skey below 2^-21 of the largest, and all of one below 2^-32; within a query column, bits of what is below
+// 2^-15 of its largest.
 //
 // Layout.  A unit is (item, group of N columns); units are cut into tiles, numbered in order, and every CTA takes
 // an equal run of tiles; a unit that several CTAs share leaves partial results in the workspace, which
@@ -31,7 +32,8 @@
 //                place (16-byte asynchronous copies) and widens fp8 codes there, so that no other warp has to be waited for;
 //   warps 16-23  softmax and results; each of the two groups of four warps has half of the columns;
 //   warp 24      issues the scores of every tile as soon as it is there;
-//   warp 25      issues the results as soon as the weights are there.
+//   warp 25      issues the results as soon as the weights are there, and zeroes what is not finite in rows that some of its
+//                columns do not see (a weight of zero does not cancel it).
 // Two tiles (64 x 576 in 16 bits, 72 KB each) and the queries (up to 72 KB) fill shared memory; the weights take the place
 // of the tile's rotated part once the scores are done.
 //
@@ -39,11 +41,11 @@
 // cycles from N = 16 to N = 64, so a call with few heads pays little for its empty columns, and more than 64 columns
 // would leave no room for the second tile.
 //
-// What bounds it.  Shared memory: a tile's copies, widening and operand reads move about 400 KB, 3100 cycles at 128 B a
-// cycle, against 2200 of products (N = 64).  Measured, 608 tokens x 2048 fp8 rows: 16 heads 289 us (2.8 TB/s of rows), 32
-// heads 295 us, 64 heads 339 us (512 TFLOP/s), that is 4.3 to 5.1 thousand cycles a tile; the producers' own chain (wait,
-// copies, 1300 cycles until they land, reading, widening, 700 to 1100 until the stores are visible) is what is left.
-// Taken back as slower, at 256 x 4 tokens of 64 heads (this form: 580 to 594 us; the tiles' number and form as given): one
+// What bounds it.  The producers' chain, not a unit of the SM: wait, copies, 1300 cycles until they land, reading, widening,
+// 700 to 1100 until the stores are visible.  Measured, 608 tokens x 2048 fp8 rows: 16 heads 290 us (2.8 TB/s of rows), 32 heads
+// 303 us, 64 heads 336 us (516 TFLOP/s), that is 4.3 to 5.1 thousand cycles a tile.  In this form a tile's copies, widening and
+// operand reads move about 400 KB in shared memory, 3100 cycles at 128 B a cycle, against 2200 of products (N = 64).
+// Taken back as slower, at 256 x 4 tokens of 64 heads (this form: 572 to 594 us; the tiles' number and form as given): one
 // 128-key tile filled in parts by copy warps 671; rows gathered by the copy engine into a ring, one 64-key tile 862 (the
 // engine takes 73 cycles a row and 80 for a gather of four, whatever their width); two tiles with copy warps of their own
 // 668; the next tile's copies issued before (606) or within (663) the widening; two teams of producers on alternate tiles

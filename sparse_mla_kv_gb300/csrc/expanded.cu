@@ -3,10 +3,10 @@
 // Mathematics.  A query row keeps a reference m, a sum l and an accumulator O over the key tiles:
 //   S = Q K^T (192 = 128 of the head + 64 of the shared rotated part), P = exp2(S scale - m), l += sum P, O += P V.
 // The reference is lazy: it starts as the first tile's maximum and moves (with l and O rescaled) only when a score exceeds
-// it by kLazy.  bf16 weights have fp32's range, so nothing is lost at the low end, and 2^kLazy leaves values of up to 2^90 room
-// in the fp32 sums.  (The weights are bf16 because the values are and both operands of a product have one type: root mean
-// square error 2.1e-3 to 2.3e-3 of the results' against 1.6e-3 to 1.7e-3 with 32 bits and one rounding.)  The rotated part of the keys is read where it is,
-// once for each head, and never copied to every head.
+// it by kLazy.  bf16 weights have fp32's range, so nothing is lost at the low end, and 2^kLazy leaves values of up to 2^90
+// room in the fp32 sums.  The weights are bf16 because the values are and both operands of a product have one type: root mean
+// square error 2.1e-3 to 2.3e-3 of the results', against 1.6e-3 to 1.7e-3 with 32 bits and one rounding.  The rotated part of
+// the keys is read where it is, once for each head, and never copied to every head.
 //
 // Layout.  A work item is (sequence, head, 256 queries): two tiles of 128 queries over the same key tiles of 128, so that
 // a key or value loaded serves 256 queries (81 KB a key tile; one query tile alone would need 64 B a cycle from L2).
@@ -20,11 +20,12 @@
 // of keys, then two of values.  Tensor memory: S and O of both tiles, 4 x 128 columns; P, in bf16, takes S's place and is
 // the left operand of the second product from there.
 // Bound: the tensor pipe, 12 x 64 + 8 x 64 cycles for 128 queries x 128 keys.  Measured: 16384 causal tokens x 8 heads
-// 490 us, 1.40 PFLOP/s (0.73 of a measured library product), about 4.3 thousand cycles for a pair of such tiles, the items' ends included,
-// against 2.6 of products.  What is left is each query tile's own chain (scores, their weights, results, scores of the
-// next key tile into the same place): tensor memory holds no second S.  Results begun when half of the weights are there
-// took 511 us (the two tiles' products then interleave in smaller pieces), one warp issuing for both query tiles 522 us, and
-// two threads a row 897 us (16 softmax warps leave each thread too few registers for its half of a row).
+// 489 us, 1.40 PFLOP/s (0.73 of a measured library product), about 4.3 thousand cycles for a pair of such tiles, the items'
+// ends included, against 2.6 of products.  What is left is each query tile's own chain (scores, their weights, results,
+// scores of the next key tile into the same place): tensor memory holds no second S.  Results begun when half of the weights
+// are there took 511 us (the two tiles' products then interleave in smaller pieces), one warp issuing for both query tiles
+// 522 us, and two threads a row 897 us (16 softmax warps leave each thread too few registers for its half of a row).  A
+// called function in the softmax's loop takes the traded registers away: 530 us.
 #include "latent.cuh"
 #include "tc.cuh"
 
