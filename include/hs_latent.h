@@ -4,6 +4,7 @@
  *   hs_append_rows      writes the rows of new tokens: the position rotation of the key part, the
  *                       quantisation of the latent part and the store into the pool, in one launch;
  *                       rotates the queries' position part in the same launch.
+ *   hs_read_rows        reads rows back by id, in 16 or 32 bits: a prefix's latents, to be expanded.
  *   hs_attend_rows      absorbed latent attention over row ids, as hs_resolve_topk hands them back.
  *   hs_attend_pages     absorbed latent attention over whole contexts through a block table (requests
  *                       whose pages are all GPU-resident).
@@ -90,6 +91,22 @@ typedef struct {
 } hs_append;
 
 hs_status hs_append_rows(const hs_pool* pool, int32_t layer, const hs_append* a, hs_stream_t stream);
+
+/* Rows by id: latent[t] = code * scale (fp8 rows; bf16 rows: the value) and rope[t] = the rotated key values, each
+ * rounded once to the tensors' type.  An id of -1 gives zeros. */
+typedef struct {
+  int64_t n;                /* rows                                                                   */
+  const int32_t* rows;      /* device [n]: pool row ids, in any order; an id may occur more than once */
+  int32_t dtype;            /* hs_dtype of latent and rope                                            */
+  void* latent;             /* device [n][512]                                                        */
+  int64_t latent_stride;
+  void* rope;               /* device [n][64]                                                         */
+  int64_t rope_stride;
+  int32_t* status;          /* optional device word: HS_ERR_ID_RANGE when a row id lies outside
+                               [-1, num_gpu_blocks * page_size) (its row of the tensors is zero)      */
+} hs_read_latent;
+
+hs_status hs_read_rows(const hs_pool* pool, int32_t layer, const hs_read_latent* a, hs_stream_t stream);
 
 /* Queries and results of an absorbed attention call.  For query token t, head h and the visible rows k
  * with latent c[k] (fp32 of the stored value, rounded to bf16) and rotated key r[k]:

@@ -12,9 +12,14 @@ Operations (the passages that define them are cited in include/hs.h):
   hot_reset      empty the hot buffers
 and on the rows themselves (include/hs_latent.h, latent.py):
   append_rows    rotate, quantise and store the rows of new tokens
+  read_rows      read rows back by id
   attend_rows    absorbed latent attention over row ids
   attend_pages   absorbed latent attention over whole contexts through a block table
   attend_expanded  attention over keys and values expanded to every head (prompts)
+and, for pools whose pages hold the keys and values of several heads in 8 bits (include/hs_heads.h, heads.py):
+  append_heads   quantise the keys and values of new tokens into their pages
+  read_heads     read tokens back
+  attend_heads   attention of grouped query heads: single tokens, verify positions, chunks and prompts
 """
 from __future__ import annotations
 
@@ -526,4 +531,6 @@ class PreparedStep:
 
 
 from .latent import (append_rows, attend_expanded, attend_pages, attend_rows, attend_workspace_bytes,  # noqa: E402
-                     alloc_attend_workspace)
+                     alloc_attend_workspace, read_rows)
+from .heads import (alloc_heads_workspace, append_heads, attend_heads, heads_row_bytes, heads_workspace_bytes,  # noqa: E402
+                    read_heads)

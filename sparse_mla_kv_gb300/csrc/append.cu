@@ -15,6 +15,7 @@
 // still spreads over the SMs.  Measured (fp8 rows): 64 tokens x 64 heads 2.1 us; 32768 tokens x 16 heads 40 us, 5.0 TB/s,
 // x 64 heads 102 us, 5.9 TB/s.  More resident warps with fewer registers (10 or 12 blocks an SM) took 43 and 54 us.
 #include "latent.cuh"
+#include "vec8.cuh"
 
 HS_CHECK_WORD
 
@@ -22,71 +23,6 @@ namespace hs {
 namespace {
 
 constexpr int kThreads = 128;
-
-template <typename T>
-struct Vec8;  // 8 values of T as they lie in memory <-> 8 floats
-template <>
-struct Vec8<__nv_bfloat16> {
-  uint4 v;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ void values(float* x) const {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-  }
-  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* x) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-  }
-};
-template <>
-struct Vec8<__half> {
-  uint4 v;
-  __device__ __forceinline__ void load(const __half* p) { v = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ void values(float* x) const {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-      x[2 * i] = f.x;
-      x[2 * i + 1] = f.y;
-    }
-  }
-  static __device__ __forceinline__ void store(__half* p, const float* x) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-  }
-};
-template <>
-struct Vec8<float> {
-  float4 v[2];
-  __device__ __forceinline__ void load(const float* p) {
-    v[0] = reinterpret_cast<const float4*>(p)[0];
-    v[1] = reinterpret_cast<const float4*>(p)[1];
-  }
-  __device__ __forceinline__ void values(float* x) const {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) x[4 * i] = v[i].x, x[4 * i + 1] = v[i].y, x[4 * i + 2] = v[i].z, x[4 * i + 3] = v[i].w;
-  }
-  static __device__ __forceinline__ void store(float* p, const float* x) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      reinterpret_cast<float4*>(p)[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-  }
-};
 
 // The 8 pairs of quarter j of a 64-vector: x[0..7] and x[8..15] hold the elements at offsets lo(j) and hi(j).
 __device__ __forceinline__ int lo(int j, bool inter) { return inter ? 16 * j : 8 * j; }
@@ -105,26 +41,6 @@ __device__ __forceinline__ void rotate(float* x, const float* c, const float* s,
 #pragma unroll
     for (int i = 0; i < 8; ++i) turn(x[i], x[8 + i], c[i], s[i]);
   }
-}
-
-// Power-of-two scale of a group whose largest finite magnitude is amax (see the head of this file).
-__device__ __forceinline__ float group_scale(float amax) {
-  if (amax == 0.f) return 1.f;
-  const uint32_t b = __float_as_uint(amax);
-  const int field = (int)(b >> 23);  // 0 for subnormal amax: its scale is the smallest one
-  int k = -126;
-  if (field > 0) {
-    const uint32_t mant = b & 0x7FFFFFu;           // amax = (1 + mant / 2^23) * 2^(field - 127)
-    k = field - 126 - 9 + (mant > 0x600000u ? 1 : 0);  // frexp exponent e = field - 126; 0.875 = 1.75 / 2
-    k = max(k, -126);
-  }
-  return __uint_as_float((uint32_t)(k + 127) << 23);
-}
-
-__device__ __forceinline__ uint32_t e4m3x2(float lo_value, float hi_value) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi_value), "f"(lo_value));
-  return r;
 }
 
 // kHeads: heads of a query unit.  blockIdx.y is the unit of a token: 0 its row, then its queries.  Everything that does not

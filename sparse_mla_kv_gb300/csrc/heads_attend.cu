@@ -1,0 +1,754 @@
+// Attention over pages of grouped heads in 8 bits, for few query columns a head of keys: single tokens and verify positions.
+//
+// Mathematics.  The columns of a unit (request, head of keys and values) are its query tokens x the query heads that share the
+// head.  Over the pages (64 tokens each), with page scales sk and sv, log2 units throughout:
+//   S = Q K^T (codes),  c = |scale| log2(e) sk qs,  t = S c + log2(sv),  P = 2^(t - R),  O += P V (codes).
+// A page enters the result as its weights times sv, so P, which is rounded to fp16, is that product, and the reference R
+// follows its largest: it is placed kTop above the largest t, and moves (with O) only when a t passes it by kLazy.  The sum of
+// the weights themselves, 2^(S c - m), follows a reference m of its own, a thread's: from P by one factor a page.  Where a page's
+// largest t is more than 2^kFar below R (values that are all but zero, say), log2(sv) is raised for its P so far that these stay
+// normal numbers in fp32 for that sum; in fp16 they are zero then.
+// Codes are exact in fp16; a query column is divided by qs, a power of two (mostly 1) that brings it into fp16's range.
+//
+// Layout.  The products are on mma.sync: what bounds a call of few columns is reading the pages, and these fragments come from
+// shared memory as the pages are, 16 bytes a lane, with no transposition, no barrier between warps and no tensor memory:
+//   scores   queries are the 16 rows, keys the 8 columns of a product.  Products of sums do not care for the order of the
+//            dimensions: lane (g, t) takes 16 consecutive dimensions 16 t.. of a key and the queries are loaded to match.  The
+//            8 keys of product j are 16 (g / 2) + 2 j + g % 2, so that lane t ends with keys 16 t .. 16 t + 15 of a query row;
+//   results  which is what the transposed product O^T = V^T P^T wants of its right operand, V^T being stored by dimension.
+// A worker is W warps (16 columns each, or 8) and a ring of copies (cp.async.bulk, a page's keys or values of a head each);
+// every worker of the grid takes an equal run of pages, whatever the contexts' lengths; units that are cut leave partial
+// results in the workspace, which join_kernel joins in a fixed order.
+#include "heads.cuh"
+#include "tc.cuh"
+#include "vec8.cuh"
+
+HS_CHECK_WORD
+
+namespace hs {
+namespace {
+
+constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kRingBytes = 192 * 1024;
+constexpr float kTop = 7.f, kLazy = 15.f, kFar = 60.f;
+// Scores beyond kLarge, in log2 units, are taken from an anchor of their own first: added to log2(sv) as they are, they would
+// swallow it, and a product that is not rounded could pass the rounded largest by far.
+constexpr float kLarge = 65536.f;
+
+// Workspace: header, a record a worker, statistics [worker][2][cols][4], results [worker][2][cols][D].
+struct RunHeader {
+  int64_t run, total;  // tiles of a worker, of the call
+};
+struct RunRecord {
+  int64_t begin, end;        // tiles of the unit that begins in this run and is cut by its end; begin == end: none
+  int32_t request, head, group, cols;
+};
+__host__ __device__ constexpr size_t ws_stats_offset(int workers) { return sizeof(RunHeader) + (size_t)workers * sizeof(RunRecord); }
+__host__ __device__ constexpr size_t ws_parts_offset(int workers, int cols) {
+  return ws_stats_offset(workers) + (size_t)workers * 2 * cols * 16;
+}
+__host__ __device__ constexpr size_t ws_bytes(int workers, int cols, int dim) {
+  return ws_parts_offset(workers, cols) + (size_t)workers * 2 * cols * dim * 4;
+}
+static_assert(sizeof(RunHeader) == 16 && sizeof(RunRecord) == 32, "the parts stay aligned to 16 bytes");
+
+// What a call has of one request.
+struct Request {
+  int64_t t0;          // its first query token
+  int n, ctx, keys;    // query tokens; context; tokens of it that the table has room for
+  int tiles, groups;   // pages (at least one), groups of columns; 0 where it has no queries, or more than `limit` columns
+  __device__ __forceinline__ void load(const HeadsAttendParams& p, int r, int cols, int limit) {
+    p.ragged.tokens(r, &t0, &n);
+    ctx = __ldg(p.a.ctx_len + r);
+    keys = max(0, min(ctx, p.a.max_pages * kHeadsPage));
+    const int all = n * p.group;
+    const bool mine = n > 0 && all <= limit;
+    tiles = mine ? max(1, (keys + kHeadsPage - 1) / kHeadsPage) : 0;
+    groups = mine ? (all + cols - 1) / cols : 0;
+  }
+  // tokens of the context that query token i (counted from t0) sees
+  __device__ __forceinline__ int sees(const HeadsAttendParams& p, int i) const {
+    return p.a.causal ? max(0, min(keys, ctx - n + 1 + i)) : keys;
+  }
+};
+
+// A place in the call's tiles: of request r, unit u (head x group), page `tile`.
+struct Cursor {
+  int r, u, tile;
+  Request q;
+  int64_t left;
+  __device__ __forceinline__ int units(const HeadsAttendParams& p) const { return p.pages.kv_heads * q.groups; }
+  // to the next tile; 1 when it is in another unit, 2 when in another request (left == 0: there is none)
+  __device__ __forceinline__ int next(const HeadsAttendParams& p, int cols, int limit) {
+    --left;
+    if (++tile < q.tiles) return 0;
+    tile = 0;
+    if (++u < units(p)) return 1;
+    u = 0;
+    if (left <= 0) return 2;
+    do q.load(p, ++r, cols, limit);
+    while (q.tiles == 0 && r + 1 < p.a.R);
+    return 2;
+  }
+};
+
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ float lds_f(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts_u(uint32_t a, uint32_t x) { asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(x) : "memory"); }
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack(bool f16, float lo, float hi) { return f16 ? pack_half(lo, hi) : tc::pack_bf16(lo, hi); }
+__device__ __forceinline__ float quad_max(float x) {
+  x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
+  return fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
+}
+__device__ __forceinline__ float quad_sum(float x) {
+  x += __shfl_xor_sync(0xFFFFFFFFu, x, 1);
+  return x + __shfl_xor_sync(0xFFFFFFFFu, x, 2);
+}
+// 0x80 in every byte that is the NaN code
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+
+template <int D, int NC, int W>
+struct Shape {
+  static constexpr int kCols = NC * W, kWorkers = kWarps / W;  // columns of a group, workers of a CTA
+  static constexpr int kUnit = D * kHeadsPage;                 // bytes of a page's keys (or values) of a head
+  // a slot: the codes, the 16 bytes that hold the scale, a word that says whether the page is there
+  static constexpr int kSlot = kUnit + 32, kSlots = kRingBytes / kUnit / kWorkers;
+  static constexpr int kBars = kWorkers * kSlots * kSlot, kNan = kBars + 2 * kWorkers * kSlots * 8;
+  static constexpr int kBytes = kNan + kWarps * D * 4;
+  static_assert(kSlots >= 3 && kBytes <= 232448 - 1024, "shared memory");
+};
+
+// Waits, and tells the whole warp when one of its lanes gave up.
+__device__ __forceinline__ void await(tc::Waiter& w, uint32_t bar, uint32_t parity) {
+  w.wait(bar, parity);
+  w.dead = __any_sync(0xFFFFFFFFu, w.dead);
+}
+
+// Copies of a worker's pages, in order: keys, values, keys, ... (one warp of the worker).
+template <int D, int NC, int W>
+struct Producer {
+  using L = Shape<D, NC, W>;
+  Cursor at;
+  uint32_t count = 0;  // copies so far
+  int cached = -1, cached_request = -1, cached_tile = -1;  // a lane's table entry of request and 32 pages
+  int block = 0;
+  bool there = false;
+
+  __device__ __forceinline__ void issue(const HeadsAttendParams& p, uint32_t ring, uint32_t full, uint32_t empty, int limit,
+                                        tc::Waiter& w) {
+    if (at.left <= 0 || w.dead) return;
+    const int lane = threadIdx.x & 31;
+    const uint32_t slot = count % L::kSlots;
+    if (W > 1 && count >= L::kSlots) {
+      await(w, empty + 8 * slot, (count / L::kSlots - 1) & 1);
+      if (w.dead) return;
+    }
+    const bool values = count & 1;
+    if (!values) {
+      if (cached_request != at.r || cached_tile != (at.tile & ~31)) {
+        cached_request = at.r, cached_tile = at.tile & ~31;
+        const int page = cached_tile + lane;
+        cached = -1;
+        if (page * kHeadsPage < at.q.keys && HS_CHECK(at.r < p.a.R && page < p.a.max_pages, kChkTablePage))
+          cached = __ldg(p.pages.table + (int64_t)at.r * p.a.max_pages + page);
+      }
+      block = __shfl_sync(0xFFFFFFFFu, cached, at.tile & 31);
+      there = block >= 0 && block < p.pages.num_blocks;
+      if (lane == 0 && (at.q.ctx > at.q.keys || (at.q.keys > 0 && !there))) report(p.a.status, HS_ERR_TABLE_RANGE);
+      if (!there) block = 0;  // (copied and not used: the ring goes on as ever)
+    }
+    __syncwarp();
+    if (lane == 0) {
+      const int head = at.u / at.q.groups, scale = values ? p.pages.kv_heads + head : head;
+      const uint32_t to = ring + slot * L::kSlot, bar = full + 8 * slot;
+      const uint8_t* codes = p.pages.codes(block, head, D) + (values ? L::kUnit : 0);
+      sts_u(to + L::kUnit + 16, there);
+      tc::mbar_expect(bar, L::kUnit + 16);
+      bulk_copy(to, codes, L::kUnit, bar);
+      bulk_copy(to + L::kUnit, p.pages.scale(block, scale & ~3, D), 16, bar);
+    }
+    ++count;
+    if (values) at.next(p, L::kCols, limit);
+  }
+};
+
+template <int D, int NC, int W>
+__global__ void __launch_bounds__(kThreads, 1) steps_kernel(const HeadsAttendParams p, int limit) {
+  using L = Shape<D, NC, W>;
+  constexpr int kHalves = NC / 8, kBlocks = D / 64;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  __shared__ Cursor starts[L::kWorkers];
+  __shared__ int64_t sums[kWarps];
+  asm volatile("griddepcontrol.launch_dependents;");  // join_kernel waits for this kernel's results by itself
+  const uint32_t smem = tc::smem_u32(smem_raw);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const int worker = warp / W, sub = warp % W;
+  const int workers = L::kWorkers * gridDim.x;
+  const int number = worker * gridDim.x + blockIdx.x;  // of this worker in the order of runs
+  const uint32_t ring = smem + worker * L::kSlots * L::kSlot;
+  const uint32_t full = smem + L::kBars + worker * L::kSlots * 8, empty = full + L::kWorkers * L::kSlots * 8;
+
+  if (threadIdx.x < L::kWorkers * L::kSlots) {
+    tc::mbar_init(smem + L::kBars + 8 * threadIdx.x, 1);
+    tc::mbar_init(smem + L::kBars + 8 * (L::kWorkers * L::kSlots + threadIdx.x), W);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  // the call's tiles, and where each worker's run begins
+  bool bad = false;
+  int64_t sum = 0;
+  for (int r = threadIdx.x; r < p.a.R; r += kThreads) {
+    int64_t t0;
+    int n;
+    bad |= !p.ragged.tokens(r, &t0, &n);
+    Request q;
+    q.load(p, r, L::kCols, limit);
+    sum += (int64_t)p.pages.kv_heads * q.groups * q.tiles;
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+  if (lane == 0) sums[warp] = sum;
+  bad = __syncthreads_or(bad);
+  int64_t total = 0;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) total += sums[i];
+  __syncthreads();
+  if (bad) total = 0;
+  const int64_t run = max((int64_t)1, (total + workers - 1) / workers);
+  int64_t before = 0;
+  for (int r0 = 0; r0 < p.a.R && total > 0; r0 += kThreads) {
+    const int r = r0 + threadIdx.x;
+    Request q{};
+    if (r < p.a.R) q.load(p, r, L::kCols, limit);
+    const int64_t mine = (int64_t)p.pages.kv_heads * q.groups * q.tiles;
+    int64_t upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t x = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+      if (lane >= d) upto += x;
+    }
+    if (lane == 31) sums[warp] = upto;
+    __syncthreads();
+    int64_t off = before, chunk = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      if (i < warp) off += sums[i];
+      chunk += sums[i];
+    }
+    const int64_t first = off + upto - mine;
+    for (int k = 0; k < L::kWorkers; ++k) {
+      const int64_t begin = run * (k * (int64_t)gridDim.x + blockIdx.x);
+      if (begin >= first && begin < first + mine) {
+        const int64_t in = begin - first;
+        starts[k].r = r;
+        starts[k].u = (int)(in / q.tiles);
+        starts[k].tile = (int)(in % q.tiles);
+        starts[k].q = q;
+      }
+    }
+    before += chunk;
+    __syncthreads();
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    if (bad) report(p.a.status, HS_ERR_ID_RANGE);
+    *reinterpret_cast<RunHeader*>(p.workspace) = RunHeader{run, total};
+  }
+  // query tokens that no request has: zeros and -infinity
+  if (p.ragged.cu) {
+    const int64_t from = bad ? 0 : __ldg(p.ragged.cu), to = bad ? 0 : __ldg(p.ragged.cu + p.a.R);
+    const int64_t none = from + (p.a.n - to), words = (int64_t)p.a.q_heads * (D / 8);
+    for (int64_t i = blockIdx.x * (int64_t)kThreads + threadIdx.x; i < none * words; i += (int64_t)gridDim.x * kThreads) {
+      const int64_t k = i / words, token = k < from ? k : to + (k - from);
+      const int head = (int)(i % words) / (D / 8), piece = (int)(i % words) % (D / 8);
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.a.out) + token * p.a.out_token_stride + head * p.a.out_head_stride +
+                                8 * piece) = make_uint4(0, 0, 0, 0);
+      if (piece == 0 && p.a.lse) p.a.lse[token * p.a.q_heads + head] = -INFINITY;
+    }
+  }
+  const int64_t begin = run * number;
+  RunRecord* record = reinterpret_cast<RunRecord*>(reinterpret_cast<uint8_t*>(p.workspace) + sizeof(RunHeader)) + number;
+  float4* stats = reinterpret_cast<float4*>(reinterpret_cast<uint8_t*>(p.workspace) + ws_stats_offset(workers)) +
+                  (int64_t)number * 2 * L::kCols;
+  float* parts = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(p.workspace) + ws_parts_offset(workers, L::kCols)) +
+                 (int64_t)number * 2 * L::kCols * D;
+  if (begin >= total) {
+    if (sub == 0 && lane == 0) *record = RunRecord{0, 0, 0, 0, 0, 0};
+    return;
+  }
+
+  const bool f16 = p.a.dtype == HS_FP16;
+  const float sign = p.scale_log2 < 0.f ? -1.f : 1.f, scale = fabsf(p.scale_log2);
+  tc::Waiter w;
+  Producer<D, NC, W> producer;
+  Cursor cur = starts[worker];
+  cur.left = min(run, total - begin);
+  producer.at = cur;
+  if (sub == 0) {
+#pragma unroll 1
+    for (int i = 0; i < L::kSlots; ++i) producer.issue(p, ring, full, empty, limit, w);
+  }
+  uint32_t taken = 0;  // copies that this warp is done with
+  int* nan_first = reinterpret_cast<int*>(smem_raw + L::kNan) + warp * D;  // by dimension: the first token whose value is NaN
+  int64_t place = begin;  // of the current tile in the call
+  RunRecord cut{0, 0, 0, 0, 0, 0};
+
+#pragma unroll 1
+  while (cur.left > 0 && !w.dead) {
+    // a unit, or this run's part of it
+    const int head = cur.u / cur.q.groups, group = cur.u % cur.q.groups, tile0 = cur.tile;
+    const int cols = min(L::kCols, cur.q.n * p.group - group * L::kCols) - sub * NC;  // of this warp
+    const Request req = cur.q;
+    const int request = cur.r;
+    const int64_t unit_begin = place - tile0;
+    uint32_t q[kBlocks][4][kHalves][2];
+    float qs[kHalves];
+    int sees[kHalves];
+    int64_t row[kHalves];  // token and head of the column, as their offset in lse
+    bool any_nan = false;
+    for (int i = lane; i < D; i += 32) nan_first[i] = INT_MAX;
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h) {
+      const int c = 8 * h + g, in_group = group * L::kCols + sub * NC + c;
+      const bool there = c < cols;
+      const int token = there ? in_group / p.group : 0, qh = head * p.group + (there ? in_group % p.group : 0);
+      sees[h] = there ? req.sees(p, token) : INT_MAX;
+      row[h] = (req.t0 + token) * p.a.q_heads + qh;
+      const uint16_t* src =
+          static_cast<const uint16_t*>(p.a.q) + (req.t0 + token) * p.a.q_token_stride + qh * p.a.q_head_stride + 16 * t;
+      float x[kBlocks][16], top = 0.f;
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint4 v = there ? __ldg(reinterpret_cast<const uint4*>(src + 64 * b) + i) : make_uint4(0, 0, 0, 0);
+          if (f16)
+            Vec8<__half>{v}.values(x[b] + 8 * i);
+          else
+            Vec8<__nv_bfloat16>{v}.values(x[b] + 8 * i);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(x[b][i]));
+      }
+      top = quad_max(top);
+      // left as they are when their largest magnitude is in 2^-2 .. 2^15: fp16 then keeps all but what is 2^-23 of it
+      const int e2 = (int)(__float_as_uint(top) >> 23);
+      const int e = top == 0.f || (e2 >= 125 && e2 < 142) ? 127 : min(max(e2 - 14, 1), 240);
+      const float f = sign * __uint_as_float((uint32_t)(254 - e) << 23);
+      qs[h] = scale * __uint_as_float((uint32_t)e << 23);
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) q[b][i][h][k] = pack_half(x[b][4 * i + 2 * k] * f, x[b][4 * i + 2 * k + 1] * f);
+    }
+    __syncwarp();
+    int all_see = sees[0];
+    if constexpr (kHalves == 2) all_see = min(all_see, sees[1]);
+    all_see = __reduce_min_sync(0xFFFFFFFFu, all_see);
+    float ref[kHalves], m[kHalves], l[kHalves], anchor[kHalves], o[kHalves][D / 16][4];
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h) {
+      ref[h] = m[h] = -INFINITY;
+      l[h] = anchor[h] = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[h][i][k] = 0.f;
+    }
+
+    int moved;
+#pragma unroll 1
+    do {
+      const int key0 = cur.tile * kHeadsPage;
+      // scores
+      uint32_t slot = ring + taken % L::kSlots * L::kSlot;
+      await(w, full + 8 * (taken % L::kSlots), taken / L::kSlots & 1);
+      const bool valid = lds_u(slot + L::kUnit + 16) != 0;
+      const float sk = lds_f(slot + L::kUnit + 4 * (head & 3));
+      float s[8][4];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint4 k = lds16(slot + b * 4096 + (16 * (g >> 1) + 2 * j + (g & 1)) * 64 + 16 * t);
+          const uint32_t words[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint2 x = half_of_codes(words[i]);
+            if constexpr (kHalves == 2)
+              mma(s[j], q[b][i][0][0], q[b][i][1][0], q[b][i][0][1], q[b][i][1][1], x.x, x.y);
+            else
+              mma(s[j], q[b][i][0][0], 0u, q[b][i][0][1], 0u, x.x, x.y);
+          }
+        }
+      }
+      __syncwarp();
+      ++taken;
+      if (W > 1 && lane == 0) tc::mbar_arrive(empty + 8 * ((taken - 1) % L::kSlots));
+      if (sub == 0) producer.issue(p, ring, full, empty, limit, w);
+
+      // weights
+      slot = ring + taken % L::kSlots * L::kSlot;
+      await(w, full + 8 * (taken % L::kSlots), taken / L::kSlots & 1);
+      const float sv = lds_f(slot + L::kUnit + 4 * ((p.pages.kv_heads + head) & 3));
+      const float size = valid ? log2f(sv) : 0.f;
+      const bool mixed = !valid || key0 + kHeadsPage > all_see;
+      uint32_t pf[kHalves][4][2];
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h) {
+        if (mixed) {
+          const int left = valid ? sees[h] - key0 - 16 * t : 0;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (2 * j + e >= left) s[j][2 * h + e] = -INFINITY;
+        }
+        float top = s[0][2 * h];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = fmaxf(fmaxf(top, s[j][2 * h]), s[j][2 * h + 1]);
+        float c = fminf(fmaxf(sk * qs[h], 1.17549435e-38f), 3.402823466e38f);
+        top = __fmul_rn(top, c);
+        if (__any_sync(0xFFFFFFFFu, fabsf(top) > kLarge || anchor[h] != 0.f)) {
+          const float most = quad_max(top);
+          if (fabsf(most) <= 3.402823466e38f && (most - anchor[h] > kLarge || (ref[h] == -INFINITY && fabsf(most) > kLarge))) {
+            const float by = most - anchor[h];
+            anchor[h] = most;
+            ref[h] -= by, m[h] -= by;
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) s[j][2 * h + e] = __fsub_rn(__fmul_rn(s[j][2 * h + e], c), anchor[h]);  // (rounded as top is)
+          top -= anchor[h];
+          c = 1.f;
+        }
+        if (__any_sync(0xFFFFFFFFu, top + size > ref[h] + kLazy)) {
+          const float most = quad_max(top + size);
+          const float now = most > ref[h] + kLazy ? most - kTop : ref[h];
+          const float alpha = now == ref[h] ? 1.f : exp2f(ref[h] - now);
+          ref[h] = now;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float f = __shfl_sync(0xFFFFFFFFu, alpha, 4 * (2 * t + e));
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) o[h][i][e] *= f, o[h][i][2 + e] *= f;
+          }
+        }
+        const float r = ref[h] == -INFINITY ? 0.f : ref[h];
+        float bias = size - r;
+        if (top + size < r - kFar) bias = top < -2.f * kLarge ? -INFINITY : -kFar - top;  // (-infinity: no weight at all)
+        float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float x = tc::exp2_fast(fmaf(s[j][2 * h], c, bias)), y = tc::exp2_fast(fmaf(s[j][2 * h + 1], c, bias));
+          sum0 += x, sum1 += y;
+          pf[h][j >> 1][j & 1] = pack_half(x, y);
+        }
+        if (top > m[h] + kFar) {
+          l[h] = m[h] == -INFINITY ? 0.f : l[h] * exp2f(m[h] - top);
+          m[h] = top;
+        }
+        if (bias != -INFINITY) l[h] += (sum0 + sum1) * exp2f(-bias - m[h]);
+      }
+
+      // results
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        const uint32_t from = slot + (i >> 2) * 4096 + (16 * (i & 3) + g) * 64 + 16 * t;
+        uint4 v0 = lds16(from), v1 = lds16(from + 512);
+        uint32_t words[2][4] = {{v0.x, v0.y, v0.z, v0.w}, {v1.x, v1.y, v1.z, v1.w}};
+        if (mixed) {  // a weight of zero does not cancel a NaN: who sees it is settled at the unit's end
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const uint32_t is = nan_codes(words[y][x]);
+              if (is) {
+                words[y][x] &= ~((is >> 7) * 0xFFu);
+                if (valid) atomicMin(nan_first + 16 * i + 8 * y + g, key0 + 16 * t + 4 * x + ((__ffs(is) - 1) >> 3));
+                any_nan = true;
+              }
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const uint2 a = half_of_codes(words[0][x]), b = half_of_codes(words[1][x]);
+#pragma unroll
+          for (int h = 0; h < kHalves; ++h) mma(o[h][i], a.x, b.x, a.y, b.y, pf[h][x][0], pf[h][x][1]);
+        }
+      }
+      __syncwarp();
+      ++taken;
+      if (W > 1 && lane == 0) tc::mbar_arrive(empty + 8 * ((taken - 1) % L::kSlots));
+      if (sub == 0) producer.issue(p, ring, full, empty, limit, w);
+      ++place;
+      moved = cur.next(p, L::kCols, limit);
+    } while (moved == 0 && cur.left > 0 && !w.dead);
+
+    // the unit's results, or this run's part of them
+    __syncwarp();
+    any_nan = __any_sync(0xFFFFFFFFu, any_nan);
+    const bool whole = tile0 == 0 && moved != 0;
+    const int part = unit_begin > begin ? 1 : 0;
+    if (moved == 0 && tile0 == 0)
+      cut = RunRecord{unit_begin, unit_begin + req.tiles, request, head, group, cols + sub * NC};
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h) {
+      const float most = quad_max(m[h]);
+      const float sum_l = quad_sum(m[h] == -INFINITY ? 0.f : l[h] * exp2f(m[h] - most));
+      const bool there = 8 * h + g < cols;
+      if (any_nan) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int limit_key = __shfl_sync(0xFFFFFFFFu, sees[h], 4 * (2 * t + e));
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+              if (limit_key > nan_first[16 * i + 8 * y + g]) o[h][i][2 * y + e] = __uint_as_float(0x7FC00000u);
+        }
+      }
+      if (whole) {
+        const float half_way = 0.5f * (ref[h] - most), up = sum_l == 0.f ? 0.f : exp2f(half_way);
+        const float inv = sum_l == 0.f ? 0.f : up / sum_l;
+        float f0[2], f1[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          f0[e] = __shfl_sync(0xFFFFFFFFu, up, 4 * (2 * t + e));
+          f1[e] = __shfl_sync(0xFFFFFFFFu, inv, 4 * (2 * t + e));
+        }
+        uint16_t* out = static_cast<uint16_t*>(p.a.out) + row[h] / p.a.q_heads * p.a.out_token_stride +
+                        row[h] % p.a.q_heads * p.a.out_head_stride + 2 * t;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const uint32_t x = transposed(pack(f16, o[h][i][2 * y] * f0[0] * f1[0], o[h][i][2 * y + 1] * f0[1] * f1[1]));
+            if (there && HS_CHECK(row[h] < p.a.n * p.a.q_heads, kChkOutPos)) *reinterpret_cast<uint32_t*>(out + 16 * i + 8 * y) = x;
+          }
+        if (there && t == 0 && p.a.lse) p.a.lse[row[h]] = sum_l == 0.f ? -INFINITY : (anchor[h] + (most + log2f(sum_l))) * kLn2;
+      } else {
+        const int at = part * L::kCols + sub * NC + 8 * h;
+        if (t == 0) stats[at + g] = make_float4(ref[h], most, sum_l, anchor[h]);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) parts[(at + 2 * t + (k & 1)) * D + 16 * i + 8 * (k >> 1) + g] = o[h][i][k];
+      }
+    }
+    __syncwarp();
+  }
+  if (sub == 0 && lane == 0) *record = cut;
+  if (sub == 0) {  // no copy is in flight when the CTA ends
+    tc::Drain drain;
+    for (; taken < producer.count; ++taken) drain.wait(full + 8 * (taken % L::kSlots), taken / L::kSlots & 1);
+  }
+  if (w.dead) report(p.a.status, HS_ERR_TIMEOUT);
+}
+
+// Joins the parts of units that several runs share.  A block takes one column of a cut unit at a time; its warps take every
+// fourth part each.
+constexpr int kJoinThreads = 128, kMaxWorkers = 2048;
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const HeadsAttendParams p, int workers, int group_cols) {
+  constexpr int kPer = D / 32;
+  __shared__ uint16_t cuts[kMaxWorkers];
+  __shared__ int counts[kJoinThreads / 32];
+  __shared__ float4 joined[4];
+  __shared__ float sums[4][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // for the results of steps_kernel
+  const uint8_t* ws = reinterpret_cast<const uint8_t*>(p.workspace);
+  const RunHeader header = *reinterpret_cast<const RunHeader*>(ws);
+  const RunRecord* records = reinterpret_cast<const RunRecord*>(ws + sizeof(RunHeader));
+  const float4* stats = reinterpret_cast<const float4*>(ws + ws_stats_offset(workers));
+  const float* parts = reinterpret_cast<const float*>(ws + ws_parts_offset(workers, group_cols));
+  // the cut units, in order
+  int n = 0;
+  for (int i0 = 0; i0 < workers; i0 += kJoinThreads) {
+    const int i = i0 + threadIdx.x;
+    const bool is = i < workers && records[i].end > records[i].begin;
+    const unsigned those = __ballot_sync(0xFFFFFFFFu, is);
+    if (lane == 0) counts[warp] = __popc(those);
+    __syncthreads();
+    int at = n + __popc(those & ((1u << lane) - 1));
+#pragma unroll
+    for (int y = 0; y < kJoinThreads / 32; ++y) {
+      if (y < warp) at += counts[y];
+      n += counts[y];
+    }
+    if (is) cuts[at] = (uint16_t)i;
+    __syncthreads();
+  }
+  for (int item = blockIdx.x; item < n * group_cols; item += gridDim.x) {
+    const int i = cuts[item / group_cols], c = item % group_cols;
+    const RunRecord rec = records[i];
+    if (c >= rec.cols) continue;
+    const int last = (int)((rec.end - 1) / header.run);
+    const int slot0 = rec.begin > i * header.run ? 1 : 0;
+    float anchor = -INFINITY;  // the largest of the parts that have any
+    for (int x = i + lane; x <= last; x += 32) {
+      const float4 st = stats[((int64_t)x * 2 + (x == i ? slot0 : 0)) * group_cols + c];
+      if (st.y != -INFINITY) anchor = fmaxf(anchor, st.w);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) anchor = fmaxf(anchor, __shfl_xor_sync(0xFFFFFFFFu, anchor, d));
+    if (anchor == -INFINITY) anchor = 0.f;
+    float ref = -INFINITY, m = -INFINITY, l = 0.f, acc[kPer] = {};
+    for (int x = i + warp; x <= last; x += 4) {
+      const int64_t at = ((int64_t)x * 2 + (x == i ? slot0 : 0)) * group_cols + c;
+      float4 st = stats[at];
+      st.x += st.w - anchor, st.y += st.w - anchor;
+      float v[kPer];
+#pragma unroll
+      for (int d = 0; d < kPer; ++d) v[d] = parts[at * D + lane * kPer + d];
+      const float now = fmaxf(ref, st.x), now_m = fmaxf(m, st.y);
+      const float a = ref == now ? 1.f : exp2f(ref - now), b = st.x == now ? (now == -INFINITY ? 0.f : 1.f) : exp2f(st.x - now);
+      const float am = m == now_m ? 1.f : exp2f(m - now_m), bm = st.y == now_m ? 1.f : exp2f(st.y - now_m);
+#pragma unroll
+      for (int d = 0; d < kPer; ++d) acc[d] = acc[d] * a + v[d] * b;
+      l = l * am + st.z * bm;
+      ref = now, m = now_m;
+    }
+    if (lane == 0) joined[warp] = make_float4(ref, m, l, 0.f);
+#pragma unroll
+    for (int d = 0; d < kPer; ++d) sums[warp][lane * kPer + d] = acc[d];
+    __syncthreads();
+    if (warp == 0) {
+      float4 all[4];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) all[y] = joined[y];
+      const float top = fmaxf(fmaxf(all[0].x, all[1].x), fmaxf(all[2].x, all[3].x));
+      const float top_m = fmaxf(fmaxf(all[0].y, all[1].y), fmaxf(all[2].y, all[3].y));
+      float res[kPer] = {};
+      l = 0.f;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const float f = all[y].x == -INFINITY ? 0.f : exp2f(all[y].x - top);
+        l += all[y].y == -INFINITY ? 0.f : all[y].z * exp2f(all[y].y - top_m);
+#pragma unroll
+        for (int d = 0; d < kPer; ++d) res[d] += sums[y][lane * kPer + d] * f;
+      }
+      const float up = l == 0.f ? 0.f : exp2f(0.5f * (top - top_m)), inv = l == 0.f ? 0.f : up / l;
+      Request q;
+      q.load(p, rec.request, group_cols, INT_MAX);
+      const int in_unit = rec.group * group_cols + c;
+      const int64_t token = q.t0 + in_unit / p.group;
+      const int qh = rec.head * p.group + in_unit % p.group;
+      if (HS_CHECK(token < p.a.n && qh < p.a.q_heads, kChkOutPos)) {
+        uint16_t* out = static_cast<uint16_t*>(p.a.out) + token * p.a.out_token_stride + qh * p.a.out_head_stride + lane * kPer;
+#pragma unroll
+        for (int d = 0; d < kPer; d += 2)
+          *reinterpret_cast<uint32_t*>(out + d) = pack(p.a.dtype == HS_FP16, res[d] * up * inv, res[d + 1] * up * inv);
+        if (lane == 0 && p.a.lse) p.a.lse[token * p.a.q_heads + qh] = l == 0.f ? -INFINITY : (anchor + (top_m + log2f(l))) * kLn2;
+      }
+    }
+    __syncthreads();
+  }
+}
+
+template <int D, int NC, int W>
+cudaError_t launch_steps(const HeadsAttendParams& p, int limit, int dev, int sms, cudaStream_t s) {
+  using L = Shape<D, NC, W>;
+  static DeviceOnce once;
+  const cudaError_t ready = once.ready(dev, [] {
+    return cudaFuncSetAttribute(steps_kernel<D, NC, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+  });
+  if (ready != cudaSuccess) return ready;
+  const int workers = sms * L::kWorkers;
+  if (workers > kMaxWorkers) return cudaErrorInvalidConfiguration;
+  steps_kernel<D, NC, W><<<sms, kThreads, L::kBytes, s>>>(p, limit);
+  count_launch();
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // its launch overlaps the end of the kernel before
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(sms * 4);
+  c.blockDim = dim3(kJoinThreads);
+  c.stream = s;
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &early;
+  c.numAttrs = 1;
+  e = cudaLaunchKernelEx(&c, join_kernel<D>, p, workers, L::kCols);
+  count_launch();
+  return e;
+}
+
+template <int D>
+cudaError_t launch_dim(const HeadsAttendParams& p, int limit, int dev, int sms, cudaStream_t s) {
+  // columns of a request, on average: a group takes them all, up to 64 (a ragged call's longer ones take several)
+  const int64_t cols = p.a.R > 0 ? (p.a.n + p.a.R - 1) / p.a.R * p.group : 1;
+  if (cols <= 8) return launch_steps<D, 8, 1>(p, limit, dev, sms, s);
+  if (cols <= 16) return launch_steps<D, 16, 1>(p, limit, dev, sms, s);
+  if (cols <= 32) return launch_steps<D, 16, 2>(p, limit, dev, sms, s);
+  return launch_steps<D, 16, 4>(p, limit, dev, sms, s);
+}
+
+}  // namespace
+
+uint32_t check_take_heads_attend() {
+#if HS_CHECKED
+  unsigned v = 0u, z = 0u;
+  if (cudaMemcpyFromSymbol(&v, hs_check_word_, sizeof(v)) != cudaSuccess ||
+      cudaMemcpyToSymbol(hs_check_word_, &z, sizeof(z)) != cudaSuccess) {
+    cudaGetLastError();
+    return 0xFFFFFFFFu;
+  }
+  return v;
+#else
+  return 0u;
+#endif
+}
+
+size_t heads_workspace_bytes(int sms) {
+  size_t most = 0;
+  for (const int w : {1, 2, 4}) {
+    const size_t b = ws_bytes(sms * (kWarps / w), 16 * w, 128);
+    most = b > most ? b : most;
+  }
+  return most;
+}
+
+cudaError_t launch_attend_heads(const HeadsAttendParams& p, int dev, int sms, cudaStream_t s) {
+  return p.a.head_dim == 64 ? launch_dim<64>(p, INT32_MAX, dev, sms, s) : launch_dim<128>(p, INT32_MAX, dev, sms, s);
+}
+
+}  // namespace hs

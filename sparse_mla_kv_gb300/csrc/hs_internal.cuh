@@ -76,6 +76,9 @@ uint32_t check_take_gather();
 uint32_t check_take_append();
 uint32_t check_take_attend();
 uint32_t check_take_expanded();
+uint32_t check_take_read_rows();
+uint32_t check_take_heads_pages();
+uint32_t check_take_heads_attend();
 
 // Per-layer base pointers, passed to kernels by value (kernel parameter space, no device
 // allocation).  host[] holds device-usable addresses of the pinned host pool.

@@ -36,6 +36,14 @@ struct AppendParams {
 };
 cudaError_t launch_append(const AppendParams& p, int sms, cudaStream_t s);
 
+struct ReadRowsParams {
+  hs_read_latent a;
+  const uint8_t* base;
+  int64_t num_rows;
+  int32_t row_bytes;
+};
+cudaError_t launch_read_rows(const ReadRowsParams& p, cudaStream_t s);
+
 // Absorbed attention.  An item is what shares keys: a token of a rows call (cols = heads), a request of a
 // pages call (cols = positions * heads; column c is position c / heads, head c % heads).
 struct AttendParams {

@@ -90,6 +90,20 @@ hs_status hs_append_rows(const hs_pool* pool, int32_t layer, const hs_append* a,
   return status_of(hs::launch_append(p, v.sms, stream));
 }
 
+hs_status hs_read_rows(const hs_pool* pool, int32_t layer, const hs_read_latent* a, hs_stream_t stream) {
+  HS_RANGE("hs_read_rows");
+  hs::LayerView v;
+  if (!a || !hs::pool_layer(pool, layer, &v) || !row_format(v.row_bytes)) return HS_ERR_INVALID_ARG;
+  if (a->n < 0 || a->n > INT32_MAX || a->dtype < HS_BF16 || a->dtype > HS_FP32) return HS_ERR_INVALID_ARG;
+  if (a->n == 0) return HS_OK;
+  const int64_t size = a->dtype == HS_FP32 ? 4 : 2;
+  if (!a->rows || !aligned(a->latent) || !aligned(a->rope)) return HS_ERR_INVALID_ARG;
+  if (!out_stride_ok(a->latent_stride, size, a->n, hs::kLatent) || !out_stride_ok(a->rope_stride, size, a->n, hs::kRope))
+    return HS_ERR_INVALID_ARG;
+  if (!on_device(v.device)) return HS_ERR_INVALID_ARG;
+  return status_of(hs::launch_read_rows(hs::ReadRowsParams{*a, v.base, v.num_rows, v.row_bytes}, stream));
+}
+
 size_t hs_attend_workspace_bytes(void) {
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) {

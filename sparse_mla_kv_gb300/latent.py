@@ -1,6 +1,7 @@
 """Operators on the latent rows of the paged KV pool (include/hs_latent.h).
 
   append_rows      write the rows of new tokens (rotation + quantisation + store, one launch)
+  read_rows        read rows back by id, in 16 or 32 bits
   attend_rows      absorbed latent attention over row ids (resolve_topk's out_rows)
   attend_pages     absorbed latent attention over whole contexts through a block table
   attend_expanded  attention over keys and values expanded to every head (prompts)
@@ -31,6 +32,11 @@ class AppendC(ctypes.Structure):
                 ("q_out", _p), ("q_out_token_stride", _i64), ("q_out_head_stride", _i64), ("status", _p)]
 
 
+class ReadLatentC(ctypes.Structure):
+    _fields_ = [("n", _i64), ("rows", _p), ("dtype", _i32), ("latent", _p), ("latent_stride", _i64), ("rope", _p),
+                ("rope_stride", _i64), ("status", _p)]
+
+
 class AttendC(ctypes.Structure):
     _fields_ = [("heads", _i32), ("scale", _f), ("q_latent", _p), ("ql_token_stride", _i64), ("ql_head_stride", _i64),
                 ("q_rope", _p), ("qr_token_stride", _i64), ("qr_head_stride", _i64), ("out", _p),
@@ -55,6 +61,8 @@ def _lib():
         L = lib()
         L.hs_append_rows.restype = _i32
         L.hs_append_rows.argtypes = [_p, _i32, ctypes.POINTER(AppendC), _p]
+        L.hs_read_rows.restype = _i32
+        L.hs_read_rows.argtypes = [_p, _i32, ctypes.POINTER(ReadLatentC), _p]
         L.hs_attend_workspace_bytes.restype = ctypes.c_size_t
         L.hs_attend_workspace_bytes.argtypes = []
         L.hs_attend_rows.restype = _i32
@@ -159,6 +167,29 @@ def append_rows(pool: Pool, rows: torch.Tensor, latent: torch.Tensor, rope: torc
                 status if status is None else _whole(status, "status", _I32, dev))
     _check(_lib().hs_append_rows(pool.handle, int(layer), ctypes.byref(a), _on(stream, latent)), "hs_append_rows")
     return q_out
+
+
+def read_rows(pool: Pool, rows: torch.Tensor, *, layer: int = 0, dtype: torch.dtype = torch.bfloat16,
+              latent: Optional[torch.Tensor] = None, rope: Optional[torch.Tensor] = None,
+              status: Optional[torch.Tensor] = None, stream=None):
+    """The latents and rotated keys of pool rows: rows int32 [n] (-1: zeros) -> (latent [n][512], rope [n][64]) in dtype:
+    bf16, fp16 or fp32, or that of latent and rope where they are given."""
+    n = int(rows.numel())
+    dev = _here(rows, "rows")
+    if latent is not None or rope is not None:
+        dtype = (latent if latent is not None else rope).dtype
+    dt = _DTYPES.get(dtype)
+    if dt is None:
+        raise TypeError("latent and rope must be bf16, fp16 or fp32")
+    if latent is None:
+        latent = _empty((n, LATENT_DIM), dtype, rows.device, stream)
+    if rope is None:
+        rope = _empty((n, ROPE_DIM), dtype, rows.device, stream)
+    a = ReadLatentC(n, _whole(rows, "rows", _I32, dev), dt, latent.data_ptr(), _tensor(latent, "latent", (n, LATENT_DIM), dev, dtype)[0],
+                    rope.data_ptr(), _tensor(rope, "rope", (n, ROPE_DIM), dev, dtype)[0],
+                    status if status is None else _whole(status, "status", _I32, dev))
+    _check(_lib().hs_read_rows(pool.handle, int(layer), ctypes.byref(a), _on(stream, rows)), "hs_read_rows")
+    return latent, rope
 
 
 def attend_workspace_bytes() -> int:
