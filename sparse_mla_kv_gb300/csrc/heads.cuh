@@ -67,5 +67,8 @@ struct HeadsAttendParams {
 };
 cudaError_t launch_attend_heads(const HeadsAttendParams& p, int dev, int sms, cudaStream_t s);
 size_t heads_workspace_bytes(int sms);
+// Requests of more than `limit` columns (query tokens x group); launch_attend_heads takes the others by itself.
+cudaError_t launch_heads_prompt(const HeadsAttendParams& p, int limit, int dev, int sms, cudaStream_t s);
+size_t heads_prompt_workspace_bytes(int sms);
 
 }  // namespace hs

@@ -19,30 +19,20 @@
 // A worker is W warps (16 columns each, or 8) and a ring of copies (cp.async.bulk, a page's keys or values of a head each);
 // every worker of the grid takes an equal run of pages, whatever the contexts' lengths; units that are cut leave partial
 // results in the workspace, which join_kernel joins in a fixed order.
-#include "heads.cuh"
-#include "tc.cuh"
-#include "vec8.cuh"
+#include "heads_device.cuh"
 
 HS_CHECK_WORD
 
 namespace hs {
 namespace {
 
+using namespace heads;
+
 constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int kRingBytes = 192 * 1024;
-constexpr float kTop = 7.f, kLazy = 15.f, kFar = 60.f;
-// Scores beyond kLarge, in log2 units, are taken from an anchor of their own first: added to log2(sv) as they are, they would
-// swallow it, and a product that is not rounded could pass the rounded largest by far.
-constexpr float kLarge = 65536.f;
+constexpr int kStepCols = 64;  // requests of more columns are left to heads_prompt.cu
 
 // Workspace: header, a record a worker, statistics [worker][2][cols][4], results [worker][2][cols][D].
-struct RunHeader {
-  int64_t run, total;  // tiles of a worker, of the call
-};
-struct RunRecord {
-  int64_t begin, end;        // tiles of the unit that begins in this run and is cut by its end; begin == end: none
-  int32_t request, head, group, cols;
-};
 __host__ __device__ constexpr size_t ws_stats_offset(int workers) { return sizeof(RunHeader) + (size_t)workers * sizeof(RunRecord); }
 __host__ __device__ constexpr size_t ws_parts_offset(int workers, int cols) {
   return ws_stats_offset(workers) + (size_t)workers * 2 * cols * 16;
@@ -50,7 +40,6 @@ __host__ __device__ constexpr size_t ws_parts_offset(int workers, int cols) {
 __host__ __device__ constexpr size_t ws_bytes(int workers, int cols, int dim) {
   return ws_parts_offset(workers, cols) + (size_t)workers * 2 * cols * dim * 4;
 }
-static_assert(sizeof(RunHeader) == 16 && sizeof(RunRecord) == 32, "the parts stay aligned to 16 bytes");
 
 // What a call has of one request.
 struct Request {
@@ -92,27 +81,6 @@ struct Cursor {
   }
 };
 
-__device__ __forceinline__ uint4 lds16(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ float lds_f(uint32_t a) {
-  float v;
-  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint32_t lds_u(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ void sts_u(uint32_t a, uint32_t x) { asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(x) : "memory"); }
-__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
-               "r"(bytes), "r"(bar)
-               : "memory");
-}
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -123,12 +91,6 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack(bool f16, float lo, float hi) { return f16 ? pack_half(lo, hi) : tc::pack_bf16(lo, hi); }
 __device__ __forceinline__ float quad_max(float x) {
   x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
   return fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
@@ -137,9 +99,6 @@ __device__ __forceinline__ float quad_sum(float x) {
   x += __shfl_xor_sync(0xFFFFFFFFu, x, 1);
   return x + __shfl_xor_sync(0xFFFFFFFFu, x, 2);
 }
-// 0x80 in every byte that is the NaN code
-__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
-
 template <int D, int NC, int W>
 struct Shape {
   static constexpr int kCols = NC * W, kWorkers = kWarps / W;  // columns of a group, workers of a CTA
@@ -150,12 +109,6 @@ struct Shape {
   static constexpr int kBytes = kNan + kWarps * D * 4;
   static_assert(kSlots >= 3 && kBytes <= 232448 - 1024, "shared memory");
 };
-
-// Waits, and tells the whole warp when one of its lanes gave up.
-__device__ __forceinline__ void await(tc::Waiter& w, uint32_t bar, uint32_t parity) {
-  w.wait(bar, parity);
-  w.dead = __any_sync(0xFFFFFFFFu, w.dead);
-}
 
 // Copies of a worker's pages, in order: keys, values, keys, ... (one warp of the worker).
 template <int D, int NC, int W>
@@ -362,11 +315,9 @@ __global__ void __launch_bounds__(kThreads, 1) steps_kernel(const HeadsAttendPar
         for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(x[b][i]));
       }
       top = quad_max(top);
-      // left as they are when their largest magnitude is in 2^-2 .. 2^15: fp16 then keeps all but what is 2^-23 of it
-      const int e2 = (int)(__float_as_uint(top) >> 23);
-      const int e = top == 0.f || (e2 >= 125 && e2 < 142) ? 127 : min(max(e2 - 14, 1), 240);
-      const float f = sign * __uint_as_float((uint32_t)(254 - e) << 23);
-      qs[h] = scale * __uint_as_float((uint32_t)e << 23);
+      const int e = query_field(top);
+      const float f = sign * power_of_field(254 - e);
+      qs[h] = scale * power_of_field(e);
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
@@ -739,7 +690,7 @@ uint32_t check_take_heads_attend() {
 }
 
 size_t heads_workspace_bytes(int sms) {
-  size_t most = 0;
+  size_t most = heads_prompt_workspace_bytes(sms);
   for (const int w : {1, 2, 4}) {
     const size_t b = ws_bytes(sms * (kWarps / w), 16 * w, 128);
     most = b > most ? b : most;
@@ -748,7 +699,14 @@ size_t heads_workspace_bytes(int sms) {
 }
 
 cudaError_t launch_attend_heads(const HeadsAttendParams& p, int dev, int sms, cudaStream_t s) {
-  return p.a.head_dim == 64 ? launch_dim<64>(p, INT32_MAX, dev, sms, s) : launch_dim<128>(p, INT32_MAX, dev, sms, s);
+  // Without offsets all requests have as many columns.  With them the host does not know, and each kernel takes its own.
+  const int64_t all = p.a.n * p.group;
+  const int64_t most = p.ragged.cu ? all : all / p.a.R;
+  if (p.ragged.cu || most <= kStepCols) {
+    const cudaError_t e = p.a.head_dim == 64 ? launch_dim<64>(p, kStepCols, dev, sms, s) : launch_dim<128>(p, kStepCols, dev, sms, s);
+    if (e != cudaSuccess) return e;
+  }
+  return most > kStepCols ? launch_heads_prompt(p, kStepCols, dev, sms, s) : cudaSuccess;
 }
 
 }  // namespace hs

@@ -1,0 +1,72 @@
+// What the attention kernels over pages of grouped heads share.
+#pragma once
+
+#include "heads.cuh"
+#include "tc.cuh"
+#include "vec8.cuh"
+
+namespace hs {
+namespace heads {
+
+// Log2 units.  A new reference R puts the largest t at kTop above it, and moves when a t passes it by kLazy: fp16 weights are
+// normal from 2^-14 to 2^16.  kFar: see heads_attend.cu.
+constexpr float kTop = 7.f, kLazy = 15.f, kFar = 60.f;
+// Scores beyond kLarge, in log2 units, are taken from an anchor of their own first: added to log2(sv) as they are, they would
+// swallow it, and a product that is not rounded could pass the rounded largest by far.
+constexpr float kLarge = 65536.f;
+
+// A call's work is numbered in tiles, and a run of them is what one worker takes.
+struct RunHeader {
+  int64_t run, total;  // tiles of a worker, of the call
+};
+struct RunRecord {
+  int64_t begin, end;        // tiles of the unit that begins in this run and is cut by its end; begin == end: none
+  int32_t request, head, group, cols;
+};
+static_assert(sizeof(RunHeader) == 16 && sizeof(RunRecord) == 32, "the parts stay aligned to 16 bytes");
+
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ float lds_f(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts_u(uint32_t a, uint32_t x) { asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(x) : "memory"); }
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack(bool f16, float lo, float hi) { return f16 ? pack_half(lo, hi) : tc::pack_bf16(lo, hi); }
+// 0x80 in every byte that is the NaN code
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+
+// Waits, and tells the whole warp when one of its lanes gave up.
+__device__ __forceinline__ void await(tc::Waiter& w, uint32_t bar, uint32_t parity) {
+  w.wait(bar, parity);
+  w.dead = __any_sync(0xFFFFFFFFu, w.dead);
+}
+// The exponent field e of a power of two that brings a query's largest magnitude into fp16's range, by division: left as they
+// are (127) when it is in 2^-2 .. 2^15, where fp16 keeps all but what is 2^-23 of it.
+__device__ __forceinline__ int query_field(float top) {
+  const int e = (int)(__float_as_uint(top) >> 23);
+  return top == 0.f || (e >= 125 && e < 142) ? 127 : min(max(e - 14, 1), 240);
+}
+__device__ __forceinline__ float power_of_field(int e) { return __uint_as_float((uint32_t)e << 23); }
+
+}  // namespace heads
+}  // namespace hs

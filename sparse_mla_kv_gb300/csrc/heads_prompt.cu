@@ -1,0 +1,944 @@
+// Attention over pages of grouped heads in 8 bits, for many query columns a head of keys: prompts and prompt chunks, on the
+// tensor cores.
+//
+// Mathematics.  As in heads_attend.cu: codes are multiplied in fp16, a page's value scale is part of its weights, the reference R
+// of the weights follows the largest product of weight and scale, and the sum of the weights has a reference m of its own.  Here a
+// query row is a thread's, and so are R, m and the sum.
+//
+// Layout.  A work item is (request, head of keys and values, 256 columns): two tiles of 128 columns (query token x query head of
+// the group, token by token) over the same key tiles of 128 tokens (two pages), so that a page widened serves 256 rows.  The
+// key tiles of all items are numbered, and every CTA takes an equal run of them, whatever the contexts' lengths and the causal
+// mask leave; items that are cut leave partial results in the workspace, which prompt_join_kernel joins in a fixed order.
+// 16 warps, one CTA per SM (the warpgroups trade registers):
+//   warps 0-3, 4-7   softmax and results of query tile 0 and 1, a row a thread;
+//   warps 8, 9       issue the products of query tile 0 and 1;
+//   warp 10          copies codes into staging (a page's keys or values at a time) and reads the pages' scales;
+//   warp 11          finds the run's items and hands them to the others, two at a time;
+//   warps 12-15      widen the codes to fp16, into the operands' places, and bring the queries there.
+// Shared memory: queries, two key tiles and two value tiles in fp16 (64 KB each for 128 dimensions), three staged pages of codes.
+// Tensor memory: S and O of both query tiles; P, in fp16, takes S's place and is the left operand of the second product there.
+// A value's NaN must not reach rows that do not see its token, and a weight of zero does not keep it from them: where a key tile
+// is not seen whole by all rows, the widening warps put zero for it and note, by dimension, the first such token; rows that see
+// it get their NaN at the end.
+#include "heads_device.cuh"
+
+HS_CHECK_WORD
+
+namespace hs {
+namespace {
+
+using namespace heads;
+
+constexpr int kQRows = 128, kKeys = 128, kBlock = 2 * kQRows;
+constexpr int kThreads = 16 * 32, kMmaWarp = 8, kLoadWarp = 10, kWalkWarp = 11, kWidenWarp = 12;
+constexpr int kTakers = 15;  // warps that the items are handed to
+constexpr int kRegsLaunch = 128, kRegsSoftmax = 200, kRegsOther = 56;
+static_assert(2 * kRegsSoftmax + 2 * kRegsOther <= 4 * kRegsLaunch, "more registers than the launch has");
+constexpr int kStaged = 3, kScales = 4;  // staged pages (keys or values); key tiles whose scales are kept
+constexpr int kMinRun = 4;               // a run's key tiles, at least: fewer would be mostly set-up and joining
+enum Bar { kStFull = 0, kStEmpty = kStFull + kStaged, kKFull = kStEmpty + kStaged, kKEmpty = kKFull + 2, kVFull = kKEmpty + 2,
+           kVEmpty = kVFull + 2, kQFull = kVEmpty + 2, kQEmpty = kQFull + 2, kSFull = kQEmpty + 2, kPReady = kSFull + 2,
+           kODone = kPReady + 2, kItem = kODone + 2, kItemDone = kItem + 2, kDrain = kItemDone + 2, kBars = kDrain + 2 };
+
+// Workspace: header, a record a CTA, statistics [CTA][2][256][4], results [CTA][2][D / 4][256][4].
+__host__ __device__ constexpr size_t ws_stats_offset(int ctas) { return sizeof(RunHeader) + (size_t)ctas * sizeof(RunRecord); }
+__host__ __device__ constexpr size_t ws_parts_offset(int ctas) { return ws_stats_offset(ctas) + (size_t)ctas * 2 * kBlock * 16; }
+__host__ __device__ constexpr size_t ws_bytes(int ctas, int dim) { return ws_parts_offset(ctas) + (size_t)ctas * 2 * kBlock * dim * 4; }
+
+// What a call has of one request: `blocks` is 0 where it has no queries, or at most `limit` columns.
+struct Request {
+  int64_t t0;
+  int n, ctx, keys, blocks;
+  __device__ __forceinline__ void load(const HeadsAttendParams& p, int r, int limit) {
+    p.ragged.tokens(r, &t0, &n);
+    ctx = __ldg(p.a.ctx_len + r);
+    keys = max(0, min(ctx, p.a.max_pages * kHeadsPage));
+    const int cols = n * p.group;
+    blocks = cols > limit ? (cols + kBlock - 1) / kBlock : 0;
+  }
+  // tokens that column c sees
+  __device__ __forceinline__ int sees(const HeadsAttendParams& p, int c) const {
+    return p.a.causal ? max(0, min(keys, ctx - n + 1 + c / p.group)) : keys;
+  }
+  // key tiles of block b
+  __device__ __forceinline__ int tiles(const HeadsAttendParams& p, int b) const {
+    return max(1, (sees(p, min(n * p.group, (b + 1) * kBlock) - 1) + kKeys - 1) / kKeys);
+  }
+};
+// Key tiles of a request's blocks (of one head), by the whole warp.
+__device__ __forceinline__ int64_t request_tiles(const HeadsAttendParams& p, const Request& q) {
+  int64_t s = 0;
+  for (int b = threadIdx.x & 31; b < q.blocks; b += 32) s += q.tiles(p, b);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+  return s;
+}
+
+struct Start {
+  int r, head, block, tile;
+  int64_t left;
+};
+
+// One item, or this run's part of it: key tiles [k0, k1) of `tiles`.  In shared memory, two of them; everything else that belongs
+// to an item is kept twice too.
+struct Item {
+  int64_t t0;          // the request's first query token
+  int32_t request, head, col0, rows;  // the item's first column of (request, head), and how many
+  int32_t k0, k1, tiles;
+  int32_t end[2];      // the query tile's part of the run ends here (at k0: it has none)
+  int32_t keys, shift, past;  // column c sees the first c / group + shift tokens, at most keys; past: of more than the table has room for
+  int32_t none;        // no item: the run has ended
+};
+static_assert(sizeof(Item) % 16 == 0, "alignment of what follows");
+
+template <int D>
+struct Smem {
+  static constexpr int kUnits = D / 64, kUnit = 128 * 128;  // a unit: 128 rows of 64 fp16
+  static constexpr int kStage = D * kHeadsPage;
+  static constexpr int kQ = 0, kK = kQ + 2 * kUnits * kUnit, kV = kK + 2 * kUnits * kUnit, kVPage = D * 128;
+  static constexpr int kStages = kV + 4 * kVPage, kMisc = kStages + kStaged * kStage;
+  // floats: query scales [2][256], first NaNs (ints) [2][D], page scales [kScales][8]
+  static constexpr int kNan = kMisc + 2 * kBlock * 4, kPage = kNan + 2 * D * 4, kFlag = kPage + kScales * 32, kItems = kFlag + 16, kBar = kItems + 2 * sizeof(Item);
+  static constexpr int kBytes = kBar + kBars * 8 + 1024;  // + alignment of the base
+  static_assert(kBytes <= 232448 - 256, "shared memory");
+};
+
+// tokens that column c of the item's request and head sees
+__device__ __forceinline__ int item_sees(const HeadsAttendParams& p, const Item& it, int c) {
+  return p.a.causal ? max(0, min(it.keys, c / p.group + it.shift)) : it.keys;
+}
+
+// Hands the run's items to the others (one warp).
+__device__ __forceinline__ void walk_items(const HeadsAttendParams& p, Start at, int limit, Item* items, uint32_t bars) {
+  const int lane = threadIdx.x & 31;
+  tc::Waiter w;
+  Request q{};
+  if (at.left > 0) q.load(p, at.r, limit);
+#pragma unroll 1
+  for (uint32_t k = 0;; ++k) {
+    Item it{};
+    if (at.left > 0) {
+      if (at.block == q.blocks) {
+        at.block = 0;
+        if (++at.head == p.pages.kv_heads) {
+          at.head = 0;
+          do q.load(p, ++at.r, limit);
+          while (q.blocks == 0 && at.r + 1 < p.a.R);
+        }
+      }
+      it.t0 = q.t0, it.request = at.r, it.head = at.head, it.col0 = at.block * kBlock;
+      it.rows = min(kBlock, q.n * p.group - it.col0);
+      it.tiles = q.tiles(p, at.block);
+      it.k0 = at.tile;
+      it.k1 = (int)min((int64_t)it.tiles, at.tile + at.left);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int last = min(it.rows, (t + 1) * kQRows) - 1;
+        const int mine = last < t * kQRows ? 0 : (q.sees(p, it.col0 + last) + kKeys - 1) / kKeys;
+        it.end[t] = max(it.k0, min(it.k1, mine));
+      }
+      it.keys = q.keys, it.shift = q.ctx - q.n + 1, it.past = q.ctx > q.keys;
+      at.left -= it.k1 - it.k0;
+      at.tile = 0;
+      ++at.block;
+    } else {
+      it.none = 1;
+    }
+    if (k >= 2) await(w, bars + 8 * (kItemDone + (k & 1)), (k / 2 - 1) & 1);
+    if (w.dead) break;
+    if (lane == 0) {
+      items[k & 1] = it;
+      tc::mbar_arrive(bars + 8 * (kItem + (k & 1)));
+    }
+    __syncwarp();
+    if (it.none) break;
+  }
+  if (w.dead) report(p.a.status, HS_ERR_TIMEOUT);
+}
+// The next item, for each of the others; null at the run's end, or after a wait that gave up.
+__device__ __forceinline__ const Item* take_item(const Item* items, uint32_t k, uint32_t bars, tc::Waiter& w) {
+  await(w, bars + 8 * (kItem + (k & 1)), k / 2 & 1);
+  const Item* it = items + (k & 1);
+  return w.dead || it->none ? nullptr : it;
+}
+__device__ __forceinline__ void done_with_item(uint32_t k, uint32_t bars) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bars + 8 * (kItemDone + (k & 1)));
+}
+
+// ---- copies (one warp) ----
+template <int D>
+__device__ __forceinline__ void load_items(const HeadsAttendParams& p, const Item* items, uint32_t smem) {
+  using L = Smem<D>;
+  const uint32_t bars = smem + L::kBar;
+  const int lane = threadIdx.x & 31;
+  tc::Waiter w;
+  uint32_t u = 0, tile = 0;  // staged pages and key tiles so far
+#pragma unroll 1
+  for (uint32_t k = 0;; ++k) {
+    const Item* item = take_item(items, k, bars, w);
+    if (!item) break;
+    const int request = item->request, head = item->head, keys = item->keys, k1 = item->k1;
+    const bool past = item->past;
+    int cached = -1, cached_at = -1;  // table entries: a page a lane
+#pragma unroll 1
+    for (int j = item->k0; j < k1 && !w.dead; ++j, ++tile) {
+      const int page0 = 2 * j;
+      if (cached_at != (page0 & ~31)) {
+        cached_at = page0 & ~31;
+        const int page = cached_at + lane;
+        cached = -1;
+        if (page * kHeadsPage < keys && HS_CHECK(request < p.a.R && page < p.a.max_pages, kChkTablePage))
+          cached = __ldg(p.pages.table + (int64_t)request * p.a.max_pages + page);
+      }
+      int block[2];
+      bool there[2];
+      bool bad = past;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        block[i] = __shfl_sync(0xFFFFFFFFu, cached, (page0 + i) & 31);
+        there[i] = block[i] >= 0 && block[i] < p.pages.num_blocks;
+        bad |= (page0 + i) * kHeadsPage < keys && !there[i];
+      }
+      if (bad && lane == 0) report(p.a.status, HS_ERR_TABLE_RANGE);
+      // lanes 0..3: the scales of keys and values of both pages
+      const int b = lane & 1 ? block[1] : block[0];
+      const bool is = lane & 1 ? there[1] : there[0];
+      float scale = 1.f;
+      if (lane < 4 && is) scale = *p.pages.scale(b, head + (lane >> 1) * p.pages.kv_heads, D);
+      if (lane >= 2 && lane < 4) scale = log2f(scale);
+      const uint32_t scales = smem + L::kPage + tile % kScales * 32;
+      __syncwarp();
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i, ++u) {
+        const uint32_t slot = u % kStaged, bar = bars + 8 * (kStFull + slot);
+        if (u >= kStaged) await(w, bars + 8 * (kStEmpty + slot), (u / kStaged - 1) & 1);
+        if (w.dead) break;
+        if (i == 0) {
+          if (lane < 4) sts_u(scales + 4 * lane, __float_as_uint(scale));
+          if (lane < 2) sts_u(scales + 16 + 4 * lane, is);
+          __syncwarp();
+        }
+        const int pg = i & 1;
+        const bool copy = pg ? there[1] : there[0];
+        if (lane == 0) {
+          if (copy) {
+            const uint8_t* from = p.pages.codes(pg ? block[1] : block[0], head, D) + (i >> 1) * L::kStage;
+            tc::mbar_expect(bar, L::kStage);
+            bulk_copy(smem + L::kStages + slot * L::kStage, from, L::kStage, bar);
+          } else {
+            tc::mbar_arrive(bar);
+          }
+        }
+        __syncwarp();
+      }
+    }
+    done_with_item(k, bars);
+  }
+  // no copy is in flight when the CTA ends
+  tc::Drain drain;
+  for (uint32_t x = u > kStaged ? u - kStaged : 0; x < u; ++x) drain.wait(bars + 8 * (kStFull + x % kStaged), x / kStaged & 1);
+  if (w.dead) report(p.a.status, HS_ERR_TIMEOUT);
+}
+
+// ---- operands (four warps) ----
+
+// Queries of query tile t, in fp16: 128 rows, a row D / 8 lanes'.
+template <int D>
+__device__ __forceinline__ void bring_queries(const HeadsAttendParams& p, const Item* it, int t, uint32_t smem, uint32_t qs, float sign) {
+  using L = Smem<D>;
+  constexpr int kLanes = D / 8, kRows = 128 / kLanes, kAhead = 4;  // lanes of a row, rows at a time, loads in flight
+  const int thread = threadIdx.x & 127, piece = thread % kLanes;
+  const bool f16 = p.a.dtype == HS_FP16;
+  const uint16_t* src = static_cast<const uint16_t*>(p.a.q) + it->t0 * p.a.q_token_stride + (it->head * p.group) * p.a.q_head_stride + 8 * piece;
+  const int rows = it->rows, col0 = it->col0;
+#pragma unroll 1
+  for (int r0 = thread / kLanes; r0 < kQRows; r0 += kRows * kAhead) {
+    uint4 v[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int row = t * kQRows + r0 + i * kRows, c = col0 + row, token = c / p.group;
+      v[i] = make_uint4(0, 0, 0, 0);
+      if (row < rows)
+        v[i] = __ldg(reinterpret_cast<const uint4*>(src + token * p.a.q_token_stride + (c - token * p.group) * p.a.q_head_stride));
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int row = r0 + i * kRows;
+      float x[8], top = 0.f;
+      if (f16)
+        Vec8<__half>{v[i]}.values(x);
+      else
+        Vec8<__nv_bfloat16>{v[i]}.values(x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[e]));
+#pragma unroll
+      for (int d = 1; d < kLanes; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+      const int e = query_field(top);
+      const float f = sign * power_of_field(254 - e);
+      if (piece == 0) sts_u(qs + 4 * (t * kQRows + row), __float_as_uint(power_of_field(e)));
+      const uint32_t to = smem + L::kQ + (t * L::kUnits + (piece >> 3)) * L::kUnit + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
+      asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(pack_half(x[0] * f, x[1] * f)),
+                   "r"(pack_half(x[2] * f, x[3] * f)), "r"(pack_half(x[4] * f, x[5] * f)), "r"(pack_half(x[6] * f, x[7] * f))
+                   : "memory");
+    }
+  }
+}
+
+// A staged page's keys or values to fp16.  Row r of block db (a token's 64 dimensions, or a dimension's 64 tokens) goes to row r
+// of `to` + db * step.  zero: the page is not there.  clean: NaN codes become zero and are noted, see the head of this file.
+template <int D>
+__device__ __forceinline__ void widen(uint32_t from, uint32_t to, int step, bool zero, bool clean, int key0, int* nan_first, int* flag) {
+  const int thread = threadIdx.x & 127;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    const int n = i * 128 + thread, db = n >> 8, row = (n >> 2) & 63, piece = n & 3;
+    uint4 v = lds16(from + n * 16);
+    if (zero) v = make_uint4(0, 0, 0, 0);
+    uint32_t words[4] = {v.x, v.y, v.z, v.w};
+    if (clean) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const uint32_t is = nan_codes(words[x]);
+        if (is) {
+          words[x] &= ~((is >> 7) * 0xFFu);
+          atomicMin(nan_first + db * 64 + row, key0 + 16 * piece + 4 * x + ((__ffs(is) - 1) >> 3));
+          *flag = 1;
+        }
+      }
+    }
+    const uint32_t at = to + db * step + row * 128;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint2 a = half_of_codes(words[2 * h]), b = half_of_codes(words[2 * h + 1]);
+      asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + (((2 * piece + h) ^ (row & 7)) << 4)), "r"(a.x), "r"(a.y),
+                   "r"(b.x), "r"(b.y)
+                   : "memory");
+    }
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void widen_items(const HeadsAttendParams& p, const Item* items, uint32_t smem, uint8_t* raw) {
+  using L = Smem<D>;
+  const uint32_t bars = smem + L::kBar;
+  const int lane = threadIdx.x & 31;
+  const float sign = p.scale_log2 < 0.f ? -1.f : 1.f;
+  tc::Waiter w;
+  uint32_t u = 0, tile = 0, queries[2] = {0, 0};
+  auto arrive = [&](int bar) {
+    tc::fence_async_smem();
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(bars + 8 * bar);
+  };
+#pragma unroll 1
+  for (uint32_t k = 0;; ++k) {
+    const Item* it = take_item(items, k, bars, w);
+    if (!it) break;
+    int* nan_first = reinterpret_cast<int*>(raw + L::kNan) + (k & 1) * D;
+    int* flag = reinterpret_cast<int*>(raw + L::kFlag) + (k & 1);
+    for (int i = threadIdx.x & 127; i < D; i += 128) nan_first[i] = INT_MAX;
+    if ((threadIdx.x & 127) == 0) *flag = 0;
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      if (it->end[t] <= it->k0) continue;
+      if (queries[t] > 0) await(w, bars + 8 * (kQEmpty + t), (queries[t] - 1) & 1);
+      ++queries[t];
+      bring_queries<D>(p, it, t, smem, smem + L::kMisc + (k & 1) * kBlock * 4, sign);
+      arrive(kQFull + t);
+    }
+    const int all_see = item_sees(p, *it, it->col0), k1 = it->k1;
+#pragma unroll 1
+    for (int j = it->k0; j < k1; ++j, ++tile) {
+      const uint32_t buf = tile & 1, scales = smem + L::kPage + tile % kScales * 32;
+      const bool clean = (j + 1) * kKeys > all_see;
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i, ++u) {
+        const uint32_t slot = u % kStaged;
+        const int page = i & 1;
+        const bool values = i >= 2;
+        if (page == 0 && tile >= 2) await(w, bars + 8 * ((values ? kVEmpty : kKEmpty) + buf), (tile / 2 - 1) & 1);
+        await(w, bars + 8 * (kStFull + slot), u / kStaged & 1);
+        const bool zero = lds_u(scales + 16 + 4 * page) == 0;
+        const uint32_t from = smem + L::kStages + slot * L::kStage;
+        if (values)
+          widen<D>(from, smem + L::kV + (2 * buf + page) * L::kVPage, 64 * 128, zero, clean, j * kKeys + page * kHeadsPage, nan_first, flag);
+        else
+          widen<D>(from, smem + L::kK + buf * L::kUnits * L::kUnit + page * 64 * 128, L::kUnit, zero, false, 0, nan_first, flag);
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bars + 8 * (kStEmpty + slot));
+        if (page == 1) arrive((values ? kVFull : kKFull) + buf);
+      }
+    }
+    done_with_item(k, bars);
+  }
+  if (w.dead) report(p.a.status, HS_ERR_TIMEOUT);
+}
+
+// ---- products (one warp a query tile) ----
+// Both warps wait for every key tile's keys and values and release them, whether their query tile needs them or not.
+template <int D>
+__device__ __forceinline__ void issue_items(const HeadsAttendParams& p, const Item* list, int t, uint32_t smem, uint32_t tmem) {
+  using L = Smem<D>;
+  constexpr uint32_t kIdS = tc::idesc(true, 128, kKeys, false, false);
+  constexpr uint32_t kIdO = tc::idesc(true, 128, D, false, false);
+  const uint32_t bars = smem + L::kBar;
+  tc::Waiter w;
+  const bool leader = tc::elect();
+  const uint64_t dq = tc::desc(smem + L::kQ + t * L::kUnits * L::kUnit, 16, 1024, tc::kSwizzle128);
+  const uint64_t dk = tc::desc(smem + L::kK, 16, 1024, tc::kSwizzle128);
+  const uint64_t dv = tc::desc(smem + L::kV, 16, 1024, tc::kSwizzle128);
+  auto wait = [&](int bar, uint32_t parity) {
+    w.wait(bars + 8 * bar, parity);
+    __syncwarp();
+    tc::fence_after();
+  };
+  uint32_t base = 0, items = 0, phase = 0;  // key tiles before this item; items with work, key tiles done, of the query tile
+#pragma unroll 1
+  for (uint32_t number = 0;; ++number) {
+    const Item* it = take_item(list, number, bars, w);
+    if (!it) break;
+    const int k0 = it->k0, k1 = it->k1, end = it->end[t];
+    auto scores = [&](int j) {
+      const uint32_t n = base + j - k0, buf = n & 1;
+      wait(kKFull + buf, n / 2 & 1);
+#pragma unroll
+      for (int i = 0; i < L::kUnits; ++i) {
+        const uint64_t da = dq + (uint32_t)(i * L::kUnit >> 4), db = dk + (uint32_t)((buf * L::kUnits + i) * L::kUnit >> 4);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tc::mma_ss(tmem + t * 128, da + (k * 32 >> 4), db + (k * 32 >> 4), kIdS, i > 0 || k > 0, leader);
+      }
+      tc::commit(bars + 8 * (kSFull + t), leader);
+      tc::commit(bars + 8 * (kKEmpty + buf), leader);
+      if (j + 1 == end) tc::commit(bars + 8 * (kQEmpty + t), leader);
+    };
+    if (end > k0) {
+      wait(kQFull + t, items & 1);
+      ++items;
+      if (phase > 0) wait(kODone + t, (phase - 1) & 1);  // the item before: its last P has been read
+      scores(k0);
+    }
+#pragma unroll 1
+    for (int j = k0; j < end; ++j, ++phase) {
+      const uint32_t n = base + j - k0, buf = n & 1;
+      wait(kPReady + t, phase & 1);
+      wait(kVFull + buf, n / 2 & 1);
+#pragma unroll
+      for (int page = 0; page < 2; ++page) {
+        const uint64_t db = dv + (uint32_t)((2 * buf + page) * L::kVPage >> 4);
+        // P: 16 tokens are 8 columns
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          tc::mma_ts(tmem + 256 + t * 128, tmem + t * 128 + (page * 4 + k) * 8, db + (k * 32 >> 4), kIdO,
+                     j > k0 || page > 0 || k > 0, leader);
+      }
+      tc::commit(bars + 8 * (kODone + t), leader);
+      tc::commit(bars + 8 * (kVEmpty + buf), leader);
+      if (j + 1 < end) {
+        wait(kODone + t, phase & 1);  // P, in S's place, has been read
+        scores(j + 1);
+      }
+    }
+#pragma unroll 1
+    for (int j = end; j < k1; ++j) {  // what only the other query tile reads
+      const uint32_t n = base + j - k0, buf = n & 1;
+      wait(kKFull + buf, n / 2 & 1);
+      tc::commit(bars + 8 * (kKEmpty + buf), leader);
+      wait(kVFull + buf, n / 2 & 1);
+      tc::commit(bars + 8 * (kVEmpty + buf), leader);
+    }
+    base += k1 - k0;
+    done_with_item(number, bars);
+  }
+  tc::commit(bars + 8 * (kDrain + t), leader);
+  tc::Drain drain;
+  drain.wait(bars + 8 * (kDrain + t), 0);
+  __syncwarp();
+  if (w.dead) report(p.a.status, HS_ERR_TIMEOUT);
+}
+
+// ---- softmax and results (128 threads a query tile) ----
+template <int D>
+__device__ __forceinline__ void softmax_items(const HeadsAttendParams& p, const Item* items, int64_t run, uint32_t smem, const uint8_t* raw,
+                                              uint32_t tmem) {
+  using L = Smem<D>;
+  const uint32_t bars = smem + L::kBar;
+  tc::Waiter w;
+  const int t = threadIdx.x >> 7, lane = threadIdx.x & 31;
+  const int row = threadIdx.x & 255;
+  const uint32_t lanes = (uint32_t)(32 * ((threadIdx.x >> 5) & 3)) << 16;
+  const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * 128;
+  const float scale = fabsf(p.scale_log2);
+  float4* stats = reinterpret_cast<float4*>(reinterpret_cast<uint8_t*>(p.workspace) + ws_stats_offset(gridDim.x)) +
+                  (int64_t)blockIdx.x * 2 * kBlock;
+  float4* parts = reinterpret_cast<float4*>(reinterpret_cast<uint8_t*>(p.workspace) + ws_parts_offset(gridDim.x)) +
+                  (int64_t)blockIdx.x * 2 * kBlock * (D / 4);
+  uint32_t phase = 0, before = 0;  // key tiles of this query tile; of the CTA, in the items before
+  int64_t place = run * blockIdx.x;
+  RunRecord* record = reinterpret_cast<RunRecord*>(reinterpret_cast<uint8_t*>(p.workspace) + sizeof(RunHeader)) + blockIdx.x;
+  if (threadIdx.x == 0) *record = RunRecord{0, 0, 0, 0, 0, 0};
+#pragma unroll 1
+  for (uint32_t k = 0;; ++k) {
+    const Item* it = take_item(items, k, bars, w);
+    if (!it) break;
+    const int col = it->col0 + row, k0 = it->k0, end = it->end[t];
+    const bool there = row < it->rows;
+    const int sees = there ? item_sees(p, *it, col) : 0;
+    const int all_see = item_sees(p, *it, it->col0 + t * kQRows);  // (its first row sees least)
+    float ref = -INFINITY, m = -INFINITY, l = 0.f, anchor = 0.f, qs = 0.f;
+#pragma unroll 1
+    for (int j = k0; j < end; ++j, ++phase) {
+      w.wait(bars + 8 * (kSFull + t), phase & 1);
+      __syncwarp();
+      tc::fence_after();
+      if (j == k0) qs = scale * lds_f(smem + L::kMisc + ((k & 1) * kBlock + row) * 4);
+      const uint32_t scales = smem + L::kPage + (before + j - k0) % kScales * 32;
+      float s[128];
+      tc::tmem_ld<128>(ts, s);
+      const float size[2] = {lds_f(scales + 8), lds_f(scales + 12)};
+      float c[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) c[i] = fminf(fmaxf(lds_f(scales + 4 * i) * qs, 1.17549435e-38f), 3.402823466e38f);
+      const bool missing = (lds_u(scales + 16) & lds_u(scales + 20)) == 0;
+      tc::tmem_wait_ld();
+      tc::touch<128>(s);
+      if (missing || (j + 1) * kKeys > all_see) {
+        const int left = sees - j * kKeys;
+        const int left0 = lds_u(scales + 16) ? left : 0, left1 = lds_u(scales + 20) ? left : 0;
+#pragma unroll
+        for (int x = 0; x < 128; ++x)
+          if (x >= (x < 64 ? left0 : left1)) s[x] = -INFINITY;
+      }
+      float top[2] = {__fmul_rn(tc::max_of<64>(s), c[0]), __fmul_rn(tc::max_of<64>(s + 64), c[1])};
+      if (__any_sync(0xFFFFFFFFu, fabsf(top[0]) > kLarge || fabsf(top[1]) > kLarge || anchor != 0.f)) {
+        // (a page that is not seen has a top of -infinity and does not count)
+        const float most = fmaxf(top[0], top[1]);
+        if (fabsf(most) <= 3.402823466e38f && (most - anchor > kLarge || (ref == -INFINITY && fabsf(most) > kLarge))) {
+          const float by = most - anchor;
+          anchor = most;
+          ref -= by, m -= by;
+        }
+#pragma unroll
+        for (int x = 0; x < 128; ++x) s[x] = __fsub_rn(__fmul_rn(s[x], c[x >> 6]), anchor);  // (rounded as the tops are)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) top[i] -= anchor, c[i] = 1.f;
+      }
+      const float most = fmaxf(top[0] + size[0], top[1] + size[1]);
+      const bool over = most > ref + kLazy;
+      if (__any_sync(0xFFFFFFFFu, over)) {
+        const float now = over ? most - kTop : ref;
+        const float alpha = over ? exp2f(ref - now) : 1.f;
+        ref = now;
+        if (j > k0) {  // the products so far have finished: this tile's scores were issued after them
+#pragma unroll 1
+          for (int x = 0; x < D; x += 16) {
+            float o[16];
+            tc::tmem_ld16(to + x, o);
+            tc::tmem_wait_ld();
+            tc::touch<16>(o);
+#pragma unroll
+            for (int y = 0; y < 16; ++y) o[y] *= alpha;
+            tc::tmem_st16(to + x, o);
+          }
+          tc::tmem_wait_st();
+        }
+      }
+      const float r = ref == -INFINITY ? 0.f : ref;
+      const float higher = fmaxf(top[0], top[1]);
+      if (higher > m + kFar) {
+        l = m == -INFINITY ? 0.f : l * tc::exp2_fast(m - higher);
+        m = higher;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float bias = size[i] - r;
+        if (top[i] + size[i] < r - kFar) bias = top[i] < -2.f * kLarge ? -INFINITY : -kFar - top[i];
+        const float2 c2 = make_float2(c[i], c[i]), b2 = make_float2(bias, bias);
+        float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+#pragma unroll
+        for (int x = 0; x < 64; x += 32) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int y = 0; y < 16; ++y) {
+            const float2 z = tc::fma2(make_float2(s[64 * i + x + 2 * y], s[64 * i + x + 2 * y + 1]), c2, b2);
+            const float2 e = make_float2(tc::exp2_fast(z.x), tc::exp2_fast(z.y));
+            if (y & 1)
+              sum1 = tc::add2(sum1, e);
+            else
+              sum0 = tc::add2(sum0, e);
+            pk[y] = pack_half(e.x, e.y);
+          }
+          tc::tmem_st16(ts + (64 * i + x) / 2, reinterpret_cast<const float*>(pk));
+        }
+        if (bias != -INFINITY) l += ((sum0.x + sum0.y) + (sum1.x + sum1.y)) * tc::exp2_fast(-bias - m);
+      }
+      tc::tmem_wait_st();
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bars + 8 * (kPReady + t));
+    }
+    // results
+    const bool work = end > k0, whole = k0 == 0 && it->k1 == it->tiles;
+    if (work) {
+      w.wait(bars + 8 * (kODone + t), (phase - 1) & 1);
+      __syncwarp();
+      tc::fence_after();
+    }
+    const int* nan_first = reinterpret_cast<const int*>(raw + L::kNan) + (k & 1) * D;
+    const bool nans = work && *(reinterpret_cast<const volatile int*>(raw + L::kFlag) + (k & 1)) != 0;
+    const int64_t begins = place - k0;
+    const int part = begins > run * blockIdx.x ? 1 : 0;
+    const float up = l == 0.f ? 0.f : exp2f(0.5f * (ref - m)), inv = l == 0.f ? 0.f : up / l;
+    const int in_token = col / p.group;
+    const int64_t token = it->t0 + (there ? in_token : 0);
+    const int head = it->head * p.group + (there ? col - in_token * p.group : 0);
+    const bool writes = there && HS_CHECK(token >= 0 && token < p.a.n && head < p.a.q_heads, kChkOutPos);
+    uint16_t* out = static_cast<uint16_t*>(p.a.out) + token * p.a.out_token_stride + head * p.a.out_head_stride;
+    const bool f16 = p.a.dtype == HS_FP16;
+    if (whole || work) {
+#pragma unroll 1
+      for (int x = 0; x < D; x += 32) {
+        float o[32];
+        if (work) {
+          tc::tmem_ld<32>(to + x, o);
+          tc::tmem_wait_ld();
+          tc::touch<32>(o);
+        }
+#pragma unroll
+        for (int y = 0; y < 32; ++y) {
+          if (!work) o[y] = 0.f;
+          if (nans && sees > nan_first[x + y]) o[y] = __uint_as_float(0x7FC00000u);
+        }
+        if (whole) {
+#pragma unroll
+          for (int y = 0; y < 32; ++y) o[y] = l == 0.f ? 0.f : o[y] * up * inv;
+          if (writes) {
+#pragma unroll
+            for (int y = 0; y < 32; y += 8)
+              *reinterpret_cast<uint4*>(out + x + y) = make_uint4(pack(f16, o[y], o[y + 1]), pack(f16, o[y + 2], o[y + 3]),
+                                                                  pack(f16, o[y + 4], o[y + 5]), pack(f16, o[y + 6], o[y + 7]));
+          }
+        } else if (there) {
+#pragma unroll
+          for (int y = 0; y < 32; y += 4)
+            parts[(part * (D / 4) + (x + y) / 4) * kBlock + row] = make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
+        }
+      }
+    }
+    if (whole) {
+      if (writes && p.a.lse) p.a.lse[token * p.a.q_heads + head] = l == 0.f ? -INFINITY : (anchor + (m + log2f(l))) * kLn2;
+    } else {
+      if (there) stats[part * kBlock + row] = make_float4(ref, m, l, anchor);
+      if (threadIdx.x == 0 && k0 == 0)
+        *record = RunRecord{begins, begins + it->tiles, it->request, it->head, it->col0 / kBlock, it->rows};
+    }
+    place += it->k1 - k0;
+    before += it->k1 - k0;
+    tc::fence_before();
+    done_with_item(k, bars);
+  }
+  if (w.dead) report(p.a.status, HS_ERR_TIMEOUT);
+}
+
+// Where this CTA's run begins; by all threads, before the roles part.  Scratch: shared memory that nothing else uses yet.
+struct Scratch {
+  int64_t sums[kThreads / 32];
+  int64_t offset;
+  Start start;
+};
+__device__ __forceinline__ int64_t find_start(const HeadsAttendParams& p, int limit, Scratch* s, int64_t* run_length) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // key tiles of the request of each thread
+  auto tiles_of = [&](int r) {
+    Request q{};
+    if (r < p.a.R) q.load(p, r, limit);
+    int64_t mine = 0;
+    for (unsigned has = __ballot_sync(0xFFFFFFFFu, q.blocks > 0); has; has &= has - 1) {
+      const int who = __ffs(has) - 1;
+      Request x;
+      x.t0 = 0;
+      x.n = __shfl_sync(0xFFFFFFFFu, q.n, who), x.ctx = __shfl_sync(0xFFFFFFFFu, q.ctx, who);
+      x.keys = __shfl_sync(0xFFFFFFFFu, q.keys, who), x.blocks = __shfl_sync(0xFFFFFFFFu, q.blocks, who);
+      const int64_t n = request_tiles(p, x) * p.pages.kv_heads;
+      if (lane == who) mine = n;
+    }
+    return mine;
+  };
+  bool bad = false;
+  int64_t sum = 0, kept = 0;
+  for (int r0 = 0; r0 < p.a.R; r0 += kThreads) {
+    const int r = r0 + threadIdx.x;
+    int64_t t0;
+    int n;
+    if (r < p.a.R) bad |= !p.ragged.tokens(r, &t0, &n);
+    kept = tiles_of(r);
+    sum += kept;
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+  if (lane == 0) s->sums[warp] = sum;
+  bad = __syncthreads_or(bad);
+  int64_t total = 0;
+  for (int i = 0; i < kThreads / 32; ++i) total += s->sums[i];
+  if (bad) total = 0;
+  const int64_t run = max((int64_t)kMinRun, (total + gridDim.x - 1) / gridDim.x), begin = run * blockIdx.x;
+  __syncthreads();
+  int64_t before = 0;
+  for (int r0 = 0; r0 < p.a.R && begin < total; r0 += kThreads) {
+    const int r = r0 + threadIdx.x;
+    const int64_t mine = p.a.R > kThreads ? tiles_of(r) : kept;
+    int64_t upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t x = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+      if (lane >= d) upto += x;
+    }
+    if (lane == 31) s->sums[warp] = upto;
+    __syncthreads();
+    int64_t first = before + upto - mine;
+    for (int i = 0; i < kThreads / 32; ++i) {
+      if (i < warp) first += s->sums[i];
+      before += s->sums[i];
+    }
+    if (begin >= first && begin < first + mine) s->start.r = r, s->offset = begin - first;
+    __syncthreads();
+  }
+  if (begin < total && warp == 0) {
+    Request q;
+    const int r = s->start.r;
+    q.load(p, r, limit);
+    const int64_t a_head = request_tiles(p, q);
+    int64_t left = s->offset % a_head;
+    int block = -1, tile = 0;
+    for (int b0 = 0; block < 0; b0 += 32) {
+      const int n = b0 + lane < q.blocks ? q.tiles(p, b0 + lane) : 0;
+      int upto = n;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int x = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+        if (lane >= d) upto += x;
+      }
+      const unsigned here = __ballot_sync(0xFFFFFFFFu, left < upto);
+      if (here) {
+        const int who = __ffs(here) - 1;
+        block = b0 + who;
+        tile = (int)left - (__shfl_sync(0xFFFFFFFFu, upto, who) - __shfl_sync(0xFFFFFFFFu, n, who));
+      } else {
+        left -= __shfl_sync(0xFFFFFFFFu, upto, 31);
+        if (b0 + 32 >= q.blocks) block = 0;  // (not reached: the offset lies within the head's tiles)
+      }
+    }
+    if (lane == 0) {
+      s->start.head = (int)(s->offset / a_head);
+      s->start.block = block, s->start.tile = tile;
+    }
+  }
+  if (threadIdx.x == 0) {
+    s->start.left = begin < total ? min(run, total - begin) : 0;
+    if (blockIdx.x == 0) *reinterpret_cast<RunHeader*>(p.workspace) = RunHeader{run, total};
+  }
+  __syncthreads();
+  *run_length = run;
+  return total;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const HeadsAttendParams p, int limit) {
+  using L = Smem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  asm volatile("griddepcontrol.launch_dependents;");  // prompt_join_kernel waits for this kernel's results by itself
+  const uint32_t smem = (tc::smem_u32(smem_raw) + 1023) & ~1023u;
+  uint8_t* raw = smem_raw + (smem - tc::smem_u32(smem_raw));
+  const uint32_t bars = smem + L::kBar;
+  const int warp = threadIdx.x >> 5;
+  Scratch* scratch = reinterpret_cast<Scratch*>(raw + L::kMisc);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(raw + L::kFlag) + 2;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStaged; ++i) tc::mbar_init(bars + 8 * (kStFull + i), 1), tc::mbar_init(bars + 8 * (kStEmpty + i), 4);
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(bars + 8 * (kKFull + i), 4);
+      tc::mbar_init(bars + 8 * (kKEmpty + i), 2);
+      tc::mbar_init(bars + 8 * (kVFull + i), 4);
+      tc::mbar_init(bars + 8 * (kVEmpty + i), 2);
+      tc::mbar_init(bars + 8 * (kQFull + i), 4);
+      tc::mbar_init(bars + 8 * (kQEmpty + i), 1);
+      tc::mbar_init(bars + 8 * (kSFull + i), 1);
+      tc::mbar_init(bars + 8 * (kPReady + i), 4);
+      tc::mbar_init(bars + 8 * (kODone + i), 1);
+      tc::mbar_init(bars + 8 * (kItem + i), 1);
+      tc::mbar_init(bars + 8 * (kItemDone + i), kTakers);
+      tc::mbar_init(bars + 8 * (kDrain + i), 1);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  int64_t run;
+  find_start(p, limit, scratch, &run);
+  const Start start = scratch->start;
+  if (warp == kMmaWarp) tc::tmem_alloc(tc::smem_u32(tmem_slot), 512);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = *tmem_slot;
+  Item* items = reinterpret_cast<Item*>(raw + L::kItems);
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    softmax_items<D>(p, items, run, smem, raw, tmem);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    if (warp >= kWidenWarp)
+      widen_items<D>(p, items, smem, raw);
+    else if (warp == kWalkWarp)
+      walk_items(p, start, limit, items, bars);
+    else if (warp == kLoadWarp)
+      load_items<D>(p, items, smem);
+    else
+      issue_items<D>(p, items, warp - kMmaWarp, smem, tmem);
+  }
+  __syncwarp();
+  tc::fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc::fence_after();
+    tc::tmem_free(tmem, 512);
+  }
+}
+
+// Joins the parts of items that several runs share: a block takes 8 rows of a cut item, a thread D / 16 dimensions of one.
+constexpr int kJoinThreads = 128, kJoinRows = 8, kMaxCtas = 512;
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const HeadsAttendParams p, int ctas) {
+  constexpr int kVecs = D / 64;  // float4 a thread
+  __shared__ uint16_t cuts[kMaxCtas];
+  __shared__ int counts[kJoinThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // for the results of prompt_kernel
+  const uint8_t* ws = reinterpret_cast<const uint8_t*>(p.workspace);
+  const RunHeader header = *reinterpret_cast<const RunHeader*>(ws);
+  const RunRecord* records = reinterpret_cast<const RunRecord*>(ws + sizeof(RunHeader));
+  const float4* stats = reinterpret_cast<const float4*>(ws + ws_stats_offset(ctas));
+  const float4* parts = reinterpret_cast<const float4*>(ws + ws_parts_offset(ctas));
+  int n = 0;
+  for (int i0 = 0; i0 < ctas; i0 += kJoinThreads) {
+    const int i = i0 + threadIdx.x;
+    const bool is = i < ctas && records[i].end > records[i].begin;
+    const unsigned those = __ballot_sync(0xFFFFFFFFu, is);
+    if (lane == 0) counts[warp] = __popc(those);
+    __syncthreads();
+    int at = n + __popc(those & ((1u << lane) - 1));
+#pragma unroll
+    for (int y = 0; y < kJoinThreads / 32; ++y) {
+      if (y < warp) at += counts[y];
+      n += counts[y];
+    }
+    if (is) cuts[at] = (uint16_t)i;
+    __syncthreads();
+  }
+  constexpr int kGroups = kBlock / kJoinRows;
+  const int in_group = threadIdx.x % kJoinRows, piece = threadIdx.x / kJoinRows;  // 16 pieces of D / 16 dimensions
+  for (int item = blockIdx.x; item < n * kGroups; item += gridDim.x) {
+    const int i = cuts[item / kGroups], row = item % kGroups * kJoinRows + in_group;
+    const RunRecord rec = records[i];
+    if (row >= rec.cols) continue;
+    const int last = (int)((rec.end - 1) / header.run);
+    const int slot0 = rec.begin > i * header.run ? 1 : 0;
+    auto slot = [&](int x) { return (int64_t)x * 2 + (x == i ? slot0 : 0); };
+    float anchor = -INFINITY, ref = -INFINITY, m = -INFINITY;
+    for (int x = i; x <= last; ++x) {
+      const float4 st = stats[slot(x) * kBlock + row];
+      if (st.y != -INFINITY) anchor = fmaxf(anchor, st.w);
+    }
+    for (int x = i; x <= last; ++x) {
+      const float4 st = stats[slot(x) * kBlock + row];
+      if (st.y == -INFINITY) continue;
+      ref = fmaxf(ref, st.x + (st.w - anchor)), m = fmaxf(m, st.y + (st.w - anchor));
+    }
+    float l = 0.f;
+    float4 acc[kVecs];
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int x = i; x <= last; ++x) {
+      const float4 st = stats[slot(x) * kBlock + row];
+      if (st.y == -INFINITY) continue;
+      const float a = exp2f(st.x + (st.w - anchor) - ref);
+      l += st.z * exp2f(st.y + (st.w - anchor) - m);
+#pragma unroll
+      for (int v = 0; v < kVecs; ++v) {
+        const float4 y = parts[(slot(x) * (D / 4) + piece * kVecs + v) * kBlock + row];
+        acc[v].x += a * y.x, acc[v].y += a * y.y, acc[v].z += a * y.z, acc[v].w += a * y.w;
+      }
+    }
+    const float up = l == 0.f ? 0.f : exp2f(0.5f * (ref - m)), inv = l == 0.f ? 0.f : up / l;
+    Request q;
+    q.load(p, rec.request, 0);
+    const int col = rec.group * kBlock + row, in_token = col / p.group;
+    const int64_t token = q.t0 + in_token;
+    const int head = rec.head * p.group + col - in_token * p.group;
+    if (!HS_CHECK(token < p.a.n && head < p.a.q_heads, kChkOutPos)) continue;
+    const bool f16 = p.a.dtype == HS_FP16;
+    uint16_t* out = static_cast<uint16_t*>(p.a.out) + token * p.a.out_token_stride + head * p.a.out_head_stride + piece * (D / 16);
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v)
+      *reinterpret_cast<uint2*>(out + 4 * v) =
+          make_uint2(pack(f16, acc[v].x * up * inv, acc[v].y * up * inv), pack(f16, acc[v].z * up * inv, acc[v].w * up * inv));
+    if (piece == 0 && p.a.lse) p.a.lse[token * p.a.q_heads + head] = l == 0.f ? -INFINITY : (anchor + (m + log2f(l))) * kLn2;
+  }
+}
+
+template <int D>
+cudaError_t launch(const HeadsAttendParams& p, int limit, int dev, int sms, cudaStream_t s) {
+  using L = Smem<D>;
+  static DeviceOnce once;
+  const cudaError_t ready = once.ready(dev, [] {
+    cudaFuncAttributes f{};
+    cudaError_t e = cudaFuncGetAttributes(&f, prompt_kernel<D>);
+    // the register trade waits for ever if the launch has fewer than it hands out
+    if (e == cudaSuccess && f.numRegs != kRegsLaunch) e = cudaErrorInvalidKernelImage;
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+    return e;
+  });
+  if (ready != cudaSuccess) return ready;
+  const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
+  prompt_kernel<D><<<ctas, kThreads, L::kBytes, s>>>(p, limit);
+  count_launch();
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // its launch overlaps the end of the kernel before
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(sms * 4);
+  c.blockDim = dim3(kJoinThreads);
+  c.stream = s;
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &early;
+  c.numAttrs = 1;
+  e = cudaLaunchKernelEx(&c, prompt_join_kernel<D>, p, ctas);
+  count_launch();
+  return e;
+}
+
+}  // namespace
+
+uint32_t check_take_heads_prompt() {
+#if HS_CHECKED
+  unsigned v = 0u, z = 0u;
+  if (cudaMemcpyFromSymbol(&v, hs_check_word_, sizeof(v)) != cudaSuccess ||
+      cudaMemcpyToSymbol(hs_check_word_, &z, sizeof(z)) != cudaSuccess) {
+    cudaGetLastError();
+    return 0xFFFFFFFFu;
+  }
+  return v;
+#else
+  return 0u;
+#endif
+}
+
+size_t heads_prompt_workspace_bytes(int sms) { return ws_bytes(sms < kMaxCtas ? sms : kMaxCtas, 128); }
+
+cudaError_t launch_heads_prompt(const HeadsAttendParams& p, int limit, int dev, int sms, cudaStream_t s) {
+  return p.a.head_dim == 64 ? launch<64>(p, limit, dev, sms, s) : launch<128>(p, limit, dev, sms, s);
+}
+
+}  // namespace hs

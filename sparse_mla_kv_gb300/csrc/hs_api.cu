@@ -118,7 +118,8 @@ int32_t hs_check_status(void) {
   uint32_t first = 0u;
   for (const uint32_t site : {hs::check_take_resolve(), hs::check_take_gather(), hs::check_take_append(),
                               hs::check_take_attend(), hs::check_take_expanded(), hs::check_take_read_rows(),
-                              hs::check_take_heads_pages(), hs::check_take_heads_attend()}) {
+                              hs::check_take_heads_pages(), hs::check_take_heads_attend(),
+                              hs::check_take_heads_prompt()}) {
     if (site == 0xFFFFFFFFu) return -2;
     if (!first) first = site;
   }

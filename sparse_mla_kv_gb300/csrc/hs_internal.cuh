@@ -79,6 +79,7 @@ uint32_t check_take_expanded();
 uint32_t check_take_read_rows();
 uint32_t check_take_heads_pages();
 uint32_t check_take_heads_attend();
+uint32_t check_take_heads_prompt();
 
 // Per-layer base pointers, passed to kernels by value (kernel parameter space, no device
 // allocation).  host[] holds device-usable addresses of the pinned host pool.

@@ -431,6 +431,34 @@ def test_attend(kv, dim, group, dtype, ctx, new, causal):
     same(lse, lse2)
 
 
+PROMPTS = [
+    (2, 128, 4, torch.bfloat16, [700, 300], [700, 300]),
+    (1, 64, 8, torch.float16, [5000], [130]),
+    (4, 128, 1, torch.bfloat16, [1500, 200, 0, 90], [300, 200, 0, 65]),
+    (3, 128, 7, torch.bfloat16, [2000], [77]),
+    (2, 64, 2, torch.bfloat16, [100 + 3 * i for i in range(600)], [i % 37 for i in range(600)]),
+    (1, 128, 2, torch.bfloat16, [50, 128, 129, 256, 300], [200, 128, 129, 128, 257]),
+    (2, 64, 1, torch.float16, [1300], [1300]),
+    (1, 128, 128, torch.bfloat16, [64, 640], [3, 1]),
+]
+
+
+@pytest.mark.parametrize("kv,dim,group,dtype,ctx,new", PROMPTS)
+@pytest.mark.parametrize("causal", [True, False])
+def test_attend_prompts(kv, dim, group, dtype, ctx, new, causal):
+    test_attend(kv, dim, group, dtype, ctx, new, causal)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_attend_even_prompts(causal):
+    g = gen(20)
+    kv, dim, group, ctx, n = 2, 128, 4, [400, 90, 333], 80
+    pool, cache, table = make(g, ctx, kv, dim)
+    q = normal(g, 3 * n, kv * group, dim)
+    out, lse = hs.attend_heads(pool, table, i32(ctx), q, 0.1, causal=causal)
+    check(cache, kv, dim, table, ctx, [n] * 3, q, 0.1, out, lse, causal)
+
+
 @pytest.mark.parametrize("spread", [20, 90])
 @pytest.mark.parametrize("kv,dim,group,ctx,new", [(2, 128, 4, [900, 70], [1, 1]), (1, 64, 8, [5000], [40])])
 def test_attend_pages_of_very_different_sizes(spread, kv, dim, group, ctx, new):
