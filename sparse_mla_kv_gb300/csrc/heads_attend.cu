@@ -534,15 +534,15 @@ __global__ void __launch_bounds__(kThreads, 1) steps_kernel(const HeadsAttendPar
 }
 
 // Joins the parts of units that several runs share.  A block takes one column of a cut unit at a time; its warps take every
-// fourth part each.
-constexpr int kJoinThreads = 128, kMaxWorkers = 2048;
+// eighth part each, four at a time, so that their loads are on their way together.
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinParts = 4, kMaxWorkers = 2048;
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const HeadsAttendParams p, int workers, int group_cols) {
   constexpr int kPer = D / 32;
   __shared__ uint16_t cuts[kMaxWorkers];
-  __shared__ int counts[kJoinThreads / 32];
-  __shared__ float4 joined[4];
-  __shared__ float sums[4][D];
+  __shared__ int counts[kJoinWarps];
+  __shared__ float4 joined[kJoinWarps];
+  __shared__ float sums[kJoinWarps][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // for the results of steps_kernel
   const uint8_t* ws = reinterpret_cast<const uint8_t*>(p.workspace);
@@ -560,7 +560,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const HeadsAttendPar
     __syncthreads();
     int at = n + __popc(those & ((1u << lane) - 1));
 #pragma unroll
-    for (int y = 0; y < kJoinThreads / 32; ++y) {
+    for (int y = 0; y < kJoinWarps; ++y) {
       if (y < warp) at += counts[y];
       n += counts[y];
     }
@@ -571,63 +571,63 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const HeadsAttendPar
     const int i = cuts[item / group_cols], c = item % group_cols;
     const RunRecord rec = records[i];
     if (c >= rec.cols) continue;
+    Request q;
+    q.load(p, rec.request, group_cols, INT_MAX);
     const int last = (int)((rec.end - 1) / header.run);
     const int slot0 = rec.begin > i * header.run ? 1 : 0;
-    float anchor = -INFINITY;  // the largest of the parts that have any
-    for (int x = i + lane; x <= last; x += 32) {
-      const float4 st = stats[((int64_t)x * 2 + (x == i ? slot0 : 0)) * group_cols + c];
-      if (st.y != -INFINITY) anchor = fmaxf(anchor, st.w);
+    Joined res;
+    float acc[kPer] = {};
+    for (int x0 = i + warp; x0 <= last; x0 += kJoinWarps * kJoinParts) {
+      float4 st[kJoinParts];
+      float v[kJoinParts][kPer];
+#pragma unroll
+      for (int y = 0; y < kJoinParts; ++y) {
+        const int x = x0 + y * kJoinWarps;
+        if (x > last) continue;
+        const int64_t at = ((int64_t)x * 2 + (x == i ? slot0 : 0)) * group_cols + c;
+        st[y] = stats[at];
+        if constexpr (kPer == 4) {
+          const float4 f = *reinterpret_cast<const float4*>(parts + at * D + 4 * lane);
+          v[y][0] = f.x, v[y][1] = f.y, v[y][2] = f.z, v[y][3] = f.w;
+        } else {
+          const float2 f = *reinterpret_cast<const float2*>(parts + at * D + 2 * lane);
+          v[y][0] = f.x, v[y][1] = f.y;
+        }
+      }
+#pragma unroll
+      for (int y = 0; y < kJoinParts; ++y) {
+        if (x0 + y * kJoinWarps > last) continue;
+        const float2 f = res.join(st[y]);
+        if (st[y].y != -INFINITY) {
+#pragma unroll
+          for (int d = 0; d < kPer; ++d) acc[d] = acc[d] * f.x + v[y][d] * f.y;
+        }
+      }
     }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) anchor = fmaxf(anchor, __shfl_xor_sync(0xFFFFFFFFu, anchor, d));
-    if (anchor == -INFINITY) anchor = 0.f;
-    float ref = -INFINITY, m = -INFINITY, l = 0.f, acc[kPer] = {};
-    for (int x = i + warp; x <= last; x += 4) {
-      const int64_t at = ((int64_t)x * 2 + (x == i ? slot0 : 0)) * group_cols + c;
-      float4 st = stats[at];
-      st.x += st.w - anchor, st.y += st.w - anchor;
-      float v[kPer];
-#pragma unroll
-      for (int d = 0; d < kPer; ++d) v[d] = parts[at * D + lane * kPer + d];
-      const float now = fmaxf(ref, st.x), now_m = fmaxf(m, st.y);
-      const float a = ref == now ? 1.f : exp2f(ref - now), b = st.x == now ? (now == -INFINITY ? 0.f : 1.f) : exp2f(st.x - now);
-      const float am = m == now_m ? 1.f : exp2f(m - now_m), bm = st.y == now_m ? 1.f : exp2f(st.y - now_m);
-#pragma unroll
-      for (int d = 0; d < kPer; ++d) acc[d] = acc[d] * a + v[d] * b;
-      l = l * am + st.z * bm;
-      ref = now, m = now_m;
-    }
-    if (lane == 0) joined[warp] = make_float4(ref, m, l, 0.f);
+    if (lane == 0) joined[warp] = make_float4(res.ref, res.m, res.l, res.anchor);
 #pragma unroll
     for (int d = 0; d < kPer; ++d) sums[warp][lane * kPer + d] = acc[d];
     __syncthreads();
     if (warp == 0) {
-      float4 all[4];
+      Joined all;
+      float out[kPer] = {};
 #pragma unroll
-      for (int y = 0; y < 4; ++y) all[y] = joined[y];
-      const float top = fmaxf(fmaxf(all[0].x, all[1].x), fmaxf(all[2].x, all[3].x));
-      const float top_m = fmaxf(fmaxf(all[0].y, all[1].y), fmaxf(all[2].y, all[3].y));
-      float res[kPer] = {};
-      l = 0.f;
+      for (int y = 0; y < kJoinWarps; ++y) {
+        const float2 f = all.join(joined[y]);
 #pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        const float f = all[y].x == -INFINITY ? 0.f : exp2f(all[y].x - top);
-        l += all[y].y == -INFINITY ? 0.f : all[y].z * exp2f(all[y].y - top_m);
-#pragma unroll
-        for (int d = 0; d < kPer; ++d) res[d] += sums[y][lane * kPer + d] * f;
+        for (int d = 0; d < kPer; ++d) out[d] = out[d] * f.x + sums[y][lane * kPer + d] * f.y;
       }
-      const float up = l == 0.f ? 0.f : exp2f(0.5f * (top - top_m)), inv = l == 0.f ? 0.f : up / l;
-      Request q;
-      q.load(p, rec.request, group_cols, INT_MAX);
+      const float up = all.l == 0.f ? 0.f : exp2f(0.5f * (all.ref - all.m)), inv = all.l == 0.f ? 0.f : up / all.l;
       const int in_unit = rec.group * group_cols + c;
       const int64_t token = q.t0 + in_unit / p.group;
       const int qh = rec.head * p.group + in_unit % p.group;
       if (HS_CHECK(token < p.a.n && qh < p.a.q_heads, kChkOutPos)) {
-        uint16_t* out = static_cast<uint16_t*>(p.a.out) + token * p.a.out_token_stride + qh * p.a.out_head_stride + lane * kPer;
+        uint16_t* to = static_cast<uint16_t*>(p.a.out) + token * p.a.out_token_stride + qh * p.a.out_head_stride + lane * kPer;
 #pragma unroll
         for (int d = 0; d < kPer; d += 2)
-          *reinterpret_cast<uint32_t*>(out + d) = pack(p.a.dtype == HS_FP16, res[d] * up * inv, res[d + 1] * up * inv);
-        if (lane == 0 && p.a.lse) p.a.lse[token * p.a.q_heads + qh] = l == 0.f ? -INFINITY : (anchor + (top_m + log2f(l))) * kLn2;
+          *reinterpret_cast<uint32_t*>(to + d) = pack(p.a.dtype == HS_FP16, out[d] * up * inv, out[d + 1] * up * inv);
+        if (lane == 0 && p.a.lse)
+          p.a.lse[token * p.a.q_heads + qh] = all.l == 0.f ? -INFINITY : (all.anchor + (all.m + log2f(all.l))) * kLn2;
       }
     }
     __syncthreads();

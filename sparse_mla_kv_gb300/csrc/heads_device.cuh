@@ -60,6 +60,23 @@ __device__ __forceinline__ void await(tc::Waiter& w, uint32_t bar, uint32_t pari
   w.wait(bar, parity);
   w.dead = __any_sync(0xFFFFFFFFu, w.dead);
 }
+// What parts of a column's (or row's) results have been joined so far: the references, the sum of weights.  A part's statistics are
+// (ref, m, l, anchor); one that has seen no token has m = -infinity.
+struct Joined {
+  float anchor = -INFINITY, ref = -INFINITY, m = -INFINITY, l = 0.f;
+  // Joins a part; returns what the results so far, and the part's, are to be multiplied by.
+  __device__ __forceinline__ float2 join(float4 st) {
+    if (st.y == -INFINITY) return make_float2(1.f, 0.f);
+    const float to = fmaxf(anchor, st.w), here = st.w - to;
+    if (to != anchor) ref += anchor - to, m += anchor - to, anchor = to;
+    const float now = fmaxf(ref, st.x + here), now_m = fmaxf(m, st.y + here);
+    const float2 f = make_float2(ref == now ? 1.f : exp2f(ref - now), exp2f(st.x + here - now));
+    l = l * (m == now_m ? 1.f : exp2f(m - now_m)) + st.z * exp2f(st.y + here - now_m);
+    ref = now, m = now_m;
+    return f;
+  }
+};
+
 // The exponent field e of a power of two that brings a query's largest magnitude into fp16's range, by division: left as they
 // are (127) when it is in 2^-2 .. 2^15, where fp16 keeps all but what is 2^-23 of it.
 __device__ __forceinline__ int query_field(float top) {

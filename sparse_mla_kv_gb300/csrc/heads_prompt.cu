@@ -7,7 +7,7 @@
 //
 // Layout.  A work item is (request, head of keys and values, 256 columns): two tiles of 128 columns (query token x query head of
 // the group, token by token) over the same key tiles of 128 tokens (two pages), so that a page widened serves 256 rows.  The
-// key tiles of all items are numbered, and every CTA takes an equal run of them, whatever the contexts' lengths and the causal
+// key tiles of all items are numbered (with something added for each item), and every CTA takes an equal run of them, whatever the contexts' lengths and the causal
 // mask leave; items that are cut leave partial results in the workspace, which prompt_join_kernel joins in a fixed order.
 // 16 warps, one CTA per SM (the warpgroups trade registers):
 //   warps 0-3, 4-7   softmax and results of query tile 0 and 1, a row a thread;
@@ -34,8 +34,9 @@ constexpr int kThreads = 16 * 32, kMmaWarp = 8, kLoadWarp = 10, kWalkWarp = 11, 
 constexpr int kTakers = 15;  // warps that the items are handed to
 constexpr int kRegsLaunch = 128, kRegsSoftmax = 200, kRegsOther = 56;
 static_assert(2 * kRegsSoftmax + 2 * kRegsOther <= 4 * kRegsLaunch, "more registers than the launch has");
-constexpr int kStaged = 3, kScales = 4;  // staged pages (keys or values); key tiles whose scales are kept
-constexpr int kMinRun = 4;               // a run's key tiles, at least: fewer would be mostly set-up and joining
+constexpr int kStaged = 4, kScales = 4;  // staged pages (keys or values); key tiles whose scales are kept
+constexpr int kMinRun = 6;               // of a run, in key tiles: fewer would be mostly set-up and joining
+constexpr int kItemCost = 3;             // what an item costs beside its key tiles, in these
 enum Bar { kStFull = 0, kStEmpty = kStFull + kStaged, kKFull = kStEmpty + kStaged, kKEmpty = kKFull + 2, kVFull = kKEmpty + 2,
            kVEmpty = kVFull + 2, kQFull = kVEmpty + 2, kQEmpty = kQFull + 2, kSFull = kQEmpty + 2, kPReady = kSFull + 2,
            kODone = kPReady + 2, kItem = kODone + 2, kItemDone = kItem + 2, kDrain = kItemDone + 2, kBars = kDrain + 2 };
@@ -65,31 +66,33 @@ struct Request {
     return max(1, (sees(p, min(n * p.group, (b + 1) * kBlock) - 1) + kKeys - 1) / kKeys);
   }
 };
-// Key tiles of a request's blocks (of one head), by the whole warp.
-__device__ __forceinline__ int64_t request_tiles(const HeadsAttendParams& p, const Request& q) {
+// Units of a request's blocks (of one head), by the whole warp.
+__device__ __forceinline__ int64_t request_units(const HeadsAttendParams& p, const Request& q) {
   int64_t s = 0;
-  for (int b = threadIdx.x & 31; b < q.blocks; b += 32) s += q.tiles(p, b);
+  for (int b = threadIdx.x & 31; b < q.blocks; b += 32) s += kItemCost + q.tiles(p, b);
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
   return s;
 }
 
+// Where a run begins: `in` units into an item.  An item is kItemCost units and one for each of its key tiles.
 struct Start {
-  int r, head, block, tile;
-  int64_t left;
+  int r, head, block, in;
+  int64_t at, left;  // in units
 };
 
 // One item, or this run's part of it: key tiles [k0, k1) of `tiles`.  In shared memory, two of them; everything else that belongs
 // to an item is kept twice too.
 struct Item {
   int64_t t0;          // the request's first query token
+  int64_t begin;       // the item's first key tile among the call's units
   int32_t request, head, col0, rows;  // the item's first column of (request, head), and how many
   int32_t k0, k1, tiles;
   int32_t end[2];      // the query tile's part of the run ends here (at k0: it has none)
   int32_t keys, shift, past;  // column c sees the first c / group + shift tokens, at most keys; past: of more than the table has room for
   int32_t none;        // no item: the run has ended
 };
-static_assert(sizeof(Item) % 16 == 0, "alignment of what follows");
+static_assert(sizeof(Item) % 8 == 0, "alignment of what follows");
 
 template <int D>
 struct Smem {
@@ -97,10 +100,10 @@ struct Smem {
   static constexpr int kStage = D * kHeadsPage;
   static constexpr int kQ = 0, kK = kQ + 2 * kUnits * kUnit, kV = kK + 2 * kUnits * kUnit, kVPage = D * 128;
   static constexpr int kStages = kV + 4 * kVPage, kMisc = kStages + kStaged * kStage;
-  // floats: query scales [2][256], first NaNs (ints) [2][D], page scales [kScales][8]
-  static constexpr int kNan = kMisc + 2 * kBlock * 4, kPage = kNan + 2 * D * 4, kFlag = kPage + kScales * 32, kItems = kFlag + 16, kBar = kItems + 2 * sizeof(Item);
-  static constexpr int kBytes = kBar + kBars * 8 + 1024;  // + alignment of the base
-  static_assert(kBytes <= 232448 - 256, "shared memory");
+  // query scales (exponent fields, a byte each) [2][256], first NaNs (ints) [2][D], floats: page scales [kScales][8]
+  static constexpr int kNan = kMisc + 2 * kBlock, kPage = kNan + 2 * D * 4, kFlag = kPage + kScales * 32, kItems = kFlag + 16, kBar = kItems + 2 * sizeof(Item);
+  static constexpr int kBytes = kBar + kBars * 8;
+  static_assert(kBytes <= 232448, "shared memory");
 };
 
 // tokens that column c of the item's request and head sees
@@ -117,7 +120,8 @@ __device__ __forceinline__ void walk_items(const HeadsAttendParams& p, Start at,
 #pragma unroll 1
   for (uint32_t k = 0;; ++k) {
     Item it{};
-    if (at.left > 0) {
+    it.none = 1;
+    while (at.left > 0 && it.none) {
       if (at.block == q.blocks) {
         at.block = 0;
         if (++at.head == p.pages.kv_heads) {
@@ -126,23 +130,27 @@ __device__ __forceinline__ void walk_items(const HeadsAttendParams& p, Start at,
           while (q.blocks == 0 && at.r + 1 < p.a.R);
         }
       }
-      it.t0 = q.t0, it.request = at.r, it.head = at.head, it.col0 = at.block * kBlock;
-      it.rows = min(kBlock, q.n * p.group - it.col0);
       it.tiles = q.tiles(p, at.block);
-      it.k0 = at.tile;
-      it.k1 = (int)min((int64_t)it.tiles, at.tile + at.left);
+      const int units = (int)min((int64_t)(kItemCost + it.tiles - at.in), at.left);
+      it.begin = at.at - at.in + kItemCost;
+      it.k0 = max(0, at.in - kItemCost);
+      it.k1 = at.in + units - kItemCost;
+      if (it.k1 > it.k0) {  // (a run that ends before an item's first key tile leaves it to the next)
+        it.none = 0;
+        it.t0 = q.t0, it.request = at.r, it.head = at.head, it.col0 = at.block * kBlock;
+        it.rows = min(kBlock, q.n * p.group - it.col0);
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const int last = min(it.rows, (t + 1) * kQRows) - 1;
-        const int mine = last < t * kQRows ? 0 : (q.sees(p, it.col0 + last) + kKeys - 1) / kKeys;
-        it.end[t] = max(it.k0, min(it.k1, mine));
+        for (int t = 0; t < 2; ++t) {
+          const int last = min(it.rows, (t + 1) * kQRows) - 1;
+          const int mine = last < t * kQRows ? 0 : (q.sees(p, it.col0 + last) + kKeys - 1) / kKeys;
+          it.end[t] = max(it.k0, min(it.k1, mine));
+        }
+        it.keys = q.keys, it.shift = q.ctx - q.n + 1, it.past = q.ctx > q.keys;
       }
-      it.keys = q.keys, it.shift = q.ctx - q.n + 1, it.past = q.ctx > q.keys;
-      at.left -= it.k1 - it.k0;
-      at.tile = 0;
+      at.left -= units;
+      at.at += units;
+      at.in = 0;
       ++at.block;
-    } else {
-      it.none = 1;
     }
     if (k >= 2) await(w, bars + 8 * (kItemDone + (k & 1)), (k / 2 - 1) & 1);
     if (w.dead) break;
@@ -243,45 +251,76 @@ __device__ __forceinline__ void load_items(const HeadsAttendParams& p, const Ite
 
 // ---- operands (four warps) ----
 
-// Queries of query tile t, in fp16: 128 rows, a row D / 8 lanes'.
+// Queries of query tile t.  First all of them are copied to their places as they are, asynchronously, a row by D / 8 lanes; then
+// each thread turns a row into fp16 in place.
 template <int D>
-__device__ __forceinline__ void bring_queries(const HeadsAttendParams& p, const Item* it, int t, uint32_t smem, uint32_t qs, float sign) {
+__device__ __forceinline__ void copy_queries(const HeadsAttendParams& p, const Item* it, int t, uint32_t smem) {
   using L = Smem<D>;
-  constexpr int kLanes = D / 8, kRows = 128 / kLanes, kAhead = 4;  // lanes of a row, rows at a time, loads in flight
+  constexpr int kLanes = D / 8, kRows = 128 / kLanes;
   const int thread = threadIdx.x & 127, piece = thread % kLanes;
-  const bool f16 = p.a.dtype == HS_FP16;
-  const uint16_t* src = static_cast<const uint16_t*>(p.a.q) + it->t0 * p.a.q_token_stride + (it->head * p.group) * p.a.q_head_stride + 8 * piece;
-  const int rows = it->rows, col0 = it->col0;
-#pragma unroll 1
-  for (int r0 = thread / kLanes; r0 < kQRows; r0 += kRows * kAhead) {
-    uint4 v[kAhead];
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int row = t * kQRows + r0 + i * kRows, c = col0 + row, token = c / p.group;
-      v[i] = make_uint4(0, 0, 0, 0);
-      if (row < rows)
-        v[i] = __ldg(reinterpret_cast<const uint4*>(src + token * p.a.q_token_stride + (c - token * p.group) * p.a.q_head_stride));
-    }
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int row = r0 + i * kRows;
-      float x[8], top = 0.f;
-      if (f16)
-        Vec8<__half>{v[i]}.values(x);
-      else
-        Vec8<__nv_bfloat16>{v[i]}.values(x);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[e]));
-#pragma unroll
-      for (int d = 1; d < kLanes; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-      const int e = query_field(top);
-      const float f = sign * power_of_field(254 - e);
-      if (piece == 0) sts_u(qs + 4 * (t * kQRows + row), __float_as_uint(power_of_field(e)));
-      const uint32_t to = smem + L::kQ + (t * L::kUnits + (piece >> 3)) * L::kUnit + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
-      asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(pack_half(x[0] * f, x[1] * f)),
-                   "r"(pack_half(x[2] * f, x[3] * f)), "r"(pack_half(x[4] * f, x[5] * f)), "r"(pack_half(x[6] * f, x[7] * f))
-                   : "memory");
-    }
+  const int rows = it->rows - t * kQRows;
+  int row = thread / kLanes, c = it->col0 + t * kQRows + row, token = c / p.group;
+  // from row to row the column moves on by kRows: `tokens` of them and `heads` of the group, or one token more
+  const int tokens = kRows / p.group, heads = kRows - tokens * p.group;
+  const int64_t step = tokens * p.a.q_token_stride + heads * p.a.q_head_stride, wrap = p.a.q_token_stride - p.group * p.a.q_head_stride;
+  int in_group = c - token * p.group;
+  const uint16_t* from = static_cast<const uint16_t*>(p.a.q) + (it->t0 + token) * p.a.q_token_stride +
+                         (it->head * p.group + in_group) * p.a.q_head_stride + 8 * piece;
+  uint32_t to = smem + L::kQ + (t * L::kUnits + (piece >> 3)) * L::kUnit + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
+#pragma unroll 2
+  for (; row < kQRows; row += kRows, to += kRows * 128) {  // (kRows is a multiple of 8: the swizzle stays)
+    const bool there = row < rows;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(there ? from : static_cast<const uint16_t*>(p.a.q)),
+                 "r"(there ? 16 : 0)
+                 : "memory");
+    from += step;
+    in_group += heads;
+    if (in_group >= p.group) in_group -= p.group, from += wrap;
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// Larger magnitudes of two values of 16 bits each, in either type (NaN is passed over).
+__device__ __forceinline__ uint32_t max_magnitudes(bool f16, uint32_t a, uint32_t b) {
+  b &= 0x7FFF7FFFu;
+  if (f16)
+    asm("max.f16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+  else
+    asm("max.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+  return a;
+}
+template <int D>
+__device__ __forceinline__ void convert_queries(bool f16, int t, uint32_t smem, uint32_t qs, float sign) {
+  using L = Smem<D>;
+  const int row = threadIdx.x & 127;
+  const uint32_t at = smem + L::kQ + t * L::kUnits * L::kUnit + row * 128;
+  auto place = [&](int piece) { return at + (piece >> 3) * L::kUnit + (((piece & 7) ^ (row & 7)) << 4); };
+  uint32_t most[4] = {0, 0, 0, 0};
+#pragma unroll 4
+  for (int i = 0; i < D / 8; ++i) {
+    const uint4 v = lds16(place(i));
+    most[0] = max_magnitudes(f16, most[0], v.x), most[1] = max_magnitudes(f16, most[1], v.y);
+    most[2] = max_magnitudes(f16, most[2], v.z), most[3] = max_magnitudes(f16, most[3], v.w);
+  }
+  most[0] = max_magnitudes(f16, max_magnitudes(f16, most[0], most[1]), max_magnitudes(f16, most[2], most[3]));
+  float2 two;
+  if (f16)
+    two = __half22float2(*reinterpret_cast<const __half2*>(&most[0]));
+  else
+    two = make_float2(__uint_as_float(most[0] << 16), __uint_as_float(most[0] & 0xFFFF0000u));
+  const int e = query_field(fmaxf(two.x, two.y));
+  const float f = sign * power_of_field(254 - e);
+  asm volatile("st.shared.u8 [%0], %1;" ::"r"(qs + t * kQRows + row), "r"(e) : "memory");
+  if (f16 && f == 1.f) return;
+#pragma unroll 2
+  for (int i = 0; i < D / 8; ++i) {
+    float x[8];
+    if (f16)
+      Vec8<__half>{lds16(place(i))}.values(x);
+    else
+      Vec8<__nv_bfloat16>{lds16(place(i))}.values(x);
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(place(i)), "r"(pack_half(x[0] * f, x[1] * f)),
+                 "r"(pack_half(x[2] * f, x[3] * f)), "r"(pack_half(x[4] * f, x[5] * f)), "r"(pack_half(x[6] * f, x[7] * f))
+                 : "memory");
   }
 }
 
@@ -289,25 +328,35 @@ __device__ __forceinline__ void bring_queries(const HeadsAttendParams& p, const 
 // of `to` + db * step.  zero: the page is not there.  clean: NaN codes become zero and are noted, see the head of this file.
 template <int D>
 __device__ __forceinline__ void widen(uint32_t from, uint32_t to, int step, bool zero, bool clean, int key0, int* nan_first, int* flag) {
-  const int thread = threadIdx.x & 127;
+  const int thread = threadIdx.x & 127, row0 = (thread >> 2) & 31, piece = thread & 3;
+  uint4 v[D / 32];
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i) {
-    const int n = i * 128 + thread, db = n >> 8, row = (n >> 2) & 63, piece = n & 3;
-    uint4 v = lds16(from + n * 16);
-    if (zero) v = make_uint4(0, 0, 0, 0);
-    uint32_t words[4] = {v.x, v.y, v.z, v.w};
-    if (clean) {
+  for (int i = 0; i < D / 32; ++i) v[i] = lds16(from + (i * 128 + thread) * 16);
+  if (zero || clean) {
+#pragma unroll 1
+    for (int i = 0; i < D / 32; ++i) {
+      const uint32_t at = from + (i * 128 + thread) * 16;
+      uint32_t words[4] = {lds_u(at), lds_u(at + 4), lds_u(at + 8), lds_u(at + 12)};
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        const uint32_t is = nan_codes(words[x]);
+        const uint32_t is = zero ? 0 : nan_codes(words[x]);
         if (is) {
           words[x] &= ~((is >> 7) * 0xFFu);
-          atomicMin(nan_first + db * 64 + row, key0 + 16 * piece + 4 * x + ((__ffs(is) - 1) >> 3));
+          atomicMin(nan_first + i * 32 + row0, key0 + 16 * piece + 4 * x + ((__ffs(is) - 1) >> 3));
           *flag = 1;
         }
+        if (is || zero) sts_u(at + 4 * x, zero ? 0 : words[x]);
       }
     }
-    const uint32_t at = to + db * step + row * 128;
+    tc::fence_async_smem();  // (the next copy goes to the same place)
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) v[i] = lds16(from + (i * 128 + thread) * 16);
+  }
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    const int row = (i & 1) * 32 + row0;
+    const uint32_t at = to + (i >> 1) * step + row * 128;
+    const uint32_t words[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const uint2 a = half_of_codes(words[2 * h]), b = half_of_codes(words[2 * h + 1]);
@@ -340,17 +389,17 @@ __device__ __forceinline__ void widen_items(const HeadsAttendParams& p, const It
     for (int i = threadIdx.x & 127; i < D; i += 128) nan_first[i] = INT_MAX;
     if ((threadIdx.x & 127) == 0) *flag = 0;
     asm volatile("bar.sync 1, 128;" ::: "memory");
+    const bool has[2] = {it->end[0] > it->k0, it->end[1] > it->k0};
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      if (it->end[t] <= it->k0) continue;
+      if (!has[t]) continue;
       if (queries[t] > 0) await(w, bars + 8 * (kQEmpty + t), (queries[t] - 1) & 1);
       ++queries[t];
-      bring_queries<D>(p, it, t, smem, smem + L::kMisc + (k & 1) * kBlock * 4, sign);
-      arrive(kQFull + t);
+      copy_queries<D>(p, it, t, smem);
     }
-    const int all_see = item_sees(p, *it, it->col0), k1 = it->k1;
+    const int all_see = item_sees(p, *it, it->col0), k0 = it->k0, k1 = it->k1;
 #pragma unroll 1
-    for (int j = it->k0; j < k1; ++j, ++tile) {
+    for (int j = k0; j < k1; ++j, ++tile) {
       const uint32_t buf = tile & 1, scales = smem + L::kPage + tile % kScales * 32;
       const bool clean = (j + 1) * kKeys > all_see;
 #pragma unroll 1
@@ -369,6 +418,15 @@ __device__ __forceinline__ void widen_items(const HeadsAttendParams& p, const It
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bars + 8 * (kStEmpty + slot));
         if (page == 1) arrive((values ? kVFull : kKFull) + buf);
+        if (i == 1 && j == k0) {  // (the first keys were widened while the queries were on their way)
+          asm volatile("cp.async.wait_group 0;\n\tbar.sync 1, 128;" ::: "memory");
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (!has[t]) continue;
+            convert_queries<D>(p.a.dtype == HS_FP16, t, smem, smem + L::kMisc + (k & 1) * kBlock, sign);
+            arrive(kQFull + t);
+          }
+        }
       }
     }
     done_with_item(k, bars);
@@ -475,7 +533,6 @@ __device__ __forceinline__ void softmax_items(const HeadsAttendParams& p, const 
   float4* parts = reinterpret_cast<float4*>(reinterpret_cast<uint8_t*>(p.workspace) + ws_parts_offset(gridDim.x)) +
                   (int64_t)blockIdx.x * 2 * kBlock * (D / 4);
   uint32_t phase = 0, before = 0;  // key tiles of this query tile; of the CTA, in the items before
-  int64_t place = run * blockIdx.x;
   RunRecord* record = reinterpret_cast<RunRecord*>(reinterpret_cast<uint8_t*>(p.workspace) + sizeof(RunHeader)) + blockIdx.x;
   if (threadIdx.x == 0) *record = RunRecord{0, 0, 0, 0, 0, 0};
 #pragma unroll 1
@@ -492,7 +549,7 @@ __device__ __forceinline__ void softmax_items(const HeadsAttendParams& p, const 
       w.wait(bars + 8 * (kSFull + t), phase & 1);
       __syncwarp();
       tc::fence_after();
-      if (j == k0) qs = scale * lds_f(smem + L::kMisc + ((k & 1) * kBlock + row) * 4);
+      if (j == k0) qs = scale * power_of_field(raw[L::kMisc + (k & 1) * kBlock + row]);
       const uint32_t scales = smem + L::kPage + (before + j - k0) % kScales * 32;
       float s[128];
       tc::tmem_ld<128>(ts, s);
@@ -587,53 +644,92 @@ __device__ __forceinline__ void softmax_items(const HeadsAttendParams& p, const 
     }
     const int* nan_first = reinterpret_cast<const int*>(raw + L::kNan) + (k & 1) * D;
     const bool nans = work && *(reinterpret_cast<const volatile int*>(raw + L::kFlag) + (k & 1)) != 0;
-    const int64_t begins = place - k0;
-    const int part = begins > run * blockIdx.x ? 1 : 0;
+    const int part = it->begin > run * blockIdx.x ? 1 : 0;
     const float up = l == 0.f ? 0.f : exp2f(0.5f * (ref - m)), inv = l == 0.f ? 0.f : up / l;
-    const int in_token = col / p.group;
-    const int64_t token = it->t0 + (there ? in_token : 0);
-    const int head = it->head * p.group + (there ? col - in_token * p.group : 0);
-    const bool writes = there && HS_CHECK(token >= 0 && token < p.a.n && head < p.a.q_heads, kChkOutPos);
-    uint16_t* out = static_cast<uint16_t*>(p.a.out) + token * p.a.out_token_stride + head * p.a.out_head_stride;
     const bool f16 = p.a.dtype == HS_FP16;
-    if (whole || work) {
+    if (!whole) {
+      if (work) {
 #pragma unroll 1
-      for (int x = 0; x < D; x += 32) {
-        float o[32];
-        if (work) {
-          tc::tmem_ld<32>(to + x, o);
+        for (int x = 0; x < D; x += 16) {
+          float o[16];
+          tc::tmem_ld16(to + x, o);
           tc::tmem_wait_ld();
-          tc::touch<32>(o);
-        }
+          tc::touch<16>(o);
 #pragma unroll
-        for (int y = 0; y < 32; ++y) {
-          if (!work) o[y] = 0.f;
-          if (nans && sees > nan_first[x + y]) o[y] = __uint_as_float(0x7FC00000u);
-        }
-        if (whole) {
+          for (int y = 0; y < 16; y += 4) {
+            if (nans) {
 #pragma unroll
-          for (int y = 0; y < 32; ++y) o[y] = l == 0.f ? 0.f : o[y] * up * inv;
-          if (writes) {
-#pragma unroll
-            for (int y = 0; y < 32; y += 8)
-              *reinterpret_cast<uint4*>(out + x + y) = make_uint4(pack(f16, o[y], o[y + 1]), pack(f16, o[y + 2], o[y + 3]),
-                                                                  pack(f16, o[y + 4], o[y + 5]), pack(f16, o[y + 6], o[y + 7]));
+              for (int z = 0; z < 4; ++z)
+                if (sees > nan_first[x + y + z]) o[y + z] = __uint_as_float(0x7FC00000u);
+            }
+            if (there) parts[(part * (D / 4) + (x + y) / 4) * kBlock + row] = make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
           }
-        } else if (there) {
-#pragma unroll
-          for (int y = 0; y < 32; y += 4)
-            parts[(part * (D / 4) + (x + y) / 4) * kBlock + row] = make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
         }
       }
-    }
-    if (whole) {
-      if (writes && p.a.lse) p.a.lse[token * p.a.q_heads + head] = l == 0.f ? -INFINITY : (anchor + (m + log2f(l))) * kLn2;
-    } else {
       if (there) stats[part * kBlock + row] = make_float4(ref, m, l, anchor);
       if (threadIdx.x == 0 && k0 == 0)
-        *record = RunRecord{begins, begins + it->tiles, it->request, it->head, it->col0 / kBlock, it->rows};
+        *record = RunRecord{it->begin, it->begin + it->tiles, it->request, it->head, it->col0 / kBlock, it->rows};
+    } else {
+      // Rows are stored by four lanes each, 64 bytes at a time: of each 8 dimensions a lane is given two of four rows, and the four
+      // lanes of a row change places so that each has 8 dimensions of its own.
+      const int warp_row = row & ~31, g = lane >> 2, t4 = lane & 3;
+      uint16_t* out[4];
+      float f0[4], f1[4];
+      int seen[4];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const int r = warp_row + 8 * y + g, c = it->col0 + r, token = c / p.group, head = it->head * p.group + c - token * p.group;
+        const bool writes = r < it->rows && HS_CHECK(it->t0 + token < p.a.n && head < p.a.q_heads, kChkOutPos);
+        out[y] = writes ? static_cast<uint16_t*>(p.a.out) + (it->t0 + token) * p.a.out_token_stride + head * p.a.out_head_stride + 8 * t4
+                        : nullptr;
+        f0[y] = __shfl_sync(0xFFFFFFFFu, up, 8 * y + g), f1[y] = __shfl_sync(0xFFFFFFFFu, inv, 8 * y + g);
+        seen[y] = __shfl_sync(0xFFFFFFFFu, sees, 8 * y + g);
+      }
+#pragma unroll 1
+      for (int x = 0; x < D; x += 32) {
+        float o[2][16];
+        if (work) {
+          tc::tmem_ld_rows16<4>(to + x, o[0]);
+          tc::tmem_ld_rows16<4>(to + (16u << 16) + x, o[1]);
+          tc::tmem_wait_ld();
+          tc::touch<16>(o[0]);
+          tc::touch<16>(o[1]);
+        }
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          uint32_t v[4];
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            float a = o[y >> 1][4 * n + 2 * (y & 1)], b = o[y >> 1][4 * n + 2 * (y & 1) + 1];
+            if (nans) {
+              if (seen[y] > nan_first[x + 8 * n + 2 * t4]) a = __uint_as_float(0x7FC00000u);
+              if (seen[y] > nan_first[x + 8 * n + 2 * t4 + 1]) b = __uint_as_float(0x7FC00000u);
+            }
+            a = work && f0[y] != 0.f ? a * f0[y] * f1[y] : 0.f, b = work && f0[y] != 0.f ? b * f0[y] * f1[y] : 0.f;
+            v[n] = pack(f16, a, b);
+          }
+#pragma unroll
+          for (int d = 1; d <= 2; d *= 2) {
+            const bool odd = t4 & d;
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              const int lo = d == 1 ? 2 * n : n, hi = lo + d;
+              const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[lo] : v[hi], d);
+              if (odd)
+                v[lo] = got;
+              else
+                v[hi] = got;
+            }
+          }
+          if (out[y]) *reinterpret_cast<uint4*>(out[y] + x) = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+      }
+      if (there && p.a.lse) {
+        const int token = col / p.group;
+        p.a.lse[(it->t0 + token) * p.a.q_heads + it->head * p.group + col - token * p.group] =
+            l == 0.f ? -INFINITY : (anchor + (m + log2f(l))) * kLn2;
+      }
     }
-    place += it->k1 - k0;
     before += it->k1 - k0;
     tc::fence_before();
     done_with_item(k, bars);
@@ -644,13 +740,12 @@ __device__ __forceinline__ void softmax_items(const HeadsAttendParams& p, const 
 // Where this CTA's run begins; by all threads, before the roles part.  Scratch: shared memory that nothing else uses yet.
 struct Scratch {
   int64_t sums[kThreads / 32];
-  int64_t offset;
   Start start;
 };
 __device__ __forceinline__ int64_t find_start(const HeadsAttendParams& p, int limit, Scratch* s, int64_t* run_length) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // key tiles of the request of each thread
-  auto tiles_of = [&](int r) {
+  // units of the request of each thread
+  auto units_of = [&](int r) {
     Request q{};
     if (r < p.a.R) q.load(p, r, limit);
     int64_t mine = 0;
@@ -660,34 +755,21 @@ __device__ __forceinline__ int64_t find_start(const HeadsAttendParams& p, int li
       x.t0 = 0;
       x.n = __shfl_sync(0xFFFFFFFFu, q.n, who), x.ctx = __shfl_sync(0xFFFFFFFFu, q.ctx, who);
       x.keys = __shfl_sync(0xFFFFFFFFu, q.keys, who), x.blocks = __shfl_sync(0xFFFFFFFFu, q.blocks, who);
-      const int64_t n = request_tiles(p, x) * p.pages.kv_heads;
+      const int64_t n = request_units(p, x) * p.pages.kv_heads;
       if (lane == who) mine = n;
     }
     return mine;
   };
+  // all units, and (in the last round) those of the requests before this thread's, in its chunk of kThreads requests
   bool bad = false;
-  int64_t sum = 0, kept = 0;
+  int64_t total = 0, mine = 0, first = 0;
   for (int r0 = 0; r0 < p.a.R; r0 += kThreads) {
     const int r = r0 + threadIdx.x;
     int64_t t0;
     int n;
-    if (r < p.a.R) bad |= !p.ragged.tokens(r, &t0, &n);
-    kept = tiles_of(r);
-    sum += kept;
-  }
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-  if (lane == 0) s->sums[warp] = sum;
-  bad = __syncthreads_or(bad);
-  int64_t total = 0;
-  for (int i = 0; i < kThreads / 32; ++i) total += s->sums[i];
-  if (bad) total = 0;
-  const int64_t run = max((int64_t)kMinRun, (total + gridDim.x - 1) / gridDim.x), begin = run * blockIdx.x;
-  __syncthreads();
-  int64_t before = 0;
-  for (int r0 = 0; r0 < p.a.R && begin < total; r0 += kThreads) {
-    const int r = r0 + threadIdx.x;
-    const int64_t mine = p.a.R > kThreads ? tiles_of(r) : kept;
+    bool wrong = false;
+    if (r < p.a.R) wrong = !p.ragged.tokens(r, &t0, &n);
+    mine = units_of(r);
     int64_t upto = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -695,24 +777,34 @@ __device__ __forceinline__ int64_t find_start(const HeadsAttendParams& p, int li
       if (lane >= d) upto += x;
     }
     if (lane == 31) s->sums[warp] = upto;
-    __syncthreads();
-    int64_t first = before + upto - mine;
+    bad |= __syncthreads_or(wrong);
+    first = total + upto - mine;
+#pragma unroll
     for (int i = 0; i < kThreads / 32; ++i) {
       if (i < warp) first += s->sums[i];
-      before += s->sums[i];
+      total += s->sums[i];
     }
-    if (begin >= first && begin < first + mine) s->start.r = r, s->offset = begin - first;
-    __syncthreads();
+    if (r0 + kThreads < p.a.R) __syncthreads();
   }
-  if (begin < total && warp == 0) {
+  if (bad) total = 0;
+  const int64_t run = max((int64_t)kMinRun, (total + gridDim.x - 1) / gridDim.x), begin = run * blockIdx.x;
+  if (threadIdx.x == 0) {
+    s->start.at = begin;
+    s->start.left = begin < total ? min(run, total - begin) : 0;
+    if (blockIdx.x == 0) *reinterpret_cast<RunHeader*>(p.workspace) = RunHeader{run, total};
+  }
+  // the warp whose requests the run begins in looks for the block
+  auto look = [&](int r0) {
+    const unsigned owner = __ballot_sync(0xFFFFFFFFu, begin >= first && begin < first + mine);
+    if (!owner) return;
+    const int who = __ffs(owner) - 1, r = r0 + warp * 32 + who;
     Request q;
-    const int r = s->start.r;
     q.load(p, r, limit);
-    const int64_t a_head = request_tiles(p, q);
-    int64_t left = s->offset % a_head;
-    int block = -1, tile = 0;
+    const int64_t a_head = __shfl_sync(0xFFFFFFFFu, mine, who) / p.pages.kv_heads, offset = begin - __shfl_sync(0xFFFFFFFFu, first, who);
+    const int head = (int)(offset / a_head);
+    int left = (int)(offset - head * a_head), block = -1, in = 0;
     for (int b0 = 0; block < 0; b0 += 32) {
-      const int n = b0 + lane < q.blocks ? q.tiles(p, b0 + lane) : 0;
+      const int n = b0 + lane < q.blocks ? kItemCost + q.tiles(p, b0 + lane) : 0;
       int upto = n;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -721,22 +813,41 @@ __device__ __forceinline__ int64_t find_start(const HeadsAttendParams& p, int li
       }
       const unsigned here = __ballot_sync(0xFFFFFFFFu, left < upto);
       if (here) {
-        const int who = __ffs(here) - 1;
-        block = b0 + who;
-        tile = (int)left - (__shfl_sync(0xFFFFFFFFu, upto, who) - __shfl_sync(0xFFFFFFFFu, n, who));
+        const int w = __ffs(here) - 1;
+        block = b0 + w;
+        in = left - (__shfl_sync(0xFFFFFFFFu, upto, w) - __shfl_sync(0xFFFFFFFFu, n, w));
       } else {
         left -= __shfl_sync(0xFFFFFFFFu, upto, 31);
-        if (b0 + 32 >= q.blocks) block = 0;  // (not reached: the offset lies within the head's tiles)
+        if (b0 + 32 >= q.blocks) block = 0;  // (not reached: the offset lies within the head's units)
       }
     }
-    if (lane == 0) {
-      s->start.head = (int)(s->offset / a_head);
-      s->start.block = block, s->start.tile = tile;
+    if (lane == 0) s->start.r = r, s->start.head = head, s->start.block = block, s->start.in = in;
+  };
+  if (begin < total) {
+    if (p.a.R <= kThreads) {
+      look(0);
+    } else {  // the chunks once more
+      int64_t before = 0;
+      for (int r0 = 0; r0 < p.a.R; r0 += kThreads) {
+        mine = units_of(r0 + threadIdx.x);
+        int64_t upto = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int64_t x = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+          if (lane >= d) upto += x;
+        }
+        __syncthreads();
+        if (lane == 31) s->sums[warp] = upto;
+        __syncthreads();
+        first = before + upto - mine;
+#pragma unroll
+        for (int i = 0; i < kThreads / 32; ++i) {
+          if (i < warp) first += s->sums[i];
+          before += s->sums[i];
+        }
+        look(r0);
+      }
     }
-  }
-  if (threadIdx.x == 0) {
-    s->start.left = begin < total ? min(run, total - begin) : 0;
-    if (blockIdx.x == 0) *reinterpret_cast<RunHeader*>(p.workspace) = RunHeader{run, total};
   }
   __syncthreads();
   *run_length = run;
@@ -746,13 +857,13 @@ __device__ __forceinline__ int64_t find_start(const HeadsAttendParams& p, int li
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const HeadsAttendParams p, int limit) {
   using L = Smem<D>;
-  extern __shared__ uint8_t smem_raw[];
+  extern __shared__ __align__(1024) uint8_t raw[];  // (all of the block's shared memory: the operands' swizzle wants this alignment)
   asm volatile("griddepcontrol.launch_dependents;");  // prompt_join_kernel waits for this kernel's results by itself
-  const uint32_t smem = (tc::smem_u32(smem_raw) + 1023) & ~1023u;
-  uint8_t* raw = smem_raw + (smem - tc::smem_u32(smem_raw));
+  const uint32_t smem = tc::smem_u32(raw);
   const uint32_t bars = smem + L::kBar;
   const int warp = threadIdx.x >> 5;
   Scratch* scratch = reinterpret_cast<Scratch*>(raw + L::kMisc);
+  static_assert(sizeof(Scratch) <= 2 * kBlock, "scratch");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(raw + L::kFlag) + 2;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStaged; ++i) tc::mbar_init(bars + 8 * (kStFull + i), 1), tc::mbar_init(bars + 8 * (kStEmpty + i), 4);
@@ -804,11 +915,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const HeadsAttendPa
   }
 }
 
-// Joins the parts of items that several runs share: a block takes 8 rows of a cut item, a thread D / 16 dimensions of one.
-constexpr int kJoinThreads = 128, kJoinRows = 8, kMaxCtas = 512;
+// Joins the parts of items that several runs share: a block takes 32 rows of a cut item, a thread D / 8 dimensions of one, and
+// four parts at a time, so that their loads are on their way together.
+constexpr int kJoinThreads = 256, kJoinRows = 32, kJoinParts = 4, kMaxCtas = 512;
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const HeadsAttendParams p, int ctas) {
-  constexpr int kVecs = D / 64;  // float4 a thread
+  constexpr int kVecs = D / 32;  // float4 a thread
   __shared__ uint16_t cuts[kMaxCtas];
   __shared__ int counts[kJoinThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -835,54 +947,55 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const HeadsAt
     __syncthreads();
   }
   constexpr int kGroups = kBlock / kJoinRows;
-  const int in_group = threadIdx.x % kJoinRows, piece = threadIdx.x / kJoinRows;  // 16 pieces of D / 16 dimensions
+  const int piece = warp;  // of 8
   for (int item = blockIdx.x; item < n * kGroups; item += gridDim.x) {
-    const int i = cuts[item / kGroups], row = item % kGroups * kJoinRows + in_group;
+    const int i = cuts[item / kGroups], row = item % kGroups * kJoinRows + lane;
     const RunRecord rec = records[i];
     if (row >= rec.cols) continue;
+    Request q;
+    q.load(p, rec.request, 0);
     const int last = (int)((rec.end - 1) / header.run);
     const int slot0 = rec.begin > i * header.run ? 1 : 0;
-    auto slot = [&](int x) { return (int64_t)x * 2 + (x == i ? slot0 : 0); };
-    float anchor = -INFINITY, ref = -INFINITY, m = -INFINITY;
-    for (int x = i; x <= last; ++x) {
-      const float4 st = stats[slot(x) * kBlock + row];
-      if (st.y != -INFINITY) anchor = fmaxf(anchor, st.w);
-    }
-    for (int x = i; x <= last; ++x) {
-      const float4 st = stats[slot(x) * kBlock + row];
-      if (st.y == -INFINITY) continue;
-      ref = fmaxf(ref, st.x + (st.w - anchor)), m = fmaxf(m, st.y + (st.w - anchor));
-    }
-    float l = 0.f;
+    Joined res;
     float4 acc[kVecs];
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-    for (int x = i; x <= last; ++x) {
-      const float4 st = stats[slot(x) * kBlock + row];
-      if (st.y == -INFINITY) continue;
-      const float a = exp2f(st.x + (st.w - anchor) - ref);
-      l += st.z * exp2f(st.y + (st.w - anchor) - m);
+    for (int x0 = i; x0 <= last; x0 += kJoinParts) {
+      float4 st[kJoinParts], y[kJoinParts][kVecs];
 #pragma unroll
-      for (int v = 0; v < kVecs; ++v) {
-        const float4 y = parts[(slot(x) * (D / 4) + piece * kVecs + v) * kBlock + row];
-        acc[v].x += a * y.x, acc[v].y += a * y.y, acc[v].z += a * y.z, acc[v].w += a * y.w;
+      for (int x = 0; x < kJoinParts; ++x) {
+        if (x0 + x > last) continue;
+        const int64_t slot = (int64_t)(x0 + x) * 2 + (x0 + x == i ? slot0 : 0);
+        st[x] = stats[slot * kBlock + row];
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v) y[x][v] = parts[(slot * (D / 4) + piece * kVecs + v) * kBlock + row];
+      }
+#pragma unroll
+      for (int x = 0; x < kJoinParts; ++x) {
+        if (x0 + x > last || st[x].y == -INFINITY) continue;  // (a part of which the row sees nothing)
+        const float2 f = res.join(st[x]);
+        const float a = f.x, b = f.y;
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v) {
+          acc[v].x = acc[v].x * a + b * y[x][v].x, acc[v].y = acc[v].y * a + b * y[x][v].y;
+          acc[v].z = acc[v].z * a + b * y[x][v].z, acc[v].w = acc[v].w * a + b * y[x][v].w;
+        }
       }
     }
-    const float up = l == 0.f ? 0.f : exp2f(0.5f * (ref - m)), inv = l == 0.f ? 0.f : up / l;
-    Request q;
-    q.load(p, rec.request, 0);
+    const float up = res.l == 0.f ? 0.f : exp2f(0.5f * (res.ref - res.m)), inv = res.l == 0.f ? 0.f : up / res.l;
     const int col = rec.group * kBlock + row, in_token = col / p.group;
     const int64_t token = q.t0 + in_token;
     const int head = rec.head * p.group + col - in_token * p.group;
     if (!HS_CHECK(token < p.a.n && head < p.a.q_heads, kChkOutPos)) continue;
     const bool f16 = p.a.dtype == HS_FP16;
-    uint16_t* out = static_cast<uint16_t*>(p.a.out) + token * p.a.out_token_stride + head * p.a.out_head_stride + piece * (D / 16);
+    uint16_t* out = static_cast<uint16_t*>(p.a.out) + token * p.a.out_token_stride + head * p.a.out_head_stride + piece * (D / 8);
 #pragma unroll
-    for (int v = 0; v < kVecs; ++v)
-      *reinterpret_cast<uint2*>(out + 4 * v) =
-          make_uint2(pack(f16, acc[v].x * up * inv, acc[v].y * up * inv), pack(f16, acc[v].z * up * inv, acc[v].w * up * inv));
-    if (piece == 0 && p.a.lse) p.a.lse[token * p.a.q_heads + head] = l == 0.f ? -INFINITY : (anchor + (m + log2f(l))) * kLn2;
+    for (int v = 0; v < kVecs; v += 2)
+      *reinterpret_cast<uint4*>(out + 4 * v) = make_uint4(
+          pack(f16, acc[v].x * up * inv, acc[v].y * up * inv), pack(f16, acc[v].z * up * inv, acc[v].w * up * inv),
+          pack(f16, acc[v + 1].x * up * inv, acc[v + 1].y * up * inv), pack(f16, acc[v + 1].z * up * inv, acc[v + 1].w * up * inv));
+    if (piece == 0 && p.a.lse)
+      p.a.lse[token * p.a.q_heads + head] = res.l == 0.f ? -INFINITY : (res.anchor + (res.m + log2f(res.l))) * kLn2;
   }
 }
 
