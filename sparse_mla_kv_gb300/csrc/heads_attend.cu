@@ -82,7 +82,7 @@ struct Cursor {
 };
 
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1) steps_kernel(const HeadsAttendPar
     do {
       const int key0 = cur.tile * kHeadsPage;
       // scores
-      uint32_t slot = ring + taken % L::kSlots * L::kSlot;
+      uint32_t slot = ring + taken % L::kSlots * L::kSlot, at = slot - smem;  // (also as an offset)
       await(w, full + 8 * (taken % L::kSlots), taken / L::kSlots & 1);
       const bool valid = lds_u(slot + L::kUnit + 16) != 0;
       const float sk = lds_f(slot + L::kUnit + 4 * (head & 3));
@@ -354,13 +354,16 @@ __global__ void __launch_bounds__(kThreads, 1) steps_kernel(const HeadsAttendPar
       for (int j = 0; j < 8; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b) {
+// (loads first, and products of eight sums in turn: each waits for its own sum's last)
+        uint4 k[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint4 k = lds16(slot + b * 4096 + (16 * (g >> 1) + 2 * j + (g & 1)) * 64 + 16 * t);
-          const uint32_t words[4] = {k.x, k.y, k.z, k.w};
+        for (int j = 0; j < 8; ++j)
+          k[j] = *reinterpret_cast<const uint4*>(smem_raw + at + b * 4096 + (16 * (g >> 1) + 2 * j + (g & 1)) * 64 + 16 * t);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint2 x = half_of_codes(words[i]);
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint2 x = half_of_codes(i == 0 ? k[j].x : i == 1 ? k[j].y : i == 2 ? k[j].z : k[j].w);
             if constexpr (kHalves == 2)
               mma(s[j], q[b][i][0][0], q[b][i][1][0], q[b][i][0][1], q[b][i][1][1], x.x, x.y);
             else
@@ -374,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1) steps_kernel(const HeadsAttendPar
       if (sub == 0) producer.issue(p, ring, full, empty, limit, w);
 
       // weights
-      slot = ring + taken % L::kSlots * L::kSlot;
+      slot = ring + taken % L::kSlots * L::kSlot, at = slot - smem;
       await(w, full + 8 * (taken % L::kSlots), taken / L::kSlots & 1);
       const float sv = lds_f(slot + L::kUnit + 4 * ((p.pages.kv_heads + head) & 3));
       const float size = valid ? log2f(sv) : 0.f;
@@ -440,28 +443,40 @@ __global__ void __launch_bounds__(kThreads, 1) steps_kernel(const HeadsAttendPar
 
       // results
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        const uint32_t from = slot + (i >> 2) * 4096 + (16 * (i & 3) + g) * 64 + 16 * t;
-        uint4 v0 = lds16(from), v1 = lds16(from + 512);
-        uint32_t words[2][4] = {{v0.x, v0.y, v0.z, v0.w}, {v1.x, v1.y, v1.z, v1.w}};
-        if (mixed) {  // a weight of zero does not cancel a NaN: who sees it is settled at the unit's end
+      for (int b = 0; b < kBlocks; ++b) {
+        uint4 v[4][2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int y = 0; y < 2; ++y)
+            v[i][y] = *reinterpret_cast<const uint4*>(smem_raw + at + b * 4096 + (16 * i + 8 * y + g) * 64 + 16 * t);
+        if (mixed) {  // a weight of zero does not cancel a NaN: who sees it is settled at the unit's end
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const uint32_t is = nan_codes(words[y][x]);
-              if (is) {
-                words[y][x] &= ~((is >> 7) * 0xFFu);
-                if (valid) atomicMin(nan_first + 16 * i + 8 * y + g, key0 + 16 * t + 4 * x + ((__ffs(is) - 1) >> 3));
-                any_nan = true;
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              uint32_t words[4] = {v[i][y].x, v[i][y].y, v[i][y].z, v[i][y].w};
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const uint32_t is = nan_codes(words[x]);
+                if (is) {
+                  words[x] &= ~((is >> 7) * 0xFFu);
+                  if (valid) atomicMin(nan_first + 64 * b + 16 * i + 8 * y + g, key0 + 16 * t + 4 * x + ((__ffs(is) - 1) >> 3));
+                  any_nan = true;
+                }
               }
+              v[i][y] = make_uint4(words[0], words[1], words[2], words[3]);
             }
         }
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          const uint2 a = half_of_codes(words[0][x]), b = half_of_codes(words[1][x]);
 #pragma unroll
-          for (int h = 0; h < kHalves; ++h) mma(o[h][i], a.x, b.x, a.y, b.y, pf[h][x][0], pf[h][x][1]);
+          for (int i = 0; i < 4; ++i) {
+            const uint2 c = half_of_codes(x == 0 ? v[i][0].x : x == 1 ? v[i][0].y : x == 2 ? v[i][0].z : v[i][0].w);
+            const uint2 d = half_of_codes(x == 0 ? v[i][1].x : x == 1 ? v[i][1].y : x == 2 ? v[i][1].z : v[i][1].w);
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h) mma(o[h][4 * b + i], c.x, d.x, c.y, d.y, pf[h][x][0], pf[h][x][1]);
+          }
         }
       }
       __syncwarp();

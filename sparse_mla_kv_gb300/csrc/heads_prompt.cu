@@ -34,12 +34,12 @@ constexpr int kThreads = 16 * 32, kMmaWarp = 8, kLoadWarp = 10, kWalkWarp = 11, 
 constexpr int kTakers = 15;  // warps that the items are handed to
 constexpr int kRegsLaunch = 128, kRegsSoftmax = 200, kRegsOther = 56;
 static_assert(2 * kRegsSoftmax + 2 * kRegsOther <= 4 * kRegsLaunch, "more registers than the launch has");
-constexpr int kStaged = 4, kScales = 4;  // staged pages (keys or values); key tiles whose scales are kept
+constexpr int kStaged = 4, kScales = 8;  // staged pages (keys or values); key tiles whose scales are kept
 constexpr int kMinRun = 6;               // of a run, in key tiles: fewer would be mostly set-up and joining
 constexpr int kItemCost = 3;             // what an item costs beside its key tiles, in these
 enum Bar { kStFull = 0, kStEmpty = kStFull + kStaged, kKFull = kStEmpty + kStaged, kKEmpty = kKFull + 2, kVFull = kKEmpty + 2,
            kVEmpty = kVFull + 2, kQFull = kVEmpty + 2, kQEmpty = kQFull + 2, kSFull = kQEmpty + 2, kPReady = kSFull + 2,
-           kODone = kPReady + 2, kItem = kODone + 2, kItemDone = kItem + 2, kDrain = kItemDone + 2, kBars = kDrain + 2 };
+           kODone = kPReady + 2, kSFree = kODone + 2, kItem = kSFree + 2, kItemDone = kItem + 2, kDrain = kItemDone + 2, kBars = kDrain + 2 };
 
 // Workspace: header, a record a CTA, statistics [CTA][2][256][4], results [CTA][2][D / 4][256][4].
 __host__ __device__ constexpr size_t ws_stats_offset(int ctas) { return sizeof(RunHeader) + (size_t)ctas * sizeof(RunRecord); }
@@ -97,6 +97,10 @@ static_assert(sizeof(Item) % 8 == 0, "alignment of what follows");
 template <int D>
 struct Smem {
   static constexpr int kUnits = D / 64, kUnit = 128 * 128;  // a unit: 128 rows of 64 fp16
+  // Tensor memory, for each query tile: 128 columns of S, D of O, and P: where there is room, in 64 of its own, so that the next
+  // scores are made while the weights are; else in S's place.
+  static constexpr bool kApart = D == 64;
+  static constexpr uint32_t kTo = kApart ? 384 : 256, kTp = kApart ? 256 : 0, kToStep = D, kTpStep = kApart ? 64 : 128;
   static constexpr int kStage = D * kHeadsPage;
   static constexpr int kQ = 0, kK = kQ + 2 * kUnits * kUnit, kV = kK + 2 * kUnits * kUnit, kVPage = D * 128;
   static constexpr int kStages = kV + 4 * kVPage, kMisc = kStages + kStaged * kStage;
@@ -288,18 +292,25 @@ __device__ __forceinline__ uint32_t max_magnitudes(bool f16, uint32_t a, uint32_
     asm("max.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
   return a;
 }
+// A thread's row.  The largest magnitude is found on the way; only where it wants the row divided (rare) is it read again.
 template <int D>
-__device__ __forceinline__ void convert_queries(bool f16, int t, uint32_t smem, uint32_t qs, float sign) {
+__device__ __forceinline__ void convert_queries(const HeadsAttendParams& p, const Item* it, int t, uint32_t smem, uint32_t qs, float sign) {
   using L = Smem<D>;
   const int row = threadIdx.x & 127;
-  const uint32_t at = smem + L::kQ + t * L::kUnits * L::kUnit + row * 128;
+  const bool f16 = p.a.dtype == HS_FP16;
+  const uint32_t at = smem + L::kQ + t * L::kUnits * L::kUnit + row * 128, flip = sign < 0.f ? 0x80008000u : 0u;
   auto place = [&](int piece) { return at + (piece >> 3) * L::kUnit + (((piece & 7) ^ (row & 7)) << 4); };
   uint32_t most[4] = {0, 0, 0, 0};
 #pragma unroll 4
   for (int i = 0; i < D / 8; ++i) {
     const uint4 v = lds16(place(i));
-    most[0] = max_magnitudes(f16, most[0], v.x), most[1] = max_magnitudes(f16, most[1], v.y);
-    most[2] = max_magnitudes(f16, most[2], v.z), most[3] = max_magnitudes(f16, most[3], v.w);
+    uint32_t w[4] = {v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip};
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      most[x] = max_magnitudes(f16, most[x], w[x]);
+      if (!f16) w[x] = pack_half(__uint_as_float(w[x] << 16), __uint_as_float(w[x] & 0xFFFF0000u));
+    }
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(place(i)), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
   }
   most[0] = max_magnitudes(f16, max_magnitudes(f16, most[0], most[1]), max_magnitudes(f16, most[2], most[3]));
   float2 two;
@@ -308,16 +319,20 @@ __device__ __forceinline__ void convert_queries(bool f16, int t, uint32_t smem, 
   else
     two = make_float2(__uint_as_float(most[0] << 16), __uint_as_float(most[0] & 0xFFFF0000u));
   const int e = query_field(fmaxf(two.x, two.y));
-  const float f = sign * power_of_field(254 - e);
   asm volatile("st.shared.u8 [%0], %1;" ::"r"(qs + t * kQRows + row), "r"(e) : "memory");
-  if (f16 && f == 1.f) return;
-#pragma unroll 2
+  if (e == 127 || t * kQRows + row >= it->rows) return;
+  const float f = sign * power_of_field(254 - e);
+  const int c = it->col0 + t * kQRows + row, token = c / p.group;
+  const uint16_t* from = static_cast<const uint16_t*>(p.a.q) + (it->t0 + token) * p.a.q_token_stride +
+                         (it->head * p.group + c - token * p.group) * p.a.q_head_stride;
+#pragma unroll 1
   for (int i = 0; i < D / 8; ++i) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(from) + i);
     float x[8];
     if (f16)
-      Vec8<__half>{lds16(place(i))}.values(x);
+      Vec8<__half>{v}.values(x);
     else
-      Vec8<__nv_bfloat16>{lds16(place(i))}.values(x);
+      Vec8<__nv_bfloat16>{v}.values(x);
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(place(i)), "r"(pack_half(x[0] * f, x[1] * f)),
                  "r"(pack_half(x[2] * f, x[3] * f)), "r"(pack_half(x[4] * f, x[5] * f)), "r"(pack_half(x[6] * f, x[7] * f))
                  : "memory");
@@ -423,7 +438,7 @@ __device__ __forceinline__ void widen_items(const HeadsAttendParams& p, const It
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             if (!has[t]) continue;
-            convert_queries<D>(p.a.dtype == HS_FP16, t, smem, smem + L::kMisc + (k & 1) * kBlock, sign);
+            convert_queries<D>(p, it, t, smem, smem + L::kMisc + (k & 1) * kBlock, sign);
             arrive(kQFull + t);
           }
         }
@@ -474,12 +489,16 @@ __device__ __forceinline__ void issue_items(const HeadsAttendParams& p, const It
     if (end > k0) {
       wait(kQFull + t, items & 1);
       ++items;
-      if (phase > 0) wait(kODone + t, (phase - 1) & 1);  // the item before: its last P has been read
+      if (phase > 0) wait((L::kApart ? kSFree : kODone) + t, (phase - 1) & 1);  // the item before: S's place is free
       scores(k0);
     }
 #pragma unroll 1
     for (int j = k0; j < end; ++j, ++phase) {
       const uint32_t n = base + j - k0, buf = n & 1;
+      if (L::kApart && j + 1 < end) {
+        wait(kSFree + t, phase & 1);
+        scores(j + 1);
+      }
       wait(kPReady + t, phase & 1);
       wait(kVFull + buf, n / 2 & 1);
 #pragma unroll
@@ -488,12 +507,12 @@ __device__ __forceinline__ void issue_items(const HeadsAttendParams& p, const It
         // P: 16 tokens are 8 columns
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          tc::mma_ts(tmem + 256 + t * 128, tmem + t * 128 + (page * 4 + k) * 8, db + (k * 32 >> 4), kIdO,
+          tc::mma_ts(tmem + L::kTo + t * L::kToStep, tmem + L::kTp + t * L::kTpStep + (page * 4 + k) * 8, db + (k * 32 >> 4), kIdO,
                      j > k0 || page > 0 || k > 0, leader);
       }
       tc::commit(bars + 8 * (kODone + t), leader);
       tc::commit(bars + 8 * (kVEmpty + buf), leader);
-      if (j + 1 < end) {
+      if (!L::kApart && j + 1 < end) {
         wait(kODone + t, phase & 1);  // P, in S's place, has been read
         scores(j + 1);
       }
@@ -526,7 +545,7 @@ __device__ __forceinline__ void softmax_items(const HeadsAttendParams& p, const 
   const int t = threadIdx.x >> 7, lane = threadIdx.x & 31;
   const int row = threadIdx.x & 255;
   const uint32_t lanes = (uint32_t)(32 * ((threadIdx.x >> 5) & 3)) << 16;
-  const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * 128;
+  const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + L::kTo + t * L::kToStep, tp = tmem + lanes + L::kTp + t * L::kTpStep;
   const float scale = fabsf(p.scale_log2);
   float4* stats = reinterpret_cast<float4*>(reinterpret_cast<uint8_t*>(p.workspace) + ws_stats_offset(gridDim.x)) +
                   (int64_t)blockIdx.x * 2 * kBlock;
@@ -560,6 +579,11 @@ __device__ __forceinline__ void softmax_items(const HeadsAttendParams& p, const 
       const bool missing = (lds_u(scales + 16) & lds_u(scales + 20)) == 0;
       tc::tmem_wait_ld();
       tc::touch<128>(s);
+      if constexpr (L::kApart) {
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bars + 8 * (kSFree + t));
+      }
       if (missing || (j + 1) * kKeys > all_see) {
         const int left = sees - j * kKeys;
         const int left0 = lds_u(scales + 16) ? left : 0, left1 = lds_u(scales + 20) ? left : 0;
@@ -581,13 +605,18 @@ __device__ __forceinline__ void softmax_items(const HeadsAttendParams& p, const 
 #pragma unroll
         for (int i = 0; i < 2; ++i) top[i] -= anchor, c[i] = 1.f;
       }
+      if (L::kApart && phase > 0) {  // the products before have read P, and are in O
+        w.wait(bars + 8 * (kODone + t), (phase - 1) & 1);
+        __syncwarp();
+        tc::fence_after();
+      }
       const float most = fmaxf(top[0] + size[0], top[1] + size[1]);
       const bool over = most > ref + kLazy;
       if (__any_sync(0xFFFFFFFFu, over)) {
         const float now = over ? most - kTop : ref;
         const float alpha = over ? exp2f(ref - now) : 1.f;
         ref = now;
-        if (j > k0) {  // the products so far have finished: this tile's scores were issued after them
+        if (j > k0) {  // (the products so far have finished: without room for P, this tile's scores were issued after them)
 #pragma unroll 1
           for (int x = 0; x < D; x += 16) {
             float o[16];
@@ -626,7 +655,7 @@ __device__ __forceinline__ void softmax_items(const HeadsAttendParams& p, const 
               sum0 = tc::add2(sum0, e);
             pk[y] = pack_half(e.x, e.y);
           }
-          tc::tmem_st16(ts + (64 * i + x) / 2, reinterpret_cast<const float*>(pk));
+          tc::tmem_st16(tp + (64 * i + x) / 2, reinterpret_cast<const float*>(pk));
         }
         if (bias != -INFINITY) l += ((sum0.x + sum0.y) + (sum1.x + sum1.y)) * tc::exp2_fast(-bias - m);
       }
@@ -877,6 +906,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const HeadsAttendPa
       tc::mbar_init(bars + 8 * (kSFull + i), 1);
       tc::mbar_init(bars + 8 * (kPReady + i), 4);
       tc::mbar_init(bars + 8 * (kODone + i), 1);
+      tc::mbar_init(bars + 8 * (kSFree + i), 4);
       tc::mbar_init(bars + 8 * (kItem + i), 1);
       tc::mbar_init(bars + 8 * (kItemDone + i), kTakers);
       tc::mbar_init(bars + 8 * (kDrain + i), 1);
