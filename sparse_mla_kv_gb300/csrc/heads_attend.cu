@@ -19,6 +19,8 @@
 // A worker is W warps (16 columns each, or 8) and a ring of copies (cp.async.bulk, a page's keys or values of a head each);
 // every worker of the grid takes an equal run of pages, whatever the contexts' lengths; units that are cut leave partial
 // results in the workspace, which join_kernel joins in a fixed order.
+#include <algorithm>
+
 #include "heads_device.cuh"
 
 HS_CHECK_WORD
@@ -28,7 +30,6 @@ namespace {
 
 using namespace heads;
 
-constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int kRingBytes = 192 * 1024;
 constexpr int kStepCols = 64;  // requests of more columns are left to heads_prompt.cu
 
@@ -61,23 +62,24 @@ struct Request {
   }
 };
 
-// A place in the call's tiles: of request r, unit u (head x group), page `tile`.
+// A place in the call's tiles: of request r, a head and a group of columns, page `tile`.
 struct Cursor {
-  int r, u, tile;
+  int r, head, group, tile;
   Request q;
   int64_t left;
-  __device__ __forceinline__ int units(const HeadsAttendParams& p) const { return p.pages.kv_heads * q.groups; }
-  // to the next tile; 1 when it is in another unit, 2 when in another request (left == 0: there is none)
-  __device__ __forceinline__ int next(const HeadsAttendParams& p, int cols, int limit) {
+  // to the next tile; true when it is in another unit (left == 0: there is none)
+  __device__ __forceinline__ bool next(const HeadsAttendParams& p, int cols, int limit) {
     --left;
-    if (++tile < q.tiles) return 0;
+    if (++tile < q.tiles) return false;
     tile = 0;
-    if (++u < units(p)) return 1;
-    u = 0;
-    if (left <= 0) return 2;
+    if (++group < q.groups) return true;
+    group = 0;
+    if (++head < p.pages.kv_heads) return true;
+    head = 0;
+    if (left <= 0) return true;
     do q.load(p, ++r, cols, limit);
     while (q.tiles == 0 && r + 1 < p.a.R);
-    return 2;
+    return true;
   }
 };
 
@@ -101,6 +103,7 @@ __device__ __forceinline__ float quad_sum(float x) {
 }
 template <int D, int NC, int W>
 struct Shape {
+  static constexpr int kWarps = 8, kThreads = kWarps * 32;
   static constexpr int kCols = NC * W, kWorkers = kWarps / W;  // columns of a group, workers of a CTA
   static constexpr int kUnit = D * kHeadsPage;                 // bytes of a page's keys (or values) of a head
   // a slot: the codes, the 16 bytes that hold the scale, a word that says whether the page is there
@@ -145,7 +148,7 @@ struct Producer {
     }
     __syncwarp();
     if (lane == 0) {
-      const int head = at.u / at.q.groups, scale = values ? p.pages.kv_heads + head : head;
+      const int head = at.head, scale = values ? p.pages.kv_heads + head : head;
       const uint32_t to = ring + slot * L::kSlot, bar = full + 8 * slot;
       const uint8_t* codes = p.pages.codes(block, head, D) + (values ? L::kUnit : 0);
       sts_u(to + L::kUnit + 16, there);
@@ -156,11 +159,18 @@ struct Producer {
     ++count;
     if (values) at.next(p, L::kCols, limit);
   }
+  // After the worker is done with `taken` copies: the next one, and another while the ring is not full yet.
+  __device__ __forceinline__ void refill(const HeadsAttendParams& p, uint32_t ring, uint32_t full, uint32_t empty, int limit,
+                                         uint32_t taken, tc::Waiter& w) {
+    issue(p, ring, full, empty, limit, w);
+    if (L::kSlots > 4 && count < taken + L::kSlots) issue(p, ring, full, empty, limit, w);
+  }
 };
 
 template <int D, int NC, int W>
-__global__ void __launch_bounds__(kThreads, 1) steps_kernel(const HeadsAttendParams p, int limit) {
+__global__ void __launch_bounds__(Shape<D, NC, W>::kThreads, 1) steps_kernel(const HeadsAttendParams p, int limit) {
   using L = Shape<D, NC, W>;
+  constexpr int kWarps = L::kWarps, kThreads = L::kThreads;
   constexpr int kHalves = NC / 8, kBlocks = D / 64;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   __shared__ Cursor starts[L::kWorkers];
@@ -226,7 +236,9 @@ __global__ void __launch_bounds__(kThreads, 1) steps_kernel(const HeadsAttendPar
       if (begin >= first && begin < first + mine) {
         const int64_t in = begin - first;
         starts[k].r = r;
-        starts[k].u = (int)(in / q.tiles);
+        const int64_t unit = in / q.tiles;
+        starts[k].head = (int)(unit / q.groups);
+        starts[k].group = (int)(unit % q.groups);
         starts[k].tile = (int)(in % q.tiles);
         starts[k].q = q;
       }
@@ -257,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1) steps_kernel(const HeadsAttendPar
   float* parts = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(p.workspace) + ws_parts_offset(workers, L::kCols)) +
                  (int64_t)number * 2 * L::kCols * D;
   if (begin >= total) {
-    if (sub == 0 && lane == 0) *record = RunRecord{0, 0, 0, 0, 0, 0};
+    if (sub == 0 && lane == 0) *record = RunRecord{};
     return;
   }
 
@@ -268,22 +280,17 @@ __global__ void __launch_bounds__(kThreads, 1) steps_kernel(const HeadsAttendPar
   Cursor cur = starts[worker];
   cur.left = min(run, total - begin);
   producer.at = cur;
-  if (sub == 0) {
-#pragma unroll 1
-    for (int i = 0; i < L::kSlots; ++i) producer.issue(p, ring, full, empty, limit, w);
-  }
   uint32_t taken = 0;  // copies that this warp is done with
   int* nan_first = reinterpret_cast<int*>(smem_raw + L::kNan) + warp * D;  // by dimension: the first token whose value is NaN
   int64_t place = begin;  // of the current tile in the call
-  RunRecord cut{0, 0, 0, 0, 0, 0};
+  RunRecord cut{};
 
 #pragma unroll 1
   while (cur.left > 0 && !w.dead) {
     // a unit, or this run's part of it
-    const int head = cur.u / cur.q.groups, group = cur.u % cur.q.groups, tile0 = cur.tile;
+    const int head = cur.head, group = cur.group, tile0 = cur.tile;
     const int cols = min(L::kCols, cur.q.n * p.group - group * L::kCols) - sub * NC;  // of this warp
     const Request req = cur.q;
-    const int request = cur.r;
     const int64_t unit_begin = place - tile0;
     uint32_t q[kBlocks][4][kHalves][2];
     float qs[kHalves];
@@ -291,25 +298,38 @@ __global__ void __launch_bounds__(kThreads, 1) steps_kernel(const HeadsAttendPar
     int64_t row[kHalves];  // token and head of the column, as their offset in lse
     bool any_nan = false;
     for (int i = lane; i < D; i += 32) nan_first[i] = INT_MAX;
+    uint4 raw[kHalves][kBlocks][2];
 #pragma unroll
     for (int h = 0; h < kHalves; ++h) {
       const int c = 8 * h + g, in_group = group * L::kCols + sub * NC + c;
       const bool there = c < cols;
-      const int token = there ? in_group / p.group : 0, qh = head * p.group + (there ? in_group % p.group : 0);
+      const int token = there ? in_group / p.group : 0, qh = head * p.group + (there ? in_group - token * p.group : 0);
       sees[h] = there ? req.sees(p, token) : INT_MAX;
       row[h] = (req.t0 + token) * p.a.q_heads + qh;
       const uint16_t* src =
           static_cast<const uint16_t*>(p.a.q) + (req.t0 + token) * p.a.q_token_stride + qh * p.a.q_head_stride + 16 * t;
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          raw[h][b][i] = there ? __ldg(reinterpret_cast<const uint4*>(src + 64 * b) + i) : make_uint4(0, 0, 0, 0);
+    }
+    // (the first copies start while the queries are on their way)
+    if (sub == 0 && producer.count == 0) {
+#pragma unroll 1
+      for (int i = 0; i < min(L::kSlots, 4); ++i) producer.issue(p, ring, full, empty, limit, w);
+    }
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h) {
       float x[kBlocks][16], top = 0.f;
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const uint4 v = there ? __ldg(reinterpret_cast<const uint4*>(src + 64 * b) + i) : make_uint4(0, 0, 0, 0);
           if (f16)
-            Vec8<__half>{v}.values(x[b] + 8 * i);
+            Vec8<__half>{raw[h][b][i]}.values(x[b] + 8 * i);
           else
-            Vec8<__nv_bfloat16>{v}.values(x[b] + 8 * i);
+            Vec8<__nv_bfloat16>{raw[h][b][i]}.values(x[b] + 8 * i);
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(x[b][i]));
@@ -340,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1) steps_kernel(const HeadsAttendPar
         for (int k = 0; k < 4; ++k) o[h][i][k] = 0.f;
     }
 
-    int moved;
+    bool moved;
 #pragma unroll 1
     do {
       const int key0 = cur.tile * kHeadsPage;
@@ -374,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1) steps_kernel(const HeadsAttendPar
       __syncwarp();
       ++taken;
       if (W > 1 && lane == 0) tc::mbar_arrive(empty + 8 * ((taken - 1) % L::kSlots));
-      if (sub == 0) producer.issue(p, ring, full, empty, limit, w);
+      if (sub == 0) producer.refill(p, ring, full, empty, limit, taken, w);
 
       // weights
       slot = ring + taken % L::kSlots * L::kSlot, at = slot - smem;
@@ -482,18 +502,18 @@ __global__ void __launch_bounds__(kThreads, 1) steps_kernel(const HeadsAttendPar
       __syncwarp();
       ++taken;
       if (W > 1 && lane == 0) tc::mbar_arrive(empty + 8 * ((taken - 1) % L::kSlots));
-      if (sub == 0) producer.issue(p, ring, full, empty, limit, w);
+      if (sub == 0) producer.refill(p, ring, full, empty, limit, taken, w);
       ++place;
       moved = cur.next(p, L::kCols, limit);
-    } while (moved == 0 && cur.left > 0 && !w.dead);
+    } while (!moved && cur.left > 0 && !w.dead);
 
     // the unit's results, or this run's part of them
     __syncwarp();
     any_nan = __any_sync(0xFFFFFFFFu, any_nan);
-    const bool whole = tile0 == 0 && moved != 0;
+    const bool whole = tile0 == 0 && moved;
     const int part = unit_begin > begin ? 1 : 0;
-    if (moved == 0 && tile0 == 0)
-      cut = RunRecord{unit_begin, unit_begin + req.tiles, request, head, group, cols + sub * NC};
+    if (!moved && tile0 == 0)
+      cut = RunRecord{unit_begin, unit_begin + req.tiles, req.t0, head, group, cols + sub * NC};
 #pragma unroll
     for (int h = 0; h < kHalves; ++h) {
       const float most = quad_max(m[h]);
@@ -548,14 +568,65 @@ __global__ void __launch_bounds__(kThreads, 1) steps_kernel(const HeadsAttendPar
   if (w.dead) report(p.a.status, HS_ERR_TIMEOUT);
 }
 
-// Joins the parts of units that several runs share.  A block takes one column of a cut unit at a time; its warps take every
-// eighth part each, four at a time, so that their loads are on their way together.
-constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinParts = 4, kMaxWorkers = 2048;
+// Joins the parts of units that several runs share, a column a warp; where there are more than kFewParts, a column a block, whose
+// warps take every eighth part each.  Four parts at a time, so that their loads are on their way together.
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinParts = 4, kFewParts = 16, kMaxWorkers = 2048;
+
+// Column c of a cut unit: parts x0, x0 + step, ... <= last.
+template <int D>
+__device__ __forceinline__ Joined join_parts(const float4* stats, const float* parts, int i, int slot0, int c, int group_cols, int x0,
+                                             int step, int last, float (&acc)[D / 32]) {
+  constexpr int kPer = D / 32;
+  const int lane = threadIdx.x & 31;
+  Joined res;
+  for (; x0 <= last; x0 += step * kJoinParts) {
+    float4 st[kJoinParts];
+    float v[kJoinParts][kPer];
+#pragma unroll
+    for (int y = 0; y < kJoinParts; ++y) {
+      const int x = x0 + y * step;
+      if (x > last) continue;
+      const int64_t at = ((int64_t)x * 2 + (x == i ? slot0 : 0)) * group_cols + c;
+      st[y] = stats[at];
+      if constexpr (kPer == 4) {
+        const float4 f = *reinterpret_cast<const float4*>(parts + at * D + 4 * lane);
+        v[y][0] = f.x, v[y][1] = f.y, v[y][2] = f.z, v[y][3] = f.w;
+      } else {
+        const float2 f = *reinterpret_cast<const float2*>(parts + at * D + 2 * lane);
+        v[y][0] = f.x, v[y][1] = f.y;
+      }
+    }
+#pragma unroll
+    for (int y = 0; y < kJoinParts; ++y) {
+      if (x0 + y * step > last || st[y].y == -INFINITY) continue;
+      const float2 f = res.join(st[y]);
+#pragma unroll
+      for (int d = 0; d < kPer; ++d) acc[d] = acc[d] * f.x + v[y][d] * f.y;
+    }
+  }
+  return res;
+}
+template <int D>
+__device__ __forceinline__ void store_joined(const HeadsAttendParams& p, const RunRecord& rec, int c, int group_cols, const Joined& all,
+                                             const float (&out)[D / 32]) {
+  constexpr int kPer = D / 32;
+  const int lane = threadIdx.x & 31;
+  const float up = all.l == 0.f ? 0.f : exp2f(0.5f * (all.ref - all.m)), inv = all.l == 0.f ? 0.f : up / all.l;
+  const int in_unit = rec.group * group_cols + c;
+  const int64_t token = rec.t0 + in_unit / p.group;
+  const int qh = rec.head * p.group + in_unit % p.group;
+  if (!HS_CHECK(token < p.a.n && qh < p.a.q_heads, kChkOutPos)) return;
+  uint16_t* to = static_cast<uint16_t*>(p.a.out) + token * p.a.out_token_stride + qh * p.a.out_head_stride + lane * kPer;
+#pragma unroll
+  for (int d = 0; d < kPer; d += 2)
+    *reinterpret_cast<uint32_t*>(to + d) = pack(p.a.dtype == HS_FP16, out[d] * up * inv, out[d + 1] * up * inv);
+  if (lane == 0 && p.a.lse) p.a.lse[token * p.a.q_heads + qh] = all.l == 0.f ? -INFINITY : (all.anchor + (all.m + log2f(all.l))) * kLn2;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const HeadsAttendParams p, int workers, int group_cols) {
   constexpr int kPer = D / 32;
-  __shared__ uint16_t cuts[kMaxWorkers];
-  __shared__ int counts[kJoinWarps];
+  __shared__ CutLists<kJoinThreads, kMaxWorkers> cuts;
   __shared__ float4 joined[kJoinWarps];
   __shared__ float sums[kJoinWarps][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -565,61 +636,25 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const HeadsAttendPar
   const RunRecord* records = reinterpret_cast<const RunRecord*>(ws + sizeof(RunHeader));
   const float4* stats = reinterpret_cast<const float4*>(ws + ws_stats_offset(workers));
   const float* parts = reinterpret_cast<const float*>(ws + ws_parts_offset(workers, group_cols));
-  // the cut units, in order
-  int n = 0;
-  for (int i0 = 0; i0 < workers; i0 += kJoinThreads) {
-    const int i = i0 + threadIdx.x;
-    const bool is = i < workers && records[i].end > records[i].begin;
-    const unsigned those = __ballot_sync(0xFFFFFFFFu, is);
-    if (lane == 0) counts[warp] = __popc(those);
-    __syncthreads();
-    int at = n + __popc(those & ((1u << lane) - 1));
-#pragma unroll
-    for (int y = 0; y < kJoinWarps; ++y) {
-      if (y < warp) at += counts[y];
-      n += counts[y];
-    }
-    if (is) cuts[at] = (uint16_t)i;
-    __syncthreads();
-  }
-  for (int item = blockIdx.x; item < n * group_cols; item += gridDim.x) {
-    const int i = cuts[item / group_cols], c = item % group_cols;
+  int n[2];
+  cuts.build(records, workers, header.run, kFewParts, n);
+  for (int item = blockIdx.x * kJoinWarps + warp; item < n[0] * group_cols; item += gridDim.x * kJoinWarps) {
+    const int i = cuts.at[0][item / group_cols], c = item % group_cols;
     const RunRecord rec = records[i];
     if (c >= rec.cols) continue;
-    Request q;
-    q.load(p, rec.request, group_cols, INT_MAX);
-    const int last = (int)((rec.end - 1) / header.run);
-    const int slot0 = rec.begin > i * header.run ? 1 : 0;
-    Joined res;
     float acc[kPer] = {};
-    for (int x0 = i + warp; x0 <= last; x0 += kJoinWarps * kJoinParts) {
-      float4 st[kJoinParts];
-      float v[kJoinParts][kPer];
-#pragma unroll
-      for (int y = 0; y < kJoinParts; ++y) {
-        const int x = x0 + y * kJoinWarps;
-        if (x > last) continue;
-        const int64_t at = ((int64_t)x * 2 + (x == i ? slot0 : 0)) * group_cols + c;
-        st[y] = stats[at];
-        if constexpr (kPer == 4) {
-          const float4 f = *reinterpret_cast<const float4*>(parts + at * D + 4 * lane);
-          v[y][0] = f.x, v[y][1] = f.y, v[y][2] = f.z, v[y][3] = f.w;
-        } else {
-          const float2 f = *reinterpret_cast<const float2*>(parts + at * D + 2 * lane);
-          v[y][0] = f.x, v[y][1] = f.y;
-        }
-      }
-#pragma unroll
-      for (int y = 0; y < kJoinParts; ++y) {
-        if (x0 + y * kJoinWarps > last) continue;
-        const float2 f = res.join(st[y]);
-        if (st[y].y != -INFINITY) {
-#pragma unroll
-          for (int d = 0; d < kPer; ++d) acc[d] = acc[d] * f.x + v[y][d] * f.y;
-        }
-      }
-    }
-    if (lane == 0) joined[warp] = make_float4(res.ref, res.m, res.l, res.anchor);
+    const Joined all = join_parts<D>(stats, parts, i, rec.begin > i * header.run ? 1 : 0, c, group_cols, i, 1,
+                                     (int)((rec.end - 1) / header.run), acc);
+    store_joined<D>(p, rec, c, group_cols, all, acc);
+  }
+  for (int item = blockIdx.x; item < n[1] * group_cols; item += gridDim.x) {
+    const int i = cuts.at[1][item / group_cols], c = item % group_cols;
+    const RunRecord rec = records[i];
+    if (c >= rec.cols) continue;
+    float acc[kPer] = {};
+    const Joined some = join_parts<D>(stats, parts, i, rec.begin > i * header.run ? 1 : 0, c, group_cols, i + warp, kJoinWarps,
+                                      (int)((rec.end - 1) / header.run), acc);
+    if (lane == 0) joined[warp] = make_float4(some.ref, some.m, some.l, some.anchor);
 #pragma unroll
     for (int d = 0; d < kPer; ++d) sums[warp][lane * kPer + d] = acc[d];
     __syncthreads();
@@ -632,18 +667,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const HeadsAttendPar
 #pragma unroll
         for (int d = 0; d < kPer; ++d) out[d] = out[d] * f.x + sums[y][lane * kPer + d] * f.y;
       }
-      const float up = all.l == 0.f ? 0.f : exp2f(0.5f * (all.ref - all.m)), inv = all.l == 0.f ? 0.f : up / all.l;
-      const int in_unit = rec.group * group_cols + c;
-      const int64_t token = q.t0 + in_unit / p.group;
-      const int qh = rec.head * p.group + in_unit % p.group;
-      if (HS_CHECK(token < p.a.n && qh < p.a.q_heads, kChkOutPos)) {
-        uint16_t* to = static_cast<uint16_t*>(p.a.out) + token * p.a.out_token_stride + qh * p.a.out_head_stride + lane * kPer;
-#pragma unroll
-        for (int d = 0; d < kPer; d += 2)
-          *reinterpret_cast<uint32_t*>(to + d) = pack(p.a.dtype == HS_FP16, out[d] * up * inv, out[d + 1] * up * inv);
-        if (lane == 0 && p.a.lse)
-          p.a.lse[token * p.a.q_heads + qh] = all.l == 0.f ? -INFINITY : (all.anchor + (all.m + log2f(all.l))) * kLn2;
-      }
+      store_joined<D>(p, rec, c, group_cols, all, out);
     }
     __syncthreads();
   }
@@ -659,7 +683,7 @@ cudaError_t launch_steps(const HeadsAttendParams& p, int limit, int dev, int sms
   if (ready != cudaSuccess) return ready;
   const int workers = sms * L::kWorkers;
   if (workers > kMaxWorkers) return cudaErrorInvalidConfiguration;
-  steps_kernel<D, NC, W><<<sms, kThreads, L::kBytes, s>>>(p, limit);
+  steps_kernel<D, NC, W><<<sms, L::kThreads, L::kBytes, s>>>(p, limit);
   count_launch();
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -706,10 +730,12 @@ uint32_t check_take_heads_attend() {
 
 size_t heads_workspace_bytes(int sms) {
   size_t most = heads_prompt_workspace_bytes(sms);
-  for (const int w : {1, 2, 4}) {
-    const size_t b = ws_bytes(sms * (kWarps / w), 16 * w, 128);
-    most = b > most ? b : most;
-  }
+  auto shape = [&](int workers, int cols, int dim) { most = std::max(most, ws_bytes(sms * workers, cols, dim)); };
+  shape(Shape<64, 8, 1>::kWorkers, 8, 64);
+  shape(Shape<128, 8, 1>::kWorkers, 8, 128);
+  shape(Shape<128, 16, 1>::kWorkers, 16, 128);
+  shape(Shape<128, 16, 2>::kWorkers, 32, 128);
+  shape(Shape<128, 16, 4>::kWorkers, 64, 128);
   return most;
 }
 

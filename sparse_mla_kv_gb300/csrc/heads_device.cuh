@@ -21,9 +21,10 @@ struct RunHeader {
 };
 struct RunRecord {
   int64_t begin, end;        // tiles of the unit that begins in this run and is cut by its end; begin == end: none
-  int32_t request, head, group, cols;
+  int64_t t0;                // first query token of its request
+  int32_t head, group, cols, unused[3];
 };
-static_assert(sizeof(RunHeader) == 16 && sizeof(RunRecord) == 32, "the parts stay aligned to 16 bytes");
+static_assert(sizeof(RunHeader) == 16 && sizeof(RunRecord) == 48, "the parts stay aligned to 16 bytes");
 
 __device__ __forceinline__ uint4 lds16(uint32_t a) {
   uint4 v;
@@ -60,6 +61,50 @@ __device__ __forceinline__ void await(tc::Waiter& w, uint32_t bar, uint32_t pari
   w.wait(bar, parity);
   w.dead = __any_sync(0xFFFFFFFFu, w.dead);
 }
+// The cut units, for the kernels that join their parts: numbers of the records in two lists (units of more than `few` parts are in
+// the second), by the whole block of kThreads threads.  kMax: records at most.
+template <int kThreads, int kMax>
+struct CutLists {
+  uint16_t at[2][kMax];
+  uint16_t counts[2][kMax / kThreads][kThreads / 32];
+  __device__ __forceinline__ void build(const RunRecord* records, int n, int64_t run, int few, int (&total)[2]) {
+    constexpr int kRounds = kMax / kThreads, kWarps = kThreads / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t begin[kRounds], end[kRounds];
+#pragma unroll
+    for (int k = 0; k < kRounds; ++k) {
+      const int i = k * kThreads + threadIdx.x;
+      begin[k] = end[k] = 0;
+      if (i < n) begin[k] = records[i].begin, end[k] = records[i].end;
+    }
+    unsigned those[2][kRounds];
+#pragma unroll
+    for (int k = 0; k < kRounds; ++k) {
+      const bool is = end[k] > begin[k], many = is && end[k] > (k * kThreads + (int)threadIdx.x + few) * run;
+      those[0][k] = __ballot_sync(0xFFFFFFFFu, is && !many), those[1][k] = __ballot_sync(0xFFFFFFFFu, many);
+      if (lane == 0) counts[0][k][warp] = __popc(those[0][k]), counts[1][k][warp] = __popc(those[1][k]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      int so_far = 0;
+#pragma unroll
+      for (int k = 0; k < kRounds; ++k) {
+        if (k * kThreads >= n) break;
+        int mine = so_far;
+#pragma unroll
+        for (int x = 0; x < kWarps; ++x) {
+          if (x < warp) mine += counts[y][k][x];
+          so_far += counts[y][k][x];
+        }
+        if (those[y][k] >> lane & 1) at[y][mine + __popc(those[y][k] & ((1u << lane) - 1))] = (uint16_t)(k * kThreads + threadIdx.x);
+      }
+      total[y] = so_far;
+    }
+    __syncthreads();
+  }
+};
+
 // What parts of a column's (or row's) results have been joined so far: the references, the sum of weights.  A part's statistics are
 // (ref, m, l, anchor); one that has seen no token has m = -infinity.
 struct Joined {

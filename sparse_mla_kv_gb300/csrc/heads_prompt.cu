@@ -553,7 +553,7 @@ __device__ __forceinline__ void softmax_items(const HeadsAttendParams& p, const 
                   (int64_t)blockIdx.x * 2 * kBlock * (D / 4);
   uint32_t phase = 0, before = 0;  // key tiles of this query tile; of the CTA, in the items before
   RunRecord* record = reinterpret_cast<RunRecord*>(reinterpret_cast<uint8_t*>(p.workspace) + sizeof(RunHeader)) + blockIdx.x;
-  if (threadIdx.x == 0) *record = RunRecord{0, 0, 0, 0, 0, 0};
+  if (threadIdx.x == 0) *record = RunRecord{};
 #pragma unroll 1
   for (uint32_t k = 0;; ++k) {
     const Item* it = take_item(items, k, bars, w);
@@ -697,7 +697,7 @@ __device__ __forceinline__ void softmax_items(const HeadsAttendParams& p, const 
       }
       if (there) stats[part * kBlock + row] = make_float4(ref, m, l, anchor);
       if (threadIdx.x == 0 && k0 == 0)
-        *record = RunRecord{it->begin, it->begin + it->tiles, it->request, it->head, it->col0 / kBlock, it->rows};
+        *record = RunRecord{it->begin, it->begin + it->tiles, it->t0, it->head, it->col0 / kBlock, it->rows};
     } else {
       // Rows are stored by four lanes each, 64 bytes at a time: of each 8 dimensions a lane is given two of four rows, and the four
       // lanes of a row change places so that each has 8 dimensions of its own.
@@ -951,8 +951,7 @@ constexpr int kJoinThreads = 256, kJoinRows = 32, kJoinParts = 4, kMaxCtas = 512
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const HeadsAttendParams p, int ctas) {
   constexpr int kVecs = D / 32;  // float4 a thread
-  __shared__ uint16_t cuts[kMaxCtas];
-  __shared__ int counts[kJoinThreads / 32];
+  __shared__ CutLists<kJoinThreads, kMaxCtas> cuts;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // for the results of prompt_kernel
   const uint8_t* ws = reinterpret_cast<const uint8_t*>(p.workspace);
@@ -960,30 +959,14 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const HeadsAt
   const RunRecord* records = reinterpret_cast<const RunRecord*>(ws + sizeof(RunHeader));
   const float4* stats = reinterpret_cast<const float4*>(ws + ws_stats_offset(ctas));
   const float4* parts = reinterpret_cast<const float4*>(ws + ws_parts_offset(ctas));
-  int n = 0;
-  for (int i0 = 0; i0 < ctas; i0 += kJoinThreads) {
-    const int i = i0 + threadIdx.x;
-    const bool is = i < ctas && records[i].end > records[i].begin;
-    const unsigned those = __ballot_sync(0xFFFFFFFFu, is);
-    if (lane == 0) counts[warp] = __popc(those);
-    __syncthreads();
-    int at = n + __popc(those & ((1u << lane) - 1));
-#pragma unroll
-    for (int y = 0; y < kJoinThreads / 32; ++y) {
-      if (y < warp) at += counts[y];
-      n += counts[y];
-    }
-    if (is) cuts[at] = (uint16_t)i;
-    __syncthreads();
-  }
+  int n[2];
+  cuts.build(records, ctas, header.run, kMaxCtas, n);
   constexpr int kGroups = kBlock / kJoinRows;
   const int piece = warp;  // of 8
-  for (int item = blockIdx.x; item < n * kGroups; item += gridDim.x) {
-    const int i = cuts[item / kGroups], row = item % kGroups * kJoinRows + lane;
+  for (int item = blockIdx.x; item < n[0] * kGroups; item += gridDim.x) {
+    const int i = cuts.at[0][item / kGroups], row = item % kGroups * kJoinRows + lane;
     const RunRecord rec = records[i];
     if (row >= rec.cols) continue;
-    Request q;
-    q.load(p, rec.request, 0);
     const int last = (int)((rec.end - 1) / header.run);
     const int slot0 = rec.begin > i * header.run ? 1 : 0;
     Joined res;
@@ -1014,7 +997,7 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const HeadsAt
     }
     const float up = res.l == 0.f ? 0.f : exp2f(0.5f * (res.ref - res.m)), inv = res.l == 0.f ? 0.f : up / res.l;
     const int col = rec.group * kBlock + row, in_token = col / p.group;
-    const int64_t token = q.t0 + in_token;
+    const int64_t token = rec.t0 + in_token;
     const int head = rec.head * p.group + col - in_token * p.group;
     if (!HS_CHECK(token < p.a.n && head < p.a.q_heads, kChkOutPos)) continue;
     const bool f16 = p.a.dtype == HS_FP16;
