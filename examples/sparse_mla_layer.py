@@ -3,8 +3,9 @@
     python examples/sparse_mla_layer.py
 
 Random weights and latents stand for the layer's projections; every other step is the library's:
-  prompt   append_rows writes the prompts' rows into the paged pool and rotates the queries; attend_expanded attends over
-           keys and values expanded from the stored rows; offload_pages copies the completed pages to the host pool.
+  prompt   append_rows writes the prompts' rows into the paged pool and rotates the queries; read_rows reads them back, and
+           attend_expanded attends over the keys and values expanded from them; offload_pages copies the completed pages
+           to the host pool.
   decode   per step append_rows writes the new token; the requests whose pages left the GPU attend over the top-K rows
            that resolve_topk hands back (attend_rows), the others over their whole context (attend_pages), both with the
            up-projections absorbed into the queries and the results.
@@ -81,7 +82,7 @@ def run(prompts=(150, 70, 333), offloaded=(0, 2), steps=4, heads=16, topk=64, se
     T = len(owner)
     q_nope, q_rope = normal(T, H, NOPE), normal(T, H, ROPE)
     q_rope = hs.append_rows(pool, rows, normal(T, LATENT), normal(T, ROPE), pos, rotation, q_rope=q_rope)
-    latent, k_rope = stored(cache, rows)
+    latent, k_rope = hs.read_rows(pool, rows)
     k_nope = torch.einsum("tl,hdl->thd", latent, w_k).contiguous()
     v = torch.einsum("tl,hel->the", latent, w_v).contiguous()
     cu = torch.tensor([0, *prompts], device=device).cumsum(0).int()

@@ -694,3 +694,40 @@ def test_layers_and_offsets_past_32_bits():
     out, lse = hs.attend_heads(pool, table, i32([70, 80]), q, 0.1)
     check(cache, kv, dim, table, [70, 80], [1, 1], q, 0.1, out, lse)
     assert bool((cache[100:blocks - 2] == 0).all())
+
+
+def test_refusals():
+    """What the library refuses by itself, with nothing launched."""
+    kv, dim = 2, 128
+    pool, (cache,) = empty_pool(4, kv, dim)
+    table, ctx = i32([[0, 1], [2, 3]]), i32([70, 80])
+    q, k = torch.zeros((2, 4, dim), dtype=torch.bfloat16, device="cuda"), torch.zeros((2, kv, dim), dtype=torch.bfloat16, device="cuda")
+    small = hs.Pool([torch.zeros((4, 32, 2 * kv * dim + 16), dtype=torch.uint8, device="cuda")])  # pages of another size
+    latent = hs.Pool([torch.zeros((4, 64, 656), dtype=torch.uint8, device="cuda")])
+    before = hs.launch_count()
+
+    def refused(call):
+        with pytest.raises((hs.HSError, ValueError, TypeError)):
+            call()
+
+    for other in (small, latent):
+        refused(lambda: hs.attend_heads(other, table, ctx, q, 1.0))
+        refused(lambda: hs.append_heads(other, table, ctx, k, k))
+        refused(lambda: hs.read_heads(other, table, None, None, 2, dim))
+    refused(lambda: hs.read_rows(pool, i32([0])))
+    refused(lambda: hs.attend_heads(pool, table, ctx, q[:, :3], 1.0))                         # heads that are no multiple
+    refused(lambda: hs.attend_heads(pool, table, ctx, q[:, :1], 1.0))
+    refused(lambda: hs.attend_heads(pool, table, ctx, q, float("nan")))
+    refused(lambda: hs.attend_heads(pool, table, ctx, q, 1.0, layer=1))
+    refused(lambda: hs.append_heads(pool, table, ctx, k, k, layer=-1))
+    refused(lambda: hs.attend_heads(pool, table, ctx, q, 1.0, workspace=torch.zeros(1000, dtype=torch.uint8, device="cuda")))
+    refused(lambda: hs.attend_heads(pool, table, ctx, q, 1.0, workspace=hs.alloc_heads_workspace()[8:]))  # not aligned
+    refused(lambda: hs.attend_heads(pool, table, ctx, q, 1.0, out=q[:1].expand(2, -1, -1)))    # results on top of one another
+    flat = torch.zeros(4096, dtype=torch.bfloat16, device="cuda")
+    refused(lambda: hs.attend_heads(pool, table, ctx, flat[4:4 + 1024].view(2, 4, dim), 1.0))  # 8 bytes off
+    refused(lambda: hs.append_heads(pool, table, ctx, flat[:2 * 260].view(2, 260)[:, :256].view(2, kv, dim), k))  # rows of 520 bytes
+    refused(lambda: hs.read_heads(pool, table, None, None, 2, dim, k=flat[:256].view(1, kv, dim).expand(2, -1, -1)))
+    refused(lambda: hs.read_rows(latent, i32([0, 1]), latent=flat[:512].view(1, 512).expand(2, -1)))
+    refused(lambda: hs.append_heads(pool, i32([[0, 1]] * 3), i32([70] * 3), k, k))             # two tokens for three requests
+    refused(lambda: hs.attend_heads(pool, torch.empty((0, 2), dtype=torch.int32, device="cuda"), i32([]), q, 1.0))
+    assert hs.launch_count() == before
