@@ -90,6 +90,7 @@ struct Item {
   int32_t k0, k1, tiles;
   int32_t end[2];      // the query tile's part of the run ends here (at k0: it has none)
   int32_t keys, shift, past;  // column c sees the first c / group + shift tokens, at most keys; past: of more than the table has room for
+  int32_t part;        // which of the run's two places for partial results is its
   int32_t none;        // no item: the run has ended
 };
 static_assert(sizeof(Item) % 8 == 0, "alignment of what follows");
@@ -119,6 +120,7 @@ __device__ __forceinline__ int item_sees(const HeadsAttendParams& p, const Item&
 __device__ __forceinline__ void walk_items(const HeadsAttendParams& p, Start at, int limit, Item* items, uint32_t bars) {
   const int lane = threadIdx.x & 31;
   tc::Waiter w;
+  const int64_t first = at.at;
   Request q{};
   if (at.left > 0) q.load(p, at.r, limit);
 #pragma unroll 1
@@ -137,6 +139,7 @@ __device__ __forceinline__ void walk_items(const HeadsAttendParams& p, Start at,
       it.tiles = q.tiles(p, at.block);
       const int units = (int)min((int64_t)(kItemCost + it.tiles - at.in), at.left);
       it.begin = at.at - at.in + kItemCost;
+      it.part = it.begin > first;
       it.k0 = max(0, at.in - kItemCost);
       it.k1 = at.in + units - kItemCost;
       if (it.k1 > it.k0) {  // (a run that ends before an item's first key tile leaves it to the next)
@@ -389,7 +392,7 @@ __device__ __forceinline__ void widen_items(const HeadsAttendParams& p, const It
   const int lane = threadIdx.x & 31;
   const float sign = p.scale_log2 < 0.f ? -1.f : 1.f;
   tc::Waiter w;
-  uint32_t u = 0, tile = 0, queries[2] = {0, 0};
+  uint32_t u = 0, tile = 0, brought = 0, odd = 0;  // query tiles that have been brought, and an odd number of times
   auto arrive = [&](int bar) {
     tc::fence_async_smem();
     __syncwarp();
@@ -404,12 +407,12 @@ __device__ __forceinline__ void widen_items(const HeadsAttendParams& p, const It
     for (int i = threadIdx.x & 127; i < D; i += 128) nan_first[i] = INT_MAX;
     if ((threadIdx.x & 127) == 0) *flag = 0;
     asm volatile("bar.sync 1, 128;" ::: "memory");
-    const bool has[2] = {it->end[0] > it->k0, it->end[1] > it->k0};
-#pragma unroll
+#pragma unroll 1
     for (int t = 0; t < 2; ++t) {
-      if (!has[t]) continue;
-      if (queries[t] > 0) await(w, bars + 8 * (kQEmpty + t), (queries[t] - 1) & 1);
-      ++queries[t];
+      if (it->end[t] <= it->k0) continue;
+      if (brought >> t & 1) await(w, bars + 8 * (kQEmpty + t), (odd >> t & 1) ^ 1);
+      brought |= 1u << t;
+      odd ^= 1u << t;
       copy_queries<D>(p, it, t, smem);
     }
     const int all_see = item_sees(p, *it, it->col0), k0 = it->k0, k1 = it->k1;
@@ -435,9 +438,9 @@ __device__ __forceinline__ void widen_items(const HeadsAttendParams& p, const It
         if (page == 1) arrive((values ? kVFull : kKFull) + buf);
         if (i == 1 && j == k0) {  // (the first keys were widened while the queries were on their way)
           asm volatile("cp.async.wait_group 0;\n\tbar.sync 1, 128;" ::: "memory");
-#pragma unroll
+#pragma unroll 1
           for (int t = 0; t < 2; ++t) {
-            if (!has[t]) continue;
+            if (it->end[t] <= k0) continue;
             convert_queries<D>(p, it, t, smem, smem + L::kMisc + (k & 1) * kBlock, sign);
             arrive(kQFull + t);
           }
@@ -473,9 +476,12 @@ __device__ __forceinline__ void issue_items(const HeadsAttendParams& p, const It
     const Item* it = take_item(list, number, bars, w);
     if (!it) break;
     const int k0 = it->k0, k1 = it->k1, end = it->end[t];
+    auto keys_there = [&](int j) {
+      const uint32_t n = base + j - k0;
+      wait(kKFull + (n & 1), n / 2 & 1);
+    };
     auto scores = [&](int j) {
-      const uint32_t n = base + j - k0, buf = n & 1;
-      wait(kKFull + buf, n / 2 & 1);
+      const uint32_t buf = (base + j - k0) & 1;
 #pragma unroll
       for (int i = 0; i < L::kUnits; ++i) {
         const uint64_t da = dq + (uint32_t)(i * L::kUnit >> 4), db = dk + (uint32_t)((buf * L::kUnits + i) * L::kUnit >> 4);
@@ -487,6 +493,7 @@ __device__ __forceinline__ void issue_items(const HeadsAttendParams& p, const It
       if (j + 1 == end) tc::commit(bars + 8 * (kQEmpty + t), leader);
     };
     if (end > k0) {
+      keys_there(k0);
       wait(kQFull + t, items & 1);
       ++items;
       if (phase > 0) wait((L::kApart ? kSFree : kODone) + t, (phase - 1) & 1);  // the item before: S's place is free
@@ -496,11 +503,12 @@ __device__ __forceinline__ void issue_items(const HeadsAttendParams& p, const It
     for (int j = k0; j < end; ++j, ++phase) {
       const uint32_t n = base + j - k0, buf = n & 1;
       if (L::kApart && j + 1 < end) {
+        keys_there(j + 1);
         wait(kSFree + t, phase & 1);
         scores(j + 1);
       }
-      wait(kPReady + t, phase & 1);
       wait(kVFull + buf, n / 2 & 1);
+      wait(kPReady + t, phase & 1);
 #pragma unroll
       for (int page = 0; page < 2; ++page) {
         const uint64_t db = dv + (uint32_t)((2 * buf + page) * L::kVPage >> 4);
@@ -513,6 +521,7 @@ __device__ __forceinline__ void issue_items(const HeadsAttendParams& p, const It
       tc::commit(bars + 8 * (kODone + t), leader);
       tc::commit(bars + 8 * (kVEmpty + buf), leader);
       if (!L::kApart && j + 1 < end) {
+        keys_there(j + 1);
         wait(kODone + t, phase & 1);  // P, in S's place, has been read
         scores(j + 1);
       }
@@ -537,8 +546,7 @@ __device__ __forceinline__ void issue_items(const HeadsAttendParams& p, const It
 
 // ---- softmax and results (128 threads a query tile) ----
 template <int D>
-__device__ __forceinline__ void softmax_items(const HeadsAttendParams& p, const Item* items, int64_t run, uint32_t smem, const uint8_t* raw,
-                                              uint32_t tmem) {
+__device__ __forceinline__ void softmax_items(const HeadsAttendParams& p, const Item* items, uint32_t smem, const uint8_t* raw, uint32_t tmem) {
   using L = Smem<D>;
   const uint32_t bars = smem + L::kBar;
   tc::Waiter w;
@@ -547,20 +555,17 @@ __device__ __forceinline__ void softmax_items(const HeadsAttendParams& p, const 
   const uint32_t lanes = (uint32_t)(32 * ((threadIdx.x >> 5) & 3)) << 16;
   const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + L::kTo + t * L::kToStep, tp = tmem + lanes + L::kTp + t * L::kTpStep;
   const float scale = fabsf(p.scale_log2);
-  float4* stats = reinterpret_cast<float4*>(reinterpret_cast<uint8_t*>(p.workspace) + ws_stats_offset(gridDim.x)) +
-                  (int64_t)blockIdx.x * 2 * kBlock;
-  float4* parts = reinterpret_cast<float4*>(reinterpret_cast<uint8_t*>(p.workspace) + ws_parts_offset(gridDim.x)) +
-                  (int64_t)blockIdx.x * 2 * kBlock * (D / 4);
   uint32_t phase = 0, before = 0;  // key tiles of this query tile; of the CTA, in the items before
-  RunRecord* record = reinterpret_cast<RunRecord*>(reinterpret_cast<uint8_t*>(p.workspace) + sizeof(RunHeader)) + blockIdx.x;
-  if (threadIdx.x == 0) *record = RunRecord{};
+  auto record = [&]() {
+    return reinterpret_cast<RunRecord*>(reinterpret_cast<uint8_t*>(p.workspace) + sizeof(RunHeader)) + blockIdx.x;
+  };
+  if (threadIdx.x == 0) *record() = RunRecord{};
 #pragma unroll 1
   for (uint32_t k = 0;; ++k) {
     const Item* it = take_item(items, k, bars, w);
     if (!it) break;
-    const int col = it->col0 + row, k0 = it->k0, end = it->end[t];
-    const bool there = row < it->rows;
-    const int sees = there ? item_sees(p, *it, col) : 0;
+    const int k0 = it->k0, end = it->end[t];
+    const int sees = row < it->rows ? item_sees(p, *it, it->col0 + row) : 0;
     const int all_see = item_sees(p, *it, it->col0 + t * kQRows);  // (its first row sees least)
     float ref = -INFINITY, m = -INFINITY, l = 0.f, anchor = 0.f, qs = 0.f;
 #pragma unroll 1
@@ -592,27 +597,29 @@ __device__ __forceinline__ void softmax_items(const HeadsAttendParams& p, const 
           if (x >= (x < 64 ? left0 : left1)) s[x] = -INFINITY;
       }
       float top[2] = {__fmul_rn(tc::max_of<64>(s), c[0]), __fmul_rn(tc::max_of<64>(s + 64), c[1])};
-      if (__any_sync(0xFFFFFFFFu, fabsf(top[0]) > kLarge || fabsf(top[1]) > kLarge || anchor != 0.f)) {
-        // (a page that is not seen has a top of -infinity and does not count)
-        const float most = fmaxf(top[0], top[1]);
-        if (fabsf(most) <= 3.402823466e38f && (most - anchor > kLarge || (ref == -INFINITY && fabsf(most) > kLarge))) {
-          const float by = most - anchor;
-          anchor = most;
-          ref -= by, m -= by;
-        }
-#pragma unroll
-        for (int x = 0; x < 128; ++x) s[x] = __fsub_rn(__fmul_rn(s[x], c[x >> 6]), anchor);  // (rounded as the tops are)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) top[i] -= anchor, c[i] = 1.f;
-      }
       if (L::kApart && phase > 0) {  // the products before have read P, and are in O
         w.wait(bars + 8 * (kODone + t), (phase - 1) & 1);
         __syncwarp();
         tc::fence_after();
       }
-      const float most = fmaxf(top[0] + size[0], top[1] + size[1]);
-      const bool over = most > ref + kLazy;
-      if (__any_sync(0xFFFFFFFFu, over)) {
+      // rare: scores beyond kLarge, or a reference that has to move
+      const bool large = fabsf(top[0]) > kLarge || fabsf(top[1]) > kLarge || anchor != 0.f;
+      if (__any_sync(0xFFFFFFFFu, large || fmaxf(top[0] + size[0], top[1] + size[1]) > ref + kLazy)) {
+        if (__any_sync(0xFFFFFFFFu, large)) {
+          // (a page that is not seen has a top of -infinity and does not count)
+          const float most = fmaxf(top[0], top[1]);
+          if (fabsf(most) <= 3.402823466e38f && (most - anchor > kLarge || (ref == -INFINITY && fabsf(most) > kLarge))) {
+            const float by = most - anchor;
+            anchor = most;
+            ref -= by, m -= by;
+          }
+#pragma unroll
+          for (int x = 0; x < 128; ++x) s[x] = __fsub_rn(__fmul_rn(s[x], c[x >> 6]), anchor);  // (rounded as the tops are)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) top[i] -= anchor, c[i] = 1.f;
+        }
+        const float most = fmaxf(top[0] + size[0], top[1] + size[1]);
+        const bool over = most > ref + kLazy;
         const float now = over ? most - kTop : ref;
         const float alpha = over ? exp2f(ref - now) : 1.f;
         ref = now;
@@ -673,10 +680,13 @@ __device__ __forceinline__ void softmax_items(const HeadsAttendParams& p, const 
     }
     const int* nan_first = reinterpret_cast<const int*>(raw + L::kNan) + (k & 1) * D;
     const bool nans = work && *(reinterpret_cast<const volatile int*>(raw + L::kFlag) + (k & 1)) != 0;
-    const int part = it->begin > run * blockIdx.x ? 1 : 0;
+    const bool there = row < it->rows;
     const float up = l == 0.f ? 0.f : exp2f(0.5f * (ref - m)), inv = l == 0.f ? 0.f : up / l;
     const bool f16 = p.a.dtype == HS_FP16;
     if (!whole) {
+      uint8_t* ws = reinterpret_cast<uint8_t*>(p.workspace);
+      const int64_t slot = (int64_t)blockIdx.x * 2 + it->part;
+      float4* parts = reinterpret_cast<float4*>(ws + ws_parts_offset(gridDim.x)) + slot * (D / 4) * kBlock + row;
       if (work) {
 #pragma unroll 1
         for (int x = 0; x < D; x += 16) {
@@ -691,13 +701,14 @@ __device__ __forceinline__ void softmax_items(const HeadsAttendParams& p, const 
               for (int z = 0; z < 4; ++z)
                 if (sees > nan_first[x + y + z]) o[y + z] = __uint_as_float(0x7FC00000u);
             }
-            if (there) parts[(part * (D / 4) + (x + y) / 4) * kBlock + row] = make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
+            if (there) parts[(x + y) / 4 * kBlock] = make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
           }
         }
       }
-      if (there) stats[part * kBlock + row] = make_float4(ref, m, l, anchor);
+      if (there)
+        *(reinterpret_cast<float4*>(ws + ws_stats_offset(gridDim.x)) + slot * kBlock + row) = make_float4(ref, m, l, anchor);
       if (threadIdx.x == 0 && k0 == 0)
-        *record = RunRecord{it->begin, it->begin + it->tiles, it->t0, it->head, it->col0 / kBlock, it->rows};
+        *record() = RunRecord{it->begin, it->begin + it->tiles, it->t0, it->head, it->col0 / kBlock, it->rows};
     } else {
       // Rows are stored by four lanes each, 64 bytes at a time: of each 8 dimensions a lane is given two of four rows, and the four
       // lanes of a row change places so that each has 8 dimensions of its own.
@@ -754,7 +765,7 @@ __device__ __forceinline__ void softmax_items(const HeadsAttendParams& p, const 
         }
       }
       if (there && p.a.lse) {
-        const int token = col / p.group;
+        const int col = it->col0 + row, token = col / p.group;
         p.a.lse[(it->t0 + token) * p.a.q_heads + it->head * p.group + col - token * p.group] =
             l == 0.f ? -INFINITY : (anchor + (m + log2f(l))) * kLn2;
       }
@@ -771,7 +782,7 @@ struct Scratch {
   int64_t sums[kThreads / 32];
   Start start;
 };
-__device__ __forceinline__ int64_t find_start(const HeadsAttendParams& p, int limit, Scratch* s, int64_t* run_length) {
+__device__ __forceinline__ void find_start(const HeadsAttendParams& p, int limit, Scratch* s) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // units of the request of each thread
   auto units_of = [&](int r) {
@@ -879,8 +890,6 @@ __device__ __forceinline__ int64_t find_start(const HeadsAttendParams& p, int li
     }
   }
   __syncthreads();
-  *run_length = run;
-  return total;
 }
 
 template <int D>
@@ -913,8 +922,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const HeadsAttendPa
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  int64_t run;
-  find_start(p, limit, scratch, &run);
+  find_start(p, limit, scratch);
   const Start start = scratch->start;
   if (warp == kMmaWarp) tc::tmem_alloc(tc::smem_u32(tmem_slot), 512);
   tc::fence_before();
@@ -924,7 +932,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const HeadsAttendPa
   Item* items = reinterpret_cast<Item*>(raw + L::kItems);
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    softmax_items<D>(p, items, run, smem, raw, tmem);
+    softmax_items<D>(p, items, smem, raw, tmem);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (warp >= kWidenWarp)
