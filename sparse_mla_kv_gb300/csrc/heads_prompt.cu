@@ -34,7 +34,8 @@ constexpr int kThreads = 16 * 32, kMmaWarp = 8, kLoadWarp = 10, kWalkWarp = 11, 
 constexpr int kTakers = 15;  // warps that the items are handed to
 constexpr int kRegsLaunch = 128, kRegsSoftmax = 200, kRegsOther = 56;
 static_assert(2 * kRegsSoftmax + 2 * kRegsOther <= 4 * kRegsLaunch, "more registers than the launch has");
-constexpr int kStaged = 4, kScales = 8;  // staged pages (keys or values); key tiles whose scales are kept
+constexpr int kStaged = 4, kScales = 8;  // staged pages (a key tile's two of keys, then two of values); key tiles whose scales are kept
+static_assert(kStaged == 4, "a key tile's");
 constexpr int kMinRun = 6;               // of a run, in key tiles: fewer would be mostly set-up and joining
 constexpr int kItemCost = 3;             // what an item costs beside its key tiles, in these
 enum Bar { kStFull = 0, kStEmpty = kStFull + kStaged, kKFull = kStEmpty + kStaged, kKEmpty = kKFull + 2, kVFull = kKEmpty + 2,
@@ -188,7 +189,7 @@ __device__ __forceinline__ void load_items(const HeadsAttendParams& p, const Ite
   const uint32_t bars = smem + L::kBar;
   const int lane = threadIdx.x & 31;
   tc::Waiter w;
-  uint32_t u = 0, tile = 0;  // staged pages and key tiles so far
+  uint32_t tile = 0, part = 0;  // key tiles so far; of the next one, the pages that have been announced (a bit each)
 #pragma unroll 1
   for (uint32_t k = 0;; ++k) {
     const Item* item = take_item(items, k, bars, w);
@@ -197,7 +198,7 @@ __device__ __forceinline__ void load_items(const HeadsAttendParams& p, const Ite
     const bool past = item->past;
     int cached = -1, cached_at = -1;  // table entries: a page a lane
 #pragma unroll 1
-    for (int j = item->k0; j < k1 && !w.dead; ++j, ++tile) {
+    for (int j = item->k0; j < k1; ++j, ++tile) {
       const int page0 = 2 * j;
       if (cached_at != (page0 & ~31)) {
         cached_at = page0 & ~31;
@@ -224,35 +225,44 @@ __device__ __forceinline__ void load_items(const HeadsAttendParams& p, const Ite
       if (lane >= 2 && lane < 4) scale = log2f(scale);
       const uint32_t scales = smem + L::kPage + tile % kScales * 32;
       __syncwarp();
-#pragma unroll 1
-      for (int i = 0; i < 4; ++i, ++u) {
-        const uint32_t slot = u % kStaged, bar = bars + 8 * (kStFull + slot);
-        if (u >= kStaged) await(w, bars + 8 * (kStEmpty + slot), (u / kStaged - 1) & 1);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t bar = bars + 8 * (kStFull + i);
+        if (tile > 0) {
+          await(w, bars + 8 * (kStEmpty + i), (tile - 1) & 1);
+          // (complete by then, unless another warp's wait gave up: nothing is announced before the copy before has landed)
+          await(w, bar, (tile - 1) & 1);
+        }
         if (w.dead) break;
         if (i == 0) {
           if (lane < 4) sts_u(scales + 4 * lane, __float_as_uint(scale));
           if (lane < 2) sts_u(scales + 16 + 4 * lane, is);
           __syncwarp();
         }
-        const int pg = i & 1;
-        const bool copy = pg ? there[1] : there[0];
         if (lane == 0) {
-          if (copy) {
-            const uint8_t* from = p.pages.codes(pg ? block[1] : block[0], head, D) + (i >> 1) * L::kStage;
+          if (there[i & 1]) {
+            const uint8_t* from = p.pages.codes(block[i & 1], head, D) + (i >> 1) * L::kStage;
             tc::mbar_expect(bar, L::kStage);
-            bulk_copy(smem + L::kStages + slot * L::kStage, from, L::kStage, bar);
+            bulk_copy(smem + L::kStages + i * L::kStage, from, L::kStage, bar);
           } else {
             tc::mbar_arrive(bar);
           }
         }
+        part |= 1u << i;
         __syncwarp();
       }
+      if (w.dead) break;
+      part = 0;
     }
     done_with_item(k, bars);
   }
   // no copy is in flight when the CTA ends
   tc::Drain drain;
-  for (uint32_t x = u > kStaged ? u - kStaged : 0; x < u; ++x) drain.wait(bars + 8 * (kStFull + x % kStaged), x / kStaged & 1);
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t n = tile + (part >> i & 1);
+    if (n > 0) drain.wait(bars + 8 * (kStFull + i), (n - 1) & 1);
+  }
   if (w.dead) report(p.a.status, HS_ERR_TIMEOUT);
 }
 
@@ -343,46 +353,43 @@ __device__ __forceinline__ void convert_queries(const HeadsAttendParams& p, cons
 }
 
 // A staged page's keys or values to fp16.  Row r of block db (a token's 64 dimensions, or a dimension's 64 tokens) goes to row r
-// of `to` + db * step.  zero: the page is not there.  clean: NaN codes become zero and are noted, see the head of this file.
+// of `to` + db * step.
 template <int D>
-__device__ __forceinline__ void widen(uint32_t from, uint32_t to, int step, bool zero, bool clean, int key0, int* nan_first, int* flag) {
-  const int thread = threadIdx.x & 127, row0 = (thread >> 2) & 31, piece = thread & 3;
+__device__ __forceinline__ void widen(uint32_t from, uint32_t to, int step) {
+  const int thread = threadIdx.x & 127, row = thread >> 2, piece = thread & 3;  // (and row + 32)
+  const uint32_t at = row * 128 + (((2 * piece) ^ (row & 7)) << 4);               // the odd piece beside it: its bit 4 turned
   uint4 v[D / 32];
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i) v[i] = lds16(from + (i * 128 + thread) * 16);
-  if (zero || clean) {
-#pragma unroll 1
-    for (int i = 0; i < D / 32; ++i) {
-      const uint32_t at = from + (i * 128 + thread) * 16;
-      uint32_t words[4] = {lds_u(at), lds_u(at + 4), lds_u(at + 8), lds_u(at + 12)};
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const uint32_t is = zero ? 0 : nan_codes(words[x]);
-        if (is) {
-          words[x] &= ~((is >> 7) * 0xFFu);
-          atomicMin(nan_first + i * 32 + row0, key0 + 16 * piece + 4 * x + ((__ffs(is) - 1) >> 3));
-          *flag = 1;
-        }
-        if (is || zero) sts_u(at + 4 * x, zero ? 0 : words[x]);
-      }
-    }
-    tc::fence_async_smem();  // (the next copy goes to the same place)
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) v[i] = lds16(from + (i * 128 + thread) * 16);
-  }
+  for (int i = 0; i < D / 32; ++i) v[i] = lds16(from + i * 2048 + thread * 16);
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) {
-    const int row = (i & 1) * 32 + row0;
-    const uint32_t at = to + (i >> 1) * step + row * 128;
     const uint32_t words[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint2 a = half_of_codes(words[2 * h]), b = half_of_codes(words[2 * h + 1]);
-      asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + (((2 * piece + h) ^ (row & 7)) << 4)), "r"(a.x), "r"(a.y),
-                   "r"(b.x), "r"(b.y)
+      const uint2 x = half_of_codes(words[2 * h]), y = half_of_codes(words[2 * h + 1]);
+      asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + (h ? at ^ 16 : at) + (i >> 1) * step + (i & 1) * 4096), "r"(x.x),
+                   "r"(x.y), "r"(y.x), "r"(y.y)
                    : "memory");
     }
   }
+}
+// Before that, where it is wanted.  zero: the page is not there.  Else NaN codes of values become zero and are noted, see the head
+// of this file.
+template <int D>
+__device__ __forceinline__ void clean_staged(uint32_t from, bool zero, int key0, int* nan_first, int* flag) {
+  const int thread = threadIdx.x & 127;
+#pragma unroll 1
+  for (int i = thread; i < D * 16; i += 128) {  // words
+    const uint32_t at = from + i * 4;
+    const uint32_t word = lds_u(at), is = zero ? 0 : nan_codes(word);
+    if (is) {
+      atomicMin(nan_first + i / 16, key0 + 4 * (i % 16) + ((__ffs(is) - 1) >> 3));
+      *flag = 1;
+    }
+    if (is || zero) sts_u(at, zero ? 0 : word & ~((is >> 7) * 0xFFu));
+  }
+  tc::fence_async_smem();  // (the next copy goes to the same place)
+  asm volatile("bar.sync 1, 128;" ::: "memory");
 }
 
 template <int D>
@@ -392,7 +399,7 @@ __device__ __forceinline__ void widen_items(const HeadsAttendParams& p, const It
   const int lane = threadIdx.x & 31;
   const float sign = p.scale_log2 < 0.f ? -1.f : 1.f;
   tc::Waiter w;
-  uint32_t u = 0, tile = 0, brought = 0, odd = 0;  // query tiles that have been brought, and an odd number of times
+  uint32_t tile = 0, brought = 0, odd = 0;  // query tiles that have been brought, and an odd number of times
   auto arrive = [&](int bar) {
     tc::fence_async_smem();
     __syncwarp();
@@ -421,20 +428,19 @@ __device__ __forceinline__ void widen_items(const HeadsAttendParams& p, const It
       const uint32_t buf = tile & 1, scales = smem + L::kPage + tile % kScales * 32;
       const bool clean = (j + 1) * kKeys > all_see;
 #pragma unroll 1
-      for (int i = 0; i < 4; ++i, ++u) {
-        const uint32_t slot = u % kStaged;
+      for (int i = 0; i < 4; ++i) {  // (staging holds a key tile's four pages: slot i)
         const int page = i & 1;
         const bool values = i >= 2;
         if (page == 0 && tile >= 2) await(w, bars + 8 * ((values ? kVEmpty : kKEmpty) + buf), (tile / 2 - 1) & 1);
-        await(w, bars + 8 * (kStFull + slot), u / kStaged & 1);
+        await(w, bars + 8 * (kStFull + i), tile & 1);
+        const uint32_t from = smem + L::kStages + i * L::kStage;
         const bool zero = lds_u(scales + 16 + 4 * page) == 0;
-        const uint32_t from = smem + L::kStages + slot * L::kStage;
-        if (values)
-          widen<D>(from, smem + L::kV + (2 * buf + page) * L::kVPage, 64 * 128, zero, clean, j * kKeys + page * kHeadsPage, nan_first, flag);
-        else
-          widen<D>(from, smem + L::kK + buf * L::kUnits * L::kUnit + page * 64 * 128, L::kUnit, zero, false, 0, nan_first, flag);
+        if (zero || (clean && values)) clean_staged<D>(from, zero, j * kKeys + page * kHeadsPage, nan_first, flag);
+        // a page's keys: rows page * 64 .. of every 64 dimensions' unit; its values: a part of D rows of its own
+        const uint32_t to = smem + (values ? L::kV + (2 * buf + page) * L::kVPage : L::kK + buf * L::kUnits * L::kUnit + page * 8192);
+        widen<D>(from, to, values ? 64 * 128 : L::kUnit);
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(bars + 8 * (kStEmpty + slot));
+        if (lane == 0) tc::mbar_arrive(bars + 8 * (kStEmpty + i));
         if (page == 1) arrive((values ? kVFull : kKFull) + buf);
         if (i == 1 && j == k0) {  // (the first keys were widened while the queries were on their way)
           asm volatile("cp.async.wait_group 0;\n\tbar.sync 1, 128;" ::: "memory");
