@@ -84,10 +84,11 @@ struct Place {
   }
 };
 
+// blockIdx.z: 0 the keys, 1 the values.
 template <typename T, int D>
 __global__ void __launch_bounds__(2 * D) append_heads_kernel(const HeadsAppendParams p) {
   const hs_heads_append& a = p.a;
-  const bool reports = blockIdx.x == 0 && blockIdx.y == 0;
+  const bool reports = blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0;
   PageWork w;
   auto first = [&](int r, int count) {
     const int ctx = __ldg(a.ctx_len + r);
@@ -95,115 +96,103 @@ __global__ void __launch_bounds__(2 * D) append_heads_kernel(const HeadsAppendPa
   };
   if (!find_page(p.ragged, blockIdx.x, reports, a.status, first, &w)) return;
   const int head = blockIdx.y;
+  const bool values = blockIdx.z == 1;
   const Place<D> at;
   auto is_new = [&](int token) { return token >= w.lo && token < w.hi; };
+  // tokens of this thread: key_token + 16 i, or 4 quad + i
+  const int token0 = values ? 4 * at.quad : at.key_token, step = values ? 1 : 16;
   // everything that the page's place does not decide is loaded first
-  Vec8<T> key[4], value[4];
-  const T* k = static_cast<const T*>(a.k) + (w.row - w.lo) * a.k_token_stride + head * a.k_head_stride + 8 * at.key_chunk;
-  const T* v = static_cast<const T*>(a.v) + (w.row - w.lo) * a.v_token_stride + head * a.v_head_stride + 8 * at.value_chunk;
+  Vec8<T> in[4];
+  const T* src = values ? static_cast<const T*>(a.v) + (w.row - w.lo) * a.v_token_stride + head * a.v_head_stride + 8 * at.value_chunk
+                        : static_cast<const T*>(a.k) + (w.row - w.lo) * a.k_token_stride + head * a.k_head_stride + 8 * at.key_chunk;
+  const int64_t stride = values ? a.v_token_stride : a.k_token_stride;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int kt = at.key_token + 16 * i, vt = 4 * at.quad + i;
-    if (is_new(kt)) key[i].load(k + kt * a.k_token_stride);
-    if (is_new(vt)) value[i].load(v + vt * a.v_token_stride);
-  }
+  for (int i = 0; i < 4; ++i)
+    if (is_new(token0 + step * i)) in[i].load(src + (token0 + step * i) * stride);
   const int block = block_of(p.pages, w, a.status);
   if (block < 0 || !HS_CHECK(block < p.pages.num_blocks && head < p.pages.kv_heads, kChkPoolRow)) return;
-  uint8_t* codes = p.pages.codes(block, head, D);
-  float* scales = p.pages.scale(block, head, D);
-  const float old_k = w.lo > 0 ? scales[0] : 0.f, old_v = w.lo > 0 ? scales[p.pages.kv_heads] : 0.f;
+  uint8_t* codes = p.pages.codes(block, head, D) + (values ? D * kHeadsPage : 0);
+  float* scale_at = p.pages.scale(block, head, D) + (values ? p.pages.kv_heads : 0);
+  const float old = w.lo > 0 ? *scale_at : 0.f;
 
-  float top_k = 0.f, top_v = 0.f;
+  float top = 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
+    if (!is_new(token0 + step * i)) continue;
     float x[8];
-    if (is_new(at.key_token + 16 * i)) {
-      key[i].values(x);
+    in[i].values(x);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) top_k = max_finite(top_k, x[e]);
-    }
-    if (is_new(4 * at.quad + i)) {
-      value[i].values(x);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) top_v = max_finite(top_v, x[e]);
-    }
+    for (int e = 0; e < 8; ++e) top = max_finite(top, x[e]);
   }
-  __shared__ uint32_t tops[2][2 * D / 32];
-  const uint32_t warp_k = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top_k));  // (not negative: ordered as their bits)
-  const uint32_t warp_v = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top_v));
-  if ((threadIdx.x & 31) == 0) tops[0][threadIdx.x >> 5] = warp_k, tops[1][threadIdx.x >> 5] = warp_v;
+  __shared__ uint32_t tops[2 * D / 32];
+  const uint32_t warp_top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top));  // (not negative: ordered as their bits)
+  if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = warp_top;
   __syncthreads();
-  uint32_t all_k = 0, all_v = 0;
+  uint32_t all = 0;
 #pragma unroll
-  for (int i = 0; i < 2 * D / 32; ++i) all_k = max(all_k, tops[0][i]), all_v = max(all_v, tops[1][i]);
-  const float scale_k = fmaxf(power_scale(__uint_as_float(all_k)), old_k);
-  const float scale_v = fmaxf(power_scale(__uint_as_float(all_v)), old_v);
-  const float inv_k = 1.f / scale_k, inv_v = 1.f / scale_v;
-  const bool grown_k = w.lo > 0 && scale_k > old_k, grown_v = w.lo > 0 && scale_v > old_v;
-  const float shrink_k = old_k * inv_k, shrink_v = old_v * inv_v;
+  for (int i = 0; i < 2 * D / 32; ++i) all = max(all, tops[i]);
+  const float scale = fmaxf(power_scale(__uint_as_float(all)), old), inv = 1.f / scale;
+  const bool grown = w.lo > 0 && scale > old;
+  const float shrink = old * inv;
+  if (threadIdx.x == 0) *scale_at = scale;  // (all threads have read it)
 
-  // keys
+  if (!values) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int token = at.key_token + 16 * i;
-    uint2* to = reinterpret_cast<uint2*>(codes + at.key_at(token));
-    float x[8];
-    if (is_new(token)) {
-      key[i].values(x);
+    for (int i = 0; i < 4; ++i) {
+      const int token = token0 + 16 * i;
+      uint2* to = reinterpret_cast<uint2*>(codes + at.key_at(token));
+      float x[8];
+      if (is_new(token)) {
+        in[i].values(x);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = scaled_finite(x[e], inv_k);
-    } else if (grown_k && token < w.lo) {
-      const uint2 c = *to;
-      float_of_codes(c.x, x);
-      float_of_codes(c.y, x + 4);
+        for (int e = 0; e < 8; ++e) x[e] = scaled_finite(x[e], inv);
+      } else if (grown && token < w.lo) {
+        const uint2 c = *to;
+        float_of_codes(c.x, x);
+        float_of_codes(c.y, x + 4);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] *= shrink_k;
-    } else {
-      continue;
+        for (int e = 0; e < 8; ++e) x[e] *= shrink;
+      } else {
+        continue;
+      }
+      *to = make_uint2(e4m3x4(x[0], x[1], x[2], x[3]), e4m3x4(x[4], x[5], x[6], x[7]));
     }
-    *to = make_uint2(e4m3x4(x[0], x[1], x[2], x[3]), e4m3x4(x[4], x[5], x[6], x[7]));
+    return;
   }
   // values: four tokens of a dimension are a word; one that has other tokens too keeps those
-  uint8_t* values = codes + D * kHeadsPage;
-  const int q0 = 4 * at.quad;
-  const bool whole = q0 >= w.lo && q0 + 4 <= w.hi, some = q0 < w.hi && q0 + 4 > w.lo, older = grown_v && q0 < w.lo;
-  if (some || older) {
-    uint32_t word[8];
-    if (!whole) {
+  const bool whole = token0 >= w.lo && token0 + 4 <= w.hi, some = token0 < w.hi && token0 + 4 > w.lo, older = grown && token0 < w.lo;
+  if (!some && !older) return;
+  uint32_t word[8];
+  if (!whole) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) word[e] = *reinterpret_cast<const uint32_t*>(values + at.value_at(e));
-    }
-    float x[4][8];
+    for (int e = 0; e < 8; ++e) word[e] = *reinterpret_cast<const uint32_t*>(codes + at.value_at(e));
+  }
+  float x[4][8];
+  uint32_t fresh = 0, grow = 0;  // bytes of a word that are new, and that are rescaled
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (is_new(q0 + i)) {
-        value[i].values(x[i]);
+  for (int i = 0; i < 4; ++i) {
+    if (is_new(token0 + i)) {
+      in[i].values(x[i]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[i][e] = scaled_finite(x[i][e], inv_v);
-      } else {
+      for (int e = 0; e < 8; ++e) x[i][e] = scaled_finite(x[i][e], inv);
+      fresh |= 0xFFu << (8 * i);
+    } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[i][e] = 0.f;
-      }
-    }
-    uint32_t fresh = 0, grow = 0;  // bytes of a word that are new, and that are rescaled
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (is_new(q0 + i)) fresh |= 0xFFu << (8 * i);
-      if (older && q0 + i < w.lo) grow |= 0xFFu << (8 * i);
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      uint32_t c = e4m3x4(x[0][e], x[1][e], x[2][e], x[3][e]);
-      if (!whole) {
-        float y[4];
-        float_of_codes(word[e], y);
-        const uint32_t smaller = e4m3x4(y[0] * shrink_v, y[1] * shrink_v, y[2] * shrink_v, y[3] * shrink_v);
-        c = (c & fresh) | (smaller & grow) | (word[e] & ~(fresh | grow));
-      }
-      *reinterpret_cast<uint32_t*>(values + at.value_at(e)) = c;
+      for (int e = 0; e < 8; ++e) x[i][e] = 0.f;
+      if (older && token0 + i < w.lo) grow |= 0xFFu << (8 * i);
     }
   }
-  if (threadIdx.x == 0) scales[0] = scale_k, scales[p.pages.kv_heads] = scale_v;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    uint32_t c = e4m3x4(x[0][e], x[1][e], x[2][e], x[3][e]);
+    if (!whole) {
+      float y[4];
+      float_of_codes(word[e], y);
+      const uint32_t smaller = e4m3x4(y[0] * shrink, y[1] * shrink, y[2] * shrink, y[3] * shrink);
+      c = (c & fresh) | (smaller & grow) | (word[e] & ~(fresh | grow));
+    }
+    *reinterpret_cast<uint32_t*>(codes + at.value_at(e)) = c;
+  }
 }
 
 template <typename T, int D>
@@ -299,7 +288,8 @@ uint32_t check_take_heads_pages() {
 }
 
 cudaError_t launch_append_heads(const HeadsAppendParams& p, cudaStream_t s) {
-  const dim3 grid = page_grid(p.a.n, p.a.R, p.a.kv_heads);
+  dim3 grid = page_grid(p.a.n, p.a.R, p.a.kv_heads);
+  grid.z = 2;
   if (p.a.dtype == HS_BF16)
     launch_append_type<__nv_bfloat16>(p, grid, s);
   else if (p.a.dtype == HS_FP16)
