@@ -189,63 +189,64 @@ __global__ void __launch_bounds__(Shape<D, NC, W>::kThreads, 1) steps_kernel(con
     tc::mbar_init(smem + L::kBars + 8 * (L::kWorkers * L::kSlots + threadIdx.x), W);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  // the call's tiles, and where each worker's run begins
+  // the call's tiles, and where each worker's run begins: those of kThreads requests at a time, looked through once for their sum
+  // and, where there are more, once again
   bool bad = false;
-  int64_t sum = 0;
-  for (int r = threadIdx.x; r < p.a.R; r += kThreads) {
-    int64_t t0;
-    int n;
-    bad |= !p.ragged.tokens(r, &t0, &n);
-    Request q;
-    q.load(p, r, L::kCols, limit);
-    sum += (int64_t)p.pages.kv_heads * q.groups * q.tiles;
-  }
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-  if (lane == 0) sums[warp] = sum;
-  bad = __syncthreads_or(bad);
-  int64_t total = 0;
-#pragma unroll
-  for (int i = 0; i < kWarps; ++i) total += sums[i];
-  __syncthreads();
-  if (bad) total = 0;
-  const int64_t run = max((int64_t)1, (total + workers - 1) / workers);
-  int64_t before = 0;
-  for (int r0 = 0; r0 < p.a.R && total > 0; r0 += kThreads) {
-    const int r = r0 + threadIdx.x;
+  int64_t total = 0, run = 1;
+  const int rounds = (p.a.R + kThreads - 1) / kThreads;
+  int64_t before = 0;  // tiles of the rounds before
+#pragma unroll 1
+  for (int pass = 0, x = 0; rounds > 0; ++x) {
+    if (x == rounds) {
+      x = 0;
+      if (++pass == 2 || rounds == 1) break;
+      before = 0;
+    }
+    const int r = x * kThreads + threadIdx.x;
     Request q{};
-    if (r < p.a.R) q.load(p, r, L::kCols, limit);
+    bool wrong = false;
+    if (r < p.a.R) {
+      int64_t t0;
+      int n;
+      wrong = !p.ragged.tokens(r, &t0, &n);
+      q.load(p, r, L::kCols, limit);
+    }
     const int64_t mine = (int64_t)p.pages.kv_heads * q.groups * q.tiles;
     int64_t upto = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int64_t x = __shfl_up_sync(0xFFFFFFFFu, upto, d);
-      if (lane >= d) upto += x;
+      const int64_t y = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+      if (lane >= d) upto += y;
     }
     if (lane == 31) sums[warp] = upto;
-    __syncthreads();
-    int64_t off = before, chunk = 0;
+    bad |= __syncthreads_or(wrong);
+    int64_t first = before + upto - mine;
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) {
-      if (i < warp) off += sums[i];
-      chunk += sums[i];
+      if (i < warp) first += sums[i];
+      before += sums[i];
     }
-    const int64_t first = off + upto - mine;
-    for (int k = 0; k < L::kWorkers; ++k) {
-      const int64_t begin = run * (k * (int64_t)gridDim.x + blockIdx.x);
-      if (begin >= first && begin < first + mine) {
-        const int64_t in = begin - first;
-        starts[k].r = r;
-        const int64_t unit = in / q.tiles;
-        starts[k].head = (int)(unit / q.groups);
-        starts[k].group = (int)(unit % q.groups);
-        starts[k].tile = (int)(in % q.tiles);
-        starts[k].q = q;
+    __syncthreads();
+    if (pass == 0 && x + 1 == rounds) {
+      total = bad ? 0 : before;
+      run = max((int64_t)1, (total + workers - 1) / workers);
+    }
+    if (total > 0 && (pass == 1 || rounds == 1)) {
+      for (int k = 0; k < L::kWorkers; ++k) {
+        const int64_t begin = run * (k * (int64_t)gridDim.x + blockIdx.x);
+        if (begin >= first && begin < first + mine) {
+          const int64_t in = begin - first;
+          const int64_t unit = in / q.tiles;
+          starts[k].r = r;
+          starts[k].head = (int)(unit / q.groups);
+          starts[k].group = (int)(unit % q.groups);
+          starts[k].tile = (int)(in % q.tiles);
+          starts[k].q = q;
+        }
       }
     }
-    before += chunk;
-    __syncthreads();
   }
+  __syncthreads();
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     if (bad) report(p.a.status, HS_ERR_ID_RANGE);
     *reinterpret_cast<RunHeader*>(p.workspace) = RunHeader{run, total};
