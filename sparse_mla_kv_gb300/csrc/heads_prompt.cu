@@ -118,7 +118,10 @@ __device__ __forceinline__ int item_sees(const HeadsAttendParams& p, const Item&
 }
 
 // Hands the run's items to the others (one warp).
-__device__ __forceinline__ void walk_items(const HeadsAttendParams& p, Start at, int limit, Item* items, uint32_t bars) {
+template <int D>
+__device__ __forceinline__ void walk_items(const HeadsAttendParams& p, Start at, int limit, uint8_t* raw, uint32_t bars) {
+  using L = Smem<D>;
+  Item* items = reinterpret_cast<Item*>(raw + L::kItems);
   const int lane = threadIdx.x & 31;
   tc::Waiter w;
   const int64_t first = at.at;
@@ -162,6 +165,9 @@ __device__ __forceinline__ void walk_items(const HeadsAttendParams& p, Start at,
     }
     if (k >= 2) await(w, bars + 8 * (kItemDone + (k & 1)), (k / 2 - 1) & 1);
     if (w.dead) break;
+    for (int i = lane; i < D; i += 32) reinterpret_cast<int*>(raw + L::kNan)[(k & 1) * D + i] = INT_MAX;
+    if (lane == 0) reinterpret_cast<int*>(raw + L::kFlag)[k & 1] = 0;
+    __syncwarp();
     if (lane == 0) {
       items[k & 1] = it;
       tc::mbar_arrive(bars + 8 * (kItem + (k & 1)));
@@ -373,23 +379,33 @@ __device__ __forceinline__ void widen(uint32_t from, uint32_t to, int step) {
     }
   }
 }
-// Before that, where it is wanted.  zero: the page is not there.  Else NaN codes of values become zero and are noted, see the head
-// of this file.
+// Before that, where it is wanted, by the same threads for the same codes.  zero: the page is not there.  Else NaN codes of values
+// become zero and are noted, see the head of this file.
 template <int D>
 __device__ __forceinline__ void clean_staged(uint32_t from, bool zero, int key0, int* nan_first, int* flag) {
   const int thread = threadIdx.x & 127;
 #pragma unroll 1
-  for (int i = thread; i < D * 16; i += 128) {  // words
-    const uint32_t at = from + i * 4;
+  for (int i = 0; i < D / 8; ++i) {  // words of this thread
+    const int piece = i >> 2;
+    const uint32_t at = from + piece * 2048 + thread * 16 + (i & 3) * 4;
     const uint32_t word = lds_u(at), is = zero ? 0 : nan_codes(word);
     if (is) {
-      atomicMin(nan_first + i / 16, key0 + 4 * (i % 16) + ((__ffs(is) - 1) >> 3));
+      atomicMin(nan_first + piece * 32 + (thread >> 2), key0 + 16 * (thread & 3) + 4 * (i & 3) + ((__ffs(is) - 1) >> 3));
       *flag = 1;
     }
     if (is || zero) sts_u(at, zero ? 0 : word & ~((is >> 7) * 0xFFu));
   }
   tc::fence_async_smem();  // (the next copy goes to the same place)
-  asm volatile("bar.sync 1, 128;" ::: "memory");
+}
+// True when x is true for any of the widening warps' threads.
+__device__ __forceinline__ bool any_of_wideners(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
 }
 
 template <int D>
@@ -408,12 +424,13 @@ __device__ __forceinline__ void widen_items(const HeadsAttendParams& p, const It
 #pragma unroll 1
   for (uint32_t k = 0;; ++k) {
     const Item* it = take_item(items, k, bars, w);
+    if (any_of_wideners(w.dead)) {  // (all of them go on, or none: they have barriers of their own within an item)
+      w.dead = true;
+      break;
+    }
     if (!it) break;
     int* nan_first = reinterpret_cast<int*>(raw + L::kNan) + (k & 1) * D;
     int* flag = reinterpret_cast<int*>(raw + L::kFlag) + (k & 1);
-    for (int i = threadIdx.x & 127; i < D; i += 128) nan_first[i] = INT_MAX;
-    if ((threadIdx.x & 127) == 0) *flag = 0;
-    asm volatile("bar.sync 1, 128;" ::: "memory");
 #pragma unroll 1
     for (int t = 0; t < 2; ++t) {
       if (it->end[t] <= it->k0) continue;
@@ -944,7 +961,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const HeadsAttendPa
     if (warp >= kWidenWarp)
       widen_items<D>(p, items, smem, raw);
     else if (warp == kWalkWarp)
-      walk_items(p, start, limit, items, bars);
+      walk_items<D>(p, start, limit, raw, bars);
     else if (warp == kLoadWarp)
       load_items<D>(p, items, smem);
     else

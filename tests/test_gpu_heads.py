@@ -440,6 +440,11 @@ PROMPTS = [
     (1, 128, 2, torch.bfloat16, [50, 128, 129, 256, 300], [200, 128, 129, 128, 257]),
     (2, 64, 1, torch.float16, [1300], [1300]),
     (1, 128, 128, torch.bfloat16, [64, 640], [3, 1]),
+    # items of one query tile and of two in turn, with parts of a run, short and long
+    (2, 128, 1, torch.bfloat16, [3000, 500, 4000, 260, 900, 2100], [100, 400, 70, 256, 300, 128]),
+    (2, 64, 1, torch.bfloat16, [3000, 500, 4000, 260, 900, 2100], [100, 400, 70, 256, 300, 128]),
+    (4, 128, 4, torch.float16, [4000, 64, 130, 5000], [20, 64, 30, 25]),
+    (4, 64, 4, torch.float16, [4000, 64, 130, 5000], [20, 64, 30, 25]),
 ]
 
 
