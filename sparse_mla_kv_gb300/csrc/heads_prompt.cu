@@ -34,11 +34,10 @@ constexpr int kThreads = 16 * 32, kMmaWarp = 8, kLoadWarp = 10, kWalkWarp = 11, 
 constexpr int kTakers = 15;  // warps that the items are handed to
 constexpr int kRegsLaunch = 128, kRegsSoftmax = 200, kRegsOther = 56;
 static_assert(2 * kRegsSoftmax + 2 * kRegsOther <= 4 * kRegsLaunch, "more registers than the launch has");
-constexpr int kStaged = 4, kScales = 8;  // staged pages (a key tile's two of keys, then two of values); key tiles whose scales are kept
-static_assert(kStaged == 4, "a key tile's");
+constexpr int kScales = 8;  // key tiles whose scales are kept
 constexpr int kMinRun = 6;               // of a run, in key tiles: fewer would be mostly set-up and joining
 constexpr int kItemCost = 3;             // what an item costs beside its key tiles, in these
-enum Bar { kStFull = 0, kStEmpty = kStFull + kStaged, kKFull = kStEmpty + kStaged, kKEmpty = kKFull + 2, kVFull = kKEmpty + 2,
+enum Bar { kStFull = 0, kStEmpty = kStFull + 4, kKFull = kStEmpty + 4, kKEmpty = kKFull + 2, kVFull = kKEmpty + 2,
            kVEmpty = kVFull + 2, kQFull = kVEmpty + 2, kQEmpty = kQFull + 2, kSFull = kQEmpty + 2, kPReady = kSFull + 2,
            kODone = kPReady + 2, kSFree = kODone + 2, kItem = kSFree + 2, kItemDone = kItem + 2, kDrain = kItemDone + 2, kBars = kDrain + 2 };
 
@@ -105,7 +104,10 @@ struct Smem {
   static constexpr uint32_t kTo = kApart ? 384 : 256, kTp = kApart ? 256 : 0, kToStep = D, kTpStep = kApart ? 64 : 128;
   static constexpr int kStage = D * kHeadsPage;
   static constexpr int kQ = 0, kK = kQ + 2 * kUnits * kUnit, kV = kK + 2 * kUnits * kUnit, kVPage = D * 128;
-  static constexpr int kStages = kV + 4 * kVPage, kMisc = kStages + kStaged * kStage;
+  // Staged key tiles: of each, the keys of its two pages, then their values.  Barriers: keys and values of the even ones, of the
+  // odd ones.
+  static constexpr int kDepth = D == 64 ? 2 : 1, kTileStage = 4 * kStage;
+  static constexpr int kStages = kV + 4 * kVPage, kMisc = kStages + kDepth * kTileStage;
   // query scales (exponent fields, a byte each) [2][256], first NaNs (ints) [2][D], floats: page scales [kScales][8]
   static constexpr int kNan = kMisc + 2 * kBlock, kPage = kNan + 2 * D * 4, kFlag = kPage + kScales * 32, kItems = kFlag + 16, kBar = kItems + 2 * sizeof(Item);
   static constexpr int kBytes = kBar + kBars * 8;
@@ -195,7 +197,7 @@ __device__ __forceinline__ void load_items(const HeadsAttendParams& p, const Ite
   const uint32_t bars = smem + L::kBar;
   const int lane = threadIdx.x & 31;
   tc::Waiter w;
-  uint32_t tile = 0, part = 0;  // key tiles so far; of the next one, the pages that have been announced (a bit each)
+  uint32_t tile = 0, part = 0;  // key tiles so far; of the next one, what has been announced (a bit for keys, one for values)
 #pragma unroll 1
   for (uint32_t k = 0;; ++k) {
     const Item* item = take_item(items, k, bars, w);
@@ -231,30 +233,34 @@ __device__ __forceinline__ void load_items(const HeadsAttendParams& p, const Ite
       if (lane >= 2 && lane < 4) scale = log2f(scale);
       const uint32_t scales = smem + L::kPage + tile % kScales * 32;
       __syncwarp();
+      const uint32_t slot = tile % L::kDepth, use = tile / L::kDepth;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t bar = bars + 8 * (kStFull + i);
-        if (tile > 0) {
-          await(w, bars + 8 * (kStEmpty + i), (tile - 1) & 1);
+      for (int side = 0; side < 2; ++side) {
+        const uint32_t bar = bars + 8 * (kStFull + 2 * slot + side);
+        if (use > 0) {
+          await(w, bars + 8 * (kStEmpty + 2 * slot + side), (use - 1) & 1);
           // (complete by then, unless another warp's wait gave up: nothing is announced before the copy before has landed)
-          await(w, bar, (tile - 1) & 1);
+          await(w, bar, (use - 1) & 1);
         }
         if (w.dead) break;
-        if (i == 0) {
+        if (side == 0) {
           if (lane < 4) sts_u(scales + 4 * lane, __float_as_uint(scale));
           if (lane < 2) sts_u(scales + 16 + 4 * lane, is);
           __syncwarp();
         }
         if (lane == 0) {
-          if (there[i & 1]) {
-            const uint8_t* from = p.pages.codes(block[i & 1], head, D) + (i >> 1) * L::kStage;
-            tc::mbar_expect(bar, L::kStage);
-            bulk_copy(smem + L::kStages + i * L::kStage, from, L::kStage, bar);
+          if (there[0] || there[1]) {
+            tc::mbar_expect(bar, (there[0] + there[1]) * L::kStage);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              if (there[i])
+                bulk_copy(smem + L::kStages + slot * L::kTileStage + (2 * side + i) * L::kStage,
+                          p.pages.codes(block[i], head, D) + side * L::kStage, L::kStage, bar);
           } else {
             tc::mbar_arrive(bar);
           }
         }
-        part |= 1u << i;
+        part |= 1u << side;
         __syncwarp();
       }
       if (w.dead) break;
@@ -265,8 +271,8 @@ __device__ __forceinline__ void load_items(const HeadsAttendParams& p, const Ite
   // no copy is in flight when the CTA ends
   tc::Drain drain;
 #pragma unroll 1
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t n = tile + (part >> i & 1);
+  for (int i = 0; i < 2 * L::kDepth; ++i) {
+    const uint32_t n = (tile + (part >> (i & 1) & 1) + L::kDepth - 1 - (i >> 1)) / L::kDepth;
     if (n > 0) drain.wait(bars + 8 * (kStFull + i), (n - 1) & 1);
   }
   if (w.dead) report(p.a.status, HS_ERR_TIMEOUT);
@@ -442,24 +448,32 @@ __device__ __forceinline__ void widen_items(const HeadsAttendParams& p, const It
     const int all_see = item_sees(p, *it, it->col0), k0 = it->k0, k1 = it->k1;
 #pragma unroll 1
     for (int j = k0; j < k1; ++j, ++tile) {
-      const uint32_t buf = tile & 1, scales = smem + L::kPage + tile % kScales * 32;
+      const uint32_t buf = tile & 1, scales = smem + L::kPage + tile % kScales * 32, slot = tile % L::kDepth;
       const bool clean = (j + 1) * kKeys > all_see;
 #pragma unroll 1
-      for (int i = 0; i < 4; ++i) {  // (staging holds a key tile's four pages: slot i)
-        const int page = i & 1;
-        const bool values = i >= 2;
-        if (page == 0 && tile >= 2) await(w, bars + 8 * ((values ? kVEmpty : kKEmpty) + buf), (tile / 2 - 1) & 1);
-        await(w, bars + 8 * (kStFull + i), tile & 1);
-        const uint32_t from = smem + L::kStages + i * L::kStage;
-        const bool zero = lds_u(scales + 16 + 4 * page) == 0;
-        if (zero || (clean && values)) clean_staged<D>(from, zero, j * kKeys + page * kHeadsPage, nan_first, flag);
+      for (int side = 0; side < 2; ++side) {
+        if (tile >= 2) await(w, bars + 8 * ((side ? kVEmpty : kKEmpty) + buf), (tile / 2 - 1) & 1);
+        await(w, bars + 8 * (kStFull + 2 * slot + side), tile / L::kDepth & 1);
+        const uint32_t from = smem + L::kStages + slot * L::kTileStage + 2 * side * L::kStage;
+#pragma unroll 1
+        for (int page = 0; page < 2; ++page) {
+          const bool zero = lds_u(scales + 16 + 4 * page) == 0;
+          if (zero || (clean && side)) clean_staged<D>(from + page * L::kStage, zero, j * kKeys + page * kHeadsPage, nan_first, flag);
+        }
         // a page's keys: rows page * 64 .. of every 64 dimensions' unit; its values: a part of D rows of its own
-        const uint32_t to = smem + (values ? L::kV + (2 * buf + page) * L::kVPage : L::kK + buf * L::kUnits * L::kUnit + page * 8192);
-        widen<D>(from, to, values ? 64 * 128 : L::kUnit);
+        const uint32_t to = smem + (side ? L::kV + 2 * buf * L::kVPage : L::kK + buf * L::kUnits * L::kUnit);
+        const int page_step = side ? L::kVPage : 8192, step = side ? 64 * 128 : L::kUnit;
+        if constexpr (D == 64) {
+          widen<D>(from, to, step);
+          widen<D>(from + L::kStage, to + page_step, step);
+        } else {
+#pragma unroll 1
+          for (int page = 0; page < 2; ++page) widen<D>(from + page * L::kStage, to + page * page_step, step);
+        }
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(bars + 8 * (kStEmpty + i));
-        if (page == 1) arrive((values ? kVFull : kKFull) + buf);
-        if (i == 1 && j == k0) {  // (the first keys were widened while the queries were on their way)
+        if (lane == 0) tc::mbar_arrive(bars + 8 * (kStEmpty + 2 * slot + side));
+        arrive((side ? kVFull : kKFull) + buf);
+        if (side == 0 && j == k0) {  // (the first keys were widened while the queries were on their way)
           asm volatile("cp.async.wait_group 0;\n\tbar.sync 1, 128;" ::: "memory");
 #pragma unroll 1
           for (int t = 0; t < 2; ++t) {
@@ -927,7 +941,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const HeadsAttendPa
   static_assert(sizeof(Scratch) <= 2 * kBlock, "scratch");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(raw + L::kFlag) + 2;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStaged; ++i) tc::mbar_init(bars + 8 * (kStFull + i), 1), tc::mbar_init(bars + 8 * (kStEmpty + i), 4);
+    for (int i = 0; i < 4; ++i) tc::mbar_init(bars + 8 * (kStFull + i), 1), tc::mbar_init(bars + 8 * (kStEmpty + i), 4);
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(bars + 8 * (kKFull + i), 4);
       tc::mbar_init(bars + 8 * (kKEmpty + i), 2);
