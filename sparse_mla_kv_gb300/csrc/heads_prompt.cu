@@ -39,7 +39,7 @@ constexpr int kMinRun = 6;               // of a run, in key tiles: fewer would 
 constexpr int kItemCost = 3;             // what an item costs beside its key tiles, in these
 enum Bar { kStFull = 0, kStEmpty = kStFull + 4, kKFull = kStEmpty + 4, kKEmpty = kKFull + 2, kVFull = kKEmpty + 2,
            kVEmpty = kVFull + 2, kQFull = kVEmpty + 2, kQEmpty = kQFull + 2, kSFull = kQEmpty + 2, kPReady = kSFull + 2,
-           kODone = kPReady + 2, kSFree = kODone + 2, kItem = kSFree + 2, kItemDone = kItem + 2, kDrain = kItemDone + 2, kBars = kDrain + 2 };
+           kPHalf = kPReady + 2, kODone = kPHalf + 2, kSFree = kODone + 2, kItem = kSFree + 2, kItemDone = kItem + 2, kDrain = kItemDone + 2, kBars = kDrain + 2 };
 
 // Workspace: header, a record a CTA, statistics [CTA][2][256][4], results [CTA][2][D / 4][256][4].
 __host__ __device__ constexpr size_t ws_stats_offset(int ctas) { return sizeof(RunHeader) + (size_t)ctas * sizeof(RunRecord); }
@@ -102,6 +102,10 @@ struct Smem {
   // scores are made while the weights are; else in S's place.
   static constexpr bool kApart = D == 64;
   static constexpr uint32_t kTo = kApart ? 384 : 256, kTp = kApart ? 256 : 0, kToStep = D, kTpStep = kApart ? 64 : 128;
+  // The first page's weights are handed over while the second's are made: where P has S's place, the next scores wait for the
+  // products (2048 rows behind 16000 tokens, 4 heads x 8: 383 -> 367 us).  Where they do not, it costs more than it gives (240 ->
+  // 256 us).
+  static constexpr bool kHalves = !kApart;
   static constexpr int kStage = D * kHeadsPage;
   static constexpr int kQ = 0, kK = kQ + 2 * kUnits * kUnit, kV = kK + 2 * kUnits * kUnit, kVPage = D * 128;
   // Staged key tiles: of each, the keys of its two pages, then their values.  Barriers: keys and values of the even ones, of the
@@ -545,9 +549,9 @@ __device__ __forceinline__ void issue_items(const HeadsAttendParams& p, const It
         scores(j + 1);
       }
       wait(kVFull + buf, n / 2 & 1);
-      wait(kPReady + t, phase & 1);
 #pragma unroll
       for (int page = 0; page < 2; ++page) {
+        if (L::kHalves || page == 0) wait((L::kHalves && page == 0 ? kPHalf : kPReady) + t, phase & 1);
         const uint64_t db = dv + (uint32_t)((2 * buf + page) * L::kVPage >> 4);
         // P: 16 tokens are 8 columns
 #pragma unroll
@@ -582,6 +586,24 @@ __device__ __forceinline__ void issue_items(const HeadsAttendParams& p, const It
 }
 
 // ---- softmax and results (128 threads a query tile) ----
+// 64 columns of tensor memory, a row a thread.
+__device__ __forceinline__ void load64(uint32_t a, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(a));
+}
 template <int D>
 __device__ __forceinline__ void softmax_items(const HeadsAttendParams& p, const Item* items, uint32_t smem, const uint8_t* raw, uint32_t tmem) {
   using L = Smem<D>;
@@ -613,7 +635,9 @@ __device__ __forceinline__ void softmax_items(const HeadsAttendParams& p, const 
       if (j == k0) qs = scale * power_of_field(raw[L::kMisc + (k & 1) * kBlock + row]);
       const uint32_t scales = smem + L::kPage + (before + j - k0) % kScales * 32;
       float s[128];
-      tc::tmem_ld<128>(ts, s);
+      // (in few, wide loads: 2048 rows behind 16000 tokens, 4 heads of 64 dimensions x 8: 247 us by sixteens, 232 us so)
+      load64(ts, s);
+      load64(ts + 64, s + 64);
       const float size[2] = {lds_f(scales + 8), lds_f(scales + 12)};
       float c[2];
 #pragma unroll
@@ -686,27 +710,26 @@ __device__ __forceinline__ void softmax_items(const HeadsAttendParams& p, const 
         if (top[i] + size[i] < r - kFar) bias = top[i] < -2.f * kLarge ? -INFINITY : -kFar - top[i];
         const float2 c2 = make_float2(c[i], c[i]), b2 = make_float2(bias, bias);
         float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+        uint32_t pk[32];
 #pragma unroll
-        for (int x = 0; x < 64; x += 32) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int y = 0; y < 16; ++y) {
-            const float2 z = tc::fma2(make_float2(s[64 * i + x + 2 * y], s[64 * i + x + 2 * y + 1]), c2, b2);
-            const float2 e = make_float2(tc::exp2_fast(z.x), tc::exp2_fast(z.y));
-            if (y & 1)
-              sum1 = tc::add2(sum1, e);
-            else
-              sum0 = tc::add2(sum0, e);
-            pk[y] = pack_half(e.x, e.y);
-          }
-          tc::tmem_st16(tp + (64 * i + x) / 2, reinterpret_cast<const float*>(pk));
+        for (int y = 0; y < 32; ++y) {
+          const float2 z = tc::fma2(make_float2(s[64 * i + 2 * y], s[64 * i + 2 * y + 1]), c2, b2);
+          const float2 e = make_float2(tc::exp2_fast(z.x), tc::exp2_fast(z.y));
+          if (y & 1)
+            sum1 = tc::add2(sum1, e);
+          else
+            sum0 = tc::add2(sum0, e);
+          pk[y] = pack_half(e.x, e.y);
         }
+        tc::tmem_st16(tp + 32 * i, reinterpret_cast<const float*>(pk));
+        tc::tmem_st16(tp + 32 * i + 16, reinterpret_cast<const float*>(pk + 16));
         if (bias != -INFINITY) l += ((sum0.x + sum0.y) + (sum1.x + sum1.y)) * tc::exp2_fast(-bias - m);
+        if (i == 0 && !L::kHalves) continue;
+        tc::tmem_wait_st();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bars + 8 * ((i ? kPReady : kPHalf) + t));
       }
-      tc::tmem_wait_st();
-      tc::fence_before();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(bars + 8 * (kPReady + t));
     }
     // results
     const bool work = end > k0, whole = k0 == 0 && it->k1 == it->tiles;
@@ -951,6 +974,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const HeadsAttendPa
       tc::mbar_init(bars + 8 * (kQEmpty + i), 1);
       tc::mbar_init(bars + 8 * (kSFull + i), 1);
       tc::mbar_init(bars + 8 * (kPReady + i), 4);
+      tc::mbar_init(bars + 8 * (kPHalf + i), 4);
       tc::mbar_init(bars + 8 * (kODone + i), 1);
       tc::mbar_init(bars + 8 * (kSFree + i), 4);
       tc::mbar_init(bars + 8 * (kItem + i), 1);
