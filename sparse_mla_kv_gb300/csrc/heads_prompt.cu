@@ -35,7 +35,7 @@ constexpr int kTakers = 15;  // warps that the items are handed to
 constexpr int kRegsLaunch = 128, kRegsSoftmax = 200, kRegsOther = 56;
 static_assert(2 * kRegsSoftmax + 2 * kRegsOther <= 4 * kRegsLaunch, "more registers than the launch has");
 constexpr int kScales = 8;  // key tiles whose scales are kept
-constexpr int kMinRun = 6;               // of a run, in key tiles: fewer would be mostly set-up and joining
+constexpr int kMinRun = 4;               // of a run, in key tiles: fewer would be mostly set-up and joining (100 tokens, 2 x 4 heads: 24 us; 34 us with 6)
 constexpr int kItemCost = 3;             // what an item costs beside its key tiles, in these
 enum Bar { kStFull = 0, kStEmpty = kStFull + 4, kKFull = kStEmpty + 4, kKEmpty = kKFull + 2, kVFull = kKEmpty + 2,
            kVEmpty = kVFull + 2, kQFull = kVEmpty + 2, kQEmpty = kQFull + 2, kSFull = kQEmpty + 2, kPReady = kSFull + 2,
@@ -1014,61 +1014,51 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const HeadsAttendPa
   }
 }
 
-// Joins the parts of items that several runs share: a block takes 32 rows of a cut item, a thread D / 8 dimensions of one, and
-// four parts at a time, so that their loads are on their way together.
-constexpr int kJoinThreads = 256, kJoinRows = 32, kJoinParts = 4, kMaxCtas = 512;
+// Joins the parts of items that several runs share, four at a time, so that their loads are on their way together.  A thread has
+// D / 8 dimensions (its warp's) of a row.  A block takes 32 rows of a cut item; where there are more than kFewParts, 8 rows, whose
+// parts its lanes share out.
+constexpr int kJoinThreads = 256, kJoinRows = 32, kJoinFewRows = 8, kJoinParts = 4, kFewParts = 16, kMaxCtas = 512;
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const HeadsAttendParams p, int ctas) {
-  constexpr int kVecs = D / 32;  // float4 a thread
-  __shared__ CutLists<kJoinThreads, kMaxCtas> cuts;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // for the results of prompt_kernel
-  const uint8_t* ws = reinterpret_cast<const uint8_t*>(p.workspace);
-  const RunHeader header = *reinterpret_cast<const RunHeader*>(ws);
-  const RunRecord* records = reinterpret_cast<const RunRecord*>(ws + sizeof(RunHeader));
-  const float4* stats = reinterpret_cast<const float4*>(ws + ws_stats_offset(ctas));
-  const float4* parts = reinterpret_cast<const float4*>(ws + ws_parts_offset(ctas));
-  int n[2];
-  cuts.build(records, ctas, header.run, kMaxCtas, n);
-  constexpr int kGroups = kBlock / kJoinRows;
-  const int piece = warp;  // of 8
-  for (int item = blockIdx.x; item < n[0] * kGroups; item += gridDim.x) {
-    const int i = cuts.at[0][item / kGroups], row = item % kGroups * kJoinRows + lane;
-    const RunRecord rec = records[i];
-    if (row >= rec.cols) continue;
-    const int last = (int)((rec.end - 1) / header.run);
-    const int slot0 = rec.begin > i * header.run ? 1 : 0;
-    Joined res;
-    float4 acc[kVecs];
+struct JoinedRow {
+  static constexpr int kVecs = D / 32;  // float4 a thread
+  Joined all;
+  float4 acc[kVecs];
+  __device__ __forceinline__ void add(float4 st, const float4* y) {
+    if (st.y == -INFINITY) return;  // (a part of which the row sees nothing)
+    const float2 f = all.join(st);
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) {
+      acc[v].x = acc[v].x * f.x + f.y * y[v].x, acc[v].y = acc[v].y * f.x + f.y * y[v].y;
+      acc[v].z = acc[v].z * f.x + f.y * y[v].z, acc[v].w = acc[v].w * f.x + f.y * y[v].w;
+    }
+  }
+  // Parts first, first + step, .. of the item whose parts are i .. last.
+  __device__ __forceinline__ void join(const float4* stats, const float4* parts, int i, int slot0, int first, int step, int last, int row, int piece) {
+    all = Joined{};
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int x0 = i; x0 <= last; x0 += kJoinParts) {
+    for (int x0 = first; x0 <= last; x0 += kJoinParts * step) {
       float4 st[kJoinParts], y[kJoinParts][kVecs];
 #pragma unroll
       for (int x = 0; x < kJoinParts; ++x) {
-        if (x0 + x > last) continue;
-        const int64_t slot = (int64_t)(x0 + x) * 2 + (x0 + x == i ? slot0 : 0);
+        const int part = x0 + x * step;
+        if (part > last) continue;
+        const int64_t slot = (int64_t)part * 2 + (part == i ? slot0 : 0);
         st[x] = stats[slot * kBlock + row];
 #pragma unroll
         for (int v = 0; v < kVecs; ++v) y[x][v] = parts[(slot * (D / 4) + piece * kVecs + v) * kBlock + row];
       }
 #pragma unroll
-      for (int x = 0; x < kJoinParts; ++x) {
-        if (x0 + x > last || st[x].y == -INFINITY) continue;  // (a part of which the row sees nothing)
-        const float2 f = res.join(st[x]);
-        const float a = f.x, b = f.y;
-#pragma unroll
-        for (int v = 0; v < kVecs; ++v) {
-          acc[v].x = acc[v].x * a + b * y[x][v].x, acc[v].y = acc[v].y * a + b * y[x][v].y;
-          acc[v].z = acc[v].z * a + b * y[x][v].z, acc[v].w = acc[v].w * a + b * y[x][v].w;
-        }
-      }
+      for (int x = 0; x < kJoinParts; ++x)
+        if (x0 + x * step <= last) add(st[x], y[x]);
     }
-    const float up = res.l == 0.f ? 0.f : exp2f(0.5f * (res.ref - res.m)), inv = res.l == 0.f ? 0.f : up / res.l;
+  }
+  __device__ __forceinline__ void store(const HeadsAttendParams& p, const RunRecord& rec, int row, int piece) const {
+    const float up = all.l == 0.f ? 0.f : exp2f(0.5f * (all.ref - all.m)), inv = all.l == 0.f ? 0.f : up / all.l;
     const int col = rec.group * kBlock + row, in_token = col / p.group;
     const int64_t token = rec.t0 + in_token;
     const int head = rec.head * p.group + col - in_token * p.group;
-    if (!HS_CHECK(token < p.a.n && head < p.a.q_heads, kChkOutPos)) continue;
+    if (!HS_CHECK(token < p.a.n && head < p.a.q_heads, kChkOutPos)) return;
     const bool f16 = p.a.dtype == HS_FP16;
     uint16_t* out = static_cast<uint16_t*>(p.a.out) + token * p.a.out_token_stride + head * p.a.out_head_stride + piece * (D / 8);
 #pragma unroll
@@ -1077,7 +1067,54 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const HeadsAt
           pack(f16, acc[v].x * up * inv, acc[v].y * up * inv), pack(f16, acc[v].z * up * inv, acc[v].w * up * inv),
           pack(f16, acc[v + 1].x * up * inv, acc[v + 1].y * up * inv), pack(f16, acc[v + 1].z * up * inv, acc[v + 1].w * up * inv));
     if (piece == 0 && p.a.lse)
-      p.a.lse[token * p.a.q_heads + head] = res.l == 0.f ? -INFINITY : (res.anchor + (res.m + log2f(res.l))) * kLn2;
+      p.a.lse[token * p.a.q_heads + head] = all.l == 0.f ? -INFINITY : (all.anchor + (all.m + log2f(all.l))) * kLn2;
+  }
+};
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const HeadsAttendParams p, int ctas) {
+  __shared__ CutLists<kJoinThreads, kMaxCtas> cuts;
+  const int lane = threadIdx.x & 31, piece = threadIdx.x >> 5;  // (of 8)
+  asm volatile("griddepcontrol.wait;" ::: "memory");            // for the results of prompt_kernel
+  const uint8_t* ws = reinterpret_cast<const uint8_t*>(p.workspace);
+  const RunHeader header = *reinterpret_cast<const RunHeader*>(ws);
+  const RunRecord* records = reinterpret_cast<const RunRecord*>(ws + sizeof(RunHeader));
+  const float4* stats = reinterpret_cast<const float4*>(ws + ws_stats_offset(ctas));
+  const float4* parts = reinterpret_cast<const float4*>(ws + ws_parts_offset(ctas));
+  int n[2];
+  cuts.build(records, ctas, header.run, kFewParts, n);
+  JoinedRow<D> mine;
+  constexpr int kGroups = kBlock / kJoinRows, kFewGroups = kBlock / kJoinFewRows;
+  for (int item = blockIdx.x; item < n[0] * kGroups; item += gridDim.x) {
+    const int i = cuts.at[0][item / kGroups], row = item % kGroups * kJoinRows + lane;
+    const RunRecord rec = records[i];
+    if (row >= rec.cols) continue;
+    mine.join(stats, parts, i, rec.begin > i * header.run ? 1 : 0, i, 1, (int)((rec.end - 1) / header.run), row, piece);
+    mine.store(p, rec, row, piece);
+  }
+  for (int item = blockIdx.x; item < n[1] * kFewGroups; item += gridDim.x) {
+    constexpr int kShares = 32 / kJoinFewRows;
+    const int i = cuts.at[1][item / kFewGroups], row = item % kFewGroups * kJoinFewRows + lane % kJoinFewRows;
+    const RunRecord rec = records[i];
+    const bool there = row < rec.cols;
+    mine.join(stats, parts, i, rec.begin > i * header.run ? 1 : 0, i + lane / kJoinFewRows, kShares,
+              there ? (int)((rec.end - 1) / header.run) : -1, row, piece);
+    // the shares are joined in their order, by all lanes of the row
+    JoinedRow<D> row_of;
+    row_of.all = Joined{};
+#pragma unroll
+    for (int v = 0; v < JoinedRow<D>::kVecs; ++v) row_of.acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int x = 0; x < kShares; ++x) {
+      const int from = x * kJoinFewRows + lane % kJoinFewRows;
+      auto of = [&](float f) { return __shfl_sync(0xFFFFFFFFu, f, from); };
+      const float4 st = make_float4(of(mine.all.ref), of(mine.all.m), of(mine.all.l), of(mine.all.anchor));
+      float4 y[JoinedRow<D>::kVecs];
+#pragma unroll
+      for (int v = 0; v < JoinedRow<D>::kVecs; ++v)
+        y[v] = make_float4(of(mine.acc[v].x), of(mine.acc[v].y), of(mine.acc[v].z), of(mine.acc[v].w));
+      row_of.add(st, y);
+    }
+    if (there && lane < kJoinFewRows) row_of.store(p, rec, row, piece);
   }
 }
 

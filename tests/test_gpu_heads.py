@@ -445,6 +445,9 @@ PROMPTS = [
     (2, 64, 1, torch.bfloat16, [3000, 500, 4000, 260, 900, 2100], [100, 400, 70, 256, 300, 128]),
     (4, 128, 4, torch.float16, [4000, 64, 130, 5000], [20, 64, 30, 25]),
     (4, 64, 4, torch.float16, [4000, 64, 130, 5000], [20, 64, 30, 25]),
+    # items of many parts, beside some of few
+    (1, 128, 8, torch.bfloat16, [20000, 900], [40, 17]),
+    (2, 64, 5, torch.float16, [17001, 13], [27, 13]),
 ]
 
 
