@@ -395,15 +395,23 @@ template <int D>
 __device__ __forceinline__ void clean_staged(uint32_t from, bool zero, int key0, int* nan_first, int* flag) {
   const int thread = threadIdx.x & 127;
 #pragma unroll 1
-  for (int i = 0; i < D / 8; ++i) {  // words of this thread
-    const int piece = i >> 2;
-    const uint32_t at = from + piece * 2048 + thread * 16 + (i & 3) * 4;
-    const uint32_t word = lds_u(at), is = zero ? 0 : nan_codes(word);
-    if (is) {
-      atomicMin(nan_first + piece * 32 + (thread >> 2), key0 + 16 * (thread & 3) + 4 * (i & 3) + ((__ffs(is) - 1) >> 3));
+  for (int i = 0; i < D / 32; ++i) {
+    const uint32_t at = from + i * 2048 + thread * 16;
+    uint4 v = lds16(at);
+    if (zero) {
+      v = make_uint4(0, 0, 0, 0);
+    } else {
+      if (!(nan_codes(v.x) | nan_codes(v.y) | nan_codes(v.z) | nan_codes(v.w))) continue;
+      auto word = [&](uint32_t& w, int x) {
+        const uint32_t is = nan_codes(w);
+        if (!is) return;
+        atomicMin(nan_first + i * 32 + (thread >> 2), key0 + 16 * (thread & 3) + 4 * x + ((__ffs(is) - 1) >> 3));
+        w &= ~((is >> 7) * 0xFFu);
+      };
+      word(v.x, 0), word(v.y, 1), word(v.z, 2), word(v.w, 3);
       *flag = 1;
     }
-    if (is || zero) sts_u(at, zero ? 0 : word & ~((is >> 7) * 0xFFu));
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
   }
   tc::fence_async_smem();  // (the next copy goes to the same place)
 }
@@ -770,58 +778,29 @@ __device__ __forceinline__ void softmax_items(const HeadsAttendParams& p, const 
       if (threadIdx.x == 0 && k0 == 0)
         *record() = RunRecord{it->begin, it->begin + it->tiles, it->t0, it->head, it->col0 / kBlock, it->rows};
     } else {
-      // Rows are stored by four lanes each, 64 bytes at a time: of each 8 dimensions a lane is given two of four rows, and the four
-      // lanes of a row change places so that each has 8 dimensions of its own.
-      const int warp_row = row & ~31, g = lane >> 2, t4 = lane & 3;
-      uint16_t* out[4];
-      float f0[4], f1[4];
-      int seen[4];
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        const int r = warp_row + 8 * y + g, c = it->col0 + r, token = c / p.group, head = it->head * p.group + c - token * p.group;
-        const bool writes = r < it->rows && HS_CHECK(it->t0 + token < p.a.n && head < p.a.q_heads, kChkOutPos);
-        out[y] = writes ? static_cast<uint16_t*>(p.a.out) + (it->t0 + token) * p.a.out_token_stride + head * p.a.out_head_stride + 8 * t4
-                        : nullptr;
-        f0[y] = __shfl_sync(0xFFFFFFFFu, up, 8 * y + g), f1[y] = __shfl_sync(0xFFFFFFFFu, inv, 8 * y + g);
-        seen[y] = __shfl_sync(0xFFFFFFFFu, sees, 8 * y + g);
-      }
+      const int c = it->col0 + row, token = c / p.group, head = it->head * p.group + c - token * p.group;
+      const bool writes = there && HS_CHECK(it->t0 + token < p.a.n && head < p.a.q_heads, kChkOutPos);
+      uint16_t* out = static_cast<uint16_t*>(p.a.out) + (it->t0 + token) * p.a.out_token_stride + head * p.a.out_head_stride;
+      const bool some = work && up != 0.f;
 #pragma unroll 1
-      for (int x = 0; x < D; x += 32) {
-        float o[2][16];
+      for (int x = 0; x < D; x += 16) {
+        float o[16];
         if (work) {
-          tc::tmem_ld_rows16<4>(to + x, o[0]);
-          tc::tmem_ld_rows16<4>(to + (16u << 16) + x, o[1]);
+          tc::tmem_ld16(to + x, o);
           tc::tmem_wait_ld();
-          tc::touch<16>(o[0]);
-          tc::touch<16>(o[1]);
+          tc::touch<16>(o);
         }
+        if (nans) {
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          uint32_t v[4];
+          for (int y = 0; y < 16; ++y)
+            if (sees > nan_first[x + y]) o[y] = __uint_as_float(0x7FC00000u);
+        }
+        uint32_t v[8];
 #pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            float a = o[y >> 1][4 * n + 2 * (y & 1)], b = o[y >> 1][4 * n + 2 * (y & 1) + 1];
-            if (nans) {
-              if (seen[y] > nan_first[x + 8 * n + 2 * t4]) a = __uint_as_float(0x7FC00000u);
-              if (seen[y] > nan_first[x + 8 * n + 2 * t4 + 1]) b = __uint_as_float(0x7FC00000u);
-            }
-            a = work && f0[y] != 0.f ? a * f0[y] * f1[y] : 0.f, b = work && f0[y] != 0.f ? b * f0[y] * f1[y] : 0.f;
-            v[n] = pack(f16, a, b);
-          }
-#pragma unroll
-          for (int d = 1; d <= 2; d *= 2) {
-            const bool odd = t4 & d;
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              const int lo = d == 1 ? 2 * n : n, hi = lo + d;
-              const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[lo] : v[hi], d);
-              if (odd)
-                v[lo] = got;
-              else
-                v[hi] = got;
-            }
-          }
-          if (out[y]) *reinterpret_cast<uint4*>(out[y] + x) = make_uint4(v[0], v[1], v[2], v[3]);
+        for (int y = 0; y < 8; ++y) v[y] = pack(f16, some ? o[2 * y] * up * inv : 0.f, some ? o[2 * y + 1] * up * inv : 0.f);
+        if (writes) {
+          *reinterpret_cast<uint4*>(out + x) = make_uint4(v[0], v[1], v[2], v[3]);
+          *reinterpret_cast<uint4*>(out + x + 8) = make_uint4(v[4], v[5], v[6], v[7]);
         }
       }
       if (there && p.a.lse) {
