@@ -7,19 +7,29 @@
 //
 // Layout.  A work item is (request, head of keys and values, 256 columns): two tiles of 128 columns (query token x query head of
 // the group, token by token) over the same key tiles of 128 tokens (two pages), so that a page widened serves 256 rows.  The
-// key tiles of all items are numbered (with something added for each item), and every CTA takes an equal run of them, whatever the contexts' lengths and the causal
-// mask leave; items that are cut leave partial results in the workspace, which prompt_join_kernel joins in a fixed order.
+// key tiles of all items are numbered (with something added for each item), and every CTA takes an equal run of them, whatever the
+// contexts' lengths and the causal mask leave; items that are cut leave partial results in the workspace, which prompt_join_kernel
+// joins in a fixed order.
 // 16 warps, one CTA per SM (the warpgroups trade registers):
 //   warps 0-3, 4-7   softmax and results of query tile 0 and 1, a row a thread;
 //   warps 8, 9       issue the products of query tile 0 and 1;
-//   warp 10          copies codes into staging (a page's keys or values at a time) and reads the pages' scales;
+//   warp 10          copies codes into staging (a key tile's keys or values at a time) and reads the pages' scales;
 //   warp 11          finds the run's items and hands them to the others, two at a time;
 //   warps 12-15      widen the codes to fp16, into the operands' places, and bring the queries there.
-// Shared memory: queries, two key tiles and two value tiles in fp16 (64 KB each for 128 dimensions), three staged pages of codes.
-// Tensor memory: S and O of both query tiles; P, in fp16, takes S's place and is the left operand of the second product there.
+// Shared memory: queries, two key tiles and two value tiles in fp16 (64 KB each for 128 dimensions), and the codes of the next key
+// tile (of the next two for 64 dimensions).  Tensor memory: S and O of both query tiles, and P, in fp16, the left operand of the
+// second product: in S's place for 128 dimensions, in one of its own for 64.
 // A value's NaN must not reach rows that do not see its token, and a weight of zero does not keep it from them: where a key tile
 // is not seen whole by all rows, the widening warps put zero for it and note, by dimension, the first such token; rows that see
 // it get their NaN at the end.
+//
+// What bounds it.  The products, 512 D operations a row and key tile, would take 291 us for 8192 tokens with 8 x 4 heads of 128
+// dimensions at 1887 TFLOP/s, the reads nothing to speak of; measured 495 us, 1110 TFLOP/s.  A key tile takes about 3500 cycles of
+// the SM: 2160 of products, 2600 of shared memory's bandwidth (the right operands are read for each query tile, the widened codes
+// written once), 1024 of exponentials, and what a query tile's chain of products, maximum, exponentials and products again
+// leaves idle, which two query tiles in turn cover in part.  For 64 dimensions the exponentials weigh twice as much: 356 us
+// for the same prompt, 774 TFLOP/s.  Instructions are fetched anew where an item begins and ends, so that short code counts there:
+// 16 values unrolled instead of whole rows took 14 us from 522.  The smallest prompts (100 tokens, 2 x 4 heads) take 20 us.
 #include "heads_device.cuh"
 
 HS_CHECK_WORD
@@ -32,14 +42,22 @@ using namespace heads;
 constexpr int kQRows = 128, kKeys = 128, kBlock = 2 * kQRows;
 constexpr int kThreads = 16 * 32, kMmaWarp = 8, kLoadWarp = 10, kWalkWarp = 11, kWidenWarp = 12;
 constexpr int kTakers = 15;  // warps that the items are handed to
-constexpr int kRegsLaunch = 128, kRegsSoftmax = 200, kRegsOther = 56;
-static_assert(2 * kRegsSoftmax + 2 * kRegsOther <= 4 * kRegsLaunch, "more registers than the launch has");
+constexpr int kRegsLaunch = 128;
+// Registers after the trade, of the softmax warps and of the others.  8192 tokens, 8 x 4 heads of 128 dimensions: 522 us with 200 and
+// 56, 495 us with 192 and 64, 496 with 184 and 72, 503 with 176 and 80; 2048 rows behind 16000, 4 x 8 heads of 64: 230, 235, 239, 247.
+template <int D>
+struct Regs {
+  static constexpr int kSoftmax = D == 64 ? 200 : 192, kOther = D == 64 ? 56 : 64;
+  static_assert(2 * kSoftmax + 2 * kOther <= 4 * kRegsLaunch, "more registers than the launch has");
+};
 constexpr int kScales = 8;  // key tiles whose scales are kept
-constexpr int kMinRun = 4;               // of a run, in key tiles: fewer would be mostly set-up and joining (100 tokens, 2 x 4 heads: 24 us; 34 us with 6)
-constexpr int kItemCost = 3;             // what an item costs beside its key tiles, in these
+// What an item costs beside its key tiles, in these (12000 tokens, 4 x 3 heads of 64: 283 us; 301 us with 2, 284 us with 4), and the
+// least of a run: fewer would be mostly set-up and joining (100 tokens, 2 x 4 heads: 24 us with 4, 34 us with 6).
+constexpr int kItemCost = 3, kMinRun = 4;
 enum Bar { kStFull = 0, kStEmpty = kStFull + 4, kKFull = kStEmpty + 4, kKEmpty = kKFull + 2, kVFull = kKEmpty + 2,
            kVEmpty = kVFull + 2, kQFull = kVEmpty + 2, kQEmpty = kQFull + 2, kSFull = kQEmpty + 2, kPReady = kSFull + 2,
-           kPHalf = kPReady + 2, kODone = kPHalf + 2, kSFree = kODone + 2, kItem = kSFree + 2, kItemDone = kItem + 2, kDrain = kItemDone + 2, kBars = kDrain + 2 };
+           kPHalf = kPReady + 2, kODone = kPHalf + 2, kSFree = kODone + 2, kItem = kSFree + 2, kItemDone = kItem + 2,
+           kDrain = kItemDone + 2, kBars = kDrain + 2 };
 
 // Workspace: header, a record a CTA, statistics [CTA][2][256][4], results [CTA][2][D / 4][256][4].
 __host__ __device__ constexpr size_t ws_stats_offset(int ctas) { return sizeof(RunHeader) + (size_t)ctas * sizeof(RunRecord); }
@@ -475,13 +493,8 @@ __device__ __forceinline__ void widen_items(const HeadsAttendParams& p, const It
         // a page's keys: rows page * 64 .. of every 64 dimensions' unit; its values: a part of D rows of its own
         const uint32_t to = smem + (side ? L::kV + 2 * buf * L::kVPage : L::kK + buf * L::kUnits * L::kUnit);
         const int page_step = side ? L::kVPage : 8192, step = side ? 64 * 128 : L::kUnit;
-        if constexpr (D == 64) {
-          widen<D>(from, to, step);
-          widen<D>(from + L::kStage, to + page_step, step);
-        } else {
-#pragma unroll 1
-          for (int page = 0; page < 2; ++page) widen<D>(from + page * L::kStage, to + page * page_step, step);
-        }
+        widen<D>(from, to, step);
+        widen<D>(from + L::kStage, to + page_step, step);
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bars + 8 * (kStEmpty + 2 * slot + side));
         arrive((side ? kVFull : kKFull) + buf);
@@ -971,10 +984,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const HeadsAttendPa
   const uint32_t tmem = *tmem_slot;
   Item* items = reinterpret_cast<Item*>(raw + L::kItems);
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<D>::kSoftmax));
     softmax_items<D>(p, items, smem, raw, tmem);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<D>::kOther));
     if (warp >= kWidenWarp)
       widen_items<D>(p, items, smem, raw);
     else if (warp == kWalkWarp)
