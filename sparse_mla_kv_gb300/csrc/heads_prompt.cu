@@ -1006,10 +1006,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const HeadsAttendPa
   }
 }
 
-// Joins the parts of items that several runs share, four at a time, so that their loads are on their way together.  A thread has
-// D / 8 dimensions (its warp's) of a row.  A block takes 32 rows of a cut item; where there are more than kFewParts, 8 rows, whose
-// parts its lanes share out.
-constexpr int kJoinThreads = 256, kJoinRows = 32, kJoinFewRows = 8, kJoinParts = 4, kFewParts = 16, kMaxCtas = 512;
+// Joins the parts of items that several runs share, two at a time, so that their loads are on their way together (four take
+// registers that more blocks need: 2 chunks of 512 behind 8000, 4 x 8 heads, 117 and 110 us).  A thread has D / 8 dimensions (its
+// warp's) of a row.  A block takes 32 rows of a cut item; where there are more than kFewParts, 8 rows, whose parts its lanes share
+// out (64 tokens behind 16000, 1 x 2 heads, 21 parts: 27 us, 34 us without; with 10 parts, 8 x 8 heads, 62 and 53 us).
+constexpr int kJoinThreads = 256, kJoinRows = 32, kJoinFewRows = 8, kJoinParts = 2, kFewParts = 16, kMaxCtas = 512;
 template <int D>
 struct JoinedRow {
   static constexpr int kVecs = D / 32;  // float4 a thread
@@ -1025,7 +1026,8 @@ struct JoinedRow {
     }
   }
   // Parts first, first + step, .. of the item whose parts are i .. last.
-  __device__ __forceinline__ void join(const float4* stats, const float4* parts, int i, int slot0, int first, int step, int last, int row, int piece) {
+  __device__ __forceinline__ void join(const float4* stats, const float4* parts, int i, int slot0, int first, int step, int last,
+                                       int row, int piece) {
     all = Joined{};
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1063,7 +1065,7 @@ struct JoinedRow {
   }
 };
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const HeadsAttendParams p, int ctas) {
+__global__ void __launch_bounds__(kJoinThreads, 2) prompt_join_kernel(const HeadsAttendParams p, int ctas) {
   __shared__ CutLists<kJoinThreads, kMaxCtas> cuts;
   const int lane = threadIdx.x & 31, piece = threadIdx.x >> 5;  // (of 8)
   asm volatile("griddepcontrol.wait;" ::: "memory");            // for the results of prompt_kernel
@@ -1090,23 +1092,18 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const HeadsAt
     const bool there = row < rec.cols;
     mine.join(stats, parts, i, rec.begin > i * header.run ? 1 : 0, i + lane / kJoinFewRows, kShares,
               there ? (int)((rec.end - 1) / header.run) : -1, row, piece);
-    // the shares are joined in their order, by all lanes of the row
-    JoinedRow<D> row_of;
-    row_of.all = Joined{};
+    // the shares are joined two and two; what the upper lanes make of them is not used
 #pragma unroll
-    for (int v = 0; v < JoinedRow<D>::kVecs; ++v) row_of.acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int x = 0; x < kShares; ++x) {
-      const int from = x * kJoinFewRows + lane % kJoinFewRows;
-      auto of = [&](float f) { return __shfl_sync(0xFFFFFFFFu, f, from); };
-      const float4 st = make_float4(of(mine.all.ref), of(mine.all.m), of(mine.all.l), of(mine.all.anchor));
+    for (int d = kJoinFewRows; d < 32; d *= 2) {
+      auto other = [&](float f) { return __shfl_xor_sync(0xFFFFFFFFu, f, d); };
+      const float4 st = make_float4(other(mine.all.ref), other(mine.all.m), other(mine.all.l), other(mine.all.anchor));
       float4 y[JoinedRow<D>::kVecs];
 #pragma unroll
       for (int v = 0; v < JoinedRow<D>::kVecs; ++v)
-        y[v] = make_float4(of(mine.acc[v].x), of(mine.acc[v].y), of(mine.acc[v].z), of(mine.acc[v].w));
-      row_of.add(st, y);
+        y[v] = make_float4(other(mine.acc[v].x), other(mine.acc[v].y), other(mine.acc[v].z), other(mine.acc[v].w));
+      mine.add(st, y);
     }
-    if (there && lane < kJoinFewRows) row_of.store(p, rec, row, piece);
+    if (there && lane < kJoinFewRows) mine.store(p, rec, row, piece);
   }
 }
 
