@@ -22,8 +22,8 @@
 //
 // What bounds it.  64 requests of up to 16384 tokens, 8 x 8 heads of 128 dimensions: 226 us, 5.5 TB/s of the codes, the copies
 // being ahead of the products.  With 64 columns (2 x 131004 tokens and less, 2 x 16 heads) the products are, 64 us: each warp
-// widens all of a page's codes for its 16 columns.  4 requests of 4096 tokens, 8 x 4 heads: 20 us, of which the two launches,
-// finding the runs and the first copies are 12.
+// widens all of a page's codes for its 16 columns.  4 requests of 4096 tokens, 8 x 4 heads: 18.5 us: 2 until
+// the runs are found, 3 until the first page is there, 5 of two pages' chains, 5 of joining, and the launches.
 #include <algorithm>
 
 #include "heads_device.cuh"
@@ -243,13 +243,9 @@ __global__ void __launch_bounds__(Shape<D, NC, W>::kThreads, 1) steps_kernel(con
       for (int k = 0; k < L::kWorkers; ++k) {
         const int64_t begin = run * (k * (int64_t)gridDim.x + blockIdx.x);
         if (begin >= first && begin < first + mine) {
-          const int64_t in = begin - first;
-          const int64_t unit = in / q.tiles;
           starts[k].r = r;
-          starts[k].head = (int)(unit / q.groups);
-          starts[k].group = (int)(unit % q.groups);
-          starts[k].tile = (int)(in % q.tiles);
           starts[k].q = q;
+          starts[k].left = begin - first;  // (from its first tile on; the worker itself finds head, group and tile)
         }
       }
     }
@@ -287,6 +283,10 @@ __global__ void __launch_bounds__(Shape<D, NC, W>::kThreads, 1) steps_kernel(con
   tc::Waiter w;
   Producer<D, NC, W> producer;
   Cursor cur = starts[worker];
+  const int64_t unit = quotient(cur.left, cur.q.tiles);
+  cur.tile = (int)(cur.left - unit * cur.q.tiles);
+  cur.head = (int)quotient(unit, cur.q.groups);
+  cur.group = (int)(unit - (int64_t)cur.head * cur.q.groups);
   cur.left = min(run, total - begin);
   producer.at = cur;
   uint32_t taken = 0;  // copies that this warp is done with

@@ -61,14 +61,19 @@ __device__ __forceinline__ void await(tc::Waiter& w, uint32_t bar, uint32_t pari
   w.wait(bar, parity);
   w.dead = __any_sync(0xFFFFFFFFu, w.dead);
 }
+// a / b, neither negative: in 32 bits where that does (a division in 64 is a long chain).
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return (a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
 // The cut units, for the kernels that join their parts: numbers of the records in two lists (units of more than `few` parts are in
 // the second), by the whole block of kThreads threads.  kMax: records at most.
 template <int kThreads, int kMax>
 struct CutLists {
   uint16_t at[2][kMax];
-  uint16_t counts[2][kMax / kThreads][kThreads / 32];
+  static constexpr int kRounds = kMax / kThreads, kWarps = kThreads / 32, kCounts = kRounds * kWarps, kPer = (kCounts + 31) / 32;
+  uint16_t counts[2][32 * kPer];  // of a round's warps, rounds one after the other
   __device__ __forceinline__ void build(const RunRecord* records, int n, int64_t run, int few, int (&total)[2]) {
-    constexpr int kRounds = kMax / kThreads, kWarps = kThreads / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int64_t begin[kRounds], end[kRounds];
 #pragma unroll
@@ -82,24 +87,40 @@ struct CutLists {
     for (int k = 0; k < kRounds; ++k) {
       const bool is = end[k] > begin[k], many = is && end[k] > (k * kThreads + (int)threadIdx.x + few) * run;
       those[0][k] = __ballot_sync(0xFFFFFFFFu, is && !many), those[1][k] = __ballot_sync(0xFFFFFFFFu, many);
-      if (lane == 0) counts[0][k][warp] = __popc(those[0][k]), counts[1][k][warp] = __popc(those[1][k]);
+      if (lane == 0) counts[0][k * kWarps + warp] = __popc(those[0][k]), counts[1][k * kWarps + warp] = __popc(those[1][k]);
     }
     __syncthreads();
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
-      int so_far = 0;
+      // each warp adds all counts up, kPer a lane
+      int count[kPer], mine = 0;
+#pragma unroll
+      for (int x = 0; x < kPer; ++x) {
+        count[x] = lane * kPer + x < kCounts ? counts[y][lane * kPer + x] : 0;
+        mine += count[x];
+      }
+      int upto = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int z = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+        if (lane >= d) upto += z;
+      }
+      total[y] = __shfl_sync(0xFFFFFFFFu, upto, 31);
+      int before[kPer];
+      before[0] = upto - mine;
+#pragma unroll
+      for (int x = 1; x < kPer; ++x) before[x] = before[x - 1] + count[x - 1];
 #pragma unroll
       for (int k = 0; k < kRounds; ++k) {
-        if (k * kThreads >= n) break;
-        int mine = so_far;
+        const int c = k * kWarps + warp;
+        int first = 0;
 #pragma unroll
-        for (int x = 0; x < kWarps; ++x) {
-          if (x < warp) mine += counts[y][k][x];
-          so_far += counts[y][k][x];
+        for (int x = 0; x < kPer; ++x) {
+          const int z = __shfl_sync(0xFFFFFFFFu, before[x], c / kPer);
+          if (c % kPer == x) first = z;
         }
-        if (those[y][k] >> lane & 1) at[y][mine + __popc(those[y][k] & ((1u << lane) - 1))] = (uint16_t)(k * kThreads + threadIdx.x);
+        if (those[y][k] >> lane & 1) at[y][first + __popc(those[y][k] & ((1u << lane) - 1))] = (uint16_t)(k * kThreads + threadIdx.x);
       }
-      total[y] = so_far;
     }
     __syncthreads();
   }

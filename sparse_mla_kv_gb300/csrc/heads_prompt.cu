@@ -892,8 +892,8 @@ __device__ __forceinline__ void find_start(const HeadsAttendParams& p, int limit
     const int who = __ffs(owner) - 1, r = r0 + warp * 32 + who;
     Request q;
     q.load(p, r, limit);
-    const int64_t a_head = __shfl_sync(0xFFFFFFFFu, mine, who) / p.pages.kv_heads, offset = begin - __shfl_sync(0xFFFFFFFFu, first, who);
-    const int head = (int)(offset / a_head);
+    const int64_t a_head = quotient(__shfl_sync(0xFFFFFFFFu, mine, who), p.pages.kv_heads), offset = begin - __shfl_sync(0xFFFFFFFFu, first, who);
+    const int head = (int)quotient(offset, a_head);
     int left = (int)(offset - head * a_head), block = -1, in = 0;
     for (int b0 = 0; block < 0; b0 += 32) {
       const int n = b0 + lane < q.blocks ? kItemCost + q.tiles(p, b0 + lane) : 0;
