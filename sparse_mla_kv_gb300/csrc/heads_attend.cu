@@ -20,7 +20,7 @@
 // every worker of the grid takes an equal run of pages, whatever the contexts' lengths; units that are cut leave partial
 // results in the workspace, which join_kernel joins in a fixed order.
 //
-// What bounds it.  64 requests of up to 16384 tokens, 8 x 8 heads of 128 dimensions: 226 us, 5.5 TB/s of the codes, the copies
+// What bounds it.  64 requests of up to 16384 tokens, 8 x 8 heads of 128 dimensions: 221 us, 5.6 TB/s of the codes, the copies
 // being ahead of the products.  With 64 columns (2 x 131004 tokens and less, 2 x 16 heads) the products are, 64 us: each warp
 // widens all of a page's codes for its 16 columns.  4 requests of 4096 tokens, 8 x 4 heads: 18.5 us: 2 until
 // the runs are found, 3 until the first page is there, 5 of two pages' chains, 5 of joining, and the launches.

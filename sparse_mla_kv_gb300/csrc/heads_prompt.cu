@@ -24,12 +24,12 @@
 // it get their NaN at the end.
 //
 // What bounds it.  The products, 512 D operations a row and key tile, would take 291 us for 8192 tokens with 8 x 4 heads of 128
-// dimensions at 1887 TFLOP/s, the reads nothing to speak of; measured 495 us, 1110 TFLOP/s.  A key tile takes about 3500 cycles of
+// dimensions at 1887 TFLOP/s, the reads nothing to speak of; measured 484 us, 1136 TFLOP/s.  A key tile takes about 3500 cycles of
 // the SM: 2160 of products, 2600 of shared memory's bandwidth (the right operands are read for each query tile, the widened codes
 // written once), 1024 of exponentials, and what a query tile's chain of products, maximum, exponentials and products again
 // leaves idle, which two query tiles in turn cover in part.  For 64 dimensions the exponentials weigh twice as much: 356 us
-// for the same prompt, 774 TFLOP/s.  Instructions are fetched anew where an item begins and ends, so that short code counts there:
-// 16 values unrolled instead of whole rows took 14 us from 522.  The smallest prompts (100 tokens, 2 x 4 heads) take 20 us.
+// for the same prompt, 770 TFLOP/s.  Instructions are fetched anew where an item begins and ends, so that short code counts there:
+// 16 values unrolled instead of whole rows took 14 us from 522.  The smallest prompts (100 tokens, 2 x 4 heads) take 18 us.
 #include "heads_device.cuh"
 
 HS_CHECK_WORD
