@@ -47,17 +47,18 @@ constexpr int kRegsLaunch = 128;
 // 56, 495 us with 192 and 64, 496 with 184 and 72, 503 with 176 and 80; 2048 rows behind 16000, 4 x 8 heads of 64: 230, 235, 239, 247.
 template <int D>
 struct Regs {
-  static constexpr int kSoftmax = D == 64 ? 200 : 192, kOther = D == 64 ? 56 : 64;
+  static constexpr int kSoftmax = D == 64 ? 200 : 152, kOther = D == 64 ? 56 : 104;
   static_assert(2 * kSoftmax + 2 * kOther <= 4 * kRegsLaunch, "more registers than the launch has");
 };
 constexpr int kScales = 8;  // key tiles whose scales are kept
 // What an item costs beside its key tiles, in these (12000 tokens, 4 x 3 heads of 64: 283 us; 301 us with 2, 284 us with 4), and the
 // least of a run: fewer would be mostly set-up and joining (100 tokens, 2 x 4 heads: 24 us with 4, 34 us with 6).
 constexpr int kItemCost = 3, kMinRun = 4;
+// (four: of query tile 0 and 1, for a key tile's first part, then for its second)
 enum Bar { kStFull = 0, kStEmpty = kStFull + 4, kKFull = kStEmpty + 4, kKEmpty = kKFull + 2, kVFull = kKEmpty + 2,
-           kVEmpty = kVFull + 2, kQFull = kVEmpty + 2, kQEmpty = kQFull + 2, kSFull = kQEmpty + 2, kPReady = kSFull + 2,
-           kPHalf = kPReady + 2, kODone = kPHalf + 2, kSFree = kODone + 2, kItem = kSFree + 2, kItemDone = kItem + 2,
-           kDrain = kItemDone + 2, kBars = kDrain + 2 };
+           kVEmpty = kVFull + 2, kQFull = kVEmpty + 2, kQEmpty = kQFull + 2, kSFull = kQEmpty + 2, kPReady = kSFull + 4,
+           kODone = kPReady + 4, kSFree = kODone + 4, kItem = kSFree + 4, kItemDone = kItem + 2, kDrain = kItemDone + 2,
+           kBars = kDrain + 2 };
 
 // Workspace: header, a record a CTA, statistics [CTA][2][256][4], results [CTA][2][D / 4][256][4].
 __host__ __device__ constexpr size_t ws_stats_offset(int ctas) { return sizeof(RunHeader) + (size_t)ctas * sizeof(RunRecord); }
@@ -116,14 +117,14 @@ static_assert(sizeof(Item) % 8 == 0, "alignment of what follows");
 template <int D>
 struct Smem {
   static constexpr int kUnits = D / 64, kUnit = 128 * 128;  // a unit: 128 rows of 64 fp16
-  // Tensor memory, for each query tile: 128 columns of S, D of O, and P: where there is room, in 64 of its own, so that the next
-  // scores are made while the weights are; else in S's place.
+  // Of a key tile, the pages that are taken together from scores to weights to results, and the number of such parts.  For 128
+  // dimensions a page at a time: its products run while the other page's weights are made (2048 rows behind 16000 tokens, 4 x 8 heads:
+  // 313 us; 333 us by key tiles).  For 64 both: the products are short, and hand-overs cost more (229 us; 285 us by pages).
+  static constexpr int kPages = D == 64 ? 2 : 1, kParts = 2 / kPages;
+  // Tensor memory, for each query tile: S, 64 columns a page; D columns of O; and P, 32 columns a page: where there is room, of its
+  // own, so that the next scores are made while the weights are; else in the place of the page's S.
   static constexpr bool kApart = D == 64;
-  static constexpr uint32_t kTo = kApart ? 384 : 256, kTp = kApart ? 256 : 0, kToStep = D, kTpStep = kApart ? 64 : 128;
-  // The first page's weights are handed over while the second's are made: where P has S's place, the next scores wait for the
-  // products (2048 rows behind 16000 tokens, 4 heads x 8: 383 -> 367 us).  Where they do not, it costs more than it gives (240 ->
-  // 256 us).
-  static constexpr bool kHalves = !kApart;
+  static constexpr uint32_t kTo = kApart ? 384 : 256, kTp = kApart ? 256 : 0, kToStep = D, kTpStep = kApart ? 64 : 128, kTpPage = kApart ? 32 : 64;
   static constexpr int kStage = D * kHeadsPage;
   static constexpr int kQ = 0, kK = kQ + 2 * kUnits * kUnit, kV = kK + 2 * kUnits * kUnit, kVPage = D * 128;
   // Staged key tiles: of each, the keys of its two pages, then their values.  Barriers: keys and values of the even ones, of the
@@ -519,7 +520,7 @@ __device__ __forceinline__ void widen_items(const HeadsAttendParams& p, const It
 template <int D>
 __device__ __forceinline__ void issue_items(const HeadsAttendParams& p, const Item* list, int t, uint32_t smem, uint32_t tmem) {
   using L = Smem<D>;
-  constexpr uint32_t kIdS = tc::idesc(true, 128, kKeys, false, false);
+  constexpr uint32_t kIdS = tc::idesc(true, 128, kHeadsPage * L::kPages, false, false);
   constexpr uint32_t kIdO = tc::idesc(true, 128, D, false, false);
   const uint32_t bars = smem + L::kBar;
   tc::Waiter w;
@@ -542,50 +543,59 @@ __device__ __forceinline__ void issue_items(const HeadsAttendParams& p, const It
       const uint32_t n = base + j - k0;
       wait(kKFull + (n & 1), n / 2 & 1);
     };
-    auto scores = [&](int j) {
+    auto scores = [&](int j, int part) {
       const uint32_t buf = (base + j - k0) & 1;
 #pragma unroll
       for (int i = 0; i < L::kUnits; ++i) {
-        const uint64_t da = dq + (uint32_t)(i * L::kUnit >> 4), db = dk + (uint32_t)((buf * L::kUnits + i) * L::kUnit >> 4);
+        const uint64_t da = dq + (uint32_t)(i * L::kUnit >> 4), db = dk + (uint32_t)(((buf * L::kUnits + i) * L::kUnit + part * 8192) >> 4);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) tc::mma_ss(tmem + t * 128, da + (k * 32 >> 4), db + (k * 32 >> 4), kIdS, i > 0 || k > 0, leader);
+        for (int k = 0; k < 4; ++k)
+          tc::mma_ss(tmem + t * 128 + part * 64, da + (k * 32 >> 4), db + (k * 32 >> 4), kIdS, i > 0 || k > 0, leader);
       }
-      tc::commit(bars + 8 * (kSFull + t), leader);
-      tc::commit(bars + 8 * (kKEmpty + buf), leader);
-      if (j + 1 == end) tc::commit(bars + 8 * (kQEmpty + t), leader);
+      tc::commit(bars + 8 * (kSFull + 2 * part + t), leader);
+      if (part == L::kParts - 1) {
+        tc::commit(bars + 8 * (kKEmpty + buf), leader);
+        if (j + 1 == end) tc::commit(bars + 8 * (kQEmpty + t), leader);
+      }
     };
     if (end > k0) {
       keys_there(k0);
       wait(kQFull + t, items & 1);
       ++items;
-      if (phase > 0) wait((L::kApart ? kSFree : kODone) + t, (phase - 1) & 1);  // the item before: S's place is free
-      scores(k0);
+#pragma unroll 1
+      for (int part = 0; part < L::kParts; ++part) {
+        if (phase > 0) wait((L::kApart ? kSFree : kODone) + 2 * part + t, (phase - 1) & 1);  // the item before: S's place is free
+        scores(k0, part);
+      }
     }
 #pragma unroll 1
     for (int j = k0; j < end; ++j, ++phase) {
       const uint32_t n = base + j - k0, buf = n & 1;
-      if (L::kApart && j + 1 < end) {
-        keys_there(j + 1);
-        wait(kSFree + t, phase & 1);
-        scores(j + 1);
-      }
-      wait(kVFull + buf, n / 2 & 1);
+#pragma unroll 1
+      for (int part = 0; part < L::kParts; ++part) {
+        if (part == 0 && j + 1 < end) keys_there(j + 1);
+        if (L::kApart && j + 1 < end) {
+          wait(kSFree + 2 * part + t, phase & 1);
+          scores(j + 1, part);
+        }
+        if (part == 0) wait(kVFull + buf, n / 2 & 1);
+        wait(kPReady + 2 * part + t, phase & 1);
 #pragma unroll
-      for (int page = 0; page < 2; ++page) {
-        if (L::kHalves || page == 0) wait((L::kHalves && page == 0 ? kPHalf : kPReady) + t, phase & 1);
-        const uint64_t db = dv + (uint32_t)((2 * buf + page) * L::kVPage >> 4);
-        // P: 16 tokens are 8 columns
+        for (int i = 0; i < L::kPages; ++i) {
+          const int page = part + i;
+          const uint64_t db = dv + (uint32_t)((2 * buf + page) * L::kVPage >> 4);
+          // P: 16 tokens are 8 columns
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          tc::mma_ts(tmem + L::kTo + t * L::kToStep, tmem + L::kTp + t * L::kTpStep + (page * 4 + k) * 8, db + (k * 32 >> 4), kIdO,
-                     j > k0 || page > 0 || k > 0, leader);
-      }
-      tc::commit(bars + 8 * (kODone + t), leader);
-      tc::commit(bars + 8 * (kVEmpty + buf), leader);
-      if (!L::kApart && j + 1 < end) {
-        keys_there(j + 1);
-        wait(kODone + t, phase & 1);  // P, in S's place, has been read
-        scores(j + 1);
+          for (int k = 0; k < 4; ++k)
+            tc::mma_ts(tmem + L::kTo + t * L::kToStep, tmem + L::kTp + t * L::kTpStep + page * L::kTpPage + k * 8, db + (k * 32 >> 4), kIdO,
+                       j > k0 || page > 0 || k > 0, leader);
+        }
+        tc::commit(bars + 8 * (kODone + 2 * part + t), leader);
+        if (part == L::kParts - 1) tc::commit(bars + 8 * (kVEmpty + buf), leader);
+        if (!L::kApart && j + 1 < end) {
+          wait(kODone + 2 * part + t, phase & 1);  // P, in S's place, has been read
+          scores(j + 1, part);
+        }
       }
     }
 #pragma unroll 1
@@ -649,63 +659,76 @@ __device__ __forceinline__ void softmax_items(const HeadsAttendParams& p, const 
     const int all_see = item_sees(p, *it, it->col0 + t * kQRows);  // (its first row sees least)
     float ref = -INFINITY, m = -INFINITY, l = 0.f, anchor = 0.f, qs = 0.f;
 #pragma unroll 1
-    for (int j = k0; j < end; ++j, ++phase) {
-      w.wait(bars + 8 * (kSFull + t), phase & 1);
+    for (int u = L::kParts * k0; u < L::kParts * end; ++u) {
+      constexpr int kPages = L::kPages, kTokens = kPages * kHeadsPage;
+      const uint32_t part = u % L::kParts, mine = 2 * part + t;
+      const uint32_t scales = smem + L::kPage + (before + u / L::kParts - k0) % kScales * 32 + 4 * part;
+      w.wait(bars + 8 * (kSFull + mine), phase & 1);
       __syncwarp();
       tc::fence_after();
-      if (j == k0) qs = scale * power_of_field(raw[L::kMisc + (k & 1) * kBlock + row]);
-      const uint32_t scales = smem + L::kPage + (before + j - k0) % kScales * 32;
-      float s[128];
-      // (in few, wide loads: 2048 rows behind 16000 tokens, 4 heads of 64 dimensions x 8: 247 us by sixteens, 232 us so)
-      load64(ts, s);
-      load64(ts + 64, s + 64);
-      const float size[2] = {lds_f(scales + 8), lds_f(scales + 12)};
-      float c[2];
+      if (u == L::kParts * k0) qs = scale * power_of_field(raw[L::kMisc + (k & 1) * kBlock + row]);
+      float s[kTokens], size[kPages], c[kPages], top[kPages];
+      bool valid[kPages], all_valid = true;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) c[i] = fminf(fmaxf(lds_f(scales + 4 * i) * qs, 1.17549435e-38f), 3.402823466e38f);
-      const bool missing = (lds_u(scales + 16) & lds_u(scales + 20)) == 0;
+      for (int i = 0; i < kPages; ++i) load64(ts + (part + i) * 64, s + 64 * i);
+#pragma unroll
+      for (int i = 0; i < kPages; ++i) {
+        size[i] = lds_f(scales + 8 + 4 * i);
+        c[i] = fminf(fmaxf(lds_f(scales + 4 * i) * qs, 1.17549435e-38f), 3.402823466e38f);
+        valid[i] = lds_u(scales + 16 + 4 * i) != 0;
+        all_valid &= valid[i];
+      }
       tc::tmem_wait_ld();
-      tc::touch<128>(s);
+      tc::touch<kTokens>(s);
       if constexpr (L::kApart) {
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(bars + 8 * (kSFree + t));
+        if (lane == 0) tc::mbar_arrive(bars + 8 * (kSFree + mine));
       }
-      if (missing || (j + 1) * kKeys > all_see) {
-        const int left = sees - j * kKeys;
-        const int left0 = lds_u(scales + 16) ? left : 0, left1 = lds_u(scales + 20) ? left : 0;
+      if (!all_valid || (u + 1) * kTokens > all_see) {
 #pragma unroll
-        for (int x = 0; x < 128; ++x)
-          if (x >= (x < 64 ? left0 : left1)) s[x] = -INFINITY;
+        for (int i = 0; i < kPages; ++i) {
+          const int left = valid[i] ? sees - u * kTokens - 64 * i : 0;
+#pragma unroll
+          for (int x = 0; x < 64; ++x)
+            if (x >= left) s[64 * i + x] = -INFINITY;
+        }
       }
-      float top[2] = {__fmul_rn(tc::max_of<64>(s), c[0]), __fmul_rn(tc::max_of<64>(s + 64), c[1])};
-      if (L::kApart && phase > 0) {  // the products before have read P, and are in O
-        w.wait(bars + 8 * (kODone + t), (phase - 1) & 1);
+      float most = -INFINITY, most_sized = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < kPages; ++i) {
+        top[i] = __fmul_rn(tc::max_of<64>(s + 64 * i), c[i]);
+        most = fmaxf(most, top[i]), most_sized = fmaxf(most_sized, top[i] + size[i]);
+      }
+      auto products_before = [&](uint32_t bar, uint32_t parity) {
+        w.wait(bars + 8 * (kODone + bar), parity);
         __syncwarp();
         tc::fence_after();
-      }
-      // rare: scores beyond kLarge, or a reference that has to move
-      const bool large = fabsf(top[0]) > kLarge || fabsf(top[1]) > kLarge || anchor != 0.f;
-      if (__any_sync(0xFFFFFFFFu, large || fmaxf(top[0] + size[0], top[1] + size[1]) > ref + kLazy)) {
+      };
+      if (L::kApart && phase > 0) products_before(mine, (phase - 1) & 1);  // have read P, and are in O
+      // rare: scores beyond kLarge, or a reference that has to move (a page that is not seen has a top of -infinity and does not count)
+      bool large = anchor != 0.f;
+#pragma unroll
+      for (int i = 0; i < kPages; ++i) large |= fabsf(top[i]) > kLarge && top[i] != -INFINITY;
+      if (__any_sync(0xFFFFFFFFu, large || most_sized > ref + kLazy)) {
         if (__any_sync(0xFFFFFFFFu, large)) {
-          // (a page that is not seen has a top of -infinity and does not count)
-          const float most = fmaxf(top[0], top[1]);
           if (fabsf(most) <= 3.402823466e38f && (most - anchor > kLarge || (ref == -INFINITY && fabsf(most) > kLarge))) {
             const float by = most - anchor;
             anchor = most;
             ref -= by, m -= by;
           }
 #pragma unroll
-          for (int x = 0; x < 128; ++x) s[x] = __fsub_rn(__fmul_rn(s[x], c[x >> 6]), anchor);  // (rounded as the tops are)
+          for (int x = 0; x < kTokens; ++x) s[x] = __fsub_rn(__fmul_rn(s[x], c[x >> 6]), anchor);  // (rounded as the tops are)
+          most -= anchor, most_sized = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) top[i] -= anchor, c[i] = 1.f;
+          for (int i = 0; i < kPages; ++i) top[i] -= anchor, c[i] = 1.f, most_sized = fmaxf(most_sized, top[i] + size[i]);
         }
-        const float most = fmaxf(top[0] + size[0], top[1] + size[1]);
-        const bool over = most > ref + kLazy;
-        const float now = over ? most - kTop : ref;
+        const bool over = most_sized > ref + kLazy;
+        const float now = over ? most_sized - kTop : ref;
         const float alpha = over ? exp2f(ref - now) : 1.f;
         ref = now;
-        if (j > k0) {  // (the products so far have finished: without room for P, this tile's scores were issued after them)
+        if (u > L::kParts * k0) {
+          if constexpr (L::kParts == 2) products_before(mine ^ 2, (part ? phase : phase - 1) & 1);  // the page before is in O
 #pragma unroll 1
           for (int x = 0; x < D; x += 16) {
             float o[16];
@@ -720,13 +743,12 @@ __device__ __forceinline__ void softmax_items(const HeadsAttendParams& p, const 
         }
       }
       const float r = ref == -INFINITY ? 0.f : ref;
-      const float higher = fmaxf(top[0], top[1]);
-      if (higher > m + kFar) {
-        l = m == -INFINITY ? 0.f : l * tc::exp2_fast(m - higher);
-        m = higher;
+      if (most > m + kFar) {
+        l = m == -INFINITY ? 0.f : l * tc::exp2_fast(m - most);
+        m = most;
       }
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < kPages; ++i) {
         float bias = size[i] - r;
         if (top[i] + size[i] < r - kFar) bias = top[i] < -2.f * kLarge ? -INFINITY : -kFar - top[i];
         const float2 c2 = make_float2(c[i], c[i]), b2 = make_float2(bias, bias);
@@ -742,20 +764,20 @@ __device__ __forceinline__ void softmax_items(const HeadsAttendParams& p, const 
             sum0 = tc::add2(sum0, e);
           pk[y] = pack_half(e.x, e.y);
         }
-        tc::tmem_st16(tp + 32 * i, reinterpret_cast<const float*>(pk));
-        tc::tmem_st16(tp + 32 * i + 16, reinterpret_cast<const float*>(pk + 16));
+        tc::tmem_st16(tp + L::kTpPage * (part + i), reinterpret_cast<const float*>(pk));
+        tc::tmem_st16(tp + L::kTpPage * (part + i) + 16, reinterpret_cast<const float*>(pk + 16));
         if (bias != -INFINITY) l += ((sum0.x + sum0.y) + (sum1.x + sum1.y)) * tc::exp2_fast(-bias - m);
-        if (i == 0 && !L::kHalves) continue;
-        tc::tmem_wait_st();
-        tc::fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(bars + 8 * ((i ? kPReady : kPHalf) + t));
       }
+      tc::tmem_wait_st();
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bars + 8 * (kPReady + mine));
+      if (part == L::kParts - 1) ++phase;
     }
     // results
     const bool work = end > k0, whole = k0 == 0 && it->k1 == it->tiles;
     if (work) {
-      w.wait(bars + 8 * (kODone + t), (phase - 1) & 1);
+      w.wait(bars + 8 * (kODone + 2 * (L::kParts - 1) + t), (phase - 1) & 1);
       __syncwarp();
       tc::fence_after();
     }
@@ -957,6 +979,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const HeadsAttendPa
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(raw + L::kFlag) + 2;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 4; ++i) tc::mbar_init(bars + 8 * (kStFull + i), 1), tc::mbar_init(bars + 8 * (kStEmpty + i), 4);
+    for (int i = 0; i < 4; ++i) {
+      tc::mbar_init(bars + 8 * (kSFull + i), 1);
+      tc::mbar_init(bars + 8 * (kPReady + i), 4);
+      tc::mbar_init(bars + 8 * (kODone + i), 1);
+      tc::mbar_init(bars + 8 * (kSFree + i), 4);
+    }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(bars + 8 * (kKFull + i), 4);
       tc::mbar_init(bars + 8 * (kKEmpty + i), 2);
@@ -964,11 +992,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const HeadsAttendPa
       tc::mbar_init(bars + 8 * (kVEmpty + i), 2);
       tc::mbar_init(bars + 8 * (kQFull + i), 4);
       tc::mbar_init(bars + 8 * (kQEmpty + i), 1);
-      tc::mbar_init(bars + 8 * (kSFull + i), 1);
-      tc::mbar_init(bars + 8 * (kPReady + i), 4);
-      tc::mbar_init(bars + 8 * (kPHalf + i), 4);
-      tc::mbar_init(bars + 8 * (kODone + i), 1);
-      tc::mbar_init(bars + 8 * (kSFree + i), 4);
       tc::mbar_init(bars + 8 * (kItem + i), 1);
       tc::mbar_init(bars + 8 * (kItemDone + i), kTakers);
       tc::mbar_init(bars + 8 * (kDrain + i), 1);
