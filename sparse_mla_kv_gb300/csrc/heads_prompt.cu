@@ -24,12 +24,13 @@
 // it get their NaN at the end.
 //
 // What bounds it.  The products, 512 D operations a row and key tile, would take 291 us for 8192 tokens with 8 x 4 heads of 128
-// dimensions at 1887 TFLOP/s, the reads nothing to speak of; measured 484 us, 1136 TFLOP/s.  A key tile takes about 3500 cycles of
-// the SM: 2160 of products, 2600 of shared memory's bandwidth (the right operands are read for each query tile, the widened codes
-// written once), 1024 of exponentials, and what a query tile's chain of products, maximum, exponentials and products again
-// leaves idle, which two query tiles in turn cover in part.  For 64 dimensions the exponentials weigh twice as much: 356 us
-// for the same prompt, 770 TFLOP/s.  Instructions are fetched anew where an item begins and ends, so that short code counts there:
-// 16 values unrolled instead of whole rows took 14 us from 522.  The smallest prompts (100 tokens, 2 x 4 heads) take 18 us.
+// dimensions at 1887 TFLOP/s, the reads nothing to speak of; measured 481 us, 1144 TFLOP/s (1300 for chunks over long contexts).
+// A key tile takes 3500 cycles of the SM or less: 2160 of products, 3100 of shared memory's bandwidth (both operands of the scores are
+// read for each page, the values for each query tile, the widened codes written once), 1024 of exponentials.  An item costs about
+// 7 us beside its key tiles: queries brought and converted, masked tiles, results, instructions fetched anew (so that short code
+// counts there: 16 values unrolled instead of whole rows took 14 us of 522).  For 64 dimensions the exponentials weigh twice as
+// much and the chain of a key tile is longer than its products: 360 us for the same prompt, 764 TFLOP/s.  The smallest prompts
+// (100 tokens, 2 x 4 heads) take 18 us.
 #include "heads_device.cuh"
 
 HS_CHECK_WORD
@@ -43,11 +44,11 @@ constexpr int kQRows = 128, kKeys = 128, kBlock = 2 * kQRows;
 constexpr int kThreads = 16 * 32, kMmaWarp = 8, kLoadWarp = 10, kWalkWarp = 11, kWidenWarp = 12;
 constexpr int kTakers = 15;  // warps that the items are handed to
 constexpr int kRegsLaunch = 128;
-// Registers after the trade, of the softmax warps and of the others.  8192 tokens, 8 x 4 heads of 128 dimensions: 522 us with 200 and
-// 56, 495 us with 192 and 64, 496 with 184 and 72, 503 with 176 and 80; 2048 rows behind 16000, 4 x 8 heads of 64: 230, 235, 239, 247.
+// Registers after the trade, of the softmax warps and of the others.  12000 tokens, 4 x 3 heads of 64 dimensions: 310 us with 208 and
+// 48, 288 us with 200 and 56, 285 us with 192 and 64.  For 128 dimensions, a page at a time, all from 136 and 120 to 168 and 88 do.
 template <int D>
 struct Regs {
-  static constexpr int kSoftmax = D == 64 ? 200 : 152, kOther = D == 64 ? 56 : 104;
+  static constexpr int kSoftmax = D == 64 ? 192 : 152, kOther = D == 64 ? 64 : 104;
   static_assert(2 * kSoftmax + 2 * kOther <= 4 * kRegsLaunch, "more registers than the launch has");
 };
 constexpr int kScales = 8;  // key tiles whose scales are kept
