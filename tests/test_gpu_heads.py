@@ -686,6 +686,29 @@ def test_captured_calls_and_calls_on_other_streams():
     same(b, hs.read_heads(pool, table, None, None, 3 * 60, dim)[0])
 
 
+def test_two_calls_at_once():
+    """Prompts on one stream and single tokens among prompts on another, over the same pages: each has the bits that it has alone."""
+    g = gen(23)
+    kv, dim, group = 2, 128, 4
+    ctx = [1500, 130, 700, 2000]
+    pool, _, table = make(g, ctx, kv, dim)
+    news = [[300, 130, 500, 64], [1, 40, 1, 900]]
+    args = [(i32(ctx), normal(g, sum(new), kv * group, dim), offsets(new)) for new in news]
+    alone = [hs.attend_heads(pool, table, lens, q, 0.1, cu_q=cu) for lens, q, cu in args]
+    ws = [hs.alloc_heads_workspace() for _ in news]
+    status = [torch.zeros(1, dtype=torch.int32, device="cuda") for _ in news]
+    streams = [torch.cuda.Stream() for _ in news]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = [hs.attend_heads(pool, table, lens, q, 0.1, cu_q=cu, workspace=w, status=st, stream=s)
+               for (lens, q, cu), w, st, s in zip(args, ws, status, streams)]
+    torch.cuda.synchronize()
+    for (out, lse), (o, l), st in zip(got, alone, status):
+        same(out, o)
+        same(lse, l)
+        assert int(st) == 0
+
+
 def test_layers_and_offsets_past_32_bits():
     g = gen(18)
     kv, dim, group = 128, 128, 1  # 2 MB a page: block 1100 begins past 2^31
