@@ -21,8 +21,8 @@
 // results in the workspace, which join_kernel joins in a fixed order.
 //
 // What bounds it.  64 requests of up to 16384 tokens, 8 x 8 heads of 128 dimensions: 221 us, 5.6 TB/s of the codes, the copies
-// being ahead of the products.  With 64 columns (2 x 131004 tokens and less, 2 x 16 heads) the products are, 64 us: each warp
-// widens all of a page's codes for its 16 columns.  4 requests of 4096 tokens, 8 x 4 heads: 18.5 us: 2 until
+// being ahead of the products.  With 32 columns (64 requests of up to 4004 tokens, 4 x 8 heads, four positions) the products are, 72 us:
+// each of two warps widens all of a page's codes for its 16 columns.  4 requests of 4096 tokens, 8 x 4 heads: 18.5 us: 2 until
 // the runs are found, 3 until the first page is there, 5 of two pages' chains, 5 of joining, and the launches.
 #include <algorithm>
 
@@ -36,10 +36,10 @@ namespace {
 using namespace heads;
 
 constexpr int kRingBytes = 192 * 1024;
-// Requests of more columns are left to heads_prompt.cu.  With 48 columns a request (4 x 8 heads of 128 dimensions) this takes 16 us for
-// one request of 3000 tokens, 77 us for four of up to 30000, 123 us for 64 of up to 4000; that, 22, 63 and 107 us.  With 64
-// columns and two long contexts of 2 x 16 heads 64 and 68 us.  Small calls count more, and the host does not know the contexts.
-constexpr int kStepCols = 64;
+// Requests of more columns are left to heads_prompt.cu.  With 48 columns a request (4 x 8 heads of 128 dimensions) that takes 84 us for
+// 64 requests of up to 4000 tokens, 52 us for four of up to 30000, 21 us for one of 3000; this, with four warps a group of 64,
+// 123, 77 and 16 us.  With 32 columns that takes 80, 52 and 21 us, this 72, 52 and 15 us.
+constexpr int kStepCols = 32;
 
 // Workspace: header, a record a worker, statistics [worker][2][cols][4], results [worker][2][cols][D].
 __host__ __device__ constexpr size_t ws_stats_offset(int workers) { return sizeof(RunHeader) + (size_t)workers * sizeof(RunRecord); }
@@ -713,12 +713,11 @@ cudaError_t launch_steps(const HeadsAttendParams& p, int limit, int dev, int sms
 
 template <int D>
 cudaError_t launch_dim(const HeadsAttendParams& p, int limit, int dev, int sms, cudaStream_t s) {
-  // columns of a request, on average: a group takes them all, up to 64 (a ragged call's longer ones take several)
+  // columns of a request, on average: a group takes them all, up to 32 (a ragged call's longer ones take several)
   const int64_t cols = p.a.R > 0 ? (p.a.n + p.a.R - 1) / p.a.R * p.group : 1;
   if (cols <= 8) return launch_steps<D, 8, 1>(p, limit, dev, sms, s);
   if (cols <= 16) return launch_steps<D, 16, 1>(p, limit, dev, sms, s);
-  if (cols <= 32) return launch_steps<D, 16, 2>(p, limit, dev, sms, s);
-  return launch_steps<D, 16, 4>(p, limit, dev, sms, s);
+  return launch_steps<D, 16, 2>(p, limit, dev, sms, s);
 }
 
 }  // namespace
@@ -744,7 +743,6 @@ size_t heads_workspace_bytes(int sms) {
   shape(Shape<128, 8, 1>::kWorkers, 8, 128);
   shape(Shape<128, 16, 1>::kWorkers, 16, 128);
   shape(Shape<128, 16, 2>::kWorkers, 32, 128);
-  shape(Shape<128, 16, 4>::kWorkers, 64, 128);
   return most;
 }
 
