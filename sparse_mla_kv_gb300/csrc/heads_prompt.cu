@@ -1102,23 +1102,19 @@ __global__ void __launch_bounds__(kJoinThreads, 2) prompt_join_kernel(const Head
   cuts.build(records, ctas, header.run, kFewParts, n);
   JoinedRow<D> mine;
   constexpr int kGroups = kBlock / kJoinRows, kFewGroups = kBlock / kJoinFewRows;
-  for (int item = blockIdx.x; item < n[0] * kGroups; item += gridDim.x) {
-    const int i = cuts.at[0][item / kGroups], row = item % kGroups * kJoinRows + lane;
-    const RunRecord rec = records[i];
-    if (row >= rec.cols) continue;
-    mine.join(stats, parts, i, rec.begin > i * header.run ? 1 : 0, i, 1, (int)((rec.end - 1) / header.run), row, piece);
-    mine.store(p, rec, row, piece);
-  }
-  for (int item = blockIdx.x; item < n[1] * kFewGroups; item += gridDim.x) {
-    constexpr int kShares = 32 / kJoinFewRows;
-    const int i = cuts.at[1][item / kFewGroups], row = item % kFewGroups * kJoinFewRows + lane % kJoinFewRows;
+  const int few = n[0] * kGroups;
+#pragma unroll 1
+  for (int item = blockIdx.x; item < few + n[1] * kFewGroups; item += gridDim.x) {
+    const bool many = item >= few;
+    const int rows = many ? kJoinFewRows : kJoinRows, groups = many ? kFewGroups : kGroups, x = many ? item - few : item;
+    const int i = cuts.at[many][x / groups], row = x % groups * rows + lane % rows;
     const RunRecord rec = records[i];
     const bool there = row < rec.cols;
-    mine.join(stats, parts, i, rec.begin > i * header.run ? 1 : 0, i + lane / kJoinFewRows, kShares,
+    mine.join(stats, parts, i, rec.begin > i * header.run ? 1 : 0, i + lane / rows, 32 / rows,
               there ? (int)((rec.end - 1) / header.run) : -1, row, piece);
-    // the shares are joined two and two; what the upper lanes make of them is not used
-#pragma unroll
-    for (int d = kJoinFewRows; d < 32; d *= 2) {
+    // the lanes' shares are joined two and two; what the upper lanes make of them is not used
+#pragma unroll 1
+    for (int d = rows; d < 32; d *= 2) {
       auto other = [&](float f) { return __shfl_xor_sync(0xFFFFFFFFu, f, d); };
       const float4 st = make_float4(other(mine.all.ref), other(mine.all.m), other(mine.all.l), other(mine.all.anchor));
       float4 y[JoinedRow<D>::kVecs];
@@ -1127,7 +1123,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) prompt_join_kernel(const Head
         y[v] = make_float4(other(mine.acc[v].x), other(mine.acc[v].y), other(mine.acc[v].z), other(mine.acc[v].w));
       mine.add(st, y);
     }
-    if (there && lane < kJoinFewRows) mine.store(p, rec, row, piece);
+    if (there && lane < rows) mine.store(p, rec, row, piece);
   }
 }
 
