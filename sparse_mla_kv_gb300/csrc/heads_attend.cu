@@ -414,8 +414,10 @@ __global__ void __launch_bounds__(Shape<D, NC, W>::kThreads, 1) steps_kernel(con
       uint32_t pf[kHalves][4][2];
 #pragma unroll
       for (int h = 0; h < kHalves; ++h) {
+        float least = kLowest;
         if (mixed) {
           const int left = valid ? sees[h] - key0 - 16 * t : 0;
+          if (left <= 0) least = -INFINITY;
 #pragma unroll
           for (int j = 0; j < 8; ++j)
 #pragma unroll
@@ -424,9 +426,9 @@ __global__ void __launch_bounds__(Shape<D, NC, W>::kThreads, 1) steps_kernel(con
         }
         float top = s[0][2 * h];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) top = fmaxf(fmaxf(top, s[j][2 * h]), s[j][2 * h + 1]);
+        for (int j = 0; j < 8; ++j) top = max_nan(top, s[j][2 * h], s[j][2 * h + 1]);
         float c = fminf(fmaxf(sk * qs[h], 1.17549435e-38f), 3.402823466e38f);
-        top = __fmul_rn(top, c);
+        top = max_nan(__fmul_rn(top, c), least);
         if (__any_sync(0xFFFFFFFFu, fabsf(top) > kLarge || anchor[h] != 0.f)) {
           const float most = quad_max(top);
           if (fabsf(most) <= 3.402823466e38f && (most - anchor[h] > kLarge || (ref[h] == -INFINITY && fabsf(most) > kLarge))) {
@@ -463,7 +465,9 @@ __global__ void __launch_bounds__(Shape<D, NC, W>::kThreads, 1) steps_kernel(con
           sum0 += x, sum1 += y;
           pf[h][j >> 1][j & 1] = pack_half(x, y);
         }
-        if (top > m[h] + kFar) {
+        if (!(top < INFINITY)) {
+          l[h] += top, m[h] = INFINITY;
+        } else if (top > m[h] + kFar) {
           l[h] = m[h] == -INFINITY ? 0.f : l[h] * exp2f(m[h] - top);
           m[h] = top;
         }
@@ -526,7 +530,7 @@ __global__ void __launch_bounds__(Shape<D, NC, W>::kThreads, 1) steps_kernel(con
 #pragma unroll
     for (int h = 0; h < kHalves; ++h) {
       const float most = quad_max(m[h]);
-      const float sum_l = quad_sum(m[h] == -INFINITY ? 0.f : l[h] * exp2f(m[h] - most));
+      const float sum_l = quad_sum(m[h] == most ? l[h] : l[h] * exp2f(m[h] - most));
       const bool there = 8 * h + g < cols;
       if (any_nan) {
 #pragma unroll
@@ -540,13 +544,12 @@ __global__ void __launch_bounds__(Shape<D, NC, W>::kThreads, 1) steps_kernel(con
         }
       }
       if (whole) {
-        const float half_way = 0.5f * (ref[h] - most), up = sum_l == 0.f ? 0.f : exp2f(half_way);
-        const float inv = sum_l == 0.f ? 0.f : up / sum_l;
+        const float2 by = result_factors(ref[h], most, sum_l);
         float f0[2], f1[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          f0[e] = __shfl_sync(0xFFFFFFFFu, up, 4 * (2 * t + e));
-          f1[e] = __shfl_sync(0xFFFFFFFFu, inv, 4 * (2 * t + e));
+          f0[e] = __shfl_sync(0xFFFFFFFFu, by.x, 4 * (2 * t + e));
+          f1[e] = __shfl_sync(0xFFFFFFFFu, by.y, 4 * (2 * t + e));
         }
         uint16_t* out = static_cast<uint16_t*>(p.a.out) + row[h] / p.a.q_heads * p.a.out_token_stride +
                         row[h] % p.a.q_heads * p.a.out_head_stride + 2 * t;
@@ -557,7 +560,7 @@ __global__ void __launch_bounds__(Shape<D, NC, W>::kThreads, 1) steps_kernel(con
             const uint32_t x = transposed(pack(f16, o[h][i][2 * y] * f0[0] * f1[0], o[h][i][2 * y + 1] * f0[1] * f1[1]));
             if (there && HS_CHECK(row[h] < p.a.n * p.a.q_heads, kChkOutPos)) *reinterpret_cast<uint32_t*>(out + 16 * i + 8 * y) = x;
           }
-        if (there && t == 0 && p.a.lse) p.a.lse[row[h]] = sum_l == 0.f ? -INFINITY : (anchor[h] + (most + log2f(sum_l))) * kLn2;
+        if (there && t == 0 && p.a.lse) p.a.lse[row[h]] = result_lse(anchor[h], most, sum_l);
       } else {
         const int at = part * L::kCols + sub * NC + 8 * h;
         if (t == 0) stats[at + g] = make_float4(ref[h], most, sum_l, anchor[h]);
@@ -607,7 +610,7 @@ __device__ __forceinline__ Joined join_parts(const float4* stats, const float* p
     }
 #pragma unroll
     for (int y = 0; y < kJoinParts; ++y) {
-      if (x0 + y * step > last || st[y].y == -INFINITY) continue;
+      if (x0 + y * step > last || saw_none(st[y].y, st[y].z)) continue;
       const float2 f = res.join(st[y]);
 #pragma unroll
       for (int d = 0; d < kPer; ++d) acc[d] = acc[d] * f.x + v[y][d] * f.y;
@@ -620,7 +623,7 @@ __device__ __forceinline__ void store_joined(const HeadsAttendParams& p, const R
                                              const float (&out)[D / 32]) {
   constexpr int kPer = D / 32;
   const int lane = threadIdx.x & 31;
-  const float up = all.l == 0.f ? 0.f : exp2f(0.5f * (all.ref - all.m)), inv = all.l == 0.f ? 0.f : up / all.l;
+  const float2 by = result_factors(all.ref, all.m, all.l);
   const int in_unit = rec.group * group_cols + c;
   const int64_t token = rec.t0 + in_unit / p.group;
   const int qh = rec.head * p.group + in_unit % p.group;
@@ -628,8 +631,8 @@ __device__ __forceinline__ void store_joined(const HeadsAttendParams& p, const R
   uint16_t* to = static_cast<uint16_t*>(p.a.out) + token * p.a.out_token_stride + qh * p.a.out_head_stride + lane * kPer;
 #pragma unroll
   for (int d = 0; d < kPer; d += 2)
-    *reinterpret_cast<uint32_t*>(to + d) = pack(p.a.dtype == HS_FP16, out[d] * up * inv, out[d + 1] * up * inv);
-  if (lane == 0 && p.a.lse) p.a.lse[token * p.a.q_heads + qh] = all.l == 0.f ? -INFINITY : (all.anchor + (all.m + log2f(all.l))) * kLn2;
+    *reinterpret_cast<uint32_t*>(to + d) = pack(p.a.dtype == HS_FP16, out[d] * by.x * by.y, out[d + 1] * by.x * by.y);
+  if (lane == 0 && p.a.lse) p.a.lse[token * p.a.q_heads + qh] = result_lse(all.anchor, all.m, all.l);
 }
 
 template <int D>
