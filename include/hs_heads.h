@@ -107,8 +107,10 @@ hs_status hs_read_heads(const hs_pool* pool, int32_t layer, const hs_heads_read*
  * two and keeps the bits of values down to 2^-15 of its largest; a token's weight times its page's value scale is
  * rounded to 11 bits and keeps them down to 2^-21 of the largest such product, and is zero below 2^-32 of it.  The
  * value scales that one query sees may differ by up to 2^100.  lse and the sum of the weights are fp32 throughout.
- * What a query does not see has no part in its result, whatever it holds; a NaN that it sees makes its result NaN
- * (in a value: that element of it). */
+ * What a query does not see has no part in its result, whatever it holds.  A NaN value that it sees makes that element
+ * of out NaN.  Scores that are not finite in fp32 (NaN keys; queries that hold NaN or an infinity) enter as the
+ * formulas say: a NaN among those that it sees makes out and lse NaN, +infinity out NaN and lse +infinity, and where all
+ * are -infinity, out is NaN and lse -infinity. */
 typedef struct {
   int32_t kv_heads, head_dim;
   int32_t q_heads;            /* a multiple of kv_heads, at most HS_MAX_HEADS                         */

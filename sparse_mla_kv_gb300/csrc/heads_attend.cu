@@ -369,6 +369,7 @@ __global__ void __launch_bounds__(Shape<D, NC, W>::kThreads, 1) steps_kernel(con
         for (int k = 0; k < 4; ++k) o[h][i][k] = 0.f;
     }
 
+    int first = INT_MAX;  // token of the pages that are there
     bool moved;
 #pragma unroll 1
     do {
@@ -410,14 +411,13 @@ __global__ void __launch_bounds__(Shape<D, NC, W>::kThreads, 1) steps_kernel(con
       await(w, full + 8 * (taken % L::kSlots), taken / L::kSlots & 1);
       const float sv = lds_f(slot + L::kUnit + 4 * ((p.pages.kv_heads + head) & 3));
       const float size = valid ? log2f(sv) : 0.f;
+      if (first == INT_MAX && valid) first = key0;
       const bool mixed = !valid || key0 + kHeadsPage > all_see;
       uint32_t pf[kHalves][4][2];
 #pragma unroll
       for (int h = 0; h < kHalves; ++h) {
-        float least = kLowest;
         if (mixed) {
           const int left = valid ? sees[h] - key0 - 16 * t : 0;
-          if (left <= 0) least = -INFINITY;
 #pragma unroll
           for (int j = 0; j < 8; ++j)
 #pragma unroll
@@ -426,9 +426,9 @@ __global__ void __launch_bounds__(Shape<D, NC, W>::kThreads, 1) steps_kernel(con
         }
         float top = s[0][2 * h];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) top = max_nan(top, s[j][2 * h], s[j][2 * h + 1]);
+        for (int j = 0; j < 8; ++j) top = fmaxf(fmaxf(top, s[j][2 * h]), s[j][2 * h + 1]);
         float c = fminf(fmaxf(sk * qs[h], 1.17549435e-38f), 3.402823466e38f);
-        top = max_nan(__fmul_rn(top, c), least);
+        top = fminf(__fmul_rn(top, c), kMost);
         if (__any_sync(0xFFFFFFFFu, fabsf(top) > kLarge || anchor[h] != 0.f)) {
           const float most = quad_max(top);
           if (fabsf(most) <= 3.402823466e38f && (most - anchor[h] > kLarge || (ref[h] == -INFINITY && fabsf(most) > kLarge))) {
@@ -465,13 +465,11 @@ __global__ void __launch_bounds__(Shape<D, NC, W>::kThreads, 1) steps_kernel(con
           sum0 += x, sum1 += y;
           pf[h][j >> 1][j & 1] = pack_half(x, y);
         }
-        if (!(top < INFINITY)) {
-          l[h] += top, m[h] = INFINITY;
-        } else if (top > m[h] + kFar) {
-          l[h] = m[h] == -INFINITY ? 0.f : l[h] * exp2f(m[h] - top);
+        if (top > m[h] + kFar) {
+          l[h] *= exp2f(m[h] - top);
           m[h] = top;
         }
-        if (bias != -INFINITY) l[h] += (sum0 + sum1) * exp2f(-bias - m[h]);
+        l[h] += (sum0 + sum1) * (bias == -INFINITY ? 0.f : exp2f(-bias - m[h]));  // (NaN stays, whatever the factor)
       }
 
       // results
@@ -529,8 +527,9 @@ __global__ void __launch_bounds__(Shape<D, NC, W>::kThreads, 1) steps_kernel(con
       cut = RunRecord{unit_begin, unit_begin + req.tiles, req.t0, head, group, cols + sub * NC};
 #pragma unroll
     for (int h = 0; h < kHalves; ++h) {
-      const float most = quad_max(m[h]);
+      float most = quad_max(m[h]);
       const float sum_l = quad_sum(m[h] == most ? l[h] : l[h] * exp2f(m[h] - most));
+      if (sees[h] > first) most = fmaxf(most, kLowest);
       const bool there = 8 * h + g < cols;
       if (any_nan) {
 #pragma unroll

@@ -15,23 +15,14 @@ constexpr float kTop = 7.f, kLazy = 15.f, kFar = 60.f;
 // swallow it, and a product that is not rounded could pass the rounded largest by far.
 constexpr float kLarge = 65536.f;
 
-// Scores that are not finite.  A largest score keeps NaN.  A row that has seen NaN or +infinity is spoilt for good: its m is
-// +infinity, above anything that follows, and its l is NaN or +infinity.  A row that has seen tokens, all of them at -infinity, has an m
-// (kLowest is taken for their largest) and an l of zero; m = -infinity and l = 0 say that it has seen no token.
-constexpr float kLowest = -3.402823466e38f;
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float max_nan(float a, float b, float c) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
+// Scores that are not finite.  Maxima pass NaN over; the sums of weights have it, whatever the reference.  The largest of the scores that
+// a row sees in a page is at most kMost: a row that sees +infinity has its anchor there, weights of +infinity and no others, and so
+// has l.  A row that has seen a token has an m of kLowest at least, also where all its scores are -infinity and l is zero: with
+// m = -infinity and l = 0 it has seen none.
+constexpr float kMost = 3.402823466e38f, kLowest = -kMost;
 __device__ __forceinline__ bool saw_none(float m, float l) { return m == -INFINITY && l == 0.f; }
 // What a row's weighted sums are multiplied by, one factor after the other: 2^(ref - m) / l, by halves; zeros for a row that saw no
-// token, NaN for one that is spoilt or has no weight at all.
+// token, NaN where the weights' sum is zero, infinite or NaN.
 __device__ __forceinline__ float2 result_factors(float ref, float m, float l) {
   if (saw_none(m, l)) return make_float2(0.f, 0.f);
   const float up = exp2f(0.5f * (ref - m));
@@ -151,7 +142,7 @@ struct CutLists {
 };
 
 // What parts of a column's (or row's) results have been joined so far: the references, the sum of weights.  A part's statistics are
-// (ref, m, l, anchor); see above for rows that are spoilt or have seen no token.
+// (ref, m, l, anchor); those of a row that has seen no token are left out.
 struct Joined {
   float anchor = -INFINITY, ref = -INFINITY, m = -INFINITY, l = 0.f;
   // Joins a part; returns what the results so far, and the part's, are to be multiplied by.
@@ -160,7 +151,7 @@ struct Joined {
     const float to = fmaxf(anchor, st.w), here = st.w - to;
     if (to != anchor) ref += anchor - to, m += anchor - to, anchor = to;
     const float now = fmaxf(ref, st.x + here), now_m = fmaxf(m, st.y + here);
-    const float2 f = make_float2(ref == now ? 1.f : exp2f(ref - now), exp2f(st.x + here - now));
+    const float2 f = make_float2(ref == now ? 1.f : exp2f(ref - now), st.x == -INFINITY ? 0.f : exp2f(st.x + here - now));
     l = l * (m == now_m ? 1.f : exp2f(m - now_m)) + st.z * (st.y + here == now_m ? 1.f : exp2f(st.y + here - now_m));
     ref = now, m = now_m;
     return f;

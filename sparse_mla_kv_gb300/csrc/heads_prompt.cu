@@ -658,6 +658,7 @@ __device__ __forceinline__ void softmax_items(const HeadsAttendParams& p, const 
     const int k0 = it->k0, end = it->end[t];
     const int sees = row < it->rows ? item_sees(p, *it, it->col0 + row) : 0;
     const int all_see = item_sees(p, *it, it->col0 + t * kQRows);  // (its first row sees least)
+    int first = INT_MAX;  // token of the pages that are there
     float ref = -INFINITY, m = -INFINITY, l = 0.f, anchor = 0.f, qs = 0.f;
 #pragma unroll 1
     for (int u = L::kParts * k0; u < L::kParts * end; ++u) {
@@ -698,7 +699,7 @@ __device__ __forceinline__ void softmax_items(const HeadsAttendParams& p, const 
       float most = -INFINITY, most_sized = -INFINITY;
 #pragma unroll
       for (int i = 0; i < kPages; ++i) {
-        top[i] = __fmul_rn(tc::max_of<64>(s + 64 * i), c[i]);
+        top[i] = fminf(__fmul_rn(tc::max_of<64>(s + 64 * i), c[i]), kMost);
         most = fmaxf(most, top[i]), most_sized = fmaxf(most_sized, top[i] + size[i]);
       }
       auto products_before = [&](uint32_t bar, uint32_t parity) {
@@ -745,7 +746,7 @@ __device__ __forceinline__ void softmax_items(const HeadsAttendParams& p, const 
       }
       const float r = ref == -INFINITY ? 0.f : ref;
       if (most > m + kFar) {
-        l = m == -INFINITY ? 0.f : l * tc::exp2_fast(m - most);
+        l *= tc::exp2_fast(m - most);
         m = most;
       }
 #pragma unroll
@@ -767,14 +768,18 @@ __device__ __forceinline__ void softmax_items(const HeadsAttendParams& p, const 
         }
         tc::tmem_st16(tp + L::kTpPage * (part + i), reinterpret_cast<const float*>(pk));
         tc::tmem_st16(tp + L::kTpPage * (part + i) + 16, reinterpret_cast<const float*>(pk + 16));
-        if (bias != -INFINITY) l += ((sum0.x + sum0.y) + (sum1.x + sum1.y)) * tc::exp2_fast(-bias - m);
+        l += ((sum0.x + sum0.y) + (sum1.x + sum1.y)) * (bias == -INFINITY ? 0.f : tc::exp2_fast(-bias - m));  // (NaN stays)
       }
       tc::tmem_wait_st();
       tc::fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(bars + 8 * (kPReady + mine));
+#pragma unroll
+      for (int i = 0; i < kPages; ++i)
+        if (first == INT_MAX && valid[i]) first = u * kTokens + 64 * i;
       if (part == L::kParts - 1) ++phase;
     }
+    if (sees > first) m = fmaxf(m, kLowest);
     // results
     const bool work = end > k0, whole = k0 == 0 && it->k1 == it->tiles;
     if (work) {
@@ -785,7 +790,6 @@ __device__ __forceinline__ void softmax_items(const HeadsAttendParams& p, const 
     const int* nan_first = reinterpret_cast<const int*>(raw + L::kNan) + (k & 1) * D;
     const bool nans = work && *(reinterpret_cast<const volatile int*>(raw + L::kFlag) + (k & 1)) != 0;
     const bool there = row < it->rows;
-    const float up = l == 0.f ? 0.f : exp2f(0.5f * (ref - m)), inv = l == 0.f ? 0.f : up / l;
     const bool f16 = p.a.dtype == HS_FP16;
     if (!whole) {
       uint8_t* ws = reinterpret_cast<uint8_t*>(p.workspace);
@@ -817,7 +821,8 @@ __device__ __forceinline__ void softmax_items(const HeadsAttendParams& p, const 
       const int c = it->col0 + row, token = c / p.group, head = it->head * p.group + c - token * p.group;
       const bool writes = there && HS_CHECK(it->t0 + token < p.a.n && head < p.a.q_heads, kChkOutPos);
       uint16_t* out = static_cast<uint16_t*>(p.a.out) + (it->t0 + token) * p.a.out_token_stride + head * p.a.out_head_stride;
-      const bool some = work && up != 0.f;
+      const bool some = work && !saw_none(m, l);
+      const float2 by = result_factors(ref, m, l);
 #pragma unroll 1
       for (int x = 0; x < D; x += 16) {
         float o[16];
@@ -833,7 +838,7 @@ __device__ __forceinline__ void softmax_items(const HeadsAttendParams& p, const 
         }
         uint32_t v[8];
 #pragma unroll
-        for (int y = 0; y < 8; ++y) v[y] = pack(f16, some ? o[2 * y] * up * inv : 0.f, some ? o[2 * y + 1] * up * inv : 0.f);
+        for (int y = 0; y < 8; ++y) v[y] = pack(f16, some ? o[2 * y] * by.x * by.y : 0.f, some ? o[2 * y + 1] * by.x * by.y : 0.f);
         if (writes) {
           *reinterpret_cast<uint4*>(out + x) = make_uint4(v[0], v[1], v[2], v[3]);
           *reinterpret_cast<uint4*>(out + x + 8) = make_uint4(v[4], v[5], v[6], v[7]);
@@ -841,8 +846,7 @@ __device__ __forceinline__ void softmax_items(const HeadsAttendParams& p, const 
       }
       if (there && p.a.lse) {
         const int col = it->col0 + row, token = col / p.group;
-        p.a.lse[(it->t0 + token) * p.a.q_heads + it->head * p.group + col - token * p.group] =
-            l == 0.f ? -INFINITY : (anchor + (m + log2f(l))) * kLn2;
+        p.a.lse[(it->t0 + token) * p.a.q_heads + it->head * p.group + col - token * p.group] = result_lse(anchor, m, l);
       }
     }
     before += it->k1 - k0;
@@ -1041,7 +1045,7 @@ struct JoinedRow {
   Joined all;
   float4 acc[kVecs];
   __device__ __forceinline__ void add(float4 st, const float4* y) {
-    if (st.y == -INFINITY) return;  // (a part of which the row sees nothing)
+    if (saw_none(st.y, st.z)) return;
     const float2 f = all.join(st);
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
@@ -1072,7 +1076,7 @@ struct JoinedRow {
     }
   }
   __device__ __forceinline__ void store(const HeadsAttendParams& p, const RunRecord& rec, int row, int piece) const {
-    const float up = all.l == 0.f ? 0.f : exp2f(0.5f * (all.ref - all.m)), inv = all.l == 0.f ? 0.f : up / all.l;
+    const float2 by = result_factors(all.ref, all.m, all.l);
     const int col = rec.group * kBlock + row, in_token = col / p.group;
     const int64_t token = rec.t0 + in_token;
     const int head = rec.head * p.group + col - in_token * p.group;
@@ -1082,10 +1086,10 @@ struct JoinedRow {
 #pragma unroll
     for (int v = 0; v < kVecs; v += 2)
       *reinterpret_cast<uint4*>(out + 4 * v) = make_uint4(
-          pack(f16, acc[v].x * up * inv, acc[v].y * up * inv), pack(f16, acc[v].z * up * inv, acc[v].w * up * inv),
-          pack(f16, acc[v + 1].x * up * inv, acc[v + 1].y * up * inv), pack(f16, acc[v + 1].z * up * inv, acc[v + 1].w * up * inv));
+          pack(f16, acc[v].x * by.x * by.y, acc[v].y * by.x * by.y), pack(f16, acc[v].z * by.x * by.y, acc[v].w * by.x * by.y),
+          pack(f16, acc[v + 1].x * by.x * by.y, acc[v + 1].y * by.x * by.y), pack(f16, acc[v + 1].z * by.x * by.y, acc[v + 1].w * by.x * by.y));
     if (piece == 0 && p.a.lse)
-      p.a.lse[token * p.a.q_heads + head] = all.l == 0.f ? -INFINITY : (all.anchor + (all.m + log2f(all.l))) * kLn2;
+      p.a.lse[token * p.a.q_heads + head] = result_lse(all.anchor, all.m, all.l);
   }
 };
 template <int D>

@@ -98,6 +98,14 @@ STEPS = [
     (2, 128, 8, torch.bfloat16, [40, 4, 5000, 2], [4, 4, 4, 4]),                    # two warps a worker, queries that see nothing
     (8, 128, 8, torch.bfloat16, [200 + i for i in range(200)], [1 + i % 4 for i in range(200)]),
 ]
+PROMPTS = [
+    (2, 128, 4, torch.bfloat16, [300, 40, 9, 700], [300, 40, 20, 100]),
+    (2, 64, 4, torch.float16, [300, 40, 9, 700], [300, 40, 20, 100]),
+    (1, 128, 8, torch.bfloat16, [9000], [30]),                                      # cut into many
+    (1, 64, 8, torch.float16, [9000], [30]),
+    (2, 128, 8, torch.bfloat16, [10 + i for i in range(300)], [5 + i % 20 for i in range(300)]),  # whole items, some of more than they see
+    (2, 64, 8, torch.bfloat16, [10 + i for i in range(300)], [5 + i % 20 for i in range(300)]),
+]
 
 
 def queries_case(kv, dim, group, dtype, ctx, new, causal):
@@ -147,7 +155,7 @@ def one_key_case(dim, place, full, n, group, kv, many):
     ctx, new = [PAGE * full + place + 1] * many, [n] * many
     pool, cache, table = make(g, ctx, kv, dim)
     for r in range(0, many, 2):
-        key_nan(cache, kv, dim, table, r, ctx[r] - 1, 1)
+        key_nan(cache, kv, dim, table, r, ctx[r] - 1, kv - 1)
     q = normal(g, sum(new), kv * group, dim)
     out, lse = hs.attend_heads(pool, table, i32(ctx), q, 0.1, cu_q=offsets(new))
     kinds = check(cache, kv, dim, table, ctx, new, q, 0.1, out, lse, True)
@@ -160,3 +168,37 @@ def test_steps_with_a_nan_key_in_the_newest_token(dim, place):
     for full, kv, many in ((0, 2, 1), (1, 32, 80), (5, 2, 2), (90, 2, 1)):
         one_key_case(dim, place, full, 1, 4, kv, many)
         one_key_case(dim, place, full, 3, 8, kv, many)
+
+
+@pytest.mark.parametrize("kv,dim,group,dtype,ctx,new", PROMPTS)
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompts_with_queries_that_are_not_finite(kv, dim, group, dtype, ctx, new, causal):
+    queries_case(kv, dim, group, dtype, ctx, new, causal)
+
+
+@pytest.mark.parametrize("kv,dim,group,dtype,ctx,new", PROMPTS)
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompts_with_nothing_but_nan_keys(kv, dim, group, dtype, ctx, new, causal):
+    all_keys_case(kv, dim, group, dtype, ctx, new, causal)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("place", [0, 1, 31, 63])
+def test_prompts_with_a_nan_key_in_the_newest_token(dim, place):
+    for full, kv, n, many in ((0, 2, 40, 1), (1, 16, 20, 40), (2, 16, 20, 40), (5, 2, 150, 2), (90, 2, 70, 1), (91, 1, 40, 1)):
+        one_key_case(dim, place, full, n, 4, kv, many)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("ctx", [[200], [33] * 200, [3000]])
+def test_prompts_with_a_nan_key_in_the_first_token(dim, ctx):
+    """Every query sees it; the first of a prompt sees nothing else."""
+    g = gen(34)
+    kv, group = 2, 4
+    pool, cache, table = make(g, ctx, kv, dim)
+    for r in range(len(ctx)):
+        key_nan(cache, kv, dim, table, r, 0, 1)
+    q = normal(g, sum(ctx), kv * group, dim)
+    out, lse = hs.attend_heads(pool, table, i32(ctx), q, 0.1, cu_q=offsets(ctx))
+    kinds = check(cache, kv, dim, table, ctx, ctx, q, 0.1, out, lse, True)
+    assert kinds[0] == group * sum(ctx) and kinds[4] == group * sum(ctx)
