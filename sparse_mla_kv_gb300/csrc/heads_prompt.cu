@@ -921,7 +921,8 @@ __device__ __forceinline__ void find_start(const HeadsAttendParams& p, int limit
     q.load(p, r, limit);
     const int64_t a_head = quotient(__shfl_sync(0xFFFFFFFFu, mine, who), p.pages.kv_heads), offset = begin - __shfl_sync(0xFFFFFFFFu, first, who);
     const int head = (int)quotient(offset, a_head);
-    int left = (int)(offset - head * a_head), block = -1, in = 0;
+    int64_t left = offset - head * a_head;  // (a head's units may pass 32 bits, those of 32 blocks do not)
+    int block = -1, in = 0;
     for (int b0 = 0; block < 0; b0 += 32) {
       const int n = b0 + lane < q.blocks ? kItemCost + q.tiles(p, b0 + lane) : 0;
       int upto = n;
@@ -934,7 +935,7 @@ __device__ __forceinline__ void find_start(const HeadsAttendParams& p, int limit
       if (here) {
         const int w = __ffs(here) - 1;
         block = b0 + w;
-        in = left - (__shfl_sync(0xFFFFFFFFu, upto, w) - __shfl_sync(0xFFFFFFFFu, n, w));
+        in = (int)left - (__shfl_sync(0xFFFFFFFFu, upto, w) - __shfl_sync(0xFFFFFFFFu, n, w));
       } else {
         left -= __shfl_sync(0xFFFFFFFFu, upto, 31);
         if (b0 + 32 >= q.blocks) block = 0;  // (not reached: the offset lies within the head's units)
