@@ -75,7 +75,7 @@ struct Request {
     ctx = __ldg(p.a.ctx_len + r);
     keys = max(0, min(ctx, p.a.max_pages * kHeadsPage));
     const int cols = n * p.group;
-    blocks = cols > limit ? (cols + kBlock - 1) / kBlock : 0;
+    blocks = cols > limit ? (cols - 1) / kBlock + 1 : 0;  // (cols may be all of 31 bits)
   }
   // tokens that column c sees
   __device__ __forceinline__ int sees(const HeadsAttendParams& p, int c) const {
@@ -83,7 +83,7 @@ struct Request {
   }
   // key tiles of block b
   __device__ __forceinline__ int tiles(const HeadsAttendParams& p, int b) const {
-    return max(1, (sees(p, min(n * p.group, (b + 1) * kBlock) - 1) + kKeys - 1) / kKeys);
+    return max(1, (sees(p, min(n * p.group - 1, b * kBlock + (kBlock - 1))) + kKeys - 1) / kKeys);
   }
 };
 // Units of a request's blocks (of one head), by the whole warp.

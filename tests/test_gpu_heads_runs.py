@@ -1,5 +1,5 @@
 """Where the CTAs of attend_heads' kernel for prompts begin: against the same numbering in Python's whole numbers, for calls whose key tiles
-do not fit 31 bits.  Such calls take many seconds and tens of GB, so the search is run alone."""
+(or whose columns) do not fit 31 bits.  Such calls take many seconds or most of the memory, so the search is run alone."""
 import bisect
 import ctypes
 import subprocess
@@ -89,3 +89,11 @@ def test_runs_begin_where_the_numbering_says(starts, kv, group, causal, ctx, new
 ])
 def test_runs_of_heads_with_more_tiles_than_31_bits_hold(starts, kv, group, causal, ctx, new, max_pages):
     assert check(starts, kv, group, causal, ctx, new, max_pages) > 2 ** 31
+
+
+@pytest.mark.parametrize("kv,group,ctx,new", [
+    (1, 1, [64], [2 ** 31 - 1]), (1, 1, [300, 64], [70, 2 ** 31 - 71]), (1, 8, [1, 64], [1, 2 ** 28 - 2]), (1, 3, [64], [(2 ** 31 - 1) // 3]),
+])
+@pytest.mark.parametrize("causal", [True, False])
+def test_runs_of_calls_with_columns_up_to_31_bits(starts, kv, group, ctx, new, causal):
+    check(starts, kv, group, causal, ctx, new, 5)
