@@ -317,6 +317,7 @@ uint32_t check_take_heads_pages() {
 }
 
 cudaError_t launch_append_heads(const HeadsAppendParams& p, cudaStream_t s) {
+  if (p.a.R == 0) return cudaSuccess;  // no request has any of the tokens
   const unsigned grid = blocks(p.a.n, p.a.R, 2 * p.a.kv_heads);
   if (grid == 0) return cudaErrorInvalidConfiguration;
   if (p.a.dtype == HS_BF16)
@@ -330,6 +331,7 @@ cudaError_t launch_append_heads(const HeadsAppendParams& p, cudaStream_t s) {
 }
 
 cudaError_t launch_read_heads(const HeadsReadParams& p, cudaStream_t s) {
+  if (p.a.R == 0) return cudaSuccess;  // no request has any of the tokens
   const unsigned grid = blocks(p.a.n, p.a.R, p.a.kv_heads);
   if (grid == 0) return cudaErrorInvalidConfiguration;
   if (p.a.dtype == HS_BF16)
