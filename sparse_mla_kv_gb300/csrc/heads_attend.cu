@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(Shape<D, NC, W>::kThreads, 1) steps_kernel(con
   }
 
   const bool f16 = p.a.dtype == HS_FP16;
-  const float sign = p.scale_log2 < 0.f ? -1.f : 1.f, scale = fabsf(p.scale_log2);
+  const float sign = scale_sign(p.scale_log2), scale = fabsf(p.scale_log2);
   tc::Waiter w;
   Producer<D, NC, W> producer;
   Cursor cur = starts[worker];

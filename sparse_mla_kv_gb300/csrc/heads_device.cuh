@@ -158,6 +158,8 @@ struct Joined {
   }
 };
 
+// What the queries take of the scale; the rest is a factor of the scores, kept above zero.
+__device__ __forceinline__ float scale_sign(float scale) { return scale < 0.f ? -1.f : scale > 0.f ? 1.f : 0.f; }
 // The exponent field e of a power of two that brings a query's largest magnitude into fp16's range, by division: left as they
 // are (127) when it is in 2^-2 .. 2^15, where fp16 keeps all but what is 2^-23 of it.
 __device__ __forceinline__ int query_field(float top) {

@@ -451,7 +451,7 @@ __device__ __forceinline__ void widen_items(const HeadsAttendParams& p, const It
   using L = Smem<D>;
   const uint32_t bars = smem + L::kBar;
   const int lane = threadIdx.x & 31;
-  const float sign = p.scale_log2 < 0.f ? -1.f : 1.f;
+  const float sign = scale_sign(p.scale_log2);
   tc::Waiter w;
   uint32_t tile = 0, brought = 0, odd = 0;  // query tiles that have been brought, and an odd number of times
   auto arrive = [&](int bar) {

@@ -202,3 +202,19 @@ def test_prompts_with_a_nan_key_in_the_first_token(dim, ctx):
     out, lse = hs.attend_heads(pool, table, i32(ctx), q, 0.1, cu_q=offsets(ctx))
     kinds = check(cache, kv, dim, table, ctx, ctx, q, 0.1, out, lse, True)
     assert kinds[0] == group * sum(ctx) and kinds[4] == group * sum(ctx)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("new", [[1, 1, 1], [3, 40, 1]])
+@pytest.mark.parametrize("scale", [0.0, -0.0])
+def test_a_scale_of_zero_does_not_hide_queries_that_are_not_finite(dim, new, scale):
+    """Zero times an infinity is NaN."""
+    g = gen(35)
+    kv, group, ctx = 2, 4, [700, 90, 64]
+    pool, cache, table = make(g, ctx, kv, dim)
+    signed_codes(cache, kv, dim)
+    q = normal(g, sum(new), kv * group, dim)
+    poison_queries(g, q, group)
+    out, lse = hs.attend_heads(pool, table, i32(ctx), q, scale, cu_q=offsets(new))
+    kinds = check(cache, kv, dim, table, ctx, new, q, scale, out, lse, True)
+    assert kinds[0] and kinds[4] and not kinds[1] and not kinds[2]
