@@ -116,7 +116,7 @@ typedef struct {
   int32_t q_heads;            /* a multiple of kv_heads, at most HS_MAX_HEADS                         */
   int32_t dtype;              /* hs_dtype of q and out: HS_BF16 or HS_FP16                            */
   int32_t causal;
-  float scale;
+  float scale;                /* of either sign, at most 2^127 in magnitude                           */
   int32_t R, max_pages;
   int64_t n;                  /* query tokens; n * q_heads is below 2^31                              */
   const int32_t* block_table; /* device [R][max_pages]                                                */

@@ -1,4 +1,6 @@
 // C ABI of the operators on pages of grouped heads: argument validation and launches (see include/hs_heads.h).
+#include <math.h>
+
 #include "heads.cuh"
 
 namespace {
@@ -100,7 +102,7 @@ hs_status hs_attend_heads(const hs_pool* pool, int32_t layer, const hs_heads_att
   hs::HeadsAttendParams p;
   if (!a || (a->dtype != HS_BF16 && a->dtype != HS_FP16) || !geometry(pool, layer, *a, a->cu_q, &v, &p.pages, &p.ragged))
     return HS_ERR_INVALID_ARG;
-  if (a->q_heads < a->kv_heads || a->q_heads > HS_MAX_HEADS || a->q_heads % a->kv_heads || !(a->scale == a->scale) ||
+  if (a->q_heads < a->kv_heads || a->q_heads > HS_MAX_HEADS || a->q_heads % a->kv_heads || !(fabsf(a->scale) <= 0x1p127f) ||
       a->n * a->q_heads > INT32_MAX)
     return HS_ERR_INVALID_ARG;
   if (a->n == 0) return HS_OK;

@@ -1,4 +1,6 @@
-"""Calls of the operators on pages of grouped heads that the header allows and that are all edge: no requests at all."""
+"""Calls of the operators on pages of grouped heads that the header allows and that are all edge (no requests at all), and some that it does not."""
+import math
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -25,3 +27,17 @@ def test_tokens_that_no_request_has_because_there_is_none(n):
     same(a, k)
     same(b, v)
     assert int(status) == 0
+
+
+def test_scales_that_are_refused():
+    """Those whose product with log2(e) is not a finite number of 32 bits, with nothing launched; the largest is taken."""
+    g = gen(42)
+    pool, _, table = make(g, [70], 1, 64)
+    q = normal(g, 1, 1, 64)
+    before = hs.launch_count()
+    for scale in (math.inf, -math.inf, math.nan, 2.0 ** 127 * 1.001, -3e38):
+        with pytest.raises(hs.HSError):
+            hs.attend_heads(pool, table, i32([70]), q, scale)
+    assert hs.launch_count() == before
+    out, lse = hs.attend_heads(pool, table, i32([70]), q * 2.0 ** -100, 2.0 ** 127)
+    assert bool(out.isfinite().all()) and bool(lse.isfinite().all())
