@@ -19,7 +19,8 @@
  * and behind the last head fp32 scales: one for the keys of each head, then one for the values of each head; the
  * rest of the page (1024 - 8 * kv_heads bytes) is not used.  value = code * scale.  All of a page, its scales
  * included, moves with it.  A page has no rows of its own: hs_resolve_topk and hs_gather_rows are not for such
- * pools.
+ * pools.  A pool knows its row_bytes only, not what its pages hold: that 128 dimensions were written as such, and not as
+ * twice the heads of 64, or that rows of 656 bytes are 5 heads of 64 and not latent rows (hs_latent.h), is the caller's to keep.
  *
  * Scales are positive; hs_append_heads writes powers of two, the reading calls take any positive normal number.
  *
@@ -48,8 +49,8 @@ extern "C" {
  * 1..HS_MAX_KV_HEADS). */
 int32_t hs_heads_row_bytes(int32_t kv_heads, int32_t head_dim);
 
-/* New tokens: the last cu[r + 1] - cu[r] of the ctx_len[r] tokens that request r then has.  For each page, head and
- * side (keys or values) that they touch:
+/* New tokens: the last cu[r + 1] - cu[r] of the ctx_len[r] tokens that request r then has.  (A page that they continue was begun
+ * by this call: its scales are powers of two.)  For each page, head and side (keys or values) that they touch:
  *   need  = the smallest power of two, at least 2^-126, with |x| <= 448 * need for all finite new values x
  *   scale = need where the new tokens begin the page (what it held before counts for nothing), and the larger of
  *           need and the page's scale where they continue it; where that raises the scale, the codes of the
@@ -62,7 +63,7 @@ typedef struct {
   int32_t dtype;              /* hs_dtype of k and v                                                  */
   int32_t R, max_pages;
   int64_t n;                  /* new tokens of all requests                                           */
-  const int32_t* block_table; /* device [R][max_pages]; no page of two requests that are appended to  */
+  const int32_t* block_table; /* device [R][max_pages]; no page that is written to occurs twice       */
   const int32_t* ctx_len;     /* device [R]                                                           */
   const int32_t* cu;          /* device [R + 1], or NULL: n / R tokens each                           */
   const void* k;              /* device [n][kv_heads][head_dim]                                       */
@@ -130,7 +131,8 @@ typedef struct {
   int32_t* status;            /* optional device word: HS_ERR_ID_RANGE where cu_q does not ascend; HS_ERR_TABLE_RANGE for a needed table entry
                                  outside [0, num_gpu_blocks) or a context past max_pages (those tokens are
                                  skipped); HS_ERR_TIMEOUT: a bounded wait inside the kernel gave up (results are
-                                 then undefined)                                                      */
+                                 then undefined), after about two seconds, which contexts beyond 2^26
+                                 tokens may take                                                      */
 } hs_heads_attend;
 
 /* Bytes of device workspace (16-byte aligned) that hs_attend_heads needs at most on the current device, whatever the

@@ -21,7 +21,7 @@
 // results in the workspace, which join_kernel joins in a fixed order.
 //
 // What bounds it.  64 requests of up to 16384 tokens, 8 x 8 heads of 128 dimensions: 221 us, 5.6 TB/s of the codes, the copies
-// being ahead of the products.  With 32 columns (64 requests of up to 4004 tokens, 4 x 8 heads, four positions) the products are, 72 us:
+// being ahead of the products.  With 32 columns (64 requests of up to 4004 tokens, 4 x 8 heads, four positions) the products are, 73 us:
 // each of two warps widens all of a page's codes for its 16 columns.  4 requests of 4096 tokens, 8 x 4 heads: 18.5 us: 2 until
 // the runs are found, 3 until the first page is there, 5 of two pages' chains, 5 of joining, and the launches.
 #include <algorithm>
@@ -36,9 +36,10 @@ namespace {
 using namespace heads;
 
 constexpr int kRingBytes = 192 * 1024;
-// Requests of more columns are left to heads_prompt.cu.  With 48 columns a request (4 x 8 heads of 128 dimensions) that takes 84 us for
-// 64 requests of up to 4000 tokens, 52 us for four of up to 30000, 21 us for one of 3000; this, with four warps a group of 64,
-// 123, 77 and 16 us.  With 32 columns that takes 80, 52 and 21 us, this 72, 52 and 15 us.
+// Requests of more columns are left to heads_prompt.cu.  With 32 columns a request (4 positions, 4 x 8 heads of 128 dimensions) this takes
+// 86 us for 64 requests of up to 4000 tokens with offsets, 52 us for four of 30000, 15 us for one of 3000; that 93, 52 and 21 us.  With
+// 48 (3 positions, 4 x 16 heads) that takes 92, 45 and 21 us; a group of 64 columns here, which four warps would share, took half as long
+// again for the first two and 16 us for the last, and is not built.
 constexpr int kStepCols = 32;
 
 // Workspace: header, a record a worker, statistics [worker][2][cols][4], results [worker][2][cols][D].
@@ -715,7 +716,11 @@ cudaError_t launch_steps(const HeadsAttendParams& p, int limit, int dev, int sms
 
 template <int D>
 cudaError_t launch_dim(const HeadsAttendParams& p, int limit, int dev, int sms, cudaStream_t s) {
-  // columns of a request, on average: a group takes them all, up to 32 (a ragged call's longer ones take several)
+  // Columns of a request, on average: a group takes them all, up to 32 (a ragged call's longer ones take several).  64 requests of up
+  // to 4000 tokens, offsets given, in groups of 8, 16 and 32: with 8 columns (8 x 8 heads of 128) 75, 83 and 123 us; with 16 (4 x 16
+  // heads) 66, 63 and 83 us; with 32 (4 positions, 4 x 8 heads) 98, 82 and 86 us, but 420 and 402 us in groups of 16 and 32 for 63 of up to
+  // 16384, 8 x 8 heads.  The mean is all that the host knows of offsets, and the tokens of prompts are in it: 63 single tokens
+  // beside a chunk of 512 (8 x 8 heads) run in groups of 32, 510 us, where groups of 8 would take 350.
   const int64_t cols = p.a.R > 0 ? (p.a.n + p.a.R - 1) / p.a.R * p.group : 1;
   if (cols <= 8) return launch_steps<D, 8, 1>(p, limit, dev, sms, s);
   if (cols <= 16) return launch_steps<D, 16, 1>(p, limit, dev, sms, s);

@@ -24,12 +24,12 @@
 // it get their NaN at the end.
 //
 // What bounds it.  The products, 512 D operations a row and key tile, would take 291 us for 8192 tokens with 8 x 4 heads of 128
-// dimensions at 1887 TFLOP/s, the reads nothing to speak of; measured 481 us, 1144 TFLOP/s (1300 for chunks over long contexts).
+// dimensions at 1887 TFLOP/s, the reads nothing to speak of; measured 481 us, 1144 TFLOP/s (1290 for 4 chunks of 512 over 16000).
 // A key tile takes 3500 cycles of the SM or less: 2160 of products, 3100 of shared memory's bandwidth (both operands of the scores are
 // read for each page, the values for each query tile, the widened codes written once), 1024 of exponentials.  An item costs about
 // 7 us beside its key tiles: queries brought and converted, masked tiles, results, instructions fetched anew (so that short code
 // counts there: 16 values unrolled instead of whole rows took 14 us of 522).  For 64 dimensions the exponentials weigh twice as
-// much and the chain of a key tile is longer than its products: 360 us for the same prompt, 764 TFLOP/s.  The smallest prompts
+// much and the chain of a key tile is longer than its products: 355 us for the same prompt, 775 TFLOP/s.  The smallest prompts
 // (100 tokens, 2 x 4 heads) take 18 us.
 #include "heads_device.cuh"
 
@@ -44,16 +44,19 @@ constexpr int kQRows = 128, kKeys = 128, kBlock = 2 * kQRows;
 constexpr int kThreads = 16 * 32, kMmaWarp = 8, kLoadWarp = 10, kWalkWarp = 11, kWidenWarp = 12;
 constexpr int kTakers = 15;  // warps that the items are handed to
 constexpr int kRegsLaunch = 128;
-// Registers after the trade, of the softmax warps and of the others.  12000 tokens, 4 x 3 heads of 64 dimensions: 310 us with 208 and
-// 48, 288 us with 200 and 56, 285 us with 192 and 64.  For 128 dimensions, a page at a time, all from 136 and 120 to 168 and 88 do.
+// Registers after the trade, of the softmax warps and of the others.  12000 tokens, 4 x 3 heads of 64 dimensions: 317 us with 208 and
+// 48, 288 us with 200 and 56, 284 us with 192 and 64.  For 128 dimensions, a page at a time, all from 136 and 120 to 168 and 88 do
+// (8192 tokens, 8 x 4 heads: 483, 480 and 482 us with 136, 152 and 168; 486 us with 184).
 template <int D>
 struct Regs {
   static constexpr int kSoftmax = D == 64 ? 192 : 152, kOther = D == 64 ? 64 : 104;
   static_assert(2 * kSoftmax + 2 * kOther <= 4 * kRegsLaunch, "more registers than the launch has");
 };
 constexpr int kScales = 8;  // key tiles whose scales are kept
-// What an item costs beside its key tiles, in these (12000 tokens, 4 x 3 heads of 64: 283 us; 301 us with 2, 284 us with 4), and the
-// least of a run: fewer would be mostly set-up and joining (100 tokens, 2 x 4 heads: 24 us with 4, 34 us with 6).
+// What an item costs beside its key tiles, in these (12000 tokens, 4 x 3 heads of 64: 293 us with 2, 284 us with 3, 278 us with 4; 8192
+// tokens, 8 x 4 heads of 128: 514, 480 and 453 us; 3 is of the time when 128 dimensions went by key tiles), and the least of a run: fewer would be mostly set-up and joining (64 tokens
+// behind 16000, 1 x 2 heads: 31 us with 2, 25 us with 4 and 6), and with more, small calls leave CTAs without any (100 tokens, 2 x 4
+// heads: 17.5 us with 4, 25 us with 6).
 constexpr int kItemCost = 3, kMinRun = 4;
 // (four: of query tile 0 and 1, for a key tile's first part, then for its second)
 enum Bar { kStFull = 0, kStEmpty = kStFull + 4, kKFull = kStEmpty + 4, kKEmpty = kKFull + 2, kVFull = kKEmpty + 2,
@@ -119,8 +122,8 @@ template <int D>
 struct Smem {
   static constexpr int kUnits = D / 64, kUnit = 128 * 128;  // a unit: 128 rows of 64 fp16
   // Of a key tile, the pages that are taken together from scores to weights to results, and the number of such parts.  For 128
-  // dimensions a page at a time: its products run while the other page's weights are made (2048 rows behind 16000 tokens, 4 x 8 heads:
-  // 313 us; 333 us by key tiles).  For 64 both: the products are short, and hand-overs cost more (229 us; 285 us by pages).
+  // dimensions a page at a time: its products run while the other page's weights are made (4 chunks of 512 behind 16000 tokens, 4 x 8
+  // heads: 313 us; 357 us by key tiles).  For 64 both: the products are short, and hand-overs cost more (227 us; 291 us by pages).
   static constexpr int kPages = D == 64 ? 2 : 1, kParts = 2 / kPages;
   // Tensor memory, for each query tile: S, 64 columns a page; D columns of O; and P, 32 columns a page: where there is room, of its
   // own, so that the next scores are made while the weights are; else in the place of the page's S.
@@ -1035,10 +1038,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const HeadsAttendPa
   }
 }
 
-// Joins the parts of items that several runs share, two at a time, so that their loads are on their way together (four take
-// registers that more blocks need: 2 chunks of 512 behind 8000, 4 x 8 heads, 117 and 110 us).  A thread has D / 8 dimensions (its
-// warp's) of a row.  A block takes 32 rows of a cut item; where there are more than kFewParts, 8 rows, whose parts its lanes share
-// out (64 tokens behind 16000, 1 x 2 heads, 21 parts: 27 us, 34 us without; with 10 parts, 8 x 8 heads, 62 and 53 us).
+// Joins the parts of items that several runs share, two at a time, so that their loads are on their way together (2 x 4 positions
+// behind 131000, 2 x 16 heads of 128: 62 us for the whole call with one at a time, 54.6 us with two, 56.4 us with four, which take
+// registers that more blocks need).  A thread has D / 8 dimensions (its warp's) of a row.  A block takes 32 rows of a cut item; where
+// there are more than kFewParts, 8 rows, whose parts its lanes share out (64 tokens behind 16000, 1 x 2 heads, 21 parts: 25 us, 37 us
+// without; with 10 parts, 8 x 8 heads, 49 us so and 48 us without).
 constexpr int kJoinThreads = 256, kJoinRows = 32, kJoinFewRows = 8, kJoinParts = 2, kFewParts = 16, kMaxCtas = 512;
 template <int D>
 struct JoinedRow {
